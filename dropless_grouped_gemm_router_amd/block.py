@@ -1,0 +1,563 @@
+"""Operators around the MoE layer (``include/moe_block.h``): layer norm, the
+dense gated feed-forward block and products with 8-bit integer weights,
+forward and, where the layer trains, backward.
+
+The ``moe_*`` functions have the C entry points' names and only marshal
+arguments, as in ``binding``. The functions without that prefix take tensors:
+they check shapes, types, contiguity and device on the host, launch on the
+tensors' own device (its current stream unless one is given) and write into
+buffers that were allocated once (``allocate_norm``, ``allocate_ffn``,
+``allocate_linear_i8``). Tensors used on a stream other than their own have to
+be ordered by the caller, as for every call of the library.
+"""
+
+from __future__ import annotations
+
+import contextlib
+import ctypes
+from dataclasses import dataclass
+from typing import Dict, Optional
+
+from . import binding
+from .binding import (DTYPES, MOE_BF16, MOE_FP32, _check, _ptr, _stream, load as _load_library,
+                      moe_routing, routing_struct)
+
+MOE_I8 = 2
+ACTS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3}
+
+EXPORTED = ["moe_layer_norm", "moe_layer_norm_workspace_bytes", "moe_layer_norm_bwd",
+            "moe_gated_ffn_workspace_bytes", "moe_gated_ffn_saved_bytes", "moe_gated_ffn",
+            "moe_gated_ffn_bwd", "moe_i8_pitch", "moe_quantize_rows", "moe_quantize_weight",
+            "moe_linear_i8_workspace_bytes", "moe_linear_i8"]
+
+
+class moe_norm(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("width", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("ld_x", ctypes.c_int64), ("ld_y", ctypes.c_int64),
+                ("ld_grad_out", ctypes.c_int64), ("ld_grad_x", ctypes.c_int64)]
+
+
+class moe_ffn(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("d_model", ctypes.c_int32),
+                ("d_hidden", ctypes.c_int32), ("dtype", ctypes.c_int32), ("act", ctypes.c_int32),
+                ("grad_dtype", ctypes.c_int32)]
+
+
+class moe_i8_linear(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64)] + [(n, ctypes.c_int32) for n in (
+        "inputs", "outputs", "x_dtype", "dtype", "groups", "top_k", "gather", "gated", "capacity")]
+
+
+_lib = None
+
+
+def load():
+    """libmoe.so with the signatures of this header's entry points."""
+    global _lib
+    if _lib is not None:
+        return _lib
+    lib = _load_library()
+    P, i32, i64, size = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
+    N, F, L = (ctypes.POINTER(t) for t in (moe_norm, moe_ffn, moe_i8_linear))
+    sig = {
+        "moe_layer_norm": (ctypes.c_int, [N] + [P] * 7),
+        "moe_layer_norm_workspace_bytes": (size, [N]),
+        "moe_layer_norm_bwd": (ctypes.c_int, [N] + [P] * 9 + [size, P]),
+        "moe_gated_ffn_workspace_bytes": (size, [F, ctypes.c_int]),
+        "moe_gated_ffn_saved_bytes": (size, [F]),
+        "moe_gated_ffn": (ctypes.c_int, [F] + [P] * 7 + [size, P]),
+        "moe_gated_ffn_bwd": (ctypes.c_int, [F] + [P] * 11 + [size, P]),
+        "moe_i8_pitch": (i64, [i32]),
+        "moe_quantize_rows": (ctypes.c_int, [i64, i32, i32, P, i64, P, P, P]),
+        "moe_quantize_weight": (ctypes.c_int, [i32, i32, i32, i32, P, i64, P, P, P]),
+        "moe_linear_i8_workspace_bytes": (size, [L]),
+        "moe_linear_i8": (ctypes.c_int, [L, P, P, P, P, P, ctypes.POINTER(moe_routing), P, P, size, P]),
+    }
+    for name, (res, args) in sig.items():
+        fn = getattr(lib, name)
+        fn.restype = res
+        fn.argtypes = args
+    _lib = lib
+    return lib
+
+
+# ---------------------------------------------------------- C entry points
+
+def _dtype(d) -> int:
+    return DTYPES[d] if isinstance(d, str) else int(d)
+
+
+def _nbytes(workspace, given: Optional[int]) -> int:
+    if given is not None:
+        return given
+    return 0 if workspace is None else workspace.numel() * workspace.element_size()
+
+
+def moe_layer_norm(n: moe_norm, x, weight, bias, y, mean, rstd, stream=None):
+    _check(load().moe_layer_norm(ctypes.byref(n), _ptr(x), _ptr(weight), _ptr(bias), _ptr(y),
+                                 _ptr(mean), _ptr(rstd), _stream(stream)), "moe_layer_norm")
+
+
+def moe_layer_norm_workspace_bytes(n: moe_norm) -> int:
+    return int(load().moe_layer_norm_workspace_bytes(ctypes.byref(n)))
+
+
+def moe_layer_norm_bwd(n: moe_norm, x, weight, mean, rstd, grad_out, grad_x, grad_weight, grad_bias,
+                       workspace, workspace_bytes: Optional[int] = None, stream=None):
+    _check(load().moe_layer_norm_bwd(ctypes.byref(n), _ptr(x), _ptr(weight), _ptr(mean), _ptr(rstd),
+                                     _ptr(grad_out), _ptr(grad_x), _ptr(grad_weight),
+                                     _ptr(grad_bias), _ptr(workspace),
+                                     _nbytes(workspace, workspace_bytes), _stream(stream)),
+           "moe_layer_norm_bwd")
+
+
+def moe_gated_ffn_workspace_bytes(f: moe_ffn, training: bool = False) -> int:
+    return int(load().moe_gated_ffn_workspace_bytes(ctypes.byref(f), int(training)))
+
+
+def moe_gated_ffn_saved_bytes(f: moe_ffn) -> int:
+    return int(load().moe_gated_ffn_saved_bytes(ctypes.byref(f)))
+
+
+def moe_gated_ffn(f: moe_ffn, x, w_gate, w_up, w_down, saved, out, workspace,
+                  workspace_bytes: Optional[int] = None, stream=None):
+    _check(load().moe_gated_ffn(ctypes.byref(f), _ptr(x), _ptr(w_gate), _ptr(w_up), _ptr(w_down),
+                                _ptr(saved), _ptr(out), _ptr(workspace),
+                                _nbytes(workspace, workspace_bytes), _stream(stream)), "moe_gated_ffn")
+
+
+def moe_gated_ffn_bwd(f: moe_ffn, x, w_gate, w_up, w_down, saved, grad_out, grad_x, grad_gate,
+                      grad_up, grad_down, workspace, workspace_bytes: Optional[int] = None,
+                      stream=None):
+    _check(load().moe_gated_ffn_bwd(ctypes.byref(f), _ptr(x), _ptr(w_gate), _ptr(w_up),
+                                    _ptr(w_down), _ptr(saved), _ptr(grad_out), _ptr(grad_x),
+                                    _ptr(grad_gate), _ptr(grad_up), _ptr(grad_down),
+                                    _ptr(workspace), _nbytes(workspace, workspace_bytes),
+                                    _stream(stream)), "moe_gated_ffn_bwd")
+
+
+def moe_i8_pitch(width: int) -> int:
+    return int(load().moe_i8_pitch(int(width)))
+
+
+def moe_quantize_rows(rows: int, width: int, dtype, x, ld_x: int, q, scale, stream=None):
+    _check(load().moe_quantize_rows(rows, width, _dtype(dtype), _ptr(x), ld_x, _ptr(q),
+                                    _ptr(scale), _stream(stream)), "moe_quantize_rows")
+
+
+def moe_quantize_weight(groups: int, width: int, outputs: int, dtype, w, q_rows: int, q, scale,
+                        stream=None):
+    _check(load().moe_quantize_weight(groups, width, outputs, _dtype(dtype), _ptr(w), q_rows,
+                                      _ptr(q), _ptr(scale), _stream(stream)), "moe_quantize_weight")
+
+
+def moe_linear_i8_workspace_bytes(l: moe_i8_linear) -> int:
+    return int(load().moe_linear_i8_workspace_bytes(ctypes.byref(l)))
+
+
+def moe_linear_i8(l: moe_i8_linear, x, x_scale, wq, w_scale, bias, routing: Optional[Dict], y,
+                  workspace, workspace_bytes: Optional[int] = None, stream=None):
+    r = None if routing is None else ctypes.byref(routing_struct(routing))
+    _check(load().moe_linear_i8(ctypes.byref(l), _ptr(x), _ptr(x_scale), _ptr(wq), _ptr(w_scale),
+                                _ptr(bias), r, _ptr(y), _ptr(workspace),
+                                _nbytes(workspace, workspace_bytes), _stream(stream)),
+           "moe_linear_i8")
+
+
+# ------------------------------------------------------------ tensor checks
+
+def _torch_dtype(d):
+    import torch
+    return {MOE_FP32: torch.float32, MOE_BF16: torch.bfloat16}[_dtype(d)]
+
+
+def _want(name, t, shape, dtype, device, strided=False):
+    """``t`` is a tensor of this shape, type and device: contiguous, or with
+    ``strided`` a matrix whose rows are contiguous."""
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: {t.dtype}, expected {dtype}")
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, expected {device}")
+    if strided:
+        if t.shape[1] > 1 and t.stride(1) != 1 or t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+            raise ValueError(f"{name}: rows have to be contiguous and apart, strides {t.stride()}")
+    elif not t.is_contiguous():
+        raise ValueError(f"{name}: has to be contiguous")
+
+
+def _ld(t) -> int:
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+@contextlib.contextmanager
+def _on(device):
+    import torch
+    if device.type != "cuda":
+        raise ValueError(f"tensors have to be on a GPU, not on {device}")
+    if torch.cuda.current_device() == device.index:
+        yield
+    else:
+        with torch.cuda.device(device):
+            yield
+
+
+def _device(device):
+    import torch
+    d = torch.device(device)
+    if d.type == "cuda" and d.index is None:
+        d = torch.device("cuda", torch.cuda.current_device())
+    return d
+
+
+# ---------------------------------------------------------------- layer norm
+
+@dataclass
+class NormBuffers:
+    """Device buffers of one layer norm, allocated once."""
+
+    y: object
+    mean: object
+    rstd: object
+    grad_x: Optional[object] = None
+    grad_weight: Optional[object] = None
+    grad_bias: Optional[object] = None
+    workspace: Optional[object] = None
+
+
+def allocate_norm(rows: int, width: int, dtype, device="cuda", training: bool = False) -> NormBuffers:
+    import torch
+    dt, device = _torch_dtype(dtype), _device(device)
+    f32 = dict(dtype=torch.float32, device=device)
+    b = NormBuffers(y=torch.empty((rows, width), dtype=dt, device=device),
+                    mean=torch.empty(rows, **f32), rstd=torch.empty(rows, **f32))
+    if training:
+        n = moe_norm(rows, width, _dtype(dtype), 0.0, 0, 0, 0, 0)
+        with _on(device):
+            nws = moe_layer_norm_workspace_bytes(n)
+        b.grad_x = torch.empty((rows, width), dtype=dt, device=device)
+        b.grad_weight, b.grad_bias = torch.empty(width, **f32), torch.empty(width, **f32)
+        b.workspace = torch.empty(nws, dtype=torch.uint8, device=device)
+    return b
+
+
+def _code(t) -> int:
+    import torch
+    if t.dtype == torch.bfloat16:
+        return MOE_BF16
+    if t.dtype == torch.float32:
+        return MOE_FP32
+    raise ValueError(f"{t.dtype}: float32 or bfloat16 is supported")
+
+
+def layer_norm(x, weight, bias, eps: float, buf: NormBuffers, stream=None):
+    """Layer norm over the rows of x [rows, width] (rows may be strided);
+    weight and bias are fp32 or None. Returns buf.y, with buf.mean and
+    buf.rstd kept for the backward pass."""
+    import torch
+    if x.dim() != 2:
+        raise ValueError(f"x: a matrix is expected, not {x.dim()} dimensions")
+    rows, width = x.shape
+    dev = x.device
+    _want("x", x, (rows, width), x.dtype, dev, strided=True)
+    for name, t in (("weight", weight), ("bias", bias)):
+        if t is not None:
+            _want(name, t, (width,), torch.float32, dev)
+    _want("y", buf.y, (rows, width), x.dtype, dev, strided=True)
+    _want("mean", buf.mean, (rows,), torch.float32, dev)
+    _want("rstd", buf.rstd, (rows,), torch.float32, dev)
+    n = moe_norm(rows, width, _code(x), eps, _ld(x), _ld(buf.y), 0, 0)
+    with _on(dev):
+        moe_layer_norm(n, x, weight, bias, buf.y, buf.mean, buf.rstd, stream)
+    return buf.y
+
+
+def layer_norm_backward(x, weight, grad_out, buf: NormBuffers, stream=None):
+    """Gradients of sum(y * grad_out) after ``layer_norm`` with the same
+    buffers: (grad_x, grad_weight, grad_bias), the last two in fp32."""
+    import torch
+    rows, width = x.shape
+    dev = x.device
+    _want("x", x, (rows, width), x.dtype, dev, strided=True)
+    if weight is not None:
+        _want("weight", weight, (width,), torch.float32, dev)
+    _want("grad_out", grad_out, (rows, width), x.dtype, dev, strided=True)
+    if buf.grad_x is None:
+        raise ValueError("the buffers were allocated without training=True")
+    _want("grad_x", buf.grad_x, (rows, width), x.dtype, dev, strided=True)
+    for name in ("mean", "rstd"):
+        _want(name, getattr(buf, name), (rows,), torch.float32, dev)
+    for name in ("grad_weight", "grad_bias"):
+        _want(name, getattr(buf, name), (width,), torch.float32, dev)
+    n = moe_norm(rows, width, _code(x), 0.0, _ld(x), 0, _ld(grad_out), _ld(buf.grad_x))
+    with _on(dev):
+        moe_layer_norm_bwd(n, x, weight, buf.mean, buf.rstd, grad_out, buf.grad_x, buf.grad_weight,
+                           buf.grad_bias, buf.workspace, stream=stream)
+    return buf.grad_x, buf.grad_weight, buf.grad_bias
+
+
+# -------------------------------------------------- gated feed-forward block
+
+@dataclass(frozen=True)
+class GatedFfn:
+    """A dense gated feed-forward block: out = (act(x W_gate) * (x W_up)) W_down."""
+
+    tokens: int
+    d_model: int
+    d_hidden: int
+    dtype: str = "bf16"
+    act: str = "silu"
+    grad_dtype: str = "fp32"  # of the weight gradients: fp32, or dtype
+
+    def struct(self) -> moe_ffn:
+        return moe_ffn(self.tokens, self.d_model, self.d_hidden, DTYPES[self.dtype], ACTS[self.act],
+                       DTYPES[self.grad_dtype])
+
+
+@dataclass
+class FfnBuffers:
+    """Device buffers of one block, allocated once."""
+
+    out: object
+    workspace: object
+    saved: Optional[object] = None
+    grad_x: Optional[object] = None
+    grads: Optional[Dict] = None
+
+
+def allocate_ffn(f: GatedFfn, device="cuda", training: bool = False) -> FfnBuffers:
+    import torch
+    dt, device, c = _torch_dtype(f.dtype), _device(device), f.struct()
+    with _on(device):
+        nws, nsv = moe_gated_ffn_workspace_bytes(c, training), moe_gated_ffn_saved_bytes(c)
+    if nws == 0:
+        _check(-2, "moe_gated_ffn")
+    b = FfnBuffers(out=torch.empty((f.tokens, f.d_model), dtype=dt, device=device),
+                   workspace=torch.empty(nws, dtype=torch.uint8, device=device))
+    if training:
+        g = dict(dtype=_torch_dtype(f.grad_dtype), device=device)
+        b.saved = torch.empty(nsv, dtype=torch.uint8, device=device)
+        b.grad_x = torch.empty((f.tokens, f.d_model), dtype=dt, device=device)
+        b.grads = dict(w_gate=torch.empty((f.d_model, f.d_hidden), **g),
+                       w_up=torch.empty((f.d_model, f.d_hidden), **g),
+                       w_down=torch.empty((f.d_hidden, f.d_model), **g))
+    return b
+
+
+def _want_ffn(f, x, weights):
+    dt, dev = _torch_dtype(f.dtype), x.device
+    _want("x", x, (f.tokens, f.d_model), dt, dev)
+    for name, shape in (("w_gate", (f.d_model, f.d_hidden)), ("w_up", (f.d_model, f.d_hidden)),
+                        ("w_down", (f.d_hidden, f.d_model))):
+        _want(name, weights[name], shape, dt, dev)
+    return dt, dev
+
+
+def gated_ffn(f: GatedFfn, x, weights: Dict, buf: FfnBuffers, training: bool = False, stream=None):
+    """The block's forward pass (weights: w_gate, w_up, w_down); returns buf.out."""
+    dt, dev = _want_ffn(f, x, weights)
+    _want("out", buf.out, (f.tokens, f.d_model), dt, dev)
+    if training and buf.saved is None:
+        raise ValueError("the buffers were allocated without training=True")
+    with _on(dev):
+        moe_gated_ffn(f.struct(), x, weights["w_gate"], weights["w_up"], weights["w_down"],
+                      buf.saved if training else None, buf.out, buf.workspace, stream=stream)
+    return buf.out
+
+
+def gated_ffn_backward(f: GatedFfn, x, weights: Dict, grad_out, buf: FfnBuffers, stream=None):
+    """Gradients of sum(out * grad_out) after ``gated_ffn(..., training=True)``:
+    (grad_x, {w_gate, w_up, w_down})."""
+    dt, dev = _want_ffn(f, x, weights)
+    if buf.saved is None:
+        raise ValueError("the buffers were allocated without training=True")
+    _want("grad_out", grad_out, (f.tokens, f.d_model), dt, dev)
+    _want("grad_x", buf.grad_x, (f.tokens, f.d_model), dt, dev)
+    for name, g in buf.grads.items():
+        _want("gradient of " + name, g, tuple(weights[name].shape), _torch_dtype(f.grad_dtype), dev)
+    with _on(dev):
+        moe_gated_ffn_bwd(f.struct(), x, weights["w_gate"], weights["w_up"], weights["w_down"],
+                          buf.saved, grad_out, buf.grad_x, buf.grads["w_gate"], buf.grads["w_up"],
+                          buf.grads["w_down"], buf.workspace, stream=stream)
+    return buf.grad_x, buf.grads
+
+
+# ------------------------------------------------- products in 8-bit integers
+
+@dataclass(frozen=True)
+class LinearI8:
+    """A product with weights in 8-bit integers, dense (groups 1) or grouped by
+    the layer's routing; see moe_linear_i8."""
+
+    tokens: int
+    inputs: int
+    outputs: int  # weight rows of a group; when gated, gate rows then up rows
+    dtype: str = "bf16"  # of the output
+    groups: int = 1
+    top_k: int = 1
+    gated: bool = False
+    sorted_input: bool = False  # routed: x rows are in expert order, not tokens
+    capacity: int = 0
+
+    @property
+    def rows(self) -> int:
+        return self.tokens * self.top_k
+
+    @property
+    def columns(self) -> int:
+        return self.outputs // 2 if self.gated else self.outputs
+
+    @property
+    def input_rows(self) -> int:
+        return self.rows if self.sorted_input else self.tokens
+
+    def struct(self, x_dtype: int, routed: bool) -> moe_i8_linear:
+        return moe_i8_linear(self.tokens, self.inputs, self.outputs, x_dtype, DTYPES[self.dtype],
+                             self.groups, self.top_k, int(routed and not self.sorted_input),
+                             int(self.gated), self.capacity)
+
+
+@dataclass
+class I8Buffers:
+    """Device buffers of one product, allocated once."""
+
+    y: object
+    workspace: object
+
+
+def allocate_linear_i8(l: LinearI8, device="cuda") -> I8Buffers:
+    import torch
+    device = _device(device)
+    with _on(device):
+        nws = moe_linear_i8_workspace_bytes(l.struct(MOE_FP32, l.groups > 1))
+    if nws == 0:
+        _check(-2, "moe_linear_i8")
+    return I8Buffers(y=torch.empty((l.rows, l.columns), dtype=_torch_dtype(l.dtype), device=device),
+                     workspace=torch.empty(nws, dtype=torch.uint8, device=device))
+
+
+def quantize_rows(x, q=None, scale=None, stream=None):
+    """Rows of x [rows, width] as (q int8 [rows, pitch], scale fp32 [rows])."""
+    import torch
+    rows, width = x.shape
+    dev = x.device
+    _want("x", x, (rows, width), x.dtype, dev, strided=True)
+    pitch = moe_i8_pitch(width)
+    q = torch.empty((rows, pitch), dtype=torch.int8, device=dev) if q is None else q
+    scale = torch.empty(rows, dtype=torch.float32, device=dev) if scale is None else scale
+    _want("q", q, (rows, pitch), torch.int8, dev)
+    _want("scale", scale, (rows,), torch.float32, dev)
+    with _on(dev):
+        moe_quantize_rows(rows, width, _code(x), x, _ld(x), q, scale, stream)
+    return q, scale
+
+
+def quantize_weights(*parts, stream=None):
+    """Weights [groups, width, outputs] (or one matrix [width, outputs]) as
+    (q int8 [groups, rows, pitch], scale fp32 [groups, rows]); several parts of
+    one shape (gate and up) follow each other in a group's rows."""
+    import torch
+    parts = [w[None] if w.dim() == 2 else w for w in parts]
+    groups, width, outputs = parts[0].shape
+    dev, rows = parts[0].device, outputs * len(parts)
+    pitch = moe_i8_pitch(width)
+    q = torch.empty((groups, rows, pitch), dtype=torch.int8, device=dev)
+    scale = torch.empty((groups, rows), dtype=torch.float32, device=dev)
+    for i, w in enumerate(parts):
+        _want("weights", w, (groups, width, outputs), parts[0].dtype, dev)
+        with _on(dev):
+            moe_quantize_weight(groups, width, outputs, _code(w), w, rows, q[:, i * outputs:],
+                                scale[:, i * outputs:], stream)
+    return q, scale
+
+
+def linear_i8(l: LinearI8, x, wq, w_scale, buf: I8Buffers, bias=None, routing: Optional[Dict] = None,
+              x_scale=None, stream=None):
+    """The product; x is fp32 or bf16 [rows, inputs] (quantised within the
+    call) or int8 [rows, pitch] with x_scale. Returns buf.y."""
+    import torch
+    dev = x.device
+    pitch = moe_i8_pitch(l.inputs)
+    if x.dtype == torch.int8:
+        code = MOE_I8
+        _want("x", x, (l.input_rows, pitch), torch.int8, dev)
+        if x_scale is None:
+            raise ValueError("an int8 input needs x_scale")
+        _want("x_scale", x_scale, (l.input_rows,), torch.float32, dev)
+    else:
+        code = _code(x)
+        _want("x", x, (l.input_rows, l.inputs), x.dtype, dev)
+    _want("weights", wq, (l.groups, l.outputs, pitch), torch.int8, dev)
+    _want("weight scales", w_scale, (l.groups, l.outputs), torch.float32, dev)
+    if bias is not None:
+        _want("bias", bias, (l.outputs,), torch.float32, dev)
+    if routing is not None:
+        _want("expert_offsets", routing["expert_offsets"], (l.groups + 1,), torch.int32, dev)
+        if not l.sorted_input:
+            _want("perm", routing["perm"], (l.rows,), torch.int32, dev)
+    _want("y", buf.y, (l.rows, l.columns), _torch_dtype(l.dtype), dev)
+    with _on(dev):
+        moe_linear_i8(l.struct(code, routing is not None), x, x_scale, wq, w_scale, bias, routing,
+                      buf.y, buf.workspace, stream=stream)
+    return buf.y
+
+
+# ------------------------------------------------------- with the layer itself
+
+def prenorm_forward(p, x, weights: Dict, buf, norm: NormBuffers, eps: float = 1e-5,
+                    training: bool = False, stream=None):
+    """The MoE layer behind its norm, MoE(norm(x)): ``binding.forward`` on
+    the normalised tokens; weights holds norm_weight and norm_bias (either may
+    be missing) beside the layer's own. Returns buf.out."""
+    h = layer_norm(x, weights.get("norm_weight"), weights.get("norm_bias"), eps, norm, stream)
+    with _on(x.device):
+        return binding.forward(p, h, weights, buf, training=training, stream=stream)
+
+
+def prenorm_backward(p, x, weights: Dict, grad_out, buf, norm: NormBuffers, stream=None,
+                     side_stream=None):
+    """Gradients of sum(out * grad_out) after prenorm_forward(..., training=True)
+    with the same buffers: (grad_x, the layer's weight gradients with
+    norm_weight and norm_bias beside them)."""
+    with _on(x.device):
+        gh, grads = binding.backward(p, norm.y, weights, grad_out, buf, stream=stream,
+                                     side_stream=side_stream)
+    gx, gw, gb = layer_norm_backward(x, weights.get("norm_weight"), gh, norm, stream)
+    return gx, dict(grads, norm_weight=gw, norm_bias=gb)
+
+
+@dataclass
+class ExpertsI8Buffers:
+    """Buffers of the routed experts in 8 bits: both products' outputs."""
+
+    gate_up: LinearI8
+    down: LinearI8
+    hidden: I8Buffers
+    sorted: I8Buffers
+
+
+def allocate_experts_i8(p, device="cuda") -> ExpertsI8Buffers:
+    name = "bf16" if _dtype(p.dtype) == MOE_BF16 else "fp32"
+    cap = int(getattr(p, "capacity", 0))
+    up = LinearI8(p.tokens, p.d_model, 2 * p.d_hidden, name, p.experts, p.top_k, gated=True,
+                  capacity=cap)
+    down = LinearI8(p.tokens, p.d_hidden, p.d_model, name, p.experts, p.top_k, sorted_input=True,
+                    capacity=cap)
+    return ExpertsI8Buffers(up, down, allocate_linear_i8(up, device), allocate_linear_i8(down, device))
+
+
+def forward_i8(p, x, w_router, gate_up, down, buf, experts: ExpertsI8Buffers, shared_out=None,
+               stream=None):
+    """The layer's forward with routed experts in 8-bit integers: route ->
+    permute -> gated product -> product -> combine. gate_up and down are
+    (q, scale) pairs of ``quantize_weights(w_gate, w_up)`` and
+    ``quantize_weights(w_down)``; buf is ``binding.allocate(p)``, and a shared
+    expert's output may be given to be added. Returns buf.out."""
+    with _on(x.device):
+        binding.moe_route(p, x, w_router, buf.routing, stream)
+        binding.moe_permute(p, buf.routing, buf.workspace, stream=stream)
+        h = linear_i8(experts.gate_up, x, *gate_up, experts.hidden, routing=buf.routing, stream=stream)
+        y = linear_i8(experts.down, h, *down, experts.sorted, routing=buf.routing, stream=stream)
+        binding.moe_combine(p, y, buf.routing, shared_out, buf.out, stream)
+    return buf.out

@@ -1,0 +1,351 @@
+// Products with weights in 8-bit integers: y = (q_x q_w^T) s_x s_w.
+//
+// The token's scale is its largest magnitude over 127, its integers x / s
+// rounded to nearest even; both divisions are exact fp32 divisions, so the
+// integers are the same on every machine and in every path below. Sums of
+// products are exact int32 (65536 products of 127 * 128 stay under 2^31).
+#include "mm.h"
+
+namespace moe {
+
+namespace {
+
+// ------------------------------------------------------------- quantising
+
+template <int kCtrl>
+__device__ __forceinline__ uint32_t dpp_u(uint32_t v) {
+  return static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(v), kCtrl, 0xf, 0xf, true));
+}
+__device__ __forceinline__ uint32_t wave_umax(uint32_t v) {
+  v = max(v, dpp_u<0xb1>(v));
+  v = max(v, dpp_u<0x4e>(v));
+  v = max(v, dpp_u<0x141>(v));
+  v = max(v, dpp_u<0x140>(v));
+  const auto a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  v = max(a[0], a[1]);
+  const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  return max(b[0], b[1]);
+}
+
+// Magnitudes are compared as bit patterns: infinities and NaN are then
+// larger than every number, and a row that holds one is seen.
+__device__ __forceinline__ float scale_of(uint32_t most) {
+  return most >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : __uint_as_float(most) / 127.0f;
+}
+// A row is quantised when its scale is positive; else (zero or NaN) q is 0.
+__device__ __forceinline__ int quantize(float v, float scale) {
+  if (!(scale > 0.0f)) return 0;
+  return static_cast<int>(fminf(fmaxf(rintf(v / scale), -127.0f), 127.0f));
+}
+
+template <int V>
+__device__ __forceinline__ void store_q(int8_t* p, const float (&f)[V], float scale) {
+  uint32_t w[V / 4];
+#pragma unroll
+  for (int i = 0; i < V / 4; ++i) {
+    w[i] = 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      w[i] |= (static_cast<uint32_t>(quantize(f[4 * i + q], scale)) & 0xffu) << (8 * q);
+  }
+  if (V == 8) *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[V / 4 - 1]);
+  else *reinterpret_cast<uint32_t*>(p) = w[0];
+}
+
+// One row per kTPR threads. kNV pieces a thread stay in registers between
+// the two passes; with kNV 0 the row is read twice (the second time from
+// cache).
+template <typename T, int kTPR, int kNV>
+__global__ __launch_bounds__(kTPR < 256 ? 256 : kTPR) void quantize_rows_kernel(
+    int64_t rows, int width, int64_t pitch, const T* __restrict__ x, int64_t ld,
+    int8_t* __restrict__ q, float* __restrict__ scale) {
+  constexpr int V = Piece<T>::V, kRows = (kTPR < 256 ? 256 : kTPR) / kTPR;
+  __shared__ uint32_t part[16];
+  const int t = threadIdx.x % kTPR;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / kTPR;
+  if (row >= rows) return;
+  const T* xr = x + row * ld;
+  float f[kNV ? kNV : 1][V];
+  uint32_t most = 0;
+  if (kNV) {
+#pragma unroll
+    for (int i = 0; i < kNV; ++i) Piece<T>::widen(load_piece(xr, (i * kTPR + t) * V, width), f[i]);
+#pragma unroll
+    for (int i = 0; i < kNV; ++i)
+#pragma unroll
+      for (int e = 0; e < V; ++e) most = max(most, __float_as_uint(f[i][e]) & 0x7fffffffu);
+  } else {
+    for (int c = t * V; c < width; c += kTPR * V) {
+      Piece<T>::widen(load_piece(xr, c, width), f[0]);
+#pragma unroll
+      for (int e = 0; e < V; ++e) most = max(most, __float_as_uint(f[0][e]) & 0x7fffffffu);
+    }
+  }
+  most = wave_umax(most);
+  if (kTPR > 64) {
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = most;
+    __syncthreads();
+    most = part[0];
+#pragma unroll
+    for (int w = 1; w < kTPR / 64; ++w) most = max(most, part[w]);
+  }
+  const float s = scale_of(most);
+  if (t == 0) scale[row] = s;
+  int8_t* qr = q + row * pitch;
+  if (kNV) {
+#pragma unroll
+    for (int i = 0; i < kNV; ++i) {
+      const int c = (i * kTPR + t) * V;
+      if (c < pitch) store_q<V>(qr + c, f[i], s);
+    }
+  } else {
+    for (int c = t * V; c < pitch; c += kTPR * V) {
+      Piece<T>::widen(load_piece(xr, c, width), f[0]);
+      store_q<V>(qr + c, f[0], s);
+    }
+  }
+}
+
+// Weights [groups][width][outputs] to rows of one output channel each: a
+// workgroup takes 64 channels, reads the group's columns twice (largest
+// magnitudes, then values) and turns 64 x 64 blocks through LDS.
+template <typename T>
+__global__ __launch_bounds__(256) void quantize_weight_kernel(int width, int outputs, int64_t pitch,
+                                                              const T* __restrict__ w, int64_t q_rows,
+                                                              int8_t* __restrict__ q,
+                                                              float* __restrict__ scale) {
+  __shared__ uint32_t most[4][64];
+  __shared__ float sc[64];
+  __shared__ int8_t turn[64][68];
+  const int c = threadIdx.x & 63, part = threadIdx.x >> 6;
+  const int n = blockIdx.x * 64 + c;
+  const T* wg = w + static_cast<int64_t>(blockIdx.y) * width * outputs;
+  uint32_t m = 0;
+  if (n < outputs)
+    for (int k = part; k < width; k += 4)
+      m = max(m, __float_as_uint(elem(wg + static_cast<int64_t>(k) * outputs + n)) & 0x7fffffffu);
+  most[part][c] = m;
+  __syncthreads();
+  if (part == 0) {
+    sc[c] = scale_of(max(max(most[0][c], most[1][c]), max(most[2][c], most[3][c])));
+    if (n < outputs) scale[blockIdx.y * q_rows + n] = sc[c];
+  }
+  __syncthreads();
+  const float s = sc[c];
+  int8_t* qg = q + blockIdx.y * q_rows * pitch;
+  for (int k0 = 0; k0 < pitch; k0 += 64) {
+    for (int k = part; k < 64; k += 4) {
+      float v = 0.0f;
+      if (n < outputs && k0 + k < width) v = elem(wg + static_cast<int64_t>(k0 + k) * outputs + n);
+      turn[c][k] = static_cast<int8_t>(quantize(v, s));
+    }
+    __syncthreads();
+    // 64 rows of 64 bytes: 16 threads a row, four bytes each
+    for (int i = threadIdx.x; i < 1024; i += 256) {
+      const int r = i >> 4, at = (i & 15) * 4;
+      if (blockIdx.x * 64 + r < outputs)
+        *reinterpret_cast<uint32_t*>(qg + static_cast<int64_t>(blockIdx.x * 64 + r) * pitch + k0 + at) =
+            *reinterpret_cast<const uint32_t*>(&turn[r][at]);
+    }
+    __syncthreads();
+  }
+}
+
+// ---------------------------------------------------------------- products
+
+struct I8Out {
+  const float* xs;    // scale of an input row
+  const float* ws;    // scale of a weight row [groups][outputs]
+  const float* bias;
+  void* y;
+  int64_t ld;         // columns of y
+  int outputs;        // weight rows a group
+};
+
+// Four consecutive columns n.. of row r, n a multiple of four.
+template <typename T>
+__device__ __forceinline__ void i8_store4(const I8Out& o, int64_t r, int n, const float (&v)[4]) {
+  T* dst = static_cast<T*>(o.y) + r * o.ld + n;
+  if (n + 4 <= o.ld && o.ld % 4 == 0) {
+    store4(dst, v[0], v[1], v[2], v[3]);
+    return;
+  }
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    if (n + q < o.ld) put(dst + q, v[q]);
+}
+
+template <typename T, typename Cfg, bool kPaired>
+__global__ __launch_bounds__(Cfg::NT) __attribute__((amdgpu_waves_per_eu(Cfg::NT == 512 ? 2 : 1)))
+void i8_tile_kernel(const MmArgs p, const I8Out o) {
+  __shared__ __attribute__((aligned(1024))) char smem[2 * Cfg::STAGE];
+  i32x16 acc[Cfg::WM][Cfg::WN];
+  MmTile t;
+  if (!mm_tile<OpI8, Cfg, kPaired>(p, smem, &t, acc)) return;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int g = lane >> 5, r32 = lane & 31;
+  const int wm = wave / Cfg::WAVES_N, wn = wave % Cfg::WAVES_N;
+  const float* ws = o.ws + static_cast<int64_t>(t.group) * o.outputs;
+#pragma unroll
+  for (int i = 0; i < Cfg::WM; ++i) {
+    const int m = (wm * Cfg::WM + i) * 32 + r32;
+    if (m >= t.rows) continue;
+    const int64_t row = t.row0 + m;
+    const float xs = o.xs[p.perm ? p.perm[row] / p.topk : row];
+#pragma unroll
+    for (int j = 0; j < Cfg::WN; ++j) {
+      const int n0 = t.nt * Cfg::BN + (wn * Cfg::WN + j) * 32;
+      if (kPaired) {
+#pragma unroll
+        for (int rr = 0; rr < 2; ++rr) {
+          const int n = n0 / 2 + 8 * rr + 4 * g;
+          float v[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int c = min(n + q, p.N - 1);
+            const float a = static_cast<float>(acc[i][j][4 * rr + q]) * xs * ws[c];
+            const float b = static_cast<float>(acc[i][j][4 * rr + 8 + q]) * xs * ws[p.N + c];
+            v[q] = silu_f(a) * b;
+          }
+          i8_store4<T>(o, row, n, v);
+        }
+      } else {
+#pragma unroll
+        for (int rr = 0; rr < 4; ++rr) {
+          const int n = n0 + 8 * rr + 4 * g;
+          float v[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int c = min(n + q, p.N - 1);
+            v[q] = static_cast<float>(acc[i][j][4 * rr + q]) * xs * ws[c] + (o.bias ? o.bias[c] : 0.0f);
+          }
+          i8_store4<T>(o, row, n, v);
+        }
+      }
+    }
+  }
+}
+
+template <typename T, typename Cfg>
+void i8_tiles(const MmArgs& a, const I8Out& o, bool paired, int64_t row_tiles, hipStream_t s) {
+  MmArgs p = a;
+  const int per = paired ? Cfg::BN / 2 : Cfg::BN;
+  p.tiles_n = (p.N + per - 1) / per;
+  const unsigned grid = static_cast<unsigned>(row_tiles * p.tiles_n);
+  if (paired)
+    MOE_LAUNCH("linear_i8_gated", (i8_tile_kernel<T, Cfg, true>), dim3(grid), dim3(Cfg::NT), 0, s, p, o);
+  else
+    MOE_LAUNCH("linear_i8", (i8_tile_kernel<T, Cfg, false>), dim3(grid), dim3(Cfg::NT), 0, s, p, o);
+}
+
+template <typename T>
+void quantize_rows_t(int64_t rows, int width, const void* x, int64_t ld, int8_t* q, float* scale,
+                     hipStream_t s) {
+  constexpr int V = Piece<T>::V;
+  const int64_t pitch = i8_pitch(width);
+#define MOE_Q(TPR, NV)                                                                            \
+  MOE_LAUNCH("quantize_rows", (quantize_rows_kernel<T, TPR, NV>),                                 \
+             dim3(static_cast<unsigned>((rows * TPR + (TPR < 256 ? 255 : TPR - 1)) / (TPR < 256 ? 256 : TPR))), \
+             dim3(TPR < 256 ? 256 : TPR), 0, s, rows, width, pitch, static_cast<const T*>(x), ld, q, scale)
+  if (pitch <= 64 * V) MOE_Q(64, 1);
+  else if (pitch <= 128 * V) MOE_Q(64, 2);
+  else if (pitch <= 256 * V) MOE_Q(256, 1);
+  else if (pitch <= 512 * V) MOE_Q(256, 2);
+  else if (pitch <= 1024 * V) MOE_Q(256, 4);
+  else MOE_Q(256, 0);
+#undef MOE_Q
+}
+
+struct I8Layout {
+  size_t q, scale, total;
+  int64_t rows;
+};
+I8Layout i8_layout(const moe_i8_linear& l) {
+  I8Layout L{};
+  L.rows = l.groups > 1 && !l.gather ? l.tokens * l.top_k : l.tokens;
+  if (l.x_dtype != MOE_I8) {
+    L.scale = align_up(static_cast<size_t>(L.rows) * i8_pitch(l.inputs), 256);
+    L.total = L.scale + align_up(static_cast<size_t>(L.rows) * sizeof(float), 256);
+  }
+  return L;
+}
+
+}  // namespace
+
+hipError_t launch_quantize_rows(int64_t rows, int width, int dtype, const void* x, int64_t ld_x,
+                                int8_t* q, float* scale, hipStream_t s) {
+  const int64_t ld = ld_x ? ld_x : width;
+  if (dtype == MOE_BF16) quantize_rows_t<bf16_t>(rows, width, x, ld, q, scale, s);
+  else quantize_rows_t<float>(rows, width, x, ld, q, scale, s);
+  return hipGetLastError();
+}
+
+hipError_t launch_quantize_weight(int groups, int width, int outputs, int dtype, const void* w,
+                                  int64_t q_rows, int8_t* q, float* scale, hipStream_t s) {
+  const dim3 grid((outputs + 63) / 64, groups);
+  const int64_t rows = q_rows ? q_rows : outputs;
+  if (dtype == MOE_BF16)
+    MOE_LAUNCH("quantize_weight", quantize_weight_kernel<bf16_t>, grid, dim3(256), 0, s, width,
+               outputs, i8_pitch(width), static_cast<const bf16_t*>(w), rows, q, scale);
+  else
+    MOE_LAUNCH("quantize_weight", quantize_weight_kernel<float>, grid, dim3(256), 0, s, width,
+               outputs, i8_pitch(width), static_cast<const float*>(w), rows, q, scale);
+  return hipGetLastError();
+}
+
+size_t linear_i8_ws_bytes(const moe_i8_linear& l) {
+  const size_t n = i8_layout(l).total;
+  return n < 256 ? 256 : n;
+}
+
+hipError_t launch_linear_i8(const moe_i8_linear& l, const void* x, const float* xs,
+                            const int8_t* wq, const float* ws, const float* bias,
+                            const moe_routing* r, void* y, void* work, hipStream_t s) {
+  const I8Layout L = i8_layout(l);
+  const int64_t pitch = i8_pitch(l.inputs);
+  const int8_t* xq = static_cast<const int8_t*>(x);
+  if (l.x_dtype != MOE_I8) {
+    int8_t* q = static_cast<int8_t*>(work);
+    float* sc = reinterpret_cast<float*>(q + L.scale);
+    const hipError_t e = launch_quantize_rows(L.rows, l.inputs, l.x_dtype, x, 0, q, sc, s);
+    if (e != hipSuccess) return e;
+    xq = q;
+    xs = sc;
+  }
+  const bool paired = l.gated != 0;
+  MmArgs p{};
+  p.a = reinterpret_cast<const char*>(xq);
+  p.a_pitch = pitch;
+  p.b = reinterpret_cast<const char*>(wq);
+  p.b_pitch = pitch;
+  p.b_group = static_cast<int64_t>(l.outputs) * pitch;
+  p.nk = static_cast<int>(pitch / kMmRow);
+  p.N = paired ? l.outputs / 2 : l.outputs;
+  p.half = p.N * pitch;
+  p.topk = l.top_k;
+  p.groups = l.groups;
+  p.cap = l.capacity;
+  if (r) {
+    p.offsets = r->expert_offsets;
+    if (l.gather) p.perm = r->perm;
+  }
+  p.M = r ? l.tokens * l.top_k : l.tokens;
+  I8Out o{xs, ws, bias, y, p.N, l.outputs};
+  auto go = [&](auto t) {
+    using T = decltype(t);
+    using Big = MmCfg<256, 256, 4, 2>;
+    using Mid = MmCfg<128, 128, 2, 2>;
+    using Low = MmCfg<32, 128, 1, 4>;
+    const int64_t per_group = p.M / p.groups;
+    const int64_t big = (p.M + 255) / 256 * ((l.outputs + 255) / 256);
+    auto tiles = [&](int bm) { return (p.M + bm - 1) / bm + (r ? p.groups : 0); };
+    if (per_group >= 256 && big >= cu_count()) i8_tiles<T, Big>(p, o, paired, tiles(256), s);
+    else if (per_group > 32) i8_tiles<T, Mid>(p, o, paired, tiles(128), s);
+    else i8_tiles<T, Low>(p, o, paired, tiles(32), s);
+  };
+  if (l.dtype == MOE_BF16) go(bf16_t{});
+  else go(float{});
+  return hipGetLastError();
+}
+
+}  // namespace moe

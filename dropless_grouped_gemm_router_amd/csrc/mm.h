@@ -1,0 +1,242 @@
+// Tiled matrix-product engine of the operators around the layer (gfx950).
+//
+//   C[m][n] = sum_k A[m][k] B[n][k]     bf16 or fp32 -> fp32, int8 -> int32
+//
+// Both operands are rows of K-contiguous bytes, a stage being 128 bytes of
+// every row (64 bf16, 32 fp32 or 128 int8), so one engine serves all types:
+// the fragments of mfma 32x32x16 bf16, of 32x32x32 i8 and of four 32x32x2
+// fp32 steps are the same 16 bytes a lane. Rows come through pointers computed once per tile, which is where
+// gathering by the expert permutation, clamping at the last row and the
+// pairing of gate and up columns happen.
+//
+// Stages go from global memory straight into LDS (no staging registers);
+// the 16-byte chunk c of LDS row r sits at position c ^ ((r >> 1) & 7), so
+// the 32 rows that a fragment read touches spread over all banks. The MFMA
+// takes the B fragment first: lane L then holds row L % 32 and runs of four
+// consecutive columns, 8 (q / 4) + 4 (L / 32) + q % 4 for register q.
+#pragma once
+
+#include "block.h"
+
+namespace moe {
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x16 __attribute__((ext_vector_type(16)));
+
+struct OpBf16 {
+  typedef f32x16_t Acc;
+  __device__ static void step(const u32x4& w, const u32x4& x, Acc& acc) {
+    acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, w),
+                                                  __builtin_bit_cast(bf16x8_t, x), acc, 0, 0, 0);
+  }
+};
+struct OpF32 {
+  typedef f32x16_t Acc;
+  // step e takes element e of each lane group's 16 bytes, on both sides
+  __device__ static void step(const u32x4& w, const u32x4& x, Acc& acc) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      acc = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(w[e]), __uint_as_float(x[e]), acc, 0, 0, 0);
+  }
+};
+struct OpI8 {
+  typedef i32x16 Acc;
+  __device__ static void step(const u32x4& w, const u32x4& x, Acc& acc) {
+    acc = __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(i32x4, w),
+                                                __builtin_bit_cast(i32x4, x), acc, 0, 0, 0);
+  }
+};
+
+struct MmArgs {
+  const char* a;
+  int64_t a_pitch;   // bytes between rows
+  const int32_t* perm;  // gather: row r reads input row perm[r] / topk
+  int topk;
+  const char* b;
+  int64_t b_pitch, b_group;  // bytes between rows, between groups
+  const char* a2;            // stages from k_split on come from a2 and b2, each
+  const char* b2;            // with its own k 0 first (null: none)
+  int k_split;
+  int nk;                    // stages
+  int64_t M;                 // dense: rows
+  int N;                     // rows of B; paired: of one half
+  const int32_t* offsets;    // routed: expert_offsets, else null
+  int groups, cap;
+  int tiles_n;
+  int64_t half;              // paired: bytes from a gate row of B to its up row
+};
+
+constexpr int kMmRow = 128;
+
+template <int BM_, int BN_, int WAVES_M_, int WAVES_N_>
+struct MmCfg {
+  static constexpr int BM = BM_, BN = BN_, WAVES_M = WAVES_M_, WAVES_N = WAVES_N_;
+  static constexpr int NW = WAVES_M * WAVES_N, NT = 64 * NW;
+  static constexpr int WM = BM / WAVES_M / 32, WN = BN / WAVES_N / 32;  // MFMA tiles per wave
+  static constexpr int A_LOADS = BM / 8 / NW, B_LOADS = BN / 8 / NW;     // a wave and stage
+  static constexpr int STAGE = (BM + BN) * kMmRow;
+  static_assert(BM == WAVES_M * WM * 32 && BN == WAVES_N * WN * 32, "tiles");
+  static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0, "loads");
+};
+
+// A tile's rows: first row, count (0: nothing to do), weight group.
+struct MmTile {
+  int64_t row0;
+  int rows, group, nt;
+};
+
+// Row tile mt of the routed rows: each lane counts one expert's tiles (at
+// most 64 experts), a prefix sum finds the expert. Uniform over the wave.
+__device__ __forceinline__ MmTile mm_routed_tile(const int32_t* offsets, int groups, int cap, int bm,
+                                                 int mt, int lane) {
+  int first = 0, count = 0;
+  if (lane < groups) {
+    first = offsets[lane];
+    count = offsets[lane + 1] - first;
+    if (cap > 0 && count > cap) count = cap;
+  }
+  const int tiles = (count + bm - 1) / bm;
+  int upto = tiles;
+#pragma unroll
+  for (int o = 1; o < 64; o *= 2) {
+    const int v = __shfl_up(upto, o);
+    if (lane >= o) upto += v;
+  }
+  const uint64_t past = __ballot(upto > mt);
+  MmTile t{0, 0, 0, 0};
+  if (past == 0) return t;
+  const int e = __ffsll(static_cast<unsigned long long>(past)) - 1;
+  const int local = mt - (__shfl(upto, e) - __shfl(tiles, e));
+  t.group = __builtin_amdgcn_readfirstlane(e);
+  t.row0 = __builtin_amdgcn_readfirstlane(__shfl(first, e) + local * bm);
+  const int left = __builtin_amdgcn_readfirstlane(__shfl(count, e) - local * bm);
+  t.rows = left < bm ? left : bm;
+  return t;
+}
+
+// Order of the dense tiles: bands of eight row tiles, column by column, so
+// that the workgroups running together share rows of A and of B in L2.
+__device__ __forceinline__ void mm_tile_order(int w, int tiles_m, int tiles_n, int* mt, int* nt) {
+  constexpr int kBand = 8;
+  const int band = w / (kBand * tiles_n), in = w % (kBand * tiles_n);
+  const int high = min(kBand, tiles_m - band * kBand);
+  *mt = band * kBand + in % high;
+  *nt = in / high;
+}
+
+// One stage's loads of one operand: NL loads a wave, of 8 rows (1 KiB) each.
+template <int NL>
+__device__ __forceinline__ void mm_issue(char* buf, const char* const* rows, int64_t off, int wave) {
+#pragma unroll
+  for (int i = 0; i < NL; ++i) {
+    const char* src = rows[i] + off;
+    char* dst = buf + (wave * NL + i) * 1024;
+    __builtin_amdgcn_global_load_lds(src, dst, 16, 0, 0);
+  }
+}
+
+template <typename Op, typename Cfg>
+__device__ __forceinline__ void mm_compute(const char* buf, int a_frag, int b_frag, int sw,
+                                           typename Op::Acc (&acc)[Cfg::WM][Cfg::WN]) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    u32x4 xf[Cfg::WM], wf[Cfg::WN];
+    const int at = ((2 * q) ^ sw) << 4;
+#pragma unroll
+    for (int i = 0; i < Cfg::WM; ++i)
+      xf[i] = *reinterpret_cast<const u32x4*>(buf + a_frag + i * 32 * kMmRow + at);
+#pragma unroll
+    for (int j = 0; j < Cfg::WN; ++j)
+      wf[j] = *reinterpret_cast<const u32x4*>(buf + b_frag + j * 32 * kMmRow + at);
+#pragma unroll
+    for (int i = 0; i < Cfg::WM; ++i)
+#pragma unroll
+      for (int j = 0; j < Cfg::WN; ++j) Op::step(wf[j], xf[i], acc[i][j]);
+  }
+}
+
+// One workgroup's tile, from its index; kPaired: B's tile holds gate rows
+// and up rows in turns of 16 (column p of the tile is gate column
+// 16 (p / 32) + p % 16 of the pair block when p % 32 < 16, else the same up
+// column), so a lane's registers 0-7 and 8-15 of an MFMA tile are matching
+// gate and up values. False: no such tile.
+template <typename Op, typename Cfg, bool kPaired>
+__device__ __forceinline__ bool mm_tile(const MmArgs& p, char* smem, MmTile* tile,
+                                        typename Op::Acc (&acc)[Cfg::WM][Cfg::WN]) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int w = xcd_remap(blockIdx.x, gridDim.x);
+  MmTile t{0, 0, 0, 0};
+  if (p.offsets) {
+    t = mm_routed_tile(p.offsets, p.groups, p.cap, Cfg::BM, w / p.tiles_n, lane);
+    t.nt = w % p.tiles_n;
+    if (t.rows <= 0) return false;
+  } else {
+    int mt;
+    mm_tile_order(w, static_cast<int>((p.M + Cfg::BM - 1) / Cfg::BM), p.tiles_n, &mt, &t.nt);
+    t.row0 = static_cast<int64_t>(mt) * Cfg::BM;
+    const int64_t left = p.M - t.row0;
+    t.rows = left < Cfg::BM ? static_cast<int>(left) : Cfg::BM;
+  }
+  *tile = t;
+
+  // Load i of a wave covers rows (wave LOADS + i) 8 + lane / 8 of an operand's
+  // tile, lane l's 16 bytes landing at position l % 8 of the row: the chunk
+  // that belongs there is (l % 8) ^ ((row >> 1) & 7). Rows past the tile
+  // repeat its last row; what they compute is not stored.
+  const char* a[Cfg::A_LOADS];
+  const char* b[Cfg::B_LOADS];
+#pragma unroll
+  for (int i = 0; i < Cfg::A_LOADS; ++i) {
+    const int r = (wave * Cfg::A_LOADS + i) * 8 + (lane >> 3);
+    int64_t src = t.row0 + min(r, t.rows - 1);
+    if (p.perm) src = p.perm[src] / p.topk;
+    a[i] = p.a + src * p.a_pitch + (((lane & 7) ^ ((r >> 1) & 7)) << 4);
+  }
+#pragma unroll
+  for (int i = 0; i < Cfg::B_LOADS; ++i) {
+    const int r = (wave * Cfg::B_LOADS + i) * 8 + (lane >> 3);
+    int64_t off;
+    if (kPaired) {
+      const int c = t.nt * (Cfg::BN / 2) + 16 * (r >> 5) + (r & 15);
+      off = min(c, p.N - 1) * p.b_pitch + ((r & 16) ? p.half : 0);
+    } else {
+      off = min(t.nt * Cfg::BN + r, p.N - 1) * p.b_pitch;
+    }
+    b[i] = p.b + t.group * p.b_group + off + (((lane & 7) ^ ((r >> 1) & 7)) << 4);
+  }
+  const int split = p.b2 ? p.k_split : p.nk;
+  const int64_t a2 = p.b2 ? (p.a2 - p.a) - static_cast<int64_t>(split) * kMmRow : 0;
+  const int64_t b2 = p.b2 ? (p.b2 - p.b) - static_cast<int64_t>(split) * kMmRow : 0;
+
+  const int g = lane >> 5, r32 = lane & 31;
+  const int wm = wave / Cfg::WAVES_N, wn = wave % Cfg::WAVES_N;
+  const int a_frag = (wm * Cfg::WM * 32 + r32) * kMmRow;
+  const int b_frag = (Cfg::BM + wn * Cfg::WN * 32 + r32) * kMmRow;
+  const int sw = g ^ ((r32 >> 1) & 7);
+#pragma unroll
+  for (int i = 0; i < Cfg::WM; ++i)
+#pragma unroll
+    for (int j = 0; j < Cfg::WN; ++j)
+#pragma unroll
+      for (int q = 0; q < 16; ++q) acc[i][j][q] = 0;
+
+  mm_issue<Cfg::A_LOADS>(smem, a, 0, wave);
+  mm_issue<Cfg::B_LOADS>(smem + Cfg::BM * kMmRow, b, 0, wave);
+  for (int s = 0; s < p.nk; ++s) {
+    // this wave's loads of stage s have landed, then everyone's have, and
+    // the other buffer's readers are done
+    __builtin_amdgcn_s_waitcnt(0 | (0x7 << 4) | (0x0 << 8));
+    asm volatile("s_barrier" ::: "memory");
+    if (s + 1 < p.nk) {
+      const int64_t off = static_cast<int64_t>(s + 1) * kMmRow;
+      const bool first = s + 1 < split;
+      char* next = smem + ((s + 1) & 1) * Cfg::STAGE;
+      mm_issue<Cfg::A_LOADS>(next, a, off + (first ? 0 : a2), wave);
+      mm_issue<Cfg::B_LOADS>(next + Cfg::BM * kMmRow, b, off + (first ? 0 : b2), wave);
+    }
+    mm_compute<Op, Cfg>(smem + (s & 1) * Cfg::STAGE, a_frag, b_frag, sw, acc);
+  }
+  return true;
+}
+
+}  // namespace moe

@@ -1,0 +1,209 @@
+"""The operators around the layer on the host, no GPU: the library exports
+every symbol include/moe_block.h declares, sizes, and every argument check,
+all of which run before any HIP call."""
+
+import ctypes
+import os
+import re
+
+import pytest
+
+from dropless_grouped_gemm_router_amd import binding as B
+from dropless_grouped_gemm_router_amd import block as K
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+INV, UNS, WS = B.MOE_ERR_INVALID, B.MOE_ERR_UNSUPPORTED, -3
+
+
+class At:
+    """Host stand-in for a tensor: an address that is never dereferenced."""
+
+    def __init__(self, addr, nbytes=1 << 40):
+        self.addr, self.nbytes = addr, nbytes
+
+    def data_ptr(self):
+        return self.addr
+
+    def numel(self):
+        return self.nbytes
+
+    def element_size(self):
+        return 1
+
+
+A, C, D, E, F, G, H = (At((i + 1) << 28) for i in range(7))
+ODD2, ODD4, ODD16 = At((1 << 28) + 2), At((1 << 28) + 4), At((1 << 28) + 16)
+
+
+def refused(code, fn, *a, **k):
+    with pytest.raises(B.MoeError) as e:
+        fn(*a, **k)
+    assert e.value.status == code
+
+
+def test_exports_every_declared_symbol():
+    src = open(os.path.join(ROOT, "include", "moe_block.h")).read()
+    src = re.sub(r"/\*.*?\*/", "", src, flags=re.S)
+    names = sorted(set(re.findall(r"\b(moe_[a-z0-9_]+)\s*\(", src)))
+    assert sorted(K.EXPORTED) == names
+    lib = K.load()
+    for n in names:
+        assert hasattr(lib, n), n
+
+
+def norm(rows=10, width=512, dtype=1, eps=1e-5, ld=(0, 0, 0, 0)):
+    return K.moe_norm(rows, width, dtype, eps, *ld)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(rows=-1), INV), (dict(width=0), INV), (dict(dtype=2), INV), (dict(eps=-1.0), INV),
+    (dict(eps=float("nan")), INV), (dict(eps=float("inf")), INV), (dict(ld=(511, 0, 0, 0)), INV),
+    (dict(ld=(0, 511, 0, 0)), INV), (dict(ld=(0, 0, 1, 0)), INV), (dict(ld=(0, 0, 0, -5)), INV),
+    (dict(width=16385), UNS), (dict(rows=1 << 31), UNS), (dict(ld=(1 << 31, 0, 0, 0)), UNS)])
+def test_norm_problem_refusals(kw, code):
+    refused(code, K.moe_layer_norm, norm(**kw), A, C, D, E, None, None, stream=0)
+    refused(code, K.moe_layer_norm_bwd, norm(**kw), A, C, D, E, F, G, H, H, A, stream=0)
+    assert K.moe_layer_norm_workspace_bytes(norm(**kw)) == 0
+
+
+def test_norm_argument_refusals():
+    fwd, bwd = K.moe_layer_norm, K.moe_layer_norm_bwd
+    refused(INV, fwd, norm(), None, C, D, E, None, None, stream=0)
+    refused(INV, fwd, norm(), At(0x1001), C, D, E, None, None, stream=0)
+    refused(INV, fwd, norm(dtype=0), ODD2, C, D, E, None, None, stream=0)
+    refused(INV, fwd, norm(), A, ODD2, D, E, None, None, stream=0)
+    refused(INV, fwd, norm(), A, C, D, None, None, None, stream=0)
+    refused(INV, fwd, norm(), A, C, D, E, F, None, stream=0)
+    refused(INV, fwd, norm(), A, C, D, E, None, F, stream=0)
+    need = K.moe_layer_norm_workspace_bytes(norm())
+    assert need >= 2 * 512 * 4
+    refused(WS, bwd, norm(), A, C, D, E, F, G, H, H, A, workspace_bytes=need - 1, stream=0)
+    refused(INV, bwd, norm(), A, C, D, E, F, G, H, H, ODD16, workspace_bytes=need, stream=0)
+    refused(INV, bwd, norm(), A, C, None, E, F, G, H, H, A, stream=0)
+    refused(INV, bwd, norm(), A, C, D, E, F, None, H, H, A, stream=0)
+    refused(INV, bwd, norm(), A, C, D, E, F, G, ODD2, H, A, stream=0)
+    fwd(norm(rows=0), None, None, None, None, None, None, stream=0)
+    bwd(norm(rows=0), None, None, None, None, None, None, None, None, None, stream=0)
+
+
+def ffn(tokens=10, d=256, h=512, dtype=1, act=0, grad=0):
+    return K.moe_ffn(tokens, d, h, dtype, act, grad)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(tokens=-1), INV), (dict(d=0), INV), (dict(h=0), INV), (dict(dtype=2), INV),
+    (dict(act=-1), INV), (dict(act=4), INV), (dict(dtype=0, grad=1), INV), (dict(grad=2), INV),
+    (dict(d=32769), UNS), (dict(h=32769), UNS), (dict(tokens=1 << 31), UNS),
+    (dict(tokens=1 << 25, h=32768), UNS)])
+def test_ffn_problem_refusals(kw, code):
+    f = ffn(**kw)
+    refused(code, K.moe_gated_ffn, f, A, C, D, E, None, F, G, stream=0)
+    refused(code, K.moe_gated_ffn_bwd, f, A, C, D, E, F, G, H, H, H, H, A, stream=0)
+    assert K.moe_gated_ffn_workspace_bytes(f) == K.moe_gated_ffn_saved_bytes(f) == 0
+
+
+def test_ffn_argument_refusals():
+    fwd, bwd, f = K.moe_gated_ffn, K.moe_gated_ffn_bwd, ffn()
+    for i in range(4):
+        args = [A, C, D, E]
+        args[i] = None
+        refused(INV, fwd, f, *args, None, F, G, stream=0)
+        args[i] = ODD4
+        refused(INV, fwd, f, *args, None, F, G, stream=0)
+    refused(INV, fwd, f, A, C, D, E, ODD16, F, G, stream=0)
+    refused(INV, fwd, f, A, C, D, E, None, None, G, stream=0)
+    refused(INV, fwd, f, A, C, D, E, None, F, ODD16, stream=0)
+    for training in (False, True):
+        need = K.moe_gated_ffn_workspace_bytes(f, training)
+        refused(WS, fwd, f, A, C, D, E, H if training else None, F, G, workspace_bytes=need - 1, stream=0)
+    refused(WS, bwd, f, A, C, D, E, F, G, H, H, H, H, A, workspace_bytes=need - 1, stream=0)
+    for i in range(11):
+        args = [A, C, D, E, F, G, H, H, H, H, A]
+        args[i] = None
+        refused(INV, bwd, f, *args, workspace_bytes=need, stream=0)
+    fwd(ffn(tokens=0), None, None, None, None, None, None, None, stream=0)
+    refused(INV, bwd, ffn(tokens=0), None, None, None, None, None, None, None, None, None, None, None, stream=0)
+
+
+def i8(tokens=10, inputs=512, outputs=256, x=1, y=1, groups=1, top_k=1, gather=0, gated=0, cap=0):
+    return K.moe_i8_linear(tokens, inputs, outputs, x, y, groups, top_k, gather, gated, cap)
+
+
+ROUTING = {"expert_offsets": A, "perm": C}
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(tokens=-1), INV), (dict(inputs=0), INV), (dict(outputs=0), INV), (dict(groups=0), INV),
+    (dict(top_k=0), INV), (dict(cap=-1), INV), (dict(x=3), INV), (dict(y=2), INV),
+    (dict(gather=2), INV), (dict(gated=-1), INV), (dict(gated=1, outputs=255), INV),
+    (dict(groups=4, top_k=5), INV), (dict(groups=65, top_k=2), UNS), (dict(inputs=65537), UNS),
+    (dict(outputs=65537), UNS), (dict(groups=8, tokens=1 << 30, top_k=2), UNS),
+    (dict(tokens=1 << 30, outputs=65536), UNS)])
+def test_i8_problem_refusals(kw, code):
+    l = i8(**kw)
+    refused(code, K.moe_linear_i8, l, A, None, C, D, None, ROUTING, E, F, stream=0)
+    assert K.moe_linear_i8_workspace_bytes(l) == 0
+
+
+def test_i8_argument_refusals():
+    fn, l = K.moe_linear_i8, i8()
+    for i, name in enumerate("x wq ws y".split()):
+        args = dict(x=A, wq=C, ws=D, y=E)
+        args[name] = None
+        refused(INV, fn, l, args["x"], None, args["wq"], args["ws"], None, None, args["y"], F, stream=0)
+    refused(INV, fn, l, ODD4, None, C, D, None, None, E, F, stream=0)
+    refused(INV, fn, l, A, None, C, D, ODD2, None, E, F, stream=0)
+    refused(INV, fn, l, A, None, C, D, None, None, E, None, stream=0)
+    refused(WS, fn, l, A, None, C, D, None, None, E, F,
+            workspace_bytes=K.moe_linear_i8_workspace_bytes(l) - 1, stream=0)
+    refused(INV, fn, i8(x=K.MOE_I8), A, None, C, D, None, None, E, None, stream=0)
+    refused(UNS, fn, i8(gated=1), A, None, C, D, G, None, E, F, stream=0)
+    # routed arguments need a routing
+    for kw in (dict(groups=4), dict(gather=1), dict(cap=3)):
+        refused(INV, fn, i8(**kw), A, None, C, D, None, None, E, F, stream=0)
+    r = i8(groups=4, top_k=2, gather=1)
+    refused(INV, fn, r, A, None, C, D, None, {"expert_offsets": A, "perm": None}, E, F, stream=0)
+    refused(INV, fn, r, A, None, C, D, None, {"expert_offsets": None, "perm": A}, E, F, stream=0)
+    fn(i8(tokens=0), None, None, None, None, None, None, None, None, stream=0)
+
+
+def test_quantize_refusals():
+    rows, weight = K.moe_quantize_rows, K.moe_quantize_weight
+    assert [K.moe_i8_pitch(w) for w in (-1, 0, 1, 128, 129)] == [0, 0, 128, 128, 256]
+    for a, code in (((-1, 8, 0, A, 0), INV), ((1, 0, 0, A, 0), INV), ((1, 8, 2, A, 0), INV),
+                    ((1, 8, 0, A, 7), INV), ((1, 65537, 0, A, 0), UNS), ((1 << 31, 8, 0, A, 0), UNS),
+                    ((1, 8, 0, None, 0), INV), ((1, 8, 0, ODD2, 0), INV)):
+        refused(code, rows, *a, C, D, stream=0)
+    refused(INV, rows, 1, 8, 0, A, 0, ODD4, D, stream=0)
+    rows(0, 8, 0, None, 0, None, None, stream=0)
+    for a, code in (((0, 8, 8, 0, A, 0), INV), ((1, 0, 8, 0, A, 0), INV), ((1, 8, 0, 0, A, 0), INV),
+                    ((1, 8, 8, 5, A, 0), INV), ((1, 8, 8, 0, A, 7), INV), ((65, 8, 8, 0, A, 0), UNS),
+                    ((1, 65537, 8, 0, A, 0), UNS), ((1, 8, 8, 0, None, 0), INV)):
+        refused(code, weight, *a, C, D, stream=0)
+
+
+def test_tensor_checks():
+    """The tensor front ends refuse CPU tensors and wrong shapes or types
+    before anything reaches the library."""
+    import torch
+    x = torch.zeros(4, 8)
+    buf = K.NormBuffers(y=torch.zeros(4, 8), mean=torch.zeros(4), rstd=torch.zeros(4))
+    with pytest.raises(ValueError, match="GPU"):
+        K.layer_norm(x, None, None, 1e-5, buf)
+    with pytest.raises(ValueError, match="weight"):
+        K.layer_norm(x, torch.zeros(9), None, 1e-5, buf)
+    with pytest.raises(ValueError, match="y: "):
+        K.layer_norm(x.bfloat16(), None, None, 1e-5, buf)
+    with pytest.raises(ValueError, match="contiguous"):
+        K.layer_norm(torch.zeros(8, 4).t(), None, None, 1e-5, buf)
+    f = K.GatedFfn(4, 8, 16, "fp32")
+    w = dict(w_gate=torch.zeros(8, 16), w_up=torch.zeros(8, 16), w_down=torch.zeros(8, 16))
+    with pytest.raises(ValueError, match="w_down"):
+        K.gated_ffn(f, x, w, K.FfnBuffers(out=x, workspace=x))
+    l = K.LinearI8(4, 8, 16, "fp32")
+    with pytest.raises(ValueError, match="weights"):
+        K.linear_i8(l, x, torch.zeros(1, 16, 8, dtype=torch.int8), torch.zeros(1, 16),
+                    K.I8Buffers(y=torch.zeros(4, 16), workspace=x))
+    with pytest.raises(ValueError, match="x_scale"):
+        K.linear_i8(l, torch.zeros(4, 128, dtype=torch.int8), torch.zeros(1, 16, 128, dtype=torch.int8),
+                    torch.zeros(1, 16), K.I8Buffers(y=torch.zeros(4, 16), workspace=x))
