@@ -81,6 +81,19 @@ __device__ __forceinline__ void store_piece(T* row, int c, int n, const float (&
     if (c + q < n) put(row + c + q, v[q]);
 }
 
+// Eight consecutive columns n.. of a row of `width`, fp32 in, stored as T.
+template <typename T>
+__device__ __forceinline__ void store8(T* row, int n, int width, const float (&v)[8]) {
+  constexpr int V = Piece<T>::V;
+#pragma unroll
+  for (int h = 0; h < 8 / V; ++h) {
+    float e[V];
+#pragma unroll
+    for (int q = 0; q < V; ++q) e[q] = v[h * V + q];
+    if (n + h * V < width) store_piece(row, n + h * V, width, e);
+  }
+}
+
 // ------------------------------------------------------------- reductions
 
 // Sum and maximum over the 64 lanes, in every lane: four data-parallel

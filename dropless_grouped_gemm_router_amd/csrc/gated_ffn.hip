@@ -54,23 +54,47 @@ __device__ __forceinline__ float act_value(float a, float* slope) {
 
 // ---------------------------------------------------------- layout changes
 
-// dst[n][kp] from src[k][n]: 32 x 32 blocks through LDS; zeros for k >= K.
+// dst[n][kp] from src[k][n]: 64 x 64 blocks through LDS; zeros for k >= K.
+// Up to three matrices in one launch, the flat block index running over them.
+struct TurnJob {
+  const void* src;
+  void* dst;
+  int K, N;
+  int64_t kp;
+  int end;  // exclusive end of the job's blocks
+};
+struct TurnJobs {
+  TurnJob job[3];
+};
 template <typename T>
-__global__ __launch_bounds__(256) void turn_kernel(const T* __restrict__ src, T* __restrict__ dst,
-                                                   int K, int N, int64_t kp) {
-  __shared__ T tile[32][33];
-  const int n0 = blockIdx.x * 32, k0 = blockIdx.y * 32;
-  const int c = threadIdx.x & 31, r = threadIdx.x >> 5;
+__global__ __launch_bounds__(256) void turn_kernel(const TurnJobs jobs) {
+  constexpr int V = Piece<T>::V, P = 64 / V;  // pieces of a block's row
+  __shared__ T tile[64][64 + 4 / sizeof(T)];
+  const int blk = blockIdx.x;
+  const int which = blk < jobs.job[0].end ? 0 : (blk < jobs.job[1].end ? 1 : 2);
+  const TurnJob& b = jobs.job[which];
+  const int local = blk - (which ? jobs.job[which - 1].end : 0);
+  const int across = (b.N + 63) / 64;
+  const int n0 = local % across * 64, k0 = local / across * 64;
+  const T* src = static_cast<const T*>(b.src);
+  T* dst = static_cast<T*>(b.dst);
+  for (int i = threadIdx.x; i < 64 * P; i += 256) {
+    const int k = i / P, c = i % P * V;
+    u32x4 v = (u32x4){0u, 0u, 0u, 0u};
+    if (k0 + k < b.K && n0 + c < b.N) v = load_piece(src + static_cast<int64_t>(k0 + k) * b.N, n0 + c, b.N);
+    const T* e = reinterpret_cast<const T*>(&v);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int k = k0 + r + 8 * i, n = n0 + c;
-    tile[r + 8 * i][c] = (k < K && n < N) ? src[static_cast<int64_t>(k) * N + n] : T{};
+    for (int q = 0; q < V; ++q) tile[k][c + q] = e[q];
   }
   __syncthreads();
+  for (int i = threadIdx.x; i < 64 * P; i += 256) {
+    const int n = i / P, c = i % P * V;
+    if (n0 + n >= b.N) continue;  // kp is a multiple of 128: whole blocks of k
+    u32x4 v;
+    T* e = reinterpret_cast<T*>(&v);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int n = n0 + r + 8 * i, k = k0 + c;
-    if (n < N && k < kp) dst[n * kp + k] = tile[c][r + 8 * i];
+    for (int q = 0; q < V; ++q) e[q] = tile[c + q][n];
+    *reinterpret_cast<u32x4*>(dst + (n0 + n) * b.kp + k0 + c) = v;
   }
 }
 
@@ -91,25 +115,89 @@ __global__ __launch_bounds__(256) void pad_rows_kernel(const T* __restrict__ src
 // ----------------------------------------------------------------- products
 
 struct FfnOut {
-  void* c;        // plain: the result
+  void* c;       // plain: the result
   int64_t ldc;
-  void *h, *a, *b;  // gated: hidden values and (training) both pre-activations
-  const void *sa, *sb;  // gradient: the pre-activations read
-  void *da, *db;        // gradient: the results
-  int64_t ld;           // columns kept of the hidden matrices (a multiple of 128)
+  void* h;       // gated: the hidden values
+  // What the backward needs of the pre-activations: f = act(a) and
+  // p = b act'(a), so that da = dh p and db = dh f. In bf16 each is kept as
+  // its high half (f, p) and the next four mantissa bits, both in one byte of
+  // `low`: 5 bytes a pair instead of 4, and a rounding of 2^-13 instead of
+  // 2^-9, which leaves the roundings of da, db and the result as the only
+  // ones that count in the gradients.
+  void *f, *p;
+  uint8_t* low;
+  int64_t ld;    // columns kept of the hidden matrices (a multiple of 128)
+  void* dab;     // gradient: da and db, a row of each side by side
 };
 
-// Columns n .. n + 3 of a row that keeps `width` columns.
-template <typename T>
-__device__ __forceinline__ void store4_any(T* row, int n, int64_t width, const float (&v)[4]) {
-  if (n + 4 <= width && width % 4 == 0) {
-    store4(row + n, v[0], v[1], v[2], v[3]);
-    return;
-  }
-#pragma unroll
-  for (int q = 0; q < 4; ++q)
-    if (n + q < width) put(row + n + q, v[q]);
+// The 20 high bits of a value, rounded: 16 to the result, four to *low.
+// Infinities and NaN stay what they are.
+__device__ __forceinline__ uint32_t split20(float v, uint32_t* low) {
+  uint32_t u = __float_as_uint(v);
+  const uint32_t m = u & 0x7fffffffu;
+  u = m < 0x7f800000u ? u + 0x800u : (m > 0x7f800000u ? u | 0x400000u : u);
+  *low = (u >> 12) & 15u;
+  return u >> 16;
 }
+
+// What is kept of eight values of f and p, and back.
+__device__ __forceinline__ void keep8(const FfnOut& o, int64_t at, const float (&f)[8],
+                                      const float (&p)[8], const bf16_t*) {
+  u32x4 fh, ph;
+  uint32_t lo[2] = {0, 0};
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    uint32_t fl, pl;
+    const uint32_t a = split20(f[q], &fl), b = split20(p[q], &pl);
+    fh[q / 2] = (q & 1) ? fh[q / 2] | (a << 16) : a;
+    ph[q / 2] = (q & 1) ? ph[q / 2] | (b << 16) : b;
+    lo[q / 4] |= (fl | (pl << 4)) << (8 * (q % 4));
+  }
+  *reinterpret_cast<u32x4*>(static_cast<bf16_t*>(o.f) + at) = fh;
+  *reinterpret_cast<u32x4*>(static_cast<bf16_t*>(o.p) + at) = ph;
+  *reinterpret_cast<uint2*>(o.low + at) = make_uint2(lo[0], lo[1]);
+}
+__device__ __forceinline__ void keep8(const FfnOut& o, int64_t at, const float (&f)[8],
+                                      const float (&p)[8], const float*) {
+  store4(static_cast<float*>(o.f) + at, f[0], f[1], f[2], f[3]);
+  store4(static_cast<float*>(o.f) + at + 4, f[4], f[5], f[6], f[7]);
+  store4(static_cast<float*>(o.p) + at, p[0], p[1], p[2], p[3]);
+  store4(static_cast<float*>(o.p) + at + 4, p[4], p[5], p[6], p[7]);
+}
+
+template <typename T>
+struct Kept;
+template <>
+struct Kept<bf16_t> {
+  u32x4 f, p;
+  uint2 low;
+  __device__ void load(const FfnOut& o, int64_t at) {
+    f = *reinterpret_cast<const u32x4*>(static_cast<const bf16_t*>(o.f) + at);
+    p = *reinterpret_cast<const u32x4*>(static_cast<const bf16_t*>(o.p) + at);
+    low = *reinterpret_cast<const uint2*>(o.low + at);
+  }
+  __device__ void get(int q, float* fv, float* pv) const {
+    const uint32_t lo = ((q < 4 ? low.x : low.y) >> (8 * (q % 4))) & 0xffu;
+    const uint32_t a = (q & 1) ? f[q / 2] & 0xffff0000u : f[q / 2] << 16;
+    const uint32_t b = (q & 1) ? p[q / 2] & 0xffff0000u : p[q / 2] << 16;
+    *fv = __uint_as_float(a | ((lo & 15u) << 12));
+    *pv = __uint_as_float(b | ((lo >> 4) << 12));
+  }
+};
+template <>
+struct Kept<float> {
+  float f[8], p[8];
+  __device__ void load(const FfnOut& o, int64_t at) {
+    load4(static_cast<const float*>(o.f) + at, f);
+    load4(static_cast<const float*>(o.f) + at + 4, f + 4);
+    load4(static_cast<const float*>(o.p) + at, p);
+    load4(static_cast<const float*>(o.p) + at + 4, p + 4);
+  }
+  __device__ void get(int q, float* fv, float* pv) const {
+    *fv = f[q];
+    *pv = p[q];
+  }
+};
 
 enum { kPlain = 0, kGated = 1, kGatedGrad = 2 };
 
@@ -122,100 +210,126 @@ struct OpOf<float> {
   typedef OpF32 type;
 };
 
+// The callbacks of mm_drain. Columns past p.N (the hidden matrices' padding)
+// are written as zeros.
+template <typename T, int kMode, int kAct, int kPasses>
+struct FfnRows {
+  const MmArgs& p;
+  const FfnOut& o;
+  const MmTile& t;
+  int base, n;
+  Kept<T> kept[kMode == kGatedGrad ? kPasses : 1];
+
+  __device__ void cols(int c) { n = base + c; }
+  __device__ void pre(int k, int m) {
+    if (kMode == kGatedGrad && n < o.ld) kept[k].load(o, (t.row0 + min(m, t.rows - 1)) * o.ld + n);
+  }
+  __device__ void row(int k, int m, const uint32_t (&v)[8]) {
+    if (m >= t.rows) return;
+    const int64_t row = t.row0 + m;
+    if (kMode == kPlain) {
+      float y[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) y[q] = __uint_as_float(v[q]);
+      store8(static_cast<T*>(o.c) + row * o.ldc, n, p.N, y);
+      return;
+    }
+    if (n >= o.ld) return;
+    float da[8], db[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      float fv, pv;
+      kept[kMode == kGatedGrad ? k : 0].get(q, &fv, &pv);
+      const float dh = __uint_as_float(v[q]);
+      const bool in = n + q < p.N;
+      da[q] = in ? dh * pv : 0.0f;
+      db[q] = in ? dh * fv : 0.0f;
+    }
+    T* dst = static_cast<T*>(o.dab) + row * 2 * o.ld;
+    store8(dst, n, static_cast<int>(o.ld), da);
+    store8(dst + o.ld, n, static_cast<int>(o.ld), db);
+  }
+  __device__ void row(int, int m, const uint32_t (&g)[8], const uint32_t (&u)[8]) {
+    if (m >= t.rows || n >= o.ld) return;
+    float h[8], f[8], s[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const bool in = n + q < p.N;
+      const float b = __uint_as_float(u[q]);
+      float slope;
+      const float fv = act_value<kAct>(__uint_as_float(g[q]), &slope);
+      h[q] = in ? fv * b : 0.0f;
+      f[q] = in ? fv : 0.0f;
+      s[q] = in ? b * slope : 0.0f;
+    }
+    store8(static_cast<T*>(o.h) + (t.row0 + m) * o.ld, n, static_cast<int>(o.ld), h);
+    if (o.f) keep8(o, (t.row0 + m) * o.ld + n, f, s, static_cast<const T*>(nullptr));
+  }
+};
+
 template <typename T, typename Cfg, int kMode, int kAct>
-__global__ __launch_bounds__(Cfg::NT) __attribute__((amdgpu_waves_per_eu(Cfg::NT == 512 ? 2 : 1)))
+__global__ __launch_bounds__(Cfg::NT) __attribute__((amdgpu_waves_per_eu(2)))
 void ffn_tile_kernel(const MmArgs p, const FfnOut o) {
   __shared__ __attribute__((aligned(1024))) char smem[2 * Cfg::STAGE];
   f32x16_t acc[Cfg::WM][Cfg::WN];
   MmTile t;
-  if (!mm_tile<typename OpOf<T>::type, Cfg, kMode == kGated>(p, smem, &t, acc)) return;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int g = lane >> 5, r32 = lane & 31;
-  const int wm = wave / Cfg::WAVES_N, wn = wave % Cfg::WAVES_N;
-#pragma unroll
-  for (int i = 0; i < Cfg::WM; ++i) {
-    const int m = (wm * Cfg::WM + i) * 32 + r32;
-    if (m >= t.rows) continue;
-    const int64_t row = t.row0 + m;
-#pragma unroll
-    for (int j = 0; j < Cfg::WN; ++j) {
-      const int n0 = t.nt * Cfg::BN + (wn * Cfg::WN + j) * 32;
-#pragma unroll
-      for (int rr = 0; rr < (kMode == kGated ? 2 : 4); ++rr) {
-        const int n = (kMode == kGated ? n0 / 2 : n0) + 8 * rr + 4 * g;
-        if (kMode == kPlain) {
-          const float v[4] = {acc[i][j][4 * rr], acc[i][j][4 * rr + 1], acc[i][j][4 * rr + 2],
-                              acc[i][j][4 * rr + 3]};
-          store4_any(static_cast<T*>(o.c) + row * o.ldc, n, o.ldc, v);
-          continue;
-        }
-        if (n >= o.ld) continue;
-        if (kMode == kGated) {
-          float h[4], a[4], b[4];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const bool in = n + q < p.N;  // zeros in the padding
-            a[q] = in ? acc[i][j][4 * rr + q] : 0.0f;
-            b[q] = in ? acc[i][j][4 * rr + 8 + q] : 0.0f;
-            float slope;
-            h[q] = act_value<kAct>(a[q], &slope) * b[q];
-          }
-          store4(static_cast<T*>(o.h) + row * o.ld + n, h[0], h[1], h[2], h[3]);
-          if (o.a) {
-            store4(static_cast<T*>(o.a) + row * o.ld + n, a[0], a[1], a[2], a[3]);
-            store4(static_cast<T*>(o.b) + row * o.ld + n, b[0], b[1], b[2], b[3]);
-          }
-        } else {
-          float a[4], b[4], da[4], db[4];
-          load4(static_cast<const T*>(o.sa) + row * o.ld + n, a);
-          load4(static_cast<const T*>(o.sb) + row * o.ld + n, b);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const float dh = n + q < p.N ? acc[i][j][4 * rr + q] : 0.0f;
-            float slope;
-            const float f = act_value<kAct>(a[q], &slope);
-            da[q] = dh * b[q] * slope;
-            db[q] = dh * f;
-          }
-          store4(static_cast<T*>(o.da) + row * o.ld + n, da[0], da[1], da[2], da[3]);
-          store4(static_cast<T*>(o.db) + row * o.ld + n, db[0], db[1], db[2], db[3]);
-        }
-      }
-    }
-  }
+  constexpr bool kPaired = kMode == kGated;
+  if (!mm_tile<typename OpOf<T>::type, Cfg, kPaired>(p, smem, &t, acc)) return;
+  FfnRows<T, kMode, kAct, mm_passes<Cfg, kPaired>()> rows{p, o, t, t.nt * (kPaired ? Cfg::BN / 2 : Cfg::BN)};
+  mm_drain<Cfg, kPaired>(smem, acc, rows);
 }
 
-// Weight gradients from the slices' partial sums [splits][Mp][Np], cropped to
-// M x N and rounded once: the slices are added in order.
+// Weight gradients from the slices' partial sums [splits][mp][ld], cropped
+// to M x N at column `col` and rounded once: the slices are added in order.
+// Up to three gradients in one launch.
+struct SliceJob {
+  const float* part;
+  int splits;
+  int64_t stride;  // floats between slices
+  int64_t ld;
+  int M, N;
+  void* out;
+  int64_t end;     // exclusive end of the job's four-column pieces
+};
+struct SliceJobs {
+  SliceJob job[3];
+};
 template <typename G>
-__global__ __launch_bounds__(256) void slice_sum_kernel(const float* __restrict__ part, int splits,
-                                                        int64_t mp, int64_t np, int M, int N,
-                                                        G* __restrict__ out) {
-  const int per = (N + 3) / 4;
-  const int64_t total = static_cast<int64_t>(M) * per, stride = mp * np / 4;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < total;
+__global__ __launch_bounds__(256) void slice_sum_kernel(const SliceJobs jobs) {
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < jobs.job[2].end;
        i += static_cast<int64_t>(gridDim.x) * 256) {
-    const int64_t m = i / per;
-    const int n = static_cast<int>(i % per) * 4;
-    const float4* src = reinterpret_cast<const float4*>(part + m * np + n);
+    const int which = i < jobs.job[0].end ? 0 : (i < jobs.job[1].end ? 1 : 2);
+    const SliceJob& b = jobs.job[which];
+    const int64_t local = i - (which ? jobs.job[which - 1].end : 0);
+    const int per = (b.N + 3) / 4;
+    const int64_t m = local / per;
+    const int n = static_cast<int>(local % per) * 4;
+    const float* src = b.part + m * b.ld + n;
     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     constexpr int kBatch = 8;
     int s = 0;
-    for (; s + kBatch <= splits; s += kBatch) {
+    for (; s + kBatch <= b.splits; s += kBatch) {
       float4 v[kBatch];
 #pragma unroll
-      for (int u = 0; u < kBatch; ++u) v[u] = src[(s + u) * stride];
+      for (int u = 0; u < kBatch; ++u) v[u] = *reinterpret_cast<const float4*>(src + (s + u) * b.stride);
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
         acc.x += v[u].x; acc.y += v[u].y; acc.z += v[u].z; acc.w += v[u].w;
       }
     }
-    for (; s < splits; ++s) {
-      const float4 v = src[s * stride];
+    for (; s < b.splits; ++s) {
+      const float4 v = *reinterpret_cast<const float4*>(src + s * b.stride);
       acc.x += v.x; acc.y += v.y; acc.z += v.z; acc.w += v.w;
     }
     const float v[4] = {acc.x, acc.y, acc.z, acc.w};
-    store4_any(out + m * N, n, N, v);
+    G* dst = static_cast<G*>(b.out) + m * b.N + n;
+    if (n + 4 <= b.N && b.N % 4 == 0) {
+      store4(dst, v[0], v[1], v[2], v[3]);
+    } else {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (n + q < b.N) put(dst + q, v[q]);
+    }
   }
 }
 
@@ -232,7 +346,7 @@ struct FfnBlockLayout {
   // forward workspace: turned weights, padded x, hidden values (inference)
   size_t tg, tu, td, xp, h;
   // backward workspace
-  size_t dyp, wgp, wup, wdp, da, db, part, zero;
+  size_t dyp, wgp, wup, wdp, dab, part_gu, part_d, zero;
   size_t total;
   int splits_gu, splits_d;
 };
@@ -268,13 +382,12 @@ FfnBlockLayout ffn_block_layout(const moe_ffn& f, bool training) {
     L.wgp = take(h == hp ? 0 : d * hp * es);
     L.wup = take(h == hp ? 0 : d * hp * es);
     L.wdp = take(d == dp ? 0 : h * dp * es);
-    L.da = take(T * hp * es);
-    L.db = take(T * hp * es);
+    L.dab = take(T * 2 * hp * es);
     const int64_t tiles = static_cast<int64_t>(dp / 128) * (hp / 128);
     L.splits_gu = slices(f.tokens, 2 * tiles);
     L.splits_d = slices(f.tokens, tiles);
-    const size_t gu = static_cast<size_t>(L.splits_gu) * 2, dn = L.splits_d;
-    L.part = take((gu > dn ? gu : dn) * dp * hp * sizeof(float));
+    L.part_gu = take(static_cast<size_t>(L.splits_gu) * 2 * dp * hp * sizeof(float));
+    L.part_d = take(static_cast<size_t>(L.splits_d) * dp * hp * sizeof(float));
     L.zero = take(kTrZeroBytes);
     if (o > L.total) L.total = o;
   }
@@ -282,11 +395,12 @@ FfnBlockLayout ffn_block_layout(const moe_ffn& f, bool training) {
 }
 
 struct SavedLayout {
-  size_t a, b, h, total;
+  size_t h, f, p, low, total;
 };
 SavedLayout saved_layout(const moe_ffn& f) {
-  const size_t n = align_up(static_cast<size_t>(f.tokens) * pad128(f.d_hidden) * elem_bytes(f), 256);
-  return SavedLayout{0, n, 2 * n, 3 * n};
+  const size_t cells = static_cast<size_t>(f.tokens) * pad128(f.d_hidden);
+  const size_t n = align_up(cells * elem_bytes(f), 256);
+  return SavedLayout{0, n, 2 * n, 3 * n, 3 * n + (f.dtype == MOE_BF16 ? align_up(cells, 256) : 0)};
 }
 
 // ----------------------------------------------------------------- launches
@@ -307,11 +421,13 @@ template <typename T, int kMode, int kAct>
 void tiles(const char* name, const MmArgs& p, const FfnOut& o, hipStream_t s) {
   using Big = MmCfg<256, 256, 4, 2>;
   using Mid = MmCfg<128, 128, 2, 2>;
+  using Small = MmCfg<64, 64, 2, 2>;
   using Low = MmCfg<32, 128, 1, 4>;
   const int64_t cols = kMode == kGated ? 2 * static_cast<int64_t>(p.N) : p.N;
-  const int64_t big = (p.M + 255) / 256 * ((cols + 255) / 256);
-  if (sizeof(T) == 2 && big >= cu_count()) tiles_at<T, Big, kMode, kAct>(name, p, o, s);
-  else if (p.M > 32) tiles_at<T, Mid, kMode, kAct>(name, p, o, s);
+  auto count = [&](int t) { return (p.M + t - 1) / t * ((cols + t - 1) / t); };
+  if (sizeof(T) == 2 && count(256) >= cu_count()) tiles_at<T, Big, kMode, kAct>(name, p, o, s);
+  else if (count(128) >= cu_count()) tiles_at<T, Mid, kMode, kAct>(name, p, o, s);
+  else if (p.M > 32) tiles_at<T, Small, kMode, kAct>(name, p, o, s);
   else tiles_at<T, Low, kMode, kAct>(name, p, o, s);
 }
 
@@ -328,13 +444,6 @@ void tiles_act(const char* name, int act, const MmArgs& p, const FfnOut& o, hipS
 unsigned blocks_for(int64_t items) {
   const int64_t b = (items + 255) / 256;
   return static_cast<unsigned>(b < 1 ? 1 : (b > 8192 ? 8192 : b));
-}
-
-template <typename T>
-void turn(const void* src, void* dst, int K, int N, int64_t kp, hipStream_t s) {
-  MOE_LAUNCH("ffn_turn_weights", turn_kernel<T>,
-             dim3((N + 31) / 32, static_cast<unsigned>((kp + 31) / 32)), dim3(256), 0, s,
-             static_cast<const T*>(src), static_cast<T*>(dst), K, N, kp);
 }
 
 template <typename T>
@@ -367,16 +476,26 @@ hipError_t ffn_fwd_t(const moe_ffn& f, const void* x, const void* wg, const void
   char *W = static_cast<char*>(ws), *SV = static_cast<char*>(saved);
   const int d = f.d_model, h = f.d_hidden;
   const int64_t dp = pad128(d), hp = pad128(h);
-  turn<T>(wg, W + L.tg, d, h, dp, s);
-  turn<T>(wu, W + L.tu, d, h, dp, s);
-  turn<T>(wd, W + L.td, h, d, hp, s);
+  TurnJobs jobs{};
+  int end = 0;
+  auto turn = [&](int i, const void* src, char* dst, int K, int N) {
+    end += static_cast<int>(pad128(K) / 64 * ((N + 63) / 64));
+    jobs.job[i] = TurnJob{src, dst, K, N, pad128(K), end};
+  };
+  turn(0, wg, W + L.tg, d, h);
+  turn(1, wu, W + L.tu, d, h);
+  turn(2, wd, W + L.td, h, d);
+  MOE_LAUNCH("ffn_turn_weights", turn_kernel<T>, dim3(end), dim3(256), 0, s, jobs);
   const void* xp = padded<T>(x, W + L.xp, f.tokens, d, s);
   MmArgs p = rows_of<T>(xp, dp, W + L.tg, dp, f.tokens, h, dp);
   p.half = static_cast<int64_t>(L.tu) - static_cast<int64_t>(L.tg);
   FfnOut o{};
   o.h = SV ? SV + S.h : W + L.h;
-  o.a = SV ? SV + S.a : nullptr;
-  o.b = SV ? SV + S.b : nullptr;
+  if (SV) {
+    o.f = SV + S.f;
+    o.p = SV + S.p;
+    o.low = reinterpret_cast<uint8_t*>(SV + S.low);
+  }
   o.ld = hp;
   tiles_act<T, kGated>("ffn_gate_up", f.act, p, o, s);
   MmArgs q = rows_of<T>(o.h, hp, W + L.td, hp, f.tokens, d, hp);
@@ -387,11 +506,11 @@ hipError_t ffn_fwd_t(const moe_ffn& f, const void* x, const void* wg, const void
   return hipGetLastError();
 }
 
-template <typename T, typename G>
-void grad_weight(const char* name, const void* a, int64_t lda, const void* b, int64_t ldb, int M,
-                 int N, int64_t rows, int splits, float* part, const void* zero, void* out,
+// Partial sums of a^T b over the slices of the rows, [splits][mp][np].
+template <typename T>
+void grad_slices(const char* name, const void* a, int64_t lda, const void* b, int64_t ldb,
+                 int64_t mp, int64_t np, int64_t rows, int splits, float* part, const void* zero,
                  hipStream_t s) {
-  const int64_t mp = pad128(M), np = pad128(N);
   WgradArgs w{};
   w.a = a;
   w.lda = lda;
@@ -412,9 +531,6 @@ void grad_weight(const char* name, const void* a, int64_t lda, const void* b, in
     MOE_LAUNCH(name, (wgrad_kernel<float, false, true>), dim3(static_cast<unsigned>(blocks)),
                dim3(256), 0, s, w);
   }
-  MOE_LAUNCH("ffn_slice_sum", slice_sum_kernel<G>,
-             dim3(blocks_for(static_cast<int64_t>(M) * ((N + 3) / 4))), dim3(256), 0, s, part,
-             splits, mp, np, M, N, static_cast<G*>(out));
 }
 
 template <typename T, typename G>
@@ -435,29 +551,41 @@ hipError_t ffn_bwd_t(const moe_ffn& f, const void* x, const void* wg, const void
 
   MmArgs p = rows_of<T>(dyp, dp, wdp, dp, tok, h, dp);
   FfnOut o{};
-  o.sa = SV + S.a;
-  o.sb = SV + S.b;
-  o.da = W + L.da;
-  o.db = W + L.db;
+  o.f = const_cast<char*>(SV + S.f);
+  o.p = const_cast<char*>(SV + S.p);
+  o.low = reinterpret_cast<uint8_t*>(const_cast<char*>(SV + S.low));
+  o.dab = W + L.dab;
   o.ld = hp;
-  tiles_act<T, kGatedGrad>("ffn_bwd_down", f.act, p, o, s);
+  tiles<T, kGatedGrad, 0>("ffn_bwd_down", p, o, s);
 
-  MmArgs q = rows_of<T>(o.da, hp, wgp, hp, tok, d, hp);
+  MmArgs q = rows_of<T>(W + L.dab, 2 * hp, wgp, hp, tok, d, hp);
   q.k_split = q.nk;
   q.nk *= 2;
-  q.a2 = static_cast<const char*>(o.db);
+  q.a2 = W + L.dab + hp * sizeof(T);
   q.b2 = static_cast<const char*>(wup);
   FfnOut c{};
   c.c = dx;
   c.ldc = d;
   tiles<T, kPlain, 0>("ffn_bwd_gate_up", q, c, s);
 
-  float* part = reinterpret_cast<float*>(W + L.part);
+  float* gu = reinterpret_cast<float*>(W + L.part_gu);
+  float* dn = reinterpret_cast<float*>(W + L.part_d);
   MOE_LAUNCH("ffn_zero", zero_kernel<uint32_t>, dim3(1), dim3(256), 0, s,
              reinterpret_cast<uint32_t*>(W + L.zero), static_cast<int64_t>(kTrZeroBytes / 4));
-  grad_weight<T, G>("ffn_bwd_wgrad", xp, dp, o.da, hp, d, h, tok, L.splits_gu, part, W + L.zero, dwg, s);
-  grad_weight<T, G>("ffn_bwd_wgrad", xp, dp, o.db, hp, d, h, tok, L.splits_gu, part, W + L.zero, dwu, s);
-  grad_weight<T, G>("ffn_bwd_wgrad", SV + S.h, hp, dyp, dp, h, d, tok, L.splits_d, part, W + L.zero, dwd, s);
+  grad_slices<T>("ffn_bwd_wgrad_gate_up", xp, dp, W + L.dab, 2 * hp, dp, 2 * hp, tok, L.splits_gu, gu,
+                 W + L.zero, s);
+  grad_slices<T>("ffn_bwd_wgrad_down", SV + S.h, hp, dyp, dp, hp, dp, tok, L.splits_d, dn,
+                 W + L.zero, s);
+  SliceJobs jobs{};
+  int64_t end = 0;
+  auto job = [&](int i, const float* part, int splits, int64_t mp, int64_t np, int M, int N, void* out) {
+    end += static_cast<int64_t>(M) * ((N + 3) / 4);
+    jobs.job[i] = SliceJob{part, splits, mp * np, np, M, N, out, end};
+  };
+  job(0, gu, L.splits_gu, dp, 2 * hp, d, h, dwg);
+  job(1, gu + hp, L.splits_gu, dp, 2 * hp, d, h, dwu);
+  job(2, dn, L.splits_d, hp, dp, h, d, dwd);
+  MOE_LAUNCH("ffn_slice_sum", slice_sum_kernel<G>, dim3(blocks_for(end)), dim3(256), 0, s, jobs);
   return hipGetLastError();
 }
 

@@ -162,68 +162,59 @@ struct I8Out {
   int outputs;        // weight rows a group
 };
 
-// Four consecutive columns n.. of row r, n a multiple of four.
-template <typename T>
-__device__ __forceinline__ void i8_store4(const I8Out& o, int64_t r, int n, const float (&v)[4]) {
-  T* dst = static_cast<T*>(o.y) + r * o.ld + n;
-  if (n + 4 <= o.ld && o.ld % 4 == 0) {
-    store4(dst, v[0], v[1], v[2], v[3]);
-    return;
-  }
+__device__ __forceinline__ float as_sum(uint32_t v) { return static_cast<float>(static_cast<int>(v)); }
+
+// Scales, bias and storage of a tile's rows (the callbacks of mm_drain).
+template <typename T, bool kPaired, int kPasses>
+struct I8Rows {
+  const MmArgs& p;
+  const I8Out& o;
+  const MmTile& t;
+  int base, n;
+  float ws[8], wu[8], bias[8], xs[kPasses];
+
+  __device__ void cols(int c) {
+    n = base + c;
+    const float* w = o.ws + static_cast<int64_t>(t.group) * o.outputs;
 #pragma unroll
-  for (int q = 0; q < 4; ++q)
-    if (n + q < o.ld) put(dst + q, v[q]);
-}
+    for (int q = 0; q < 8; ++q) {
+      const int at = min(n + q, p.N - 1);
+      ws[q] = w[at];
+      if (kPaired) wu[q] = w[p.N + at];
+      else bias[q] = o.bias ? o.bias[at] : 0.0f;
+    }
+  }
+  __device__ void pre(int k, int m) {
+    const int64_t row = t.row0 + min(m, t.rows - 1);
+    xs[k] = o.xs[p.perm ? p.perm[row] / p.topk : row];
+  }
+  __device__ void row(int k, int m, const uint32_t (&v)[8]) {
+    if (m >= t.rows) return;
+    float y[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) y[q] = as_sum(v[q]) * xs[k] * ws[q] + bias[q];
+    store8(static_cast<T*>(o.y) + (t.row0 + m) * o.ld, n, p.N, y);
+  }
+  __device__ void row(int k, int m, const uint32_t (&g)[8], const uint32_t (&u)[8]) {
+    if (m >= t.rows) return;
+    float y[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      y[q] = silu_f(as_sum(g[q]) * xs[k] * ws[q]) * (as_sum(u[q]) * xs[k] * wu[q]);
+    store8(static_cast<T*>(o.y) + (t.row0 + m) * o.ld, n, p.N, y);
+  }
+};
 
 template <typename T, typename Cfg, bool kPaired>
-__global__ __launch_bounds__(Cfg::NT) __attribute__((amdgpu_waves_per_eu(Cfg::NT == 512 ? 2 : 1)))
+__global__ __launch_bounds__(Cfg::NT) __attribute__((amdgpu_waves_per_eu(2)))
 void i8_tile_kernel(const MmArgs p, const I8Out o) {
   __shared__ __attribute__((aligned(1024))) char smem[2 * Cfg::STAGE];
   i32x16 acc[Cfg::WM][Cfg::WN];
   MmTile t;
   if (!mm_tile<OpI8, Cfg, kPaired>(p, smem, &t, acc)) return;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int g = lane >> 5, r32 = lane & 31;
-  const int wm = wave / Cfg::WAVES_N, wn = wave % Cfg::WAVES_N;
-  const float* ws = o.ws + static_cast<int64_t>(t.group) * o.outputs;
-#pragma unroll
-  for (int i = 0; i < Cfg::WM; ++i) {
-    const int m = (wm * Cfg::WM + i) * 32 + r32;
-    if (m >= t.rows) continue;
-    const int64_t row = t.row0 + m;
-    const float xs = o.xs[p.perm ? p.perm[row] / p.topk : row];
-#pragma unroll
-    for (int j = 0; j < Cfg::WN; ++j) {
-      const int n0 = t.nt * Cfg::BN + (wn * Cfg::WN + j) * 32;
-      if (kPaired) {
-#pragma unroll
-        for (int rr = 0; rr < 2; ++rr) {
-          const int n = n0 / 2 + 8 * rr + 4 * g;
-          float v[4];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int c = min(n + q, p.N - 1);
-            const float a = static_cast<float>(acc[i][j][4 * rr + q]) * xs * ws[c];
-            const float b = static_cast<float>(acc[i][j][4 * rr + 8 + q]) * xs * ws[p.N + c];
-            v[q] = silu_f(a) * b;
-          }
-          i8_store4<T>(o, row, n, v);
-        }
-      } else {
-#pragma unroll
-        for (int rr = 0; rr < 4; ++rr) {
-          const int n = n0 + 8 * rr + 4 * g;
-          float v[4];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int c = min(n + q, p.N - 1);
-            v[q] = static_cast<float>(acc[i][j][4 * rr + q]) * xs * ws[c] + (o.bias ? o.bias[c] : 0.0f);
-          }
-          i8_store4<T>(o, row, n, v);
-        }
-      }
-    }
-  }
+  I8Rows<T, kPaired, mm_passes<Cfg, kPaired>()> rows{p, o, t};
+  rows.base = t.nt * (kPaired ? Cfg::BN / 2 : Cfg::BN);
+  mm_drain<Cfg, kPaired>(smem, acc, rows);
 }
 
 template <typename T, typename Cfg>
@@ -335,12 +326,14 @@ hipError_t launch_linear_i8(const moe_i8_linear& l, const void* x, const float* 
     using T = decltype(t);
     using Big = MmCfg<256, 256, 4, 2>;
     using Mid = MmCfg<128, 128, 2, 2>;
+    using Small = MmCfg<64, 64, 2, 2>;
     using Low = MmCfg<32, 128, 1, 4>;
     const int64_t per_group = p.M / p.groups;
-    const int64_t big = (p.M + 255) / 256 * ((l.outputs + 255) / 256);
+    auto count = [&](int t) { return (p.M + t - 1) / t * ((l.outputs + t - 1) / t); };
     auto tiles = [&](int bm) { return (p.M + bm - 1) / bm + (r ? p.groups : 0); };
-    if (per_group >= 256 && big >= cu_count()) i8_tiles<T, Big>(p, o, paired, tiles(256), s);
-    else if (per_group > 32) i8_tiles<T, Mid>(p, o, paired, tiles(128), s);
+    if (per_group >= 256 && count(256) >= cu_count()) i8_tiles<T, Big>(p, o, paired, tiles(256), s);
+    else if (per_group >= 128 && count(128) >= cu_count()) i8_tiles<T, Mid>(p, o, paired, tiles(128), s);
+    else if (per_group > 32) i8_tiles<T, Small>(p, o, paired, tiles(64), s);
     else i8_tiles<T, Low>(p, o, paired, tiles(32), s);
   };
   if (l.dtype == MOE_BF16) go(bf16_t{});

@@ -239,4 +239,81 @@ __device__ __forceinline__ bool mm_tile(const MmArgs& p, char* smem, MmTile* til
   return true;
 }
 
+// Hands a finished tile out by rows. Stored straight from the accumulators,
+// a store instruction would touch 32 rows with a few bytes each; instead each
+// wave writes strips of 32 rows into LDS of its own (the stage buffers, free
+// by now) and every lane takes eight consecutive columns of a row, so eight
+// (paired: four) lanes cover whole cache lines. f.cols(n) is called with the
+// lane's first column (within the tile; paired: within the tile's hidden
+// columns) before its rows, f.pre(k, m) for pass k's row m before the strip is
+// written (loads go there, so that they are all in flight at once), then
+// f.row(k, m, v) with the eight sums, or f.row(k, m, gate, up).
+constexpr int kMmStripPad = 16;  // bytes behind a strip row: spreads the rows over the banks
+template <typename Cfg>
+struct MmStrip {
+  static constexpr int CB = Cfg::WN < 2 ? Cfg::WN : 2;  // MFMA tiles side by side in a strip
+  static constexpr int PITCH = CB * 128 + kMmStripPad, BYTES = 32 * PITCH;
+  static_assert(Cfg::NW * BYTES <= 2 * Cfg::STAGE, "strips fit the stage buffers");
+};
+
+template <typename Cfg, bool kPaired, typename Acc, typename F>
+__device__ __forceinline__ void mm_drain(char* smem, const Acc (&acc)[Cfg::WM][Cfg::WN], F&& f) {
+  using S = MmStrip<Cfg>;
+  constexpr int COLS = S::CB * (kPaired ? 16 : 32);  // columns handed out per strip row
+  constexpr int LPR = COLS / 8, RPP = 64 / LPR, PASSES = 32 / RPP;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int g = lane >> 5, r32 = lane & 31;
+  const int wm = wave / Cfg::WAVES_N, wn = wave % Cfg::WAVES_N;
+  char* strip = smem + wave * S::BYTES;
+  // every wave is done with the stages
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  const int c8 = (lane % LPR) * 8, r0 = lane / LPR;
+  // byte of the lane's first column in a strip row (paired: of its gate columns)
+  const int at = kPaired ? (c8 / 16) * 128 + (c8 % 16) * 4 : c8 * 4;
+#pragma unroll
+  for (int jb = 0; jb < Cfg::WN; jb += S::CB) {
+    f.cols((wn * Cfg::WN + jb) * (kPaired ? 16 : 32) + c8);
+#pragma unroll
+    for (int i = 0; i < Cfg::WM; ++i) {
+      const int m0 = (wm * Cfg::WM + i) * 32 + r0;
+#pragma unroll
+      for (int k = 0; k < PASSES; ++k) f.pre(k, m0 + k * RPP);
+#pragma unroll
+      for (int j = 0; j < S::CB; ++j)
+#pragma unroll
+        for (int rr = 0; rr < 4; ++rr) {
+          u32x4 v;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const auto e = acc[i][jb + j][4 * rr + q];  // a value: bit_cast takes no vector element
+            v[q] = __builtin_bit_cast(uint32_t, e);
+          }
+          *reinterpret_cast<u32x4*>(strip + r32 * S::PITCH + j * 128 + rr * 32 + g * 16) = v;
+        }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll
+      for (int k = 0; k < PASSES; ++k) {
+        const char* src = strip + (r0 + k * RPP) * S::PITCH + at;
+        u32x4 lo = *reinterpret_cast<const u32x4*>(src), hi = *reinterpret_cast<const u32x4*>(src + 16);
+        const uint32_t v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+        if constexpr (kPaired) {
+          lo = *reinterpret_cast<const u32x4*>(src + 64);
+          hi = *reinterpret_cast<const u32x4*>(src + 80);
+          const uint32_t u[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+          f.row(k, m0 + k * RPP, v, u);
+        } else {
+          f.row(k, m0 + k * RPP, v);
+        }
+      }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    }
+  }
+}
+
+// Passes of mm_drain over a strip (the k of its callbacks).
+template <typename Cfg, bool kPaired>
+constexpr int mm_passes() {
+  return 32 / (64 / (MmStrip<Cfg>::CB * (kPaired ? 16 : 32) / 8));
+}
+
 }  // namespace moe

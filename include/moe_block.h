@@ -108,7 +108,8 @@ typedef struct {
 size_t moe_gated_ffn_workspace_bytes(const moe_ffn* f, int training);
 
 /* Bytes (host) of the buffer that moe_gated_ffn fills for
- * moe_gated_ffn_bwd: both pre-activations and the hidden values, in dtype. */
+ * moe_gated_ffn_bwd: h in dtype, and act(a) and b act'(a), in fp32 or, in
+ * bf16, as the 20 high bits of their fp32 values. */
 size_t moe_gated_ffn_saved_bytes(const moe_ffn* f);
 
 /* Forward. saved: NULL for inference, or moe_gated_ffn_saved_bytes(f) bytes
@@ -118,8 +119,8 @@ int moe_gated_ffn(const moe_ffn* f, const void* x, const void* w_gate, const voi
                   size_t workspace_bytes, void* stream);
 
 /*
- * Backward of L = sum(out * grad_out); a, b are the pre-activations x W_gate
- * and x W_up as saved (rounded to dtype), h = act(a) b:
+ * Backward of L = sum(out * grad_out), with a = x W_gate, b = x W_up and
+ * h = act(a) b:
  *   dh = grad_out W_down^T, da = dh b act'(a), db = dh act(a)
  *   grad_x = da W_gate^T + db W_up^T
  *   grad_gate = x^T da, grad_up = x^T db, grad_down = h^T grad_out
