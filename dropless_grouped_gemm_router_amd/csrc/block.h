@@ -81,8 +81,9 @@ __device__ __forceinline__ void store_piece(T* row, int c, int n, const float (&
     if (c + q < n) put(row + c + q, v[q]);
 }
 
-// Eight consecutive columns n.. of a row of `width`, fp32 in, stored as T.
-template <typename T>
+// Eight consecutive columns n.. of a row of `width`, fp32 in, stored as T;
+// kFull: all eight exist.
+template <typename T, bool kFull>
 __device__ __forceinline__ void store8(T* row, int n, int width, const float (&v)[8]) {
   constexpr int V = Piece<T>::V;
 #pragma unroll
@@ -90,7 +91,8 @@ __device__ __forceinline__ void store8(T* row, int n, int width, const float (&v
     float e[V];
 #pragma unroll
     for (int q = 0; q < V; ++q) e[q] = v[h * V + q];
-    if (n + h * V < width) store_piece(row, n + h * V, width, e);
+    if (kFull) store_any(row + n + h * V, Piece<T>::narrow(e));
+    else if (n + h * V < width) store_piece(row, n + h * V, width, e);
   }
 }
 

@@ -210,51 +210,56 @@ struct OpOf<float> {
   typedef OpF32 type;
 };
 
-// The callbacks of mm_drain. Columns past p.N (the hidden matrices' padding)
-// are written as zeros.
-template <typename T, int kMode, int kAct, int kPasses>
+// The callbacks of mm_drain; kFull: every column of the tile exists (of a
+// hidden matrix: below its padded width o.ld). Columns past p.N, the hidden
+// matrices' padding, are written as zeros.
+template <typename T, typename Cfg, int kMode, int kAct, bool kFull>
 struct FfnRows {
+  static constexpr int kJ = Cfg::WN / MmStrip<Cfg>::CB;
+  static constexpr bool kGrad = kMode == kGatedGrad;
   const MmArgs& p;
   const FfnOut& o;
   const MmTile& t;
-  int base, n;
-  Kept<T> kept[kMode == kGatedGrad ? kPasses : 1];
+  int base, n[kJ];
+  Kept<T> kept[kGrad ? 2 : 1][kGrad ? mm_passes<Cfg, false>() : 1];
 
-  __device__ void cols(int c) { n = base + c; }
-  __device__ void pre(int k, int m) {
-    if (kMode == kGatedGrad && n < o.ld) kept[k].load(o, (t.row0 + min(m, t.rows - 1)) * o.ld + n);
+  __device__ void cols(int j, int c) { n[j] = base + c; }
+  __device__ void start(int, int, int) {}
+  __device__ void pre(int set, int j, int k, int m) {
+    if constexpr (kGrad) {
+      if (kFull || n[j] < o.ld) kept[set][k].load(o, (t.row0 + m) * o.ld + n[j]);
+    }
   }
-  __device__ void row(int k, int m, const uint32_t (&v)[8]) {
-    if (m >= t.rows) return;
+  __device__ void row(int set, int, int j, int k, int m, const uint32_t (&v)[8]) {
     const int64_t row = t.row0 + m;
-    if (kMode == kPlain) {
+    if constexpr (!kGrad) {
       float y[8];
 #pragma unroll
       for (int q = 0; q < 8; ++q) y[q] = __uint_as_float(v[q]);
-      store8(static_cast<T*>(o.c) + row * o.ldc, n, p.N, y);
-      return;
-    }
-    if (n >= o.ld) return;
-    float da[8], db[8];
+      store8<T, kFull>(static_cast<T*>(o.c) + row * o.ldc, n[j], p.N, y);
+    } else {
+      if (!kFull && n[j] >= o.ld) return;
+      float da[8], db[8];
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      float fv, pv;
-      kept[kMode == kGatedGrad ? k : 0].get(q, &fv, &pv);
-      const float dh = __uint_as_float(v[q]);
-      const bool in = n + q < p.N;
-      da[q] = in ? dh * pv : 0.0f;
-      db[q] = in ? dh * fv : 0.0f;
+      for (int q = 0; q < 8; ++q) {
+        float fv, pv;
+        kept[set][k].get(q, &fv, &pv);
+        const float dh = __uint_as_float(v[q]);
+        const bool in = n[j] + q < p.N;
+        da[q] = in ? dh * pv : 0.0f;
+        db[q] = in ? dh * fv : 0.0f;
+      }
+      T* dst = static_cast<T*>(o.dab) + row * 2 * o.ld;
+      store8<T, true>(dst, n[j], 0, da);
+      store8<T, true>(dst + o.ld, n[j], 0, db);
     }
-    T* dst = static_cast<T*>(o.dab) + row * 2 * o.ld;
-    store8(dst, n, static_cast<int>(o.ld), da);
-    store8(dst + o.ld, n, static_cast<int>(o.ld), db);
   }
-  __device__ void row(int, int m, const uint32_t (&g)[8], const uint32_t (&u)[8]) {
-    if (m >= t.rows || n >= o.ld) return;
+  __device__ void row(int, int, int j, int, int m, const uint32_t (&g)[8], const uint32_t (&u)[8]) {
+    if (!kFull && n[j] >= o.ld) return;
     float h[8], f[8], s[8];
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
-      const bool in = n + q < p.N;
+      const bool in = n[j] + q < p.N;
       const float b = __uint_as_float(u[q]);
       float slope;
       const float fv = act_value<kAct>(__uint_as_float(g[q]), &slope);
@@ -262,21 +267,28 @@ struct FfnRows {
       f[q] = in ? fv : 0.0f;
       s[q] = in ? b * slope : 0.0f;
     }
-    store8(static_cast<T*>(o.h) + (t.row0 + m) * o.ld, n, static_cast<int>(o.ld), h);
-    if (o.f) keep8(o, (t.row0 + m) * o.ld + n, f, s, static_cast<const T*>(nullptr));
+    store8<T, true>(static_cast<T*>(o.h) + (t.row0 + m) * o.ld, n[j], 0, h);
+    if (o.f) keep8(o, (t.row0 + m) * o.ld + n[j], f, s, static_cast<const T*>(nullptr));
   }
 };
 
 template <typename T, typename Cfg, int kMode, int kAct>
-__global__ __launch_bounds__(Cfg::NT) __attribute__((amdgpu_waves_per_eu(2)))
+__global__ __launch_bounds__(Cfg::NT) __attribute__((amdgpu_waves_per_eu(Cfg::WPE)))
 void ffn_tile_kernel(const MmArgs p, const FfnOut o) {
-  __shared__ __attribute__((aligned(1024))) char smem[2 * Cfg::STAGE];
+  __shared__ __attribute__((aligned(1024))) char smem[MmStrip<Cfg>::LDS];
   f32x16_t acc[Cfg::WM][Cfg::WN];
   MmTile t;
   constexpr bool kPaired = kMode == kGated;
-  if (!mm_tile<typename OpOf<T>::type, Cfg, kPaired>(p, smem, &t, acc)) return;
-  FfnRows<T, kMode, kAct, mm_passes<Cfg, kPaired>()> rows{p, o, t, t.nt * (kPaired ? Cfg::BN / 2 : Cfg::BN)};
-  mm_drain<Cfg, kPaired>(smem, acc, rows);
+  if (!mm_find<Cfg>(p, &t)) return;
+  constexpr int kCols = kPaired ? Cfg::BN / 2 : Cfg::BN;
+  auto go = [&](auto full) {
+    FfnRows<T, Cfg, kMode, kAct, decltype(full)::value> rows{p, o, t, t.nt * kCols};
+    mm_begin<Cfg, kPaired>(t.rows, rows);
+    mm_drain<Cfg, kPaired>(smem, acc, t.rows, rows);
+  };
+  mm_tile<typename OpOf<T>::type, Cfg, kPaired>(p, smem, t, acc);
+  if ((t.nt + 1) * kCols <= (kMode == kPlain ? p.N : o.ld)) go(std::true_type{});
+  else go(std::false_type{});
 }
 
 // Weight gradients from the slices' partial sums [splits][mp][ld], cropped
@@ -419,13 +431,13 @@ void tiles_at(const char* name, const MmArgs& a, const FfnOut& o, hipStream_t s)
 
 template <typename T, int kMode, int kAct>
 void tiles(const char* name, const MmArgs& p, const FfnOut& o, hipStream_t s) {
-  using Big = MmCfg<256, 256, 4, 2>;
-  using Mid = MmCfg<128, 128, 2, 2>;
+  using Big = MmCfg<256, 256, 2, 2>;
+  using Mid = MmCfg<128, 128, 2, 2, 3>;
   using Small = MmCfg<64, 64, 2, 2>;
-  using Low = MmCfg<32, 128, 1, 4>;
+  using Low = MmCfg<32, 64, 1, 2>;
   const int64_t cols = kMode == kGated ? 2 * static_cast<int64_t>(p.N) : p.N;
   auto count = [&](int t) { return (p.M + t - 1) / t * ((cols + t - 1) / t); };
-  if (sizeof(T) == 2 && count(256) >= cu_count()) tiles_at<T, Big, kMode, kAct>(name, p, o, s);
+  if (sizeof(T) == 2 && p.nk >= 32 && count(256) >= cu_count()) tiles_at<T, Big, kMode, kAct>(name, p, o, s);
   else if (count(128) >= cu_count()) tiles_at<T, Mid, kMode, kAct>(name, p, o, s);
   else if (p.M > 32) tiles_at<T, Small, kMode, kAct>(name, p, o, s);
   else tiles_at<T, Low, kMode, kAct>(name, p, o, s);

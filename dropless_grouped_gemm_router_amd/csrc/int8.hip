@@ -164,57 +164,63 @@ struct I8Out {
 
 __device__ __forceinline__ float as_sum(uint32_t v) { return static_cast<float>(static_cast<int>(v)); }
 
-// Scales, bias and storage of a tile's rows (the callbacks of mm_drain).
-template <typename T, bool kPaired, int kPasses>
+// Scales, bias and storage of a tile's rows (the callbacks of mm_drain);
+// kFull: every column of the tile exists.
+template <typename T, typename Cfg, bool kPaired, bool kFull>
 struct I8Rows {
+  static constexpr int kJ = Cfg::WN / MmStrip<Cfg>::CB;
   const MmArgs& p;
   const I8Out& o;
   const MmTile& t;
-  int base, n;
-  float ws[8], wu[8], bias[8], xs[kPasses];
+  int base, n[kJ];
+  float ws[kJ][8], wu[kJ][8], xs[Cfg::WM][mm_passes<Cfg, kPaired>()];  // wu: paired up scales, else bias
 
-  __device__ void cols(int c) {
-    n = base + c;
+  __device__ void cols(int j, int c) {
+    n[j] = base + c;
     const float* w = o.ws + static_cast<int64_t>(t.group) * o.outputs;
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
-      const int at = min(n + q, p.N - 1);
-      ws[q] = w[at];
-      if (kPaired) wu[q] = w[p.N + at];
-      else bias[q] = o.bias ? o.bias[at] : 0.0f;
+      const int at = kFull ? n[j] + q : min(n[j] + q, p.N - 1);
+      ws[j][q] = w[at];
+      wu[j][q] = kPaired ? w[p.N + at] : (o.bias ? o.bias[at] : 0.0f);
     }
   }
-  __device__ void pre(int k, int m) {
-    const int64_t row = t.row0 + min(m, t.rows - 1);
-    xs[k] = o.xs[p.perm ? p.perm[row] / p.topk : row];
+  __device__ void start(int i, int k, int m) {
+    const int64_t row = t.row0 + m;
+    xs[i][k] = o.xs[p.perm ? p.perm[row] / p.topk : row];
   }
-  __device__ void row(int k, int m, const uint32_t (&v)[8]) {
-    if (m >= t.rows) return;
+  __device__ void pre(int, int, int, int) {}
+  __device__ void row(int, int i, int j, int k, int m, const uint32_t (&v)[8]) {
     float y[8];
 #pragma unroll
-    for (int q = 0; q < 8; ++q) y[q] = as_sum(v[q]) * xs[k] * ws[q] + bias[q];
-    store8(static_cast<T*>(o.y) + (t.row0 + m) * o.ld, n, p.N, y);
+    for (int q = 0; q < 8; ++q) y[q] = as_sum(v[q]) * xs[i][k] * ws[j][q] + wu[j][q];
+    store8<T, kFull>(static_cast<T*>(o.y) + (t.row0 + m) * o.ld, n[j], p.N, y);
   }
-  __device__ void row(int k, int m, const uint32_t (&g)[8], const uint32_t (&u)[8]) {
-    if (m >= t.rows) return;
+  __device__ void row(int, int i, int j, int k, int m, const uint32_t (&g)[8], const uint32_t (&u)[8]) {
     float y[8];
 #pragma unroll
     for (int q = 0; q < 8; ++q)
-      y[q] = silu_f(as_sum(g[q]) * xs[k] * ws[q]) * (as_sum(u[q]) * xs[k] * wu[q]);
-    store8(static_cast<T*>(o.y) + (t.row0 + m) * o.ld, n, p.N, y);
+      y[q] = silu_f(as_sum(g[q]) * xs[i][k] * ws[j][q]) * (as_sum(u[q]) * xs[i][k] * wu[j][q]);
+    store8<T, kFull>(static_cast<T*>(o.y) + (t.row0 + m) * o.ld, n[j], p.N, y);
   }
 };
 
 template <typename T, typename Cfg, bool kPaired>
-__global__ __launch_bounds__(Cfg::NT) __attribute__((amdgpu_waves_per_eu(2)))
+__global__ __launch_bounds__(Cfg::NT) __attribute__((amdgpu_waves_per_eu(Cfg::WPE)))
 void i8_tile_kernel(const MmArgs p, const I8Out o) {
-  __shared__ __attribute__((aligned(1024))) char smem[2 * Cfg::STAGE];
+  __shared__ __attribute__((aligned(1024))) char smem[MmStrip<Cfg>::LDS];
   i32x16 acc[Cfg::WM][Cfg::WN];
   MmTile t;
-  if (!mm_tile<OpI8, Cfg, kPaired>(p, smem, &t, acc)) return;
-  I8Rows<T, kPaired, mm_passes<Cfg, kPaired>()> rows{p, o, t};
-  rows.base = t.nt * (kPaired ? Cfg::BN / 2 : Cfg::BN);
-  mm_drain<Cfg, kPaired>(smem, acc, rows);
+  if (!mm_find<Cfg>(p, &t)) return;
+  constexpr int kCols = kPaired ? Cfg::BN / 2 : Cfg::BN;
+  auto go = [&](auto full) {
+    I8Rows<T, Cfg, kPaired, decltype(full)::value> rows{p, o, t, t.nt * kCols};
+    mm_begin<Cfg, kPaired>(t.rows, rows);
+    mm_tile<OpI8, Cfg, kPaired>(p, smem, t, acc);
+    mm_drain<Cfg, kPaired>(smem, acc, t.rows, rows);
+  };
+  if ((t.nt + 1) * kCols <= p.N) go(std::true_type{});
+  else go(std::false_type{});
 }
 
 template <typename T, typename Cfg>
@@ -324,14 +330,14 @@ hipError_t launch_linear_i8(const moe_i8_linear& l, const void* x, const float* 
   I8Out o{xs, ws, bias, y, p.N, l.outputs};
   auto go = [&](auto t) {
     using T = decltype(t);
-    using Big = MmCfg<256, 256, 4, 2>;
-    using Mid = MmCfg<128, 128, 2, 2>;
+    auto tiles = [&](int bm) { return (p.M + bm - 1) / bm + (r ? p.groups : 0); };
+    using Big = MmCfg<256, 256, 2, 2>;
+    using Mid = MmCfg<128, 128, 2, 2, 3>;
     using Small = MmCfg<64, 64, 2, 2>;
-    using Low = MmCfg<32, 128, 1, 4>;
+    using Low = MmCfg<32, 64, 1, 2>;
     const int64_t per_group = p.M / p.groups;
     auto count = [&](int t) { return (p.M + t - 1) / t * ((l.outputs + t - 1) / t); };
-    auto tiles = [&](int bm) { return (p.M + bm - 1) / bm + (r ? p.groups : 0); };
-    if (per_group >= 256 && count(256) >= cu_count()) i8_tiles<T, Big>(p, o, paired, tiles(256), s);
+    if (p.nk >= 32 && per_group >= 256 && count(256) >= cu_count()) i8_tiles<T, Big>(p, o, paired, tiles(256), s);
     else if (per_group >= 128 && count(128) >= cu_count()) i8_tiles<T, Mid>(p, o, paired, tiles(128), s);
     else if (per_group > 32) i8_tiles<T, Small>(p, o, paired, tiles(64), s);
     else i8_tiles<T, Low>(p, o, paired, tiles(32), s);

@@ -2,16 +2,16 @@
 //
 //   C[m][n] = sum_k A[m][k] B[n][k]     bf16 or fp32 -> fp32, int8 -> int32
 //
-// Both operands are rows of K-contiguous bytes, a stage being 128 bytes of
-// every row (64 bf16, 32 fp32 or 128 int8), so one engine serves all types:
+// Both operands are rows of K-contiguous bytes, a stage being 64 bytes of
+// every row (32 bf16, 16 fp32 or 64 int8), so one engine serves all types:
 // the fragments of mfma 32x32x16 bf16, of 32x32x32 i8 and of four 32x32x2
 // fp32 steps are the same 16 bytes a lane. Rows come through pointers computed once per tile, which is where
 // gathering by the expert permutation, clamping at the last row and the
 // pairing of gate and up columns happen.
 //
 // Stages go from global memory straight into LDS (no staging registers);
-// the 16-byte chunk c of LDS row r sits at position c ^ ((r >> 1) & 7), so
-// the 32 rows that a fragment read touches spread over all banks. The MFMA
+// the 16-byte chunk c of LDS row r sits at position c ^ ((r >> 2) & 3), so
+// the rows that a fragment read touches spread over all banks. The MFMA
 // takes the B fragment first: lane L then holds row L % 32 and runs of four
 // consecutive columns, 8 (q / 4) + 4 (L / 32) + q % 4 for register q.
 #pragma once
@@ -66,17 +66,20 @@ struct MmArgs {
   int64_t half;              // paired: bytes from a gate row of B to its up row
 };
 
-constexpr int kMmRow = 128;
+constexpr int kMmRow = 64;  // bytes of a row in a stage
 
-template <int BM_, int BN_, int WAVES_M_, int WAVES_N_>
+template <int BM_, int BN_, int WAVES_M_, int WAVES_N_, int RING_ = 4>
 struct MmCfg {
+  static constexpr int RING = RING_;  // stage buffers
   static constexpr int BM = BM_, BN = BN_, WAVES_M = WAVES_M_, WAVES_N = WAVES_N_;
   static constexpr int NW = WAVES_M * WAVES_N, NT = 64 * NW;
   static constexpr int WM = BM / WAVES_M / 32, WN = BN / WAVES_N / 32;  // MFMA tiles per wave
-  static constexpr int A_LOADS = BM / 8 / NW, B_LOADS = BN / 8 / NW;     // a wave and stage
-  static constexpr int STAGE = (BM + BN) * kMmRow;
+  static constexpr int A_LOADS = BM / 16 / NW, B_LOADS = BN / 16 / NW;     // a wave and stage
+  static constexpr bool DEEP = WM * WN == 16;  // one wave to a SIMD: mm_deep
+  static constexpr int WPE = DEEP ? 1 : 2;       // waves to a SIMD
+  static constexpr int STAGE = (BM + BN) * kMmRow, LDS = RING * STAGE;
   static_assert(BM == WAVES_M * WM * 32 && BN == WAVES_N * WN * 32, "tiles");
-  static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0, "loads");
+  static_assert(BM % (16 * NW) == 0 && BN % (16 * NW) == 0, "loads");
 };
 
 // A tile's rows: first row, count (0: nothing to do), weight group.
@@ -124,7 +127,7 @@ __device__ __forceinline__ void mm_tile_order(int w, int tiles_m, int tiles_n, i
   *nt = in / high;
 }
 
-// One stage's loads of one operand: NL loads a wave, of 8 rows (1 KiB) each.
+// One stage's loads of one operand: NL loads a wave, of 16 rows (1 KiB) each.
 template <int NL>
 __device__ __forceinline__ void mm_issue(char* buf, const char* const* rows, int64_t off, int wave) {
 #pragma unroll
@@ -135,11 +138,18 @@ __device__ __forceinline__ void mm_issue(char* buf, const char* const* rows, int
   }
 }
 
+// At most N of this wave's loads left in flight, its LDS reads done.
+template <int N>
+__device__ __forceinline__ void mm_wait() {
+  static_assert(N < 64, "vmcnt");
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));
+}
+
 template <typename Op, typename Cfg>
 __device__ __forceinline__ void mm_compute(const char* buf, int a_frag, int b_frag, int sw,
                                            typename Op::Acc (&acc)[Cfg::WM][Cfg::WN]) {
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
+  for (int q = 0; q < 2; ++q) {
     u32x4 xf[Cfg::WM], wf[Cfg::WN];
     const int at = ((2 * q) ^ sw) << 4;
 #pragma unroll
@@ -155,21 +165,83 @@ __device__ __forceinline__ void mm_compute(const char* buf, int a_frag, int b_fr
   }
 }
 
-// One workgroup's tile, from its index; kPaired: B's tile holds gate rows
-// and up rows in turns of 16 (column p of the tile is gate column
-// 16 (p / 32) + p % 16 of the pair block when p % 32 < 16, else the same up
-// column), so a lane's registers 0-7 and 8-15 of an MFMA tile are matching
-// gate and up values. False: no such tile.
-template <typename Op, typename Cfg, bool kPaired>
-__device__ __forceinline__ bool mm_tile(const MmArgs& p, char* smem, MmTile* tile,
-                                        typename Op::Acc (&acc)[Cfg::WM][Cfg::WN]) {
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+// The main loop with one wave to a SIMD and 128 x 128 of the tile to a wave:
+// 64 FLOP (bf16) a byte read from LDS against 42.7 for eight waves of
+// 64 x 128, whose reads and the stage writes together would fill the LDS
+// pipe for as long as the MFMAs run. Nothing else hides a latency here, so
+// the fragments of a step (half a stage) are read while the step before is
+// multiplied, two MFMAs to a read, and a stage's loads are spread the same
+// way. One barrier a stage, between its two steps: it says that the next
+// stage is whole and that nobody reads this one any more, whose buffer is
+// then loaded again (four stages ahead).
+template <typename Op, typename Cfg, typename Load>
+__device__ __forceinline__ void mm_deep(char* smem, int nk, int a_frag, int b_frag, int sw,
+                                        typename Op::Acc (&acc)[Cfg::WM][Cfg::WN], Load&& load) {
+  constexpr int W = 4, kLoads = Cfg::A_LOADS + Cfg::B_LOADS;
+  static_assert(Cfg::WM == W && Cfg::WN == W && kLoads == 8, "128 x 128 a wave");
+  u32x4 x[2][W], w[2][W];
+  const int at0 = sw << 4, at1 = (2 ^ sw) << 4;
+  // fragment f of a step: 0-3 of A, 4-7 of B
+  auto read = [&](const char* buf, int at, int f, int set) {
+    if (f < W) x[set][f & 3] = *reinterpret_cast<const u32x4*>(buf + a_frag + (f & 3) * 32 * kMmRow + at);
+    else w[set][f & 3] = *reinterpret_cast<const u32x4*>(buf + b_frag + (f & 3) * 32 * kMmRow + at);
+  };
+  auto multiply = [&](int set, int n) {
+    const int i = n >> 2, j = n & 3;
+    Op::step(w[set][j], x[set][i], acc[i][j]);
+  };
+#pragma unroll
+  for (int st = 0; st < Cfg::RING; ++st)
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u) load(min(st, nk - 1), smem + st * Cfg::STAGE, u);
+  mm_wait<kLoads * (Cfg::RING - 1)>();
+  asm volatile("s_barrier" ::: "memory");
+#pragma unroll
+  for (int f = 0; f < 2 * W; ++f) read(smem, at0, f, 0);
+  for (int s = 0; s < nk; ++s) {
+    const char* cur = smem + (s % Cfg::RING) * Cfg::STAGE;
+    const char* next = smem + ((s + 1) % Cfg::RING) * Cfg::STAGE;
+#pragma unroll
+    for (int f = 0; f < 8; ++f) {
+      read(cur, at1, f, 1);
+      multiply(0, 2 * f);
+      multiply(0, 2 * f + 1);
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // an LDS read
+      __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);  // two MFMAs
+    }
+    // stage s + 1 has landed (s + 2, s + 3 may be in flight), the reads of
+    // stage s are done
+    __builtin_amdgcn_sched_barrier(0);
+    mm_wait<kLoads * (Cfg::RING - 2)>();
+    asm volatile("s_barrier" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    // past the last stage its loads are made again, into a buffer that is
+    // not read, so that the loop has one body and one count
+    const int ahead = min(s + Cfg::RING, nk - 1);
+    char* into = smem + (s % Cfg::RING) * Cfg::STAGE;
+#pragma unroll
+    for (int f = 0; f < 8; ++f) {
+      load(ahead, into, f);
+      read(next, at0, f, 0);
+      multiply(1, 2 * f);
+      multiply(1, 2 * f + 1);
+      __builtin_amdgcn_sched_group_barrier(0x010, 1, 1);  // a load
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 1);
+      __builtin_amdgcn_sched_group_barrier(0x008, 2, 1);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  mm_wait<0>();
+}
+
+// One workgroup's tile, from its index. False: no such tile.
+template <typename Cfg>
+__device__ __forceinline__ bool mm_find(const MmArgs& p, MmTile* tile) {
   const int w = xcd_remap(blockIdx.x, gridDim.x);
   MmTile t{0, 0, 0, 0};
   if (p.offsets) {
-    t = mm_routed_tile(p.offsets, p.groups, p.cap, Cfg::BM, w / p.tiles_n, lane);
+    t = mm_routed_tile(p.offsets, p.groups, p.cap, Cfg::BM, w / p.tiles_n, threadIdx.x & 63);
     t.nt = w % p.tiles_n;
-    if (t.rows <= 0) return false;
   } else {
     int mt;
     mm_tile_order(w, static_cast<int>((p.M + Cfg::BM - 1) / Cfg::BM), p.tiles_n, &mt, &t.nt);
@@ -178,23 +250,34 @@ __device__ __forceinline__ bool mm_tile(const MmArgs& p, char* smem, MmTile* til
     t.rows = left < Cfg::BM ? static_cast<int>(left) : Cfg::BM;
   }
   *tile = t;
+  return t.rows > 0;
+}
 
-  // Load i of a wave covers rows (wave LOADS + i) 8 + lane / 8 of an operand's
-  // tile, lane l's 16 bytes landing at position l % 8 of the row: the chunk
-  // that belongs there is (l % 8) ^ ((row >> 1) & 7). Rows past the tile
+// The tile's sums. kPaired: B's tile holds gate rows and up rows in turns of
+// 16 (column p of the tile is gate column 16 (p / 32) + p % 16 of the pair
+// block when p % 32 < 16, else the same up column), so a lane's registers
+// 0-7 and 8-15 of an MFMA tile are matching gate and up values.
+template <typename Op, typename Cfg, bool kPaired>
+__device__ __forceinline__ void mm_tile(const MmArgs& p, char* smem, const MmTile& t,
+                                        typename Op::Acc (&acc)[Cfg::WM][Cfg::WN]) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  // Load i of a wave covers rows (wave LOADS + i) 16 + lane / 4 of an operand's
+  // tile, lane l's 16 bytes landing at position l % 4 of the row: the chunk
+  // that belongs there is (l % 4) ^ ((row >> 2) & 3). Rows past the tile
   // repeat its last row; what they compute is not stored.
+  const int chunk = ((lane & 3) ^ ((lane >> 4) & 3)) << 4;
   const char* a[Cfg::A_LOADS];
   const char* b[Cfg::B_LOADS];
 #pragma unroll
   for (int i = 0; i < Cfg::A_LOADS; ++i) {
-    const int r = (wave * Cfg::A_LOADS + i) * 8 + (lane >> 3);
+    const int r = (wave * Cfg::A_LOADS + i) * 16 + (lane >> 2);
     int64_t src = t.row0 + min(r, t.rows - 1);
     if (p.perm) src = p.perm[src] / p.topk;
-    a[i] = p.a + src * p.a_pitch + (((lane & 7) ^ ((r >> 1) & 7)) << 4);
+    a[i] = p.a + src * p.a_pitch + chunk;
   }
 #pragma unroll
   for (int i = 0; i < Cfg::B_LOADS; ++i) {
-    const int r = (wave * Cfg::B_LOADS + i) * 8 + (lane >> 3);
+    const int r = (wave * Cfg::B_LOADS + i) * 16 + (lane >> 2);
     int64_t off;
     if (kPaired) {
       const int c = t.nt * (Cfg::BN / 2) + 16 * (r >> 5) + (r & 15);
@@ -202,7 +285,7 @@ __device__ __forceinline__ bool mm_tile(const MmArgs& p, char* smem, MmTile* til
     } else {
       off = min(t.nt * Cfg::BN + r, p.N - 1) * p.b_pitch;
     }
-    b[i] = p.b + t.group * p.b_group + off + (((lane & 7) ^ ((r >> 1) & 7)) << 4);
+    b[i] = p.b + t.group * p.b_group + off + chunk;
   }
   const int split = p.b2 ? p.k_split : p.nk;
   const int64_t a2 = p.b2 ? (p.a2 - p.a) - static_cast<int64_t>(split) * kMmRow : 0;
@@ -212,7 +295,7 @@ __device__ __forceinline__ bool mm_tile(const MmArgs& p, char* smem, MmTile* til
   const int wm = wave / Cfg::WAVES_N, wn = wave % Cfg::WAVES_N;
   const int a_frag = (wm * Cfg::WM * 32 + r32) * kMmRow;
   const int b_frag = (Cfg::BM + wn * Cfg::WN * 32 + r32) * kMmRow;
-  const int sw = g ^ ((r32 >> 1) & 7);
+  const int sw = g ^ ((r32 >> 2) & 3);
 #pragma unroll
   for (int i = 0; i < Cfg::WM; ++i)
 #pragma unroll
@@ -220,100 +303,150 @@ __device__ __forceinline__ bool mm_tile(const MmArgs& p, char* smem, MmTile* til
 #pragma unroll
       for (int q = 0; q < 16; ++q) acc[i][j][q] = 0;
 
-  mm_issue<Cfg::A_LOADS>(smem, a, 0, wave);
-  mm_issue<Cfg::B_LOADS>(smem + Cfg::BM * kMmRow, b, 0, wave);
+  // A ring of stage buffers: while stage s is multiplied out, the next
+  // Cfg::RING - 2 are in flight and one more is being issued.
+  constexpr int kLoads = Cfg::A_LOADS + Cfg::B_LOADS;
+  auto issue = [&](int st) {
+    char* buf = smem + (st % Cfg::RING) * Cfg::STAGE;
+    const int64_t off = static_cast<int64_t>(st) * kMmRow;
+    const bool first = st < split;
+    mm_issue<Cfg::A_LOADS>(buf, a, off + (first ? 0 : a2), wave);
+    mm_issue<Cfg::B_LOADS>(buf + Cfg::BM * kMmRow, b, off + (first ? 0 : b2), wave);
+  };
+  if constexpr (Cfg::DEEP) {
+    mm_deep<Op, Cfg>(smem, p.nk, a_frag, b_frag, sw, acc, [&](int st, char* buf, int u) {
+      const int64_t off = static_cast<int64_t>(st) * kMmRow;
+      const bool first = st < split;
+      if (u < Cfg::A_LOADS) {
+        const char* src = a[u < Cfg::A_LOADS ? u : 0] + off + (first ? 0 : a2);
+        char* dst = buf + (wave * Cfg::A_LOADS + u) * 1024;
+        __builtin_amdgcn_global_load_lds(src, dst, 16, 0, 0);
+      } else {
+        const char* src = b[u < Cfg::A_LOADS ? 0 : u - Cfg::A_LOADS] + off + (first ? 0 : b2);
+        char* dst = buf + Cfg::BM * kMmRow + (wave * Cfg::B_LOADS + u - Cfg::A_LOADS) * 1024;
+        __builtin_amdgcn_global_load_lds(src, dst, 16, 0, 0);
+      }
+    });
+    return;
+  }
+#pragma unroll
+  for (int st = 0; st < Cfg::RING - 1; ++st)
+    if (st < p.nk) issue(st);
   for (int s = 0; s < p.nk; ++s) {
     // this wave's loads of stage s have landed, then everyone's have, and
-    // the other buffer's readers are done
-    __builtin_amdgcn_s_waitcnt(0 | (0x7 << 4) | (0x0 << 8));
+    // the readers of the buffer before it are done
+    if (s + Cfg::RING - 2 < p.nk) mm_wait<kLoads * (Cfg::RING - 2)>();
+    else mm_wait<0>();
     asm volatile("s_barrier" ::: "memory");
-    if (s + 1 < p.nk) {
-      const int64_t off = static_cast<int64_t>(s + 1) * kMmRow;
-      const bool first = s + 1 < split;
-      char* next = smem + ((s + 1) & 1) * Cfg::STAGE;
-      mm_issue<Cfg::A_LOADS>(next, a, off + (first ? 0 : a2), wave);
-      mm_issue<Cfg::B_LOADS>(next + Cfg::BM * kMmRow, b, off + (first ? 0 : b2), wave);
-    }
-    mm_compute<Op, Cfg>(smem + (s & 1) * Cfg::STAGE, a_frag, b_frag, sw, acc);
+    if (s + Cfg::RING - 1 < p.nk) issue(s + Cfg::RING - 1);
+    mm_compute<Op, Cfg>(smem + (s % Cfg::RING) * Cfg::STAGE, a_frag, b_frag, sw, acc);
   }
-  return true;
 }
 
 // Hands a finished tile out by rows. Stored straight from the accumulators,
 // a store instruction would touch 32 rows with a few bytes each; instead each
 // wave writes strips of 32 rows into LDS of its own (the stage buffers, free
 // by now) and every lane takes eight consecutive columns of a row, so eight
-// (paired: four) lanes cover whole cache lines. f.cols(n) is called with the
-// lane's first column (within the tile; paired: within the tile's hidden
-// columns) before its rows, f.pre(k, m) for pass k's row m before the strip is
-// written (loads go there, so that they are all in flight at once), then
-// f.row(k, m, v) with the eight sums, or f.row(k, m, gate, up).
+// (paired: four) lanes cover whole cache lines. Callbacks, all inlined:
+//   f.cols(j, n)      strip column j's first column of this lane (within the
+//                     tile; paired: within the tile's hidden columns)
+//   f.start(i, k, m)  row m of strip row i, pass k
+//   f.pre(set, k, m)  the same before strip `set`'s rows are handed out
+//   f.row(set, i, j, k, m, v), or (.., gate, up): the eight sums
+// Vector memory completes in issue order, loads behind stores: a load that
+// is issued after a strip's stores costs the wait for all of them (24 us a
+// tile, more than the product took at 8 stages). So everything that does not
+// change is read first, and pre runs one strip ahead of the stores. For the
+// same reason nothing branches: a row past the tile repeats its last row's
+// bits (its operands were that row's) and is stored over it.
 constexpr int kMmStripPad = 16;  // bytes behind a strip row: spreads the rows over the banks
 template <typename Cfg>
 struct MmStrip {
   static constexpr int CB = Cfg::WN < 2 ? Cfg::WN : 2;  // MFMA tiles side by side in a strip
   static constexpr int PITCH = CB * 128 + kMmStripPad, BYTES = 32 * PITCH;
-  static_assert(Cfg::NW * BYTES <= 2 * Cfg::STAGE, "strips fit the stage buffers");
+  // the workgroup's LDS: the ring, or the strips where they are larger
+  static constexpr int LDS = Cfg::LDS > Cfg::NW * BYTES ? Cfg::LDS : Cfg::NW * BYTES;
 };
 
+// Passes over a strip: rows of it that a lane hands out.
+template <typename Cfg, bool kPaired>
+constexpr int mm_passes() {
+  return 32 / (64 / (MmStrip<Cfg>::CB * (kPaired ? 16 : 32) / 8));
+}
+
+// The callbacks that read what does not change; called before the main loop,
+// whose first wait covers them.
+template <typename Cfg, bool kPaired, typename F>
+__device__ __forceinline__ void mm_begin(int rows, F&& f) {
+  using S = MmStrip<Cfg>;
+  constexpr int COLS = S::CB * (kPaired ? 16 : 32), LPR = COLS / 8, RPP = 64 / LPR, PASSES = 32 / RPP;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int wm = wave / Cfg::WAVES_N, wn = wave % Cfg::WAVES_N;
+#pragma unroll
+  for (int j = 0; j < Cfg::WN / S::CB; ++j)
+    f.cols(j, (wn * Cfg::WN + j * S::CB) * (kPaired ? 16 : 32) + (lane % LPR) * 8);
+#pragma unroll
+  for (int i = 0; i < Cfg::WM; ++i)
+#pragma unroll
+    for (int k = 0; k < PASSES; ++k)
+      f.start(i, k, min((wm * Cfg::WM + i) * 32 + lane / LPR + k * RPP, rows - 1));
+}
+
 template <typename Cfg, bool kPaired, typename Acc, typename F>
-__device__ __forceinline__ void mm_drain(char* smem, const Acc (&acc)[Cfg::WM][Cfg::WN], F&& f) {
+__device__ __forceinline__ void mm_drain(char* smem, const Acc (&acc)[Cfg::WM][Cfg::WN], int rows, F&& f) {
   using S = MmStrip<Cfg>;
   constexpr int COLS = S::CB * (kPaired ? 16 : 32);  // columns handed out per strip row
   constexpr int LPR = COLS / 8, RPP = 64 / LPR, PASSES = 32 / RPP;
+  constexpr int NJ = Cfg::WN / S::CB, STRIPS = NJ * Cfg::WM;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int g = lane >> 5, r32 = lane & 31;
   const int wm = wave / Cfg::WAVES_N, wn = wave % Cfg::WAVES_N;
   char* strip = smem + wave * S::BYTES;
-  // every wave is done with the stages
-  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
   const int c8 = (lane % LPR) * 8, r0 = lane / LPR;
   // byte of the lane's first column in a strip row (paired: of its gate columns)
   const int at = kPaired ? (c8 / 16) * 128 + (c8 % 16) * 4 : c8 * 4;
+  auto m_of = [&](int i, int k) { return min((wm * Cfg::WM + i) * 32 + r0 + k * RPP, rows - 1); };
 #pragma unroll
-  for (int jb = 0; jb < Cfg::WN; jb += S::CB) {
-    f.cols((wn * Cfg::WN + jb) * (kPaired ? 16 : 32) + c8);
+  for (int k = 0; k < PASSES; ++k) f.pre(0, 0, k, m_of(0, k));
+  // every wave is done with the stages
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 #pragma unroll
-    for (int i = 0; i < Cfg::WM; ++i) {
-      const int m0 = (wm * Cfg::WM + i) * 32 + r0;
+  for (int n = 0; n < STRIPS; ++n) {
+    const int i = n % Cfg::WM, j = n / Cfg::WM;
+    if (n + 1 < STRIPS) {
 #pragma unroll
-      for (int k = 0; k < PASSES; ++k) f.pre(k, m0 + k * RPP);
-#pragma unroll
-      for (int j = 0; j < S::CB; ++j)
-#pragma unroll
-        for (int rr = 0; rr < 4; ++rr) {
-          u32x4 v;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const auto e = acc[i][jb + j][4 * rr + q];  // a value: bit_cast takes no vector element
-            v[q] = __builtin_bit_cast(uint32_t, e);
-          }
-          *reinterpret_cast<u32x4*>(strip + r32 * S::PITCH + j * 128 + rr * 32 + g * 16) = v;
-        }
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-#pragma unroll
-      for (int k = 0; k < PASSES; ++k) {
-        const char* src = strip + (r0 + k * RPP) * S::PITCH + at;
-        u32x4 lo = *reinterpret_cast<const u32x4*>(src), hi = *reinterpret_cast<const u32x4*>(src + 16);
-        const uint32_t v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-        if constexpr (kPaired) {
-          lo = *reinterpret_cast<const u32x4*>(src + 64);
-          hi = *reinterpret_cast<const u32x4*>(src + 80);
-          const uint32_t u[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-          f.row(k, m0 + k * RPP, v, u);
-        } else {
-          f.row(k, m0 + k * RPP, v);
-        }
-      }
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      for (int k = 0; k < PASSES; ++k)
+        f.pre((n + 1) & 1, (n + 1) / Cfg::WM, k, m_of((n + 1) % Cfg::WM, k));
     }
+#pragma unroll
+    for (int c = 0; c < S::CB; ++c)
+#pragma unroll
+      for (int rr = 0; rr < 4; ++rr) {
+        u32x4 v;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const auto e = acc[i][j * S::CB + c][4 * rr + q];  // a value: bit_cast takes no vector element
+          v[q] = __builtin_bit_cast(uint32_t, e);
+        }
+        *reinterpret_cast<u32x4*>(strip + r32 * S::PITCH + c * 128 + rr * 32 + g * 16) = v;
+      }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll
+    for (int k = 0; k < PASSES; ++k) {
+      const char* src = strip + (r0 + k * RPP) * S::PITCH + at;
+      u32x4 lo = *reinterpret_cast<const u32x4*>(src), hi = *reinterpret_cast<const u32x4*>(src + 16);
+      const uint32_t v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+      if constexpr (kPaired) {
+        lo = *reinterpret_cast<const u32x4*>(src + 64);
+        hi = *reinterpret_cast<const u32x4*>(src + 80);
+        const uint32_t u[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+        f.row(n & 1, i, j, k, m_of(i, k), v, u);
+      } else {
+        f.row(n & 1, i, j, k, m_of(i, k), v);
+      }
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   }
-}
-
-// Passes of mm_drain over a strip (the k of its callbacks).
-template <typename Cfg, bool kPaired>
-constexpr int mm_passes() {
-  return 32 / (64 / (MmStrip<Cfg>::CB * (kPaired ? 16 : 32) / 8));
 }
 
 }  // namespace moe
