@@ -424,6 +424,8 @@ void tiles_at(const char* name, const MmArgs& a, const FfnOut& o, hipStream_t s)
   // the hidden matrices are written to their padded width
   const int64_t n = kMode == kPlain ? p.N : o.ld;
   p.tiles_n = static_cast<int>((n + per - 1) / per);
+  p.nk *= 128 / Cfg::ROW;
+  p.k_split *= 128 / Cfg::ROW;
   const int64_t grid = (p.M + Cfg::BM - 1) / Cfg::BM * p.tiles_n;
   MOE_LAUNCH(name, (ffn_tile_kernel<T, Cfg, kMode, kAct>), dim3(static_cast<unsigned>(grid)),
              dim3(Cfg::NT), 0, s, p, o);
@@ -431,13 +433,13 @@ void tiles_at(const char* name, const MmArgs& a, const FfnOut& o, hipStream_t s)
 
 template <typename T, int kMode, int kAct>
 void tiles(const char* name, const MmArgs& p, const FfnOut& o, hipStream_t s) {
-  using Big = MmCfg<256, 256, 2, 2>;
-  using Mid = MmCfg<128, 128, 2, 2, 3>;
-  using Small = MmCfg<64, 64, 2, 2>;
-  using Low = MmCfg<32, 64, 1, 2>;
+  using Big = MmCfg<256, 256, 2, 2, 2, 128>;
+  using Mid = MmCfg<128, 128, 2, 2, 3, 64>;
+  using Small = MmCfg<64, 64, 2, 2, 2, 128>;
+  using Low = MmCfg<32, 64, 1, 2, 2, 128>;
   const int64_t cols = kMode == kGated ? 2 * static_cast<int64_t>(p.N) : p.N;
   auto count = [&](int t) { return (p.M + t - 1) / t * ((cols + t - 1) / t); };
-  if (sizeof(T) == 2 && p.nk >= 32 && count(256) >= cu_count()) tiles_at<T, Big, kMode, kAct>(name, p, o, s);
+  if (sizeof(T) == 2 && p.nk >= 16 && count(256) >= cu_count()) tiles_at<T, Big, kMode, kAct>(name, p, o, s);
   else if (count(128) >= cu_count()) tiles_at<T, Mid, kMode, kAct>(name, p, o, s);
   else if (p.M > 32) tiles_at<T, Small, kMode, kAct>(name, p, o, s);
   else tiles_at<T, Low, kMode, kAct>(name, p, o, s);
@@ -474,7 +476,7 @@ MmArgs rows_of(const void* a, int64_t lda, const void* b, int64_t ldb, int64_t M
   p.a_pitch = lda * static_cast<int64_t>(sizeof(T));
   p.b = static_cast<const char*>(b);
   p.b_pitch = ldb * static_cast<int64_t>(sizeof(T));
-  p.nk = static_cast<int>(K * static_cast<int64_t>(sizeof(T)) / kMmRow);
+  p.nk = static_cast<int>(K * static_cast<int64_t>(sizeof(T)) / 128);
   p.M = M;
   p.N = N;
   return p;

@@ -228,6 +228,8 @@ void i8_tiles(const MmArgs& a, const I8Out& o, bool paired, int64_t row_tiles, h
   MmArgs p = a;
   const int per = paired ? Cfg::BN / 2 : Cfg::BN;
   p.tiles_n = (p.N + per - 1) / per;
+  p.nk *= 128 / Cfg::ROW;
+  p.k_split *= 128 / Cfg::ROW;
   const unsigned grid = static_cast<unsigned>(row_tiles * p.tiles_n);
   if (paired)
     MOE_LAUNCH("linear_i8_gated", (i8_tile_kernel<T, Cfg, true>), dim3(grid), dim3(Cfg::NT), 0, s, p, o);
@@ -316,7 +318,7 @@ hipError_t launch_linear_i8(const moe_i8_linear& l, const void* x, const float* 
   p.b = reinterpret_cast<const char*>(wq);
   p.b_pitch = pitch;
   p.b_group = static_cast<int64_t>(l.outputs) * pitch;
-  p.nk = static_cast<int>(pitch / kMmRow);
+  p.nk = static_cast<int>(pitch / 128);
   p.N = paired ? l.outputs / 2 : l.outputs;
   p.half = p.N * pitch;
   p.topk = l.top_k;
@@ -331,13 +333,13 @@ hipError_t launch_linear_i8(const moe_i8_linear& l, const void* x, const float* 
   auto go = [&](auto t) {
     using T = decltype(t);
     auto tiles = [&](int bm) { return (p.M + bm - 1) / bm + (r ? p.groups : 0); };
-    using Big = MmCfg<256, 256, 2, 2>;
-    using Mid = MmCfg<128, 128, 2, 2, 3>;
-    using Small = MmCfg<64, 64, 2, 2>;
-    using Low = MmCfg<32, 64, 1, 2>;
+    using Big = MmCfg<256, 256, 2, 2, 2, 128>;
+    using Mid = MmCfg<128, 128, 2, 2, 3, 64>;
+    using Small = MmCfg<64, 64, 2, 2, 2, 128>;
+    using Low = MmCfg<32, 64, 1, 2, 2, 128>;
     const int64_t per_group = p.M / p.groups;
     auto count = [&](int t) { return (p.M + t - 1) / t * ((l.outputs + t - 1) / t); };
-    if (p.nk >= 32 && per_group >= 256 && count(256) >= cu_count()) i8_tiles<T, Big>(p, o, paired, tiles(256), s);
+    if (p.nk >= 16 && per_group >= 256 && count(256) >= cu_count()) i8_tiles<T, Big>(p, o, paired, tiles(256), s);
     else if (per_group >= 128 && count(128) >= cu_count()) i8_tiles<T, Mid>(p, o, paired, tiles(128), s);
     else if (per_group > 32) i8_tiles<T, Small>(p, o, paired, tiles(64), s);
     else i8_tiles<T, Low>(p, o, paired, tiles(32), s);

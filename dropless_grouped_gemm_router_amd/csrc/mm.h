@@ -2,8 +2,8 @@
 //
 //   C[m][n] = sum_k A[m][k] B[n][k]     bf16 or fp32 -> fp32, int8 -> int32
 //
-// Both operands are rows of K-contiguous bytes, a stage being 64 bytes of
-// every row (32 bf16, 16 fp32 or 64 int8), so one engine serves all types:
+// Both operands are rows of K-contiguous bytes, a stage being 64 or 128
+// bytes of every row (128: 64 bf16, 32 fp32 or 128 int8), so one engine serves all types:
 // the fragments of mfma 32x32x16 bf16, of 32x32x32 i8 and of four 32x32x2
 // fp32 steps are the same 16 bytes a lane. Rows come through pointers computed once per tile, which is where
 // gathering by the expert permutation, clamping at the last row and the
@@ -66,21 +66,30 @@ struct MmArgs {
   int64_t half;              // paired: bytes from a gate row of B to its up row
 };
 
-constexpr int kMmRow = 64;  // bytes of a row in a stage
 
-template <int BM_, int BN_, int WAVES_M_, int WAVES_N_, int RING_ = 4>
+template <int BM_, int BN_, int WAVES_M_, int WAVES_N_, int RING_ = 4, int ROW_ = 64>
 struct MmCfg {
+  static constexpr int ROW = ROW_;    // bytes of a row in a stage
+  static constexpr int CPR = ROW / 16, RPL = 64 / CPR;  // chunks of a row; rows of a load
+  static constexpr int STEPS = ROW / 32;
   static constexpr int RING = RING_;  // stage buffers
   static constexpr int BM = BM_, BN = BN_, WAVES_M = WAVES_M_, WAVES_N = WAVES_N_;
   static constexpr int NW = WAVES_M * WAVES_N, NT = 64 * NW;
   static constexpr int WM = BM / WAVES_M / 32, WN = BN / WAVES_N / 32;  // MFMA tiles per wave
-  static constexpr int A_LOADS = BM / 16 / NW, B_LOADS = BN / 16 / NW;     // a wave and stage
+  static constexpr int A_LOADS = BM / RPL / NW, B_LOADS = BN / RPL / NW;     // a wave and stage
   static constexpr bool DEEP = WM * WN == 16;  // one wave to a SIMD: mm_deep
   static constexpr int WPE = DEEP ? 1 : 2;       // waves to a SIMD
-  static constexpr int STAGE = (BM + BN) * kMmRow, LDS = RING * STAGE;
+  static constexpr int STAGE = (BM + BN) * ROW, LDS = RING * STAGE;
   static_assert(BM == WAVES_M * WM * 32 && BN == WAVES_N * WN * 32, "tiles");
-  static_assert(BM % (16 * NW) == 0 && BN % (16 * NW) == 0, "loads");
+  static_assert(BM % (RPL * NW) == 0 && BN % (RPL * NW) == 0, "loads");
 };
+
+// Position of chunk c of LDS row r: c ^ mm_swizzle(r), which spreads the rows
+// that a fragment read touches over all banks.
+template <typename Cfg>
+__device__ __forceinline__ int mm_swizzle(int r) {
+  return Cfg::ROW == 128 ? (r >> 1) & 7 : (r >> 2) & 3;
+}
 
 // A tile's rows: first row, count (0: nothing to do), weight group.
 struct MmTile {
@@ -127,7 +136,7 @@ __device__ __forceinline__ void mm_tile_order(int w, int tiles_m, int tiles_n, i
   *nt = in / high;
 }
 
-// One stage's loads of one operand: NL loads a wave, of 16 rows (1 KiB) each.
+// One stage's loads of one operand: NL loads a wave, of 1 KiB each.
 template <int NL>
 __device__ __forceinline__ void mm_issue(char* buf, const char* const* rows, int64_t off, int wave) {
 #pragma unroll
@@ -149,15 +158,15 @@ template <typename Op, typename Cfg>
 __device__ __forceinline__ void mm_compute(const char* buf, int a_frag, int b_frag, int sw,
                                            typename Op::Acc (&acc)[Cfg::WM][Cfg::WN]) {
 #pragma unroll
-  for (int q = 0; q < 2; ++q) {
+  for (int q = 0; q < Cfg::STEPS; ++q) {
     u32x4 xf[Cfg::WM], wf[Cfg::WN];
     const int at = ((2 * q) ^ sw) << 4;
 #pragma unroll
     for (int i = 0; i < Cfg::WM; ++i)
-      xf[i] = *reinterpret_cast<const u32x4*>(buf + a_frag + i * 32 * kMmRow + at);
+      xf[i] = *reinterpret_cast<const u32x4*>(buf + a_frag + i * 32 * Cfg::ROW + at);
 #pragma unroll
     for (int j = 0; j < Cfg::WN; ++j)
-      wf[j] = *reinterpret_cast<const u32x4*>(buf + b_frag + j * 32 * kMmRow + at);
+      wf[j] = *reinterpret_cast<const u32x4*>(buf + b_frag + j * 32 * Cfg::ROW + at);
 #pragma unroll
     for (int i = 0; i < Cfg::WM; ++i)
 #pragma unroll
@@ -169,22 +178,24 @@ __device__ __forceinline__ void mm_compute(const char* buf, int a_frag, int b_fr
 // 64 FLOP (bf16) a byte read from LDS against 42.7 for eight waves of
 // 64 x 128, whose reads and the stage writes together would fill the LDS
 // pipe for as long as the MFMAs run. Nothing else hides a latency here, so
-// the fragments of a step (half a stage) are read while the step before is
-// multiplied, two MFMAs to a read, and a stage's loads are spread the same
-// way. One barrier a stage, between its two steps: it says that the next
-// stage is whole and that nobody reads this one any more, whose buffer is
-// then loaded again (four stages ahead).
+// the fragments of a step (32 bytes of K) are read while the step before is
+// multiplied, two MFMAs to a read. One barrier a stage, before its last step:
+// it says that the next stage is whole and that nobody reads this one any
+// more, whose buffer is then loaded again. At 16384 x 4096 x 4096 int8: 310
+// us against 328 for eight waves; four buffers of 64-byte rows, with twice
+// the requests for the same bytes, take 325, and 335 with the loads spread
+// over all steps.
 template <typename Op, typename Cfg, typename Load>
 __device__ __forceinline__ void mm_deep(char* smem, int nk, int a_frag, int b_frag, int sw,
                                         typename Op::Acc (&acc)[Cfg::WM][Cfg::WN], Load&& load) {
-  constexpr int W = 4, kLoads = Cfg::A_LOADS + Cfg::B_LOADS;
-  static_assert(Cfg::WM == W && Cfg::WN == W && kLoads == 8, "128 x 128 a wave");
+  constexpr int W = 4, kLoads = Cfg::A_LOADS + Cfg::B_LOADS, kSteps = Cfg::STEPS;
+  static_assert(Cfg::WM == W && Cfg::WN == W && kLoads % 8 == 0 && kSteps % 2 == 0, "128 x 128 a wave");
   u32x4 x[2][W], w[2][W];
-  const int at0 = sw << 4, at1 = (2 ^ sw) << 4;
-  // fragment f of a step: 0-3 of A, 4-7 of B
-  auto read = [&](const char* buf, int at, int f, int set) {
-    if (f < W) x[set][f & 3] = *reinterpret_cast<const u32x4*>(buf + a_frag + (f & 3) * 32 * kMmRow + at);
-    else w[set][f & 3] = *reinterpret_cast<const u32x4*>(buf + b_frag + (f & 3) * 32 * kMmRow + at);
+  // fragment f of step q: 0-3 of A, 4-7 of B
+  auto read = [&](const char* buf, int q, int f, int set) {
+    const int at = ((2 * q) ^ sw) << 4;
+    if (f < W) x[set][f & 3] = *reinterpret_cast<const u32x4*>(buf + a_frag + (f & 3) * 32 * Cfg::ROW + at);
+    else w[set][f & 3] = *reinterpret_cast<const u32x4*>(buf + b_frag + (f & 3) * 32 * Cfg::ROW + at);
   };
   auto multiply = [&](int set, int n) {
     const int i = n >> 2, j = n & 3;
@@ -197,35 +208,37 @@ __device__ __forceinline__ void mm_deep(char* smem, int nk, int a_frag, int b_fr
   mm_wait<kLoads * (Cfg::RING - 1)>();
   asm volatile("s_barrier" ::: "memory");
 #pragma unroll
-  for (int f = 0; f < 2 * W; ++f) read(smem, at0, f, 0);
+  for (int f = 0; f < 2 * W; ++f) read(smem, 0, f, 0);
   for (int s = 0; s < nk; ++s) {
-    const char* cur = smem + (s % Cfg::RING) * Cfg::STAGE;
+    char* cur = smem + (s % Cfg::RING) * Cfg::STAGE;
     const char* next = smem + ((s + 1) % Cfg::RING) * Cfg::STAGE;
 #pragma unroll
-    for (int f = 0; f < 8; ++f) {
-      read(cur, at1, f, 1);
-      multiply(0, 2 * f);
-      multiply(0, 2 * f + 1);
-      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // an LDS read
-      __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);  // two MFMAs
+    for (int q = 0; q + 1 < kSteps; ++q) {
+#pragma unroll
+      for (int f = 0; f < 8; ++f) {
+        read(cur, q + 1, f, (q + 1) & 1);
+        multiply(q & 1, 2 * f);
+        multiply(q & 1, 2 * f + 1);
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // an LDS read
+        __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);  // two MFMAs
+      }
+      __builtin_amdgcn_sched_barrier(0);
     }
-    // stage s + 1 has landed (s + 2, s + 3 may be in flight), the reads of
-    // stage s are done
-    __builtin_amdgcn_sched_barrier(0);
+    // stage s + 1 has landed, the reads of stage s are done
     mm_wait<kLoads * (Cfg::RING - 2)>();
     asm volatile("s_barrier" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
     // past the last stage its loads are made again, into a buffer that is
     // not read, so that the loop has one body and one count
     const int ahead = min(s + Cfg::RING, nk - 1);
-    char* into = smem + (s % Cfg::RING) * Cfg::STAGE;
 #pragma unroll
     for (int f = 0; f < 8; ++f) {
-      load(ahead, into, f);
-      read(next, at0, f, 0);
+#pragma unroll
+      for (int u = 0; u < kLoads / 8; ++u) load(ahead, cur, f * (kLoads / 8) + u);
+      read(next, 0, f, 0);
       multiply(1, 2 * f);
       multiply(1, 2 * f + 1);
-      __builtin_amdgcn_sched_group_barrier(0x010, 1, 1);  // a load
+      __builtin_amdgcn_sched_group_barrier(0x010, kLoads / 8, 1);  // loads
       __builtin_amdgcn_sched_group_barrier(0x100, 1, 1);
       __builtin_amdgcn_sched_group_barrier(0x008, 2, 1);
     }
@@ -261,23 +274,24 @@ template <typename Op, typename Cfg, bool kPaired>
 __device__ __forceinline__ void mm_tile(const MmArgs& p, char* smem, const MmTile& t,
                                         typename Op::Acc (&acc)[Cfg::WM][Cfg::WN]) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  // Load i of a wave covers rows (wave LOADS + i) 16 + lane / 4 of an operand's
-  // tile, lane l's 16 bytes landing at position l % 4 of the row: the chunk
-  // that belongs there is (l % 4) ^ ((row >> 2) & 3). Rows past the tile
-  // repeat its last row; what they compute is not stored.
-  const int chunk = ((lane & 3) ^ ((lane >> 4) & 3)) << 4;
+  // Load i of a wave covers rows (wave LOADS + i) RPL + lane / CPR of an
+  // operand's tile, lane l's 16 bytes landing at position l % CPR of the row:
+  // the chunk that belongs there is (l % CPR) ^ mm_swizzle(row). Rows past the
+  // tile repeat its last row; what they compute is not stored.
   const char* a[Cfg::A_LOADS];
   const char* b[Cfg::B_LOADS];
 #pragma unroll
   for (int i = 0; i < Cfg::A_LOADS; ++i) {
-    const int r = (wave * Cfg::A_LOADS + i) * 16 + (lane >> 2);
+    const int r = (wave * Cfg::A_LOADS + i) * Cfg::RPL + lane / Cfg::CPR;
+    const int chunk = ((lane % Cfg::CPR) ^ mm_swizzle<Cfg>(r)) << 4;
     int64_t src = t.row0 + min(r, t.rows - 1);
     if (p.perm) src = p.perm[src] / p.topk;
     a[i] = p.a + src * p.a_pitch + chunk;
   }
 #pragma unroll
   for (int i = 0; i < Cfg::B_LOADS; ++i) {
-    const int r = (wave * Cfg::B_LOADS + i) * 16 + (lane >> 2);
+    const int r = (wave * Cfg::B_LOADS + i) * Cfg::RPL + lane / Cfg::CPR;
+    const int chunk = ((lane % Cfg::CPR) ^ mm_swizzle<Cfg>(r)) << 4;
     int64_t off;
     if (kPaired) {
       const int c = t.nt * (Cfg::BN / 2) + 16 * (r >> 5) + (r & 15);
@@ -288,14 +302,14 @@ __device__ __forceinline__ void mm_tile(const MmArgs& p, char* smem, const MmTil
     b[i] = p.b + t.group * p.b_group + off + chunk;
   }
   const int split = p.b2 ? p.k_split : p.nk;
-  const int64_t a2 = p.b2 ? (p.a2 - p.a) - static_cast<int64_t>(split) * kMmRow : 0;
-  const int64_t b2 = p.b2 ? (p.b2 - p.b) - static_cast<int64_t>(split) * kMmRow : 0;
+  const int64_t a2 = p.b2 ? (p.a2 - p.a) - static_cast<int64_t>(split) * Cfg::ROW : 0;
+  const int64_t b2 = p.b2 ? (p.b2 - p.b) - static_cast<int64_t>(split) * Cfg::ROW : 0;
 
   const int g = lane >> 5, r32 = lane & 31;
   const int wm = wave / Cfg::WAVES_N, wn = wave % Cfg::WAVES_N;
-  const int a_frag = (wm * Cfg::WM * 32 + r32) * kMmRow;
-  const int b_frag = (Cfg::BM + wn * Cfg::WN * 32 + r32) * kMmRow;
-  const int sw = g ^ ((r32 >> 2) & 3);
+  const int a_frag = (wm * Cfg::WM * 32 + r32) * Cfg::ROW;
+  const int b_frag = (Cfg::BM + wn * Cfg::WN * 32 + r32) * Cfg::ROW;
+  const int sw = g ^ mm_swizzle<Cfg>(r32);
 #pragma unroll
   for (int i = 0; i < Cfg::WM; ++i)
 #pragma unroll
@@ -308,14 +322,14 @@ __device__ __forceinline__ void mm_tile(const MmArgs& p, char* smem, const MmTil
   constexpr int kLoads = Cfg::A_LOADS + Cfg::B_LOADS;
   auto issue = [&](int st) {
     char* buf = smem + (st % Cfg::RING) * Cfg::STAGE;
-    const int64_t off = static_cast<int64_t>(st) * kMmRow;
+    const int64_t off = static_cast<int64_t>(st) * Cfg::ROW;
     const bool first = st < split;
     mm_issue<Cfg::A_LOADS>(buf, a, off + (first ? 0 : a2), wave);
-    mm_issue<Cfg::B_LOADS>(buf + Cfg::BM * kMmRow, b, off + (first ? 0 : b2), wave);
+    mm_issue<Cfg::B_LOADS>(buf + Cfg::BM * Cfg::ROW, b, off + (first ? 0 : b2), wave);
   };
   if constexpr (Cfg::DEEP) {
     mm_deep<Op, Cfg>(smem, p.nk, a_frag, b_frag, sw, acc, [&](int st, char* buf, int u) {
-      const int64_t off = static_cast<int64_t>(st) * kMmRow;
+      const int64_t off = static_cast<int64_t>(st) * Cfg::ROW;
       const bool first = st < split;
       if (u < Cfg::A_LOADS) {
         const char* src = a[u < Cfg::A_LOADS ? u : 0] + off + (first ? 0 : a2);
@@ -323,7 +337,7 @@ __device__ __forceinline__ void mm_tile(const MmArgs& p, char* smem, const MmTil
         __builtin_amdgcn_global_load_lds(src, dst, 16, 0, 0);
       } else {
         const char* src = b[u < Cfg::A_LOADS ? 0 : u - Cfg::A_LOADS] + off + (first ? 0 : b2);
-        char* dst = buf + Cfg::BM * kMmRow + (wave * Cfg::B_LOADS + u - Cfg::A_LOADS) * 1024;
+        char* dst = buf + Cfg::BM * Cfg::ROW + (wave * Cfg::B_LOADS + u - Cfg::A_LOADS) * 1024;
         __builtin_amdgcn_global_load_lds(src, dst, 16, 0, 0);
       }
     });
