@@ -13,10 +13,12 @@ be ordered by the caller, as for every call of the library.
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
 from dataclasses import dataclass
+from functools import lru_cache
 from typing import Dict, Optional
+
+import torch
 
 from . import binding
 from .binding import (DTYPES, MOE_BF16, MOE_FP32, _check, _ptr, _stream, load as _load_library,
@@ -165,15 +167,17 @@ def moe_linear_i8(l: moe_i8_linear, x, x_scale, wq, w_scale, bias, routing: Opti
 
 
 # ------------------------------------------------------------ tensor checks
+#
+# These run on every call, in front of kernels that take a few microseconds:
+# a tensor that fits costs one expression, and the problem structs of the C
+# calls are kept by their values.
 
-def _torch_dtype(d):
-    import torch
-    return {MOE_FP32: torch.float32, MOE_BF16: torch.bfloat16}[_dtype(d)]
+_TORCH = {"fp32": torch.float32, "bf16": torch.bfloat16, MOE_FP32: torch.float32,
+          MOE_BF16: torch.bfloat16}
+_CODE = {torch.float32: MOE_FP32, torch.bfloat16: MOE_BF16}
 
 
-def _want(name, t, shape, dtype, device, strided=False):
-    """``t`` is a tensor of this shape, type and device: contiguous, or with
-    ``strided`` a matrix whose rows are contiguous."""
+def _refuse(name, t, shape, dtype, device, strided=False):
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.dtype != dtype:
@@ -181,30 +185,49 @@ def _want(name, t, shape, dtype, device, strided=False):
     if t.device != device:
         raise ValueError(f"{name}: on {t.device}, expected {device}")
     if strided:
-        if t.shape[1] > 1 and t.stride(1) != 1 or t.shape[0] > 1 and t.stride(0) < t.shape[1]:
-            raise ValueError(f"{name}: rows have to be contiguous and apart, strides {t.stride()}")
-    elif not t.is_contiguous():
-        raise ValueError(f"{name}: has to be contiguous")
+        raise ValueError(f"{name}: rows have to be contiguous and apart, strides {t.stride()}")
+    raise ValueError(f"{name}: has to be contiguous")
 
 
-def _ld(t) -> int:
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+def _want(name, t, shape, dtype, device):
+    """``t`` is a contiguous tensor of this shape, type and device."""
+    if t.shape != shape or t.dtype is not dtype or t.device != device or not t.is_contiguous():
+        _refuse(name, t, shape, dtype, device)
 
 
-@contextlib.contextmanager
-def _on(device):
-    import torch
+def _want_rows(name, t, shape, dtype, device) -> int:
+    """``t`` is a matrix of this shape, type and device whose rows are
+    contiguous and do not overlap; returns the elements between rows."""
+    if t.shape != shape or t.dtype is not dtype or t.device != device:
+        _refuse(name, t, shape, dtype, device)
+    if t.is_contiguous():
+        return shape[1]
+    row, col = t.stride()
+    if shape[1] > 1 and col != 1 or shape[0] > 1 and row < shape[1]:
+        _refuse(name, t, shape, dtype, device, strided=True)
+    return row if shape[0] > 1 else shape[1]
+
+
+def _code(t) -> int:
+    if t.dtype not in _CODE:
+        raise ValueError(f"{t.dtype}: float32 or bfloat16 is supported")
+    return _CODE[t.dtype]
+
+
+def _run(where, device, stream, fn, *args):
+    """fn(*args, stream) on the tensors' device."""
     if device.type != "cuda":
         raise ValueError(f"tensors have to be on a GPU, not on {device}")
-    if torch.cuda.current_device() == device.index:
-        yield
-    else:
+    if torch.cuda.current_device() != device.index:
         with torch.cuda.device(device):
-            yield
+            status = fn(*args, _stream(stream))
+    else:
+        status = fn(*args, _stream(stream))
+    if status:
+        _check(status, where)
 
 
 def _device(device):
-    import torch
     d = torch.device(device)
     if d.type == "cuda" and d.index is None:
         d = torch.device("cuda", torch.cuda.current_device())
@@ -226,75 +249,70 @@ class NormBuffers:
     workspace: Optional[object] = None
 
 
+@lru_cache(maxsize=256)
+def _norm(*fields):
+    n = moe_norm(*fields)
+    return n, ctypes.byref(n)
+
+
 def allocate_norm(rows: int, width: int, dtype, device="cuda", training: bool = False) -> NormBuffers:
-    import torch
-    dt, device = _torch_dtype(dtype), _device(device)
+    dt, device = _TORCH[dtype], _device(device)
     f32 = dict(dtype=torch.float32, device=device)
     b = NormBuffers(y=torch.empty((rows, width), dtype=dt, device=device),
                     mean=torch.empty(rows, **f32), rstd=torch.empty(rows, **f32))
     if training:
-        n = moe_norm(rows, width, _dtype(dtype), 0.0, 0, 0, 0, 0)
-        with _on(device):
-            nws = moe_layer_norm_workspace_bytes(n)
+        nws = moe_layer_norm_workspace_bytes(moe_norm(rows, width, _dtype(dtype), 0.0, 0, 0, 0, 0))
         b.grad_x = torch.empty((rows, width), dtype=dt, device=device)
         b.grad_weight, b.grad_bias = torch.empty(width, **f32), torch.empty(width, **f32)
         b.workspace = torch.empty(nws, dtype=torch.uint8, device=device)
     return b
 
 
-def _code(t) -> int:
-    import torch
-    if t.dtype == torch.bfloat16:
-        return MOE_BF16
-    if t.dtype == torch.float32:
-        return MOE_FP32
-    raise ValueError(f"{t.dtype}: float32 or bfloat16 is supported")
-
-
 def layer_norm(x, weight, bias, eps: float, buf: NormBuffers, stream=None):
     """Layer norm over the rows of x [rows, width] (rows may be strided);
     weight and bias are fp32 or None. Returns buf.y, with buf.mean and
     buf.rstd kept for the backward pass."""
-    import torch
     if x.dim() != 2:
         raise ValueError(f"x: a matrix is expected, not {x.dim()} dimensions")
-    rows, width = x.shape
-    dev = x.device
-    _want("x", x, (rows, width), x.dtype, dev, strided=True)
-    for name, t in (("weight", weight), ("bias", bias)):
-        if t is not None:
-            _want(name, t, (width,), torch.float32, dev)
-    _want("y", buf.y, (rows, width), x.dtype, dev, strided=True)
-    _want("mean", buf.mean, (rows,), torch.float32, dev)
-    _want("rstd", buf.rstd, (rows,), torch.float32, dev)
-    n = moe_norm(rows, width, _code(x), eps, _ld(x), _ld(buf.y), 0, 0)
-    with _on(dev):
-        moe_layer_norm(n, x, weight, bias, buf.y, buf.mean, buf.rstd, stream)
-    return buf.y
+    shape, dt, dev, f32 = x.shape, x.dtype, x.device, torch.float32
+    rows, width = shape
+    ld_x = _want_rows("x", x, shape, dt, dev)
+    if weight is not None:
+        _want("weight", weight, (width,), f32, dev)
+    if bias is not None:
+        _want("bias", bias, (width,), f32, dev)
+    y, mean, rstd = buf.y, buf.mean, buf.rstd
+    ld_y = _want_rows("y", y, shape, dt, dev)
+    _want("mean", mean, (rows,), f32, dev)
+    _want("rstd", rstd, (rows,), f32, dev)
+    n = _norm(rows, width, _code(x), eps, ld_x, ld_y, 0, 0)
+    _run("moe_layer_norm", dev, stream, load().moe_layer_norm, n[1], x.data_ptr(), _ptr(weight),
+         _ptr(bias), y.data_ptr(), mean.data_ptr(), rstd.data_ptr())
+    return y
 
 
 def layer_norm_backward(x, weight, grad_out, buf: NormBuffers, stream=None):
     """Gradients of sum(y * grad_out) after ``layer_norm`` with the same
     buffers: (grad_x, grad_weight, grad_bias), the last two in fp32."""
-    import torch
-    rows, width = x.shape
-    dev = x.device
-    _want("x", x, (rows, width), x.dtype, dev, strided=True)
-    if weight is not None:
-        _want("weight", weight, (width,), torch.float32, dev)
-    _want("grad_out", grad_out, (rows, width), x.dtype, dev, strided=True)
-    if buf.grad_x is None:
+    shape, dt, dev, f32 = x.shape, x.dtype, x.device, torch.float32
+    rows, width = shape
+    gx, gw, gb = buf.grad_x, buf.grad_weight, buf.grad_bias
+    if gx is None:
         raise ValueError("the buffers were allocated without training=True")
-    _want("grad_x", buf.grad_x, (rows, width), x.dtype, dev, strided=True)
-    for name in ("mean", "rstd"):
-        _want(name, getattr(buf, name), (rows,), torch.float32, dev)
-    for name in ("grad_weight", "grad_bias"):
-        _want(name, getattr(buf, name), (width,), torch.float32, dev)
-    n = moe_norm(rows, width, _code(x), 0.0, _ld(x), 0, _ld(grad_out), _ld(buf.grad_x))
-    with _on(dev):
-        moe_layer_norm_bwd(n, x, weight, buf.mean, buf.rstd, grad_out, buf.grad_x, buf.grad_weight,
-                           buf.grad_bias, buf.workspace, stream=stream)
-    return buf.grad_x, buf.grad_weight, buf.grad_bias
+    ld_x = _want_rows("x", x, shape, dt, dev)
+    ld_go = _want_rows("grad_out", grad_out, shape, dt, dev)
+    ld_gx = _want_rows("grad_x", gx, shape, dt, dev)
+    if weight is not None:
+        _want("weight", weight, (width,), f32, dev)
+    _want("mean", buf.mean, (rows,), f32, dev)
+    _want("rstd", buf.rstd, (rows,), f32, dev)
+    _want("grad_weight", gw, (width,), f32, dev)
+    _want("grad_bias", gb, (width,), f32, dev)
+    n = _norm(rows, width, _code(x), 0.0, ld_x, 0, ld_go, ld_gx)
+    _run("moe_layer_norm_bwd", dev, stream, load().moe_layer_norm_bwd, n[1], x.data_ptr(),
+         _ptr(weight), buf.mean.data_ptr(), buf.rstd.data_ptr(), grad_out.data_ptr(), gx.data_ptr(),
+         gw.data_ptr(), gb.data_ptr(), buf.workspace.data_ptr(), buf.workspace.numel())
+    return gx, gw, gb
 
 
 # -------------------------------------------------- gated feed-forward block
@@ -311,8 +329,14 @@ class GatedFfn:
     grad_dtype: str = "fp32"  # of the weight gradients: fp32, or dtype
 
     def struct(self) -> moe_ffn:
-        return moe_ffn(self.tokens, self.d_model, self.d_hidden, DTYPES[self.dtype], ACTS[self.act],
-                       DTYPES[self.grad_dtype])
+        return _ffn(self.tokens, self.d_model, self.d_hidden, DTYPES[self.dtype], ACTS[self.act],
+                    DTYPES[self.grad_dtype])[0]
+
+
+@lru_cache(maxsize=256)
+def _ffn(*fields):
+    f = moe_ffn(*fields)
+    return f, ctypes.byref(f)
 
 
 @dataclass
@@ -327,16 +351,14 @@ class FfnBuffers:
 
 
 def allocate_ffn(f: GatedFfn, device="cuda", training: bool = False) -> FfnBuffers:
-    import torch
-    dt, device, c = _torch_dtype(f.dtype), _device(device), f.struct()
-    with _on(device):
-        nws, nsv = moe_gated_ffn_workspace_bytes(c, training), moe_gated_ffn_saved_bytes(c)
+    dt, device, c = _TORCH[f.dtype], _device(device), f.struct()
+    nws, nsv = moe_gated_ffn_workspace_bytes(c, training), moe_gated_ffn_saved_bytes(c)
     if nws == 0:
-        _check(-2, "moe_gated_ffn")
+        raise ValueError(f"unsupported problem {f}")
     b = FfnBuffers(out=torch.empty((f.tokens, f.d_model), dtype=dt, device=device),
                    workspace=torch.empty(nws, dtype=torch.uint8, device=device))
     if training:
-        g = dict(dtype=_torch_dtype(f.grad_dtype), device=device)
+        g = dict(dtype=_TORCH[f.grad_dtype], device=device)
         b.saved = torch.empty(nsv, dtype=torch.uint8, device=device)
         b.grad_x = torch.empty((f.tokens, f.d_model), dtype=dt, device=device)
         b.grads = dict(w_gate=torch.empty((f.d_model, f.d_hidden), **g),
@@ -346,41 +368,44 @@ def allocate_ffn(f: GatedFfn, device="cuda", training: bool = False) -> FfnBuffe
 
 
 def _want_ffn(f, x, weights):
-    dt, dev = _torch_dtype(f.dtype), x.device
+    dt, dev = _TORCH[f.dtype], x.device
+    up = (f.d_model, f.d_hidden)
+    wg, wu, wd = weights["w_gate"], weights["w_up"], weights["w_down"]
     _want("x", x, (f.tokens, f.d_model), dt, dev)
-    for name, shape in (("w_gate", (f.d_model, f.d_hidden)), ("w_up", (f.d_model, f.d_hidden)),
-                        ("w_down", (f.d_hidden, f.d_model))):
-        _want(name, weights[name], shape, dt, dev)
-    return dt, dev
+    _want("w_gate", wg, up, dt, dev)
+    _want("w_up", wu, up, dt, dev)
+    _want("w_down", wd, up[::-1], dt, dev)
+    c = _ffn(f.tokens, f.d_model, f.d_hidden, DTYPES[f.dtype], ACTS[f.act], DTYPES[f.grad_dtype])[1]
+    return dt, dev, c, wg.data_ptr(), wu.data_ptr(), wd.data_ptr()
 
 
 def gated_ffn(f: GatedFfn, x, weights: Dict, buf: FfnBuffers, training: bool = False, stream=None):
     """The block's forward pass (weights: w_gate, w_up, w_down); returns buf.out."""
-    dt, dev = _want_ffn(f, x, weights)
+    dt, dev, c, wg, wu, wd = _want_ffn(f, x, weights)
     _want("out", buf.out, (f.tokens, f.d_model), dt, dev)
     if training and buf.saved is None:
         raise ValueError("the buffers were allocated without training=True")
-    with _on(dev):
-        moe_gated_ffn(f.struct(), x, weights["w_gate"], weights["w_up"], weights["w_down"],
-                      buf.saved if training else None, buf.out, buf.workspace, stream=stream)
+    _run("moe_gated_ffn", dev, stream, load().moe_gated_ffn, c, x.data_ptr(), wg, wu, wd,
+         buf.saved.data_ptr() if training else None, buf.out.data_ptr(), buf.workspace.data_ptr(),
+         buf.workspace.numel())
     return buf.out
 
 
 def gated_ffn_backward(f: GatedFfn, x, weights: Dict, grad_out, buf: FfnBuffers, stream=None):
     """Gradients of sum(out * grad_out) after ``gated_ffn(..., training=True)``:
     (grad_x, {w_gate, w_up, w_down})."""
-    dt, dev = _want_ffn(f, x, weights)
+    dt, dev, c, wg, wu, wd = _want_ffn(f, x, weights)
     if buf.saved is None:
         raise ValueError("the buffers were allocated without training=True")
     _want("grad_out", grad_out, (f.tokens, f.d_model), dt, dev)
     _want("grad_x", buf.grad_x, (f.tokens, f.d_model), dt, dev)
-    for name, g in buf.grads.items():
-        _want("gradient of " + name, g, tuple(weights[name].shape), _torch_dtype(f.grad_dtype), dev)
-    with _on(dev):
-        moe_gated_ffn_bwd(f.struct(), x, weights["w_gate"], weights["w_up"], weights["w_down"],
-                          buf.saved, grad_out, buf.grad_x, buf.grads["w_gate"], buf.grads["w_up"],
-                          buf.grads["w_down"], buf.workspace, stream=stream)
-    return buf.grad_x, buf.grads
+    g, gdt = buf.grads, _TORCH[f.grad_dtype]
+    for name in ("w_gate", "w_up", "w_down"):
+        _want("gradient of " + name, g[name], weights[name].shape, gdt, dev)
+    _run("moe_gated_ffn_bwd", dev, stream, load().moe_gated_ffn_bwd, c, x.data_ptr(), wg, wu, wd,
+         buf.saved.data_ptr(), grad_out.data_ptr(), buf.grad_x.data_ptr(), g["w_gate"].data_ptr(),
+         g["w_up"].data_ptr(), g["w_down"].data_ptr(), buf.workspace.data_ptr(), buf.workspace.numel())
+    return buf.grad_x, g
 
 
 # ------------------------------------------------- products in 8-bit integers
@@ -413,9 +438,14 @@ class LinearI8:
         return self.rows if self.sorted_input else self.tokens
 
     def struct(self, x_dtype: int, routed: bool) -> moe_i8_linear:
-        return moe_i8_linear(self.tokens, self.inputs, self.outputs, x_dtype, DTYPES[self.dtype],
-                             self.groups, self.top_k, int(routed and not self.sorted_input),
-                             int(self.gated), self.capacity)
+        return _i8(self, x_dtype, routed)[0]
+
+
+@lru_cache(maxsize=256)
+def _i8(l, x_dtype, routed):
+    c = moe_i8_linear(l.tokens, l.inputs, l.outputs, x_dtype, DTYPES[l.dtype], l.groups, l.top_k,
+                      int(routed and not l.sorted_input), int(l.gated), l.capacity)
+    return c, ctypes.byref(c), moe_i8_pitch(l.inputs)
 
 
 @dataclass
@@ -427,29 +457,26 @@ class I8Buffers:
 
 
 def allocate_linear_i8(l: LinearI8, device="cuda") -> I8Buffers:
-    import torch
     device = _device(device)
-    with _on(device):
-        nws = moe_linear_i8_workspace_bytes(l.struct(MOE_FP32, l.groups > 1))
+    nws = moe_linear_i8_workspace_bytes(l.struct(MOE_FP32, l.groups > 1))
     if nws == 0:
-        _check(-2, "moe_linear_i8")
-    return I8Buffers(y=torch.empty((l.rows, l.columns), dtype=_torch_dtype(l.dtype), device=device),
+        raise ValueError(f"unsupported problem {l}")
+    return I8Buffers(y=torch.empty((l.rows, l.columns), dtype=_TORCH[l.dtype], device=device),
                      workspace=torch.empty(nws, dtype=torch.uint8, device=device))
 
 
 def quantize_rows(x, q=None, scale=None, stream=None):
     """Rows of x [rows, width] as (q int8 [rows, pitch], scale fp32 [rows])."""
-    import torch
     rows, width = x.shape
     dev = x.device
-    _want("x", x, (rows, width), x.dtype, dev, strided=True)
+    ld = _want_rows("x", x, x.shape, x.dtype, dev)
     pitch = moe_i8_pitch(width)
     q = torch.empty((rows, pitch), dtype=torch.int8, device=dev) if q is None else q
     scale = torch.empty(rows, dtype=torch.float32, device=dev) if scale is None else scale
     _want("q", q, (rows, pitch), torch.int8, dev)
     _want("scale", scale, (rows,), torch.float32, dev)
-    with _on(dev):
-        moe_quantize_rows(rows, width, _code(x), x, _ld(x), q, scale, stream)
+    _run("moe_quantize_rows", dev, stream, load().moe_quantize_rows, rows, width, _code(x),
+         x.data_ptr(), ld, q.data_ptr(), scale.data_ptr())
     return q, scale
 
 
@@ -457,7 +484,6 @@ def quantize_weights(*parts, stream=None):
     """Weights [groups, width, outputs] (or one matrix [width, outputs]) as
     (q int8 [groups, rows, pitch], scale fp32 [groups, rows]); several parts of
     one shape (gate and up) follow each other in a group's rows."""
-    import torch
     parts = [w[None] if w.dim() == 2 else w for w in parts]
     groups, width, outputs = parts[0].shape
     dev, rows = parts[0].device, outputs * len(parts)
@@ -466,9 +492,8 @@ def quantize_weights(*parts, stream=None):
     scale = torch.empty((groups, rows), dtype=torch.float32, device=dev)
     for i, w in enumerate(parts):
         _want("weights", w, (groups, width, outputs), parts[0].dtype, dev)
-        with _on(dev):
-            moe_quantize_weight(groups, width, outputs, _code(w), w, rows, q[:, i * outputs:],
-                                scale[:, i * outputs:], stream)
+        _run("moe_quantize_weight", dev, stream, load().moe_quantize_weight, groups, width, outputs,
+             _code(w), w.data_ptr(), rows, q[:, i * outputs:].data_ptr(), scale[:, i * outputs:].data_ptr())
     return q, scale
 
 
@@ -476,31 +501,31 @@ def linear_i8(l: LinearI8, x, wq, w_scale, buf: I8Buffers, bias=None, routing: O
               x_scale=None, stream=None):
     """The product; x is fp32 or bf16 [rows, inputs] (quantised within the
     call) or int8 [rows, pitch] with x_scale. Returns buf.y."""
-    import torch
-    dev = x.device
-    pitch = moe_i8_pitch(l.inputs)
-    if x.dtype == torch.int8:
-        code = MOE_I8
-        _want("x", x, (l.input_rows, pitch), torch.int8, dev)
+    dev, xdt, xs = x.device, x.dtype, None
+    whole = xdt is torch.int8
+    _, c, pitch = _i8(l, MOE_I8 if whole else _code(x), routing is not None)
+    _want("x", x, (l.input_rows, pitch if whole else l.inputs), xdt, dev)
+    if whole:
         if x_scale is None:
             raise ValueError("an int8 input needs x_scale")
         _want("x_scale", x_scale, (l.input_rows,), torch.float32, dev)
-    else:
-        code = _code(x)
-        _want("x", x, (l.input_rows, l.inputs), x.dtype, dev)
+        xs = x_scale.data_ptr()
     _want("weights", wq, (l.groups, l.outputs, pitch), torch.int8, dev)
     _want("weight scales", w_scale, (l.groups, l.outputs), torch.float32, dev)
     if bias is not None:
         _want("bias", bias, (l.outputs,), torch.float32, dev)
+    r = None
     if routing is not None:
         _want("expert_offsets", routing["expert_offsets"], (l.groups + 1,), torch.int32, dev)
         if not l.sorted_input:
             _want("perm", routing["perm"], (l.rows,), torch.int32, dev)
-    _want("y", buf.y, (l.rows, l.columns), _torch_dtype(l.dtype), dev)
-    with _on(dev):
-        moe_linear_i8(l.struct(code, routing is not None), x, x_scale, wq, w_scale, bias, routing,
-                      buf.y, buf.workspace, stream=stream)
-    return buf.y
+        r = ctypes.byref(routing_struct(routing))
+    y = buf.y
+    _want("y", y, (l.rows, l.columns), _TORCH[l.dtype], dev)
+    _run("moe_linear_i8", dev, stream, load().moe_linear_i8, c, x.data_ptr(), xs, wq.data_ptr(),
+         w_scale.data_ptr(), _ptr(bias), r, y.data_ptr(), buf.workspace.data_ptr(),
+         buf.workspace.numel())
+    return y
 
 
 # ------------------------------------------------------- with the layer itself
@@ -511,7 +536,7 @@ def prenorm_forward(p, x, weights: Dict, buf, norm: NormBuffers, eps: float = 1e
     the normalised tokens; weights holds norm_weight and norm_bias (either may
     be missing) beside the layer's own. Returns buf.out."""
     h = layer_norm(x, weights.get("norm_weight"), weights.get("norm_bias"), eps, norm, stream)
-    with _on(x.device):
+    with torch.cuda.device(x.device):
         return binding.forward(p, h, weights, buf, training=training, stream=stream)
 
 
@@ -520,7 +545,7 @@ def prenorm_backward(p, x, weights: Dict, grad_out, buf, norm: NormBuffers, stre
     """Gradients of sum(out * grad_out) after prenorm_forward(..., training=True)
     with the same buffers: (grad_x, the layer's weight gradients with
     norm_weight and norm_bias beside them)."""
-    with _on(x.device):
+    with torch.cuda.device(x.device):
         gh, grads = binding.backward(p, norm.y, weights, grad_out, buf, stream=stream,
                                      side_stream=side_stream)
     gx, gw, gb = layer_norm_backward(x, weights.get("norm_weight"), gh, norm, stream)
@@ -554,7 +579,7 @@ def forward_i8(p, x, w_router, gate_up, down, buf, experts: ExpertsI8Buffers, sh
     (q, scale) pairs of ``quantize_weights(w_gate, w_up)`` and
     ``quantize_weights(w_down)``; buf is ``binding.allocate(p)``, and a shared
     expert's output may be given to be added. Returns buf.out."""
-    with _on(x.device):
+    with torch.cuda.device(x.device):
         binding.moe_route(p, x, w_router, buf.routing, stream)
         binding.moe_permute(p, buf.routing, buf.workspace, stream=stream)
         h = linear_i8(experts.gate_up, x, *gate_up, experts.hidden, routing=buf.routing, stream=stream)

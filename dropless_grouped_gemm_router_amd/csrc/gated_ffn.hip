@@ -19,10 +19,14 @@
 
 #include "gemm_wgrad.h"
 #include "mm.h"
+#include "skinny.h"
 
 namespace moe {
 
 namespace {
+
+// Tokens up to which inference takes the serving form.
+constexpr int64_t kFewRows = 512;
 
 constexpr int64_t pad128(int64_t v) { return (v + 127) / 128 * 128; }
 size_t elem_bytes(const moe_ffn& f) { return f.dtype == MOE_BF16 ? 2 : 4; }
@@ -291,6 +295,72 @@ void ffn_tile_kernel(const MmArgs p, const FfnOut o) {
   else go(std::false_type{});
 }
 
+// ------------------------------------------------------------ few tokens
+
+// Hidden values of the serving form. In bf16 they are kept as the sum of two
+// bf16 numbers (high and low half: 2^-17 instead of 2^-9): the second
+// product is bound by the weights' bytes, so the second MFMA is free.
+__device__ __forceinline__ void put_hidden(bf16_t* high, bf16_t* low, float v) {
+  const bf16_t h = f32_to_bf16(v);
+  *high = h;
+  // an infinite or NaN high half says it all
+  const float rest = v - bf16_to_f32(h);
+  *low = (__float_as_uint(rest) & 0x7f800000u) == 0x7f800000u ? 0 : f32_to_bf16(rest);
+}
+__device__ __forceinline__ void put_hidden(float* high, float*, float v) { *high = v; }
+
+template <typename T, int kR, int kAct>
+__global__ __launch_bounds__(512) void ffn_rows_gate_up_kernel(const SkinnyArgs<T, 2> a, T* high, T* low) {
+  __shared__ float lds[kSkinnyWaves][16 * 64];
+  float sum[kR][2][2];
+  skinny_sums<T, 2, kR, false>(a, lds, sum);
+#pragma unroll
+  for (int i = 0; i < kR; ++i)
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+      int r, c;
+      skinny_place(threadIdx.x + 512 * v, &r, &c);
+      const int64_t row = (static_cast<int64_t>(blockIdx.y) * kR + i) * 16 + r;
+      const int n = blockIdx.x * kSkinnyCols + c;
+      if (row >= a.rows || n >= a.N) continue;
+      float slope;
+      const int64_t at = row * a.N + n;
+      put_hidden(high + at, low + at, act_value<kAct>(sum[i][v][0], &slope) * sum[i][v][1]);
+    }
+}
+
+// part: null (one slice of K): out is written; else the slices' sums
+// [k_parts][rows][N].
+template <typename T, int kR>
+__global__ __launch_bounds__(512) void ffn_rows_down_kernel(const SkinnyArgs<T, 1> a, T* out, float* part) {
+  __shared__ float lds[kSkinnyWaves][16 * 64];
+  float sum[kR][2][1];
+  skinny_sums<T, 1, kR, sizeof(T) == 2>(a, lds, sum);
+#pragma unroll
+  for (int i = 0; i < kR; ++i)
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+      int r, c;
+      skinny_place(threadIdx.x + 512 * v, &r, &c);
+      const int64_t row = (static_cast<int64_t>(blockIdx.y) * kR + i) * 16 + r;
+      const int n = blockIdx.x * kSkinnyCols + c;
+      if (row >= a.rows || n >= a.N) continue;
+      if (part) part[(blockIdx.z * a.rows + row) * a.N + n] = sum[i][v][0];
+      else put(out + row * a.N + n, sum[i][v][0]);
+    }
+}
+
+template <typename T>
+__global__ __launch_bounds__(256) void ffn_rows_join_kernel(const float* __restrict__ part, int parts,
+                                                            int64_t cells, T* __restrict__ out) {
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= cells) return;
+  float v = 0.0f;
+#pragma unroll 8
+  for (int p = 0; p < parts; ++p) v += part[p * cells + i];
+  put(out + i, v);
+}
+
 // Weight gradients from the slices' partial sums [splits][mp][ld], cropped
 // to M x N at column `col` and rounded once: the slices are added in order.
 // Up to three gradients in one launch.
@@ -359,8 +429,10 @@ struct FfnBlockLayout {
   size_t tg, tu, td, xp, h;
   // backward workspace
   size_t dyp, wgp, wup, wdp, dab, part_gu, part_d, zero;
+  // serving form: hidden values (both halves) and the second product's slices
+  size_t rows_h, rows_part;
   size_t total;
-  int splits_gu, splits_d;
+  int splits_gu, splits_d, k_parts;
 };
 
 int slices(int64_t rows, int64_t tiles) {
@@ -369,6 +441,11 @@ int slices(int64_t rows, int64_t tiles) {
   const int64_t most = (rows + 63) / 64;  // a stage of 64 rows each at least
   return static_cast<int>(k > most ? (most < 1 ? 1 : most) : k);
 }
+
+// Row tiles of 16 a workgroup of the serving form takes.
+int rows_tile(const moe_ffn& f) { return f.tokens <= 16 || f.dtype != MOE_BF16 ? 1 : 2; }
+// Whether the serving form is taken (inference only).
+bool few_rows(const moe_ffn& f) { return f.tokens <= kFewRows; }
 
 FfnBlockLayout ffn_block_layout(const moe_ffn& f, bool training) {
   FfnBlockLayout L{};
@@ -380,6 +457,18 @@ FfnBlockLayout ffn_block_layout(const moe_ffn& f, bool training) {
     o = align_up(o + bytes, 256);
     return at;
   };
+  if (!training && few_rows(f)) {
+    L.rows_h = take(T * h * es * (es == 2 ? 2 : 1));
+    // slices of K so that every CU has a workgroup, of two steps a wave at least
+    const int r = 16 * rows_tile(f);
+    const int64_t blocks = f.tokens == 0 ? 1 : (f.d_model + kSkinnyCols - 1) / kSkinnyCols * ((f.tokens + r - 1) / r);
+    const int64_t most = (f.d_hidden + 2 * kSkinnyStep * kSkinnyWaves - 1) / (2 * kSkinnyStep * kSkinnyWaves);
+    const int64_t want = (256 + blocks - 1) / blocks;
+    L.k_parts = static_cast<int>(want < most ? want : most);
+    L.rows_part = take(L.k_parts > 1 ? L.k_parts * T * d * sizeof(float) : 0);
+    L.total = o;
+    return L;
+  }
   L.xp = take(d == dp ? 0 : T * dp * es);
   const size_t start = o;
   L.tg = take(h * dp * es);
@@ -482,9 +571,53 @@ MmArgs rows_of(const void* a, int64_t lda, const void* b, int64_t ldb, int64_t M
   return p;
 }
 
+template <typename T, int kR>
+hipError_t ffn_rows_t(const moe_ffn& f, const void* x, const void* wg, const void* wu,
+                      const void* wd, void* out, void* ws, hipStream_t s) {
+  const FfnBlockLayout L = ffn_block_layout(f, false);
+  char* W = static_cast<char*>(ws);
+  const int d = f.d_model, h = f.d_hidden;
+  T* high = reinterpret_cast<T*>(W + L.rows_h);
+  T* low = sizeof(T) == 2 ? high + f.tokens * h : nullptr;
+  const unsigned tall = static_cast<unsigned>((f.tokens + 16 * kR - 1) / (16 * kR));
+  SkinnyArgs<T, 2> a{static_cast<const T*>(x), nullptr, d,
+                     {static_cast<const T*>(wg), static_cast<const T*>(wu)}, f.tokens, d, h, 1};
+  const dim3 ga((h + kSkinnyCols - 1) / kSkinnyCols, tall);
+  switch (f.act) {
+#define MOE_ROWS(ACT)                                                                              \
+  case ACT:                                                                                        \
+    MOE_LAUNCH("ffn_rows_gate_up", (ffn_rows_gate_up_kernel<T, kR, ACT>), ga, dim3(512), 0, s, a, \
+               high, low);                                                                         \
+    break
+    MOE_ROWS(MOE_ACT_SILU);
+    MOE_ROWS(MOE_ACT_GELU);
+    MOE_ROWS(MOE_ACT_GELU_TANH);
+    MOE_ROWS(MOE_ACT_RELU);
+#undef MOE_ROWS
+  }
+  float* part = L.k_parts > 1 ? reinterpret_cast<float*>(W + L.rows_part) : nullptr;
+  SkinnyArgs<T, 1> b{high, low, h, {static_cast<const T*>(wd)}, f.tokens, h, d, L.k_parts};
+  MOE_LAUNCH("ffn_rows_down", (ffn_rows_down_kernel<T, kR>),
+             dim3((d + kSkinnyCols - 1) / kSkinnyCols, tall, L.k_parts), dim3(512), 0, s, b,
+             static_cast<T*>(out), part);
+  if (part) {
+    const int64_t cells = f.tokens * d;
+    MOE_LAUNCH("ffn_rows_join", ffn_rows_join_kernel<T>, dim3(static_cast<unsigned>((cells + 255) / 256)),
+               dim3(256), 0, s, part, L.k_parts, cells, static_cast<T*>(out));
+  }
+  return hipGetLastError();
+}
+
 template <typename T>
 hipError_t ffn_fwd_t(const moe_ffn& f, const void* x, const void* wg, const void* wu,
                      const void* wd, void* saved, void* out, void* ws, hipStream_t s) {
+  if (!saved && few_rows(f)) {
+    [[maybe_unused]] const int r = rows_tile(f);
+    if constexpr (sizeof(T) == 2) {
+      if (r == 2) return ffn_rows_t<T, 2>(f, x, wg, wu, wd, out, ws, s);
+    }
+    return ffn_rows_t<T, 1>(f, x, wg, wu, wd, out, ws, s);
+  }
   const FfnBlockLayout L = ffn_block_layout(f, saved != nullptr);
   const SavedLayout S = saved_layout(f);
   char *W = static_cast<char*>(ws), *SV = static_cast<char*>(saved);
