@@ -218,11 +218,13 @@ def _run(where, device, stream, fn, *args):
     """fn(*args, stream) on the tensors' device."""
     if device.type != "cuda":
         raise ValueError(f"tensors have to be on a GPU, not on {device}")
+    # the raw handle: a tenth of the time of making a torch.cuda.Stream
+    s = torch._C._cuda_getCurrentRawStream(device.index) if stream is None else _stream(stream)
     if torch.cuda.current_device() != device.index:
         with torch.cuda.device(device):
-            status = fn(*args, _stream(stream))
+            status = fn(*args, s)
     else:
-        status = fn(*args, _stream(stream))
+        status = fn(*args, s)
     if status:
         _check(status, where)
 

@@ -51,10 +51,10 @@ int check_i8(const moe_i8_linear* l) {
   if (l->gated && l->outputs % 2) return MOE_ERR_INVALID;
   if (l->top_k > l->groups) return MOE_ERR_INVALID;
   if (l->groups > 64 || l->inputs > 65536 || l->outputs > 65536) return MOE_ERR_UNSUPPORTED;
-  // token-slots and, in every tiling, the workgroups of a launch
+  // token-slots, and the workgroups of a launch (64 x 64 tiles at least)
   if (l->tokens > (kRowLimit - 1) / l->top_k) return MOE_ERR_UNSUPPORTED;
-  const int64_t tiles = (l->tokens * l->top_k + 15) / 16 + l->groups;
-  if (tiles > (kRowLimit - 1) / ((l->outputs + 15) / 16)) return MOE_ERR_UNSUPPORTED;
+  const int64_t tiles = (l->tokens * l->top_k + 63) / 64 + l->groups;
+  if (tiles > (kRowLimit - 1) / ((l->outputs + 63) / 64)) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 

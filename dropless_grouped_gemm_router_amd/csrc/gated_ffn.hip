@@ -26,7 +26,8 @@ namespace moe {
 namespace {
 
 // Tokens up to which inference takes the serving form.
-constexpr int64_t kFewRows = 512;
+constexpr int64_t kFewRows = 128;
+constexpr int64_t kCUs = 256;
 
 constexpr int64_t pad128(int64_t v) { return (v + 127) / 128 * 128; }
 size_t elem_bytes(const moe_ffn& f) { return f.dtype == MOE_BF16 ? 2 : 4; }
@@ -69,12 +70,15 @@ struct TurnJob {
 };
 struct TurnJobs {
   TurnJob job[3];
+  u32x4* zero;  // kTrZeroBytes to clear, or null
 };
 template <typename T>
 __global__ __launch_bounds__(256) void turn_kernel(const TurnJobs jobs) {
   constexpr int V = Piece<T>::V, P = 64 / V;  // pieces of a block's row
   __shared__ T tile[64][64 + 4 / sizeof(T)];
   const int blk = blockIdx.x;
+  if (blk == 0 && jobs.zero && threadIdx.x < kTrZeroBytes / 16)
+    jobs.zero[threadIdx.x] = (u32x4){0u, 0u, 0u, 0u};
   const int which = blk < jobs.job[0].end ? 0 : (blk < jobs.job[1].end ? 1 : 2);
   const TurnJob& b = jobs.job[which];
   const int local = blk - (which ? jobs.job[which - 1].end : 0);
@@ -102,17 +106,32 @@ __global__ __launch_bounds__(256) void turn_kernel(const TurnJobs jobs) {
   }
 }
 
-// dst[r][wp] = src[r][w], zeros from w on.
+// dst[r][wp] = src[r][w], zeros from w on: up to five matrices in one launch.
+struct PadJob {
+  const void* src;
+  void* dst;
+  int64_t end;  // exclusive end of the job's 16-byte pieces
+  int w, wp;
+};
+struct PadJobs {
+  PadJob job[5];
+  int n;
+};
 template <typename T>
-__global__ __launch_bounds__(256) void pad_rows_kernel(const T* __restrict__ src, T* __restrict__ dst,
-                                                       int64_t rows, int w, int wp) {
+__global__ __launch_bounds__(256) void pad_rows_kernel(const PadJobs jobs) {
   constexpr int V = Piece<T>::V;
-  const int per = wp / V;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < rows * per;
+  const int64_t total = jobs.job[jobs.n - 1].end;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < total;
        i += static_cast<int64_t>(gridDim.x) * 256) {
-    const int64_t r = i / per;
-    const int c = static_cast<int>(i % per) * V;
-    *reinterpret_cast<u32x4*>(dst + r * wp + c) = load_piece(src + r * w, c, w);
+    int j = 0;
+    while (i >= jobs.job[j].end) ++j;
+    const PadJob& b = jobs.job[j];
+    const int64_t local = i - (j ? jobs.job[j - 1].end : 0);
+    const int per = b.wp / V;
+    const int64_t r = local / per;
+    const int c = static_cast<int>(local % per) * V;
+    *reinterpret_cast<u32x4*>(static_cast<T*>(b.dst) + r * b.wp + c) =
+        load_piece(static_cast<const T*>(b.src) + r * b.w, c, b.w);
   }
 }
 
@@ -203,7 +222,7 @@ struct Kept<float> {
   }
 };
 
-enum { kPlain = 0, kGated = 1, kGatedGrad = 2 };
+enum { kPlain = 0, kGated = 1, kGatedGrad = 2, kPart = 3 };  // kPart: a K slice's sums, fp32
 
 template <typename T>
 struct OpOf {
@@ -240,7 +259,10 @@ struct FfnRows {
       float y[8];
 #pragma unroll
       for (int q = 0; q < 8; ++q) y[q] = __uint_as_float(v[q]);
-      store8<T, kFull>(static_cast<T*>(o.c) + row * o.ldc, n[j], p.N, y);
+      if constexpr (kMode == kPart)
+        store8<float, kFull>(static_cast<float*>(o.c) + (t.part * p.M + row) * o.ldc, n[j], p.N, y);
+      else
+        store8<T, kFull>(static_cast<T*>(o.c) + row * o.ldc, n[j], p.N, y);
     } else {
       if (!kFull && n[j] >= o.ld) return;
       float da[8], db[8];
@@ -291,7 +313,7 @@ void ffn_tile_kernel(const MmArgs p, const FfnOut o) {
     mm_drain<Cfg, kPaired>(smem, acc, t.rows, rows);
   };
   mm_tile<typename OpOf<T>::type, Cfg, kPaired>(p, smem, t, acc);
-  if ((t.nt + 1) * kCols <= (kMode == kPlain ? p.N : o.ld)) go(std::true_type{});
+  if ((t.nt + 1) * kCols <= (kMode == kPlain || kMode == kPart ? p.N : o.ld)) go(std::true_type{});
   else go(std::false_type{});
 }
 
@@ -351,7 +373,7 @@ __global__ __launch_bounds__(512) void ffn_rows_down_kernel(const SkinnyArgs<T, 
 }
 
 template <typename T>
-__global__ __launch_bounds__(256) void ffn_rows_join_kernel(const float* __restrict__ part, int parts,
+__global__ __launch_bounds__(256) void join_kernel(const float* __restrict__ part, int parts,
                                                             int64_t cells, T* __restrict__ out) {
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   if (i >= cells) return;
@@ -424,13 +446,16 @@ __global__ __launch_bounds__(256) void zero_kernel(G* __restrict__ p, int64_t n)
 
 // ------------------------------------------------------------------ layouts
 
+int parts_of(size_t elem, int64_t M, int64_t N, int64_t stages);
+
 struct FfnBlockLayout {
   // forward workspace: turned weights, padded x, hidden values (inference)
   size_t tg, tu, td, xp, h;
   // backward workspace
-  size_t dyp, wgp, wup, wdp, dab, part_gu, part_d, zero;
+  size_t dyp, wgp, wup, wdp, dab, part_gu, part_d;
   // serving form: hidden values (both halves) and the second product's slices
   size_t rows_h, rows_part;
+  size_t k_sums;  // sums of the slices of K of a plain product
   size_t total;
   int splits_gu, splits_d, k_parts;
 };
@@ -475,6 +500,11 @@ FfnBlockLayout ffn_block_layout(const moe_ffn& f, bool training) {
   L.tu = take(h * dp * es);
   L.td = take(d * hp * es);
   if (!training) L.h = take(T * hp * es);
+  auto sums = [&](int64_t K) {
+    const int n = parts_of(es, f.tokens, d, K * es / 128);
+    return n > 1 ? n * T * d * sizeof(float) : 0;
+  };
+  L.k_sums = take(sums(hp));
   L.total = o;
   if (training) {
     // the backward reuses the turned weights' place
@@ -489,19 +519,22 @@ FfnBlockLayout ffn_block_layout(const moe_ffn& f, bool training) {
     L.splits_d = slices(f.tokens, tiles);
     L.part_gu = take(static_cast<size_t>(L.splits_gu) * 2 * dp * hp * sizeof(float));
     L.part_d = take(static_cast<size_t>(L.splits_d) * dp * hp * sizeof(float));
-    L.zero = take(kTrZeroBytes);
-    if (o > L.total) L.total = o;
+    // one place for the sums of either pass
+    L.k_sums = std::max(o, L.total);
+    L.total = L.k_sums + std::max(sums(hp), sums(2 * hp));
   }
   return L;
 }
 
+// `zero`: a row of zeros for the weight gradients' loads past the last token.
 struct SavedLayout {
-  size_t h, f, p, low, total;
+  size_t h, f, p, low, zero, total;
 };
 SavedLayout saved_layout(const moe_ffn& f) {
   const size_t cells = static_cast<size_t>(f.tokens) * pad128(f.d_hidden);
   const size_t n = align_up(cells * elem_bytes(f), 256);
-  return SavedLayout{0, n, 2 * n, 3 * n, 3 * n + (f.dtype == MOE_BF16 ? align_up(cells, 256) : 0)};
+  const size_t zero = 3 * n + (f.dtype == MOE_BF16 ? align_up(cells, 256) : 0);
+  return SavedLayout{0, n, 2 * n, 3 * n, zero, zero + kTrZeroBytes};
 }
 
 // ----------------------------------------------------------------- launches
@@ -511,27 +544,65 @@ void tiles_at(const char* name, const MmArgs& a, const FfnOut& o, hipStream_t s)
   MmArgs p = a;
   const int per = kMode == kGated ? Cfg::BN / 2 : Cfg::BN;
   // the hidden matrices are written to their padded width
-  const int64_t n = kMode == kPlain ? p.N : o.ld;
+  const int64_t n = kMode == kPlain || kMode == kPart ? p.N : o.ld;
   p.tiles_n = static_cast<int>((n + per - 1) / per);
   p.nk *= 128 / Cfg::ROW;
   p.k_split *= 128 / Cfg::ROW;
-  const int64_t grid = (p.M + Cfg::BM - 1) / Cfg::BM * p.tiles_n;
+  const int64_t grid = (p.M + Cfg::BM - 1) / Cfg::BM * p.tiles_n * (p.parts > 1 ? p.parts : 1);
   MOE_LAUNCH(name, (ffn_tile_kernel<T, Cfg, kMode, kAct>), dim3(static_cast<unsigned>(grid)),
              dim3(Cfg::NT), 0, s, p, o);
 }
 
+using Big = MmCfg<256, 256, 2, 2, 2, 128>;
+using Mid = MmCfg<128, 128, 2, 2, 3, 64>;
+using Small = MmCfg<64, 64, 2, 2, 2, 128>;
+
+// Tile size by the number of tiles: the largest that still gives every CU
+// one. 256 x 256 needs a long K (stages of 128 bytes) to pay for the epilogue
+// that nothing overlaps; fp32 takes 128 x 128 at most.
+int tile_of(size_t elem, int64_t M, int64_t cols, int64_t stages) {
+  auto count = [&](int t) { return (M + t - 1) / t * ((cols + t - 1) / t); };
+  if (elem == 2 && stages >= 16 && count(256) >= kCUs) return 256;
+  return count(128) >= kCUs ? 128 : 64;
+}
+// Slices of K of a plain product: two workgroups a CU, four stages each at
+// least (777 x 500 with K 2048 in fp32: 104 tiles of 64 x 64).
+int parts_of(size_t elem, int64_t M, int64_t N, int64_t stages) {
+  if (tile_of(elem, M, N, stages) != 64) return 1;
+  const int64_t tiles = (M + 63) / 64 * ((N + 63) / 64);
+  if (tiles == 0) return 1;  // no tokens
+  int64_t k = tiles < kCUs ? 2 * kCUs / tiles : 1;
+  if (k > stages / 4) k = stages / 4;
+  return static_cast<int>(k < 1 ? 1 : (k > 16 ? 16 : k));
+}
+
 template <typename T, int kMode, int kAct>
 void tiles(const char* name, const MmArgs& p, const FfnOut& o, hipStream_t s) {
-  using Big = MmCfg<256, 256, 2, 2, 2, 128>;
-  using Mid = MmCfg<128, 128, 2, 2, 3, 64>;
-  using Small = MmCfg<64, 64, 2, 2, 2, 128>;
-  using Low = MmCfg<32, 64, 1, 2, 2, 128>;
   const int64_t cols = kMode == kGated ? 2 * static_cast<int64_t>(p.N) : p.N;
-  auto count = [&](int t) { return (p.M + t - 1) / t * ((cols + t - 1) / t); };
-  if (sizeof(T) == 2 && p.nk >= 16 && count(256) >= cu_count()) tiles_at<T, Big, kMode, kAct>(name, p, o, s);
-  else if (count(128) >= cu_count()) tiles_at<T, Mid, kMode, kAct>(name, p, o, s);
-  else if (p.M > 32) tiles_at<T, Small, kMode, kAct>(name, p, o, s);
-  else tiles_at<T, Low, kMode, kAct>(name, p, o, s);
+  switch (tile_of(sizeof(T), p.M, cols, p.nk)) {
+    case 256: return tiles_at<T, Big, kMode, kAct>(name, p, o, s);
+    case 128: return tiles_at<T, Mid, kMode, kAct>(name, p, o, s);
+    default: return tiles_at<T, Small, kMode, kAct>(name, p, o, s);
+  }
+}
+
+// A plain product [M][N], over slices of K (sums in `part`) where it has few
+// tiles.
+template <typename T>
+void product(const char* name, const MmArgs& a, void* out, float* part, hipStream_t s) {
+  MmArgs p = a;
+  FfnOut o{};
+  o.ldc = p.N;
+  p.parts = parts_of(sizeof(T), p.M, p.N, p.nk);
+  if (p.parts == 1) {
+    o.c = out;
+    return tiles<T, kPlain, 0>(name, p, o, s);
+  }
+  o.c = part;
+  tiles_at<T, Small, kPart, 0>(name, p, o, s);
+  const int64_t cells = p.M * p.N;
+  MOE_LAUNCH("ffn_join", join_kernel<T>, dim3(static_cast<unsigned>((cells + 255) / 256)), dim3(256), 0, s,
+             part, p.parts, cells, static_cast<T*>(out));
 }
 
 template <typename T, int kMode>
@@ -549,13 +620,21 @@ unsigned blocks_for(int64_t items) {
   return static_cast<unsigned>(b < 1 ? 1 : (b > 8192 ? 8192 : b));
 }
 
+// The matrix itself, or the place of its copy with rows padded to a multiple
+// of 128, which `jobs` then makes.
 template <typename T>
-const void* padded(const void* src, char* dst, int64_t rows, int w, hipStream_t s) {
+const void* padded(PadJobs& jobs, const void* src, char* dst, int64_t rows, int w) {
   const int wp = static_cast<int>(pad128(w));
   if (w == wp) return src;
-  MOE_LAUNCH("ffn_pad_rows", pad_rows_kernel<T>, dim3(blocks_for(rows * (wp / Piece<T>::V))),
-             dim3(256), 0, s, static_cast<const T*>(src), reinterpret_cast<T*>(dst), rows, w, wp);
+  const int64_t start = jobs.n ? jobs.job[jobs.n - 1].end : 0;
+  jobs.job[jobs.n++] = PadJob{src, dst, start + rows * (wp / Piece<T>::V), w, wp};
   return dst;
+}
+template <typename T>
+void pad(const PadJobs& jobs, hipStream_t s) {
+  if (jobs.n)
+    MOE_LAUNCH("ffn_pad_rows", pad_rows_kernel<T>, dim3(blocks_for(jobs.job[jobs.n - 1].end)), dim3(256),
+               0, s, jobs);
 }
 
 template <typename T>
@@ -602,7 +681,7 @@ hipError_t ffn_rows_t(const moe_ffn& f, const void* x, const void* wg, const voi
              static_cast<T*>(out), part);
   if (part) {
     const int64_t cells = f.tokens * d;
-    MOE_LAUNCH("ffn_rows_join", ffn_rows_join_kernel<T>, dim3(static_cast<unsigned>((cells + 255) / 256)),
+    MOE_LAUNCH("ffn_join", join_kernel<T>, dim3(static_cast<unsigned>((cells + 255) / 256)),
                dim3(256), 0, s, part, L.k_parts, cells, static_cast<T*>(out));
   }
   return hipGetLastError();
@@ -624,6 +703,7 @@ hipError_t ffn_fwd_t(const moe_ffn& f, const void* x, const void* wg, const void
   const int d = f.d_model, h = f.d_hidden;
   const int64_t dp = pad128(d), hp = pad128(h);
   TurnJobs jobs{};
+  jobs.zero = SV ? reinterpret_cast<u32x4*>(SV + S.zero) : nullptr;
   int end = 0;
   auto turn = [&](int i, const void* src, char* dst, int K, int N) {
     end += static_cast<int>(pad128(K) / 64 * ((N + 63) / 64));
@@ -633,7 +713,9 @@ hipError_t ffn_fwd_t(const moe_ffn& f, const void* x, const void* wg, const void
   turn(1, wu, W + L.tu, d, h);
   turn(2, wd, W + L.td, h, d);
   MOE_LAUNCH("ffn_turn_weights", turn_kernel<T>, dim3(end), dim3(256), 0, s, jobs);
-  const void* xp = padded<T>(x, W + L.xp, f.tokens, d, s);
+  PadJobs pads{};
+  const void* xp = padded<T>(pads, x, W + L.xp, f.tokens, d);
+  pad<T>(pads, s);
   MmArgs p = rows_of<T>(xp, dp, W + L.tg, dp, f.tokens, h, dp);
   p.half = static_cast<int64_t>(L.tu) - static_cast<int64_t>(L.tg);
   FfnOut o{};
@@ -646,10 +728,7 @@ hipError_t ffn_fwd_t(const moe_ffn& f, const void* x, const void* wg, const void
   o.ld = hp;
   tiles_act<T, kGated>("ffn_gate_up", f.act, p, o, s);
   MmArgs q = rows_of<T>(o.h, hp, W + L.td, hp, f.tokens, d, hp);
-  FfnOut c{};
-  c.c = out;
-  c.ldc = d;
-  tiles<T, kPlain, 0>("ffn_down", q, c, s);
+  product<T>("ffn_down", q, out, reinterpret_cast<float*>(W + L.k_sums), s);
   return hipGetLastError();
 }
 
@@ -690,11 +769,13 @@ hipError_t ffn_bwd_t(const moe_ffn& f, const void* x, const void* wg, const void
   const char* SV = static_cast<const char*>(saved);
   const int d = f.d_model, h = f.d_hidden;
   const int64_t dp = pad128(d), hp = pad128(h), tok = f.tokens;
-  const void* xp = padded<T>(x, W + L.xp, tok, d, s);
-  const void* dyp = padded<T>(dy, W + L.dyp, tok, d, s);
-  const void* wdp = padded<T>(wd, W + L.wdp, h, d, s);
-  const void* wgp = padded<T>(wg, W + L.wgp, d, h, s);
-  const void* wup = padded<T>(wu, W + L.wup, d, h, s);
+  PadJobs pads{};
+  const void* xp = padded<T>(pads, x, W + L.xp, tok, d);
+  const void* dyp = padded<T>(pads, dy, W + L.dyp, tok, d);
+  const void* wdp = padded<T>(pads, wd, W + L.wdp, h, d);
+  const void* wgp = padded<T>(pads, wg, W + L.wgp, d, h);
+  const void* wup = padded<T>(pads, wu, W + L.wup, d, h);
+  pad<T>(pads, s);
 
   MmArgs p = rows_of<T>(dyp, dp, wdp, dp, tok, h, dp);
   FfnOut o{};
@@ -710,19 +791,14 @@ hipError_t ffn_bwd_t(const moe_ffn& f, const void* x, const void* wg, const void
   q.nk *= 2;
   q.a2 = W + L.dab + hp * sizeof(T);
   q.b2 = static_cast<const char*>(wup);
-  FfnOut c{};
-  c.c = dx;
-  c.ldc = d;
-  tiles<T, kPlain, 0>("ffn_bwd_gate_up", q, c, s);
+  product<T>("ffn_bwd_gate_up", q, dx, reinterpret_cast<float*>(W + L.k_sums), s);
 
   float* gu = reinterpret_cast<float*>(W + L.part_gu);
   float* dn = reinterpret_cast<float*>(W + L.part_d);
-  MOE_LAUNCH("ffn_zero", zero_kernel<uint32_t>, dim3(1), dim3(256), 0, s,
-             reinterpret_cast<uint32_t*>(W + L.zero), static_cast<int64_t>(kTrZeroBytes / 4));
   grad_slices<T>("ffn_bwd_wgrad_gate_up", xp, dp, W + L.dab, 2 * hp, dp, 2 * hp, tok, L.splits_gu, gu,
-                 W + L.zero, s);
+                 SV + S.zero, s);
   grad_slices<T>("ffn_bwd_wgrad_down", SV + S.h, hp, dyp, dp, hp, dp, tok, L.splits_d, dn,
-                 W + L.zero, s);
+                 SV + S.zero, s);
   SliceJobs jobs{};
   int64_t end = 0;
   auto job = [&](int i, const float* part, int splits, int64_t mp, int64_t np, int M, int N, void* out) {
@@ -742,7 +818,7 @@ size_t ffn_block_ws_bytes(const moe_ffn& f, bool training) {
   // a training workspace serves inference too
   size_t n = ffn_block_layout(f, false).total;
   if (training) n = std::max(n, ffn_block_layout(f, true).total);
-  return n < 256 ? 256 : n;
+  return align_up(n < 256 ? 256 : n, 256);
 }
 size_t ffn_block_saved_bytes(const moe_ffn& f) { return saved_layout(f).total; }
 

@@ -32,21 +32,33 @@ __device__ __forceinline__ uint32_t wave_umax(uint32_t v) {
 __device__ __forceinline__ float scale_of(uint32_t most) {
   return most >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : __uint_as_float(most) / 127.0f;
 }
-// A row is quantised when its scale is positive; else (zero or NaN) q is 0.
-__device__ __forceinline__ int quantize(float v, float scale) {
-  if (!(scale > 0.0f)) return 0;
-  return static_cast<int>(fminf(fmaxf(rintf(v / scale), -127.0f), 127.0f));
-}
+// rint(v / scale), by the scale's reciprocal where that cannot differ: v inv
+// is within 127 * 2^-23 of the quotient and the rounded quotient within
+// 127 * 2^-24, so unless v inv is that near to a half both round alike (five
+// instructions instead of the dozen of a division; 16384 x 4096 bf16 rows 54
+// -> 41 us, which is the time of their bytes). NaN takes the division too.
+// A row whose scale is not positive (zero or NaN) has q 0.
+struct Quantizer {
+  float scale, inv;
+  __device__ explicit Quantizer(float s) : scale(s), inv(1.0f / s) {}
+  __device__ int operator()(float v) const {
+    const float t = v * inv;
+    float r = rintf(t);
+    if (!(fabsf(t - r) < 0.4999f)) r = rintf(v / scale);
+    r = fminf(fmaxf(r, -127.0f), 127.0f);
+    return scale > 0.0f ? static_cast<int>(r) : 0;
+  }
+};
 
 template <int V>
-__device__ __forceinline__ void store_q(int8_t* p, const float (&f)[V], float scale) {
+__device__ __forceinline__ void store_q(int8_t* p, const float (&f)[V], const Quantizer& quantize) {
   uint32_t w[V / 4];
 #pragma unroll
   for (int i = 0; i < V / 4; ++i) {
     w[i] = 0;
 #pragma unroll
     for (int q = 0; q < 4; ++q)
-      w[i] |= (static_cast<uint32_t>(quantize(f[4 * i + q], scale)) & 0xffu) << (8 * q);
+      w[i] |= (static_cast<uint32_t>(quantize(f[4 * i + q])) & 0xffu) << (8 * q);
   }
   if (V == 8) *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[V / 4 - 1]);
   else *reinterpret_cast<uint32_t*>(p) = w[0];
@@ -91,17 +103,18 @@ __global__ __launch_bounds__(kTPR < 256 ? 256 : kTPR) void quantize_rows_kernel(
   }
   const float s = scale_of(most);
   if (t == 0) scale[row] = s;
+  const Quantizer quantize(s);
   int8_t* qr = q + row * pitch;
   if (kNV) {
 #pragma unroll
     for (int i = 0; i < kNV; ++i) {
       const int c = (i * kTPR + t) * V;
-      if (c < pitch) store_q<V>(qr + c, f[i], s);
+      if (c < pitch) store_q<V>(qr + c, f[i], quantize);
     }
   } else {
     for (int c = t * V; c < pitch; c += kTPR * V) {
       Piece<T>::widen(load_piece(xr, c, width), f[0]);
-      store_q<V>(qr + c, f[0], s);
+      store_q<V>(qr + c, f[0], quantize);
     }
   }
 }
@@ -131,13 +144,13 @@ __global__ __launch_bounds__(256) void quantize_weight_kernel(int width, int out
     if (n < outputs) scale[blockIdx.y * q_rows + n] = sc[c];
   }
   __syncthreads();
-  const float s = sc[c];
+  const Quantizer quantize(sc[c]);
   int8_t* qg = q + blockIdx.y * q_rows * pitch;
   for (int k0 = 0; k0 < pitch; k0 += 64) {
     for (int k = part; k < 64; k += 4) {
       float v = 0.0f;
       if (n < outputs && k0 + k < width) v = elem(wg + static_cast<int64_t>(k0 + k) * outputs + n);
-      turn[c][k] = static_cast<int8_t>(quantize(v, s));
+      turn[c][k] = static_cast<int8_t>(quantize(v));
     }
     __syncthreads();
     // 64 rows of 64 bytes: 16 threads a row, four bytes each
@@ -223,6 +236,153 @@ void i8_tile_kernel(const MmArgs p, const I8Out o) {
   else go(std::false_type{});
 }
 
+// ------------------------------------------------------------------ few rows
+//
+// Serving form, up to 16 rows of a group at a time: the weights' bytes are
+// the cost, so they go from memory straight into the operand of mfma
+// 16x16x64 (a lane's 16 bytes of one weight row) and are read once. A
+// workgroup takes 16 output columns (paired: 16 gate and the 16 up rows) and
+// its eight waves share K. Rows that are not yet integers are quantised into
+// LDS by every workgroup for itself while its first weights are on their way:
+// one launch instead of two, and the rows come from L2.
+constexpr int kRowsWaves = 8, kRowsBatch = 4;
+
+struct I8Few {
+  const void* x;
+  int64_t ldx;            // elements between rows
+  const float* xs;        // int8 input: scales
+  const int8_t* w;
+  int64_t pitch, group;   // bytes between weight rows, groups
+  int width;              // elements of an input row
+  const int32_t* perm;
+  int topk;
+  const int32_t* offsets;
+  int cap;
+  int64_t M;
+  int N;                  // columns of y
+};
+
+template <typename T, typename X, bool kPaired>
+__global__ __launch_bounds__(64 * kRowsWaves) void i8_few_kernel(const I8Few p, const I8Out o) {
+  constexpr int kW = kPaired ? 2 : 1;
+  constexpr bool kInt = sizeof(X) == 1;
+  extern __shared__ __attribute__((aligned(16))) char rows_q[];  // [min(16, M)][pitch + 16], unless kInt
+  __shared__ float scale[16];
+  __shared__ int sums[kRowsWaves][kW][16 * 16];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int g = blockIdx.y;
+  int64_t first = 0, last = p.M;
+  if (p.offsets) {
+    first = p.offsets[g];
+    last = p.offsets[g + 1];
+    if (p.cap > 0 && last - first > p.cap) last = first + p.cap;
+  }
+  const int n0 = blockIdx.x * 16;
+  const int8_t* w[kW];
+#pragma unroll
+  for (int m = 0; m < kW; ++m)
+    w[m] = p.w + g * p.group + (min(n0 + (lane & 15), p.N - 1) + static_cast<int64_t>(m) * p.N) * p.pitch +
+           16 * (lane >> 4);
+  const int steps = static_cast<int>(p.pitch / 64);
+  const int q_pitch = static_cast<int>(p.pitch) + 16;  // rows of 16 banks apart
+
+  for (int64_t r0 = first; r0 < last; r0 += 16) {
+    const int rows = last - r0 < 16 ? static_cast<int>(last - r0) : 16;
+    // the input row behind this lane's token (the last one again past the end)
+    auto input = [&](int t) {
+      const int64_t r = r0 + min(t, rows - 1);
+      return p.perm ? static_cast<int64_t>(p.perm[r] / p.topk) : r;
+    };
+    u32x4 wv[2][kRowsBatch][kW], xv[2][kInt ? kRowsBatch : 1];
+    const int8_t* xi = kInt ? static_cast<const int8_t*>(p.x) + input(lane & 15) * p.ldx + 16 * (lane >> 4) : nullptr;
+    auto load = [&](int set, int s) {
+#pragma unroll
+      for (int u = 0; u < kRowsBatch; ++u) {
+        const int64_t at = static_cast<int64_t>(min(s + u * kRowsWaves, steps - 1)) * 64;
+#pragma unroll
+        for (int m = 0; m < kW; ++m) wv[set][u][m] = *reinterpret_cast<const u32x4*>(w[m] + at);
+        if (kInt) xv[set][u] = *reinterpret_cast<const u32x4*>(xi + at);
+      }
+    };
+    int s = wave;
+    load(0, s);
+    load(1, s + kRowsBatch * kRowsWaves);
+    if constexpr (!kInt) {
+      constexpr int V = Piece<X>::V;
+      for (int t = wave; t < rows; t += kRowsWaves) {
+        const X* row = static_cast<const X*>(p.x) + input(t) * p.ldx;
+        uint32_t most = 0;
+#pragma unroll 4
+        for (int c = lane * V; c < p.width; c += 64 * V) {
+          float f[V];
+          Piece<X>::widen(load_piece(row, c, p.width), f);
+#pragma unroll
+          for (int e = 0; e < V; ++e) most = max(most, __float_as_uint(f[e]) & 0x7fffffffu);
+        }
+        const float sc = scale_of(wave_umax(most));
+        if (lane == 0) scale[t] = sc;
+        const Quantizer quantize(sc);
+#pragma unroll 4
+        for (int c = lane * V; c < p.pitch; c += 64 * V) {
+          float f[V];
+          Piece<X>::widen(load_piece(row, c, p.width), f);
+          store_q<V>(reinterpret_cast<int8_t*>(rows_q) + t * q_pitch + c, f, quantize);
+        }
+      }
+      __syncthreads();
+    }
+    i32x4 acc[kW];
+#pragma unroll
+    for (int m = 0; m < kW; ++m) acc[m] = (i32x4){0, 0, 0, 0};
+    const char* xl = rows_q + min(lane & 15, rows - 1) * q_pitch + 16 * (lane >> 4);
+    auto multiply = [&](int set, int s) {
+#pragma unroll
+      for (int u = 0; u < kRowsBatch; ++u) {
+        const int st = s + u * kRowsWaves;
+        if (st >= steps) break;
+        u32x4 x;
+        if (kInt) x = xv[set][kInt ? u : 0];
+        else x = *reinterpret_cast<const u32x4*>(xl + st * 64);
+#pragma unroll
+        for (int m = 0; m < kW; ++m)
+          acc[m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, wv[set][u][m]),
+                                                         __builtin_bit_cast(i32x4, x), acc[m], 0, 0, 0);
+      }
+    };
+    constexpr int kSpan = kRowsBatch * kRowsWaves;
+    for (; s < steps; s += 2 * kSpan) {
+      multiply(0, s);
+      if (s + 2 * kSpan < steps) load(0, s + 2 * kSpan);
+      multiply(1, s + kSpan);
+      if (s + 3 * kSpan < steps) load(1, s + 3 * kSpan);
+    }
+    // lane L holds token L % 16 and columns 4 (L / 16) .. + 3
+#pragma unroll
+    for (int m = 0; m < kW; ++m)
+      *reinterpret_cast<i32x4*>(&sums[wave][m][(lane & 15) * 16 + 4 * (lane >> 4)]) = acc[m];
+    __syncthreads();
+    if (threadIdx.x < 256) {
+      const int t = threadIdx.x >> 4, n = n0 + (threadIdx.x & 15);
+      int v[kW];
+#pragma unroll
+      for (int m = 0; m < kW; ++m) {
+        v[m] = 0;
+#pragma unroll
+        for (int u = 0; u < kRowsWaves; ++u) v[m] += sums[u][m][threadIdx.x];
+      }
+      if (t < rows && n < p.N) {
+        const float xs = kInt ? o.xs[input(t)] : scale[t];
+        const float* ws = o.ws + static_cast<int64_t>(g) * o.outputs;
+        float y = static_cast<float>(v[0]) * xs * ws[n];
+        if (kPaired) y = silu_f(y) * (static_cast<float>(v[kW - 1]) * xs * ws[p.N + n]);
+        else y += o.bias ? o.bias[n] : 0.0f;
+        put(static_cast<T*>(o.y) + (r0 + t) * o.ld + n, y);
+      }
+    }
+    __syncthreads();
+  }
+}
+
 template <typename T, typename Cfg>
 void i8_tiles(const MmArgs& a, const I8Out& o, bool paired, int64_t row_tiles, hipStream_t s) {
   MmArgs p = a;
@@ -297,29 +457,76 @@ size_t linear_i8_ws_bytes(const moe_i8_linear& l) {
   return n < 256 ? 256 : n;
 }
 
+// Rows a group up to which the serving form is taken, and the largest rows
+// that it quantises for itself (elements; past them, and for several chunks
+// of rows, the quantising launch is cheaper than every workgroup's own).
+constexpr int64_t kFewRows = 16, kOwnElements = 32768, kOwnLds = 120 * 1024;
+
+template <typename T, typename X>
+void i8_few(const I8Few& p, const I8Out& o, int groups, bool paired, hipStream_t s) {
+  const dim3 grid((p.N + 15) / 16, groups);
+  const size_t lds = sizeof(X) == 1 ? 0 : (p.M < 16 ? p.M : 16) * (p.pitch + 16);
+  if (paired)
+    MOE_LAUNCH("linear_i8_few", (i8_few_kernel<T, X, true>), grid, dim3(64 * kRowsWaves), lds, s, p, o);
+  else
+    MOE_LAUNCH("linear_i8_few", (i8_few_kernel<T, X, false>), grid, dim3(64 * kRowsWaves), lds, s, p, o);
+}
+
 hipError_t launch_linear_i8(const moe_i8_linear& l, const void* x, const float* xs,
                             const int8_t* wq, const float* ws, const float* bias,
                             const moe_routing* r, void* y, void* work, hipStream_t s) {
   const I8Layout L = i8_layout(l);
-  const int64_t pitch = i8_pitch(l.inputs);
-  const int8_t* xq = static_cast<const int8_t*>(x);
-  if (l.x_dtype != MOE_I8) {
+  const int64_t pitch = i8_pitch(l.inputs), M = l.tokens * l.top_k;
+  const bool paired = l.gated != 0;
+  const int N = paired ? l.outputs / 2 : l.outputs;
+  const bool few = M <= kFewRows * l.groups;
+  // 16 rows have to fit in LDS beside the sums
+  const bool own = few && l.x_dtype != MOE_I8 && 16 * (pitch + 16) <= kOwnLds &&
+                   M * pitch <= kOwnElements * static_cast<int64_t>(l.groups);
+  if (l.x_dtype != MOE_I8 && !own) {
     int8_t* q = static_cast<int8_t*>(work);
     float* sc = reinterpret_cast<float*>(q + L.scale);
     const hipError_t e = launch_quantize_rows(L.rows, l.inputs, l.x_dtype, x, 0, q, sc, s);
     if (e != hipSuccess) return e;
-    xq = q;
+    x = q;
     xs = sc;
   }
-  const bool paired = l.gated != 0;
+  I8Out o{xs, ws, bias, y, N, l.outputs};
+  if (few) {
+    I8Few p{};
+    p.x = x;
+    p.ldx = own ? l.inputs : pitch;
+    p.xs = xs;
+    p.w = wq;
+    p.pitch = pitch;
+    p.group = static_cast<int64_t>(l.outputs) * pitch;
+    p.width = l.inputs;
+    p.topk = l.top_k;
+    p.cap = l.capacity;
+    p.M = M;
+    p.N = N;
+    if (r) {
+      p.offsets = r->expert_offsets;
+      if (l.gather) p.perm = r->perm;
+    }
+    auto go = [&](auto t) {
+      using T = decltype(t);
+      if (!own) i8_few<T, int8_t>(p, o, l.groups, paired, s);
+      else if (l.x_dtype == MOE_BF16) i8_few<T, bf16_t>(p, o, l.groups, paired, s);
+      else i8_few<T, float>(p, o, l.groups, paired, s);
+    };
+    if (l.dtype == MOE_BF16) go(bf16_t{});
+    else go(float{});
+    return hipGetLastError();
+  }
   MmArgs p{};
-  p.a = reinterpret_cast<const char*>(xq);
+  p.a = static_cast<const char*>(x);
   p.a_pitch = pitch;
   p.b = reinterpret_cast<const char*>(wq);
   p.b_pitch = pitch;
   p.b_group = static_cast<int64_t>(l.outputs) * pitch;
   p.nk = static_cast<int>(pitch / 128);
-  p.N = paired ? l.outputs / 2 : l.outputs;
+  p.N = N;
   p.half = p.N * pitch;
   p.topk = l.top_k;
   p.groups = l.groups;
@@ -328,21 +535,18 @@ hipError_t launch_linear_i8(const moe_i8_linear& l, const void* x, const float* 
     p.offsets = r->expert_offsets;
     if (l.gather) p.perm = r->perm;
   }
-  p.M = r ? l.tokens * l.top_k : l.tokens;
-  I8Out o{xs, ws, bias, y, p.N, l.outputs};
+  p.M = M;
   auto go = [&](auto t) {
     using T = decltype(t);
-    auto tiles = [&](int bm) { return (p.M + bm - 1) / bm + (r ? p.groups : 0); };
     using Big = MmCfg<256, 256, 2, 2, 2, 128>;
     using Mid = MmCfg<128, 128, 2, 2, 3, 64>;
     using Small = MmCfg<64, 64, 2, 2, 2, 128>;
-    using Low = MmCfg<32, 64, 1, 2, 2, 128>;
-    const int64_t per_group = p.M / p.groups;
-    auto count = [&](int t) { return (p.M + t - 1) / t * ((l.outputs + t - 1) / t); };
+    auto tiles = [&](int bm) { return (M + bm - 1) / bm + (r ? p.groups : 0); };
+    const int64_t per_group = M / p.groups;
+    auto count = [&](int t) { return (M + t - 1) / t * ((l.outputs + t - 1) / t); };
     if (p.nk >= 16 && per_group >= 256 && count(256) >= cu_count()) i8_tiles<T, Big>(p, o, paired, tiles(256), s);
     else if (per_group >= 128 && count(128) >= cu_count()) i8_tiles<T, Mid>(p, o, paired, tiles(128), s);
-    else if (per_group > 32) i8_tiles<T, Small>(p, o, paired, tiles(64), s);
-    else i8_tiles<T, Low>(p, o, paired, tiles(32), s);
+    else i8_tiles<T, Small>(p, o, paired, tiles(64), s);
   };
   if (l.dtype == MOE_BF16) go(bf16_t{});
   else go(float{});

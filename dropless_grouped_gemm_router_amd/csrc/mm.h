@@ -62,6 +62,7 @@ struct MmArgs {
   int N;                     // rows of B; paired: of one half
   const int32_t* offsets;    // routed: expert_offsets, else null
   int groups, cap;
+  int parts;                 // dense: slices of K, each a workgroup's own sum
   int tiles_n;
   int64_t half;              // paired: bytes from a gate row of B to its up row
 };
@@ -95,6 +96,7 @@ __device__ __forceinline__ int mm_swizzle(int r) {
 struct MmTile {
   int64_t row0;
   int rows, group, nt;
+  int part, k0, k1;  // slice of K and its stages
 };
 
 // Row tile mt of the routed rows: each lane counts one expert's tiles (at
@@ -115,7 +117,7 @@ __device__ __forceinline__ MmTile mm_routed_tile(const int32_t* offsets, int gro
     if (lane >= o) upto += v;
   }
   const uint64_t past = __ballot(upto > mt);
-  MmTile t{0, 0, 0, 0};
+  MmTile t{};
   if (past == 0) return t;
   const int e = __ffsll(static_cast<unsigned long long>(past)) - 1;
   const int local = mt - (__shfl(upto, e) - __shfl(tiles, e));
@@ -250,8 +252,14 @@ __device__ __forceinline__ void mm_deep(char* smem, int nk, int a_frag, int b_fr
 // One workgroup's tile, from its index. False: no such tile.
 template <typename Cfg>
 __device__ __forceinline__ bool mm_find(const MmArgs& p, MmTile* tile) {
-  const int w = xcd_remap(blockIdx.x, gridDim.x);
-  MmTile t{0, 0, 0, 0};
+  int w = xcd_remap(blockIdx.x, gridDim.x);
+  MmTile t{};
+  int part = 0;
+  if (p.parts > 1) {
+    const int tiles = gridDim.x / p.parts;
+    part = w / tiles;
+    w %= tiles;
+  }
   if (p.offsets) {
     t = mm_routed_tile(p.offsets, p.groups, p.cap, Cfg::BM, w / p.tiles_n, threadIdx.x & 63);
     t.nt = w % p.tiles_n;
@@ -262,6 +270,9 @@ __device__ __forceinline__ bool mm_find(const MmArgs& p, MmTile* tile) {
     const int64_t left = p.M - t.row0;
     t.rows = left < Cfg::BM ? static_cast<int>(left) : Cfg::BM;
   }
+  t.part = part;
+  t.k0 = p.parts > 1 ? static_cast<int>(static_cast<int64_t>(p.nk) * part / p.parts) : 0;
+  t.k1 = p.parts > 1 ? static_cast<int>(static_cast<int64_t>(p.nk) * (part + 1) / p.parts) : p.nk;
   *tile = t;
   return t.rows > 0;
 }
@@ -301,6 +312,7 @@ __device__ __forceinline__ void mm_tile(const MmArgs& p, char* smem, const MmTil
     }
     b[i] = p.b + t.group * p.b_group + off + chunk;
   }
+  const int nk = t.k1 - t.k0;
   const int split = p.b2 ? p.k_split : p.nk;
   const int64_t a2 = p.b2 ? (p.a2 - p.a) - static_cast<int64_t>(split) * Cfg::ROW : 0;
   const int64_t b2 = p.b2 ? (p.b2 - p.b) - static_cast<int64_t>(split) * Cfg::ROW : 0;
@@ -322,15 +334,15 @@ __device__ __forceinline__ void mm_tile(const MmArgs& p, char* smem, const MmTil
   constexpr int kLoads = Cfg::A_LOADS + Cfg::B_LOADS;
   auto issue = [&](int st) {
     char* buf = smem + (st % Cfg::RING) * Cfg::STAGE;
-    const int64_t off = static_cast<int64_t>(st) * Cfg::ROW;
-    const bool first = st < split;
+    const int64_t off = static_cast<int64_t>(st + t.k0) * Cfg::ROW;
+    const bool first = st + t.k0 < split;
     mm_issue<Cfg::A_LOADS>(buf, a, off + (first ? 0 : a2), wave);
     mm_issue<Cfg::B_LOADS>(buf + Cfg::BM * Cfg::ROW, b, off + (first ? 0 : b2), wave);
   };
   if constexpr (Cfg::DEEP) {
-    mm_deep<Op, Cfg>(smem, p.nk, a_frag, b_frag, sw, acc, [&](int st, char* buf, int u) {
-      const int64_t off = static_cast<int64_t>(st) * Cfg::ROW;
-      const bool first = st < split;
+    mm_deep<Op, Cfg>(smem, nk, a_frag, b_frag, sw, acc, [&](int st, char* buf, int u) {
+      const int64_t off = static_cast<int64_t>(st + t.k0) * Cfg::ROW;
+      const bool first = st + t.k0 < split;
       if (u < Cfg::A_LOADS) {
         const char* src = a[u < Cfg::A_LOADS ? u : 0] + off + (first ? 0 : a2);
         char* dst = buf + (wave * Cfg::A_LOADS + u) * 1024;
@@ -345,14 +357,14 @@ __device__ __forceinline__ void mm_tile(const MmArgs& p, char* smem, const MmTil
   }
 #pragma unroll
   for (int st = 0; st < Cfg::RING - 1; ++st)
-    if (st < p.nk) issue(st);
-  for (int s = 0; s < p.nk; ++s) {
+    if (st < nk) issue(st);
+  for (int s = 0; s < nk; ++s) {
     // this wave's loads of stage s have landed, then everyone's have, and
     // the readers of the buffer before it are done
-    if (s + Cfg::RING - 2 < p.nk) mm_wait<kLoads * (Cfg::RING - 2)>();
+    if (s + Cfg::RING - 2 < nk) mm_wait<kLoads * (Cfg::RING - 2)>();
     else mm_wait<0>();
     asm volatile("s_barrier" ::: "memory");
-    if (s + Cfg::RING - 1 < p.nk) issue(s + Cfg::RING - 1);
+    if (s + Cfg::RING - 1 < nk) issue(s + Cfg::RING - 1);
     mm_compute<Op, Cfg>(smem + (s % Cfg::RING) * Cfg::STAGE, a_frag, b_frag, sw, acc);
   }
 }

@@ -52,8 +52,18 @@ __device__ __forceinline__ void row_sums(float (&v)[N], float (*slot)[16]) {
 
 constexpr int block_threads(int tpr) { return tpr < 256 ? 256 : tpr; }
 
-template <int V, int N>
+// V parameters from column c on (`fill` where there is no array).
+template <int V>
 __device__ __forceinline__ void load_param(const float* p, float fill, int c, int n, float (&o)[V]) {
+  if (p && c + V <= n) {
+#pragma unroll
+    for (int h = 0; h < V; h += 4) {
+      const u32x4 v = load_any(p + c + h);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) o[h + q] = __uint_as_float(v[q]);
+    }
+    return;
+  }
 #pragma unroll
   for (int q = 0; q < V; ++q) o[q] = (p && c + q < n) ? p[c + q] : fill;
 }
@@ -75,8 +85,8 @@ __global__ __launch_bounds__(block_threads(kTPR)) void norm_fwd_kernel(
   float wv[NV][V], bv[NV][V];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    load_param<V, NV>(w, 1.0f, (i * kTPR + t) * V, a.width, wv[i]);
-    load_param<V, NV>(b, 0.0f, (i * kTPR + t) * V, a.width, bv[i]);
+    load_param<V>(w, 1.0f, (i * kTPR + t) * V, a.width, wv[i]);
+    load_param<V>(b, 0.0f, (i * kTPR + t) * V, a.width, bv[i]);
   }
   while (true) {
     const int64_t next = row + step;
@@ -137,7 +147,7 @@ __global__ __launch_bounds__(block_threads(kTPR)) void norm_bwd_kernel(
   float wv[NV][V], dw[NV][V], db[NV][V];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    load_param<V, NV>(w, 1.0f, (i * kTPR + t) * V, a.width, wv[i]);
+    load_param<V>(w, 1.0f, (i * kTPR + t) * V, a.width, wv[i]);
 #pragma unroll
     for (int q = 0; q < V; ++q) dw[i][q] = db[i][q] = 0.0f;
   }

@@ -185,8 +185,8 @@ int moe_quantize_weight(int32_t groups, int32_t width, int32_t outputs, int32_t 
  * moe_quantize_rows does, and x_scale is ignored.
  *
  * Supported (else MOE_ERR_UNSUPPORTED): inputs and outputs up to 65536 (any
- * value; outputs even when gated), groups <= 64 (weights of a group and
- * tokens * top_k < 2^31).
+ * value; outputs even when gated), groups <= 64, tokens * top_k < 2^31 and
+ * fewer than 2^31 output tiles of 64 x 64.
  */
 typedef struct {
   int64_t tokens;

@@ -125,6 +125,19 @@ def test_ffn_argument_refusals():
     refused(INV, bwd, ffn(tokens=0), None, None, None, None, None, None, None, None, None, None, None, stream=0)
 
 
+def test_size_queries_over_the_range():
+    """Sizes exist, and grow with training, from no token to the largest."""
+    for t in (0, 1, 16, 17, 128, 129, 5000, (1 << 24) - 1):
+        for d, h in ((1, 1), (128, 256), (500, 1001), (8192, 32768)):
+            for dtype in (0, 1):
+                f = ffn(t, d, h, dtype)
+                few, more = (K.moe_gated_ffn_workspace_bytes(f, training) for training in (False, True))
+                assert 0 < few <= more and few % 256 == 0
+                assert K.moe_gated_ffn_saved_bytes(f) >= 3 * t * h * (4 if dtype == 0 else 2)
+                assert K.moe_layer_norm_workspace_bytes(norm(t, min(d, 16384), dtype)) > 0
+                assert K.moe_linear_i8_workspace_bytes(i8(t, d, h)) >= t * (d + 4)
+
+
 def i8(tokens=10, inputs=512, outputs=256, x=1, y=1, groups=1, top_k=1, gather=0, gated=0, cap=0):
     return K.moe_i8_linear(tokens, inputs, outputs, x, y, groups, top_k, gather, gated, cap)
 
