@@ -114,27 +114,19 @@ __device__ __forceinline__ float lane32(float v, float* other) {
   *other = __uint_as_float(r[1]);
   return __uint_as_float(r[0]);
 }
-__device__ __forceinline__ float wave_sum(float v) {
+__device__ __forceinline__ float row16_sum(float v) {  // over the lane's row of 16
   v += dpp<0xb1>(v);   // lane ^ 1
   v += dpp<0x4e>(v);   // lane ^ 2
   v += dpp<0x141>(v);  // half row mirrored
-  v += dpp<0x140>(v);  // row mirrored
+  return v + dpp<0x140>(v);  // row mirrored
+}
+__device__ __forceinline__ float wave_sum(float v) {
+  v = row16_sum(v);
   float o;
   v = lane16(v, &o);
   v += o;
   v = lane32(v, &o);
   return v + o;
-}
-__device__ __forceinline__ float wave_max(float v) {
-  v = fmaxf(v, dpp<0xb1>(v));
-  v = fmaxf(v, dpp<0x4e>(v));
-  v = fmaxf(v, dpp<0x141>(v));
-  v = fmaxf(v, dpp<0x140>(v));
-  float o;
-  v = lane16(v, &o);
-  v = fmaxf(v, o);
-  v = lane32(v, &o);
-  return fmaxf(v, o);
 }
 
 // ---------------------------------------------------------------- launches

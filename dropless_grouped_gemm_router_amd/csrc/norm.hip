@@ -27,14 +27,14 @@ struct NormArgs {
   int64_t ld_x, ld_y, ld_dy, ld_dx;
 };
 
-// Sums of a row over its threads, kTPR of them: one wave, or a workgroup
+// Sums of a row over its threads, kTPR of them: 16 lanes, one wave, or a workgroup
 // through LDS (slot: this reduction's own array, so that one barrier is
 // enough; the next use of the same slot is a later barrier away).
 template <int kTPR, int N>
 __device__ __forceinline__ void row_sums(float (&v)[N], float (*slot)[16]) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
-  if (kTPR == 64) return;
+  for (int i = 0; i < N; ++i) v[i] = kTPR == 16 ? row16_sum(v[i]) : wave_sum(v[i]);
+  if (kTPR <= 64) return;
   const int wave = threadIdx.x >> 6;
   if ((threadIdx.x & 63) == 0) {
 #pragma unroll
@@ -78,7 +78,7 @@ __global__ __launch_bounds__(block_threads(kTPR)) void norm_fwd_kernel(
   const int t = threadIdx.x % kTPR;
   const int64_t step = static_cast<int64_t>(gridDim.x) * kRows;
   int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / kTPR;
-  if (row >= a.rows) return;  // whole waves, and whole workgroups where they share a row
+  if (row >= a.rows) return;  // all threads of a row together
   u32x4 cur[NV], nxt[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) cur[i] = load_piece(x + row * a.ld_x, (i * kTPR + t) * V, a.width);
@@ -279,13 +279,23 @@ __global__ __launch_bounds__(256) void norm_zero_kernel(float* dw, float* db, in
   if (db) db[c] = 0.0f;
 }
 
-// Threads of a row: the fewest of 64, 256 and 1024 that hold it in at most
-// two pieces each (one wave holds up to 1024 bf16 or 512 fp32 elements);
-// fp32 rows past 8192 take four pieces of 1024 threads.
-int row_threads(int width, int V) { return width <= 128 * V ? 64 : (width <= 512 * V ? 256 : 1024); }
-int row_pieces(int width, int V) {
-  const int t = row_threads(width, V);
-  return width <= t * V ? 1 : (width <= 2 * t * V ? 2 : 4);
+// Threads of a row and pieces a thread. As few threads as its registers allow:
+// the rows of one wave need no barrier and a CU holds more of them (1155 fp32
+// columns, 5001 rows, backward: 64 threads with five pieces 22 us, 256 with
+// two 23 us). Past 16 bytes x 64 x 3 (bf16; fp32: 5) a workgroup shares a
+// row; rows up to 256 bytes (one piece) or 512 take 16 lanes, so that a wave
+// holds four.
+struct RowShape {
+  int threads, pieces;
+};
+RowShape row_shape(int width, int V) {
+  const int n = (width + V - 1) / V;  // pieces of a row
+  if (n <= 32) return {16, n <= 16 ? 1 : 2};
+  const int wave = V == 8 ? 3 : 5;
+  if (n <= 64 * wave) return {64, (n + 63) / 64};
+  if (n <= 512) return {256, n <= 256 ? 1 : 2};
+  if (n <= 2048) return {512, n <= 1024 ? 2 : 4};
+  return {1024, 4};
 }
 
 int per_piece(const moe_norm& n) { return n.dtype == MOE_BF16 ? 8 : 4; }
@@ -293,7 +303,7 @@ int per_piece(const moe_norm& n) { return n.dtype == MOE_BF16 ? 8 : 4; }
 // Workgroups of the backward: enough to fill the chip, at least four row
 // steps each (the partial rows cost 8 bytes a column).
 int bwd_blocks(const moe_norm& n) {
-  const int tpr = row_threads(n.width, per_piece(n));
+  const int tpr = row_shape(n.width, per_piece(n)).threads;
   const int64_t steps = (n.rows * tpr + block_threads(tpr) - 1) / block_threads(tpr);
   const int64_t most = static_cast<int64_t>(256) * 1024 / block_threads(tpr);
   const int64_t b = (steps + 3) / 4;
@@ -302,24 +312,31 @@ int bwd_blocks(const moe_norm& n) {
 
 template <typename F>
 void with_shape(int dtype, int width, F&& f) {
-  const int V = dtype == MOE_BF16 ? 8 : 4;
-  const int t = row_threads(width, V), nv = row_pieces(width, V);
-#define MOE_NORM_CASE(T, TPR, NV) \
-  if (t == TPR && nv == NV) return f(T{}, std::integral_constant<int, TPR>{}, std::integral_constant<int, NV>{})
+  const RowShape r = row_shape(width, dtype == MOE_BF16 ? 8 : 4);
+#define MOE_NORM_CASE(T, TPR, NV)           \
+  if (r.threads == TPR && r.pieces == NV)   \
+  return f(T{}, std::integral_constant<int, TPR>{}, std::integral_constant<int, NV>{})
   if (dtype == MOE_BF16) {
+    MOE_NORM_CASE(bf16_t, 16, 1);
+    MOE_NORM_CASE(bf16_t, 16, 2);
     MOE_NORM_CASE(bf16_t, 64, 1);
     MOE_NORM_CASE(bf16_t, 64, 2);
+    MOE_NORM_CASE(bf16_t, 64, 3);
     MOE_NORM_CASE(bf16_t, 256, 1);
     MOE_NORM_CASE(bf16_t, 256, 2);
-    MOE_NORM_CASE(bf16_t, 1024, 1);
-    MOE_NORM_CASE(bf16_t, 1024, 2);
+    MOE_NORM_CASE(bf16_t, 512, 2);
+    MOE_NORM_CASE(bf16_t, 512, 4);
   } else {
+    MOE_NORM_CASE(float, 16, 1);
+    MOE_NORM_CASE(float, 16, 2);
     MOE_NORM_CASE(float, 64, 1);
     MOE_NORM_CASE(float, 64, 2);
-    MOE_NORM_CASE(float, 256, 1);
+    MOE_NORM_CASE(float, 64, 3);
+    MOE_NORM_CASE(float, 64, 4);
+    MOE_NORM_CASE(float, 64, 5);
     MOE_NORM_CASE(float, 256, 2);
-    MOE_NORM_CASE(float, 1024, 1);
-    MOE_NORM_CASE(float, 1024, 2);
+    MOE_NORM_CASE(float, 512, 2);
+    MOE_NORM_CASE(float, 512, 4);
     MOE_NORM_CASE(float, 1024, 4);
   }
 #undef MOE_NORM_CASE

@@ -85,7 +85,9 @@ def norm64(x, w, b, eps, dy=None):
     (7, 513, "bf16"), (1000, 512, "bf16"), (33, 1024, "bf16"), (33, 1025, "bf16"), (6, 4096, "bf16"),
     (5, 4097, "bf16"), (5, 8192, "bf16"), (3, 8193, "bf16"), (2, 16384, "bf16"), (4, 255, "fp32"),
     (4, 257, "fp32"), (11, 1155, "fp32"), (3, 2049, "fp32"), (2, 4096, "fp32"), (2, 8191, "fp32"),
-    (3, 8193, "fp32"), (2, 16383, "fp32"), (70001, 64, "bf16"), (5001, 130, "fp32")])
+    (3, 8193, "fp32"), (2, 16383, "fp32"), (70001, 64, "bf16"), (5001, 130, "fp32"),
+    (17, 200, "bf16"), (19, 100, "fp32"), (13, 700, "fp32"), (11, 900, "fp32"), (9, 2000, "bf16"), (7, 1500, "fp32"),
+    (5, 5000, "bf16"), (4, 9000, "bf16"), (6, 2300, "fp32"), (3, 5000, "fp32")])
 def test_norm(rows, width, dtype):
     note(f"norm {rows} {width} {dtype}")
     r = gen(rows + width)
