@@ -52,9 +52,9 @@ __device__ __forceinline__ float act_value(float a, float* slope) {
     *slope = s + a * 2.0f * s * (1.0f - s) * k * (1.0f + 3.0f * c * a * a);
     return a * s;
   }
-  const float s = sigmoid_f(a);
-  *slope = s * (1.0f + a * (1.0f - s));
-  return a * s;
+  const float s = sigmoid_f(a), v = a * s;
+  *slope = __builtin_fmaf(v, 1.0f - s, s);
+  return v;
 }
 
 // ---------------------------------------------------------- layout changes
@@ -144,37 +144,33 @@ struct FfnOut {
   // What the backward needs of the pre-activations: f = act(a) and
   // p = b act'(a), so that da = dh p and db = dh f. In bf16 each is kept as
   // its high half (f, p) and the next four mantissa bits, both in one byte of
-  // `low`: 5 bytes a pair instead of 4, and a rounding of 2^-13 instead of
-  // 2^-9, which leaves the roundings of da, db and the result as the only
-  // ones that count in the gradients.
+  // `low`: 5 bytes a pair instead of 4, and 2^-12 lost instead of 2^-9, which
+  // leaves the roundings of da, db and the result as the only ones that count
+  // in the gradients.
   void *f, *p;
   uint8_t* low;
   int64_t ld;    // columns kept of the hidden matrices (a multiple of 128)
   void* dab;     // gradient: da and db, a row of each side by side
 };
 
-// The 20 high bits of a value, rounded: 16 to the result, four to *low.
-// Infinities and NaN stay what they are.
-__device__ __forceinline__ uint32_t split20(float v, uint32_t* low) {
-  uint32_t u = __float_as_uint(v);
-  const uint32_t m = u & 0x7fffffffu;
-  u = m < 0x7f800000u ? u + 0x800u : (m > 0x7f800000u ? u | 0x400000u : u);
-  *low = (u >> 12) & 15u;
-  return u >> 16;
-}
-
-// What is kept of eight values of f and p, and back.
+// What is kept of eight values of f and p. The bits below the 20th are cut
+// off, not rounded: infinities and quiet NaN stay what they are without a test
+// (rounding with its tests took three times the instructions, in an epilogue
+// that is bound by them), and 2^-12 at most is lost.
 __device__ __forceinline__ void keep8(const FfnOut& o, int64_t at, const float (&f)[8],
                                       const float (&p)[8], const bf16_t*) {
   u32x4 fh, ph;
   uint32_t lo[2] = {0, 0};
 #pragma unroll
-  for (int q = 0; q < 8; ++q) {
-    uint32_t fl, pl;
-    const uint32_t a = split20(f[q], &fl), b = split20(p[q], &pl);
-    fh[q / 2] = (q & 1) ? fh[q / 2] | (a << 16) : a;
-    ph[q / 2] = (q & 1) ? ph[q / 2] | (b << 16) : b;
-    lo[q / 4] |= (fl | (pl << 4)) << (8 * (q % 4));
+  for (int q = 0; q < 8; q += 2) {
+    const uint32_t a = __float_as_uint(f[q]), b = __float_as_uint(f[q + 1]);
+    const uint32_t c = __float_as_uint(p[q]), d = __float_as_uint(p[q + 1]);
+    fh[q / 2] = __builtin_amdgcn_perm(b, a, 0x07060302u);
+    ph[q / 2] = __builtin_amdgcn_perm(d, c, 0x07060302u);
+    // byte 1 of each: its high nibble follows the 16 bits that are kept
+    const uint32_t fl = __builtin_amdgcn_perm(b, a, 0x0c0c0501u), pl = __builtin_amdgcn_perm(d, c, 0x0c0c0501u);
+    const uint32_t both = ((fl >> 4) & 0x0f0fu) | (pl & 0xf0f0u);
+    lo[q / 4] |= (q & 2) ? both << 16 : both;
   }
   *reinterpret_cast<u32x4*>(static_cast<bf16_t*>(o.f) + at) = fh;
   *reinterpret_cast<u32x4*>(static_cast<bf16_t*>(o.p) + at) = ph;
@@ -233,9 +229,9 @@ struct OpOf<float> {
   typedef OpF32 type;
 };
 
-// The callbacks of mm_drain; kFull: every column of the tile exists (of a
-// hidden matrix: below its padded width o.ld). Columns past p.N, the hidden
-// matrices' padding, are written as zeros.
+// The callbacks of mm_drain; kFull: every column of the tile is below p.N.
+// Else columns past p.N are left out, or, up to its padded width o.ld, are
+// written as zeros in a hidden matrix.
 template <typename T, typename Cfg, int kMode, int kAct, bool kFull>
 struct FfnRows {
   static constexpr int kJ = Cfg::WN / MmStrip<Cfg>::CB;
@@ -271,7 +267,7 @@ struct FfnRows {
         float fv, pv;
         kept[set][k].get(q, &fv, &pv);
         const float dh = __uint_as_float(v[q]);
-        const bool in = n[j] + q < p.N;
+        const bool in = kFull || n[j] + q < p.N;
         da[q] = in ? dh * pv : 0.0f;
         db[q] = in ? dh * fv : 0.0f;
       }
@@ -285,7 +281,7 @@ struct FfnRows {
     float h[8], f[8], s[8];
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
-      const bool in = n[j] + q < p.N;
+      const bool in = kFull || n[j] + q < p.N;
       const float b = __uint_as_float(u[q]);
       float slope;
       const float fv = act_value<kAct>(__uint_as_float(g[q]), &slope);
@@ -313,7 +309,7 @@ void ffn_tile_kernel(const MmArgs p, const FfnOut o) {
     mm_drain<Cfg, kPaired>(smem, acc, t.rows, rows);
   };
   mm_tile<typename OpOf<T>::type, Cfg, kPaired>(p, smem, t, acc);
-  if ((t.nt + 1) * kCols <= (kMode == kPlain || kMode == kPart ? p.N : o.ld)) go(std::true_type{});
+  if ((t.nt + 1) * kCols <= p.N) go(std::true_type{});
   else go(std::false_type{});
 }
 

@@ -200,7 +200,7 @@ struct I8Rows {
   }
   __device__ void start(int i, int k, int m) {
     const int64_t row = t.row0 + m;
-    xs[i][k] = o.xs[p.perm ? p.perm[row] / p.topk : row];
+    xs[i][k] = o.xs[p.perm ? mm_token(p, p.perm[row]) : row];
   }
   __device__ void pre(int, int, int, int) {}
   __device__ void row(int, int i, int j, int k, int m, const uint32_t (&v)[8]) {
@@ -528,7 +528,7 @@ hipError_t launch_linear_i8(const moe_i8_linear& l, const void* x, const float* 
   p.nk = static_cast<int>(pitch / 128);
   p.N = N;
   p.half = p.N * pitch;
-  p.topk = l.top_k;
+  p.per_token = 1.0 / l.top_k;
   p.groups = l.groups;
   p.cap = l.capacity;
   if (r) {

@@ -50,8 +50,8 @@ struct OpI8 {
 struct MmArgs {
   const char* a;
   int64_t a_pitch;   // bytes between rows
-  const int32_t* perm;  // gather: row r reads input row perm[r] / topk
-  int topk;
+  const int32_t* perm;  // gather: row r reads input row perm[r] / top_k
+  double per_token;     // 1 / topk
   const char* b;
   int64_t b_pitch, b_group;  // bytes between rows, between groups
   const char* a2;            // stages from k_split on come from a2 and b2, each
@@ -84,6 +84,12 @@ struct MmCfg {
   static_assert(BM == WAVES_M * WM * 32 && BN == WAVES_N * WN * 32, "tiles");
   static_assert(BM % (RPL * NW) == 0 && BN % (RPL * NW) == 0, "loads");
 };
+
+// Token of a slot: slot / topk without an integer division (a slot plus a half
+// is at least a half of 1 / topk from a multiple, far more than a rounding).
+__device__ __forceinline__ int mm_token(const MmArgs& p, int32_t slot) {
+  return static_cast<int>(__builtin_fma(static_cast<double>(slot), p.per_token, 0.5 * p.per_token));
+}
 
 // Position of chunk c of LDS row r: c ^ mm_swizzle(r), which spreads the rows
 // that a fragment read touches over all banks.
@@ -296,7 +302,7 @@ __device__ __forceinline__ void mm_tile(const MmArgs& p, char* smem, const MmTil
     const int r = (wave * Cfg::A_LOADS + i) * Cfg::RPL + lane / Cfg::CPR;
     const int chunk = ((lane % Cfg::CPR) ^ mm_swizzle<Cfg>(r)) << 4;
     int64_t src = t.row0 + min(r, t.rows - 1);
-    if (p.perm) src = p.perm[src] / p.topk;
+    if (p.perm) src = mm_token(p, p.perm[src]);
     a[i] = p.a + src * p.a_pitch + chunk;
   }
 #pragma unroll
