@@ -85,6 +85,10 @@ struct MmCfg {
   static_assert(BM % (RPL * NW) == 0 && BN % (RPL * NW) == 0, "loads");
 };
 
+// This wave's number, as a scalar: what is made of it stays off the vector
+// units (the LDS addresses of the loads among it).
+__device__ __forceinline__ int mm_wave() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
+
 // Token of a slot: slot / topk without an integer division (a slot plus a half
 // is at least a half of 1 / topk from a multiple, far more than a rounding).
 __device__ __forceinline__ int mm_token(const MmArgs& p, int32_t slot) {
@@ -290,7 +294,7 @@ __device__ __forceinline__ bool mm_find(const MmArgs& p, MmTile* tile) {
 template <typename Op, typename Cfg, bool kPaired>
 __device__ __forceinline__ void mm_tile(const MmArgs& p, char* smem, const MmTile& t,
                                         typename Op::Acc (&acc)[Cfg::WM][Cfg::WN]) {
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int lane = threadIdx.x & 63, wave = mm_wave();
   // Load i of a wave covers rows (wave LOADS + i) RPL + lane / CPR of an
   // operand's tile, lane l's 16 bytes landing at position l % CPR of the row:
   // the chunk that belongs there is (l % CPR) ^ mm_swizzle(row). Rows past the
@@ -412,7 +416,7 @@ template <typename Cfg, bool kPaired, typename F>
 __device__ __forceinline__ void mm_begin(int rows, F&& f) {
   using S = MmStrip<Cfg>;
   constexpr int COLS = S::CB * (kPaired ? 16 : 32), LPR = COLS / 8, RPP = 64 / LPR, PASSES = 32 / RPP;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = mm_wave();
   const int wm = wave / Cfg::WAVES_N, wn = wave % Cfg::WAVES_N;
 #pragma unroll
   for (int j = 0; j < Cfg::WN / S::CB; ++j)
@@ -430,7 +434,7 @@ __device__ __forceinline__ void mm_drain(char* smem, const Acc (&acc)[Cfg::WM][C
   constexpr int COLS = S::CB * (kPaired ? 16 : 32);  // columns handed out per strip row
   constexpr int LPR = COLS / 8, RPP = 64 / LPR, PASSES = 32 / RPP;
   constexpr int NJ = Cfg::WN / S::CB, STRIPS = NJ * Cfg::WM;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = mm_wave();
   const int g = lane >> 5, r32 = lane & 31;
   const int wm = wave / Cfg::WAVES_N, wn = wave % Cfg::WAVES_N;
   char* strip = smem + wave * S::BYTES;
