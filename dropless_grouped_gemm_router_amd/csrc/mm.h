@@ -24,6 +24,7 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x16 __attribute__((ext_vector_type(16)));
 
 struct OpBf16 {
+  static constexpr int kMfma = 1;  // MFMAs a step
   typedef f32x16_t Acc;
   __device__ static void step(const u32x4& w, const u32x4& x, Acc& acc) {
     acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, w),
@@ -31,6 +32,7 @@ struct OpBf16 {
   }
 };
 struct OpF32 {
+  static constexpr int kMfma = 4;
   typedef f32x16_t Acc;
   // step e takes element e of each lane group's 16 bytes, on both sides
   __device__ static void step(const u32x4& w, const u32x4& x, Acc& acc) {
@@ -40,6 +42,7 @@ struct OpF32 {
   }
 };
 struct OpI8 {
+  static constexpr int kMfma = 1;
   typedef i32x16 Acc;
   __device__ static void step(const u32x4& w, const u32x4& x, Acc& acc) {
     acc = __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(i32x4, w),
@@ -78,8 +81,7 @@ struct MmCfg {
   static constexpr int NW = WAVES_M * WAVES_N, NT = 64 * NW;
   static constexpr int WM = BM / WAVES_M / 32, WN = BN / WAVES_N / 32;  // MFMA tiles per wave
   static constexpr int A_LOADS = BM / RPL / NW, B_LOADS = BN / RPL / NW;     // a wave and stage
-  static constexpr bool DEEP = WM * WN == 16;  // one wave to a SIMD: mm_deep
-  static constexpr int WPE = DEEP ? 1 : 2;       // waves to a SIMD
+  static constexpr int WPE = WM * WN == 16 ? 1 : 2;  // waves to a SIMD: 256 accumulators leave room for one
   static constexpr int STAGE = (BM + BN) * ROW, LDS = RING * STAGE;
   static_assert(BM == WAVES_M * WM * 32 && BN == WAVES_N * WN * 32, "tiles");
   static_assert(BM % (RPL * NW) == 0 && BN % (RPL * NW) == 0, "loads");
@@ -148,17 +150,6 @@ __device__ __forceinline__ void mm_tile_order(int w, int tiles_m, int tiles_n, i
   *nt = in / high;
 }
 
-// One stage's loads of one operand: NL loads a wave, of 1 KiB each.
-template <int NL>
-__device__ __forceinline__ void mm_issue(char* buf, const char* const* rows, int64_t off, int wave) {
-#pragma unroll
-  for (int i = 0; i < NL; ++i) {
-    const char* src = rows[i] + off;
-    char* dst = buf + (wave * NL + i) * 1024;
-    __builtin_amdgcn_global_load_lds(src, dst, 16, 0, 0);
-  }
-}
-
 // At most N of this wave's loads left in flight, its LDS reads done.
 template <int N>
 __device__ __forceinline__ void mm_wait() {
@@ -166,97 +157,78 @@ __device__ __forceinline__ void mm_wait() {
   __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));
 }
 
-template <typename Op, typename Cfg>
-__device__ __forceinline__ void mm_compute(const char* buf, int a_frag, int b_frag, int sw,
-                                           typename Op::Acc (&acc)[Cfg::WM][Cfg::WN]) {
-#pragma unroll
-  for (int q = 0; q < Cfg::STEPS; ++q) {
-    u32x4 xf[Cfg::WM], wf[Cfg::WN];
-    const int at = ((2 * q) ^ sw) << 4;
-#pragma unroll
-    for (int i = 0; i < Cfg::WM; ++i)
-      xf[i] = *reinterpret_cast<const u32x4*>(buf + a_frag + i * 32 * Cfg::ROW + at);
-#pragma unroll
-    for (int j = 0; j < Cfg::WN; ++j)
-      wf[j] = *reinterpret_cast<const u32x4*>(buf + b_frag + j * 32 * Cfg::ROW + at);
-#pragma unroll
-    for (int i = 0; i < Cfg::WM; ++i)
-#pragma unroll
-      for (int j = 0; j < Cfg::WN; ++j) Op::step(wf[j], xf[i], acc[i][j]);
-  }
-}
+constexpr int mm_gcd(int a, int b) { return b ? mm_gcd(b, a % b) : a; }
 
-// The main loop with one wave to a SIMD and 128 x 128 of the tile to a wave:
-// 64 FLOP (bf16) a byte read from LDS against 42.7 for eight waves of
-// 64 x 128, whose reads and the stage writes together would fill the LDS
-// pipe for as long as the MFMAs run. Nothing else hides a latency here, so
-// the fragments of a step (32 bytes of K) are read while the step before is
-// multiplied, two MFMAs to a read. One barrier a stage, before its last step:
-// it says that the next stage is whole and that nobody reads this one any
-// more, whose buffer is then loaded again. At 16384 x 4096 x 4096 int8: 310
-// us against 328 for eight waves; four buffers of 64-byte rows, with twice
-// the requests for the same bytes, take 325, and 335 with the loads spread
-// over all steps.
+// The main loop. The fragments of a step (32 bytes of K) are read while the
+// step before is multiplied, the reads spread between the MFMAs, so that no
+// wave waits for LDS. One barrier a stage, before its last step: it says that
+// the next stage is whole and that nobody reads this one any more, whose
+// buffer is then loaded again, RING stages ahead.
 template <typename Op, typename Cfg, typename Load>
-__device__ __forceinline__ void mm_deep(char* smem, int nk, int a_frag, int b_frag, int sw,
+__device__ __forceinline__ void mm_loop(char* smem, int nk, int a_frag, int b_frag, int sw,
                                         typename Op::Acc (&acc)[Cfg::WM][Cfg::WN], Load&& load) {
-  constexpr int W = 4, kLoads = Cfg::A_LOADS + Cfg::B_LOADS, kSteps = Cfg::STEPS;
-  static_assert(Cfg::WM == W && Cfg::WN == W && kLoads % 8 == 0 && kSteps % 2 == 0, "128 x 128 a wave");
-  u32x4 x[2][W], w[2][W];
-  // fragment f of step q: 0-3 of A, 4-7 of B
+  constexpr int WM = Cfg::WM, WN = Cfg::WN, kFrags = WM + WN, kMfma = WM * WN;
+  constexpr int kLoads = Cfg::A_LOADS + Cfg::B_LOADS, kSteps = Cfg::STEPS;
+  constexpr int G = mm_gcd(mm_gcd(kFrags, kMfma), kLoads);  // groups of a step
+  static_assert(kSteps % 2 == 0, "the last step of a stage uses set 1");
+  u32x4 x[2][WM], w[2][WN];
+  // fragment f of step q: A's, then B's
   auto read = [&](const char* buf, int q, int f, int set) {
     const int at = ((2 * q) ^ sw) << 4;
-    if (f < W) x[set][f & 3] = *reinterpret_cast<const u32x4*>(buf + a_frag + (f & 3) * 32 * Cfg::ROW + at);
-    else w[set][f & 3] = *reinterpret_cast<const u32x4*>(buf + b_frag + (f & 3) * 32 * Cfg::ROW + at);
+    if (f < WM) x[set][f < WM ? f : 0] = *reinterpret_cast<const u32x4*>(buf + a_frag + f * 32 * Cfg::ROW + at);
+    else w[set][f < WM ? 0 : f - WM] = *reinterpret_cast<const u32x4*>(buf + b_frag + (f - WM) * 32 * Cfg::ROW + at);
   };
-  auto multiply = [&](int set, int n) {
-    const int i = n >> 2, j = n & 3;
-    Op::step(w[set][j], x[set][i], acc[i][j]);
+  // The MFMAs of one step on `set`, with the reads of step q of `from` into
+  // the other set and, where kLoad, the loads of stage st into `into`; the
+  // scheduler is given the same order.
+  auto step = [&](auto with_loads, int set, const char* from, int q, int st, char* into) {
+    constexpr bool kLoad = decltype(with_loads)::value;
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      if constexpr (kLoad) {
+#pragma unroll
+        for (int u = 0; u < kLoads / G; ++u) load(st, into, g * (kLoads / G) + u);
+        __builtin_amdgcn_sched_group_barrier(0x010, kLoads / G, 0);
+      }
+#pragma unroll
+      for (int f = 0; f < kFrags / G; ++f) read(from, q, g * (kFrags / G) + f, set ^ 1);
+      __builtin_amdgcn_sched_group_barrier(0x100, kFrags / G, 0);
+#pragma unroll
+      for (int m = 0; m < kMfma / G; ++m) {
+        const int n = g * (kMfma / G) + m;
+        Op::step(w[set][n % WN], x[set][n / WN], acc[n / WN][n % WN]);
+      }
+      __builtin_amdgcn_sched_group_barrier(0x008, kMfma / G * Op::kMfma, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
   };
-#pragma unroll
-  for (int st = 0; st < Cfg::RING; ++st)
-#pragma unroll
-    for (int u = 0; u < kLoads; ++u) load(min(st, nk - 1), smem + st * Cfg::STAGE, u);
-  mm_wait<kLoads * (Cfg::RING - 1)>();
-  asm volatile("s_barrier" ::: "memory");
-#pragma unroll
-  for (int f = 0; f < 2 * W; ++f) read(smem, 0, f, 0);
-  for (int s = 0; s < nk; ++s) {
+  auto stage = [&](auto with_loads, int s) {
+    constexpr bool kLoad = decltype(with_loads)::value;
     char* cur = smem + (s % Cfg::RING) * Cfg::STAGE;
     const char* next = smem + ((s + 1) % Cfg::RING) * Cfg::STAGE;
 #pragma unroll
-    for (int q = 0; q + 1 < kSteps; ++q) {
-#pragma unroll
-      for (int f = 0; f < 8; ++f) {
-        read(cur, q + 1, f, (q + 1) & 1);
-        multiply(q & 1, 2 * f);
-        multiply(q & 1, 2 * f + 1);
-        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // an LDS read
-        __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);  // two MFMAs
-      }
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    // stage s + 1 has landed, the reads of stage s are done
-    mm_wait<kLoads * (Cfg::RING - 2)>();
+    for (int q = 0; q + 1 < kSteps; ++q) step(std::false_type{}, q & 1, cur, q + 1, 0, nullptr);
+    // stage s + 1 has landed (those behind it may be in flight), the reads of
+    // stage s are done
+    mm_wait<kLoad ? kLoads * (Cfg::RING - 2) : 0>();
     asm volatile("s_barrier" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
-    // past the last stage its loads are made again, into a buffer that is
-    // not read, so that the loop has one body and one count
-    const int ahead = min(s + Cfg::RING, nk - 1);
+    step(with_loads, 1, next, 0, s + Cfg::RING, cur);
+  };
 #pragma unroll
-    for (int f = 0; f < 8; ++f) {
+  for (int st = 0; st < Cfg::RING; ++st)
+    if (st < nk) {
 #pragma unroll
-      for (int u = 0; u < kLoads / 8; ++u) load(ahead, cur, f * (kLoads / 8) + u);
-      read(next, 0, f, 0);
-      multiply(1, 2 * f);
-      multiply(1, 2 * f + 1);
-      __builtin_amdgcn_sched_group_barrier(0x010, kLoads / 8, 1);  // loads
-      __builtin_amdgcn_sched_group_barrier(0x100, 1, 1);
-      __builtin_amdgcn_sched_group_barrier(0x008, 2, 1);
+      for (int u = 0; u < kLoads; ++u) load(st, smem + st * Cfg::STAGE, u);
     }
-    __builtin_amdgcn_sched_barrier(0);
-  }
-  mm_wait<0>();
+  if (nk >= Cfg::RING) mm_wait<kLoads * (Cfg::RING - 1)>();
+  else mm_wait<0>();
+  asm volatile("s_barrier" ::: "memory");
+#pragma unroll
+  for (int f = 0; f < kFrags; ++f) read(smem, 0, f, 0);
+  int s = 0;
+  for (; s + Cfg::RING < nk; ++s) stage(std::true_type{}, s);
+  for (; s < nk; ++s) stage(std::false_type{}, s);  // after the last one `next` is read without use
 }
 
 // One workgroup's tile, from its index. False: no such tile.
@@ -339,44 +311,19 @@ __device__ __forceinline__ void mm_tile(const MmArgs& p, char* smem, const MmTil
 #pragma unroll
       for (int q = 0; q < 16; ++q) acc[i][j][q] = 0;
 
-  // A ring of stage buffers: while stage s is multiplied out, the next
-  // Cfg::RING - 2 are in flight and one more is being issued.
-  constexpr int kLoads = Cfg::A_LOADS + Cfg::B_LOADS;
-  auto issue = [&](int st) {
-    char* buf = smem + (st % Cfg::RING) * Cfg::STAGE;
+  mm_loop<Op, Cfg>(smem, nk, a_frag, b_frag, sw, acc, [&](int st, char* buf, int u) {
     const int64_t off = static_cast<int64_t>(st + t.k0) * Cfg::ROW;
     const bool first = st + t.k0 < split;
-    mm_issue<Cfg::A_LOADS>(buf, a, off + (first ? 0 : a2), wave);
-    mm_issue<Cfg::B_LOADS>(buf + Cfg::BM * Cfg::ROW, b, off + (first ? 0 : b2), wave);
-  };
-  if constexpr (Cfg::DEEP) {
-    mm_deep<Op, Cfg>(smem, nk, a_frag, b_frag, sw, acc, [&](int st, char* buf, int u) {
-      const int64_t off = static_cast<int64_t>(st + t.k0) * Cfg::ROW;
-      const bool first = st + t.k0 < split;
-      if (u < Cfg::A_LOADS) {
-        const char* src = a[u < Cfg::A_LOADS ? u : 0] + off + (first ? 0 : a2);
-        char* dst = buf + (wave * Cfg::A_LOADS + u) * 1024;
-        __builtin_amdgcn_global_load_lds(src, dst, 16, 0, 0);
-      } else {
-        const char* src = b[u < Cfg::A_LOADS ? 0 : u - Cfg::A_LOADS] + off + (first ? 0 : b2);
-        char* dst = buf + Cfg::BM * Cfg::ROW + (wave * Cfg::B_LOADS + u - Cfg::A_LOADS) * 1024;
-        __builtin_amdgcn_global_load_lds(src, dst, 16, 0, 0);
-      }
-    });
-    return;
-  }
-#pragma unroll
-  for (int st = 0; st < Cfg::RING - 1; ++st)
-    if (st < nk) issue(st);
-  for (int s = 0; s < nk; ++s) {
-    // this wave's loads of stage s have landed, then everyone's have, and
-    // the readers of the buffer before it are done
-    if (s + Cfg::RING - 2 < nk) mm_wait<kLoads * (Cfg::RING - 2)>();
-    else mm_wait<0>();
-    asm volatile("s_barrier" ::: "memory");
-    if (s + Cfg::RING - 1 < nk) issue(s + Cfg::RING - 1);
-    mm_compute<Op, Cfg>(smem + (s % Cfg::RING) * Cfg::STAGE, a_frag, b_frag, sw, acc);
-  }
+    if (u < Cfg::A_LOADS) {
+      const char* src = a[u < Cfg::A_LOADS ? u : 0] + off + (first ? 0 : a2);
+      char* dst = buf + (wave * Cfg::A_LOADS + u) * 1024;
+      __builtin_amdgcn_global_load_lds(src, dst, 16, 0, 0);
+    } else {
+      const char* src = b[u < Cfg::A_LOADS ? 0 : u - Cfg::A_LOADS] + off + (first ? 0 : b2);
+      char* dst = buf + Cfg::BM * Cfg::ROW + (wave * Cfg::B_LOADS + u - Cfg::A_LOADS) * 1024;
+      __builtin_amdgcn_global_load_lds(src, dst, 16, 0, 0);
+    }
+  });
 }
 
 // Hands a finished tile out by rows. Stored straight from the accumulators,
