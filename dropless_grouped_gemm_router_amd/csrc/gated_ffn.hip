@@ -549,22 +549,25 @@ void tiles_at(const char* name, const MmArgs& a, const FfnOut& o, hipStream_t s)
              dim3(Cfg::NT), 0, s, p, o);
 }
 
-using Big = MmCfg<256, 256, 2, 2, 2, 128>;
-using Mid = MmCfg<128, 128, 2, 2, 3, 64>;
-using Small = MmCfg<64, 64, 2, 2, 2, 128>;
-
 // Tile size by the number of tiles: the largest that still gives every CU
-// one. 256 x 256 needs a long K (stages of 128 bytes) to pay for the epilogue
-// that nothing overlaps; fp32 takes 128 x 128 at most.
-int tile_of(size_t elem, int64_t M, int64_t cols, int64_t stages) {
-  auto count = [&](int t) { return (M + t - 1) / t * ((cols + t - 1) / t); };
-  if (elem == 2 && stages >= 16 && count(256) >= kCUs) return 256;
-  return count(128) >= kCUs ? 128 : 64;
+// one, since a tile's bytes through a CU's 64-byte-a-clock load path are what
+// bounds it (128 x 128: as many clocks as its MFMAs take). 256 x 256 needs a
+// long K (stages of 128 bytes) to pay for an epilogue that nothing overlaps:
+// with K 512 gate and up of 131072 tokens take 460 us against 418 in 256 x
+// 128, with K 2048 to 8192 546 against 630. 16384 tokens, 512 x 1024: gate and
+// up 63 us in 128 x 128, 55 in 256 x 128. fp32 (its MFMAs take 16 times as
+// long for the same bytes) keeps to 128 x 128 at most.
+enum TileSize { kSmall, kMid, kTall, kBig };
+TileSize tile_of(size_t elem, int64_t M, int64_t cols, int64_t stages) {
+  auto count = [&](int m, int n) { return (M + m - 1) / m * ((cols + n - 1) / n); };
+  if (elem == 2 && stages >= 16 && count(256, 256) >= kCUs) return kBig;
+  if (elem == 2 && count(256, 128) >= kCUs) return kTall;
+  return count(128, 128) >= kCUs ? kMid : kSmall;
 }
 // Slices of K of a plain product: two workgroups a CU, four stages each at
 // least (777 x 500 with K 2048 in fp32: 104 tiles of 64 x 64).
 int parts_of(size_t elem, int64_t M, int64_t N, int64_t stages) {
-  if (tile_of(elem, M, N, stages) != 64) return 1;
+  if (tile_of(elem, M, N, stages) != kSmall) return 1;
   const int64_t tiles = (M + 63) / 64 * ((N + 63) / 64);
   if (tiles == 0) return 1;  // no tokens
   int64_t k = tiles < kCUs ? 2 * kCUs / tiles : 1;
@@ -576,9 +579,13 @@ template <typename T, int kMode, int kAct>
 void tiles(const char* name, const MmArgs& p, const FfnOut& o, hipStream_t s) {
   const int64_t cols = kMode == kGated ? 2 * static_cast<int64_t>(p.N) : p.N;
   switch (tile_of(sizeof(T), p.M, cols, p.nk)) {
-    case 256: return tiles_at<T, Big, kMode, kAct>(name, p, o, s);
-    case 128: return tiles_at<T, Mid, kMode, kAct>(name, p, o, s);
-    default: return tiles_at<T, Small, kMode, kAct>(name, p, o, s);
+    case kSmall: return tiles_at<T, MmSmall, kMode, kAct>(name, p, o, s);
+    case kMid: return tiles_at<T, MmMid, kMode, kAct>(name, p, o, s);
+    default: break;
+  }
+  if constexpr (sizeof(T) == 2) {
+    if (tile_of(sizeof(T), p.M, cols, p.nk) == kBig) return tiles_at<T, MmBig, kMode, kAct>(name, p, o, s);
+    tiles_at<T, MmTall, kMode, kAct>(name, p, o, s);
   }
 }
 
@@ -595,7 +602,7 @@ void product(const char* name, const MmArgs& a, void* out, float* part, hipStrea
     return tiles<T, kPlain, 0>(name, p, o, s);
   }
   o.c = part;
-  tiles_at<T, Small, kPart, 0>(name, p, o, s);
+  tiles_at<T, MmSmall, kPart, 0>(name, p, o, s);
   const int64_t cells = p.M * p.N;
   MOE_LAUNCH("ffn_join", join_kernel<T>, dim3(static_cast<unsigned>((cells + 255) / 256)), dim3(256), 0, s,
              part, p.parts, cells, static_cast<T*>(out));

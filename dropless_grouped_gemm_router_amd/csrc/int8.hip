@@ -460,6 +460,7 @@ size_t linear_i8_ws_bytes(const moe_i8_linear& l) {
 // Rows a group up to which the serving form is taken, and the largest rows
 // that it quantises for itself (elements; past them, and for several chunks
 // of rows, the quantising launch is cheaper than every workgroup's own).
+constexpr int64_t kCUs = 256;
 constexpr int64_t kFewRows = 16, kOwnElements = 32768, kOwnLds = 120 * 1024;
 
 template <typename T, typename X>
@@ -538,15 +539,18 @@ hipError_t launch_linear_i8(const moe_i8_linear& l, const void* x, const float* 
   p.M = M;
   auto go = [&](auto t) {
     using T = decltype(t);
-    using Big = MmCfg<256, 256, 2, 2, 2, 128>;
-    using Mid = MmCfg<128, 128, 2, 2, 3, 64>;
-    using Small = MmCfg<64, 64, 2, 2, 2, 128>;
+    // As for the gated block (tile_of): the largest tiles that give every CU
+    // one, 256 x 256 from eight stages on (16384 x 1024 x 2048: 48 us against 51
+    // in 256 x 128 and 54 in 128 x 128; with four stages 66, 62 and 61). Routed
+    // rows lose less of their last tile in 128 rows (64 experts, 131072 slots
+    // of 512: 72 us against 78).
     auto tiles = [&](int bm) { return (M + bm - 1) / bm + (r ? p.groups : 0); };
     const int64_t per_group = M / p.groups;
-    auto count = [&](int t) { return (M + t - 1) / t * ((l.outputs + t - 1) / t); };
-    if (p.nk >= 16 && per_group >= 256 && count(256) >= cu_count()) i8_tiles<T, Big>(p, o, paired, tiles(256), s);
-    else if (per_group >= 128 && count(128) >= cu_count()) i8_tiles<T, Mid>(p, o, paired, tiles(128), s);
-    else i8_tiles<T, Small>(p, o, paired, tiles(64), s);
+    auto count = [&](int m, int n) { return (M + m - 1) / m * ((l.outputs + n - 1) / n); };
+    if (p.nk >= 8 && per_group >= 512 && count(256, 256) >= kCUs) i8_tiles<T, MmBig>(p, o, paired, tiles(256), s);
+    else if (!r && count(256, 128) >= kCUs) i8_tiles<T, MmTall>(p, o, paired, tiles(256), s);
+    else if (per_group >= 128 && count(128, 128) >= kCUs) i8_tiles<T, MmMid>(p, o, paired, tiles(128), s);
+    else i8_tiles<T, MmSmall>(p, o, paired, tiles(64), s);
   };
   if (l.dtype == MOE_BF16) go(bf16_t{});
   else go(float{});

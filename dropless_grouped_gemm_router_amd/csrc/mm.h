@@ -104,6 +104,12 @@ __device__ __forceinline__ int mm_swizzle(int r) {
   return Cfg::ROW == 128 ? (r >> 1) & 7 : (r >> 2) & 3;
 }
 
+// The tile sizes in use.
+using MmBig = MmCfg<256, 256, 2, 2, 2, 128>;   // one wave to a SIMD
+using MmTall = MmCfg<256, 128, 2, 2, 3, 64>;   // two workgroups a CU
+using MmMid = MmCfg<128, 128, 2, 2, 3, 64>;    // three
+using MmSmall = MmCfg<64, 64, 2, 2, 2, 128>;   // five
+
 // A tile's rows: first row, count (0: nothing to do), weight group.
 struct MmTile {
   int64_t row0;

@@ -246,15 +246,21 @@ def test_ffn_activations(t, d, h, dtype, grad, act):
         near(name, buf.grads[name], g, 6 * u)  # one more rounding into grad_dtype
 
 
-def test_ffn_large_and_ragged():
-    """Sizes that take the 256-row tiles, with a ragged last one."""
-    f, x, w, dy, buf = ffn_case(8200, 512, 1024, "bf16", grad="bf16")
+@pytest.mark.parametrize("t,d,h,dtype", [(8200, 512, 1024, "bf16"), (16400, 1024, 1000, "bf16"),
+                                         (8200, 512, 515, "fp32")])
+def test_ffn_large_and_ragged(t, d, h, dtype):
+    """Sizes that take the larger tiles, with ragged last ones."""
+    note(f"ffn large {t} {d} {h} {dtype}")
+    f, x, w, dy, buf = ffn_case(t, d, h, dtype, grad=dtype)
     K.gated_ffn(f, x, w, buf, training=True)
     K.gated_ffn_backward(f, x, w, dy, buf)
     y, grads = ffn64(x, w, dy, "silu")
-    near("out", buf.out, y, 2 * U["bf16"])
+    u = U[dtype] if dtype == "bf16" else 1e-5
+    near("out", buf.out, y, 2 * u)
     for got, want in zip((buf.grad_x, *buf.grads.values()), grads):
-        near("gradient", got, want, 6 * U["bf16"])
+        near("gradient", got, want, 6 * u)
+    K.gated_ffn(f, x, w, buf)
+    near("inference", buf.out, y, 2 * u)
 
 
 def test_ffn_gradient_against_differences():
@@ -382,7 +388,8 @@ def dequantized(x):
 @pytest.mark.parametrize("t,k,n", [(1, 1, 1), (1, 512, 512), (2, 100, 300), (4, 4096, 4096), (7, 130, 33),
                                    (16, 1024, 256), (17, 640, 129), (32, 128, 128), (33, 257, 1001),
                                    (100, 1111, 515), (128, 512, 512), (129, 8200, 64), (400, 333, 2049),
-                                   (700, 65, 7), (2100, 384, 8200)])
+                                   (700, 65, 7), (2100, 384, 8200), (2100, 300, 2100),
+                                   (4200, 1100, 4100)])
 def test_linear_i8(t, k, n, dtype):
     note(f"linear_i8 {t} {k} {n} {dtype}")
     r = gen(t + k + n)
@@ -439,7 +446,8 @@ def routing_of(t, e, top, seed, skew=0.0):
 @pytest.mark.parametrize("t,k,n,e,top,gated,dtype", [
     (1, 128, 256, 8, 2, True, "bf16"), (3, 100, 66, 5, 3, False, "fp32"), (40, 512, 512, 64, 8, True, "bf16"),
     (200, 130, 70, 4, 1, True, "fp32"), (500, 256, 258, 33, 4, False, "bf16"), (2000, 512, 256, 8, 2, True, "bf16"),
-    (2500, 128, 130, 3, 3, False, "bf16"), (3000, 512, 512, 2, 1, True, "bf16")])
+    (2500, 128, 130, 3, 3, False, "bf16"), (3000, 512, 512, 2, 1, True, "bf16"),
+    (9000, 128, 258, 8, 2, True, "bf16"), (4000, 1100, 2100, 2, 2, False, "fp32"), (4000, 1100, 2200, 3, 2, True, "bf16")])
 def test_linear_i8_routed(t, k, n, e, top, gated, dtype):
     import torch
     note(f"linear_i8 routed {t} {k} {n} {e} {top} {gated} {dtype}")
