@@ -41,24 +41,41 @@ __device__ __forceinline__ float scale_of(uint32_t most) {
 struct Quantizer {
   float scale, inv;
   __device__ explicit Quantizer(float s) : scale(s), inv(1.0f / s) {}
-  __device__ int operator()(float v) const {
-    const float t = v * inv;
-    float r = rintf(t);
-    if (!(fabsf(t - r) < 0.4999f)) r = rintf(v / scale);
+  // The integer as a float, by the reciprocal; *near: it may differ.
+  __device__ float fast(float v, bool* near) const {
+    const float t = v * inv, r = rintf(t);
+    *near |= !(fabsf(t - r) < 0.4999f);
+    return r;
+  }
+  __device__ int whole(float r) const {
     r = fminf(fmaxf(r, -127.0f), 127.0f);
     return scale > 0.0f ? static_cast<int>(r) : 0;
+  }
+  __device__ int operator()(float v) const {
+    bool near = false;
+    float r = fast(v, &near);
+    if (near) r = rintf(v / scale);
+    return whole(r);
   }
 };
 
 template <int V>
 __device__ __forceinline__ void store_q(int8_t* p, const float (&f)[V], const Quantizer& quantize) {
+  float r[V];
+  bool near = false;
+#pragma unroll
+  for (int q = 0; q < V; ++q) r[q] = quantize.fast(f[q], &near);
+  if (near) {  // one branch a piece
+#pragma unroll
+    for (int q = 0; q < V; ++q) r[q] = rintf(f[q] / quantize.scale);
+  }
   uint32_t w[V / 4];
 #pragma unroll
   for (int i = 0; i < V / 4; ++i) {
     w[i] = 0;
 #pragma unroll
     for (int q = 0; q < 4; ++q)
-      w[i] |= (static_cast<uint32_t>(quantize(f[4 * i + q])) & 0xffu) << (8 * q);
+      w[i] |= (static_cast<uint32_t>(quantize.whole(r[4 * i + q])) & 0xffu) << (8 * q);
   }
   if (V == 8) *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[V / 4 - 1]);
   else *reinterpret_cast<uint32_t*>(p) = w[0];
