@@ -59,37 +59,47 @@ __device__ __forceinline__ float act_value(float a, float* slope) {
 
 // ---------------------------------------------------------- layout changes
 
-// dst[n][kp] from src[k][n]: 64 x 64 blocks through LDS; zeros for k >= K.
-// Up to three matrices in one launch, the flat block index running over them.
+// dst[n][kp] from src[k][n] (row stride ld): 64 x 64 blocks through LDS; zeros
+// for k >= K (kp: K rounded up to 128). Up to four matrices in one launch, the
+// flat block index running over them.
 struct TurnJob {
   const void* src;
   void* dst;
-  int K, N;
-  int64_t kp;
-  int end;  // exclusive end of the job's blocks
+  int64_t K, ld, kp;
+  int N;
+  int64_t end;  // exclusive end of the job's blocks
 };
 struct TurnJobs {
-  TurnJob job[3];
+  TurnJob job[4];
+  int n;
   u32x4* zero;  // kTrZeroBytes to clear, or null
+
+  void add(const void* src, void* dst, int64_t K, int N, int64_t ld) {
+    const int64_t blocks = pad128(K) / 64 * ((N + 63) / 64);
+    job[n] = TurnJob{src, dst, K, ld, pad128(K), N, (n ? job[n - 1].end : 0) + blocks};
+    ++n;
+  }
 };
 template <typename T>
 __global__ __launch_bounds__(256) void turn_kernel(const TurnJobs jobs) {
   constexpr int V = Piece<T>::V, P = 64 / V;  // pieces of a block's row
   __shared__ T tile[64][64 + 4 / sizeof(T)];
-  const int blk = blockIdx.x;
+  const int64_t blk = blockIdx.x;
   if (blk == 0 && jobs.zero && threadIdx.x < kTrZeroBytes / 16)
     jobs.zero[threadIdx.x] = (u32x4){0u, 0u, 0u, 0u};
-  const int which = blk < jobs.job[0].end ? 0 : (blk < jobs.job[1].end ? 1 : 2);
+  int which = 0;
+  while (blk >= jobs.job[which].end) ++which;
   const TurnJob& b = jobs.job[which];
-  const int local = blk - (which ? jobs.job[which - 1].end : 0);
+  const int64_t local = blk - (which ? jobs.job[which - 1].end : 0);
   const int across = (b.N + 63) / 64;
-  const int n0 = local % across * 64, k0 = local / across * 64;
+  const int n0 = static_cast<int>(local % across) * 64;
+  const int64_t k0 = local / across * 64;
   const T* src = static_cast<const T*>(b.src);
   T* dst = static_cast<T*>(b.dst);
   for (int i = threadIdx.x; i < 64 * P; i += 256) {
     const int k = i / P, c = i % P * V;
     u32x4 v = (u32x4){0u, 0u, 0u, 0u};
-    if (k0 + k < b.K && n0 + c < b.N) v = load_piece(src + static_cast<int64_t>(k0 + k) * b.N, n0 + c, b.N);
+    if (k0 + k < b.K && n0 + c < b.N) v = load_piece(src + (k0 + k) * b.ld, n0 + c, b.N);
     const T* e = reinterpret_cast<const T*>(&v);
 #pragma unroll
     for (int q = 0; q < V; ++q) tile[k][c + q] = e[q];
@@ -379,6 +389,36 @@ __global__ __launch_bounds__(256) void join_kernel(const float* __restrict__ par
   put(out + i, v);
 }
 
+// The three weight gradients in fp32, in one launch: products over the
+// tokens of turned operands, [rows of the gradient][tokens] each.
+struct GradArgs {
+  MmArgs p[3];
+  FfnOut o[3];
+  int end[3];  // exclusive end of each product's tiles
+};
+template <typename Cfg, int kMode>
+__global__ __launch_bounds__(Cfg::NT) __attribute__((amdgpu_waves_per_eu(Cfg::WPE)))
+void ffn_grad_kernel(const GradArgs a) {
+  __shared__ __attribute__((aligned(1024))) char smem[MmStrip<Cfg>::LDS];
+  int w = xcd_remap(blockIdx.x, gridDim.x);
+  const int part = w / a.end[2];
+  w %= a.end[2];
+  const int which = w < a.end[0] ? 0 : (w < a.end[1] ? 1 : 2);
+  const MmArgs& p = a.p[which];
+  const FfnOut& o = a.o[which];
+  f32x16_t acc[Cfg::WM][Cfg::WN];
+  MmTile t;
+  if (!mm_place<Cfg>(p, w - (which ? a.end[which - 1] : 0), part, &t)) return;
+  mm_tile<OpF32, Cfg, false>(p, smem, t, acc);
+  auto go = [&](auto full) {
+    FfnRows<float, Cfg, kMode, 0, decltype(full)::value> rows{p, o, t, t.nt * Cfg::BN};
+    mm_begin<Cfg, false>(t.rows, rows);
+    mm_drain<Cfg, false>(smem, acc, t.rows, rows);
+  };
+  if ((t.nt + 1) * Cfg::BN <= p.N) go(std::true_type{});
+  else go(std::false_type{});
+}
+
 // Weight gradients from the slices' partial sums [splits][mp][ld], cropped
 // to M x N at column `col` and rounded once: the slices are added in order.
 // Up to three gradients in one launch.
@@ -443,17 +483,19 @@ __global__ __launch_bounds__(256) void zero_kernel(G* __restrict__ p, int64_t n)
 // ------------------------------------------------------------------ layouts
 
 int parts_of(size_t elem, int64_t M, int64_t N, int64_t stages);
+int grad_parts(const moe_ffn& f);
 
 struct FfnBlockLayout {
   // forward workspace: turned weights, padded x, hidden values (inference)
   size_t tg, tu, td, xp, h;
   // backward workspace
   size_t dyp, wgp, wup, wdp, dab, part_gu, part_d;
+  size_t xt, dabt, ht, dyt;  // fp32: operands of the weight gradients, turned
   // serving form: hidden values (both halves) and the second product's slices
   size_t rows_h, rows_part;
   size_t k_sums;  // sums of the slices of K of a plain product
   size_t total;
-  int splits_gu, splits_d, k_parts;
+  int splits_gu, splits_d, k_parts, grad_parts;
 };
 
 int slices(int64_t rows, int64_t tiles) {
@@ -510,11 +552,23 @@ FfnBlockLayout ffn_block_layout(const moe_ffn& f, bool training) {
     L.wup = take(h == hp ? 0 : d * hp * es);
     L.wdp = take(d == dp ? 0 : h * dp * es);
     L.dab = take(T * 2 * hp * es);
-    const int64_t tiles = static_cast<int64_t>(dp / 128) * (hp / 128);
-    L.splits_gu = slices(f.tokens, 2 * tiles);
-    L.splits_d = slices(f.tokens, tiles);
-    L.part_gu = take(static_cast<size_t>(L.splits_gu) * 2 * dp * hp * sizeof(float));
-    L.part_d = take(static_cast<size_t>(L.splits_d) * dp * hp * sizeof(float));
+    if (f.dtype == MOE_BF16) {
+      const int64_t tiles = static_cast<int64_t>(dp / 128) * (hp / 128);
+      L.splits_gu = slices(f.tokens, 2 * tiles);
+      L.splits_d = slices(f.tokens, tiles);
+      L.part_gu = take(static_cast<size_t>(L.splits_gu) * 2 * dp * hp * sizeof(float));
+      L.part_d = take(static_cast<size_t>(L.splits_d) * dp * hp * sizeof(float));
+    } else {
+      const size_t tp = pad128(f.tokens);
+      L.xt = take(d * tp * es);
+      L.dabt = take(2 * hp * tp * es);
+      L.ht = take(h * tp * es);
+      L.dyt = take(d * tp * es);
+      L.grad_parts = grad_parts(f);
+      const size_t n = L.grad_parts > 1 ? L.grad_parts : 0;
+      L.part_gu = take(n * 2 * d * ((h + 3) / 4 * 4) * sizeof(float));
+      L.part_d = take(n * h * ((d + 3) / 4 * 4) * sizeof(float));
+    }
     // one place for the sums of either pass
     L.k_sums = std::max(o, L.total);
     L.total = L.k_sums + std::max(sums(hp), sums(2 * hp));
@@ -589,6 +643,18 @@ void tiles(const char* name, const MmArgs& p, const FfnOut& o, hipStream_t s) {
   }
 }
 
+// Tiles of the fp32 weight gradients in tiles of t, and the slices of the
+// tokens: one and a half workgroups a CU, four stages each at least.
+int64_t grad_tiles(const moe_ffn& f, int t) {
+  return 3 * ((f.d_model + t - 1) / t) * static_cast<int64_t>((f.d_hidden + t - 1) / t);
+}
+int grad_parts(const moe_ffn& f) {
+  const int64_t tiles = grad_tiles(f, 64), stages = pad128(f.tokens) / 32;
+  int64_t k = (kCUs * 3 / 2 + tiles - 1) / tiles;
+  if (k > stages / 4) k = stages / 4;
+  return static_cast<int>(k < 1 ? 1 : (k > 64 ? 64 : k));
+}
+
 // A plain product [M][N], over slices of K (sums in `part`) where it has few
 // tiles.
 template <typename T>
@@ -621,6 +687,11 @@ void tiles_act(const char* name, int act, const MmArgs& p, const FfnOut& o, hipS
 unsigned blocks_for(int64_t items) {
   const int64_t b = (items + 255) / 256;
   return static_cast<unsigned>(b < 1 ? 1 : (b > 8192 ? 8192 : b));
+}
+
+template <typename T>
+void turn(const char* name, const TurnJobs& jobs, hipStream_t s) {
+  MOE_LAUNCH(name, turn_kernel<T>, dim3(static_cast<unsigned>(jobs.job[jobs.n - 1].end)), dim3(256), 0, s, jobs);
 }
 
 // The matrix itself, or the place of its copy with rows padded to a multiple
@@ -707,15 +778,10 @@ hipError_t ffn_fwd_t(const moe_ffn& f, const void* x, const void* wg, const void
   const int64_t dp = pad128(d), hp = pad128(h);
   TurnJobs jobs{};
   jobs.zero = SV ? reinterpret_cast<u32x4*>(SV + S.zero) : nullptr;
-  int end = 0;
-  auto turn = [&](int i, const void* src, char* dst, int K, int N) {
-    end += static_cast<int>(pad128(K) / 64 * ((N + 63) / 64));
-    jobs.job[i] = TurnJob{src, dst, K, N, pad128(K), end};
-  };
-  turn(0, wg, W + L.tg, d, h);
-  turn(1, wu, W + L.tu, d, h);
-  turn(2, wd, W + L.td, h, d);
-  MOE_LAUNCH("ffn_turn_weights", turn_kernel<T>, dim3(end), dim3(256), 0, s, jobs);
+  jobs.add(wg, W + L.tg, d, h, h);
+  jobs.add(wu, W + L.tu, d, h, h);
+  jobs.add(wd, W + L.td, h, d, d);
+  turn<T>("ffn_turn_weights", jobs, s);
   PadJobs pads{};
   const void* xp = padded<T>(pads, x, W + L.xp, f.tokens, d);
   pad<T>(pads, s);
@@ -735,7 +801,21 @@ hipError_t ffn_fwd_t(const moe_ffn& f, const void* x, const void* wg, const void
   return hipGetLastError();
 }
 
-// Partial sums of a^T b over the slices of the rows, [splits][mp][np].
+template <typename Cfg, int kMode>
+void launch_grad(GradArgs& a, int parts, hipStream_t s) {
+  int64_t tiles = 0;
+  for (int i = 0; i < 3; ++i) {
+    MmArgs& p = a.p[i];
+    p.tiles_n = (p.N + Cfg::BN - 1) / Cfg::BN;
+    p.nk *= 128 / Cfg::ROW;
+    tiles += (p.M + Cfg::BM - 1) / Cfg::BM * p.tiles_n;
+    a.end[i] = static_cast<int>(tiles);
+  }
+  MOE_LAUNCH("ffn_bwd_wgrad", (ffn_grad_kernel<Cfg, kMode>), dim3(static_cast<unsigned>(tiles * parts)),
+             dim3(Cfg::NT), 0, s, a);
+}
+
+// Partial sums of a^T b over the slices of the rows, [splits][mp][np] (bf16).
 template <typename T>
 void grad_slices(const char* name, const void* a, int64_t lda, const void* b, int64_t ldb,
                  int64_t mp, int64_t np, int64_t rows, int splits, float* part, const void* zero,
@@ -753,13 +833,7 @@ void grad_slices(const char* name, const void* a, int64_t lda, const void* b, in
   w.nsplit = w.N;
   w.ldc = np;
   w.c_group_stride = mp * np;
-  if (std::is_same<T, bf16_t>::value) {
-    wgrad_tr<true>(name, w, splits, static_cast<const bf16_t*>(zero), s);
-  } else {
-    const int64_t blocks = splits * (mp / 128) * (np / 128);
-    MOE_LAUNCH(name, (wgrad_kernel<float, false, true>), dim3(static_cast<unsigned>(blocks)),
-               dim3(256), 0, s, w);
-  }
+  wgrad_tr<true>(name, w, splits, static_cast<const bf16_t*>(zero), s);
 }
 
 template <typename T, typename G>
@@ -773,7 +847,8 @@ hipError_t ffn_bwd_t(const moe_ffn& f, const void* x, const void* wg, const void
   const int d = f.d_model, h = f.d_hidden;
   const int64_t dp = pad128(d), hp = pad128(h), tok = f.tokens;
   PadJobs pads{};
-  const void* xp = padded<T>(pads, x, W + L.xp, tok, d);
+  [[maybe_unused]] const void* xp = x;
+  if constexpr (std::is_same<T, bf16_t>::value) xp = padded<T>(pads, x, W + L.xp, tok, d);
   const void* dyp = padded<T>(pads, dy, W + L.dyp, tok, d);
   const void* wdp = padded<T>(pads, wd, W + L.wdp, h, d);
   const void* wgp = padded<T>(pads, wg, W + L.wgp, d, h);
@@ -798,19 +873,52 @@ hipError_t ffn_bwd_t(const moe_ffn& f, const void* x, const void* wg, const void
 
   float* gu = reinterpret_cast<float*>(W + L.part_gu);
   float* dn = reinterpret_cast<float*>(W + L.part_d);
-  grad_slices<T>("ffn_bwd_wgrad_gate_up", xp, dp, W + L.dab, 2 * hp, dp, 2 * hp, tok, L.splits_gu, gu,
-                 SV + S.zero, s);
-  grad_slices<T>("ffn_bwd_wgrad_down", SV + S.h, hp, dyp, dp, hp, dp, tok, L.splits_d, dn,
-                 SV + S.zero, s);
   SliceJobs jobs{};
   int64_t end = 0;
-  auto job = [&](int i, const float* part, int splits, int64_t mp, int64_t np, int M, int N, void* out) {
+  auto job = [&](int i, const float* part, int splits, int64_t stride, int64_t ld, int M, int N, void* out) {
     end += static_cast<int64_t>(M) * ((N + 3) / 4);
-    jobs.job[i] = SliceJob{part, splits, mp * np, np, M, N, out, end};
+    jobs.job[i] = SliceJob{part, splits, stride, ld, M, N, out, end};
   };
-  job(0, gu, L.splits_gu, dp, 2 * hp, d, h, dwg);
-  job(1, gu + hp, L.splits_gu, dp, 2 * hp, d, h, dwu);
-  job(2, dn, L.splits_d, hp, dp, h, d, dwd);
+  if constexpr (std::is_same<T, bf16_t>::value) {
+    grad_slices<T>("ffn_bwd_wgrad_gate_up", xp, dp, W + L.dab, 2 * hp, dp, 2 * hp, tok, L.splits_gu, gu,
+                   SV + S.zero, s);
+    grad_slices<T>("ffn_bwd_wgrad_down", SV + S.h, hp, dyp, dp, hp, dp, tok, L.splits_d, dn,
+                   SV + S.zero, s);
+    job(0, gu, L.splits_gu, 2 * dp * hp, 2 * hp, d, h, dwg);
+    job(1, gu + hp, L.splits_gu, 2 * dp * hp, 2 * hp, d, h, dwu);
+    job(2, dn, L.splits_d, dp * hp, dp, h, d, dwd);
+  } else {
+    // fp32 has no transposing LDS read: the operands are turned (their bytes
+    // are little beside fp32 MFMAs) and the gradients are plain products,
+    // written in place where the tokens are not cut into slices. 777 tokens,
+    // 500 x 1001: 42 us, against 64 with row slices turned in registers and
+    // their partial sums.
+    TurnJobs turns{};
+    turns.add(x, W + L.xt, tok, d, d);
+    turns.add(W + L.dab, W + L.dabt, tok, static_cast<int>(2 * hp), 2 * hp);
+    turns.add(SV + S.h, W + L.ht, tok, h, hp);
+    turns.add(dy, W + L.dyt, tok, d, d);
+    turn<T>("ffn_bwd_turn", turns, s);
+    const int64_t tp = pad128(tok);
+    GradArgs a{};
+    const int parts = L.grad_parts;
+    const int64_t h4 = (h + 3) / 4 * 4, d4 = (d + 3) / 4 * 4;  // rows of the slices' sums
+    auto grad = [&](int i, const char* A, const char* B, int M, int N, void* out, float* sums, int64_t ld) {
+      a.p[i] = rows_of<T>(A, tp, B, tp, M, N, tp);
+      a.p[i].parts = parts;
+      a.o[i].c = parts > 1 ? sums : out;
+      a.o[i].ldc = parts > 1 ? ld : N;
+      if (parts > 1) job(i, sums, parts, M * ld, ld, M, N, out);
+    };
+    const char* dabt = W + L.dabt;
+    grad(0, W + L.xt, dabt, d, h, dwg, gu, h4);
+    grad(1, W + L.xt, dabt + hp * tp * sizeof(T), d, h, dwu, gu + parts * d * h4, h4);
+    grad(2, W + L.ht, W + L.dyt, h, d, dwd, dn, d4);
+    if (parts > 1) launch_grad<MmSmall, kPart>(a, parts, s);
+    else if (grad_tiles(f, 128) >= kCUs) launch_grad<MmMid, kPlain>(a, 1, s);
+    else launch_grad<MmSmall, kPlain>(a, 1, s);
+    if (parts == 1) return hipGetLastError();
+  }
   MOE_LAUNCH("ffn_slice_sum", slice_sum_kernel<G>, dim3(blocks_for(end)), dim3(256), 0, s, jobs);
   return hipGetLastError();
 }

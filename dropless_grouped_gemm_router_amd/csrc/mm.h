@@ -237,17 +237,10 @@ __device__ __forceinline__ void mm_loop(char* smem, int nk, int a_frag, int b_fr
   for (; s < nk; ++s) stage(std::false_type{}, s);  // after the last one `next` is read without use
 }
 
-// One workgroup's tile, from its index. False: no such tile.
+// Tile w (of part `part`) of a product. False: no such tile.
 template <typename Cfg>
-__device__ __forceinline__ bool mm_find(const MmArgs& p, MmTile* tile) {
-  int w = xcd_remap(blockIdx.x, gridDim.x);
+__device__ __forceinline__ bool mm_place(const MmArgs& p, int w, int part, MmTile* tile) {
   MmTile t{};
-  int part = 0;
-  if (p.parts > 1) {
-    const int tiles = gridDim.x / p.parts;
-    part = w / tiles;
-    w %= tiles;
-  }
   if (p.offsets) {
     t = mm_routed_tile(p.offsets, p.groups, p.cap, Cfg::BM, w / p.tiles_n, threadIdx.x & 63);
     t.nt = w % p.tiles_n;
@@ -263,6 +256,14 @@ __device__ __forceinline__ bool mm_find(const MmArgs& p, MmTile* tile) {
   t.k1 = p.parts > 1 ? static_cast<int>(static_cast<int64_t>(p.nk) * (part + 1) / p.parts) : p.nk;
   *tile = t;
   return t.rows > 0;
+}
+
+// One workgroup's tile, from its index.
+template <typename Cfg>
+__device__ __forceinline__ bool mm_find(const MmArgs& p, MmTile* tile) {
+  const int w = xcd_remap(blockIdx.x, gridDim.x);
+  const int tiles = p.parts > 1 ? gridDim.x / p.parts : gridDim.x;
+  return mm_place<Cfg>(p, w % tiles, w / tiles, tile);
 }
 
 // The tile's sums. kPaired: B's tile holds gate rows and up rows in turns of

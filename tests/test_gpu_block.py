@@ -247,7 +247,7 @@ def test_ffn_activations(t, d, h, dtype, grad, act):
 
 
 @pytest.mark.parametrize("t,d,h,dtype", [(8200, 512, 1024, "bf16"), (16400, 1024, 1000, "bf16"),
-                                         (8200, 512, 515, "fp32")])
+                                         (8200, 512, 515, "fp32"), (200, 1024, 1400, "fp32")])
 def test_ffn_large_and_ragged(t, d, h, dtype):
     """Sizes that take the larger tiles, with ragged last ones."""
     note(f"ffn large {t} {d} {h} {dtype}")
