@@ -38,7 +38,8 @@ int check_ffn(const moe_ffn* f) {
   if (f->grad_dtype != MOE_FP32 && f->grad_dtype != f->dtype) return MOE_ERR_INVALID;
   if (f->d_model > 32768 || f->d_hidden > 32768 || f->tokens >= kRowLimit) return MOE_ERR_UNSUPPORTED;
   const int64_t wide = f->d_model > 2 * f->d_hidden ? f->d_model : 2 * f->d_hidden;
-  if (f->tokens >= (int64_t{1} << 40) / wide) return MOE_ERR_UNSUPPORTED;
+  // a launch stays under 2^32 threads: 256 for 64 x 64 outputs
+  if (f->tokens >= (int64_t{1} << 36) / wide) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
@@ -51,10 +52,10 @@ int check_i8(const moe_i8_linear* l) {
   if (l->gated && l->outputs % 2) return MOE_ERR_INVALID;
   if (l->top_k > l->groups) return MOE_ERR_INVALID;
   if (l->groups > 64 || l->inputs > 65536 || l->outputs > 65536) return MOE_ERR_UNSUPPORTED;
-  // token-slots, and the workgroups of a launch (64 x 64 tiles at least)
+  // token-slots, and the threads of a launch (256 for 64 x 64 outputs)
   if (l->tokens > (kRowLimit - 1) / l->top_k) return MOE_ERR_UNSUPPORTED;
   const int64_t tiles = (l->tokens * l->top_k + 63) / 64 + l->groups;
-  if (tiles > (kRowLimit - 1) / ((l->outputs + 63) / 64)) return MOE_ERR_UNSUPPORTED;
+  if (tiles >= (int64_t{1} << 24) / ((l->outputs + 63) / 64)) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 

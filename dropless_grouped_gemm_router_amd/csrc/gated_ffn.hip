@@ -38,7 +38,7 @@ template <int kAct>
 __device__ __forceinline__ float act_value(float a, float* slope) {
   if (kAct == MOE_ACT_RELU) {
     *slope = a > 0.0f ? 1.0f : 0.0f;
-    return fmaxf(a, 0.0f);
+    return a < 0.0f ? 0.0f : a;  // NaN stays
   }
   if (kAct == MOE_ACT_GELU) {
     const float cdf = 0.5f * (1.0f + erff(a * 0.70710678118654752f));
@@ -49,7 +49,8 @@ __device__ __forceinline__ float act_value(float a, float* slope) {
     // (1 + tanh u) / 2 is the logistic function of 2 u
     const float k = 0.79788456080286536f, c = 0.044715f;
     const float s = sigmoid_f(2.0f * k * (a + c * a * a * a));
-    *slope = s + a * 2.0f * s * (1.0f - s) * k * (1.0f + 3.0f * c * a * a);
+    const float bend = s * (1.0f - s);  // 0 where a^2 may overflow
+    *slope = bend > 0.0f ? s + a * 2.0f * bend * k * (1.0f + 3.0f * c * a * a) : s;
     return a * s;
   }
   const float s = sigmoid_f(a), v = a * s;

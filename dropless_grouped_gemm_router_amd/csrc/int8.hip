@@ -81,57 +81,59 @@ __device__ __forceinline__ void store_q(int8_t* p, const float (&f)[V], const Qu
   else *reinterpret_cast<uint32_t*>(p) = w[0];
 }
 
-// One row per kTPR threads. kNV pieces a thread stay in registers between
+// One row per kTPR threads (rows past the grid in turns). kNV pieces a thread stay in registers between
 // the two passes; with kNV 0 the row is read twice (the second time from
 // cache).
 template <typename T, int kTPR, int kNV>
-__global__ __launch_bounds__(kTPR < 256 ? 256 : kTPR) void quantize_rows_kernel(
-    int64_t rows, int width, int64_t pitch, const T* __restrict__ x, int64_t ld,
-    int8_t* __restrict__ q, float* __restrict__ scale) {
-  constexpr int V = Piece<T>::V, kRows = (kTPR < 256 ? 256 : kTPR) / kTPR;
-  __shared__ uint32_t part[16];
+__global__ __launch_bounds__(256) void quantize_rows_kernel(int64_t rows, int width, int64_t pitch,
+                                                            const T* __restrict__ x, int64_t ld,
+                                                            int8_t* __restrict__ q,
+                                                            float* __restrict__ scale) {
+  constexpr int V = Piece<T>::V, kRows = 256 / kTPR;
+  __shared__ uint32_t part[2][4];
   const int t = threadIdx.x % kTPR;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / kTPR;
-  if (row >= rows) return;
-  const T* xr = x + row * ld;
-  float f[kNV ? kNV : 1][V];
-  uint32_t most = 0;
-  if (kNV) {
+  int odd = 0;
+  for (int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / kTPR; row < rows;
+       row += static_cast<int64_t>(gridDim.x) * kRows, odd ^= 1) {
+    const T* xr = x + row * ld;
+    float f[kNV ? kNV : 1][V];
+    uint32_t most = 0;
+    if (kNV) {
 #pragma unroll
-    for (int i = 0; i < kNV; ++i) Piece<T>::widen(load_piece(xr, (i * kTPR + t) * V, width), f[i]);
+      for (int i = 0; i < kNV; ++i) Piece<T>::widen(load_piece(xr, (i * kTPR + t) * V, width), f[i]);
 #pragma unroll
-    for (int i = 0; i < kNV; ++i)
+      for (int i = 0; i < kNV; ++i)
 #pragma unroll
-      for (int e = 0; e < V; ++e) most = max(most, __float_as_uint(f[i][e]) & 0x7fffffffu);
-  } else {
-    for (int c = t * V; c < width; c += kTPR * V) {
-      Piece<T>::widen(load_piece(xr, c, width), f[0]);
+        for (int e = 0; e < V; ++e) most = max(most, __float_as_uint(f[i][e]) & 0x7fffffffu);
+    } else {
+      for (int c = t * V; c < width; c += kTPR * V) {
+        Piece<T>::widen(load_piece(xr, c, width), f[0]);
 #pragma unroll
-      for (int e = 0; e < V; ++e) most = max(most, __float_as_uint(f[0][e]) & 0x7fffffffu);
+        for (int e = 0; e < V; ++e) most = max(most, __float_as_uint(f[0][e]) & 0x7fffffffu);
+      }
     }
-  }
-  most = wave_umax(most);
-  if (kTPR > 64) {
-    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = most;
-    __syncthreads();
-    most = part[0];
-#pragma unroll
-    for (int w = 1; w < kTPR / 64; ++w) most = max(most, part[w]);
-  }
-  const float s = scale_of(most);
-  if (t == 0) scale[row] = s;
-  const Quantizer quantize(s);
-  int8_t* qr = q + row * pitch;
-  if (kNV) {
-#pragma unroll
-    for (int i = 0; i < kNV; ++i) {
-      const int c = (i * kTPR + t) * V;
-      if (c < pitch) store_q<V>(qr + c, f[i], quantize);
+    most = wave_umax(most);
+    if (kTPR > 64) {
+      // two sets of maxima: one barrier a row
+      if ((threadIdx.x & 63) == 0) part[odd][threadIdx.x >> 6] = most;
+      __syncthreads();
+      most = max(max(part[odd][0], part[odd][1]), max(part[odd][2], part[odd][3]));
     }
-  } else {
-    for (int c = t * V; c < pitch; c += kTPR * V) {
-      Piece<T>::widen(load_piece(xr, c, width), f[0]);
-      store_q<V>(qr + c, f[0], quantize);
+    const float s = scale_of(most);
+    if (t == 0) scale[row] = s;
+    const Quantizer quantize(s);
+    int8_t* qr = q + row * pitch;
+    if (kNV) {
+#pragma unroll
+      for (int i = 0; i < kNV; ++i) {
+        const int c = (i * kTPR + t) * V;
+        if (c < pitch) store_q<V>(qr + c, f[i], quantize);
+      }
+    } else {
+      for (int c = t * V; c < pitch; c += kTPR * V) {
+        Piece<T>::widen(load_piece(xr, c, width), f[0]);
+        store_q<V>(qr + c, f[0], quantize);
+      }
     }
   }
 }
@@ -419,10 +421,14 @@ void quantize_rows_t(int64_t rows, int width, const void* x, int64_t ld, int8_t*
                      hipStream_t s) {
   constexpr int V = Piece<T>::V;
   const int64_t pitch = i8_pitch(width);
-#define MOE_Q(TPR, NV)                                                                            \
-  MOE_LAUNCH("quantize_rows", (quantize_rows_kernel<T, TPR, NV>),                                 \
-             dim3(static_cast<unsigned>((rows * TPR + (TPR < 256 ? 255 : TPR - 1)) / (TPR < 256 ? 256 : TPR))), \
-             dim3(TPR < 256 ? 256 : TPR), 0, s, rows, width, pitch, static_cast<const T*>(x), ld, q, scale)
+  // at most 2^22 workgroups (a launch has to stay under 2^32 threads)
+  auto grid = [&](int tpr) {
+    const int64_t need = (rows * tpr + 255) / 256, most = int64_t{1} << 22;
+    return dim3(static_cast<unsigned>(need < most ? need : most));
+  };
+#define MOE_Q(TPR, NV)                                                                         \
+  MOE_LAUNCH("quantize_rows", (quantize_rows_kernel<T, TPR, NV>), grid(TPR), dim3(256), 0, s, \
+             rows, width, pitch, static_cast<const T*>(x), ld, q, scale)
   if (pitch <= 64 * V) MOE_Q(64, 1);
   else if (pitch <= 128 * V) MOE_Q(64, 2);
   else if (pitch <= 256 * V) MOE_Q(256, 1);

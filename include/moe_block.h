@@ -90,7 +90,7 @@ typedef enum {
  * the two pre-activations.
  *
  * Supported (else MOE_ERR_UNSUPPORTED): d_model and d_hidden up to 32768
- * (any value), tokens * max(d_model, 2 * d_hidden) < 2^40, tokens < 2^31.
+ * (any value), tokens * max(d_model, 2 * d_hidden) < 2^36.
  */
 typedef struct {
   int64_t tokens;
@@ -186,7 +186,7 @@ int moe_quantize_weight(int32_t groups, int32_t width, int32_t outputs, int32_t 
  *
  * Supported (else MOE_ERR_UNSUPPORTED): inputs and outputs up to 65536 (any
  * value; outputs even when gated), groups <= 64, tokens * top_k < 2^31 and
- * fewer than 2^31 output tiles of 64 x 64.
+ * fewer than 2^24 output tiles of 64 x 64.
  */
 typedef struct {
   int64_t tokens;

@@ -94,7 +94,7 @@ def ffn(tokens=10, d=256, h=512, dtype=1, act=0, grad=0):
     (dict(tokens=-1), INV), (dict(d=0), INV), (dict(h=0), INV), (dict(dtype=2), INV),
     (dict(act=-1), INV), (dict(act=4), INV), (dict(dtype=0, grad=1), INV), (dict(grad=2), INV),
     (dict(d=32769), UNS), (dict(h=32769), UNS), (dict(tokens=1 << 31), UNS),
-    (dict(tokens=1 << 25, h=32768), UNS)])
+    (dict(tokens=1 << 20, h=32768), UNS)])
 def test_ffn_problem_refusals(kw, code):
     f = ffn(**kw)
     refused(code, K.moe_gated_ffn, f, A, C, D, E, None, F, G, stream=0)
@@ -127,7 +127,7 @@ def test_ffn_argument_refusals():
 
 def test_size_queries_over_the_range():
     """Sizes exist, and grow with training, from no token to the largest."""
-    for t in (0, 1, 16, 17, 128, 129, 5000, (1 << 24) - 1):
+    for t in (0, 1, 16, 17, 128, 129, 5000, 1 << 19):
         for d, h in ((1, 1), (128, 256), (500, 1001), (8192, 32768)):
             for dtype in (0, 1):
                 f = ffn(t, d, h, dtype)
@@ -151,7 +151,7 @@ ROUTING = {"expert_offsets": A, "perm": C}
     (dict(gather=2), INV), (dict(gated=-1), INV), (dict(gated=1, outputs=255), INV),
     (dict(groups=4, top_k=5), INV), (dict(groups=65, top_k=2), UNS), (dict(inputs=65537), UNS),
     (dict(outputs=65537), UNS), (dict(groups=8, tokens=1 << 30, top_k=2), UNS),
-    (dict(tokens=1 << 30, outputs=65536), UNS)])
+    (dict(tokens=1 << 20, outputs=65536), UNS)])
 def test_i8_problem_refusals(kw, code):
     l = i8(**kw)
     refused(code, K.moe_linear_i8, l, A, None, C, D, None, ROUTING, E, F, stream=0)

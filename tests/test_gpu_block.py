@@ -302,6 +302,16 @@ def test_ffn_odd_values_and_zero_tokens(t):
     keep = [i for i in range(t) if i != t // 2]
     assert torch.equal(room[:t][keep], clean[keep]) and bool(room[t // 2].isnan().all())
     assert bool((room[t:] == 9).all())
+    # every activation keeps a NaN and the sizes that overflow inside its formula
+    for act in ("silu", "gelu", "gelu_tanh", "relu"):
+        fa = K.GatedFfn(t, 96, 160, "bf16", act, "bf16")
+        K.gated_ffn(fa, x, w, buf)
+        assert bool(room[t // 2].isnan().all()), act
+        ba = K.allocate_ffn(fa, training=True)
+        big = torch.where(x.isnan(), torch.zeros_like(x), x) * 1e18
+        K.gated_ffn(fa, big, {n: v * (1e-19 if n == "w_up" else 1.0) for n, v in w.items()}, ba, training=True)
+        K.gated_ffn_backward(fa, big, w, dy * 1e-12, ba)
+        assert bool(torch.isfinite(ba.out.float()).all()) and bool(torch.isfinite(ba.grad_x.float()).all()), act
     f0 = K.GatedFfn(0, 96, 160, "bf16", grad_dtype="bf16")
     b0 = K.allocate_ffn(f0, training=True)
     for g in b0.grads.values():
@@ -467,6 +477,8 @@ def test_linear_i8_routed(t, k, n, e, top, gated, dtype):
     buf = K.allocate_linear_i8(l)
     near("gathered", K.linear_i8(l, x, wq, ws, buf, routing=routing), want, tol)
     first = buf.y.clone()
+    q, qs = K.quantize_rows(x)
+    assert torch.equal(K.linear_i8(l, q, wq, ws, buf, routing=routing, x_scale=qs), first)
     ls = K.LinearI8(t, k, n, dtype, groups=e, top_k=top, gated=gated, sorted_input=True)
     K.linear_i8(ls, x[token.cuda()].contiguous(), wq, ws, buf2 := K.allocate_linear_i8(ls), routing=routing)
     assert torch.equal(buf2.y, first)
@@ -479,6 +491,67 @@ def test_linear_i8_routed(t, k, n, e, top, gated, dtype):
         assert torch.equal(buf.y[at:at + kept], first[at:at + kept])
         assert bool((buf.y[at + kept:at + c] == 11).all()), "rows past the capacity were written"
         at += c
+
+
+def test_linear_i8_one_expert():
+    """A routing over a single expert is the dense product in perm's order."""
+    import torch
+    r = gen(8)
+    for t in (9, 150):
+        x, (wq, ws) = r(t, 200, dtype="bf16"), K.quantize_weights(r(200, 130))
+        l = K.LinearI8(t, 200, 130, "bf16")
+        want = K.linear_i8(l, x, wq, ws, K.allocate_linear_i8(l))
+        perm = torch.arange(t, device="cuda", dtype=torch.int32).flip(0).contiguous()
+        routing = {"perm": perm, "expert_offsets": torch.tensor([0, t], dtype=torch.int32, device="cuda")}
+        got = K.linear_i8(l, x, wq, ws, K.allocate_linear_i8(l), routing=routing)
+        assert torch.equal(got, want.flip(0))
+
+
+# ----------------------------------------------------------------- long ones
+
+def test_offsets_past_32_bits():
+    """Matrices of more than 2^32 bytes and 2^31 elements: the last rows come
+    out as a small call makes them."""
+    import torch
+    note("large norm and int8")
+    rows, width, last = 1_100_000, 2048, 300
+    x = torch.empty(rows, width, dtype=torch.bfloat16, device="cuda")
+    x.normal_(generator=torch.Generator(device="cuda").manual_seed(1))
+    w = 1 + gen(2)(width, std=0.1)
+    big = K.allocate_norm(rows, width, "bf16", training=True)
+    small = K.allocate_norm(last, width, "bf16", training=True)
+    tail = x[-last:].contiguous()
+    assert torch.equal(K.layer_norm(x, w, None, 1e-5, big)[-last:], K.layer_norm(tail, w, None, 1e-5, small))
+    K.layer_norm_backward(x, w, big.y, big)
+    K.layer_norm_backward(tail, w, small.y, small)
+    assert torch.equal(big.grad_x[-last:], small.grad_x)
+    del big
+    wide = x.view(rows // 2, 2 * width)
+    q, s = K.quantize_rows(wide)
+    wq, ws = K.quantize_weights(gen(3)(2 * width, 130))
+    l = K.LinearI8(rows // 2, 2 * width, 130, "bf16")
+    got = K.linear_i8(l, q, wq, ws, K.allocate_linear_i8(l), x_scale=s)
+    ls = K.LinearI8(last, 2 * width, 130, "bf16")
+    assert torch.equal(got[-last:], K.linear_i8(ls, wide[-last:].contiguous(), wq, ws, K.allocate_linear_i8(ls)))
+    del x, wide, q
+    note("large ffn")
+    f, x, w, dy, buf = ffn_case(280_000, 64, 8000, "bf16", training=False)
+    K.gated_ffn(f, x, w, buf)
+    fs = K.GatedFfn(300, 64, 8000, "bf16")
+    bs = K.allocate_ffn(fs)
+    K.gated_ffn(fs, x[-300:].contiguous(), w, bs)
+    near("last rows", buf.out[-300:], bs.out.double(), 2 * U["bf16"])
+
+
+def test_many_rows():
+    """More rows than a launch has workgroups for."""
+    import torch
+    n = 17_000_000
+    x = torch.ones(n, 3, device="cuda")
+    x[-1] = torch.tensor([1.0, -2.0, 0.5])
+    q, s = K.quantize_rows(x)
+    assert q[-1, :3].tolist() == [64, -127, 32] and float(s[-1]) == float(np.float32(2) / np.float32(127))
+    assert bool((q[:-1, :3] == 127).all()) and not q[:, 3:].any()
 
 
 # ------------------------------------------------------------- used together
@@ -528,6 +601,46 @@ def test_streams_and_graphs():
         step(*others[0], xs)
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, outs(*others[0]))), i
+
+
+def test_answering_in_a_graph():
+    """One step of answering four sequences, captured and replayed: norm,
+    gated block and a product in their serving forms, and the layer with 8-bit
+    experts."""
+    import torch
+    p = Problem(4, 16, 4, 256, 128, 0, "bf16", 64)
+    c = Case(p, seed=5)
+    wt = c.weights()
+    gu, dn = K.quantize_weights(wt["w_gate"], wt["w_up"]), K.quantize_weights(wt["w_down"])
+    f, x, w, _, _ = ffn_case(4, 256, 500, "bf16", training=False)
+    wq, ws = K.quantize_weights(gen(4)(256, 300))
+    l = K.LinearI8(4, 256, 300, "bf16")
+    nw = 1 + gen(1)(256, std=0.1)
+
+    def make():
+        return (K.allocate_norm(4, 256, "bf16"), K.allocate_ffn(f), K.allocate_experts_i8(p),
+                B.allocate(p, "cuda"), K.allocate_linear_i8(l))
+
+    def step(x, bufs):
+        nb, fb, eb, mb, lb = bufs
+        h = K.layer_norm(x, nw, None, 1e-5, nb)
+        y = K.gated_ffn(f, h, w, fb)
+        z = K.forward_i8(p, y, wt["w_router"], gu, dn, mb, eb)
+        return K.linear_i8(l, z, wq, ws, lb)
+
+    one, two, xs = make(), make(), x.clone()
+    step(xs, one)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(xs, one)
+    for i in range(4):
+        xs.copy_(x * (i + 1) + i)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = out.clone()
+        assert torch.equal(got, step(xs, two)), i
+        torch.cuda.synchronize()
 
 
 def test_int8_experts_in_the_layer():
