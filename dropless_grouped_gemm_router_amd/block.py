@@ -249,6 +249,9 @@ class NormBuffers:
     grad_weight: Optional[object] = None
     grad_bias: Optional[object] = None
     workspace: Optional[object] = None
+    # what allocate_norm made, with its shape, type and device: tensors put in
+    # their place are checked on every call, these are known to fit
+    made: Optional[tuple] = None
 
 
 @lru_cache(maxsize=256)
@@ -267,6 +270,7 @@ def allocate_norm(rows: int, width: int, dtype, device="cuda", training: bool = 
         b.grad_x = torch.empty((rows, width), dtype=dt, device=device)
         b.grad_weight, b.grad_bias = torch.empty(width, **f32), torch.empty(width, **f32)
         b.workspace = torch.empty(nws, dtype=torch.uint8, device=device)
+    b.made = (b.y.shape, dt, device, b.y, b.mean, b.rstd, b.grad_x, b.grad_weight, b.grad_bias)
     return b
 
 
@@ -283,13 +287,17 @@ def layer_norm(x, weight, bias, eps: float, buf: NormBuffers, stream=None):
         _want("weight", weight, (width,), f32, dev)
     if bias is not None:
         _want("bias", bias, (width,), f32, dev)
-    y, mean, rstd = buf.y, buf.mean, buf.rstd
-    ld_y = _want_rows("y", y, shape, dt, dev)
-    _want("mean", mean, (rows,), f32, dev)
-    _want("rstd", rstd, (rows,), f32, dev)
+    y, mean, rstd, m = buf.y, buf.mean, buf.rstd, buf.made
+    if m and y is m[3] and mean is m[4] and rstd is m[5] and m[0] == shape and m[1] is dt and m[2] == dev:
+        ld_y = width
+    else:
+        ld_y = _want_rows("y", y, shape, dt, dev)
+        _want("mean", mean, (rows,), f32, dev)
+        _want("rstd", rstd, (rows,), f32, dev)
     n = _norm(rows, width, _code(x), eps, ld_x, ld_y, 0, 0)
-    _run("moe_layer_norm", dev, stream, load().moe_layer_norm, n[1], x.data_ptr(), _ptr(weight),
-         _ptr(bias), y.data_ptr(), mean.data_ptr(), rstd.data_ptr())
+    _run("moe_layer_norm", dev, stream, load().moe_layer_norm, n[1], x.data_ptr(),
+         None if weight is None else weight.data_ptr(), None if bias is None else bias.data_ptr(),
+         y.data_ptr(), mean.data_ptr(), rstd.data_ptr())
     return y
 
 
@@ -303,16 +311,21 @@ def layer_norm_backward(x, weight, grad_out, buf: NormBuffers, stream=None):
         raise ValueError("the buffers were allocated without training=True")
     ld_x = _want_rows("x", x, shape, dt, dev)
     ld_go = _want_rows("grad_out", grad_out, shape, dt, dev)
-    ld_gx = _want_rows("grad_x", gx, shape, dt, dev)
     if weight is not None:
         _want("weight", weight, (width,), f32, dev)
-    _want("mean", buf.mean, (rows,), f32, dev)
-    _want("rstd", buf.rstd, (rows,), f32, dev)
-    _want("grad_weight", gw, (width,), f32, dev)
-    _want("grad_bias", gb, (width,), f32, dev)
+    m = buf.made
+    if (m and gx is m[6] and gw is m[7] and gb is m[8] and buf.mean is m[4] and buf.rstd is m[5]
+            and m[0] == shape and m[1] is dt and m[2] == dev):
+        ld_gx = width
+    else:
+        ld_gx = _want_rows("grad_x", gx, shape, dt, dev)
+        _want("mean", buf.mean, (rows,), f32, dev)
+        _want("rstd", buf.rstd, (rows,), f32, dev)
+        _want("grad_weight", gw, (width,), f32, dev)
+        _want("grad_bias", gb, (width,), f32, dev)
     n = _norm(rows, width, _code(x), 0.0, ld_x, 0, ld_go, ld_gx)
     _run("moe_layer_norm_bwd", dev, stream, load().moe_layer_norm_bwd, n[1], x.data_ptr(),
-         _ptr(weight), buf.mean.data_ptr(), buf.rstd.data_ptr(), grad_out.data_ptr(), gx.data_ptr(),
+         None if weight is None else weight.data_ptr(), buf.mean.data_ptr(), buf.rstd.data_ptr(), grad_out.data_ptr(), gx.data_ptr(),
          gw.data_ptr(), gb.data_ptr(), buf.workspace.data_ptr(), buf.workspace.numel())
     return gx, gw, gb
 
