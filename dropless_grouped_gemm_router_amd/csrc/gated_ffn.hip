@@ -338,23 +338,44 @@ __device__ __forceinline__ void put_hidden(bf16_t* high, bf16_t* low, float v) {
 }
 __device__ __forceinline__ void put_hidden(float* high, float*, float v) { *high = v; }
 
+// One value of f and p as keep8 keeps eight.
+__device__ __forceinline__ void keep1(const FfnOut& o, int64_t at, float f, float p, const bf16_t*) {
+  const uint32_t a = __float_as_uint(f), b = __float_as_uint(p);
+  static_cast<bf16_t*>(o.f)[at] = static_cast<bf16_t>(a >> 16);
+  static_cast<bf16_t*>(o.p)[at] = static_cast<bf16_t>(b >> 16);
+  o.low[at] = static_cast<uint8_t>(((a >> 12) & 0x0fu) | ((b >> 8) & 0xf0u));
+}
+__device__ __forceinline__ void keep1(const FfnOut& o, int64_t at, float f, float p, const float*) {
+  static_cast<float*>(o.f)[at] = f;
+  static_cast<float*>(o.p)[at] = p;
+}
+
+// Training (o.f): also what the backward needs, over the padded width o.ld
+// (columns past N come out as zeros: no weights are read for them), and the
+// backward's row of zeros.
 template <typename T, int kR, int kAct>
-__global__ __launch_bounds__(512) void ffn_rows_gate_up_kernel(const SkinnyArgs<T, 2> a, T* high, T* low) {
-  __shared__ float lds[kSkinnyWaves][16 * 64];
+__global__ __launch_bounds__(512) void ffn_rows_gate_up_kernel(const SkinnyArgs<T, 2> a, T* high, T* low,
+                                                               const FfnOut o, u32x4* zero) {
+  __shared__ float lds[kSkinnyWaves][kSkinnyLds];
   float sum[kR][2][2];
+  if (zero && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < kTrZeroBytes / 16)
+    zero[threadIdx.x] = (u32x4){0u, 0u, 0u, 0u};
   skinny_sums<T, 2, kR, false>(a, lds, sum);
 #pragma unroll
   for (int i = 0; i < kR; ++i)
 #pragma unroll
     for (int v = 0; v < 2; ++v) {
-      int r, c;
-      skinny_place(threadIdx.x + 512 * v, &r, &c);
-      const int64_t row = (static_cast<int64_t>(blockIdx.y) * kR + i) * 16 + r;
-      const int n = blockIdx.x * kSkinnyCols + c;
-      if (row >= a.rows || n >= a.N) continue;
+      const int64_t row = (static_cast<int64_t>(blockIdx.y) * kR + i) * 16 + (threadIdx.x >> 6) + 8 * v;
+      const int n = blockIdx.x * kSkinnyCols + (threadIdx.x & 63);
+      if (row >= a.rows) continue;
+      const float b = sum[i][v][1];
       float slope;
-      const int64_t at = row * a.N + n;
-      put_hidden(high + at, low + at, act_value<kAct>(sum[i][v][0], &slope) * sum[i][v][1]);
+      const float f = act_value<kAct>(sum[i][v][0], &slope), h = f * b;
+      if (n < a.N) put_hidden(high + row * a.N + n, low + row * a.N + n, h);
+      if (o.f) {
+        put(static_cast<T*>(o.h) + row * o.ld + n, h);
+        keep1(o, row * o.ld + n, f, b * slope, static_cast<const T*>(nullptr));
+      }
     }
 }
 
@@ -362,17 +383,15 @@ __global__ __launch_bounds__(512) void ffn_rows_gate_up_kernel(const SkinnyArgs<
 // [k_parts][rows][N].
 template <typename T, int kR>
 __global__ __launch_bounds__(512) void ffn_rows_down_kernel(const SkinnyArgs<T, 1> a, T* out, float* part) {
-  __shared__ float lds[kSkinnyWaves][16 * 64];
+  __shared__ float lds[kSkinnyWaves][kSkinnyLds];
   float sum[kR][2][1];
   skinny_sums<T, 1, kR, sizeof(T) == 2>(a, lds, sum);
 #pragma unroll
   for (int i = 0; i < kR; ++i)
 #pragma unroll
     for (int v = 0; v < 2; ++v) {
-      int r, c;
-      skinny_place(threadIdx.x + 512 * v, &r, &c);
-      const int64_t row = (static_cast<int64_t>(blockIdx.y) * kR + i) * 16 + r;
-      const int n = blockIdx.x * kSkinnyCols + c;
+      const int64_t row = (static_cast<int64_t>(blockIdx.y) * kR + i) * 16 + (threadIdx.x >> 6) + 8 * v;
+      const int n = blockIdx.x * kSkinnyCols + (threadIdx.x & 63);
       if (row >= a.rows || n >= a.N) continue;
       if (part) part[(blockIdx.z * a.rows + row) * a.N + n] = sum[i][v][0];
       else put(out + row * a.N + n, sum[i][v][0]);
@@ -508,7 +527,8 @@ int slices(int64_t rows, int64_t tiles) {
 
 // Row tiles of 16 a workgroup of the serving form takes.
 int rows_tile(const moe_ffn& f) { return f.tokens <= 16 || f.dtype != MOE_BF16 ? 1 : 2; }
-// Whether the serving form is taken (inference only).
+// Whether the forward takes the serving form (training too: what it keeps is
+// the same, and the weights are not turned).
 bool few_rows(const moe_ffn& f) { return f.tokens <= kFewRows; }
 
 FfnBlockLayout ffn_block_layout(const moe_ffn& f, bool training) {
@@ -521,7 +541,7 @@ FfnBlockLayout ffn_block_layout(const moe_ffn& f, bool training) {
     o = align_up(o + bytes, 256);
     return at;
   };
-  if (!training && few_rows(f)) {
+  if (few_rows(f)) {
     L.rows_h = take(T * h * es * (es == 2 ? 2 : 1));
     // slices of K so that every CU has a workgroup, of two steps a wave at least
     const int r = 16 * rows_tile(f);
@@ -531,20 +551,23 @@ FfnBlockLayout ffn_block_layout(const moe_ffn& f, bool training) {
     L.k_parts = static_cast<int>(want < most ? want : most);
     L.rows_part = take(L.k_parts > 1 ? L.k_parts * T * d * sizeof(float) : 0);
     L.total = o;
-    return L;
+    if (!training) return L;
+    o = 0;  // the backward has the place for itself
   }
   L.xp = take(d == dp ? 0 : T * dp * es);
   const size_t start = o;
-  L.tg = take(h * dp * es);
-  L.tu = take(h * dp * es);
-  L.td = take(d * hp * es);
+  if (!few_rows(f)) {
+    L.tg = take(h * dp * es);
+    L.tu = take(h * dp * es);
+    L.td = take(d * hp * es);
+  }
   if (!training) L.h = take(T * hp * es);
   auto sums = [&](int64_t K) {
     const int n = parts_of(es, f.tokens, d, K * es / 128);
     return n > 1 ? n * T * d * sizeof(float) : 0;
   };
   L.k_sums = take(sums(hp));
-  L.total = o;
+  L.total = std::max(L.total, o);
   if (training) {
     // the backward reuses the turned weights' place
     o = start;
@@ -586,6 +609,16 @@ SavedLayout saved_layout(const moe_ffn& f) {
   const size_t n = align_up(cells * elem_bytes(f), 256);
   const size_t zero = 3 * n + (f.dtype == MOE_BF16 ? align_up(cells, 256) : 0);
   return SavedLayout{0, n, 2 * n, 3 * n, zero, zero + kTrZeroBytes};
+}
+
+FfnOut saved_out(const SavedLayout& S, char* saved, int64_t hp) {
+  FfnOut o{};
+  o.h = saved + S.h;
+  o.f = saved + S.f;
+  o.p = saved + S.p;
+  o.low = reinterpret_cast<uint8_t*>(saved + S.low);
+  o.ld = hp;
+  return o;
 }
 
 // ----------------------------------------------------------------- launches
@@ -727,21 +760,28 @@ MmArgs rows_of(const void* a, int64_t lda, const void* b, int64_t ldb, int64_t M
 
 template <typename T, int kR>
 hipError_t ffn_rows_t(const moe_ffn& f, const void* x, const void* wg, const void* wu,
-                      const void* wd, void* out, void* ws, hipStream_t s) {
-  const FfnBlockLayout L = ffn_block_layout(f, false);
-  char* W = static_cast<char*>(ws);
+                      const void* wd, void* saved, void* out, void* ws, hipStream_t s) {
+  const FfnBlockLayout L = ffn_block_layout(f, saved != nullptr);
+  char *W = static_cast<char*>(ws), *SV = static_cast<char*>(saved);
   const int d = f.d_model, h = f.d_hidden;
   T* high = reinterpret_cast<T*>(W + L.rows_h);
   T* low = sizeof(T) == 2 ? high + f.tokens * h : nullptr;
   const unsigned tall = static_cast<unsigned>((f.tokens + 16 * kR - 1) / (16 * kR));
   SkinnyArgs<T, 2> a{static_cast<const T*>(x), nullptr, d,
                      {static_cast<const T*>(wg), static_cast<const T*>(wu)}, f.tokens, d, h, 1};
-  const dim3 ga((h + kSkinnyCols - 1) / kSkinnyCols, tall);
+  FfnOut o{};
+  u32x4* zero = nullptr;
+  if (SV) {
+    const SavedLayout S = saved_layout(f);
+    o = saved_out(S, SV, pad128(h));
+    zero = reinterpret_cast<u32x4*>(SV + S.zero);
+  }
+  const dim3 ga((SV ? pad128(h) : h + kSkinnyCols - 1) / kSkinnyCols, tall);
   switch (f.act) {
 #define MOE_ROWS(ACT)                                                                              \
   case ACT:                                                                                        \
     MOE_LAUNCH("ffn_rows_gate_up", (ffn_rows_gate_up_kernel<T, kR, ACT>), ga, dim3(512), 0, s, a, \
-               high, low);                                                                         \
+               high, low, o, zero);                                                                         \
     break
     MOE_ROWS(MOE_ACT_SILU);
     MOE_ROWS(MOE_ACT_GELU);
@@ -765,12 +805,12 @@ hipError_t ffn_rows_t(const moe_ffn& f, const void* x, const void* wg, const voi
 template <typename T>
 hipError_t ffn_fwd_t(const moe_ffn& f, const void* x, const void* wg, const void* wu,
                      const void* wd, void* saved, void* out, void* ws, hipStream_t s) {
-  if (!saved && few_rows(f)) {
+  if (few_rows(f)) {
     [[maybe_unused]] const int r = rows_tile(f);
     if constexpr (sizeof(T) == 2) {
-      if (r == 2) return ffn_rows_t<T, 2>(f, x, wg, wu, wd, out, ws, s);
+      if (r == 2) return ffn_rows_t<T, 2>(f, x, wg, wu, wd, saved, out, ws, s);
     }
-    return ffn_rows_t<T, 1>(f, x, wg, wu, wd, out, ws, s);
+    return ffn_rows_t<T, 1>(f, x, wg, wu, wd, saved, out, ws, s);
   }
   const FfnBlockLayout L = ffn_block_layout(f, saved != nullptr);
   const SavedLayout S = saved_layout(f);
@@ -789,12 +829,8 @@ hipError_t ffn_fwd_t(const moe_ffn& f, const void* x, const void* wg, const void
   MmArgs p = rows_of<T>(xp, dp, W + L.tg, dp, f.tokens, h, dp);
   p.half = static_cast<int64_t>(L.tu) - static_cast<int64_t>(L.tg);
   FfnOut o{};
-  o.h = SV ? SV + S.h : W + L.h;
-  if (SV) {
-    o.f = SV + S.f;
-    o.p = SV + S.p;
-    o.low = reinterpret_cast<uint8_t*>(SV + S.low);
-  }
+  if (SV) o = saved_out(S, SV, hp);
+  else o.h = W + L.h;
   o.ld = hp;
   tiles_act<T, kGated>("ffn_gate_up", f.act, p, o, s);
   MmArgs q = rows_of<T>(o.h, hp, W + L.td, hp, f.tokens, d, hp);
@@ -857,12 +893,8 @@ hipError_t ffn_bwd_t(const moe_ffn& f, const void* x, const void* wg, const void
   pad<T>(pads, s);
 
   MmArgs p = rows_of<T>(dyp, dp, wdp, dp, tok, h, dp);
-  FfnOut o{};
-  o.f = const_cast<char*>(SV + S.f);
-  o.p = const_cast<char*>(SV + S.p);
-  o.low = reinterpret_cast<uint8_t*>(const_cast<char*>(SV + S.low));
+  FfnOut o = saved_out(S, const_cast<char*>(SV), hp);
   o.dab = W + L.dab;
-  o.ld = hp;
   tiles<T, kGatedGrad, 0>("ffn_bwd_down", p, o, s);
 
   MmArgs q = rows_of<T>(W + L.dab, 2 * hp, wgp, hp, tok, d, hp);

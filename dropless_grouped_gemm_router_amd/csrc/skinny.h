@@ -126,10 +126,12 @@ struct SkinnyArgs {
 };
 
 // Sums of this workgroup's columns over its slice of K, for 16 kR rows:
-// after the call thread t holds, for row tile i and v = 0, 1, the sums of
-// item t + 512 v: register (item / 64) of lane item % 64, all kW of them.
+// after the call thread t holds, for row tile i and v = 0, 1, those of column
+// t % 64 and row t / 64 + 8 v of the tile, all kW of them. In LDS register
+// 4 q + j of a lane stands at 65 (4 q + j) + lane: both sides use all banks.
+constexpr int kSkinnyLds = 16 * 65;
 template <typename T, int kW, int kR, bool kLow>
-__device__ __forceinline__ void skinny_sums(const SkinnyArgs<T, kW>& a, float (*lds)[16 * 64],
+__device__ __forceinline__ void skinny_sums(const SkinnyArgs<T, kW>& a, float (*lds)[kSkinnyLds],
                                             float (&sum)[kR][2][kW]) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int n = blockIdx.x * kSkinnyCols + 4 * (lane & 15);
@@ -183,6 +185,7 @@ __device__ __forceinline__ void skinny_sums(const SkinnyArgs<T, kW>& a, float (*
     if (s + kSkinnyWaves < s1) multiply(1);
   }
 
+  const int c = lane;  // column that this thread adds up
 #pragma unroll
   for (int i = 0; i < kR; ++i)
 #pragma unroll
@@ -191,24 +194,17 @@ __device__ __forceinline__ void skinny_sums(const SkinnyArgs<T, kW>& a, float (*
 #pragma unroll
       for (int j = 0; j < 4; ++j)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) lds[wave][(4 * q + j) * 64 + lane] = acc[i][m][j][q];
+        for (int q = 0; q < 4; ++q) lds[wave][(4 * q + j) * 65 + lane] = acc[i][m][j][q];
       __syncthreads();
 #pragma unroll
       for (int v = 0; v < 2; ++v) {
         float t = 0.0f;
 #pragma unroll
-        for (int u = 0; u < kSkinnyWaves; ++u) t += lds[u][threadIdx.x + 512 * v];
+        for (int u = 0; u < kSkinnyWaves; ++u) t += lds[u][(c & 15) * 65 + (c >> 4) * 16 + wave + 8 * v];
         sum[i][v][m] = t;
       }
       __syncthreads();
     }
-}
-
-// Row (within the workgroup's row tile) and column (within its 64) of item e.
-__device__ __forceinline__ void skinny_place(int e, int* row, int* col) {
-  const int lane = e & 63;
-  *row = lane & 15;
-  *col = 16 * (lane >> 4) + (e >> 6);
 }
 
 }  // namespace moe
