@@ -409,6 +409,116 @@ __global__ __launch_bounds__(256) void join_kernel(const float* __restrict__ par
   put(out + i, v);
 }
 
+// A weight gradient in bf16 operands that needs no slices of the tokens (few
+// tokens, or weights with tiles enough): the ring of wgrad_tr_kernel, but each
+// tile is written once, in the gradient's type and cropped, instead of as
+// fp32 sums that another launch reads again (2048 x 8192: 10 bytes an element
+// against 2). Rows of the gradient past M, and columns past N of each half
+// (gate and up side by side), are not stored.
+struct GradDirect {
+  const bf16_t *a, *b;
+  int64_t lda, ldb, rows;
+  int tiles_m, tiles_n, M, N, half;
+  void *out, *out2;
+};
+template <typename Cfg, typename G>
+__global__ __launch_bounds__(Cfg::NT) void grad_direct_kernel(const GradDirect p,
+                                                              const bf16_t* __restrict__ zero) {
+  constexpr int BM = Cfg::BM, BN = Cfg::BN, NS = Cfg::NS;
+  __shared__ __attribute__((aligned(1024))) char smem[NS * Cfg::STAGE];
+  const int w = xcd_remap(blockIdx.x, gridDim.x);
+  const int mt = w / p.tiles_n, nt = w % p.tiles_n;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int wm = wave / Cfg::WAVES_N, wn = wave % Cfg::WAVES_N;
+  const int a_col = mt * BM, b_col = nt * BN;
+  int a_off[2][2], b_off[2][2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      a_off[i][h] = tr_frag_off<Cfg::A_PITCH>(wm * 64 + i * 32, lane, h);
+      b_off[i][h] = Cfg::A_BYTES + tr_frag_off<Cfg::B_PITCH>(wn * 64 + i * 32, lane, h);
+    }
+  f32x16_t acc[2][2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.0f;
+  const uint32_t lds_base = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(smem));
+  const int nk = static_cast<int>((p.rows + kTrKT - 1) / kTrKT);
+  auto issue = [&](int st) {
+    char* buf = smem + (st % NS) * Cfg::STAGE;
+    const int64_t row0 = static_cast<int64_t>(st) * kTrKT;
+    tr_issue<Cfg::A_CPR, Cfg::A_LOADS>(buf, p.a, p.lda, a_col, row0, p.rows, zero, wave, lane);
+    tr_issue<Cfg::B_CPR, Cfg::B_LOADS>(buf + Cfg::A_BYTES, p.b, p.ldb, b_col, row0, p.rows, zero, wave, lane);
+  };
+#pragma unroll
+  for (int st = 0; st < NS - 1; ++st) issue(st);
+  for (int s = 0; s < nk; ++s) {
+    tr_wait_vm<Cfg::LOADS * (NS - 2)>();
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    issue(s + NS - 1);
+    const uint32_t buf = lds_base + (s % NS) * Cfg::STAGE;
+#pragma unroll
+    for (int ks = 0; ks < kTrKT / 16; ++ks) {
+      uint32_t ad[8];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          ad[2 * i + h] = buf + ks * 16 * Cfg::A_PITCH + a_off[i][h];
+          ad[4 + 2 * i + h] = buf + ks * 16 * Cfg::B_PITCH + b_off[i][h];
+        }
+      tr_v4i16 v[8];
+      tr_read_kstep(ad, v);
+      bf16x8_t af[2], bf[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        af[i] = __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(v[2 * i], v[2 * i + 1], 0, 1, 2, 3, 4, 5, 6, 7));
+        bf[i] = __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(v[4 + 2 * i], v[5 + 2 * i], 0, 1, 2, 3, 4, 5, 6, 7));
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bf[j], af[i], acc[i][j], 0, 0, 0);
+    }
+  }
+  // the loads past the end land before the workgroup's LDS is reused below
+  tr_wait_vm<0>();
+  __syncthreads();
+  // 32 x 32 blocks through LDS of this wave: whole pieces of a row of the
+  // gradient per store
+  constexpr int kPitch = 36;  // floats
+  static_assert(Cfg::NT / 64 * 32 * kPitch * 4 <= NS * Cfg::STAGE, "blocks fit");
+  float* block = reinterpret_cast<float*>(smem) + wave * 32 * kPitch;
+  const int r32 = lane & 31, g = lane >> 5;
+  const bool second = b_col >= p.half;
+  G* out = static_cast<G*>(second ? p.out2 : p.out);
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+#pragma unroll
+      for (int rr = 0; rr < 4; ++rr)
+        *reinterpret_cast<float4*>(block + r32 * kPitch + 8 * rr + 4 * g) =
+            make_float4(acc[i][j][4 * rr], acc[i][j][4 * rr + 1], acc[i][j][4 * rr + 2], acc[i][j][4 * rr + 3]);
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      const int n = b_col - (second ? p.half : 0) + wn * 64 + j * 32 + (lane & 3) * 8;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int r = (lane >> 2) + 16 * k, m = a_col + wm * 64 + i * 32 + r;
+        float v[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[q] = block[r * kPitch + (lane & 3) * 8 + q];
+        if (m < p.M && n < p.N) store8<G, false>(out + static_cast<int64_t>(m) * p.N, n, p.N, v);
+      }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    }
+}
+
 // The three weight gradients in fp32, in one launch: products over the
 // tokens of turned operands, [rows of the gradient][tokens] each.
 struct GradArgs {
@@ -453,12 +563,14 @@ struct SliceJob {
 };
 struct SliceJobs {
   SliceJob job[3];
+  int n;
 };
 template <typename G>
 __global__ __launch_bounds__(256) void slice_sum_kernel(const SliceJobs jobs) {
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < jobs.job[2].end;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < jobs.job[jobs.n - 1].end;
        i += static_cast<int64_t>(gridDim.x) * 256) {
-    const int which = i < jobs.job[0].end ? 0 : (i < jobs.job[1].end ? 1 : 2);
+    int which = 0;
+    while (i >= jobs.job[which].end) ++which;
     const SliceJob& b = jobs.job[which];
     const int64_t local = i - (which ? jobs.job[which - 1].end : 0);
     const int per = (b.N + 3) / 4;
@@ -580,8 +692,8 @@ FfnBlockLayout ffn_block_layout(const moe_ffn& f, bool training) {
       const int64_t tiles = static_cast<int64_t>(dp / 128) * (hp / 128);
       L.splits_gu = slices(f.tokens, 2 * tiles);
       L.splits_d = slices(f.tokens, tiles);
-      L.part_gu = take(static_cast<size_t>(L.splits_gu) * 2 * dp * hp * sizeof(float));
-      L.part_d = take(static_cast<size_t>(L.splits_d) * dp * hp * sizeof(float));
+      L.part_gu = take(L.splits_gu > 1 ? static_cast<size_t>(L.splits_gu) * 2 * dp * hp * sizeof(float) : 0);
+      L.part_d = take(L.splits_d > 1 ? static_cast<size_t>(L.splits_d) * dp * hp * sizeof(float) : 0);
     } else {
       const size_t tp = pad128(f.tokens);
       L.xt = take(d * tp * es);
@@ -838,6 +950,23 @@ hipError_t ffn_fwd_t(const moe_ffn& f, const void* x, const void* wg, const void
   return hipGetLastError();
 }
 
+template <typename G>
+void grad_direct(const char* name, const void* a, int64_t lda, const void* b, int64_t ldb, int64_t mp,
+                 int64_t np, int64_t rows, int M, int N, int64_t half, void* out, void* out2,
+                 const void* zero, hipStream_t s) {
+  GradDirect p{static_cast<const bf16_t*>(a), static_cast<const bf16_t*>(b), lda, ldb, rows, 0,
+               static_cast<int>(np / 128), M, N, static_cast<int>(half), out, out2};
+  // as wgrad_tr: 256-row tiles where they divide and still give every CU one
+  const bool tall = mp % 256 == 0 && mp / 256 * (np / 128) >= kCUs;
+  p.tiles_m = static_cast<int>(mp / (tall ? 256 : 128));
+  const dim3 grid(p.tiles_m * p.tiles_n);
+  const bf16_t* z = static_cast<const bf16_t*>(zero);
+  if (tall)
+    MOE_LAUNCH(name, (grad_direct_kernel<TrCfg<256, 3>, G>), grid, dim3(512), 0, s, p, z);
+  else
+    MOE_LAUNCH(name, (grad_direct_kernel<TrCfg<128, 4>, G>), grid, dim3(256), 0, s, p, z);
+}
+
 template <typename Cfg, int kMode>
 void launch_grad(GradArgs& a, int parts, hipStream_t s) {
   int64_t tiles = 0;
@@ -908,18 +1037,27 @@ hipError_t ffn_bwd_t(const moe_ffn& f, const void* x, const void* wg, const void
   float* dn = reinterpret_cast<float*>(W + L.part_d);
   SliceJobs jobs{};
   int64_t end = 0;
-  auto job = [&](int i, const float* part, int splits, int64_t stride, int64_t ld, int M, int N, void* out) {
+  auto job = [&](const float* part, int splits, int64_t stride, int64_t ld, int M, int N, void* out) {
     end += static_cast<int64_t>(M) * ((N + 3) / 4);
-    jobs.job[i] = SliceJob{part, splits, stride, ld, M, N, out, end};
+    jobs.job[jobs.n++] = SliceJob{part, splits, stride, ld, M, N, out, end};
   };
   if constexpr (std::is_same<T, bf16_t>::value) {
-    grad_slices<T>("ffn_bwd_wgrad_gate_up", xp, dp, W + L.dab, 2 * hp, dp, 2 * hp, tok, L.splits_gu, gu,
-                   SV + S.zero, s);
-    grad_slices<T>("ffn_bwd_wgrad_down", SV + S.h, hp, dyp, dp, hp, dp, tok, L.splits_d, dn,
-                   SV + S.zero, s);
-    job(0, gu, L.splits_gu, 2 * dp * hp, 2 * hp, d, h, dwg);
-    job(1, gu + hp, L.splits_gu, 2 * dp * hp, 2 * hp, d, h, dwu);
-    job(2, dn, L.splits_d, dp * hp, dp, h, d, dwd);
+    const void* zero = SV + S.zero;
+    if (L.splits_gu == 1) {
+      grad_direct<G>("ffn_bwd_wgrad_gate_up", xp, dp, W + L.dab, 2 * hp, dp, 2 * hp, tok, d, h, hp, dwg,
+                     dwu, zero, s);
+    } else {
+      grad_slices<T>("ffn_bwd_wgrad_gate_up", xp, dp, W + L.dab, 2 * hp, dp, 2 * hp, tok, L.splits_gu,
+                     gu, zero, s);
+      job(gu, L.splits_gu, 2 * dp * hp, 2 * hp, d, h, dwg);
+      job(gu + hp, L.splits_gu, 2 * dp * hp, 2 * hp, d, h, dwu);
+    }
+    if (L.splits_d == 1) {
+      grad_direct<G>("ffn_bwd_wgrad_down", SV + S.h, hp, dyp, dp, hp, dp, tok, h, d, dp, dwd, dwd, zero, s);
+    } else {
+      grad_slices<T>("ffn_bwd_wgrad_down", SV + S.h, hp, dyp, dp, hp, dp, tok, L.splits_d, dn, zero, s);
+      job(dn, L.splits_d, dp * hp, dp, h, d, dwd);
+    }
   } else {
     // fp32 has no transposing LDS read: the operands are turned (their bytes
     // are little beside fp32 MFMAs) and the gradients are plain products,
@@ -941,7 +1079,7 @@ hipError_t ffn_bwd_t(const moe_ffn& f, const void* x, const void* wg, const void
       a.p[i].parts = parts;
       a.o[i].c = parts > 1 ? sums : out;
       a.o[i].ldc = parts > 1 ? ld : N;
-      if (parts > 1) job(i, sums, parts, M * ld, ld, M, N, out);
+      if (parts > 1) job(sums, parts, M * ld, ld, M, N, out);
     };
     const char* dabt = W + L.dabt;
     grad(0, W + L.xt, dabt, d, h, dwg, gu, h4);
@@ -950,9 +1088,9 @@ hipError_t ffn_bwd_t(const moe_ffn& f, const void* x, const void* wg, const void
     if (parts > 1) launch_grad<MmSmall, kPart>(a, parts, s);
     else if (grad_tiles(f, 128) >= kCUs) launch_grad<MmMid, kPlain>(a, 1, s);
     else launch_grad<MmSmall, kPlain>(a, 1, s);
-    if (parts == 1) return hipGetLastError();
   }
-  MOE_LAUNCH("ffn_slice_sum", slice_sum_kernel<G>, dim3(blocks_for(end)), dim3(256), 0, s, jobs);
+  if (jobs.n)
+    MOE_LAUNCH("ffn_slice_sum", slice_sum_kernel<G>, dim3(blocks_for(end)), dim3(256), 0, s, jobs);
   return hipGetLastError();
 }
 
