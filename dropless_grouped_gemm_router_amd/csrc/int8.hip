@@ -263,7 +263,10 @@ void i8_tile_kernel(const MmArgs p, const I8Out o) {
 // workgroup takes 16 output columns (paired: 16 gate and the 16 up rows) and
 // its eight waves share K. Rows that are not yet integers are quantised into
 // LDS by every workgroup for itself while its first weights are on their way:
-// one launch instead of two, and the rows come from L2.
+// one launch instead of two, and the rows come from L2. 4 rows of 4096 through
+// 4096 x 4096 weights (16.8 MB): 9.2 us against 20 with 32 x 64 tiles; what is
+// left above the bytes' 3.5 us is the launch, the rows' two passes and the
+// sum over the waves.
 constexpr int kRowsWaves = 8, kRowsBatch = 4;
 
 struct I8Few {

