@@ -9,7 +9,8 @@
 // Wd^T and the activation's gradient. The weights come [d][h] and [h][d]:
 // the forward's products run over their leading dimension, so they are
 // turned K-contiguous into the workspace first; the backward's data
-// gradients read them as they are. The weight gradients reduce over tokens,
+// gradients read them as they are. In bf16, few tokens and widths in multiples
+// of 64 the forward does so too (in_place). The weight gradients reduce over tokens,
 // in slices whose partial sums are added in a fixed order.
 //
 // Widths that are no multiple of 128 take zero-padded copies of the operands
@@ -29,8 +30,13 @@ namespace moe {
 
 namespace {
 
-// Tokens up to which inference takes the serving form.
-constexpr int64_t kFewRows = 128;
+// Tokens up to which the forward takes the serving form: the second where the
+// other choice is to turn the weights, the first where it is tiles that read
+// them in place (the shapes of in_place). The serving form and those tiles
+// take, bf16, 16 tokens, 2048 x 8192: 25.0 and 27.8 us, 1024 x 4096: 14.1 and
+// 13.4; 32 tokens: 29.3 and 28.5, 18.1 and 14.0; 128 tokens: 59.4 and 37.4,
+// 23.3 and 19.5; 512 x 1024: 15.1 and 11.8.
+constexpr int64_t kFewRowsInPlace = 16, kFewRows = 128;
 constexpr int64_t kCUs = 256;
 
 constexpr int64_t pad128(int64_t v) { return (v + 127) / 128 * 128; }
@@ -166,6 +172,7 @@ struct FfnOut {
   uint8_t* low;
   int64_t ld;    // columns kept of the hidden matrices (a multiple of 128)
   void* dab;     // gradient: da and db, a row of each side by side
+  u32x4* zero;   // null, or a zero row that kTurned tiles write (else turn_kernel does)
 };
 
 // What is kept of eight values of f and p. The bits below the 20th are cut
@@ -309,13 +316,15 @@ struct FfnRows {
   }
 };
 
-template <typename T, typename Cfg, int kMode, int kAct>
+template <typename T, typename Cfg, int kMode, int kAct, bool kTurned>
 __global__ __launch_bounds__(Cfg::NT) __attribute__((amdgpu_waves_per_eu(Cfg::WPE)))
 void ffn_tile_kernel(const MmArgs p, const FfnOut o) {
   __shared__ __attribute__((aligned(1024))) char smem[MmStrip<Cfg>::LDS];
   f32x16_t acc[Cfg::WM][Cfg::WN];
   MmTile t;
   constexpr bool kPaired = kMode == kGated;
+  if (kTurned && o.zero && blockIdx.x == 0 && threadIdx.x < kTrZeroBytes / 16)
+    o.zero[threadIdx.x] = (u32x4){0u, 0u, 0u, 0u};
   if (!mm_find<Cfg>(p, &t)) return;
   constexpr int kCols = kPaired ? Cfg::BN / 2 : Cfg::BN;
   auto go = [&](auto full) {
@@ -323,7 +332,7 @@ void ffn_tile_kernel(const MmArgs p, const FfnOut o) {
     mm_begin<Cfg, kPaired>(t.rows, rows);
     mm_drain<Cfg, kPaired>(smem, acc, t.rows, rows);
   };
-  mm_tile<typename OpOf<T>::type, Cfg, kPaired>(p, smem, t, acc);
+  mm_tile<typename OpOf<T>::type, Cfg, kPaired, kTurned>(p, smem, t, acc);
   if ((t.nt + 1) * kCols <= p.N) go(std::true_type{});
   else go(std::false_type{});
 }
@@ -620,6 +629,7 @@ __global__ __launch_bounds__(256) void zero_kernel(G* __restrict__ p, int64_t n)
 
 int parts_of(size_t elem, int64_t M, int64_t N, int64_t stages);
 int grad_parts(const moe_ffn& f);
+bool in_place(const moe_ffn& f);
 
 struct FfnBlockLayout {
   // forward workspace: turned weights, padded x, hidden values (inference)
@@ -645,7 +655,7 @@ int slices(int64_t rows, int64_t tiles) {
 int rows_tile(const moe_ffn& f) { return f.tokens <= 16 || f.dtype != MOE_BF16 ? 1 : 2; }
 // Whether the forward takes the serving form (training too: what it keeps is
 // the same, and the weights are not turned).
-bool few_rows(const moe_ffn& f) { return f.tokens <= kFewRows; }
+bool few_rows(const moe_ffn& f) { return f.tokens <= (in_place(f) ? kFewRowsInPlace : kFewRows); }
 
 FfnBlockLayout ffn_block_layout(const moe_ffn& f, bool training) {
   FfnBlockLayout L{};
@@ -672,7 +682,7 @@ FfnBlockLayout ffn_block_layout(const moe_ffn& f, bool training) {
   }
   L.xp = take(d == dp ? 0 : T * dp * es);
   const size_t start = o;
-  if (!few_rows(f)) {
+  if (!few_rows(f) && !in_place(f)) {
     L.tg = take(h * dp * es);
     L.tu = take(h * dp * es);
     L.td = take(d * hp * es);
@@ -739,7 +749,7 @@ FfnOut saved_out(const SavedLayout& S, char* saved, int64_t hp) {
 
 // ----------------------------------------------------------------- launches
 
-template <typename T, typename Cfg, int kMode, int kAct>
+template <typename T, typename Cfg, int kMode, int kAct, bool kTurned = false>
 void tiles_at(const char* name, const MmArgs& a, const FfnOut& o, hipStream_t s) {
   MmArgs p = a;
   const int per = kMode == kGated ? Cfg::BN / 2 : Cfg::BN;
@@ -749,7 +759,7 @@ void tiles_at(const char* name, const MmArgs& a, const FfnOut& o, hipStream_t s)
   p.nk *= 128 / Cfg::ROW;
   p.k_split *= 128 / Cfg::ROW;
   const int64_t grid = (p.M + Cfg::BM - 1) / Cfg::BM * p.tiles_n * (p.parts > 1 ? p.parts : 1);
-  MOE_LAUNCH(name, (ffn_tile_kernel<T, Cfg, kMode, kAct>), dim3(static_cast<unsigned>(grid)),
+  MOE_LAUNCH(name, (ffn_tile_kernel<T, Cfg, kMode, kAct, kTurned>), dim3(static_cast<unsigned>(grid)),
              dim3(Cfg::NT), 0, s, p, o);
 }
 
@@ -779,8 +789,23 @@ int parts_of(size_t elem, int64_t M, int64_t N, int64_t stages) {
   return static_cast<int>(k < 1 ? 1 : (k > 16 ? 16 : k));
 }
 
+// Whether the forward's tiles read the weights where they are (mm_tile,
+// kTurned): bf16, both products in 64 x 64 tiles, widths that fill stages.
+// Those are few tokens, for which turning the weights costs as much as a
+// product. Turned first and in place, 300 tokens, 1024 x 4096: 35.1 and 28.4
+// us; 200 tokens, 2048 x 2048: 39.6 and 24.4; 2000 tokens, 512 x 512: 17.1
+// and 12.6.
+bool in_place(const moe_ffn& f) {
+  if (f.dtype != MOE_BF16 || f.d_model % 64 || f.d_hidden % 64) return false;
+  return tile_of(2, f.tokens, 2 * static_cast<int64_t>(f.d_hidden), f.d_model / 64) == kSmall &&
+         tile_of(2, f.tokens, f.d_model, f.d_hidden / 64) == kSmall;
+}
+
 template <typename T, int kMode, int kAct>
-void tiles(const char* name, const MmArgs& p, const FfnOut& o, hipStream_t s) {
+void tiles(const char* name, const MmArgs& p, const FfnOut& o, hipStream_t s, bool turned = false) {
+  if constexpr (sizeof(T) == 2 && (kMode == kPlain || kMode == kGated)) {
+    if (turned) return tiles_at<T, MmTurned, kMode, kAct, true>(name, p, o, s);
+  }
   const int64_t cols = kMode == kGated ? 2 * static_cast<int64_t>(p.N) : p.N;
   switch (tile_of(sizeof(T), p.M, cols, p.nk)) {
     case kSmall: return tiles_at<T, MmSmall, kMode, kAct>(name, p, o, s);
@@ -808,29 +833,32 @@ int grad_parts(const moe_ffn& f) {
 // A plain product [M][N], over slices of K (sums in `part`) where it has few
 // tiles.
 template <typename T>
-void product(const char* name, const MmArgs& a, void* out, float* part, hipStream_t s) {
+void product(const char* name, const MmArgs& a, void* out, float* part, hipStream_t s, bool turned = false) {
   MmArgs p = a;
   FfnOut o{};
   o.ldc = p.N;
   p.parts = parts_of(sizeof(T), p.M, p.N, p.nk);
   if (p.parts == 1) {
     o.c = out;
-    return tiles<T, kPlain, 0>(name, p, o, s);
+    return tiles<T, kPlain, 0>(name, p, o, s, turned);
   }
   o.c = part;
-  tiles_at<T, MmSmall, kPart, 0>(name, p, o, s);
+  if constexpr (sizeof(T) == 2) {
+    if (turned) tiles_at<T, MmTurned, kPart, 0, true>(name, p, o, s);
+  }
+  if (!turned) tiles_at<T, MmSmall, kPart, 0>(name, p, o, s);
   const int64_t cells = p.M * p.N;
   MOE_LAUNCH("ffn_join", join_kernel<T>, dim3(static_cast<unsigned>((cells + 255) / 256)), dim3(256), 0, s,
              part, p.parts, cells, static_cast<T*>(out));
 }
 
 template <typename T, int kMode>
-void tiles_act(const char* name, int act, const MmArgs& p, const FfnOut& o, hipStream_t s) {
+void tiles_act(const char* name, int act, const MmArgs& p, const FfnOut& o, hipStream_t s, bool turned) {
   switch (act) {
-    case MOE_ACT_SILU: return tiles<T, kMode, MOE_ACT_SILU>(name, p, o, s);
-    case MOE_ACT_GELU: return tiles<T, kMode, MOE_ACT_GELU>(name, p, o, s);
-    case MOE_ACT_GELU_TANH: return tiles<T, kMode, MOE_ACT_GELU_TANH>(name, p, o, s);
-    default: return tiles<T, kMode, MOE_ACT_RELU>(name, p, o, s);
+    case MOE_ACT_SILU: return tiles<T, kMode, MOE_ACT_SILU>(name, p, o, s, turned);
+    case MOE_ACT_GELU: return tiles<T, kMode, MOE_ACT_GELU>(name, p, o, s, turned);
+    case MOE_ACT_GELU_TANH: return tiles<T, kMode, MOE_ACT_GELU_TANH>(name, p, o, s, turned);
+    default: return tiles<T, kMode, MOE_ACT_RELU>(name, p, o, s, turned);
   }
 }
 
@@ -933,24 +961,34 @@ hipError_t ffn_fwd_t(const moe_ffn& f, const void* x, const void* wg, const void
   char *W = static_cast<char*>(ws), *SV = static_cast<char*>(saved);
   const int d = f.d_model, h = f.d_hidden;
   const int64_t dp = pad128(d), hp = pad128(h);
-  TurnJobs jobs{};
-  jobs.zero = SV ? reinterpret_cast<u32x4*>(SV + S.zero) : nullptr;
-  jobs.add(wg, W + L.tg, d, h, h);
-  jobs.add(wu, W + L.tu, d, h, h);
-  jobs.add(wd, W + L.td, h, d, d);
-  turn<T>("ffn_turn_weights", jobs, s);
-  PadJobs pads{};
-  const void* xp = padded<T>(pads, x, W + L.xp, f.tokens, d);
-  pad<T>(pads, s);
-  MmArgs p = rows_of<T>(xp, dp, W + L.tg, dp, f.tokens, h, dp);
-  p.half = static_cast<int64_t>(L.tu) - static_cast<int64_t>(L.tg);
+  u32x4* zero = SV ? reinterpret_cast<u32x4*>(SV + S.zero) : nullptr;
+  const bool there = in_place(f);  // the weights stay there
+  MmArgs p;
+  if (there) {
+    p = rows_of<T>(x, d, wg, h, f.tokens, h, d);
+    p.half = static_cast<const char*>(wu) - static_cast<const char*>(wg);
+  } else {
+    TurnJobs jobs{};
+    jobs.zero = zero;
+    jobs.add(wg, W + L.tg, d, h, h);
+    jobs.add(wu, W + L.tu, d, h, h);
+    jobs.add(wd, W + L.td, h, d, d);
+    turn<T>("ffn_turn_weights", jobs, s);
+    PadJobs pads{};
+    const void* xp = padded<T>(pads, x, W + L.xp, f.tokens, d);
+    pad<T>(pads, s);
+    p = rows_of<T>(xp, dp, W + L.tg, dp, f.tokens, h, dp);
+    p.half = static_cast<int64_t>(L.tu) - static_cast<int64_t>(L.tg);
+  }
   FfnOut o{};
   if (SV) o = saved_out(S, SV, hp);
   else o.h = W + L.h;
   o.ld = hp;
-  tiles_act<T, kGated>("ffn_gate_up", f.act, p, o, s);
-  MmArgs q = rows_of<T>(o.h, hp, W + L.td, hp, f.tokens, d, hp);
-  product<T>("ffn_down", q, out, reinterpret_cast<float*>(W + L.k_sums), s);
+  if (there) o.zero = zero;
+  tiles_act<T, kGated>("ffn_gate_up", f.act, p, o, s, there);
+  MmArgs q = there ? rows_of<T>(o.h, hp, wd, d, f.tokens, d, h)
+                   : rows_of<T>(o.h, hp, W + L.td, hp, f.tokens, d, hp);
+  product<T>("ffn_down", q, out, reinterpret_cast<float*>(W + L.k_sums), s, there);
   return hipGetLastError();
 }
 

@@ -16,7 +16,8 @@
 // times 33.5 MB): 23 to 30 us, 3.4 to 4.4 TB/s; turning them for the tiles
 // first takes 37 us alone. From about 130 rows on the weights' repeated way
 // through L2 costs more than the turning (300 rows, 1024 x 4096: 66 us against
-// 34).
+// 34), and from 17 on more than tiles that need no turning (gated_ffn.hip,
+// kFewRowsInPlace).
 #pragma once
 
 #include "block.h"

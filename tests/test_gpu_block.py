@@ -230,6 +230,29 @@ def test_ffn(t, d, h, dtype):
         near(name, buf.grads[name], g, 5 * u)
 
 
+@pytest.mark.parametrize("act", ["silu", "relu"])
+@pytest.mark.parametrize("t,d,h", [(17, 64, 64), (40, 2048, 512), (129, 64, 192), (200, 192, 320), (257, 1024, 4096),
+                                   (300, 512, 64), (1000, 128, 512), (384, 1088, 576)])
+def test_ffn_weights_in_place(t, d, h, act):
+    """More tokens than the serving form is for, in widths that are multiples
+    of 64 but not all of 128: the forward multiplies by the weights where they are."""
+    note(f"ffn in place {t} {d} {h} {act}")
+    f, x, w, dy, buf = ffn_case(t, d, h, "bf16", act)
+    before = [v.clone() for v in w.values()]
+    K.gated_ffn(f, x, w, buf)
+    infer = buf.out.clone()
+    K.gated_ffn(f, x, w, buf, training=True)
+    K.gated_ffn_backward(f, x, w, dy, buf)
+    y, grads = ffn64(x, w, dy, act)
+    u = U["bf16"]
+    near("inference", infer, y, 2 * u)
+    near("out", buf.out, y, 2 * u)
+    near("grad_x", buf.grad_x, grads[0], 5 * u)
+    for name, g in zip(("w_gate", "w_up", "w_down"), grads[1:]):
+        near(name, buf.grads[name], g, 5 * u)
+    assert all(bool((a == b).all()) for a, b in zip(before, w.values()))
+
+
 @pytest.mark.parametrize("act", ["gelu", "gelu_tanh", "relu"])
 @pytest.mark.parametrize("t,d,h,dtype,grad", [(7, 128, 256, "bf16", "bf16"), (300, 256, 385, "bf16", "bf16"),
                                               (150, 100, 200, "fp32", "fp32")])
