@@ -1,9 +1,12 @@
 // Products with weights in 8-bit integers: y = (q_x q_w^T) s_x s_w.
 //
-// The token's scale is its largest magnitude over 127, its integers x / s
-// rounded to nearest even; both divisions are exact fp32 divisions, so the
-// integers are the same on every machine and in every path below. Sums of
-// products are exact int32 (65536 products of 127 * 128 stay under 2^31).
+// The token's scale is its largest magnitude times 1 / 127 in fp32, its
+// integers x / s in an exact fp32 division, rounded to nearest even. The
+// product, not the division by 127 (5% of the rows differ in the scale's last
+// bit): it is what torch computes on this device for a tensor over a number,
+// so weights and inputs quantised by that expression are the same integers
+// as in every path below. Sums of products are exact int32 (65536 products
+// of 127 * 128 stay under 2^31).
 #include "mm.h"
 
 namespace moe {
@@ -30,7 +33,7 @@ __device__ __forceinline__ uint32_t wave_umax(uint32_t v) {
 // Magnitudes are compared as bit patterns: infinities and NaN are then
 // larger than every number, and a row that holds one is seen.
 __device__ __forceinline__ float scale_of(uint32_t most) {
-  return most >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : __uint_as_float(most) / 127.0f;
+  return most >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : __uint_as_float(most) * (1.0f / 127.0f);
 }
 // rint(v / scale), by the scale's reciprocal where that cannot differ: v inv
 // is within 127 * 2^-23 of the quotient and the rounded quotient within

@@ -144,9 +144,10 @@ int64_t moe_i8_pitch(int32_t width);
 /*
  * Rows of x [rows, width] (dtype fp32 or bf16; ld_x elements between rows, 0:
  * width) in 8 bits with a scale each:
- *   scale[t] = max_j |x[t,j]| / 127,  q[t,j] = rint(x[t,j] / scale[t])
- * both fp32 divisions rounded to nearest, rint to nearest even, clamped to
- * [-127, 127]. A zero row has scale 0 and q 0; a row with an infinity or a
+ *   scale[t] = max_j |x[t,j]| * (1 / 127),  q[t,j] = rint(x[t,j] / scale[t])
+ * in fp32, 1 / 127 a number of fp32 and the division rounded to nearest, rint
+ * to nearest even, clamped to [-127, 127]: what torch makes on this device of
+ * scale = x.abs().amax(1) / 127, q = round(x / scale). A zero row has scale 0 and q 0; a row with an infinity or a
  * NaN has scale NaN and q 0, so that whatever is made of it is NaN. q is
  * [rows, moe_i8_pitch(width)], its padding zeroed. It is the layout of
  * activations and, with a row for each output channel, of weights.

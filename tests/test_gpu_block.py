@@ -347,11 +347,11 @@ def test_ffn_odd_values_and_zero_tokens(t):
 # ------------------------------------------------- products in 8-bit integers
 
 def quantized(x):
-    """The definition with numpy's fp32 divisions: (q int64, scale fp32)."""
+    """The definition in numpy's fp32: (q int64, scale fp32)."""
     x = x.float().cpu().numpy()
     bad = ~np.isfinite(x).all(1)
     with np.errstate(all="ignore"):
-        scale = np.abs(x).max(1) / np.float32(127)
+        scale = np.abs(x).max(1) * np.float32(1 / 127)
         q = np.clip(np.round(x / np.where(scale > 0, scale, 1).astype(np.float32)[:, None]), -127, 127)
     q[bad] = 0
     scale[bad] = np.nan
@@ -376,6 +376,10 @@ def test_quantize_rows(rows, width, dtype):
     assert np.array_equal(s.cpu().numpy(), sw, equal_nan=True)
     assert np.array_equal(q[:, :width].cpu().numpy(), qw)
     assert not q[:, width:].any()
+    ts = x.float().abs().amax(1) / 127.0  # the same expression in torch
+    assert torch.equal(s[3:], ts[3:])
+    if rows > 3:
+        assert torch.equal(q[3:, :width].float(), torch.round(x[3:].float() / ts[3:, None]))
     # rows that lie apart
     wide = torch.cat([x, x], 1)[:, 1:1 + width]
     q2, s2 = K.quantize_rows(wide)
