@@ -260,8 +260,8 @@ void i8_tile_kernel(const MmArgs p, const I8Out o) {
 
 // ------------------------------------------------------------------ few rows
 //
-// Serving form, up to 16 rows of a group at a time: the weights' bytes are
-// the cost, so they go from memory straight into the operand of mfma
+// Serving form, up to 16 rows of a dense product: the weights' bytes are the
+// cost, so they go from memory straight into the operand of mfma
 // 16x16x64 (a lane's 16 bytes of one weight row) and are read once. A
 // workgroup takes 16 output columns (paired: 16 gate and the 16 up rows) and
 // its eight waves share K. Rows that are not yet integers are quantised into
@@ -277,13 +277,9 @@ struct I8Few {
   int64_t ldx;            // elements between rows
   const float* xs;        // int8 input: scales
   const int8_t* w;
-  int64_t pitch, group;   // bytes between weight rows, groups
+  int64_t pitch;          // bytes between weight rows
   int width;              // elements of an input row
-  const int32_t* perm;
-  int topk;
-  const int32_t* offsets;
-  int cap;
-  int64_t M;
+  int rows;               // 1 to 16
   int N;                  // columns of y
 };
 
@@ -291,120 +287,105 @@ template <typename T, typename X, bool kPaired>
 __global__ __launch_bounds__(64 * kRowsWaves) void i8_few_kernel(const I8Few p, const I8Out o) {
   constexpr int kW = kPaired ? 2 : 1;
   constexpr bool kInt = sizeof(X) == 1;
-  extern __shared__ __attribute__((aligned(16))) char rows_q[];  // [min(16, M)][pitch + 16], unless kInt
+  extern __shared__ __attribute__((aligned(16))) char rows_q[];  // [rows][pitch + 16], unless kInt
   __shared__ float scale[16];
   __shared__ int sums[kRowsWaves][kW][16 * 16];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int g = blockIdx.y;
-  int64_t first = 0, last = p.M;
-  if (p.offsets) {
-    first = p.offsets[g];
-    last = p.offsets[g + 1];
-    if (p.cap > 0 && last - first > p.cap) last = first + p.cap;
-  }
   const int n0 = blockIdx.x * 16;
   const int8_t* w[kW];
 #pragma unroll
   for (int m = 0; m < kW; ++m)
-    w[m] = p.w + g * p.group + (min(n0 + (lane & 15), p.N - 1) + static_cast<int64_t>(m) * p.N) * p.pitch +
+    w[m] = p.w + (min(n0 + (lane & 15), p.N - 1) + static_cast<int64_t>(m) * p.N) * p.pitch +
            16 * (lane >> 4);
   const int steps = static_cast<int>(p.pitch / 64);
   const int q_pitch = static_cast<int>(p.pitch) + 16;  // rows of 16 banks apart
 
-  for (int64_t r0 = first; r0 < last; r0 += 16) {
-    const int rows = last - r0 < 16 ? static_cast<int>(last - r0) : 16;
-    // the input row behind this lane's token (the last one again past the end)
-    auto input = [&](int t) {
-      const int64_t r = r0 + min(t, rows - 1);
-      return p.perm ? static_cast<int64_t>(p.perm[r] / p.topk) : r;
-    };
-    u32x4 wv[2][kRowsBatch][kW], xv[2][kInt ? kRowsBatch : 1];
-    const int8_t* xi = kInt ? static_cast<const int8_t*>(p.x) + input(lane & 15) * p.ldx + 16 * (lane >> 4) : nullptr;
-    auto load = [&](int set, int s) {
+  u32x4 wv[2][kRowsBatch][kW], xv[2][kInt ? kRowsBatch : 1];
+  // the input row behind this lane's token (the last one again past the end)
+  const int mine = min(lane & 15, p.rows - 1);
+  const int8_t* xi = kInt ? static_cast<const int8_t*>(p.x) + mine * p.ldx + 16 * (lane >> 4) : nullptr;
+  auto load = [&](int set, int s) {
 #pragma unroll
-      for (int u = 0; u < kRowsBatch; ++u) {
-        const int64_t at = static_cast<int64_t>(min(s + u * kRowsWaves, steps - 1)) * 64;
+    for (int u = 0; u < kRowsBatch; ++u) {
+      const int64_t at = static_cast<int64_t>(min(s + u * kRowsWaves, steps - 1)) * 64;
 #pragma unroll
-        for (int m = 0; m < kW; ++m) wv[set][u][m] = *reinterpret_cast<const u32x4*>(w[m] + at);
-        if (kInt) xv[set][u] = *reinterpret_cast<const u32x4*>(xi + at);
-      }
-    };
-    int s = wave;
-    load(0, s);
-    load(1, s + kRowsBatch * kRowsWaves);
-    if constexpr (!kInt) {
-      constexpr int V = Piece<X>::V;
-      for (int t = wave; t < rows; t += kRowsWaves) {
-        const X* row = static_cast<const X*>(p.x) + input(t) * p.ldx;
-        uint32_t most = 0;
-#pragma unroll 4
-        for (int c = lane * V; c < p.width; c += 64 * V) {
-          float f[V];
-          Piece<X>::widen(load_piece(row, c, p.width), f);
-#pragma unroll
-          for (int e = 0; e < V; ++e) most = max(most, __float_as_uint(f[e]) & 0x7fffffffu);
-        }
-        const float sc = scale_of(wave_umax(most));
-        if (lane == 0) scale[t] = sc;
-        const Quantizer quantize(sc);
-#pragma unroll 4
-        for (int c = lane * V; c < p.pitch; c += 64 * V) {
-          float f[V];
-          Piece<X>::widen(load_piece(row, c, p.width), f);
-          store_q<V>(reinterpret_cast<int8_t*>(rows_q) + t * q_pitch + c, f, quantize);
-        }
-      }
-      __syncthreads();
+      for (int m = 0; m < kW; ++m) wv[set][u][m] = *reinterpret_cast<const u32x4*>(w[m] + at);
+      if (kInt) xv[set][u] = *reinterpret_cast<const u32x4*>(xi + at);
     }
-    i32x4 acc[kW];
+  };
+  int s = wave;
+  load(0, s);
+  load(1, s + kRowsBatch * kRowsWaves);
+  if constexpr (!kInt) {
+    constexpr int V = Piece<X>::V;
+    for (int t = wave; t < p.rows; t += kRowsWaves) {
+      const X* row = static_cast<const X*>(p.x) + t * p.ldx;
+      uint32_t most = 0;
+#pragma unroll 4
+      for (int c = lane * V; c < p.width; c += 64 * V) {
+        float f[V];
+        Piece<X>::widen(load_piece(row, c, p.width), f);
 #pragma unroll
-    for (int m = 0; m < kW; ++m) acc[m] = (i32x4){0, 0, 0, 0};
-    const char* xl = rows_q + min(lane & 15, rows - 1) * q_pitch + 16 * (lane >> 4);
-    auto multiply = [&](int set, int s) {
-#pragma unroll
-      for (int u = 0; u < kRowsBatch; ++u) {
-        const int st = s + u * kRowsWaves;
-        if (st >= steps) break;
-        u32x4 x;
-        if (kInt) x = xv[set][kInt ? u : 0];
-        else x = *reinterpret_cast<const u32x4*>(xl + st * 64);
-#pragma unroll
-        for (int m = 0; m < kW; ++m)
-          acc[m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, wv[set][u][m]),
-                                                         __builtin_bit_cast(i32x4, x), acc[m], 0, 0, 0);
+        for (int e = 0; e < V; ++e) most = max(most, __float_as_uint(f[e]) & 0x7fffffffu);
       }
-    };
-    constexpr int kSpan = kRowsBatch * kRowsWaves;
-    for (; s < steps; s += 2 * kSpan) {
-      multiply(0, s);
-      if (s + 2 * kSpan < steps) load(0, s + 2 * kSpan);
-      multiply(1, s + kSpan);
-      if (s + 3 * kSpan < steps) load(1, s + 3 * kSpan);
-    }
-    // lane L holds token L % 16 and columns 4 (L / 16) .. + 3
-#pragma unroll
-    for (int m = 0; m < kW; ++m)
-      *reinterpret_cast<i32x4*>(&sums[wave][m][(lane & 15) * 16 + 4 * (lane >> 4)]) = acc[m];
-    __syncthreads();
-    if (threadIdx.x < 256) {
-      const int t = threadIdx.x >> 4, n = n0 + (threadIdx.x & 15);
-      int v[kW];
-#pragma unroll
-      for (int m = 0; m < kW; ++m) {
-        v[m] = 0;
-#pragma unroll
-        for (int u = 0; u < kRowsWaves; ++u) v[m] += sums[u][m][threadIdx.x];
-      }
-      if (t < rows && n < p.N) {
-        const float xs = kInt ? o.xs[input(t)] : scale[t];
-        const float* ws = o.ws + static_cast<int64_t>(g) * o.outputs;
-        float y = static_cast<float>(v[0]) * xs * ws[n];
-        if (kPaired) y = silu_f(y) * (static_cast<float>(v[kW - 1]) * xs * ws[p.N + n]);
-        else y += o.bias ? o.bias[n] : 0.0f;
-        put(static_cast<T*>(o.y) + (r0 + t) * o.ld + n, y);
+      const float sc = scale_of(wave_umax(most));
+      if (lane == 0) scale[t] = sc;
+      const Quantizer quantize(sc);
+#pragma unroll 4
+      for (int c = lane * V; c < p.pitch; c += 64 * V) {
+        float f[V];
+        Piece<X>::widen(load_piece(row, c, p.width), f);
+        store_q<V>(reinterpret_cast<int8_t*>(rows_q) + t * q_pitch + c, f, quantize);
       }
     }
     __syncthreads();
+  }
+  i32x4 acc[kW];
+#pragma unroll
+  for (int m = 0; m < kW; ++m) acc[m] = (i32x4){0, 0, 0, 0};
+  const char* xl = rows_q + mine * q_pitch + 16 * (lane >> 4);
+  auto multiply = [&](int set, int s) {
+#pragma unroll
+    for (int u = 0; u < kRowsBatch; ++u) {
+      const int st = s + u * kRowsWaves;
+      if (st >= steps) break;
+      u32x4 x;
+      if (kInt) x = xv[set][kInt ? u : 0];
+      else x = *reinterpret_cast<const u32x4*>(xl + st * 64);
+#pragma unroll
+      for (int m = 0; m < kW; ++m)
+        acc[m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, wv[set][u][m]),
+                                                       __builtin_bit_cast(i32x4, x), acc[m], 0, 0, 0);
+    }
+  };
+  constexpr int kSpan = kRowsBatch * kRowsWaves;
+  for (; s < steps; s += 2 * kSpan) {
+    multiply(0, s);
+    if (s + 2 * kSpan < steps) load(0, s + 2 * kSpan);
+    multiply(1, s + kSpan);
+    if (s + 3 * kSpan < steps) load(1, s + 3 * kSpan);
+  }
+  // lane L holds token L % 16 and columns 4 (L / 16) .. + 3
+#pragma unroll
+  for (int m = 0; m < kW; ++m)
+    *reinterpret_cast<i32x4*>(&sums[wave][m][(lane & 15) * 16 + 4 * (lane >> 4)]) = acc[m];
+  __syncthreads();
+  if (threadIdx.x < 256) {
+    const int t = threadIdx.x >> 4, n = n0 + (threadIdx.x & 15);
+    int v[kW];
+#pragma unroll
+    for (int m = 0; m < kW; ++m) {
+      v[m] = 0;
+#pragma unroll
+      for (int u = 0; u < kRowsWaves; ++u) v[m] += sums[u][m][threadIdx.x];
+    }
+    if (t < p.rows && n < p.N) {
+      const float xs = kInt ? o.xs[t] : scale[t];
+      float y = static_cast<float>(v[0]) * xs * o.ws[n];
+      if (kPaired) y = silu_f(y) * (static_cast<float>(v[kW - 1]) * xs * o.ws[p.N + n]);
+      else y += o.bias ? o.bias[n] : 0.0f;
+      put(static_cast<T*>(o.y) + t * o.ld + n, y);
+    }
   }
 }
 
@@ -486,16 +467,23 @@ size_t linear_i8_ws_bytes(const moe_i8_linear& l) {
   return n < 256 ? 256 : n;
 }
 
-// Rows a group up to which the serving form is taken, and the largest rows
-// that it quantises for itself (elements; past them, and for several chunks
-// of rows, the quantising launch is cheaper than every workgroup's own).
 constexpr int64_t kCUs = 256;
-constexpr int64_t kFewRows = 16, kOwnElements = 32768, kOwnLds = 120 * 1024;
+// The serving form's place: up to 16 rows (8 of up to 1024 bytes) and as many
+// columns as two workgroups a CU take. In it and in 64 x 64 tiles: 4096 x 4096
+// 1 row 8.4 and 13.5 us, 16 rows 9.6 and 14.2; 1024 x 8192 4 rows 8.0 and 7.6,
+// 16 rows 12.0 and 8.2; 4096 x 12288 1 row 21.1 and 15.0. Not routed rows,
+// whose groups' columns are too many: 128 tokens to 64 groups of 2048 x 2048,
+// top-2, 139 and 49 us; 8 tokens 35 and 16, 1 token 11.4 and 10.0.
+constexpr int64_t kFewRows = 16, kFewShort = 1024, kFewRowsShort = 8, kFewColumns = 16 * 2 * kCUs;
+// The most elements of x that each of its workgroups quantises for itself;
+// past them a launch for it is cheaper (8 rows, 4096 x 4096: 11.4 us against
+// 9.0; 8 rows, 2048 x 4096: 7.4 against 8.0).
+constexpr int64_t kOwnElements = 16384, kOwnLds = 120 * 1024;
 
 template <typename T, typename X>
-void i8_few(const I8Few& p, const I8Out& o, int groups, bool paired, hipStream_t s) {
-  const dim3 grid((p.N + 15) / 16, groups);
-  const size_t lds = sizeof(X) == 1 ? 0 : (p.M < 16 ? p.M : 16) * (p.pitch + 16);
+void i8_few(const I8Few& p, const I8Out& o, bool paired, hipStream_t s) {
+  const dim3 grid((p.N + 15) / 16);
+  const size_t lds = sizeof(X) == 1 ? 0 : p.rows * (p.pitch + 16);
   if (paired)
     MOE_LAUNCH("linear_i8_few", (i8_few_kernel<T, X, true>), grid, dim3(64 * kRowsWaves), lds, s, p, o);
   else
@@ -509,10 +497,10 @@ hipError_t launch_linear_i8(const moe_i8_linear& l, const void* x, const float* 
   const int64_t pitch = i8_pitch(l.inputs), M = l.tokens * l.top_k;
   const bool paired = l.gated != 0;
   const int N = paired ? l.outputs / 2 : l.outputs;
-  const bool few = M <= kFewRows * l.groups;
+  const bool few = !r && M <= (pitch <= kFewShort ? kFewRowsShort : kFewRows) && N <= kFewColumns;
   // 16 rows have to fit in LDS beside the sums
   const bool own = few && l.x_dtype != MOE_I8 && 16 * (pitch + 16) <= kOwnLds &&
-                   M * pitch <= kOwnElements * static_cast<int64_t>(l.groups);
+                   M * pitch <= kOwnElements;
   if (l.x_dtype != MOE_I8 && !own) {
     int8_t* q = static_cast<int8_t*>(work);
     float* sc = reinterpret_cast<float*>(q + L.scale);
@@ -529,21 +517,14 @@ hipError_t launch_linear_i8(const moe_i8_linear& l, const void* x, const float* 
     p.xs = xs;
     p.w = wq;
     p.pitch = pitch;
-    p.group = static_cast<int64_t>(l.outputs) * pitch;
     p.width = l.inputs;
-    p.topk = l.top_k;
-    p.cap = l.capacity;
-    p.M = M;
+    p.rows = static_cast<int>(M);
     p.N = N;
-    if (r) {
-      p.offsets = r->expert_offsets;
-      if (l.gather) p.perm = r->perm;
-    }
     auto go = [&](auto t) {
       using T = decltype(t);
-      if (!own) i8_few<T, int8_t>(p, o, l.groups, paired, s);
-      else if (l.x_dtype == MOE_BF16) i8_few<T, bf16_t>(p, o, l.groups, paired, s);
-      else i8_few<T, float>(p, o, l.groups, paired, s);
+      if (!own) i8_few<T, int8_t>(p, o, paired, s);
+      else if (l.x_dtype == MOE_BF16) i8_few<T, bf16_t>(p, o, paired, s);
+      else i8_few<T, float>(p, o, paired, s);
     };
     if (l.dtype == MOE_BF16) go(bf16_t{});
     else go(float{});
@@ -572,12 +553,15 @@ hipError_t launch_linear_i8(const moe_i8_linear& l, const void* x, const float* 
     // one, 256 x 256 from eight stages on (16384 x 1024 x 2048: 48 us against 51
     // in 256 x 128 and 54 in 128 x 128; with four stages 66, 62 and 61). Routed
     // rows lose less of their last tile in 128 rows (64 experts, 131072 slots
-    // of 512: 72 us against 78).
-    auto tiles = [&](int bm) { return (M + bm - 1) / bm + (r ? p.groups : 0); };
+    // of 512: 72 us against 78), few rows in 64 (64 rows, 4096 x 65536: 50 us
+    // against 78).
+    const int64_t busy = r ? (M < p.groups ? M : p.groups) : 1;  // groups with rows, at most
+    auto tiles = [&](int bm) { return (M + busy * (bm - 1)) / bm; };
     const int64_t per_group = M / p.groups;
     auto count = [&](int m, int n) { return (M + m - 1) / m * ((l.outputs + n - 1) / n); };
-    if (p.nk >= 8 && per_group >= 512 && count(256, 256) >= kCUs) i8_tiles<T, MmBig>(p, o, paired, tiles(256), s);
-    else if (!r && count(256, 128) >= kCUs) i8_tiles<T, MmTall>(p, o, paired, tiles(256), s);
+    if (!r && M <= 64) i8_tiles<T, MmSmall>(p, o, paired, tiles(64), s);
+    else if (p.nk >= 8 && per_group >= 512 && count(256, 256) >= kCUs) i8_tiles<T, MmBig>(p, o, paired, tiles(256), s);
+    else if (!r && M > 128 && count(256, 128) >= kCUs) i8_tiles<T, MmTall>(p, o, paired, tiles(256), s);
     else if (per_group >= 128 && count(128, 128) >= kCUs) i8_tiles<T, MmMid>(p, o, paired, tiles(128), s);
     else i8_tiles<T, MmSmall>(p, o, paired, tiles(64), s);
   };

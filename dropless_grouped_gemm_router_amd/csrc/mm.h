@@ -117,8 +117,7 @@ __device__ __forceinline__ int mm_swizzle(int r) {
 using MmBig = MmCfg<256, 256, 2, 2, 2, 128>;   // one wave to a SIMD
 using MmTall = MmCfg<256, 128, 2, 2, 3, 64>;   // two workgroups a CU
 using MmMid = MmCfg<128, 128, 2, 2, 3, 64>;    // three
-using MmSmall = MmCfg<64, 64, 2, 2, 2, 128>;   // five
-using MmTurned = MmCfg<64, 64, 2, 2, 3, 128>;  // three, B as [K][N]: a third buffer, for the loads' latency shows
+using MmSmall = MmCfg<64, 64, 2, 2, 3, 128>;   // three
 
 // A tile's rows: first row, count (0: nothing to do), weight group.
 struct MmTile {
@@ -127,10 +126,14 @@ struct MmTile {
   int part, k0, k1;  // slice of K and its stages
 };
 
-// Row tile mt of the routed rows: each lane counts one expert's tiles (at
-// most 64 experts), a prefix sum finds the expert. Uniform over the wave.
+// The workgroup's tile of routed rows: each lane counts one expert's row tiles
+// (at most 64 experts), a prefix sum finds the expert. Uniform over the wave.
+// The grid is for the most tiles that the rows can make; those that there are
+// go to the XCDs in equal ranges: in the order of the grid a few experts' rows
+// would keep two of the eight busy (8 tokens, top-2 of 64 experts of 2048 x
+// 2048 in int8: 40 us against 16).
 __device__ __forceinline__ MmTile mm_routed_tile(const int32_t* offsets, int groups, int cap, int bm,
-                                                 int mt, int lane) {
+                                                 int tiles_n, int lane) {
   int first = 0, count = 0;
   if (lane < groups) {
     first = offsets[lane];
@@ -144,9 +147,12 @@ __device__ __forceinline__ MmTile mm_routed_tile(const int32_t* offsets, int gro
     const int v = __shfl_up(upto, o);
     if (lane >= o) upto += v;
   }
-  const uint64_t past = __ballot(upto > mt);
   MmTile t{};
-  if (past == 0) return t;
+  const int total = __shfl(upto, 63) * tiles_n;
+  if (static_cast<int>(blockIdx.x) >= total) return t;
+  const int w = xcd_remap(blockIdx.x, total), mt = w / tiles_n;
+  t.nt = w % tiles_n;
+  const uint64_t past = __ballot(upto > mt);
   const int e = __ffsll(static_cast<unsigned long long>(past)) - 1;
   const int local = mt - (__shfl(upto, e) - __shfl(tiles, e));
   t.group = __builtin_amdgcn_readfirstlane(e);
@@ -247,20 +253,15 @@ __device__ __forceinline__ void mm_loop(char* smem, int nk, int a_frag, int b_fr
   for (; s < nk; ++s) stage(std::false_type{}, s);  // after the last one `next` is read without use
 }
 
-// Tile w (of part `part`) of a product. False: no such tile.
+// Tile w (of part `part`) of a dense product. False: no such tile.
 template <typename Cfg>
 __device__ __forceinline__ bool mm_place(const MmArgs& p, int w, int part, MmTile* tile) {
   MmTile t{};
-  if (p.offsets) {
-    t = mm_routed_tile(p.offsets, p.groups, p.cap, Cfg::BM, w / p.tiles_n, threadIdx.x & 63);
-    t.nt = w % p.tiles_n;
-  } else {
-    int mt;
-    mm_tile_order(w, static_cast<int>((p.M + Cfg::BM - 1) / Cfg::BM), p.tiles_n, &mt, &t.nt);
-    t.row0 = static_cast<int64_t>(mt) * Cfg::BM;
-    const int64_t left = p.M - t.row0;
-    t.rows = left < Cfg::BM ? static_cast<int>(left) : Cfg::BM;
-  }
+  int mt;
+  mm_tile_order(w, static_cast<int>((p.M + Cfg::BM - 1) / Cfg::BM), p.tiles_n, &mt, &t.nt);
+  t.row0 = static_cast<int64_t>(mt) * Cfg::BM;
+  const int64_t left = p.M - t.row0;
+  t.rows = left < Cfg::BM ? static_cast<int>(left) : Cfg::BM;
   t.part = part;
   t.k0 = p.parts > 1 ? static_cast<int>(static_cast<int64_t>(p.nk) * part / p.parts) : 0;
   t.k1 = p.parts > 1 ? static_cast<int>(static_cast<int64_t>(p.nk) * (part + 1) / p.parts) : p.nk;
@@ -271,6 +272,11 @@ __device__ __forceinline__ bool mm_place(const MmArgs& p, int w, int part, MmTil
 // One workgroup's tile, from its index.
 template <typename Cfg>
 __device__ __forceinline__ bool mm_find(const MmArgs& p, MmTile* tile) {
+  if (p.offsets) {
+    *tile = mm_routed_tile(p.offsets, p.groups, p.cap, Cfg::BM, p.tiles_n, threadIdx.x & 63);
+    tile->k1 = p.nk;
+    return tile->rows > 0;
+  }
   const int w = xcd_remap(blockIdx.x, gridDim.x);
   const int tiles = p.parts > 1 ? gridDim.x / p.parts : gridDim.x;
   return mm_place<Cfg>(p, w % tiles, w / tiles, tile);
@@ -350,7 +356,7 @@ __device__ __forceinline__ void mm_loop_turned(char* smem, int nk, int a_frag, i
 // block when p % 32 < 16, else the same up column), so a lane's registers
 // 0-7 and 8-15 of an MFMA tile are matching gate and up values.
 //
-// kTurned (MmTurned): B is [K][N], N contiguous, K a multiple of 64 and N of 8.
+// kTurned (mm_loop_turned): B is [K][N], N contiguous, K a multiple of 64 and N of 8.
 template <typename Op, typename Cfg, bool kPaired, bool kTurned = false>
 __device__ __forceinline__ void mm_tile(const MmArgs& p, char* smem, const MmTile& t,
                                         typename Op::Acc (&acc)[Cfg::WM][Cfg::WN]) {

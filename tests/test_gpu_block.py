@@ -232,7 +232,8 @@ def test_ffn(t, d, h, dtype):
 
 @pytest.mark.parametrize("act", ["silu", "relu"])
 @pytest.mark.parametrize("t,d,h", [(17, 64, 64), (40, 2048, 512), (129, 64, 192), (200, 192, 320), (257, 1024, 4096),
-                                   (300, 512, 64), (1000, 128, 512), (384, 1088, 576)])
+                                   (300, 512, 64), (1000, 128, 512), (384, 1088, 576),
+                                   (100, 64, 16384), (33, 128, 16448)])
 def test_ffn_weights_in_place(t, d, h, act):
     """More tokens than the serving form is for, in widths that are multiples
     of 64 but not all of 128: the forward multiplies by the weights where they are."""
@@ -426,7 +427,8 @@ def dequantized(x):
                                    (16, 1024, 256), (17, 640, 129), (32, 128, 128), (33, 257, 1001),
                                    (100, 1111, 515), (128, 512, 512), (129, 8200, 64), (400, 333, 2049),
                                    (700, 65, 7), (2100, 384, 8200), (2100, 300, 2100),
-                                   (4200, 1100, 4100)])
+                                   (4200, 1100, 4100), (8, 900, 300), (9, 1000, 40), (16, 1024, 8193),
+                                   (3, 200, 8209), (16, 2000, 520), (60, 256, 16500), (120, 200, 33000)])
 def test_linear_i8(t, k, n, dtype):
     note(f"linear_i8 {t} {k} {n} {dtype}")
     r = gen(t + k + n)
@@ -484,6 +486,7 @@ def routing_of(t, e, top, seed, skew=0.0):
     (1, 128, 256, 8, 2, True, "bf16"), (3, 100, 66, 5, 3, False, "fp32"), (40, 512, 512, 64, 8, True, "bf16"),
     (200, 130, 70, 4, 1, True, "fp32"), (500, 256, 258, 33, 4, False, "bf16"), (2000, 512, 256, 8, 2, True, "bf16"),
     (2500, 128, 130, 3, 3, False, "bf16"), (3000, 512, 512, 2, 1, True, "bf16"),
+    (1, 130, 70, 64, 3, False, "fp32"), (7, 640, 512, 64, 1, True, "bf16"), (2, 100, 4200, 8, 2, False, "bf16"),
     (9000, 128, 258, 8, 2, True, "bf16"), (4000, 1100, 2100, 2, 2, False, "fp32"), (4000, 1100, 2200, 3, 2, True, "bf16")])
 def test_linear_i8_routed(t, k, n, e, top, gated, dtype):
     import torch
