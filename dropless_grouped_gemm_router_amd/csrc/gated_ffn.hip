@@ -9,9 +9,10 @@
 // Wd^T and the activation's gradient. The weights come [d][h] and [h][d]:
 // the forward's products run over their leading dimension, so they are
 // turned K-contiguous into the workspace first; the backward's data
-// gradients read them as they are. In bf16, few tokens and widths in multiples
-// of 64 the forward does so too (in_place). The weight gradients reduce over tokens,
-// in slices whose partial sums are added in a fixed order.
+// gradients read them as they are, and so does the forward in bf16 with widths
+// in multiples of 64, up to some thousand tokens (in_place). The weight
+// gradients reduce over tokens, in slices whose partial sums are added in a
+// fixed order.
 //
 // Widths that are no multiple of 128 take zero-padded copies of the operands
 // in the workspace (x and dout, and the weights the backward reads), with the
@@ -793,23 +794,28 @@ int parts_of(size_t elem, int64_t M, int64_t N, int64_t stages) {
 }
 
 // Whether the forward's tiles read the weights where they are (mm_tile,
-// kTurned): bf16, both products in 64 x 64 tiles, widths that fill stages.
-// Those are few tokens, for which turning the weights costs as much as a
-// product. Turned first and in place, 300 tokens, 1024 x 4096: 35.1 and 28.4
-// us; 200 tokens, 2048 x 2048: 39.6 and 24.4; 2000 tokens, 512 x 512: 17.1
-// and 12.6.
+// kTurned), in 64 x 64 or 128 x 128: bf16, widths that fill stages, and not so
+// many tokens that turning the weights once for the larger tiles is less.
+// Turned first and in place, 300 tokens, 1024 x 4096: 35.1 and 28.4 us; 1000
+// tokens, 2048 x 8192: 154 and 145, 4000: 441 and 439, 8192: 790 and 925;
+// 8192 tokens, 1024 x 4096: 258 and 243; 16384 tokens, 512 x 1024: 93 and 91,
+// 32768: 147 and 152.
+constexpr int64_t kInPlace = int64_t{1} << 23;  // elements of x
 bool in_place(const moe_ffn& f) {
   if (f.dtype != MOE_BF16 || f.d_model % 64 || f.d_hidden % 64) return false;
-  return tile_of(2, f.tokens, 2 * static_cast<int64_t>(f.d_hidden), f.d_model / 64) == kSmall &&
-         tile_of(2, f.tokens, f.d_model, f.d_hidden / 64) == kSmall;
+  return f.tokens * f.d_model <= kInPlace;
 }
 
 template <typename T, int kMode, int kAct>
 void tiles(const char* name, const MmArgs& p, const FfnOut& o, hipStream_t s, bool turned = false) {
-  if constexpr (sizeof(T) == 2 && (kMode == kPlain || kMode == kGated)) {
-    if (turned) return tiles_at<T, MmSmall, kMode, kAct, true>(name, p, o, s);
-  }
   const int64_t cols = kMode == kGated ? 2 * static_cast<int64_t>(p.N) : p.N;
+  if constexpr (sizeof(T) == 2 && (kMode == kPlain || kMode == kGated)) {
+    if (turned) {
+      if (tile_of(2, p.M, cols, p.nk) == kSmall) tiles_at<T, MmSmall, kMode, kAct, true>(name, p, o, s);
+      else tiles_at<T, MmMid, kMode, kAct, true>(name, p, o, s);
+      return;
+    }
+  }
   switch (tile_of(sizeof(T), p.M, cols, p.nk)) {
     case kSmall: return tiles_at<T, MmSmall, kMode, kAct>(name, p, o, s);
     case kMid: return tiles_at<T, MmMid, kMode, kAct>(name, p, o, s);

@@ -282,29 +282,42 @@ __device__ __forceinline__ bool mm_find(const MmArgs& p, MmTile* tile) {
   return mm_place<Cfg>(p, w % tiles, w / tiles, tile);
 }
 
-// The loop for a B that is [K][N], N contiguous, of bf16 and in 64 columns: a
-// stage holds 64 rows of k of them (128 bytes each, chunk c of row r at c ^ 4
-// (r / 2 % 2): the rows of a read then touch every bank once). The transposing
-// LDS read makes eight k of a column of them: in a group of 16 lanes, lane s
-// addresses row s / 4, columns 4 (s % 4) .. + 3, and lane j receives the four
-// rows of column j. All the reads of a stage are one statement with their
-// wait, for the compiler would wait before its builtin for every load in
-// flight (200 tokens, 2048 x 2048: 35 us against 24); what is not spread
-// between MFMAs, the other workgroups of the CU cover. Loads go RING - 1
-// stages ahead, into the buffer that all waves have read when they meet at
-// the one barrier of a stage. Two buffers took 32 us there, four 25.
+// Position of chunk c of k row r in a stage of a B that is [K][N]: the four
+// rows of a transposing read spread over all banks.
+template <typename Cfg>
+__device__ __forceinline__ int mm_turned_at(int r, int c) {
+  return c ^ (Cfg::BN == 64 ? ((r >> 1) & 1) << 2 : (r & 3) << 2);
+}
+
+// The loop for a B that is [K][N], N contiguous, of bf16, in 64 or 128
+// columns: a stage holds as many rows of k as its rows of A have elements. The
+// transposing LDS read makes eight k of a column of them: in a group of 16
+// lanes, lane s addresses row s / 4, columns 4 (s % 4) .. + 3, and lane j
+// receives the four rows of column j. All the reads of a stage are one
+// statement with their wait, for the compiler would wait before its builtin
+// for every load in flight (200 tokens, 2048 x 2048: 35 us against 24); what
+// is not spread between MFMAs, the other workgroups of the CU cover. Loads go
+// RING - 1 stages ahead, into the buffer that all waves have read when they
+// meet at the one barrier of a stage. Two buffers took 32 us there, four 25.
 template <typename Op, typename Cfg, typename Load>
 __device__ __forceinline__ void mm_loop_turned(char* smem, int nk, int a_frag, int sw, int col0,
-                                               typename Op::Acc& acc, Load&& load) {
-  static_assert(Cfg::BN == 64 && Cfg::ROW == 128 && Cfg::WM == 1 && Cfg::WN == 1, "64 columns a row");
+                                               typename Op::Acc (&acc)[Cfg::WM][Cfg::WN], Load&& load) {
+  constexpr bool kWide = Cfg::BN == 128;
+  static_assert(kWide ? Cfg::ROW == 64 && Cfg::WM == 2 && Cfg::WN == 2
+                      : Cfg::BN == 64 && Cfg::ROW == 128 && Cfg::WM == 1 && Cfg::WN == 1, "tiles");
   constexpr int kLoads = Cfg::A_LOADS + Cfg::B_LOADS, kAhead = Cfg::RING - 1;
+  constexpr int kSteps = Cfg::STEPS, kB = Cfg::WN;
   const int lane = threadIdx.x & 63, s16 = lane & 15, g16 = lane >> 4;
-  const int col = col0 + 16 * (g16 & 1) + 4 * (s16 & 3), row = 8 * (g16 >> 1) + (s16 >> 2);
   const uint32_t base = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(smem));
-  const uint32_t b = base + Cfg::BM * Cfg::ROW + row * 128 + (((col >> 3) ^ (((row >> 1) & 1) << 2)) << 4) + (col & 7) * 2;
-  uint32_t a[4];
+  const int row = 8 * (g16 >> 1) + (s16 >> 2);
+  uint32_t a[kSteps], b[kB];
 #pragma unroll
-  for (int q = 0; q < 4; ++q) a[q] = base + a_frag + (((2 * q) ^ sw) << 4);
+  for (int q = 0; q < kSteps; ++q) a[q] = base + a_frag + (((2 * q) ^ sw) << 4);
+#pragma unroll
+  for (int j = 0; j < kB; ++j) {
+    const int col = col0 + 32 * j + 16 * (g16 & 1) + 4 * (s16 & 3);
+    b[j] = base + Cfg::BM * Cfg::ROW + row * Cfg::BN * 2 + (mm_turned_at<Cfg>(row, col >> 3) << 4) + (col & 7) * 2;
+  }
 #pragma unroll
   for (int st = 0; st < kAhead; ++st)
     if (st < nk) {
@@ -320,32 +333,59 @@ __device__ __forceinline__ void mm_loop_turned(char* smem, int nk, int a_frag, i
 #pragma unroll
       for (int u = 0; u < kLoads; ++u) load(s + kAhead, smem + to, u);
     }
+    // x[step WM + i], w[2 (step WN + j) + half]: steps are 16 rows of k apart,
+    // halves four, A's fragments 32 rows
     u32x4 x[4];
     uint64_t w[8];
-    asm volatile(
-        "ds_read_b64_tr_b16 %4, %16\n\t"
-        "ds_read_b64_tr_b16 %5, %16 offset:512\n\t"
-        "ds_read_b128 %0, %12\n\t"
-        "ds_read_b64_tr_b16 %6, %16 offset:2048\n\t"
-        "ds_read_b64_tr_b16 %7, %16 offset:2560\n\t"
-        "ds_read_b128 %1, %13\n\t"
-        "ds_read_b64_tr_b16 %8, %16 offset:4096\n\t"
-        "ds_read_b64_tr_b16 %9, %16 offset:4608\n\t"
-        "ds_read_b128 %2, %14\n\t"
-        "ds_read_b64_tr_b16 %10, %16 offset:6144\n\t"
-        "ds_read_b64_tr_b16 %11, %16 offset:6656\n\t"
-        "ds_read_b128 %3, %15\n\t"
-        "s_waitcnt lgkmcnt(0)"
-        : "=&v"(x[0]), "=&v"(x[1]), "=&v"(x[2]), "=&v"(x[3]), "=&v"(w[0]), "=&v"(w[1]), "=&v"(w[2]),
-          "=&v"(w[3]), "=&v"(w[4]), "=&v"(w[5]), "=&v"(w[6]), "=&v"(w[7])
-        : "v"(a[0] + at), "v"(a[1] + at), "v"(a[2] + at), "v"(a[3] + at), "v"(b + at)
-        : "memory");
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const u32x4 v = {static_cast<uint32_t>(w[2 * q]), static_cast<uint32_t>(w[2 * q] >> 32),
-                       static_cast<uint32_t>(w[2 * q + 1]), static_cast<uint32_t>(w[2 * q + 1] >> 32)};
-      Op::step(v, x[q], acc);
+    if constexpr (kWide) {
+      asm volatile(
+          "ds_read_b64_tr_b16 %4, %14\n\t"
+          "ds_read_b64_tr_b16 %5, %14 offset:1024\n\t"
+          "ds_read_b128 %0, %12\n\t"
+          "ds_read_b64_tr_b16 %6, %15\n\t"
+          "ds_read_b64_tr_b16 %7, %15 offset:1024\n\t"
+          "ds_read_b128 %1, %12 offset:2048\n\t"
+          "ds_read_b64_tr_b16 %8, %14 offset:4096\n\t"
+          "ds_read_b64_tr_b16 %9, %14 offset:5120\n\t"
+          "ds_read_b128 %2, %13\n\t"
+          "ds_read_b64_tr_b16 %10, %15 offset:4096\n\t"
+          "ds_read_b64_tr_b16 %11, %15 offset:5120\n\t"
+          "ds_read_b128 %3, %13 offset:2048\n\t"
+          "s_waitcnt lgkmcnt(0)"
+          : "=&v"(x[0]), "=&v"(x[1]), "=&v"(x[2]), "=&v"(x[3]), "=&v"(w[0]), "=&v"(w[1]), "=&v"(w[2]),
+            "=&v"(w[3]), "=&v"(w[4]), "=&v"(w[5]), "=&v"(w[6]), "=&v"(w[7])
+          : "v"(a[0] + at), "v"(a[1] + at), "v"(b[0] + at), "v"(b[kB - 1] + at)
+          : "memory");
+    } else {
+      asm volatile(
+          "ds_read_b64_tr_b16 %4, %16\n\t"
+          "ds_read_b64_tr_b16 %5, %16 offset:512\n\t"
+          "ds_read_b128 %0, %12\n\t"
+          "ds_read_b64_tr_b16 %6, %16 offset:2048\n\t"
+          "ds_read_b64_tr_b16 %7, %16 offset:2560\n\t"
+          "ds_read_b128 %1, %13\n\t"
+          "ds_read_b64_tr_b16 %8, %16 offset:4096\n\t"
+          "ds_read_b64_tr_b16 %9, %16 offset:4608\n\t"
+          "ds_read_b128 %2, %14\n\t"
+          "ds_read_b64_tr_b16 %10, %16 offset:6144\n\t"
+          "ds_read_b64_tr_b16 %11, %16 offset:6656\n\t"
+          "ds_read_b128 %3, %15\n\t"
+          "s_waitcnt lgkmcnt(0)"
+          : "=&v"(x[0]), "=&v"(x[1]), "=&v"(x[2]), "=&v"(x[3]), "=&v"(w[0]), "=&v"(w[1]), "=&v"(w[2]),
+            "=&v"(w[3]), "=&v"(w[4]), "=&v"(w[5]), "=&v"(w[6]), "=&v"(w[7])
+          : "v"(a[0] + at), "v"(a[1] + at), "v"(a[kSteps - 2] + at), "v"(a[kSteps - 1] + at), "v"(b[0] + at)
+          : "memory");
     }
+#pragma unroll
+    for (int q = 0; q < kSteps; ++q)
+#pragma unroll
+      for (int j = 0; j < kB; ++j) {
+        const uint64_t lo = w[2 * (q * kB + j)], hi = w[2 * (q * kB + j) + 1];
+        const u32x4 v = {static_cast<uint32_t>(lo), static_cast<uint32_t>(lo >> 32),
+                         static_cast<uint32_t>(hi), static_cast<uint32_t>(hi >> 32)};
+#pragma unroll
+        for (int i = 0; i < Cfg::WM; ++i) Op::step(v, x[q * Cfg::WM + i], acc[i][j]);
+      }
     at = at + Cfg::STAGE == Cfg::LDS ? 0 : at + Cfg::STAGE;
     to = to + Cfg::STAGE == Cfg::LDS ? 0 : to + Cfg::STAGE;
   }
@@ -377,13 +417,15 @@ __device__ __forceinline__ void mm_tile(const MmArgs& p, char* smem, const MmTil
   }
 #pragma unroll
   for (int i = 0; i < Cfg::B_LOADS; ++i) {
-    const int r = (wave * Cfg::B_LOADS + i) * Cfg::RPL + lane / Cfg::CPR;
     if constexpr (kTurned) {
-      const int c = (lane % Cfg::CPR) ^ (((r >> 1) & 1) << 2);
+      constexpr int kChunks = Cfg::BN / 8;  // of a k row
+      const int r = (wave * Cfg::B_LOADS + i) * (64 / kChunks) + lane / kChunks;
+      const int c = mm_turned_at<Cfg>(r, lane % kChunks);
       const int col = kPaired ? t.nt * (Cfg::BN / 2) + 16 * (c >> 2) + 8 * (c & 1) : t.nt * Cfg::BN + 8 * c;
       b[i] = p.b + r * p.b_pitch + min(col, p.N - 8) * 2 + (kPaired && (c & 2) ? p.half : 0);
       continue;
     }
+    const int r = (wave * Cfg::B_LOADS + i) * Cfg::RPL + lane / Cfg::CPR;
     const int chunk = ((lane % Cfg::CPR) ^ mm_swizzle<Cfg>(r)) << 4;
     int64_t off;
     if (kPaired) {
@@ -413,7 +455,7 @@ __device__ __forceinline__ void mm_tile(const MmArgs& p, char* smem, const MmTil
 
   auto load = [&](int st, char* buf, int u) {
     const int64_t off = static_cast<int64_t>(st + t.k0) * Cfg::ROW;
-    const int64_t off_b = kTurned ? static_cast<int64_t>(st + t.k0) * 64 * p.b_pitch : off;
+    const int64_t off_b = kTurned ? static_cast<int64_t>(st + t.k0) * (Cfg::ROW / 2) * p.b_pitch : off;
     const bool first = st + t.k0 < split;
     if (u < Cfg::A_LOADS) {
       const char* src = a[u < Cfg::A_LOADS ? u : 0] + off + (first ? 0 : a2);
@@ -425,7 +467,7 @@ __device__ __forceinline__ void mm_tile(const MmArgs& p, char* smem, const MmTil
       __builtin_amdgcn_global_load_lds(src, dst, 16, 0, 0);
     }
   };
-  if constexpr (kTurned) mm_loop_turned<Op, Cfg>(smem, nk, a_frag, sw, wn * 32, acc[0][0], load);
+  if constexpr (kTurned) mm_loop_turned<Op, Cfg>(smem, nk, a_frag, sw, wn * Cfg::WN * 32, acc, load);
   else mm_loop<Op, Cfg>(smem, nk, a_frag, b_frag, sw, acc, load);
 }
 

@@ -233,7 +233,8 @@ def test_ffn(t, d, h, dtype):
 @pytest.mark.parametrize("act", ["silu", "relu"])
 @pytest.mark.parametrize("t,d,h", [(17, 64, 64), (40, 2048, 512), (129, 64, 192), (200, 192, 320), (257, 1024, 4096),
                                    (300, 512, 64), (1000, 128, 512), (384, 1088, 576),
-                                   (100, 64, 16384), (33, 128, 16448)])
+                                   (100, 64, 16384), (33, 128, 16448), (1300, 576, 2112), (515, 2048, 8192),
+                                   (8200, 64, 192), (9000, 832, 64)])
 def test_ffn_weights_in_place(t, d, h, act):
     """More tokens than the serving form is for, in widths that are multiples
     of 64 but not all of 128: the forward multiplies by the weights where they are."""
