@@ -475,10 +475,11 @@ constexpr int64_t kCUs = 256;
 // whose groups' columns are too many: 128 tokens to 64 groups of 2048 x 2048,
 // top-2, 139 and 49 us; 8 tokens 35 and 16, 1 token 11.4 and 10.0.
 constexpr int64_t kFewRows = 16, kFewShort = 1024, kFewRowsShort = 8, kFewColumns = 16 * 2 * kCUs;
-// The most elements of x that each of its workgroups quantises for itself;
-// past them a launch for it is cheaper (8 rows, 4096 x 4096: 11.4 us against
-// 9.0; 8 rows, 2048 x 4096: 7.4 against 8.0).
-constexpr int64_t kOwnElements = 16384, kOwnLds = 120 * 1024;
+// The most elements of x that each of its workgroups quantises for itself, and
+// of a row, which is one wave's; past them a launch for it is cheaper (8 rows,
+// 4096 x 4096: 11.4 us against 9.0; 2 rows, 5000 x 1000: 10.5 against 9.4; but
+// 8 rows, 2048 x 4096: 7.4 against 8.0).
+constexpr int64_t kOwnElements = 16384, kOwnWidth = 4096;
 
 template <typename T, typename X>
 void i8_few(const I8Few& p, const I8Out& o, bool paired, hipStream_t s) {
@@ -498,9 +499,7 @@ hipError_t launch_linear_i8(const moe_i8_linear& l, const void* x, const float* 
   const bool paired = l.gated != 0;
   const int N = paired ? l.outputs / 2 : l.outputs;
   const bool few = !r && M <= (pitch <= kFewShort ? kFewRowsShort : kFewRows) && N <= kFewColumns;
-  // 16 rows have to fit in LDS beside the sums
-  const bool own = few && l.x_dtype != MOE_I8 && 16 * (pitch + 16) <= kOwnLds &&
-                   M * pitch <= kOwnElements;
+  const bool own = few && l.x_dtype != MOE_I8 && pitch <= kOwnWidth && M * pitch <= kOwnElements;
   if (l.x_dtype != MOE_I8 && !own) {
     int8_t* q = static_cast<int8_t*>(work);
     float* sc = reinterpret_cast<float*>(q + L.scale);
