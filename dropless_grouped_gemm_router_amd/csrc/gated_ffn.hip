@@ -31,13 +31,13 @@ namespace moe {
 
 namespace {
 
-// Tokens up to which the forward takes the serving form: the second where the
-// other choice is to turn the weights, the first where it is tiles that read
-// them in place (the shapes of in_place). The serving form and those tiles
-// take, bf16, 16 tokens, 2048 x 8192: 25.0 and 27.8 us, 1024 x 4096: 14.1 and
-// 13.4; 32 tokens: 29.3 and 28.5, 18.1 and 14.0; 128 tokens: 59.4 and 37.4,
-// 23.3 and 19.5; 512 x 1024: 15.1 and 11.8.
-constexpr int64_t kFewRowsInPlace = 16, kFewRows = 128;
+// Tokens up to which the forward takes the serving form, bf16 and fp32. The
+// serving form and tiles take, bf16, 16 tokens, 2048 x 8192: 25.0 and 27.8 us,
+// 1024 x 4096: 14.1 and 13.4; 32 tokens: 29.3 and 28.5, 18.1 and 14.0; where
+// tiles have the weights turned first, 17 tokens, 2047 x 8191: 88 and 76, 500 x
+// 1001: 22.6 and 18.6. fp32, 64 tokens, 1024 x 4096: 39 and 52, 2048 x 2048: 55
+// and 73; 128 tokens: 66 and 58, 63 and 77; 512 x 1024: 22 and 28.
+constexpr int64_t kFewRows = 16, kFewRowsF32 = 128;
 constexpr int64_t kCUs = 256;
 
 constexpr int64_t pad128(int64_t v) { return (v + 127) / 128 * 128; }
@@ -367,49 +367,45 @@ __device__ __forceinline__ void keep1(const FfnOut& o, int64_t at, float f, floa
 // Training (o.f): also what the backward needs, over the padded width o.ld
 // (columns past N come out as zeros: no weights are read for them), and the
 // backward's row of zeros.
-template <typename T, int kR, int kAct>
+template <typename T, int kAct>
 __global__ __launch_bounds__(512) void ffn_rows_gate_up_kernel(const SkinnyArgs<T, 2> a, T* high, T* low,
                                                                const FfnOut o, u32x4* zero) {
   __shared__ float lds[kSkinnyWaves][kSkinnyLds];
-  float sum[kR][2][2];
+  float sum[2][2];
   if (zero && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < kTrZeroBytes / 16)
     zero[threadIdx.x] = (u32x4){0u, 0u, 0u, 0u};
-  skinny_sums<T, 2, kR, false>(a, lds, sum);
+  skinny_sums<T, 2, false>(a, lds, sum);
 #pragma unroll
-  for (int i = 0; i < kR; ++i)
-#pragma unroll
-    for (int v = 0; v < 2; ++v) {
-      const int64_t row = (static_cast<int64_t>(blockIdx.y) * kR + i) * 16 + (threadIdx.x >> 6) + 8 * v;
-      const int n = blockIdx.x * kSkinnyCols + (threadIdx.x & 63);
-      if (row >= a.rows) continue;
-      const float b = sum[i][v][1];
-      float slope;
-      const float f = act_value<kAct>(sum[i][v][0], &slope), h = f * b;
-      if (n < a.N) put_hidden(high + row * a.N + n, low + row * a.N + n, h);
-      if (o.f) {
-        put(static_cast<T*>(o.h) + row * o.ld + n, h);
-        keep1(o, row * o.ld + n, f, b * slope, static_cast<const T*>(nullptr));
-      }
+  for (int v = 0; v < 2; ++v) {
+    const int64_t row = static_cast<int64_t>(blockIdx.y) * 16 + (threadIdx.x >> 6) + 8 * v;
+    const int n = blockIdx.x * kSkinnyCols + (threadIdx.x & 63);
+    if (row >= a.rows) continue;
+    const float b = sum[v][1];
+    float slope;
+    const float f = act_value<kAct>(sum[v][0], &slope), h = f * b;
+    if (n < a.N) put_hidden(high + row * a.N + n, low + row * a.N + n, h);
+    if (o.f) {
+      put(static_cast<T*>(o.h) + row * o.ld + n, h);
+      keep1(o, row * o.ld + n, f, b * slope, static_cast<const T*>(nullptr));
     }
+  }
 }
 
 // part: null (one slice of K): out is written; else the slices' sums
 // [k_parts][rows][N].
-template <typename T, int kR>
+template <typename T>
 __global__ __launch_bounds__(512) void ffn_rows_down_kernel(const SkinnyArgs<T, 1> a, T* out, float* part) {
   __shared__ float lds[kSkinnyWaves][kSkinnyLds];
-  float sum[kR][2][1];
-  skinny_sums<T, 1, kR, sizeof(T) == 2>(a, lds, sum);
+  float sum[2][1];
+  skinny_sums<T, 1, sizeof(T) == 2>(a, lds, sum);
 #pragma unroll
-  for (int i = 0; i < kR; ++i)
-#pragma unroll
-    for (int v = 0; v < 2; ++v) {
-      const int64_t row = (static_cast<int64_t>(blockIdx.y) * kR + i) * 16 + (threadIdx.x >> 6) + 8 * v;
-      const int n = blockIdx.x * kSkinnyCols + (threadIdx.x & 63);
-      if (row >= a.rows || n >= a.N) continue;
-      if (part) part[(blockIdx.z * a.rows + row) * a.N + n] = sum[i][v][0];
-      else put(out + row * a.N + n, sum[i][v][0]);
-    }
+  for (int v = 0; v < 2; ++v) {
+    const int64_t row = static_cast<int64_t>(blockIdx.y) * 16 + (threadIdx.x >> 6) + 8 * v;
+    const int n = blockIdx.x * kSkinnyCols + (threadIdx.x & 63);
+    if (row >= a.rows || n >= a.N) continue;
+    if (part) part[(blockIdx.z * a.rows + row) * a.N + n] = sum[v][0];
+    else put(out + row * a.N + n, sum[v][0]);
+  }
 }
 
 template <typename T>
@@ -652,11 +648,9 @@ int slices(int64_t rows, int64_t tiles) {
   return static_cast<int>(k > most ? (most < 1 ? 1 : most) : k);
 }
 
-// Row tiles of 16 a workgroup of the serving form takes.
-int rows_tile(const moe_ffn& f) { return f.tokens <= 16 || f.dtype != MOE_BF16 ? 1 : 2; }
 // Whether the forward takes the serving form (training too: what it keeps is
 // the same, and the weights are not turned).
-bool few_rows(const moe_ffn& f) { return f.tokens <= (in_place(f) ? kFewRowsInPlace : kFewRows); }
+bool few_rows(const moe_ffn& f) { return f.tokens <= (f.dtype == MOE_BF16 ? kFewRows : kFewRowsF32); }
 
 FfnBlockLayout ffn_block_layout(const moe_ffn& f, bool training) {
   FfnBlockLayout L{};
@@ -671,8 +665,7 @@ FfnBlockLayout ffn_block_layout(const moe_ffn& f, bool training) {
   if (few_rows(f)) {
     L.rows_h = take(T * h * es * (es == 2 ? 2 : 1));
     // slices of K so that every CU has a workgroup, of two steps a wave at least
-    const int r = 16 * rows_tile(f);
-    const int64_t blocks = f.tokens == 0 ? 1 : (f.d_model + kSkinnyCols - 1) / kSkinnyCols * ((f.tokens + r - 1) / r);
+    const int64_t blocks = f.tokens == 0 ? 1 : (f.d_model + kSkinnyCols - 1) / kSkinnyCols * ((f.tokens + 15) / 16);
     const int64_t most = (f.d_hidden + 2 * kSkinnyStep * kSkinnyWaves - 1) / (2 * kSkinnyStep * kSkinnyWaves);
     const int64_t want = (256 + blocks - 1) / blocks;
     L.k_parts = static_cast<int>(want < most ? want : most);
@@ -911,7 +904,7 @@ MmArgs rows_of(const void* a, int64_t lda, const void* b, int64_t ldb, int64_t M
   return p;
 }
 
-template <typename T, int kR>
+template <typename T>
 hipError_t ffn_rows_t(const moe_ffn& f, const void* x, const void* wg, const void* wu,
                       const void* wd, void* saved, void* out, void* ws, hipStream_t s) {
   const FfnBlockLayout L = ffn_block_layout(f, saved != nullptr);
@@ -919,7 +912,7 @@ hipError_t ffn_rows_t(const moe_ffn& f, const void* x, const void* wg, const voi
   const int d = f.d_model, h = f.d_hidden;
   T* high = reinterpret_cast<T*>(W + L.rows_h);
   T* low = sizeof(T) == 2 ? high + f.tokens * h : nullptr;
-  const unsigned tall = static_cast<unsigned>((f.tokens + 16 * kR - 1) / (16 * kR));
+  const unsigned tall = static_cast<unsigned>((f.tokens + 15) / 16);
   SkinnyArgs<T, 2> a{static_cast<const T*>(x), nullptr, d,
                      {static_cast<const T*>(wg), static_cast<const T*>(wu)}, f.tokens, d, h, 1};
   FfnOut o{};
@@ -933,7 +926,7 @@ hipError_t ffn_rows_t(const moe_ffn& f, const void* x, const void* wg, const voi
   switch (f.act) {
 #define MOE_ROWS(ACT)                                                                              \
   case ACT:                                                                                        \
-    MOE_LAUNCH("ffn_rows_gate_up", (ffn_rows_gate_up_kernel<T, kR, ACT>), ga, dim3(512), 0, s, a, \
+    MOE_LAUNCH("ffn_rows_gate_up", (ffn_rows_gate_up_kernel<T, ACT>), ga, dim3(512), 0, s, a, \
                high, low, o, zero);                                                                         \
     break
     MOE_ROWS(MOE_ACT_SILU);
@@ -944,7 +937,7 @@ hipError_t ffn_rows_t(const moe_ffn& f, const void* x, const void* wg, const voi
   }
   float* part = L.k_parts > 1 ? reinterpret_cast<float*>(W + L.rows_part) : nullptr;
   SkinnyArgs<T, 1> b{high, low, h, {static_cast<const T*>(wd)}, f.tokens, h, d, L.k_parts};
-  MOE_LAUNCH("ffn_rows_down", (ffn_rows_down_kernel<T, kR>),
+  MOE_LAUNCH("ffn_rows_down", (ffn_rows_down_kernel<T>),
              dim3((d + kSkinnyCols - 1) / kSkinnyCols, tall, L.k_parts), dim3(512), 0, s, b,
              static_cast<T*>(out), part);
   if (part) {
@@ -958,13 +951,7 @@ hipError_t ffn_rows_t(const moe_ffn& f, const void* x, const void* wg, const voi
 template <typename T>
 hipError_t ffn_fwd_t(const moe_ffn& f, const void* x, const void* wg, const void* wu,
                      const void* wd, void* saved, void* out, void* ws, hipStream_t s) {
-  if (few_rows(f)) {
-    [[maybe_unused]] const int r = rows_tile(f);
-    if constexpr (sizeof(T) == 2) {
-      if (r == 2) return ffn_rows_t<T, 2>(f, x, wg, wu, wd, saved, out, ws, s);
-    }
-    return ffn_rows_t<T, 1>(f, x, wg, wu, wd, saved, out, ws, s);
-  }
+  if (few_rows(f)) return ffn_rows_t<T>(f, x, wg, wu, wd, saved, out, ws, s);
   const FfnBlockLayout L = ffn_block_layout(f, saved != nullptr);
   const SavedLayout S = saved_layout(f);
   char *W = static_cast<char*>(ws), *SV = static_cast<char*>(saved);

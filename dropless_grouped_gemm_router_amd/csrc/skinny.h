@@ -14,10 +14,8 @@
 // columns 16 (L / 16) .. + 15. The waves of a workgroup share K; their sums are
 // added in LDS in wave order. One token through weights of 2048 x 8192 (three
 // times 33.5 MB): 23 to 30 us, 3.4 to 4.4 TB/s; turning them for the tiles
-// first takes 37 us alone. From about 130 rows on the weights' repeated way
-// through L2 costs more than the turning (300 rows, 1024 x 4096: 66 us against
-// 34), and from 17 on more than tiles that need no turning (gated_ffn.hip,
-// kFewRowsInPlace).
+// first takes 37 us alone. From 17 rows of bf16 on the weights' repeated way
+// through L2 costs more than tiles (gated_ffn.hip, kFewRows).
 #pragma once
 
 #include "block.h"
@@ -130,55 +128,43 @@ struct SkinnyArgs {
   int k_parts;  // slices of K, one per blockIdx.z
 };
 
-// Sums of this workgroup's columns over its slice of K, for 16 kR rows:
-// after the call thread t holds, for row tile i and v = 0, 1, those of column
-// t % 64 and row t / 64 + 8 v of the tile, all kW of them. In LDS register
+// Sums of this workgroup's columns over its slice of K, for 16 rows: after the
+// call thread t holds, for v = 0, 1, those of column t % 64 and row t / 64 +
+// 8 v of the tile, all kW of them. In LDS register
 // 4 q + j of a lane stands at 65 (4 q + j) + lane: both sides use all banks.
 constexpr int kSkinnyLds = 16 * 65;
-template <typename T, int kW, int kR, bool kLow>
+template <typename T, int kW, bool kLow>
 __device__ __forceinline__ void skinny_sums(const SkinnyArgs<T, kW>& a, float (*lds)[kSkinnyLds],
-                                            float (&sum)[kR][2][kW]) {
+                                            float (&sum)[2][kW]) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int n = blockIdx.x * kSkinnyCols + 4 * (lane & 15);
-  const int64_t r0 = static_cast<int64_t>(blockIdx.y) * 16 * kR;
   const int steps = (a.K + kSkinnyStep - 1) / kSkinnyStep;
   const int s0 = static_cast<int>(static_cast<int64_t>(steps) * blockIdx.z / a.k_parts);
   const int s1 = static_cast<int>(static_cast<int64_t>(steps) * (blockIdx.z + 1) / a.k_parts);
-  const T *row[kR], *low[kR];
+  int64_t r = static_cast<int64_t>(blockIdx.y) * 16 + (lane & 15);
+  r = r < a.rows ? r : a.rows - 1;  // computed, not stored
+  const T* row = a.x + r * a.ldx;
+  const T* low = kLow ? a.low + r * a.ldx : nullptr;
+  f32x4_t acc[kW][4];
 #pragma unroll
-  for (int i = 0; i < kR; ++i) {
-    int64_t r = r0 + 16 * i + (lane & 15);
-    r = r < a.rows ? r : a.rows - 1;  // computed, not stored
-    row[i] = a.x + r * a.ldx;
-    low[i] = kLow ? a.low + r * a.ldx : nullptr;
-  }
-  f32x4_t acc[kR][kW][4];
+  for (int m = 0; m < kW; ++m)
 #pragma unroll
-  for (int i = 0; i < kR; ++i)
-#pragma unroll
-    for (int m = 0; m < kW; ++m)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][m][j] = (f32x4_t){0.0f, 0.0f, 0.0f, 0.0f};
+    for (int j = 0; j < 4; ++j) acc[m][j] = (f32x4_t){0.0f, 0.0f, 0.0f, 0.0f};
 
   SkinnyW<T> w[2][kW];
-  SkinnyX<T> x[2][kR], xl[2][kLow ? kR : 1];
+  SkinnyX<T> x[2], xl[2];
   auto load = [&](int set, int s) {
 #pragma unroll
     for (int m = 0; m < kW; ++m) w[set][m].load(a.w[m], a.N, s * kSkinnyStep, a.K, n, a.N, lane);
-#pragma unroll
-    for (int i = 0; i < kR; ++i) {
-      x[set][i].load(row[i], s * kSkinnyStep, a.K, lane);
-      if (kLow) xl[set][i].load(low[i], s * kSkinnyStep, a.K, lane);
-    }
+    x[set].load(row, s * kSkinnyStep, a.K, lane);
+    if (kLow) xl[set].load(low, s * kSkinnyStep, a.K, lane);
   };
   auto multiply = [&](int set) {
 #pragma unroll
-    for (int i = 0; i < kR; ++i)
-#pragma unroll
-      for (int m = 0; m < kW; ++m) {
-        skinny_step(w[set][m], x[set][i], acc[i][m]);
-        if (kLow) skinny_step(w[set][m], xl[set][i], acc[i][m]);
-      }
+    for (int m = 0; m < kW; ++m) {
+      skinny_step(w[set][m], x[set], acc[m]);
+      if (kLow) skinny_step(w[set][m], xl[set], acc[m]);
+    }
   };
   // two steps in flight
   int s = s0 + wave;
@@ -192,24 +178,22 @@ __device__ __forceinline__ void skinny_sums(const SkinnyArgs<T, kW>& a, float (*
 
   const int c = lane;  // column that this thread adds up
 #pragma unroll
-  for (int i = 0; i < kR; ++i)
+  for (int m = 0; m < kW; ++m) {
+    // register q of fragment j is column 4 q + j of the lane's 16
 #pragma unroll
-    for (int m = 0; m < kW; ++m) {
-      // register q of fragment j is column 4 q + j of the lane's 16
+    for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+      for (int q = 0; q < 4; ++q) lds[wave][(4 * q + j) * 65 + lane] = acc[m][j][q];
+    __syncthreads();
 #pragma unroll
-        for (int q = 0; q < 4; ++q) lds[wave][(4 * q + j) * 65 + lane] = acc[i][m][j][q];
-      __syncthreads();
+    for (int v = 0; v < 2; ++v) {
+      float t = 0.0f;
 #pragma unroll
-      for (int v = 0; v < 2; ++v) {
-        float t = 0.0f;
-#pragma unroll
-        for (int u = 0; u < kSkinnyWaves; ++u) t += lds[u][(c & 15) * 65 + (c >> 4) * 16 + wave + 8 * v];
-        sum[i][v][m] = t;
-      }
-      __syncthreads();
+      for (int u = 0; u < kSkinnyWaves; ++u) t += lds[u][(c & 15) * 65 + (c >> 4) * 16 + wave + 8 * v];
+      sum[v][m] = t;
     }
+    __syncthreads();
+  }
 }
 
 }  // namespace moe
