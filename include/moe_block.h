@@ -147,10 +147,11 @@ int64_t moe_i8_pitch(int32_t width);
  *   scale[t] = max_j |x[t,j]| * (1 / 127),  q[t,j] = rint(x[t,j] / scale[t])
  * in fp32, 1 / 127 a number of fp32 and the division rounded to nearest, rint
  * to nearest even, clamped to [-127, 127]: what torch makes on this device of
- * scale = x.abs().amax(1) / 127, q = round(x / scale). A zero row has scale 0 and q 0; a row with an infinity or a
- * NaN has scale NaN and q 0, so that whatever is made of it is NaN. q is
- * [rows, moe_i8_pitch(width)], its padding zeroed. It is the layout of
- * activations and, with a row for each output channel, of weights.
+ * scale = x.abs().amax(1) / 127, q = round(x / scale). A zero row has scale 0
+ * and q 0; a row with an infinity or a NaN has scale NaN and q 0, so that
+ * whatever is made of it is NaN. q is [rows, moe_i8_pitch(width)], its padding
+ * zeroed. It is the layout of activations and, with a row for each output
+ * channel, of weights.
  * Supported: rows < 2^31, width <= 65536.
  */
 int moe_quantize_rows(int64_t rows, int32_t width, int32_t dtype, const void* x, int64_t ld_x,

@@ -674,6 +674,39 @@ def test_answering_in_a_graph():
         torch.cuda.synchronize()
 
 
+def test_linear_i8_routing_changes_between_replays():
+    """The tiles are counted on the device: a captured product follows rows
+    that gather in one expert, spread over all, or leave most without any."""
+    import torch
+    note("linear_i8 replays")
+    t, k, n, e = 130, 200, 192, 16
+    r = gen(3)
+    x, w = r(t, k, dtype="bf16"), r(e, k, n, std=k ** -0.5)
+    wq, ws = K.quantize_weights(w)
+    l = K.LinearI8(t, k, n, "bf16", groups=e)
+    buf = K.allocate_linear_i8(l)
+    routing = {"perm": torch.arange(t, dtype=torch.int32, device="cuda"),
+               "expert_offsets": torch.zeros(e + 1, dtype=torch.int32, device="cuda")}
+    routing["expert_offsets"][1:] = t
+    K.linear_i8(l, x, wq, ws, buf, routing=routing)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        K.linear_i8(l, x, wq, ws, buf, routing=routing)
+    xd = dequantized(x)
+    for chosen in ([15], list(range(16)), [0], [3, 9], [0, 15]):
+        idx = torch.tensor([chosen[i * 7 % len(chosen)] for i in range(t)], device="cuda")
+        routing["perm"].copy_(torch.sort(idx, stable=True).indices)
+        routing["expert_offsets"][1:] = torch.cumsum(torch.bincount(idx, minlength=e), 0)
+        buf.y.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        order = routing["perm"].long()
+        wd = wq[:, :, :k].double() * ws.double()[:, :, None]
+        want = torch.stack([xd[i] @ wd[idx[i]].t() for i in order.tolist()])
+        near(f"experts {chosen}", buf.y, want, U["bf16"] + 2.0 ** -20)
+
+
 def test_int8_experts_in_the_layer():
     """Serving with 8-bit experts: route, permute, gated product, product,
     combine, against the layer with the experts' weights as they were rounded."""
