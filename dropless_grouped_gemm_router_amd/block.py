@@ -208,6 +208,15 @@ def _want_rows(name, t, shape, dtype, device) -> int:
     return row if shape[0] > 1 else shape[1]
 
 
+def _want_bytes(name, t, least, device):
+    """``t`` is a contiguous buffer of bytes on this device, of ``least`` or more."""
+    if t.dtype is torch.uint8 and t.device == device and t.numel() >= least and t.is_contiguous():
+        return
+    if t.numel() < least:
+        raise ValueError(f"{name}: {t.numel()} bytes, {least} are needed: allocated for another problem?")
+    _refuse(name, t, t.shape, torch.uint8, device)
+
+
 def _code(t) -> int:
     if t.dtype not in _CODE:
         raise ValueError(f"{t.dtype}: float32 or bfloat16 is supported")
@@ -270,7 +279,7 @@ def allocate_norm(rows: int, width: int, dtype, device="cuda", training: bool = 
         b.grad_x = torch.empty((rows, width), dtype=dt, device=device)
         b.grad_weight, b.grad_bias = torch.empty(width, **f32), torch.empty(width, **f32)
         b.workspace = torch.empty(nws, dtype=torch.uint8, device=device)
-    b.made = (b.y.shape, dt, device, b.y, b.mean, b.rstd, b.grad_x, b.grad_weight, b.grad_bias)
+    b.made = (b.y.shape, dt, device, b.y, b.mean, b.rstd, b.grad_x, b.grad_weight, b.grad_bias, b.workspace)
     return b
 
 
@@ -315,7 +324,7 @@ def layer_norm_backward(x, weight, grad_out, buf: NormBuffers, stream=None):
         _want("weight", weight, (width,), f32, dev)
     m = buf.made
     if (m and gx is m[6] and gw is m[7] and gb is m[8] and buf.mean is m[4] and buf.rstd is m[5]
-            and m[0] == shape and m[1] is dt and m[2] == dev):
+            and buf.workspace is m[9] and m[0] == shape and m[1] is dt and m[2] == dev):
         ld_gx = width
     else:
         ld_gx = _want_rows("grad_x", gx, shape, dt, dev)
@@ -323,6 +332,7 @@ def layer_norm_backward(x, weight, grad_out, buf: NormBuffers, stream=None):
         _want("rstd", buf.rstd, (rows,), f32, dev)
         _want("grad_weight", gw, (width,), f32, dev)
         _want("grad_bias", gb, (width,), f32, dev)
+        _want_bytes("workspace", buf.workspace, 0, dev)
     n = _norm(rows, width, _code(x), 0.0, ld_x, 0, ld_go, ld_gx)
     _run("moe_layer_norm_bwd", dev, stream, load().moe_layer_norm_bwd, n[1], x.data_ptr(),
          None if weight is None else weight.data_ptr(), buf.mean.data_ptr(), buf.rstd.data_ptr(), grad_out.data_ptr(), gx.data_ptr(),
@@ -351,7 +361,7 @@ class GatedFfn:
 @lru_cache(maxsize=256)
 def _ffn(*fields):
     f = moe_ffn(*fields)
-    return f, ctypes.byref(f)
+    return f, ctypes.byref(f), moe_gated_ffn_saved_bytes(f)
 
 
 @dataclass
@@ -390,16 +400,24 @@ def _want_ffn(f, x, weights):
     _want("w_gate", wg, up, dt, dev)
     _want("w_up", wu, up, dt, dev)
     _want("w_down", wd, up[::-1], dt, dev)
-    c = _ffn(f.tokens, f.d_model, f.d_hidden, DTYPES[f.dtype], ACTS[f.act], DTYPES[f.grad_dtype])[1]
-    return dt, dev, c, wg.data_ptr(), wu.data_ptr(), wd.data_ptr()
+    _, c, nsv = _ffn(f.tokens, f.d_model, f.d_hidden, DTYPES[f.dtype], ACTS[f.act], DTYPES[f.grad_dtype])
+    return dt, dev, c, nsv, wg.data_ptr(), wu.data_ptr(), wd.data_ptr()
+
+
+def _want_saved(buf, least, device):
+    # the library is not told this buffer's size
+    if buf.saved is None:
+        raise ValueError("the buffers were allocated without training=True")
+    _want_bytes("saved", buf.saved, least, device)
 
 
 def gated_ffn(f: GatedFfn, x, weights: Dict, buf: FfnBuffers, training: bool = False, stream=None):
     """The block's forward pass (weights: w_gate, w_up, w_down); returns buf.out."""
-    dt, dev, c, wg, wu, wd = _want_ffn(f, x, weights)
+    dt, dev, c, nsv, wg, wu, wd = _want_ffn(f, x, weights)
     _want("out", buf.out, (f.tokens, f.d_model), dt, dev)
-    if training and buf.saved is None:
-        raise ValueError("the buffers were allocated without training=True")
+    _want_bytes("workspace", buf.workspace, 0, dev)
+    if training:
+        _want_saved(buf, nsv, dev)
     _run("moe_gated_ffn", dev, stream, load().moe_gated_ffn, c, x.data_ptr(), wg, wu, wd,
          buf.saved.data_ptr() if training else None, buf.out.data_ptr(), buf.workspace.data_ptr(),
          buf.workspace.numel())
@@ -409,9 +427,9 @@ def gated_ffn(f: GatedFfn, x, weights: Dict, buf: FfnBuffers, training: bool = F
 def gated_ffn_backward(f: GatedFfn, x, weights: Dict, grad_out, buf: FfnBuffers, stream=None):
     """Gradients of sum(out * grad_out) after ``gated_ffn(..., training=True)``:
     (grad_x, {w_gate, w_up, w_down})."""
-    dt, dev, c, wg, wu, wd = _want_ffn(f, x, weights)
-    if buf.saved is None:
-        raise ValueError("the buffers were allocated without training=True")
+    dt, dev, c, nsv, wg, wu, wd = _want_ffn(f, x, weights)
+    _want_saved(buf, nsv, dev)
+    _want_bytes("workspace", buf.workspace, 0, dev)
     _want("grad_out", grad_out, (f.tokens, f.d_model), dt, dev)
     _want("grad_x", buf.grad_x, (f.tokens, f.d_model), dt, dev)
     g, gdt = buf.grads, _TORCH[f.grad_dtype]
@@ -537,6 +555,7 @@ def linear_i8(l: LinearI8, x, wq, w_scale, buf: I8Buffers, bias=None, routing: O
         r = ctypes.byref(routing_struct(routing))
     y = buf.y
     _want("y", y, (l.rows, l.columns), _TORCH[l.dtype], dev)
+    _want_bytes("workspace", buf.workspace, 0, dev)
     _run("moe_linear_i8", dev, stream, load().moe_linear_i8, c, x.data_ptr(), xs, wq.data_ptr(),
          w_scale.data_ptr(), _ptr(bias), r, y.data_ptr(), buf.workspace.data_ptr(),
          buf.workspace.numel())

@@ -220,3 +220,49 @@ def test_tensor_checks():
     with pytest.raises(ValueError, match="x_scale"):
         K.linear_i8(l, torch.zeros(4, 128, dtype=torch.int8), torch.zeros(1, 16, 128, dtype=torch.int8),
                     torch.zeros(1, 16), K.I8Buffers(y=torch.zeros(4, 16), workspace=x))
+
+
+def ffn_tensors(t, d, h):
+    import torch
+    make = lambda *shape: torch.zeros(*shape, dtype=torch.bfloat16)
+    return make(t, d), dict(w_gate=make(d, h), w_up=make(d, h), w_down=make(h, d)), make(t, d)
+
+
+# A workspace is not larger for every larger d_hidden (widths that are no
+# multiple of 128 or 64 take copies of the weights), so its size, which the
+# library checks, does not stand for that of `saved`.
+@pytest.mark.parametrize("t,d,small,large", [(8, 512, 1000, 1152), (300, 2048, 64, 4096)])
+def test_ffn_buffers_of_another_block(t, d, small, large):
+    made = K.allocate_ffn(K.GatedFfn(t, d, small), "cpu", training=True)
+    f = K.GatedFfn(t, d, large)
+    assert made.workspace.numel() >= K.moe_gated_ffn_workspace_bytes(f.struct(), True)
+    assert made.saved.numel() < K.moe_gated_ffn_saved_bytes(f.struct())
+    x, w, dy = ffn_tensors(t, d, large)
+    with pytest.raises(ValueError, match="saved: .* bytes"):
+        K.gated_ffn(f, x, w, made, training=True)
+    made.grads = K.allocate_ffn(f, "cpu", training=True).grads
+    with pytest.raises(ValueError, match="saved: .* bytes"):
+        K.gated_ffn_backward(f, x, w, dy, made)
+
+
+@pytest.mark.parametrize("what", ["saved", "workspace"])
+def test_byte_buffers_of_another_device_or_type(what):
+    """`saved` and workspaces are bytes on the tensors' device."""
+    import torch
+    f, (x, w, dy) = K.GatedFfn(20, 64, 128), ffn_tensors(20, 64, 128)
+    l, n = K.LinearI8(20, 64, 128), K.allocate_norm(20, 64, "bf16", "cpu", training=True)
+    wq, ws = torch.zeros(1, 128, 128, dtype=torch.int8), torch.zeros(1, 128)
+    b, i = K.allocate_ffn(f, "cpu", training=True), K.allocate_linear_i8(l, "cpu")
+    size = getattr(b, what).numel()
+    for wrong in (torch.empty(size, dtype=torch.uint8, device="meta"), torch.empty(size, dtype=torch.float32),
+                  torch.empty(2 * size, dtype=torch.uint8)[::2]):
+        setattr(b, what, wrong)
+        i.workspace = n.workspace = wrong
+        with pytest.raises(ValueError, match=what):
+            K.gated_ffn(f, x, w, b, training=True)
+        with pytest.raises(ValueError, match=what):
+            K.gated_ffn_backward(f, x, w, dy, b)
+        with pytest.raises(ValueError, match="workspace"):
+            K.linear_i8(l, x, wq, ws, i)
+        with pytest.raises(ValueError, match="workspace"):
+            K.layer_norm_backward(x, None, dy, n)
