@@ -353,9 +353,14 @@ class GatedFfn:
     act: str = "silu"
     grad_dtype: str = "fp32"  # of the weight gradients: fp32, or dtype
 
+    @property
+    def _fields(self):
+        return (self.tokens, self.d_model, self.d_hidden, DTYPES[self.dtype], ACTS[self.act],
+                DTYPES[self.grad_dtype])
+
     def struct(self) -> moe_ffn:
-        return _ffn(self.tokens, self.d_model, self.d_hidden, DTYPES[self.dtype], ACTS[self.act],
-                    DTYPES[self.grad_dtype])[0]
+        """The C problem, the caller's own to change."""
+        return moe_ffn(*self._fields)
 
 
 @lru_cache(maxsize=256)
@@ -400,7 +405,7 @@ def _want_ffn(f, x, weights):
     _want("w_gate", wg, up, dt, dev)
     _want("w_up", wu, up, dt, dev)
     _want("w_down", wd, up[::-1], dt, dev)
-    _, c, nsv = _ffn(f.tokens, f.d_model, f.d_hidden, DTYPES[f.dtype], ACTS[f.act], DTYPES[f.grad_dtype])
+    _, c, nsv = _ffn(*f._fields)
     return dt, dev, c, nsv, wg.data_ptr(), wu.data_ptr(), wd.data_ptr()
 
 
@@ -471,13 +476,15 @@ class LinearI8:
         return self.rows if self.sorted_input else self.tokens
 
     def struct(self, x_dtype: int, routed: bool) -> moe_i8_linear:
-        return _i8(self, x_dtype, routed)[0]
+        """The C problem, the caller's own to change."""
+        return moe_i8_linear(self.tokens, self.inputs, self.outputs, x_dtype, DTYPES[self.dtype],
+                             self.groups, self.top_k, int(routed and not self.sorted_input),
+                             int(self.gated), self.capacity)
 
 
 @lru_cache(maxsize=256)
 def _i8(l, x_dtype, routed):
-    c = moe_i8_linear(l.tokens, l.inputs, l.outputs, x_dtype, DTYPES[l.dtype], l.groups, l.top_k,
-                      int(routed and not l.sorted_input), int(l.gated), l.capacity)
+    c = l.struct(x_dtype, routed)
     return c, ctypes.byref(c), moe_i8_pitch(l.inputs)
 
 

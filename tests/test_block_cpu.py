@@ -266,3 +266,17 @@ def test_byte_buffers_of_another_device_or_type(what):
             K.linear_i8(l, x, wq, ws, i)
         with pytest.raises(ValueError, match="workspace"):
             K.layer_norm_backward(x, None, dy, n)
+
+
+def test_problem_structs_are_the_callers_own():
+    """What a caller changes in a problem's struct reaches no other call."""
+    f, l = K.GatedFfn(300, 192, 320), K.LinearI8(300, 192, 320)
+    ffn_size = K.allocate_ffn(f, "cpu", training=True).workspace.numel()
+    i8_size = K.allocate_linear_i8(l, "cpu").workspace.numel()
+    f.struct().d_hidden = 64
+    l.struct(B.MOE_FP32, False).tokens = 1
+    assert f.struct().d_hidden == 320 and l.struct(B.MOE_FP32, False).tokens == 300
+    assert K.allocate_ffn(f, "cpu", training=True).workspace.numel() == ffn_size
+    assert K.allocate_linear_i8(l, "cpu").workspace.numel() == i8_size
+    # the structs that calls take are kept by value: none was handed out
+    assert K._ffn(*f._fields)[0].d_hidden == 320 and K._i8(l, B.MOE_FP32, False)[0].tokens == 300
