@@ -223,10 +223,14 @@ def _code(t) -> int:
     return _CODE[t.dtype]
 
 
-def _run(where, device, stream, fn, *args):
-    """fn(*args, stream) on the tensors' device."""
+def _want_gpu(device):
     if device.type != "cuda":
         raise ValueError(f"tensors have to be on a GPU, not on {device}")
+
+
+def _run(where, device, stream, fn, *args):
+    """fn(*args, stream) on the tensors' device."""
+    _want_gpu(device)
     # the raw handle: a tenth of the time of making a torch.cuda.Stream
     s = torch._C._cuda_getCurrentRawStream(device.index) if stream is None else _stream(stream)
     if torch.cuda.current_device() != device.index:
@@ -571,11 +575,74 @@ def linear_i8(l: LinearI8, x, wq, w_scale, buf: I8Buffers, bias=None, routing: O
 
 # ------------------------------------------------------- with the layer itself
 
+@dataclass(frozen=True)
+class _Layer:
+    """What the layer's stages take for a problem, as (name, shape, type)."""
+
+    x: tuple
+    routing: tuple
+    weights: tuple
+    grads: tuple
+    sorted: tuple
+    shared: bool
+    tiles: int
+    saved: int
+
+
+@lru_cache(maxsize=256)
+def _layer(T, E, k, d, h, hs, dtype, block_m, capacity):
+    c = ctypes.byref(binding.moe_problem(T, E, k, d, h, hs, dtype, block_m, capacity))
+    lib, dt, f32, i32 = _load_library(), _TORCH[dtype], torch.float32, torch.int32
+    w = [("w_gate", (E, d, h)), ("w_up", (E, d, h)), ("w_down", (E, h, d))]
+    if hs > 0:
+        w += [("ws_gate", (d, hs)), ("ws_up", (d, hs)), ("ws_down", (hs, d))]
+    size, tiles = torch.Size, int(lib.moe_max_tiles(c))  # no tiles: a problem that the library refuses
+    return _Layer((size((T, d)), dt),
+                  tuple((n, size(s), t) for n, s, t in (
+                      ("topk_idx", (T, k), i32), ("topk_w", (T, k), f32), ("expert_offsets", (E + 1,), i32),
+                      ("perm", (T * k,), i32), ("inv_perm", (T * k,), i32), ("num_tiles", (1,), i32))),
+                  tuple([("w_router", size((d, E)), f32)] + [(n, size(s), dt) for n, s in w]),
+                  tuple([("w_router", size((d, E)), f32)] + [(n, size(s), f32) for n, s in w]),
+                  (size((T * k, d)), dt), hs > 0, tiles, int(lib.moe_saved_bytes(c)))
+
+
+def _want_all(what, tensors, specs, device):
+    for name, shape, dtype in specs:
+        _want(what + name, tensors[name], shape, dtype, device)
+
+
+def _want_layer(p, name, x, buf, weights: Optional[Dict] = None, training: bool = False, grad_out=None):
+    """The layer's input, buffers and, where they are given, weights and
+    output gradient fit its problem: ``binding`` passes their pointers on as
+    they are."""
+    l = _layer(p.tokens, p.experts, p.top_k, p.d_model, p.d_hidden, p.d_shared, _dtype(p.dtype), p.block_m,
+               getattr(p, "capacity", 0))
+    dev, r = x.device, buf.routing
+    _want(name, x, *l.x, dev)
+    _want_all("", r, l.routing, dev)
+    _want("tiles", r["tiles"], (max(1, l.tiles, r["tiles"].shape[0]), 3), torch.int32, dev)
+    _want("out", buf.out, *l.x, dev)
+    _want_bytes("workspace", buf.workspace, 0, dev)
+    if weights is not None:
+        _want_all("", weights, l.weights, dev)
+        _want("y_sorted", buf.y_sorted, *l.sorted, dev)
+        if l.shared:
+            _want("shared_out", buf.shared_out, *l.x, dev)
+        if training:
+            _want_saved(buf, l.saved, dev)
+    if grad_out is not None:
+        _want("grad_out", grad_out, *l.x, dev)
+        _want("grad_x of the layer", buf.grad_x, *l.x, dev)
+        _want_all("gradient of ", buf.grads, l.grads, dev)
+    _want_gpu(dev)
+
+
 def prenorm_forward(p, x, weights: Dict, buf, norm: NormBuffers, eps: float = 1e-5,
                     training: bool = False, stream=None):
     """The MoE layer behind its norm, MoE(norm(x)): ``binding.forward`` on
     the normalised tokens; weights holds norm_weight and norm_bias (either may
     be missing) beside the layer's own. Returns buf.out."""
+    _want_layer(p, "y of the norm", norm.y, buf, weights, training)
     h = layer_norm(x, weights.get("norm_weight"), weights.get("norm_bias"), eps, norm, stream)
     with torch.cuda.device(x.device):
         return binding.forward(p, h, weights, buf, training=training, stream=stream)
@@ -586,6 +653,9 @@ def prenorm_backward(p, x, weights: Dict, grad_out, buf, norm: NormBuffers, stre
     """Gradients of sum(out * grad_out) after prenorm_forward(..., training=True)
     with the same buffers: (grad_x, the layer's weight gradients with
     norm_weight and norm_bias beside them)."""
+    if buf.grads is None:
+        raise ValueError("the buffers were allocated without training=True")
+    _want_layer(p, "y of the norm", norm.y, buf, weights, True, grad_out)
     with torch.cuda.device(x.device):
         gh, grads = binding.backward(p, norm.y, weights, grad_out, buf, stream=stream,
                                      side_stream=side_stream)
@@ -603,13 +673,21 @@ class ExpertsI8Buffers:
     sorted: I8Buffers
 
 
+@lru_cache(maxsize=256)
+def _experts(tokens, experts, top_k, d_model, d_hidden, dtype, cap):
+    name = "bf16" if dtype == MOE_BF16 else "fp32"
+    up = LinearI8(tokens, d_model, 2 * d_hidden, name, experts, top_k, gated=True, capacity=cap)
+    down = LinearI8(tokens, d_hidden, d_model, name, experts, top_k, sorted_input=True, capacity=cap)
+    return up, down
+
+
+def _experts_of(p):
+    return _experts(p.tokens, p.experts, p.top_k, p.d_model, p.d_hidden, _dtype(p.dtype),
+                    int(getattr(p, "capacity", 0)))
+
+
 def allocate_experts_i8(p, device="cuda") -> ExpertsI8Buffers:
-    name = "bf16" if _dtype(p.dtype) == MOE_BF16 else "fp32"
-    cap = int(getattr(p, "capacity", 0))
-    up = LinearI8(p.tokens, p.d_model, 2 * p.d_hidden, name, p.experts, p.top_k, gated=True,
-                  capacity=cap)
-    down = LinearI8(p.tokens, p.d_hidden, p.d_model, name, p.experts, p.top_k, sorted_input=True,
-                    capacity=cap)
+    up, down = _experts_of(p)
     return ExpertsI8Buffers(up, down, allocate_linear_i8(up, device), allocate_linear_i8(down, device))
 
 
@@ -620,6 +698,12 @@ def forward_i8(p, x, w_router, gate_up, down, buf, experts: ExpertsI8Buffers, sh
     (q, scale) pairs of ``quantize_weights(w_gate, w_up)`` and
     ``quantize_weights(w_down)``; buf is ``binding.allocate(p)``, and a shared
     expert's output may be given to be added. Returns buf.out."""
+    _want("w_router", w_router, (p.d_model, p.experts), torch.float32, x.device)
+    if shared_out is not None:
+        _want("shared_out", shared_out, x.shape, x.dtype, x.device)
+    if (experts.gate_up, experts.down) != _experts_of(p):
+        raise ValueError(f"experts: buffers of {experts.gate_up} and {experts.down}, not of {p}")
+    _want_layer(p, "x", x, buf)
     with torch.cuda.device(x.device):
         binding.moe_route(p, x, w_router, buf.routing, stream)
         binding.moe_permute(p, buf.routing, buf.workspace, stream=stream)

@@ -280,3 +280,83 @@ def test_problem_structs_are_the_callers_own():
     assert K.allocate_linear_i8(l, "cpu").workspace.numel() == i8_size
     # the structs that calls take are kept by value: none was handed out
     assert K._ffn(*f._fields)[0].d_hidden == 320 and K._i8(l, B.MOE_FP32, False)[0].tokens == 300
+
+
+def layer_case(dtype="bf16", **kw):
+    """A layer's problem, input, weights, output gradient, its buffers and its norm's."""
+    import torch
+    from dropless_grouped_gemm_router_amd.inputs import Problem
+    p = Problem(**{**dict(tokens=12, experts=4, top_k=2, d_model=128, d_hidden=128, d_shared=128, dtype=dtype,
+                          block_m=32), **kw})
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    E, d, h, hs = p.experts, p.d_model, p.d_hidden, p.d_shared
+    w = dict(w_router=torch.zeros(d, E), w_gate=torch.zeros(E, d, h, dtype=dt), w_up=torch.zeros(E, d, h, dtype=dt),
+             w_down=torch.zeros(E, h, d, dtype=dt), ws_gate=torch.zeros(d, hs, dtype=dt),
+             ws_up=torch.zeros(d, hs, dtype=dt), ws_down=torch.zeros(hs, d, dtype=dt))
+    return (p, torch.zeros(p.tokens, d, dtype=dt), w, torch.zeros(p.tokens, d, dtype=dt),
+            B.allocate(p, "cpu", training=True), K.allocate_norm(p.tokens, d, dtype, "cpu", training=True))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_layer_behind_its_norm_refusals(dtype):
+    """The layer's stages only pass pointers on: inputs, weights, gradients and
+    buffers that are not the problem's are refused before any of them runs."""
+    import torch
+    p, x, w, dy, buf, nb = layer_case(dtype)
+    for fn in (lambda: K.prenorm_forward(p, x, w, buf, nb, training=True),
+               lambda: K.prenorm_backward(p, x, w, dy, buf, nb)):
+        with pytest.raises(ValueError, match="GPU"):
+            fn()
+    # an output gradient as sum().backward() makes it: one element, expanded
+    with pytest.raises(ValueError, match="grad_out"):
+        K.prenorm_backward(p, x, w, dy[:1, :1].expand(12, 128), buf, nb)
+    with pytest.raises(ValueError, match="grad_out"):
+        K.prenorm_backward(p, x, w, dy.half(), buf, nb)
+    for name in w:
+        for wrong in (w[name].transpose(-1, -2), w[name][..., :-1].contiguous(), w[name].half()):
+            with pytest.raises(ValueError, match=name):
+                K.prenorm_forward(p, x, {**w, name: wrong}, buf, nb)
+            with pytest.raises(ValueError, match=name):
+                K.prenorm_backward(p, x, {**w, name: wrong}, dy, buf, nb)
+    # buffers of the layer with fewer tokens, fewer experts, or another width
+    for kw in (dict(tokens=11), dict(experts=3), dict(top_k=1), dict(d_hidden=64), dict(d_shared=64)):
+        q, qx, qw, qdy, qbuf, qnb = layer_case(dtype, **kw)
+        with pytest.raises(ValueError, match="shape|bytes"):
+            K.prenorm_forward(p, x, w, qbuf, nb, training=True)
+        buf2 = B.allocate(p, "cpu", training=True)
+        buf2.saved = qbuf.saved
+        if qbuf.saved.numel() < buf.saved.numel():
+            with pytest.raises(ValueError, match="saved"):
+                K.prenorm_forward(p, x, w, buf2, nb, training=True)
+            with pytest.raises(ValueError, match="saved"):
+                K.prenorm_backward(p, x, w, dy, buf2, nb)
+    # normalised rows that lie apart
+    nb.y = torch.zeros(12, 256, dtype=x.dtype)[:, :128]
+    with pytest.raises(ValueError, match="y of the norm"):
+        K.prenorm_forward(p, x, w, buf, nb)
+    with pytest.raises(ValueError, match="training"):
+        K.prenorm_backward(p, x, w, dy, B.allocate(p, "cpu"), nb)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_layer_with_8_bit_experts_refusals(dtype):
+    import torch
+    p, x, w, _, buf, _ = layer_case(dtype)
+    q8 = lambda rows, width: (torch.zeros(4, rows, width, dtype=torch.int8), torch.zeros(4, rows))
+    gu, dn, ex = q8(256, 128), q8(128, 128), K.allocate_experts_i8(p, "cpu")
+    with pytest.raises(ValueError, match="GPU"):
+        K.forward_i8(p, x, w["w_router"], gu, dn, buf, ex)
+    for wrong in (x[:11], x.t().contiguous().t(), x.half(), x[:1].expand(12, 128)):
+        with pytest.raises(ValueError, match="x: "):
+            K.forward_i8(p, wrong, w["w_router"], gu, dn, buf, ex)
+    with pytest.raises(ValueError, match="w_router"):
+        K.forward_i8(p, x, w["w_router"].t(), gu, dn, buf, ex)
+    with pytest.raises(ValueError, match="shared_out"):
+        K.forward_i8(p, x, w["w_router"], gu, dn, buf, ex, shared_out=x[:11])
+    for kw in (dict(tokens=11), dict(experts=3), dict(top_k=1), dict(d_hidden=64)):
+        q, *_, qbuf, _ = layer_case(dtype, **kw)
+        with pytest.raises(ValueError, match="experts"):
+            K.forward_i8(p, x, w["w_router"], gu, dn, buf, K.allocate_experts_i8(q, "cpu"))
+        if "d_hidden" not in kw:  # nothing that this path uses of the buffers knows it
+            with pytest.raises(ValueError, match="shape"):
+                K.forward_i8(p, x, w["w_router"], gu, dn, qbuf, ex)
