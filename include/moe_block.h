@@ -109,7 +109,7 @@ size_t moe_gated_ffn_workspace_bytes(const moe_ffn* f, int training);
 
 /* Bytes (host) of the buffer that moe_gated_ffn fills for
  * moe_gated_ffn_bwd: h in dtype, and act(a) and b act'(a), in fp32 or, in
- * bf16, as the 20 high bits of their fp32 values. */
+ * bf16, rounded to 20 bits (2^-12). */
 size_t moe_gated_ffn_saved_bytes(const moe_ffn* f);
 
 /* Forward. saved: NULL for inference, or moe_gated_ffn_saved_bytes(f) bytes
