@@ -290,7 +290,10 @@ __global__ __launch_bounds__(64 * kRowsWaves) void i8_few_kernel(const I8Few p, 
   extern __shared__ __attribute__((aligned(16))) char rows_q[];  // [rows][pitch + 16], unless kInt
   __shared__ float scale[16];
   __shared__ int sums[kRowsWaves][kW][16 * 16];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  // The wave's number as a scalar: MFMAs run whatever lanes are on, so a step
+  // past the end has to be branched over, which is only certain for a scalar
+  // condition.
+  const int lane = threadIdx.x & 63, wave = mm_wave();
   const int n0 = blockIdx.x * 16;
   const int8_t* w[kW];
 #pragma unroll

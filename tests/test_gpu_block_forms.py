@@ -1,12 +1,12 @@
 """Forms of the operators around the layer that need a look of their own: what
-the gated block keeps of its activations."""
+the gated block keeps of its activations, and the dense gated 8-bit product."""
 
 import pytest
 
 from dropless_grouped_gemm_router_amd import block as K
 
 from gpu_util import note
-from test_gpu_block import act64, ffn64, ffn_case
+from test_gpu_block import U, act64, ffn64, ffn_case, gen, quantized
 
 pytestmark = pytest.mark.gpu
 
@@ -104,3 +104,80 @@ def test_ffn_kept_activations_that_are_not_finite():
         for got, want in zip(kept, (act, slope)):
             assert torch.equal(got.isnan(), want.isnan())
             assert torch.equal(got.isposinf(), want.isposinf()) and torch.equal(got.isneginf(), want.isneginf())
+
+
+# ------------------------------------------- the dense gated product in 8 bits
+
+def product64(q, s, wq, ws):
+    """The product of integers, exact in 64 bits (a sum that is 0 is 0), by the
+    rows' and the weights' scales."""
+    k = q.shape[1]
+    return (q.double() @ wq[:, :k].double().t()) * s.double()[:, None] * ws.double()
+
+
+def integers(x):
+    """The definition's (integers, scales) of the rows of x, on the device."""
+    import torch
+    return [torch.from_numpy(v).cuda() for v in quantized(x)]
+
+
+def each(name, got, gate, up, dtype):
+    """Every element: the result's rounding (and 2^-20 of the scalings), and the
+    SiLU: the gate is 2^-22 off after three roundings, which its slope of at most
+    1.1 passes on, the logistic function another 2^-22: 2^-20 of the gate,
+    2^-19 of gate times up with the up value's own."""
+    import torch
+    want = gate * torch.sigmoid(gate) * up
+    over = (got.double() - want).abs() - (U[dtype] + 2.0 ** -20) * want.abs() - 2.0 ** -19 * (gate * up).abs()
+    assert got.shape == want.shape and bool(torch.isfinite(got.float()).all()), name
+    assert float(over.max()) <= 0, (name, float(over.max()))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("t,k,h", [
+    (1, 1, 1), (1, 512, 33), (4, 4096, 256), (7, 130, 17), (8, 1000, 257), (2, 5000, 65), (8, 2000, 515),  # few rows
+    (9, 1100, 129), (16, 2000, 515), (16, 1152, 8191),
+    (9, 1000, 257), (17, 640, 65), (3, 200, 8200), (64, 333, 1001), (100, 1111, 515),  # 64 x 64 tiles
+    (1100, 200, 2001), (2100, 300, 2101), (4200, 1100, 2051)])  # 128 x 128, 256 x 128, 256 x 256
+def test_linear_i8_dense_gated(t, k, h, dtype):
+    import torch
+    note(f"linear_i8 dense gated {t} {k} {h} {dtype}")
+    r = gen(t + k + h)
+    x, g, u = r(t, k, dtype=dtype), r(k, h, std=k ** -0.5), r(k, h, std=k ** -0.5)
+    wq, ws = K.quantize_weights(g, u)
+    l = K.LinearI8(t, k, 2 * h, dtype, gated=True)
+    buf = K.allocate_linear_i8(l)
+    assert buf.y.shape == (t, h)
+    gate, up = product64(*integers(x), wq[0], ws[0]).chunk(2, 1)
+    each("y", K.linear_i8(l, x, wq, ws, buf), gate, up, dtype)
+    first = buf.y.clone()
+    # rows that are already in 8 bits give the same bits, into either type
+    q, s = K.quantize_rows(x)
+    assert torch.equal(K.linear_i8(l, q, wq, ws, buf, x_scale=s), first)
+    other = "fp32" if dtype == "bf16" else "bf16"
+    lo = K.LinearI8(t, k, 2 * h, other, gated=True)
+    each("other type", K.linear_i8(lo, x, wq, ws, K.allocate_linear_i8(lo)), gate, up, other)
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("t", [1, 8, 16])
+def test_linear_i8_few_rows_of_every_length(t, gated):
+    """The serving form shares the 64-byte steps of a row among eight waves, four
+    at a time: every number of steps up to past two rounds of that, in rows that
+    are already in 8 bits and, where they are short enough, quantised on the way."""
+    import torch
+    note(f"linear_i8 lengths {t} {gated}")
+    r, n = gen(t), 20
+    for k in range(128, 84 * 64, 128):
+        x, w = r(t, k - 3), r(k - 3, 2 * n, std=k ** -0.5)
+        q, s = K.quantize_rows(x)
+        wq, ws = K.quantize_weights(w)
+        l = K.LinearI8(t, k - 3, 2 * n, "fp32", gated=gated)
+        buf = K.allocate_linear_i8(l)
+        want = product64(q[:, :k - 3], s, wq[0], ws[0])
+        for got in (K.linear_i8(l, q, wq, ws, buf, x_scale=s).clone(), K.linear_i8(l, x, wq, ws, buf)):
+            if gated:
+                each(f"{k - 3}", got, *want.chunk(2, 1), "fp32")
+            else:
+                # a sum of integers, exact, rounded by its conversion and two scalings: 3 u
+                assert bool(((got.double() - want).abs() <= 3.01 * U["fp32"] * want.abs()).all()), k - 3
