@@ -136,7 +136,9 @@ constexpr int kSkinnyLds = 16 * 65;
 template <typename T, int kW, bool kLow>
 __device__ __forceinline__ void skinny_sums(const SkinnyArgs<T, kW>& a, float (*lds)[kSkinnyLds],
                                             float (&sum)[2][kW]) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  // the wave's number as a scalar: a step past the end has to be branched over,
+  // for MFMAs run whatever lanes are on
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = blockIdx.x * kSkinnyCols + 4 * (lane & 15);
   const int steps = (a.K + kSkinnyStep - 1) / kSkinnyStep;
   const int s0 = static_cast<int>(static_cast<int64_t>(steps) * blockIdx.z / a.k_parts);
