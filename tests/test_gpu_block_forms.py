@@ -1,12 +1,27 @@
 """Forms of the operators around the layer that need a look of their own: what
-the gated block keeps of its activations, and the dense gated 8-bit product."""
+the gated block's roundings leave, that its calls repeat bit for bit whatever
+their buffers held, the dense gated 8-bit product, and every buffer of the
+layer with 8-bit experts.
+
+The gated block in bf16 rounds: the hidden values (in the serving form to a
+sum of two bf16 numbers, 2^-17, which does not count), act(a) and b act'(a)
+to 20 bits (2^-12), da and db, and every result of that type. These roundings
+are made here in 64 bits, and a kernel may be off the unrounded result by at
+most 1.08 times what they are, in the 2-norm: the 20 bits add 2^-12 / sqrt(3)
+to errors of 2^-9 and more, under 1 %, sums in fp32 less, and the rounding
+errors of thousands of elements average to a few per cent at most. Values
+kept to 16 bits instead of 20 would give 1.35 times and more, swapped low bits
+1.3, a serving form that rounds its hidden values 1.4.
+"""
 
 import pytest
 
+from dropless_grouped_gemm_router_amd import binding as B
 from dropless_grouped_gemm_router_amd import block as K
+from dropless_grouped_gemm_router_amd.inputs import Problem
 
-from gpu_util import note
-from test_gpu_block import U, act64, ffn64, ffn_case, gen, quantized
+from gpu_util import Case, note
+from test_gpu_block import U, act64, ffn64, ffn_case, gen, near, off, quantized
 
 pytestmark = pytest.mark.gpu
 
@@ -35,6 +50,28 @@ def along(got, want):
     """How much longer ``got`` is than ``want`` in its direction."""
     got, want = got.double(), want.double()
     return float((got * want).sum() / (want * want).sum()) - 1
+
+
+ROUNDINGS = [(4, 512, 1024, "silu"), (16, 500, 1001, "gelu"), (17, 512, 1024, "silu"), (130, 333, 1001, "gelu_tanh"),
+             (200, 512, 1024, "silu"), (2000, 256, 512, "silu"), (4100, 640, 1152, "gelu")]
+
+
+@pytest.mark.parametrize("t,d,h,act", ROUNDINGS)
+def test_ffn_roundings(t, d, h, act):
+    note(f"ffn roundings {t} {d} {h} {act}")
+    f, x, w, dy, buf = ffn_case(t, d, h, "bf16", act)
+    y, grads = ffn64(x, w, dy, act)
+    ry, rgrads = rounded64(x, w, dy, act, hidden=t > 16)
+    K.gated_ffn(f, x, w, buf)
+    limit = 1.08 * off(ry.bfloat16(), y)
+    assert off(buf.out, y) <= limit, "inference"
+    K.gated_ffn(f, x, w, buf, training=True)
+    assert off(buf.out, y) <= limit, "training"
+    K.gated_ffn_backward(f, x, w, dy, buf)
+    got = (buf.grad_x, buf.grads["w_gate"], buf.grads["w_up"], buf.grads["w_down"])
+    for name, g, rg, want in zip(("x", "w_gate", "w_up", "w_down"), got, rgrads, grads):
+        limit = 1.08 * off(rg.bfloat16() if name == "x" else rg, want)
+        assert off(g, want) <= limit, name
 
 
 @pytest.mark.parametrize("t,d,h,act", [(2000, 256, 512, "silu"), (3000, 200, 400, "gelu")])
@@ -104,6 +141,30 @@ def test_ffn_kept_activations_that_are_not_finite():
         for got, want in zip(kept, (act, slope)):
             assert torch.equal(got.isnan(), want.isnan())
             assert torch.equal(got.isposinf(), want.isposinf()) and torch.equal(got.isneginf(), want.isneginf())
+
+
+@pytest.mark.parametrize("t,d,h,dtype", [(1, 2048, 512, "bf16"), (300, 1024, 4096, "bf16"), (130, 333, 1001, "bf16"),
+                                         (8200, 512, 1024, "bf16"), (20, 100, 333, "fp32"), (300, 500, 1001, "fp32")])
+def test_ffn_repeats_whatever_its_buffers_held(t, d, h, dtype):
+    """The same bits from every call, over workspaces, kept activations and
+    results that hold NaN or large numbers before it."""
+    import torch
+    note(f"ffn repeats {t} {d} {h} {dtype}")
+    f, x, w, dy, buf = ffn_case(t, d, h, dtype)
+    first = None
+    for fill in (0, 255, 127, 255):
+        buf.workspace.fill_(fill), buf.saved.fill_(fill)
+        for v in (buf.out, buf.grad_x, *buf.grads.values()):
+            v.fill_(float("nan"))
+        outs = [K.gated_ffn(f, x, w, buf).clone()]
+        buf.workspace.fill_(fill)
+        outs.append(K.gated_ffn(f, x, w, buf, training=True).clone())
+        buf.workspace.fill_(fill)
+        gx, g = K.gated_ffn_backward(f, x, w, dy, buf)
+        outs += [v.clone() for v in (gx, *g.values())]
+        first = first or outs
+        assert all(torch.equal(a, b) for a, b in zip(first, outs)), fill
+    assert all(bool(torch.isfinite(v.float()).all()) for v in first)
 
 
 # ------------------------------------------- the dense gated product in 8 bits
@@ -181,3 +242,52 @@ def test_linear_i8_few_rows_of_every_length(t, gated):
             else:
                 # a sum of integers, exact, rounded by its conversion and two scalings: 3 u
                 assert bool(((got.double() - want).abs() <= 3.01 * U["fp32"] * want.abs()).all()), k - 3
+
+
+# ---------------------------------------------- the layer with 8-bit experts
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("t,e,top,d,h,cap,shared", [
+    (1, 8, 2, 128, 64, 0, False), (4, 16, 4, 256, 128, 0, True), (4, 64, 8, 512, 128, 0, False),
+    (9, 1, 1, 128, 64, 0, True), (60, 4, 2, 128, 192, 11, False), (700, 16, 4, 256, 128, 100, True),
+    (3000, 8, 2, 512, 320, 0, True), (3000, 3, 1, 384, 64, 700, False)])
+def test_layer_with_8_bit_experts(t, e, top, d, h, cap, shared, dtype):
+    """Every buffer of the path against 64 bits of what went into it: the hidden
+    values, the experts' outputs and the sum, with and without a capacity and a
+    shared expert's output. Rows past a capacity stay as they were."""
+    import torch
+    note(f"layer in 8 bits {t} {e} {top} {d} {h} {cap} {shared} {dtype}")
+    p = Problem(t, e, top, d, h, 0, dtype, 64, skew=0.5 if cap else 0.0, capacity=cap)
+    c = Case(p, seed=4)
+    x, wt = c.dev["x"], c.weights()
+    gu, dn = K.quantize_weights(wt["w_gate"], wt["w_up"]), K.quantize_weights(wt["w_down"])
+    more = gen(6)(t, d, dtype=dtype) if shared else None
+    ex = K.allocate_experts_i8(p)
+    ex.hidden.y.fill_(7.0), ex.sorted.y.fill_(7.0)
+    out = K.forward_i8(p, x, wt["w_router"], gu, dn, c.buf, ex, shared_out=more)
+    assert out is c.buf.out
+    B.moe_route(p, x, wt["w_router"], (r := B.allocate(p, "cuda")).routing)
+    for name in ("topk_idx", "topk_w"):
+        assert torch.equal(c.buf.routing[name], r.routing[name])
+    ends = c.buf.routing["expert_offsets"].tolist()
+    assert ends[-1] == t * top
+    token = c.buf.routing["perm"].long() // top
+    q, s = integers(x)
+    kept = torch.zeros(t * top, dtype=torch.bool, device="cuda")
+    for g in range(e):
+        i, j = ends[g], min(ends[g + 1], ends[g] + cap) if cap else ends[g + 1]
+        if i < j:
+            both = product64(q[token[i:j]], s[token[i:j]], gu[0][g], gu[1][g])
+            each(f"hidden {g}", ex.hidden.y[i:j], *both.chunk(2, 1), dtype)
+            want = product64(*integers(ex.hidden.y[i:j]), dn[0][g], dn[1][g])
+            near(f"sorted {g}", ex.sorted.y[i:j], want, U[dtype] + 2.0 ** -20)
+        kept[i:j] = True
+    assert bool(kept.all()) == (not cap or max(b - a for a, b in zip(ends, ends[1:])) <= cap)
+    assert bool((ex.hidden.y[~kept] == 7).all() and (ex.sorted.y[~kept] == 7).all())
+    if cap:
+        assert not bool(kept.all()), "the capacity drops nothing here"
+    at = c.buf.routing["inv_perm"].view(t, top).long()
+    assert torch.equal((at >= 0).sum(), kept.sum())
+    w = torch.where(at >= 0, c.buf.routing["topk_w"], 0.0).double()
+    want = (w[:, :, None] * ex.sorted.y.double()[at.clamp(min=0)]).sum(1) + (more.double() if shared else 0.0)
+    near("out", out, want, U[dtype] + top * 2.0 ** -24)
