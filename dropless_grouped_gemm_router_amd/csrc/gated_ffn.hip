@@ -18,9 +18,10 @@
 // in the workspace (x and dout, and the weights the backward reads), with the
 // hidden values kept at the padded width.
 //
-// 16384 tokens, 512 x 1024, bf16, forward and backward: 245 to 260 us (155
-// GFLOP; products of this depth are bound by what their epilogues write and
-// read, see mm.h). 8192 tokens, 2048 x 8192: 2.5 ms, 0.99 PFLOP/s.
+// 16384 tokens, 512 x 1024, bf16, forward and backward: 247 to 271 us (155
+// GFLOP; at this depth a tile's loop and its epilogue, which writes and reads
+// as many bytes, take turns: gate and up keep the MFMA pipes 23% busy and move
+// 3.0 TB/s). 8192 tokens, 2048 x 8192: 2.5 ms, 0.99 PFLOP/s.
 #include <algorithm>
 
 #include "gemm_wgrad.h"
@@ -37,6 +38,11 @@ namespace {
 // tiles have the weights turned first, 17 tokens, 2047 x 8191: 88 and 76, 500 x
 // 1001: 22.6 and 18.6. fp32, 64 tokens, 1024 x 4096: 39 and 52, 2048 x 2048: 55
 // and 73; 128 tokens: 66 and 58, 63 and 77; 512 x 1024: 22 and 28.
+// In bf16 the tiles round the hidden values for the second product, as the
+// layer's experts do, and the serving form does not: from 17 tokens on the
+// result is 2.35e-3 off 64 bits in the 2-norm instead of 1.66e-3, which its own
+// rounding is. Two halves in the tiles too would be a third more MFMAs and two
+// more bytes a hidden value.
 constexpr int64_t kFewRows = 16, kFewRowsF32 = 128;
 constexpr int64_t kCUs = 256;
 
@@ -798,7 +804,10 @@ int parts_of(size_t elem, int64_t M, int64_t N, int64_t stages) {
 // Turned first and in place, 300 tokens, 1024 x 4096: 35.1 and 28.4 us; 1000
 // tokens, 2048 x 8192: 154 and 145, 4000: 441 and 439, 8192: 790 and 925;
 // 8192 tokens, 1024 x 4096: 258 and 243; 16384 tokens, 512 x 1024: 93 and 91,
-// 32768: 147 and 152.
+// 32768: 147 and 152. Narrower ones at the limit, inference and training: 131072
+// tokens, 64 x 256: 70 and 49, 93 and 61; 65536, 128 x 1024: 111 and 93, 159 and
+// 162; 32768, 256 x 1024: 79 and 76, 97 and 96; the one that loses, 16384, 256 x
+// 4096: 147 and 146, 237 and 255.
 constexpr int64_t kInPlace = int64_t{1} << 23;  // elements of x
 bool in_place(const moe_ffn& f) {
   if (f.dtype != MOE_BF16 || f.d_model % 64 || f.d_hidden % 64) return false;
@@ -1103,11 +1112,12 @@ hipError_t ffn_bwd_t(const moe_ffn& f, const void* x, const void* wg, const void
       job(dn, L.splits_d, dp * hp, dp, h, d, dwd);
     }
   } else {
-    // fp32 has no transposing LDS read: the operands are turned (their bytes
-    // are little beside fp32 MFMAs) and the gradients are plain products,
-    // written in place where the tokens are not cut into slices. 777 tokens,
-    // 500 x 1001: 42 us, against 64 with row slices turned in registers and
-    // their partial sums.
+    // The tiles take rows of consecutive tokens, so fp32 operands are turned
+    // first (their bytes are little beside fp32 MFMAs; a stage loop that reads
+    // single elements of [tokens][columns] from LDS would do without) and the
+    // gradients are plain products, written in place where the tokens are not
+    // cut into slices. 777 tokens, 500 x 1001: 42 us, against 64 with row
+    // slices turned in registers and their partial sums.
     TurnJobs turns{};
     turns.add(x, W + L.xt, tok, d, d);
     turns.add(W + L.dab, W + L.dabt, tok, static_cast<int>(2 * hp), 2 * hp);

@@ -267,15 +267,15 @@ void i8_tile_kernel(const MmArgs p, const I8Out o) {
 // its eight waves share K. Rows that are not yet integers are quantised into
 // LDS by every workgroup for itself while its first weights are on their way:
 // one launch instead of two, and the rows come from L2. 4 rows of 4096 through
-// 4096 x 4096 weights (16.8 MB): 9.2 us against 20 with 32 x 64 tiles; what is
-// left above the bytes' 3.5 us is the launch, the rows' two passes and the
-// sum over the waves.
+// 4096 x 4096 weights (16.8 MB), one call after another: 9.2 us against 13.9 in
+// 64 x 64 tiles. From a graph 8.2 us, and 4.9 with rows that are in 8 bits
+// already: above the bytes' 3.5 us are the rows' two passes, which few waves
+// make, the launch and the sum over the waves.
 constexpr int kRowsWaves = 8, kRowsBatch = 4;
 
 struct I8Few {
   const void* x;
   int64_t ldx;            // elements between rows
-  const float* xs;        // int8 input: scales
   const int8_t* w;
   int64_t pitch;          // bytes between weight rows
   int width;              // elements of an input row
@@ -516,7 +516,6 @@ hipError_t launch_linear_i8(const moe_i8_linear& l, const void* x, const float* 
     I8Few p{};
     p.x = x;
     p.ldx = own ? l.inputs : pitch;
-    p.xs = xs;
     p.w = wq;
     p.pitch = pitch;
     p.width = l.inputs;

@@ -116,7 +116,7 @@ __device__ __forceinline__ void skinny_step(const SkinnyW<float>& w, const Skinn
 }
 
 // One operand: rows x [rows][K] (row stride ldx) and, where kLow, their low
-// halves (see SkinnyHidden); kW weight matrices [K][N].
+// halves (put_hidden in gated_ffn.hip); kW weight matrices [K][N].
 template <typename T, int kW>
 struct SkinnyArgs {
   const T* x;

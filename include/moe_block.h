@@ -87,7 +87,9 @@ typedef enum {
  * [tokens, d_model], all in dtype; accumulation is fp32. The hidden values
  * act(x W_gate) * (x W_up) are rounded to dtype for the second product (as
  * the routed experts' are), and in the backward pass so are the gradients of
- * the two pre-activations.
+ * the two pre-activations. In bf16 and up to 16 tokens the second product
+ * takes the hidden values as a sum of two bf16 numbers instead (2^-17); the
+ * backward's h is rounded there too.
  *
  * Supported (else MOE_ERR_UNSUPPORTED): d_model and d_hidden up to 32768
  * (any value), tokens * max(d_model, 2 * d_hidden) < 2^36.

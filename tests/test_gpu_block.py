@@ -13,8 +13,9 @@ sign, which the 2-norm over a whole matrix of random sums respects with room).
 * norm: y and dx are rounded once from fp32: u + 64 * 2^-24 (sums of up to
   16384 terms in a tree of at most 64 sequential additions a thread).
 * ffn: hidden values rounded (1 u), output rounded (1 u): 2 u forward.
-  Backward: saved pre-activations (2 u together in dh b act'(a), where act'
-  is at most doubly as sensitive), da and db (1 u), result (1 u): 5 u.
+  Backward: the 20 bits kept of act(a) and b act'(a) (2^-12 each, far under
+  1 u), da and db (1 u), result (1 u); 5 u has room over that, and
+  test_gpu_block_forms.py holds the roundings themselves.
   fp32: sums of n products by MFMA in sequence add at most n 2^-24 in the
   worst case and about sqrt(n) 2^-24 in the 2-norm; 1e-5 covers n = 2^14.
 * int8: the integers and their sums are exact; scaling rounds three times in
