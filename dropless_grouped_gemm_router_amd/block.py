@@ -1,13 +1,15 @@
 """Operators around the MoE layer (``include/moe_block.h``): layer norm, the
-dense gated feed-forward block and products with 8-bit integer weights,
-forward and, where the layer trains, backward.
+dense gated feed-forward block, products with 8-bit integer weights, products
+with bias, activation and residual, the norms, gate and residual between two
+blocks, and the router's balance loss; forward and, where they train, backward.
 
 The ``moe_*`` functions have the C entry points' names and only marshal
 arguments, as in ``binding``. The functions without that prefix take tensors:
 they check shapes, types, contiguity and device on the host, launch on the
 tensors' own device (its current stream unless one is given) and write into
 buffers that were allocated once (``allocate_norm``, ``allocate_ffn``,
-``allocate_linear_i8``). Tensors used on a stream other than their own have to
+``allocate_linear_i8``, ``allocate_linear``, ``allocate_residual_norm``,
+``allocate_balance_loss``). Tensors used on a stream other than their own have to
 be ordered by the caller, as for every call of the library.
 """
 
@@ -26,11 +28,18 @@ from .binding import (DTYPES, MOE_BF16, MOE_FP32, _check, _ptr, _stream, load as
 
 MOE_I8 = 2
 ACTS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3}
+LINEAR_ACTS = dict(ACTS, none=4)
+NORM_KINDS = {"layer": 0, "rms": 1}
+NORM_PARAMS = ("post_weight", "post_bias", "gate", "pre_weight", "pre_bias")
 
 EXPORTED = ["moe_layer_norm", "moe_layer_norm_workspace_bytes", "moe_layer_norm_bwd",
             "moe_gated_ffn_workspace_bytes", "moe_gated_ffn_saved_bytes", "moe_gated_ffn",
             "moe_gated_ffn_bwd", "moe_i8_pitch", "moe_quantize_rows", "moe_quantize_weight",
-            "moe_linear_i8_workspace_bytes", "moe_linear_i8"]
+            "moe_linear_i8_workspace_bytes", "moe_linear_i8",
+            "moe_linear_workspace_bytes", "moe_linear_saved_bytes", "moe_linear_fwd", "moe_linear_bwd",
+            "moe_residual_norm_fwd", "moe_residual_norm_workspace_bytes", "moe_residual_norm_bwd",
+            "moe_balance_workspace_bytes", "moe_balance_saved_bytes", "moe_balance_loss",
+            "moe_balance_loss_bwd"]
 
 
 class moe_norm(ctypes.Structure):
@@ -50,6 +59,33 @@ class moe_i8_linear(ctypes.Structure):
         "inputs", "outputs", "x_dtype", "dtype", "groups", "top_k", "gather", "gated", "capacity")]
 
 
+class moe_linear(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64)] + [(n, ctypes.c_int32) for n in (
+        "inputs", "outputs", "dtype", "act", "grad_dtype")]
+
+
+class moe_residual_norm(ctypes.Structure):
+    _fields_ = ([("rows", ctypes.c_int64)]
+                + [(n, ctypes.c_int32) for n in ("width", "dtype", "kind", "post", "pre")]
+                + [("eps", ctypes.c_float), ("scale", ctypes.c_float)]
+                + [("ld_" + n, ctypes.c_int64) for n in (
+                    "z", "res", "out", "y", "grad_out", "grad_y", "grad_z", "grad_res")])
+
+
+class moe_norm_params(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in NORM_PARAMS]
+
+
+class moe_norm_grads(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in NORM_PARAMS]
+
+
+class moe_balance(ctypes.Structure):
+    _fields_ = ([("tokens", ctypes.c_int64)]
+                + [(n, ctypes.c_int32) for n in ("experts", "top_k", "d_model", "dtype")]
+                + [("balance", ctypes.c_float), ("z", ctypes.c_float)])
+
+
 _lib = None
 
 
@@ -61,6 +97,8 @@ def load():
     lib = _load_library()
     P, i32, i64, size = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
     N, F, L = (ctypes.POINTER(t) for t in (moe_norm, moe_ffn, moe_i8_linear))
+    D, R, S = (ctypes.POINTER(t) for t in (moe_linear, moe_residual_norm, moe_balance))
+    W, G = ctypes.POINTER(moe_norm_params), ctypes.POINTER(moe_norm_grads)
     sig = {
         "moe_layer_norm": (ctypes.c_int, [N] + [P] * 7),
         "moe_layer_norm_workspace_bytes": (size, [N]),
@@ -74,6 +112,17 @@ def load():
         "moe_quantize_weight": (ctypes.c_int, [i32, i32, i32, i32, P, i64, P, P, P]),
         "moe_linear_i8_workspace_bytes": (size, [L]),
         "moe_linear_i8": (ctypes.c_int, [L, P, P, P, P, P, ctypes.POINTER(moe_routing), P, P, size, P]),
+        "moe_linear_workspace_bytes": (size, [D, ctypes.c_int]),
+        "moe_linear_saved_bytes": (size, [D]),
+        "moe_linear_fwd": (ctypes.c_int, [D] + [P] * 7 + [size, P]),
+        "moe_linear_bwd": (ctypes.c_int, [D] + [P] * 8 + [size, P]),
+        "moe_residual_norm_fwd": (ctypes.c_int, [R, P, P, W, P, P, P, P]),
+        "moe_residual_norm_workspace_bytes": (size, [R]),
+        "moe_residual_norm_bwd": (ctypes.c_int, [R, P, P, W] + [P] * 5 + [G, P, size, P]),
+        "moe_balance_workspace_bytes": (size, [S]),
+        "moe_balance_saved_bytes": (size, [S]),
+        "moe_balance_loss": (ctypes.c_int, [S] + [P] * 9 + [size, P]),
+        "moe_balance_loss_bwd": (ctypes.c_int, [S] + [P] * 5 + [ctypes.c_int] + [P] * 3 + [size, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -164,6 +213,85 @@ def moe_linear_i8(l: moe_i8_linear, x, x_scale, wq, w_scale, bias, routing: Opti
                                 _ptr(bias), r, _ptr(y), _ptr(workspace),
                                 _nbytes(workspace, workspace_bytes), _stream(stream)),
            "moe_linear_i8")
+
+
+def moe_linear_workspace_bytes(l: moe_linear, training: bool = False) -> int:
+    return int(load().moe_linear_workspace_bytes(ctypes.byref(l), int(training)))
+
+
+def moe_linear_saved_bytes(l: moe_linear) -> int:
+    return int(load().moe_linear_saved_bytes(ctypes.byref(l)))
+
+
+def moe_linear_fwd(l: moe_linear, x, w, bias, residual, saved, y, workspace,
+                   workspace_bytes: Optional[int] = None, stream=None):
+    _check(load().moe_linear_fwd(ctypes.byref(l), _ptr(x), _ptr(w), _ptr(bias), _ptr(residual),
+                                 _ptr(saved), _ptr(y), _ptr(workspace),
+                                 _nbytes(workspace, workspace_bytes), _stream(stream)),
+           "moe_linear_fwd")
+
+
+def moe_linear_bwd(l: moe_linear, x, w, saved, grad_out, grad_x, grad_w, grad_bias, workspace,
+                   workspace_bytes: Optional[int] = None, stream=None):
+    _check(load().moe_linear_bwd(ctypes.byref(l), _ptr(x), _ptr(w), _ptr(saved), _ptr(grad_out),
+                                 _ptr(grad_x), _ptr(grad_w), _ptr(grad_bias), _ptr(workspace),
+                                 _nbytes(workspace, workspace_bytes), _stream(stream)),
+           "moe_linear_bwd")
+
+
+def norm_params_struct(params: Dict) -> moe_norm_params:
+    return moe_norm_params(*[_ptr(params.get(n)) for n in NORM_PARAMS])
+
+
+def norm_grads_struct(grads: Dict) -> moe_norm_grads:
+    return moe_norm_grads(*[_ptr(grads.get(n)) for n in NORM_PARAMS])
+
+
+def moe_residual_norm_fwd(n: moe_residual_norm, z, res, params: Dict, out, y, stats, stream=None):
+    p = norm_params_struct(params)
+    _check(load().moe_residual_norm_fwd(ctypes.byref(n), _ptr(z), _ptr(res), ctypes.byref(p),
+                                        _ptr(out), _ptr(y), _ptr(stats), _stream(stream)),
+           "moe_residual_norm_fwd")
+
+
+def moe_residual_norm_workspace_bytes(n: moe_residual_norm) -> int:
+    return int(load().moe_residual_norm_workspace_bytes(ctypes.byref(n)))
+
+
+def moe_residual_norm_bwd(n: moe_residual_norm, z, res, params: Dict, stats, grad_out, grad_y, grad_z,
+                          grad_res, grads: Dict, workspace, workspace_bytes: Optional[int] = None,
+                          stream=None):
+    p, g = norm_params_struct(params), norm_grads_struct(grads)
+    _check(load().moe_residual_norm_bwd(ctypes.byref(n), _ptr(z), _ptr(res), ctypes.byref(p),
+                                        _ptr(stats), _ptr(grad_out), _ptr(grad_y), _ptr(grad_z),
+                                        _ptr(grad_res), ctypes.byref(g), _ptr(workspace),
+                                        _nbytes(workspace, workspace_bytes), _stream(stream)),
+           "moe_residual_norm_bwd")
+
+
+def moe_balance_workspace_bytes(b: moe_balance) -> int:
+    return int(load().moe_balance_workspace_bytes(ctypes.byref(b)))
+
+
+def moe_balance_saved_bytes(b: moe_balance) -> int:
+    return int(load().moe_balance_saved_bytes(ctypes.byref(b)))
+
+
+def moe_balance_loss(b: moe_balance, x, w_router, topk_idx, mask, counts, mean_prob, loss, saved,
+                     workspace, workspace_bytes: Optional[int] = None, stream=None):
+    _check(load().moe_balance_loss(ctypes.byref(b), _ptr(x), _ptr(w_router), _ptr(topk_idx),
+                                   _ptr(mask), _ptr(counts), _ptr(mean_prob), _ptr(loss), _ptr(saved),
+                                   _ptr(workspace), _nbytes(workspace, workspace_bytes),
+                                   _stream(stream)), "moe_balance_loss")
+
+
+def moe_balance_loss_bwd(b: moe_balance, x, w_router, mask, saved, grad_loss, add: bool, grad_x,
+                         grad_router, workspace, workspace_bytes: Optional[int] = None, stream=None):
+    _check(load().moe_balance_loss_bwd(ctypes.byref(b), _ptr(x), _ptr(w_router), _ptr(mask),
+                                       _ptr(saved), _ptr(grad_loss), int(add), _ptr(grad_x),
+                                       _ptr(grad_router), _ptr(workspace),
+                                       _nbytes(workspace, workspace_bytes), _stream(stream)),
+           "moe_balance_loss_bwd")
 
 
 # ------------------------------------------------------------ tensor checks
@@ -573,6 +701,345 @@ def linear_i8(l: LinearI8, x, wq, w_scale, buf: I8Buffers, bias=None, routing: O
     return y
 
 
+# ----------------------------------- products with bias, activation and residual
+
+@dataclass(frozen=True)
+class Linear:
+    """A dense product with its epilogue: y = act(x W + bias) + residual."""
+
+    tokens: int
+    inputs: int
+    outputs: int
+    dtype: str = "bf16"
+    act: str = "none"
+    grad_dtype: str = "fp32"  # of the weights' gradient: fp32, or dtype
+
+    @property
+    def _fields(self):
+        return (self.tokens, self.inputs, self.outputs, DTYPES[self.dtype], LINEAR_ACTS[self.act],
+                DTYPES[self.grad_dtype])
+
+    def struct(self) -> moe_linear:
+        """The C problem, the caller's own to change."""
+        return moe_linear(*self._fields)
+
+
+@lru_cache(maxsize=256)
+def _linear(l):
+    c = l.struct()
+    return (ctypes.byref(c), moe_linear_saved_bytes(c), torch.Size((l.tokens, l.inputs)),
+            torch.Size((l.inputs, l.outputs)), torch.Size((l.tokens, l.outputs)), _TORCH[l.dtype])
+
+
+@dataclass
+class LinearBuffers:
+    """Device buffers of one product, allocated once."""
+
+    y: object
+    workspace: object
+    saved: Optional[object] = None  # training, with an activation
+    grad_x: Optional[object] = None
+    grad_w: Optional[object] = None
+    grad_bias: Optional[object] = None
+
+
+def allocate_linear(l: Linear, device="cuda", training: bool = False) -> LinearBuffers:
+    dt, device, c = _TORCH[l.dtype], _device(device), l.struct()
+    nws = moe_linear_workspace_bytes(c, training)
+    if nws == 0:
+        raise ValueError(f"unsupported problem {l}")
+    b = LinearBuffers(y=torch.empty((l.tokens, l.outputs), dtype=dt, device=device),
+                      workspace=torch.empty(nws, dtype=torch.uint8, device=device))
+    if training:
+        b.saved = torch.empty(moe_linear_saved_bytes(c), dtype=torch.uint8, device=device)
+        b.grad_x = torch.empty((l.tokens, l.inputs), dtype=dt, device=device)
+        b.grad_w = torch.empty((l.inputs, l.outputs), dtype=_TORCH[l.grad_dtype], device=device)
+        b.grad_bias = torch.empty(l.outputs, dtype=torch.float32, device=device)
+    return b
+
+
+def linear(l: Linear, x, w, buf: LinearBuffers, bias=None, residual=None, training: bool = False,
+           stream=None):
+    """The product of x [tokens, inputs] and w [inputs, outputs] with its
+    epilogue; bias is fp32. Returns buf.y."""
+    c, nsv, xs, ws, ys, dt = _linear(l)
+    dev, y = x.device, buf.y
+    _want("x", x, xs, dt, dev)
+    _want("w", w, ws, dt, dev)
+    if bias is not None:
+        _want("bias", bias, (l.outputs,), torch.float32, dev)
+    if residual is not None:
+        _want("residual", residual, ys, dt, dev)
+    _want("y", y, ys, dt, dev)
+    _want_bytes("workspace", buf.workspace, 0, dev)
+    if training:
+        _want_saved(buf, nsv, dev)
+    _run("moe_linear_fwd", dev, stream, load().moe_linear_fwd, c, x.data_ptr(), w.data_ptr(),
+         None if bias is None else bias.data_ptr(), None if residual is None else residual.data_ptr(),
+         buf.saved.data_ptr() if training else None, y.data_ptr(), buf.workspace.data_ptr(),
+         buf.workspace.numel())
+    return y
+
+
+def linear_backward(l: Linear, x, w, grad_out, buf: LinearBuffers, bias: bool = True, stream=None):
+    """Gradients of sum(y * grad_out) after ``linear(..., training=True)`` with
+    the same buffers: (grad_x, grad_w, grad_bias), the last None where bias is
+    False; the residual's gradient is grad_out."""
+    c, nsv, xs, ws, ys, dt = _linear(l)
+    dev = x.device
+    _want("x", x, xs, dt, dev)
+    _want("w", w, ws, dt, dev)
+    _want_saved(buf, nsv, dev)
+    _want("grad_out", grad_out, ys, dt, dev)
+    _want("grad_x", buf.grad_x, xs, dt, dev)
+    _want("gradient of w", buf.grad_w, ws, _TORCH[l.grad_dtype], dev)
+    if bias:
+        _want("gradient of bias", buf.grad_bias, (l.outputs,), torch.float32, dev)
+    _want_bytes("workspace", buf.workspace, 0, dev)
+    _run("moe_linear_bwd", dev, stream, load().moe_linear_bwd, c, x.data_ptr(), w.data_ptr(),
+         buf.saved.data_ptr(), grad_out.data_ptr(), buf.grad_x.data_ptr(), buf.grad_w.data_ptr(),
+         buf.grad_bias.data_ptr() if bias else None, buf.workspace.data_ptr(), buf.workspace.numel())
+    return buf.grad_x, buf.grad_w, buf.grad_bias if bias else None
+
+
+# ---------------------------------------------------------- between two blocks
+
+@dataclass(frozen=True)
+class ResidualNorm:
+    """What lies between two blocks: out = scale res + gate (norm(z) post_weight
+    + post_bias), y = norm(out) pre_weight + pre_bias; without post the block's
+    output z is added as it is, without pre there is no y."""
+
+    rows: int
+    width: int
+    dtype: str = "bf16"
+    kind: str = "layer"  # of both norms: layer or rms
+    eps: float = 1e-5
+    scale: float = 1.0
+    post: bool = True
+    pre: bool = True
+
+    def struct(self, *lds) -> moe_residual_norm:
+        """The C problem, the caller's own to change."""
+        return moe_residual_norm(self.rows, self.width, DTYPES[self.dtype], NORM_KINDS[self.kind],
+                                 int(self.post), int(self.pre), self.eps, self.scale, *lds)
+
+
+@lru_cache(maxsize=256)
+def _step(n, *lds):
+    return ctypes.byref(n.struct(*lds))
+
+
+@lru_cache(maxsize=256)
+def _step_shapes(n):
+    return torch.Size((n.rows, n.width)), torch.Size((4, n.rows)), _TORCH[n.dtype]
+
+
+@dataclass
+class ResidualNormBuffers:
+    """Device buffers of one step, allocated once."""
+
+    out: object
+    y: Optional[object]
+    stats: object
+    grad_z: Optional[object] = None
+    grad_res: Optional[object] = None
+    grads: Optional[Dict] = None
+    workspace: Optional[object] = None
+
+
+def allocate_residual_norm(n: ResidualNorm, device="cuda", training: bool = False) -> ResidualNormBuffers:
+    dt, device = _TORCH[n.dtype], _device(device)
+    nws = moe_residual_norm_workspace_bytes(n.struct())
+    if nws == 0:
+        raise ValueError(f"unsupported problem {n}")
+    f32 = dict(dtype=torch.float32, device=device)
+
+    def matrix():
+        return torch.empty((n.rows, n.width), dtype=dt, device=device)
+
+    b = ResidualNormBuffers(out=matrix(), y=matrix() if n.pre else None, stats=torch.empty((4, n.rows), **f32))
+    if training:
+        b.grad_z, b.grad_res = matrix(), matrix()
+        b.grads = {name: torch.empty(n.width, **f32) for name in NORM_PARAMS}
+        b.workspace = torch.empty(nws, dtype=torch.uint8, device=device)
+    return b
+
+
+def _want_step(n, z, res, params):
+    shape, stats, dt = _step_shapes(n)
+    dev = z.device
+    ld_z, ld_res = _want_rows("z", z, shape, dt, dev), _want_rows("res", res, shape, dt, dev)
+    ptrs = []
+    for name in NORM_PARAMS:
+        t = params.get(name)
+        if t is not None:
+            _want(name, t, (n.width,), torch.float32, dev)
+            t = t.data_ptr()
+        ptrs.append(t)
+    return shape, stats, dt, dev, ld_z, ld_res, moe_norm_params(*ptrs)
+
+
+def residual_norm(n: ResidualNorm, z, res, params: Dict, buf: ResidualNormBuffers, stream=None):
+    """The step from a block's output z and the residual res [rows, width]
+    (rows may be strided); params may hold post_weight, post_bias, gate,
+    pre_weight and pre_bias (fp32). Returns (buf.out, buf.y), with buf.stats
+    kept for the backward pass."""
+    shape, stats, dt, dev, ld_z, ld_res, p = _want_step(n, z, res, params)
+    ld_out, ld_y, y = _want_rows("out", buf.out, shape, dt, dev), 0, None
+    if n.pre:
+        y = buf.y
+        if y is None:
+            raise ValueError("y: the buffers were allocated for a step without the norm before the next block")
+        ld_y, y = _want_rows("y", y, shape, dt, dev), y.data_ptr()
+    _want("stats", buf.stats, stats, torch.float32, dev)
+    _run("moe_residual_norm_fwd", dev, stream, load().moe_residual_norm_fwd,
+         _step(n, ld_z, ld_res, ld_out, ld_y, 0, 0, 0, 0), z.data_ptr(), res.data_ptr(), ctypes.byref(p),
+         buf.out.data_ptr(), y, buf.stats.data_ptr())
+    return buf.out, buf.y if n.pre else None
+
+
+def residual_norm_backward(n: ResidualNorm, z, res, params: Dict, grad_out, grad_y,
+                           buf: ResidualNormBuffers, stream=None):
+    """Gradients of sum(out * grad_out) + sum(y * grad_y) after
+    ``residual_norm`` with the same buffers: (grad_z, grad_res, {the
+    parameters' gradients, fp32}). grad_out may be None; grad_y is None without
+    the norm before the next block."""
+    shape, stats, dt, dev, ld_z, ld_res, p = _want_step(n, z, res, params)
+    gz, gr, g = buf.grad_z, buf.grad_res, buf.grads
+    if gz is None:
+        raise ValueError("the buffers were allocated without training=True")
+    if (grad_y is not None) != n.pre:
+        raise ValueError("grad_y: expected exactly where there is a norm before the next block")
+    ld_go = 0 if grad_out is None else _want_rows("grad_out", grad_out, shape, dt, dev)
+    ld_gy = 0 if grad_y is None else _want_rows("grad_y", grad_y, shape, dt, dev)
+    ld_gz, ld_gr = _want_rows("grad_z", gz, shape, dt, dev), _want_rows("grad_res", gr, shape, dt, dev)
+    _want("stats", buf.stats, stats, torch.float32, dev)
+    for name in NORM_PARAMS:
+        _want("gradient of " + name, g[name], (n.width,), torch.float32, dev)
+    _want_bytes("workspace", buf.workspace, 0, dev)
+    grads = norm_grads_struct(g)
+    _run("moe_residual_norm_bwd", dev, stream, load().moe_residual_norm_bwd,
+         _step(n, ld_z, ld_res, 0, 0, ld_go, ld_gy, ld_gz, ld_gr), z.data_ptr(), res.data_ptr(),
+         ctypes.byref(p), buf.stats.data_ptr(), _ptr(grad_out), _ptr(grad_y), gz.data_ptr(), gr.data_ptr(),
+         ctypes.byref(grads), buf.workspace.data_ptr(), buf.workspace.numel())
+    return gz, gr, g
+
+
+# ------------------------------------------------------ balance of the router
+
+@dataclass(frozen=True)
+class BalanceLoss:
+    """The router's balance loss and z loss over a batch; see moe_balance_loss."""
+
+    tokens: int
+    experts: int
+    top_k: int
+    d_model: int
+    dtype: str = "bf16"
+    balance: float = 0.01
+    z: float = 0.001
+
+    def struct(self) -> moe_balance:
+        """The C problem, the caller's own to change."""
+        return moe_balance(self.tokens, self.experts, self.top_k, self.d_model, DTYPES[self.dtype],
+                           self.balance, self.z)
+
+
+@lru_cache(maxsize=256)
+def _balance(b):
+    c = b.struct()
+    return (ctypes.byref(c), moe_balance_saved_bytes(c), torch.Size((b.tokens, b.d_model)),
+            torch.Size((b.d_model, b.experts)), _TORCH[b.dtype])
+
+
+@dataclass
+class BalanceBuffers:
+    """Device buffers of one balance loss, allocated once."""
+
+    loss: object       # [3] fp32: the weighted sum, the balance loss, the z loss
+    mean_prob: object  # [experts] fp32
+    counts: object     # [experts] int32
+    workspace: object
+    saved: Optional[object] = None
+    grad_x: Optional[object] = None
+    grad_router: Optional[object] = None
+
+
+def allocate_balance_loss(b: BalanceLoss, device="cuda", training: bool = False) -> BalanceBuffers:
+    device, c = _device(device), b.struct()
+    nws = moe_balance_workspace_bytes(c)
+    if nws == 0:
+        raise ValueError(f"unsupported problem {b}")
+    f32 = dict(dtype=torch.float32, device=device)
+    buf = BalanceBuffers(loss=torch.empty(3, **f32), mean_prob=torch.empty(b.experts, **f32),
+                         counts=torch.empty(b.experts, dtype=torch.int32, device=device),
+                         workspace=torch.empty(nws, dtype=torch.uint8, device=device))
+    if training:
+        buf.saved = torch.empty(moe_balance_saved_bytes(c), dtype=torch.uint8, device=device)
+        buf.grad_x = torch.empty((b.tokens, b.d_model), dtype=_TORCH[b.dtype], device=device)
+        buf.grad_router = torch.empty((b.d_model, b.experts), **f32)
+    return buf
+
+
+def _want_mask(mask, b, device):
+    if mask is None:
+        return None
+    if mask.dtype is not torch.uint8:
+        _want("mask", mask, (b.tokens,), torch.bool, device)
+    else:
+        _want("mask", mask, (b.tokens,), torch.uint8, device)
+    return mask.data_ptr()
+
+
+def balance_loss(b: BalanceLoss, x, w_router, topk_idx, buf: BalanceBuffers, mask=None,
+                 training: bool = False, stream=None):
+    """The loss over the tokens x [tokens, d_model] that the routing topk_idx
+    [tokens, top_k] was made of (the routing's dictionary holds it); mask [tokens]
+    (bool or uint8) leaves out tokens where it is false. Returns buf.loss, with
+    buf.mean_prob and buf.counts beside it."""
+    c, nsv, xs, ws, dt = _balance(b)
+    dev = x.device
+    _want("x", x, xs, dt, dev)
+    _want("w_router", w_router, ws, torch.float32, dev)
+    _want("topk_idx", topk_idx, (b.tokens, b.top_k), torch.int32, dev)
+    m = _want_mask(mask, b, dev)
+    _want("counts", buf.counts, (b.experts,), torch.int32, dev)
+    _want("mean_prob", buf.mean_prob, (b.experts,), torch.float32, dev)
+    _want("loss", buf.loss, (3,), torch.float32, dev)
+    _want_bytes("workspace", buf.workspace, 0, dev)
+    if training:
+        _want_saved(buf, nsv, dev)
+    _run("moe_balance_loss", dev, stream, load().moe_balance_loss, c, x.data_ptr(), w_router.data_ptr(),
+         topk_idx.data_ptr(), m, buf.counts.data_ptr(), buf.mean_prob.data_ptr(), buf.loss.data_ptr(),
+         buf.saved.data_ptr() if training else None, buf.workspace.data_ptr(), buf.workspace.numel())
+    return buf.loss
+
+
+def balance_loss_backward(b: BalanceLoss, x, w_router, buf: BalanceBuffers, grad_loss=None, mask=None,
+                          add_to=None, stream=None):
+    """Gradients of grad_loss * loss[0] (grad_loss: an fp32 tensor of one
+    number, or None: 1) after ``balance_loss(..., training=True)`` with the same
+    buffers and mask: (grad_x, grad_router). add_to: a pair of gradients, the
+    layer's own for instance, that they are added to in place of the buffers'."""
+    c, nsv, xs, ws, dt = _balance(b)
+    dev = x.device
+    gx, gw = (buf.grad_x, buf.grad_router) if add_to is None else add_to
+    _want("x", x, xs, dt, dev)
+    _want("w_router", w_router, ws, torch.float32, dev)
+    m = _want_mask(mask, b, dev)
+    _want_saved(buf, nsv, dev)
+    if grad_loss is not None:
+        _want("grad_loss", grad_loss.reshape(-1), (1,), torch.float32, dev)
+    _want("grad_x", gx, xs, dt, dev)
+    _want("gradient of w_router", gw, ws, torch.float32, dev)
+    _want_bytes("workspace", buf.workspace, 0, dev)
+    _run("moe_balance_loss_bwd", dev, stream, load().moe_balance_loss_bwd, c, x.data_ptr(),
+         w_router.data_ptr(), m, buf.saved.data_ptr(), _ptr(grad_loss), int(add_to is not None),
+         gx.data_ptr(), gw.data_ptr(), buf.workspace.data_ptr(), buf.workspace.numel())
+    return gx, gw
+
+
 # ------------------------------------------------------- with the layer itself
 
 @dataclass(frozen=True)
@@ -661,6 +1128,50 @@ def prenorm_backward(p, x, weights: Dict, grad_out, buf, norm: NormBuffers, stre
                                      side_stream=side_stream)
     gx, gw, gb = layer_norm_backward(x, weights.get("norm_weight"), gh, norm, stream)
     return gx, dict(grads, norm_weight=gw, norm_bias=gb)
+
+
+def _want_loss(p, loss):
+    b = loss[0]
+    if (b.tokens, b.experts, b.top_k, b.d_model, b.dtype) != (p.tokens, p.experts, p.top_k, p.d_model, p.dtype):
+        raise ValueError(f"loss: of {b}, not of {p}")
+
+
+def residual_layer_forward(p, h, res, weights: Dict, buf, n: ResidualNorm, step: ResidualNormBuffers,
+                           loss=None, mask=None, training: bool = False, stream=None):
+    """The MoE layer as a block of a residual stream: ``binding.forward`` on h
+    (the last step's y), then the step from its output and res; weights holds the
+    step's parameters (``NORM_PARAMS``, each may be missing) beside the layer's.
+    loss: a pair (BalanceLoss, BalanceBuffers) to have the router's balance loss
+    of the tokens that mask keeps in its buffers. Returns (step.out, step.y)."""
+    _want_layer(p, "h", h, buf, weights, training)
+    if loss is not None:
+        _want_loss(p, loss)
+    with torch.cuda.device(h.device):
+        out = binding.forward(p, h, weights, buf, training=training, stream=stream)
+    if loss is not None:
+        balance_loss(loss[0], h, weights["w_router"], buf.routing["topk_idx"], loss[1], mask, training, stream)
+    return residual_norm(n, out, res, weights, step, stream)
+
+
+def residual_layer_backward(p, h, res, weights: Dict, grad_out, grad_y, buf, n: ResidualNorm,
+                            step: ResidualNormBuffers, loss=None, grad_loss=None, mask=None, stream=None,
+                            side_stream=None):
+    """Gradients of sum(out * grad_out) + sum(y * grad_y) + grad_loss * the
+    balance loss after residual_layer_forward(..., training=True) with the same
+    buffers: (grad_h, grad_res, the layer's weight gradients with the step's
+    parameters' beside them), the loss's part added to the layer's."""
+    if buf.grads is None:
+        raise ValueError("the buffers were allocated without training=True")
+    if loss is not None:
+        _want_loss(p, loss)
+    gz, gres, steps = residual_norm_backward(n, buf.out, res, weights, grad_out, grad_y, step, stream)
+    _want_layer(p, "h", h, buf, weights, True, gz)
+    with torch.cuda.device(h.device):
+        gh, grads = binding.backward(p, h, weights, gz, buf, stream=stream, side_stream=side_stream)
+    if loss is not None:
+        balance_loss_backward(loss[0], h, weights["w_router"], loss[1], grad_loss, mask,
+                              add_to=(gh, grads["w_router"]), stream=stream)
+    return gh, gres, dict(grads, **steps)
 
 
 @dataclass

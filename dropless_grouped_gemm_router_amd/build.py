@@ -32,6 +32,9 @@ FLAGS = [
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     "-Wall", "-Wno-unused-function",
 ]
+# 256 x 256 tiles hand out 32 row pieces a lane from registers, so their loop has
+# to be unrolled whole; with an activation and its slope it is past the default.
+FILE_FLAGS = {"linear.hip": ["-mllvm", "-pragma-unroll-threshold=40000"]}
 
 
 def sources():
@@ -43,7 +46,7 @@ def _compile(src: str) -> str:
     if src == PROBE_SRC:
         obj = os.path.join(BUILD, "probe_" + os.path.basename(src) + ".o")
     lang = ["-x", "hip"] if src.endswith(".hip") else []
-    cmd = [HIPCC] + FLAGS + lang + ["-c", src, "-o", obj]
+    cmd = [HIPCC] + FLAGS + FILE_FLAGS.get(os.path.basename(src), []) + lang + ["-c", src, "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"hipcc failed on {src}:\n{r.stdout}\n{r.stderr}")

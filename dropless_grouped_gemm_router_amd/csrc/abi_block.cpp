@@ -59,6 +59,45 @@ int check_i8(const moe_i8_linear* l) {
   return MOE_OK;
 }
 
+int check_linear(const moe_linear* l) {
+  if (!l || l->tokens < 0 || l->inputs < 1 || l->outputs < 1 || !is_float(l->dtype)) return MOE_ERR_INVALID;
+  if (l->act < MOE_ACT_SILU || l->act > MOE_ACT_NONE) return MOE_ERR_INVALID;
+  if (l->grad_dtype != MOE_FP32 && l->grad_dtype != l->dtype) return MOE_ERR_INVALID;
+  if (l->inputs > 65536 || l->outputs > 65536 || l->tokens >= kRowLimit) return MOE_ERR_UNSUPPORTED;
+  const int64_t wide = l->inputs > l->outputs ? l->inputs : l->outputs;
+  // a launch stays under 2^32 threads: 256 for 64 x 64 outputs
+  if (l->tokens >= (int64_t{1} << 36) / wide) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+int check_residual_norm(const moe_residual_norm* n) {
+  if (!n || n->rows < 0 || n->width < 1 || !is_float(n->dtype)) return MOE_ERR_INVALID;
+  if (n->kind != MOE_NORM_LAYER && n->kind != MOE_NORM_RMS) return MOE_ERR_INVALID;
+  if ((n->post != 0 && n->post != 1) || (n->pre != 0 && n->pre != 1)) return MOE_ERR_INVALID;
+  if (!std::isfinite(n->eps) || n->eps < 0.0f || !std::isfinite(n->scale)) return MOE_ERR_INVALID;
+  if (n->width > 16384 || n->rows >= kRowLimit) return MOE_ERR_UNSUPPORTED;
+  for (int64_t ld : {n->ld_z, n->ld_res, n->ld_out, n->ld_y, n->ld_grad_out, n->ld_grad_y, n->ld_grad_z,
+                     n->ld_grad_res}) {
+    if (ld != 0 && ld < n->width) return MOE_ERR_INVALID;
+    if (ld >= kRowLimit) return MOE_ERR_UNSUPPORTED;
+  }
+  return MOE_OK;
+}
+
+bool ok_params(const moe_norm_params* p) {
+  return p && aligned(p->post_weight, 4) && aligned(p->post_bias, 4) && aligned(p->gate, 4) &&
+         aligned(p->pre_weight, 4) && aligned(p->pre_bias, 4);
+}
+
+int check_balance(const moe_balance* b) {
+  if (!b || b->tokens < 0 || b->experts < 1 || b->top_k < 1 || b->top_k > b->experts || b->d_model < 1 ||
+      !is_float(b->dtype) || !std::isfinite(b->balance) || !std::isfinite(b->z))
+    return MOE_ERR_INVALID;
+  if (b->experts > 64 || b->d_model % 128 || b->d_model > 8192) return MOE_ERR_UNSUPPORTED;
+  if (b->tokens > (kRowLimit - 1) / b->top_k) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
 }  // namespace
 
 MOE_EXPORT int moe_layer_norm(const moe_norm* n, const void* x, const float* weight,
@@ -185,4 +224,127 @@ MOE_EXPORT int moe_linear_i8(const moe_i8_linear* l, const void* x, const float*
   }
   return hip_status(moe::launch_linear_i8(*l, x, x_scale, wq, w_scale, bias, r, y, workspace,
                                           as_stream(stream)));
+}
+
+MOE_EXPORT size_t moe_linear_workspace_bytes(const moe_linear* l, int training) {
+  return check_linear(l) == MOE_OK ? moe::linear_ws_bytes(*l, training != 0) : 0;
+}
+
+MOE_EXPORT size_t moe_linear_saved_bytes(const moe_linear* l) {
+  return check_linear(l) == MOE_OK ? moe::linear_saved_bytes(*l) : 0;
+}
+
+MOE_EXPORT int moe_linear_fwd(const moe_linear* l, const void* x, const void* w, const float* bias,
+                              const void* residual, void* saved, void* y, void* workspace,
+                              size_t workspace_bytes, void* stream) {
+  const int st = check_linear(l);
+  if (st != MOE_OK) return st;
+  if (l->tokens == 0) return MOE_OK;
+  if (!ok_ptr(x) || !ok_ptr(w) || !aligned(bias, 16) || !aligned(residual, 16) || !aligned(saved, 256) ||
+      !ok_ptr(y) || !ok_ptr(workspace, 256))
+    return MOE_ERR_INVALID;
+  if (workspace_bytes < moe::linear_ws_bytes(*l, false)) return MOE_ERR_WORKSPACE;
+  return hip_status(moe::launch_linear(*l, x, w, bias, residual, saved, y, workspace, as_stream(stream)));
+}
+
+MOE_EXPORT int moe_linear_bwd(const moe_linear* l, const void* x, const void* w, const void* saved,
+                              const void* grad_out, void* grad_x, void* grad_w, float* grad_bias,
+                              void* workspace, size_t workspace_bytes, void* stream) {
+  const int st = check_linear(l);
+  if (st != MOE_OK) return st;
+  if (!ok_ptr(grad_w) || !aligned(grad_bias, 16)) return MOE_ERR_INVALID;
+  if (l->tokens > 0) {
+    if (!ok_ptr(x) || !ok_ptr(w) || !ok_ptr(grad_out) || !ok_ptr(grad_x) || !ok_ptr(workspace, 256))
+      return MOE_ERR_INVALID;
+    if (l->act != MOE_ACT_NONE && !ok_ptr(saved, 256)) return MOE_ERR_INVALID;
+    if (workspace_bytes < moe::linear_ws_bytes(*l, true)) return MOE_ERR_WORKSPACE;
+  }
+  return hip_status(moe::launch_linear_bwd(*l, x, w, saved, grad_out, grad_x, grad_w, grad_bias, workspace,
+                                           as_stream(stream)));
+}
+
+MOE_EXPORT int moe_residual_norm_fwd(const moe_residual_norm* n, const void* z, const void* res,
+                                     const moe_norm_params* params, void* out, void* y, float* stats,
+                                     void* stream) {
+  const int st = check_residual_norm(n);
+  if (st != MOE_OK) return st;
+  if (!ok_params(params)) return MOE_ERR_INVALID;
+  if (n->rows == 0) return MOE_OK;
+  const size_t e = bytes_of(n->dtype);
+  if (!ok_ptr(z, e) || !ok_ptr(res, e) || !ok_ptr(out, e) || !aligned(y, e) || !aligned(stats, 4) ||
+      (y != nullptr) != (n->pre == 1) || out == y)
+    return MOE_ERR_INVALID;
+  return hip_status(moe::launch_residual_norm(*n, z, res, *params, out, y, stats, as_stream(stream)));
+}
+
+MOE_EXPORT size_t moe_residual_norm_workspace_bytes(const moe_residual_norm* n) {
+  return check_residual_norm(n) == MOE_OK ? moe::residual_norm_ws_bytes(*n) : 0;
+}
+
+MOE_EXPORT int moe_residual_norm_bwd(const moe_residual_norm* n, const void* z, const void* res,
+                                     const moe_norm_params* params, const float* stats, const void* grad_out,
+                                     const void* grad_y, void* grad_z, void* grad_res,
+                                     const moe_norm_grads* grads, void* workspace, size_t workspace_bytes,
+                                     void* stream) {
+  const int st = check_residual_norm(n);
+  if (st != MOE_OK) return st;
+  if (!ok_params(params) || !grads) return MOE_ERR_INVALID;
+  bool any = false;
+  for (const float* g : {grads->post_weight, grads->post_bias, grads->gate, grads->pre_weight, grads->pre_bias}) {
+    if (!aligned(g, 4)) return MOE_ERR_INVALID;
+    any = any || g;
+  }
+  if (n->rows > 0) {
+    const size_t e = bytes_of(n->dtype);
+    if (!ok_ptr(z, e) || !ok_ptr(res, e) || !ok_ptr(stats, 4) || !aligned(grad_out, e) || !aligned(grad_y, e) ||
+        !ok_ptr(grad_z, e) || !ok_ptr(grad_res, e) || grad_z == grad_res)
+      return MOE_ERR_INVALID;
+    if ((grad_y != nullptr) != (n->pre == 1)) return MOE_ERR_INVALID;
+    if (any) {
+      if (!ok_ptr(workspace, 256)) return MOE_ERR_INVALID;
+      if (workspace_bytes < moe::residual_norm_ws_bytes(*n)) return MOE_ERR_WORKSPACE;
+    }
+  }
+  return hip_status(moe::launch_residual_norm_bwd(*n, z, res, *params, stats, grad_out, grad_y, grad_z, grad_res,
+                                                  *grads, workspace, as_stream(stream)));
+}
+
+MOE_EXPORT size_t moe_balance_workspace_bytes(const moe_balance* b) {
+  return check_balance(b) == MOE_OK ? moe::balance_ws_bytes(*b) : 0;
+}
+
+MOE_EXPORT size_t moe_balance_saved_bytes(const moe_balance* b) {
+  return check_balance(b) == MOE_OK ? moe::balance_saved_bytes(*b) : 0;
+}
+
+MOE_EXPORT int moe_balance_loss(const moe_balance* b, const void* x, const float* w_router,
+                                const int32_t* topk_idx, const uint8_t* mask, int32_t* counts,
+                                float* mean_prob, float* loss, void* saved, void* workspace,
+                                size_t workspace_bytes, void* stream) {
+  const int st = check_balance(b);
+  if (st != MOE_OK) return st;
+  if (!ok_ptr(counts, 4) || !ok_ptr(mean_prob, 4) || !ok_ptr(loss, 4) || !aligned(saved, 256) || !ok_ptr(workspace, 256) ||
+      !ok_ptr(w_router, 4))
+    return MOE_ERR_INVALID;
+  if (b->tokens > 0 && (!ok_ptr(x) || !ok_ptr(topk_idx, 4))) return MOE_ERR_INVALID;
+  if (workspace_bytes < moe::balance_ws_bytes(*b)) return MOE_ERR_WORKSPACE;
+  return hip_status(moe::launch_balance(*b, x, w_router, topk_idx, mask, counts, mean_prob, loss, saved, workspace,
+                                        as_stream(stream)));
+}
+
+MOE_EXPORT int moe_balance_loss_bwd(const moe_balance* b, const void* x, const float* w_router,
+                                    const uint8_t* mask, const void* saved, const float* grad_loss, int add,
+                                    void* grad_x, float* grad_router, void* workspace, size_t workspace_bytes,
+                                    void* stream) {
+  const int st = check_balance(b);
+  if (st != MOE_OK) return st;
+  if (add != 0 && add != 1) return MOE_ERR_INVALID;
+  if (!ok_ptr(grad_router, 4) || !aligned(grad_loss, 4)) return MOE_ERR_INVALID;
+  if (b->tokens > 0) {
+    if (!ok_ptr(x) || !ok_ptr(w_router, 4) || !ok_ptr(saved, 256) || !ok_ptr(grad_x) || !ok_ptr(workspace, 256))
+      return MOE_ERR_INVALID;
+    if (workspace_bytes < moe::balance_ws_bytes(*b)) return MOE_ERR_WORKSPACE;
+  }
+  return hip_status(moe::launch_balance_bwd(*b, x, w_router, mask, saved, grad_loss, add != 0, grad_x, grad_router,
+                                            workspace, as_stream(stream)));
 }

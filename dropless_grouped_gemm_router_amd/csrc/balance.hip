@@ -1,0 +1,893 @@
+// Balance loss and z loss of the router, with the experts' loads, forward and
+// backward.
+//
+//   l = x W, p = softmax(l), lse = log sum exp(l); over the n kept tokens
+//   loss = c1 sum_e f_e mean(p_e) + c2 mean(lse^2),  f = counts / (n k), c1 = balance E
+//   dl = p (c1 (f - sum_j f_j p_j) + 2 c2 lse) / n,  dx = dl W^T, dW = x^T dl
+//
+// Bound by reading x once in the forward, and in the backward by reading x and
+// writing dx. The gradient by the logits needs the counts, which the routing
+// already fixes, and nothing else of the batch: a first launch counts, the pass
+// over x then makes p and dl while the logits are in registers, and the backward
+// starts from dl (a seventh of x's bytes at 64 experts of 512 columns in bf16: two
+// halves of 2 bytes) instead of multiplying by W again.
+//
+// Precision. bf16: x is exact in bf16 and W is the sum of three bf16 numbers, all
+// of fp32's 24 bits, so three bf16 MFMAs make the logits as fp32 products would,
+// at a fifth of fp32 MFMAs' time. dl is the sum of two bf16 numbers (2^-17) and W
+// of two in the backward: dx is off by 2^-16 before it is rounded to bf16, dW is
+// x (exact) times dl. fp32: fp32 MFMAs throughout.
+#include "block.h"
+#include "skinny.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int kCountBlocks = 32, kCountThreads = 1024;
+
+// Experts are padded to 32 or 64: EB blocks of 32.
+inline int expert_blocks(int E) { return E <= 32 ? 1 : 2; }
+
+struct BalArgs {
+  int64_t T;
+  int E, k, d;
+  float c1, c2;           // balance * E, 2 * z
+  const uint8_t* mask;    // or null
+  const int32_t* parts;   // [count_blocks][65]: counts by expert, kept tokens
+  int count_blocks;
+  float* stats;           // [workgroups][65]: sums of p by expert, of lse^2
+};
+
+// ---------------------------------------------------- counts, and W in operands
+
+// W as the logits' first MFMA operand: 16 bytes a lane, lane l holding expert
+// 32 eb + l % 32 for k 8 (l / 32) .. + 7 of a step of 16 (fp32: 4 (l / 32) .. + 3
+// of 8); bf16: three numbers that add up to W, in three such pieces.
+template <typename T>
+__device__ void split_router(const float* __restrict__ w, int d, int E, int EB, u32x4* __restrict__ out, int i) {
+  constexpr int V = Piece<T>::V, S = sizeof(T) == 2 ? 3 : 1;
+  const int lane = i % 64, eb = i / 64 % EB, step = i / 64 / EB;
+  const int e = 32 * eb + lane % 32, k0 = step * 2 * V + V * (lane / 32);
+  if (k0 >= d) return;
+  float v[V];
+#pragma unroll
+  for (int q = 0; q < V; ++q) v[q] = e < E ? w[static_cast<int64_t>(k0 + q) * E + e] : 0.0f;
+#pragma unroll
+  for (int s = 0; s < S; ++s) {
+    const u32x4 p = Piece<T>::narrow(v);
+    out[((static_cast<int64_t>(step) * EB + eb) * S + s) * 64 + lane] = p;
+    float back[V];
+    Piece<T>::widen(p, back);
+#pragma unroll
+    for (int q = 0; q < V; ++q) v[q] -= back[q];
+  }
+}
+
+// Workgroups below count_blocks count their share of the tokens; the others
+// lay W out.
+template <typename T>
+__global__ __launch_bounds__(kCountThreads) void balance_count_kernel(const BalArgs a,
+                                                                     const int32_t* __restrict__ idx,
+                                                                     const float* __restrict__ w, int EB,
+                                                                     u32x4* __restrict__ wf,
+                                                                     int32_t* __restrict__ parts) {
+  constexpr int kWaves = kCountThreads / 64;
+  __shared__ int hist[kWaves][65];
+  if (static_cast<int>(blockIdx.x) >= a.count_blocks) {
+    split_router<T>(w, a.d, a.E, EB, wf, (blockIdx.x - a.count_blocks) * kCountThreads + threadIdx.x);
+    return;
+  }
+  for (int i = threadIdx.x; i < kWaves * 65; i += kCountThreads) (&hist[0][0])[i] = 0;
+  __syncthreads();
+  int* mine = hist[threadIdx.x >> 6];
+  const int64_t t0 = a.T * blockIdx.x / a.count_blocks, t1 = a.T * (blockIdx.x + 1) / a.count_blocks;
+  const int64_t s1 = t1 * a.k;
+  constexpr int kBatch = 8;
+  for (int64_t s0 = t0 * a.k + threadIdx.x; s0 < s1; s0 += kBatch * kCountThreads) {
+    int e[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int64_t s = s0 + u * kCountThreads;
+      e[u] = s < s1 ? idx[s] : -1;
+    }
+    if (a.mask) {
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int64_t s = s0 + u * kCountThreads;
+        // slots are below 2^31
+        if (s < s1 && !a.mask[static_cast<uint32_t>(s) / static_cast<uint32_t>(a.k)]) e[u] = -1;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u)
+      if (static_cast<unsigned>(e[u]) < static_cast<unsigned>(a.E)) atomicAdd(mine + e[u], 1);
+  }
+  int kept = 0;
+  if (a.mask) {
+    for (int64_t t = t0 + threadIdx.x; t < t1; t += kCountThreads) kept += a.mask[t] != 0;
+  } else if (threadIdx.x == 0) {
+    kept = static_cast<int>(t1 - t0);
+  }
+  if (kept) atomicAdd(mine + 64, kept);
+  __syncthreads();
+  if (threadIdx.x < 65) {
+    int v = 0;
+#pragma unroll
+    for (int u = 0; u < kWaves; ++u) v += hist[u][threadIdx.x];
+    parts[blockIdx.x * 65 + threadIdx.x] = v;
+  }
+}
+
+// ------------------------------------------------------------------- logits
+
+__device__ __forceinline__ bool kept_token(const BalArgs& a, int64_t t) {
+  return t < a.T && (!a.mask || a.mask[t]);
+}
+
+template <typename T>
+struct BalOp;
+template <>
+struct BalOp<bf16_t> {
+  static constexpr int S = 3;
+  __device__ static void step(const u32x4 (&w)[3], const u32x4& x, f32x16_t& acc) {
+    const bf16x8_t xv = __builtin_bit_cast(bf16x8_t, x);
+    // the smallest products first
+#pragma unroll
+    for (int s = 2; s >= 0; --s)
+      acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, w[s]), xv, acc, 0, 0, 0);
+  }
+};
+template <>
+struct BalOp<float> {
+  static constexpr int S = 1;
+  __device__ static void step(const u32x4 (&w)[1], const u32x4& x, f32x16_t& acc) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      acc = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(w[0][e]), __uint_as_float(x[e]), acc, 0, 0, 0);
+  }
+};
+
+// The kept gradient by the logits of eight experts of a token (one lane) or,
+// in fp32, of four; the two lanes of a token hold experts in turns of four.
+__device__ __forceinline__ void store_dl(bf16_t* row, int eb, int EP, int g, const float (&dl)[16]) {
+  uint32_t hi[8], lo[8];
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    hi[q] = pack_bf16x2(dl[2 * q], dl[2 * q + 1]);
+    lo[q] = pack_bf16x2(dl[2 * q] - bf16lo(hi[q]), dl[2 * q + 1] - bf16hi(hi[q]));
+  }
+  // registers 2 r, 2 r + 1 are experts 8 r + 4 g .. + 3: after the swap of two
+  // runs the lower lane has all eight of the first, the upper of the second
+#pragma unroll
+  for (int r = 0; r < 4; r += 2) {
+    auto put = [&](bf16_t* dst, const uint32_t (&v)[8]) {
+      const auto a = __builtin_amdgcn_permlane32_swap(v[2 * r], v[2 * r + 2], false, false);
+      const auto b = __builtin_amdgcn_permlane32_swap(v[2 * r + 1], v[2 * r + 3], false, false);
+      *reinterpret_cast<u32x4*>(dst + 32 * eb + 8 * (r + g)) = (u32x4){a[0], b[0], a[1], b[1]};
+    };
+    put(row, hi);
+    put(row + EP, lo);
+  }
+}
+__device__ __forceinline__ void store_dl(float* row, int eb, int, int g, const float (&dl)[16]) {
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+    store4(row + 32 * eb + 8 * r + 4 * g, dl[4 * r], dl[4 * r + 1], dl[4 * r + 2], dl[4 * r + 3]);
+}
+
+// A wave makes the logits of 32 RT tokens: MFMA 32x32 with W first, so a lane
+// ends up with 16 EB experts of token lane % 32 and the lane 32 on with the
+// others. x goes from memory straight into operands (a row's 128 bytes over
+// four loads), W's operands come from the caches, where every wave finds the
+// same. KS waves share a token's columns and are added in order.
+template <typename T, int EB, int RT, int KS, int NW>
+__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(RT == 2 ? 2 : 3)))
+void balance_logits_kernel(const BalArgs a, const T* __restrict__ x, const u32x4* __restrict__ wf,
+                           T* __restrict__ saved) {
+  constexpr int S = BalOp<T>::S, kLine = 128 / sizeof(T), EP = 32 * EB;
+  __shared__ float acc_lds[KS > 1 ? NW : 1][KS > 1 ? 16 * EB * 64 : 1];
+  __shared__ float sums[NW][EP + 1];
+  __shared__ int tallies[NW][65];
+  __shared__ __attribute__((aligned(16))) float share[64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int g = lane >> 5, r32 = lane & 31;
+  const int slice = wave % KS;
+  const int64_t row0 = (static_cast<int64_t>(blockIdx.x) * (NW / KS) + wave / KS) * 32 * RT;
+  if (saved) {
+    // the loads, for the gradient
+    for (int e = lane; e < 65; e += 64) {
+      int v = 0;
+#pragma unroll 8
+      for (int p = wave; p < a.count_blocks; p += NW) v += a.parts[p * 65 + e];
+      tallies[wave][e] = v;
+    }
+  }
+  f32x16_t acc[RT][EB];
+#pragma unroll
+  for (int i = 0; i < RT; ++i)
+#pragma unroll
+    for (int b = 0; b < EB; ++b)
+#pragma unroll
+      for (int q = 0; q < 16; ++q) acc[i][b][q] = 0.0f;
+
+  const int lines = a.d / kLine;
+  const T* rows[RT];
+#pragma unroll
+  for (int i = 0; i < RT; ++i) {
+    const int64_t r = row0 + 32 * i + r32;
+    rows[i] = x + (r < a.T ? r : a.T - 1) * a.d + g * (16 / static_cast<int>(sizeof(T)));
+  }
+  u32x4 xv[2][RT][4], wv[2][EB][S];
+  auto load_x = [&](int set, int line) {
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        xv[set][i][q] = *reinterpret_cast<const u32x4*>(rows[i] + line * kLine + q * (kLine / 4));
+  };
+  auto load_w = [&](int set, int step) {
+#pragma unroll
+    for (int b = 0; b < EB; ++b)
+#pragma unroll
+      for (int s = 0; s < S; ++s) wv[set][b][s] = wf[((static_cast<int64_t>(step) * EB + b) * S + s) * 64 + lane];
+  };
+  auto multiply = [&](int set, int line, int next) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      load_w((q & 1) ^ 1, q < 3 ? line * 4 + q + 1 : next * 4);
+#pragma unroll
+      for (int b = 0; b < EB; ++b)
+#pragma unroll
+        for (int i = 0; i < RT; ++i) BalOp<T>::step(wv[q & 1][b], xv[set][i][q], acc[i][b]);
+    }
+  };
+  if (slice < lines) {
+    load_x(0, slice);
+    load_w(0, slice * 4);
+    for (int line = slice; line < lines; line += 2 * KS) {
+      const int n1 = line + KS < lines ? line + KS : line, n2 = line + 2 * KS < lines ? line + 2 * KS : n1;
+      load_x(1, n1);
+      multiply(0, line, n1);
+      load_x(0, n2);
+      if (line + KS < lines) multiply(1, n1, n2);
+    }
+  }
+  if constexpr (KS > 1) {
+#pragma unroll
+    for (int b = 0; b < EB; ++b)
+#pragma unroll
+      for (int q = 0; q < 16; ++q) acc_lds[wave][(b * 16 + q) * 64 + lane] = acc[0][b][q];
+  }
+  __syncthreads();
+  if constexpr (KS > 1) {
+    if (slice == 0) {
+#pragma unroll
+      for (int b = 0; b < EB; ++b)
+#pragma unroll
+        for (int q = 0; q < 16; ++q) {
+          float v = acc_lds[wave][(b * 16 + q) * 64 + lane];
+#pragma unroll
+          for (int s = 1; s < KS; ++s) v += acc_lds[wave + s][(b * 16 + q) * 64 + lane];
+          acc[0][b][q] = v;
+        }
+    }
+  }
+  float inv_n = 0.0f;
+  if (saved) {
+    int n = 0;
+#pragma unroll
+    for (int u = 0; u < NW; ++u) n += tallies[u][64];
+    inv_n = n > 0 ? 1.0f / static_cast<float>(n) : 0.0f;
+    if (threadIdx.x < 64) {
+      int v = 0;
+#pragma unroll
+      for (int u = 0; u < NW; ++u) v += tallies[u][threadIdx.x];
+      share[threadIdx.x] = n > 0 ? static_cast<float>(v) / (static_cast<float>(n) * static_cast<float>(a.k)) : 0.0f;
+    }
+    __syncthreads();
+  }
+
+  float psum[EB][16], zsum = 0.0f;
+#pragma unroll
+  for (int b = 0; b < EB; ++b)
+#pragma unroll
+    for (int q = 0; q < 16; ++q) psum[b][q] = 0.0f;
+  if (slice == 0) {
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      const int64_t t = row0 + 32 * i + r32;
+      const bool keep = kept_token(a, t);
+      float other, most = -__builtin_inff();
+#pragma unroll
+      for (int b = 0; b < EB; ++b)
+#pragma unroll
+        for (int q = 0; q < 16; ++q)
+          if (32 * b + 8 * (q / 4) + 4 * g + q % 4 < a.E) most = fmaxf(most, acc[i][b][q]);
+      most = lane32(most, &other);
+      most = fmaxf(most, other);
+      float p[EB][16], total = 0.0f;
+#pragma unroll
+      for (int b = 0; b < EB; ++b)
+#pragma unroll
+        for (int q = 0; q < 16; ++q) {
+          p[b][q] = 32 * b + 8 * (q / 4) + 4 * g + q % 4 < a.E ? __expf(acc[i][b][q] - most) : 0.0f;
+          total += p[b][q];
+        }
+      total = lane32(total, &other);
+      total += other;
+      const float inv = 1.0f / total, lse = most + logf(total);
+      float inner = 0.0f;
+#pragma unroll
+      for (int b = 0; b < EB; ++b)
+#pragma unroll
+        for (int q = 0; q < 16; ++q) {
+          p[b][q] *= inv;
+          if (keep) psum[b][q] += p[b][q];
+        }
+      if (keep && g == 0) zsum += lse * lse;
+      if (!saved) continue;
+      float f[EB][16];
+#pragma unroll
+      for (int b = 0; b < EB; ++b)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float4 v = *reinterpret_cast<const float4*>(share + 32 * b + 8 * r + 4 * g);
+          f[b][4 * r] = v.x; f[b][4 * r + 1] = v.y; f[b][4 * r + 2] = v.z; f[b][4 * r + 3] = v.w;
+        }
+#pragma unroll
+      for (int b = 0; b < EB; ++b)
+#pragma unroll
+        for (int q = 0; q < 16; ++q) inner = __builtin_fmaf(f[b][q], p[b][q], inner);
+      inner = lane32(inner, &other);
+      inner += other;
+      const float zed = a.c2 * lse;
+#pragma unroll
+      for (int b = 0; b < EB; ++b) {
+        float dl[16];
+#pragma unroll
+        for (int q = 0; q < 16; ++q)
+          dl[q] = keep ? p[b][q] * __builtin_fmaf(a.c1, f[b][q] - inner, zed) * inv_n : 0.0f;
+        if (t < a.T) store_dl(saved + t * (sizeof(T) == 2 ? 2 * EP : EP), b, EP, g, dl);
+      }
+    }
+  }
+  // sums over the wave's 32 lanes, then over the waves
+#pragma unroll
+  for (int b = 0; b < EB; ++b)
+#pragma unroll
+    for (int q = 0; q < 16; ++q) {
+      float other, v = row16_sum(psum[b][q]);
+      v = lane16(v, &other) + other;
+      if (r32 == 0) sums[wave][32 * b + 8 * (q / 4) + 4 * g + q % 4] = v;
+    }
+  zsum = wave_sum(zsum);
+  if (lane == 0) sums[wave][EP] = zsum;
+  __syncthreads();
+  if (threadIdx.x <= EP) {
+    float v = 0.0f;
+#pragma unroll
+    for (int u = 0; u < NW; u += KS) v += sums[u][threadIdx.x];
+    // the last one is the sum of lse^2
+    a.stats[static_cast<int64_t>(blockIdx.x) * 65 + (static_cast<int>(threadIdx.x) == EP ? 64 : threadIdx.x)] = v;
+  }
+}
+
+// The results from the workgroups' sums: column e of them in thread e's group,
+// 16 threads to a column.
+__global__ __launch_bounds__(1024) void balance_loss_kernel(const BalArgs a, int groups, float balance, float z,
+                                                            int32_t* __restrict__ counts,
+                                                            float* __restrict__ mean_prob,
+                                                            float* __restrict__ loss) {
+  __shared__ float sums[16][64], zeds[1024], even[64];
+  __shared__ int tallies[65];
+  const int e = threadIdx.x % 64, j = threadIdx.x / 64;
+  if (threadIdx.x < 65) {
+    int v = 0;
+#pragma unroll 8
+    for (int p = 0; p < a.count_blocks; ++p) v += a.parts[p * 65 + threadIdx.x];
+    tallies[threadIdx.x] = v;
+  }
+  float v = 0.0f, zed = 0.0f;
+  if (e < a.E) {
+#pragma unroll 8
+    for (int p = j; p < groups; p += 16) v += a.stats[static_cast<int64_t>(p) * 65 + e];
+  }
+  for (int p = threadIdx.x; p < groups; p += 1024) zed += a.stats[static_cast<int64_t>(p) * 65 + 64];
+  sums[j][e] = v;
+  zeds[threadIdx.x] = zed;
+  __syncthreads();
+#pragma unroll
+  for (int half = 512; half > 0; half /= 2) {
+    if (static_cast<int>(threadIdx.x) < half) zeds[threadIdx.x] += zeds[threadIdx.x + half];
+    __syncthreads();
+  }
+  const int n = tallies[64];
+  const float inv_n = n > 0 ? 1.0f / static_cast<float>(n) : 0.0f;
+  if (j == 0) {
+    float p = 0.0f;
+#pragma unroll
+    for (int u = 0; u < 16; ++u) p += sums[u][e];
+    p *= inv_n;
+    even[e] = 0.0f;
+    if (e < a.E) {
+      mean_prob[e] = p;
+      counts[e] = tallies[e];
+      even[e] = n > 0 ? static_cast<float>(tallies[e]) / (static_cast<float>(n) * static_cast<float>(a.k)) * p : 0.0f;
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x < 64) {
+    const float total = static_cast<float>(a.E) * wave_sum(even[threadIdx.x]);
+    if (threadIdx.x == 0) {
+      const float zz = zeds[0] * inv_n;
+      loss[0] = __builtin_fmaf(balance, total, z * zz);
+      loss[1] = total;
+      loss[2] = zz;
+    }
+  }
+}
+
+// ----------------------------------------------------------------- backward
+
+// dx and partial sums of dW for 128 columns: two waves side by side, four pairs
+// of them over the tokens, 32 at a time. dl of these goes through LDS, where
+// each wave takes it twice: token rows for dx = dl W^T (W of its 64 columns stays
+// in registers) and, turned, expert rows for dW = dl^T x, whose 64 x 64 sums stay
+// in registers too. x comes from memory straight into operands (skinny.h).
+constexpr int kGradCols = 128, kGradSets = 4, kGradThreads = 512;
+
+struct BalGradArgs {
+  int64_t T;
+  int E, d;
+  int ranges;          // of the tokens: a partial dW each
+  const uint8_t* mask;
+  const float* gloss;  // or null
+  bool add;
+};
+
+// W of a wave's 64 columns as the first operand of dx = dl W^T, and dl's LDS rows.
+template <typename T, int EB>
+struct BalGrad;
+
+template <int EB>
+struct BalGrad<bf16_t, EB> {
+  static constexpr int EP = 32 * EB, ROW = 4 * EP;  // bytes of a token: high halves, then low
+  // Fragment j's row i is column 32 (j / 2) + 8 (i / 4) + 4 (j % 2) + i % 4: a
+  // lane ends up with eight consecutive columns of two fragments.
+  u32x4 hi[4][EB], lo[4][EB];
+  __device__ void load(const float* w, int c0, int E, int lane) {
+    const int i = lane & 15, g = lane >> 4;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float* row = w + static_cast<int64_t>(c0 + 32 * (j / 2) + 8 * (i / 4) + 4 * (j % 2) + i % 4) * E;
+#pragma unroll
+      for (int b = 0; b < EB; ++b) {
+        float v[8], back[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          const int e = 32 * b + 8 * g + q;
+          v[q] = e < E ? row[e] : 0.0f;
+        }
+        hi[j][b] = Piece<bf16_t>::narrow(v);
+        Piece<bf16_t>::widen(hi[j][b], back);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[q] -= back[q];
+        lo[j][b] = Piece<bf16_t>::narrow(v);
+      }
+    }
+  }
+  // 16-byte chunk c of token row r: spread over the banks
+  __device__ static int at(int r, int c) { return r * ROW + ((c ^ (r & (ROW / 16 - 1))) << 4); }
+  // dx of 16 tokens (rows r0..): v[h] are columns c0 + 32 h + 8 (lane / 16) .. + 7
+  // of token lane % 16.
+  __device__ void dx(const char* lds, int r0, int lane, float (&v)[2][8]) const {
+    const int r = r0 + (lane & 15), g = lane >> 4;
+    f32x4_t acc[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[j] = (f32x4_t){0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int b = 0; b < EB; ++b) {
+      const bf16x8_t dh = *reinterpret_cast<const bf16x8_t*>(lds + at(r, 4 * b + g));
+      const bf16x8_t dlo = *reinterpret_cast<const bf16x8_t*>(lds + at(r, 4 * EB + 4 * b + g));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, lo[j][b]), dh, acc[j], 0, 0, 0);
+        acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, hi[j][b]), dlo, acc[j], 0, 0, 0);
+        acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, hi[j][b]), dh, acc[j], 0, 0, 0);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[j / 2][4 * (j % 2) + q] = acc[j][q];
+  }
+  // dW: expert rows 16 m + i of the 32 tokens, high and low half, times x.
+  __device__ static void dw(const char* lds, const SkinnyW<bf16_t>& x, int lane, f32x4_t (&acc)[4][2 * EB]) {
+    typedef short v4i16 __attribute__((ext_vector_type(4)));
+    typedef __attribute__((address_space(3))) v4i16 lds_v4i16;
+    const int s = lane & 15, g = lane >> 4;
+    bf16x8_t xf[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) xf[j] = x.frag(j);
+#pragma unroll
+    for (int m = 0; m < 4 * EB; ++m) {  // low halves behind the high ones
+      const int c = 16 * m + 4 * (s & 3), r = 8 * g + (s >> 2);
+      const char* p0 = lds + at(r, c >> 3) + (c & 7) * 2;
+      const char* p1 = lds + at(r + 4, c >> 3) + (c & 7) * 2;
+      const v4i16 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(p0));
+      const v4i16 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(p1));
+      const bf16x8_t dl = __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        acc[j][m % (2 * EB)] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(dl, xf[j], acc[j][m % (2 * EB)], 0, 0, 0);
+    }
+  }
+  // Expert of register q of sums m.
+  __device__ static int expert(int m, int q, int lane) { return 16 * m + 4 * (lane >> 4) + q; }
+};
+
+template <int EB>
+struct BalGrad<float, EB> {
+  static constexpr int EP = 32 * EB, ROW = 4 * EP;
+  // Fragment j's row i is column 16 j + i; step s takes element s % 4 of the lane
+  // groups' 16 bytes s / 4 on both sides: experts 16 (s / 4) + 4 (lane / 16) + s % 4.
+  float w[4][2 * EB][4];
+  __device__ void load(const float* src, int c0, int E, int lane) {
+    const int i = lane & 15, g = lane >> 4;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int b = 0; b < 2 * EB; ++b)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int e = 16 * b + 4 * g + q;
+          w[j][b][q] = e < E ? src[static_cast<int64_t>(c0 + 16 * j + i) * E + e] : 0.0f;
+        }
+  }
+  __device__ static int at(int r, int c) { return r * ROW + ((c ^ (r & (ROW / 16 - 1))) << 4); }
+  // v[h]: columns c0 + 16 (2 h) + 4 (lane / 16) .. + 3, then 16 further on
+  __device__ void dx(const char* lds, int r0, int lane, float (&v)[2][8]) const {
+    const int r = r0 + (lane & 15), g = lane >> 4;
+    f32x4_t acc[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[j] = (f32x4_t){0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int b = 0; b < 2 * EB; ++b) {
+      const f32x4_t dl = *reinterpret_cast<const f32x4_t*>(lds + at(r, 4 * b + g));
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          acc[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(w[j][b][q], dl[q], acc[j], 0, 0, 0);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[j / 2][4 * (j % 2) + q] = acc[j][q];
+  }
+  // Sums m take experts 4 i + m of every 64 (32 with one block: 2 i + m).
+  __device__ static void dw(const char* lds, const SkinnyW<float>& x, int lane, f32x4_t (&acc)[4][2 * EB]) {
+    const int s = lane & 15, g = lane >> 4;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = 4 * i + g;
+      float dl[2 * EB];
+      const char* p = lds + at(r, s * EB / 2) + (EB == 1 ? (s & 1) * 8 : 0);
+#pragma unroll
+      for (int m = 0; m < 2 * EB; ++m) dl[m] = reinterpret_cast<const float*>(p)[m];
+#pragma unroll
+      for (int m = 0; m < 2 * EB; ++m)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          acc[j][m] = __builtin_amdgcn_mfma_f32_16x16x4f32(dl[m], __uint_as_float(x.r[i][j]), acc[j][m], 0, 0, 0);
+    }
+  }
+  __device__ static int expert(int m, int q, int lane) { return 2 * EB * (4 * (lane >> 4) + q) + m; }
+};
+
+// Tokens of x that the mask leaves out, zeroed: they may hold NaN.
+__device__ __forceinline__ void drop_tokens(SkinnyW<bf16_t>& x, const uint8_t* mask, int64_t t0, int64_t T, int lane) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int64_t t = t0 + 8 * (lane >> 4) + i;
+    if (t < T && !mask[t]) x.r[i] = (u32x2){0u, 0u};
+  }
+}
+__device__ __forceinline__ void drop_tokens(SkinnyW<float>& x, const uint8_t* mask, int64_t t0, int64_t T, int lane) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int64_t t = t0 + 4 * i + (lane >> 4);
+    if (t < T && !mask[t]) x.r[i] = (u32x4){0u, 0u, 0u, 0u};
+  }
+}
+
+template <typename T, int EB>
+__global__ __launch_bounds__(kGradThreads) __attribute__((amdgpu_waves_per_eu(2)))
+void balance_grad_kernel(const BalGradArgs a, const T* __restrict__ x, const float* __restrict__ w,
+                         const T* __restrict__ saved, T* dx, float* __restrict__ partial) {
+  typedef BalGrad<T, EB> G;
+  constexpr int EP = 32 * EB, kPieces = 32 * G::ROW / 16;       // 16-byte pieces of 32 tokens
+  constexpr int kLoads = kGradSets * kPieces / kGradThreads;    // of a thread
+  constexpr int kBuf = kGradSets * 32 * G::ROW;
+  static_assert(kGradSets * kPieces % kGradThreads == 0 && kPieces % 64 == 0, "loads");
+  // the sums of three sets, a quarter at a time, share the place
+  constexpr int kSums = (kGradSets - 1) * 2 * 2 * EB * 4 * 64 * 4;
+  __shared__ __attribute__((aligned(1024))) char smem[2 * kBuf > kSums ? 2 * kBuf : kSums];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int set = wave / 2;
+  const int slices = a.d / kGradCols;
+  const int logical = xcd_remap(blockIdx.x, gridDim.x);
+  const int range = logical / slices, c0 = logical % slices * kGradCols + 64 * (wave & 1);
+  const int64_t chunks = (a.T + 31) / 32;
+  const int64_t k0 = chunks * range / a.ranges, k1 = chunks * (range + 1) / a.ranges;
+  const float scale = a.gloss ? a.gloss[0] : 1.0f;
+  G weights;
+  weights.load(w, c0, a.E, lane);
+  f32x4_t acc[4][2 * EB];
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int m = 0; m < 2 * EB; ++m) acc[j][m] = (f32x4_t){0.0f, 0.0f, 0.0f, 0.0f};
+
+  u32x4 dl[kLoads];
+  // tokens past the end, and chunks past the range, as zeros
+  auto load_dl = [&](int64_t k) {
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u) {
+      const int i = u * kGradThreads + threadIdx.x, r = i % kPieces / (G::ROW / 16);
+      const int64_t chunk = k + i / kPieces, t = chunk * 32 + r;
+      dl[u] = (u32x4){0u, 0u, 0u, 0u};
+      if (chunk < k1 && t < a.T)
+        dl[u] = *reinterpret_cast<const u32x4*>(reinterpret_cast<const char*>(saved) + t * G::ROW + i % (G::ROW / 16) * 16);
+    }
+  };
+  auto store_lds = [&](char* buf) {
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u) {
+      const int i = u * kGradThreads + threadIdx.x, r = i % kPieces / (G::ROW / 16);
+      *reinterpret_cast<u32x4*>(buf + i / kPieces * 32 * G::ROW + G::at(r, i % (G::ROW / 16))) = dl[u];
+    }
+  };
+  SkinnyW<T> xv[2];
+  auto load_x = [&](int to, int64_t k) {
+    const int64_t chunk = k + set, t0 = chunk * 32;
+    // rows from t0 on, none past the range or the end
+    const int64_t left = chunk < k1 ? a.T - t0 : 0;
+    xv[to].load(x + t0 * a.d, a.d, 0, static_cast<int>(left < 32 ? left : 32), c0 + 4 * (lane & 15), a.d, lane);
+    if (a.mask && left > 0) drop_tokens(xv[to], a.mask, t0, a.T, lane);
+  };
+  auto work = [&](int from, const char* lds, int64_t k) {
+    const int64_t t0 = (k + set) * 32;
+    if (k + set < k1) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float v[2][8];
+        weights.dx(lds, 16 * h, lane, v);
+        const int64_t t = t0 + 16 * h + (lane & 15);
+        if (t >= a.T) continue;
+        T* row = dx + t * a.d + c0;
+        constexpr int V = Piece<T>::V;
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int q = 0; q < 8 / V; ++q) {
+            const int c = sizeof(T) == 2 ? 32 * n + 8 * (lane >> 4) : 16 * (2 * n + q) + 4 * (lane >> 4);
+            float e[V], old[V];
+            u32x4 o = (u32x4){0u, 0u, 0u, 0u};
+            if (a.add) o = *reinterpret_cast<const u32x4*>(row + c);
+            Piece<T>::widen(o, old);
+#pragma unroll
+            for (int m = 0; m < V; ++m) e[m] = __builtin_fmaf(scale, v[n][q * V + m], old[m]);
+            *reinterpret_cast<u32x4*>(row + c) = Piece<T>::narrow(e);
+          }
+      }
+      G::dw(lds, xv[from], lane, acc);
+    }
+  };
+  load_dl(k0);
+  load_x(0, k0);
+  store_lds(smem);
+  __syncthreads();
+  for (int64_t k = k0; k < k1; k += 2 * kGradSets) {
+    // buffers in turn; the other one was last read before the last barrier
+    load_dl(k + kGradSets);
+    load_x(1, k + kGradSets);
+    work(0, smem + set * 32 * G::ROW, k);
+    store_lds(smem + kBuf);
+    __syncthreads();
+    load_dl(k + 2 * kGradSets);
+    load_x(0, k + 2 * kGradSets);
+    work(1, smem + kBuf + set * 32 * G::ROW, k + kGradSets);
+    store_lds(smem);
+    __syncthreads();
+  }
+  // the sets' sums in order, a fragment of columns at a time, then out
+  float* sums = reinterpret_cast<float*>(smem);
+  float* out = partial + static_cast<int64_t>(range) * a.d * EP;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (j) __syncthreads();
+    if (set > 0) {
+#pragma unroll
+      for (int m = 0; m < 2 * EB; ++m)
+        *reinterpret_cast<f32x4_t*>(sums + (((wave - 2) * 2 * EB + m) * 64 + lane) * 4) = acc[j][m];
+    }
+    __syncthreads();
+    if (set == 0) {
+#pragma unroll
+      for (int m = 0; m < 2 * EB; ++m) {
+        f32x4_t v = acc[j][m];
+#pragma unroll
+        for (int u = 0; u < kGradSets - 1; ++u)
+          v += *reinterpret_cast<const f32x4_t*>(sums + (((2 * u + wave) * 2 * EB + m) * 64 + lane) * 4);
+        // column of x: 4 (lane % 16) + j
+        float* row = out + static_cast<int64_t>(c0 + 4 * (lane & 15) + j) * EP;
+        if (sizeof(T) == 2) {
+          *reinterpret_cast<f32x4_t*>(row + G::expert(m, 0, lane)) = v;
+        } else {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) row[G::expert(m, q, lane)] = v[q];
+        }
+      }
+    }
+  }
+}
+
+// dW [d][E] from the ranges' partial sums [ranges][d][EP], in order within 16
+// threads, these then in order: four experts a thread.
+__global__ __launch_bounds__(256) void balance_sum_kernel(const float* __restrict__ partial, int ranges, int d,
+                                                          int E, int EP, const float* __restrict__ gloss,
+                                                          bool add, float* __restrict__ dw) {
+  __shared__ float4 sums[16][16];
+  const int c = threadIdx.x % 16, j = threadIdx.x / 16;
+  const int64_t cells = static_cast<int64_t>(d) * EP / 4, i = static_cast<int64_t>(blockIdx.x) * 16 + c;
+  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+  for (int p = j; p < ranges; p += 16) {
+    const float4 o = *reinterpret_cast<const float4*>(partial + (p * cells + i) * 4);
+    v.x += o.x; v.y += o.y; v.z += o.z; v.w += o.w;
+  }
+  sums[j][c] = v;
+  __syncthreads();
+  if (j) return;
+#pragma unroll
+  for (int u = 1; u < 16; ++u) {
+    const float4 o = sums[u][c];
+    v.x += o.x; v.y += o.y; v.z += o.z; v.w += o.w;
+  }
+  const float scale = gloss ? gloss[0] : 1.0f, s[4] = {v.x, v.y, v.z, v.w};
+  const int64_t row = i * 4 / EP;
+  const int e = static_cast<int>(i * 4 % EP);
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    if (e + q < E) {
+      float* p = dw + row * E + e + q;
+      *p = add ? __builtin_fmaf(scale, s[q], *p) : scale * s[q];
+    }
+}
+
+__global__ __launch_bounds__(256) void balance_zero_kernel(float* p, int64_t n) {
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i < n) p[i] = 0.0f;
+}
+
+// ------------------------------------------------------------------ layouts
+
+// Tokens of a logits workgroup, and its form: 256 with whole rows of 64 a wave
+// where that gives every CU two workgroups, else waves that share the columns.
+int logits_rows(int64_t T) { return T >= 65536 ? 256 : 32; }
+
+int grad_ranges(const moe_balance& b) {
+  const int64_t slices = b.d_model / kGradCols, chunks = (b.tokens + 31) / 32;
+  int64_t r = (256 + slices - 1) / slices;
+  const int64_t most = (chunks + kGradSets - 1) / kGradSets;
+  if (r > most) r = most;
+  return static_cast<int>(r < 1 ? 1 : r);
+}
+
+struct BalLayout {
+  size_t parts, stats, wf, partial, total;
+};
+BalLayout bal_layout(const moe_balance& b) {
+  BalLayout L{};
+  size_t o = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = o;
+    o = align_up(o + bytes, 256);
+    return at;
+  };
+  const size_t EP = 32 * expert_blocks(b.experts), d = b.d_model;
+  L.parts = take(kCountBlocks * 65 * sizeof(int32_t));
+  L.stats = take((b.tokens + logits_rows(b.tokens) - 1) / logits_rows(b.tokens) * 65 * sizeof(float));
+  L.wf = take(d * EP * (b.dtype == MOE_BF16 ? 6 : 4));
+  L.total = o;
+  o = 0;  // the backward has the place for itself
+  L.partial = take(static_cast<size_t>(grad_ranges(b)) * d * EP * sizeof(float));
+  if (o > L.total) L.total = o;
+  return L;
+}
+
+template <typename T, int EB>
+void launch_logits(const BalArgs& a, const T* x, const u32x4* wf, T* saved, hipStream_t s) {
+  const int rows = logits_rows(a.T);
+  const dim3 grid(static_cast<unsigned>((a.T + rows - 1) / rows));
+  if (rows == 256)
+    MOE_LAUNCH("balance_logits", (balance_logits_kernel<T, EB, 2, 1, 4>), grid, dim3(256), 0, s, a, x, wf, saved);
+  else
+    MOE_LAUNCH("balance_logits", (balance_logits_kernel<T, EB, 1, 4, 4>), grid, dim3(256), 0, s, a, x, wf, saved);
+}
+
+template <typename T>
+hipError_t balance_t(const moe_balance& b, const void* x, const float* w, const int32_t* idx, const uint8_t* mask,
+                     int32_t* counts, float* mean_prob, float* loss, void* saved, void* ws, hipStream_t s) {
+  const BalLayout L = bal_layout(b);
+  char* W = static_cast<char*>(ws);
+  const int EB = expert_blocks(b.experts);
+  int32_t* parts = reinterpret_cast<int32_t*>(W + L.parts);
+  u32x4* wf = reinterpret_cast<u32x4*>(W + L.wf);
+  BalArgs a{b.tokens, b.experts, b.top_k, b.d_model, b.balance * static_cast<float>(b.experts), 2.0f * b.z, mask,
+            parts, 0, reinterpret_cast<float*>(W + L.stats)};
+  int groups = 0;
+  if (b.tokens > 0) {
+    const int64_t blocks = (b.tokens * b.top_k + 8 * kCountThreads - 1) / (8 * kCountThreads);
+    a.count_blocks = static_cast<int>(blocks > kCountBlocks ? kCountBlocks : blocks);
+    const int pieces = b.d_model / (2 * Piece<T>::V) * EB * 64;
+    MOE_LAUNCH("balance_count", balance_count_kernel<T>,
+               dim3(a.count_blocks + (pieces + kCountThreads - 1) / kCountThreads), dim3(kCountThreads), 0, s, a, idx,
+               w, EB, wf, parts);
+    if (EB == 1) launch_logits<T, 1>(a, static_cast<const T*>(x), wf, static_cast<T*>(saved), s);
+    else launch_logits<T, 2>(a, static_cast<const T*>(x), wf, static_cast<T*>(saved), s);
+    groups = static_cast<int>((b.tokens + logits_rows(b.tokens) - 1) / logits_rows(b.tokens));
+  }
+  MOE_LAUNCH("balance_loss", balance_loss_kernel, dim3(1), dim3(1024), 0, s, a, groups, b.balance, b.z, counts,
+             mean_prob, loss);
+  return hipGetLastError();
+}
+
+template <typename T, int EB>
+hipError_t balance_bwd_t(const moe_balance& b, const void* x, const float* w, const uint8_t* mask, const void* saved,
+                         const float* gloss, bool add, void* dx, float* dw, void* ws, hipStream_t s) {
+  const int ranges = grad_ranges(b), EP = 32 * EB;
+  float* partial = reinterpret_cast<float*>(static_cast<char*>(ws) + bal_layout(b).partial);
+  const BalGradArgs a{b.tokens, b.experts, b.d_model, ranges, mask, gloss, add};
+  MOE_LAUNCH("balance_grad", (balance_grad_kernel<T, EB>), dim3(b.d_model / kGradCols * ranges), dim3(kGradThreads), 0, s, a,
+             static_cast<const T*>(x), w, static_cast<const T*>(saved), static_cast<T*>(dx), partial);
+  MOE_LAUNCH("balance_sum", balance_sum_kernel, dim3(b.d_model * EP / 4 / 16), dim3(256), 0, s, partial, ranges,
+             b.d_model, b.experts, EP, gloss, add, dw);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+size_t balance_ws_bytes(const moe_balance& b) { return bal_layout(b).total; }
+size_t balance_saved_bytes(const moe_balance& b) {
+  const size_t n = align_up(static_cast<size_t>(b.tokens) * 32 * expert_blocks(b.experts) * 4, 256);
+  return n ? n : 256;
+}
+
+hipError_t launch_balance(const moe_balance& b, const void* x, const float* w, const int32_t* idx,
+                          const uint8_t* mask, int32_t* counts, float* mean_prob, float* loss, void* saved, void* ws,
+                          hipStream_t s) {
+  return b.dtype == MOE_BF16 ? balance_t<bf16_t>(b, x, w, idx, mask, counts, mean_prob, loss, saved, ws, s)
+                             : balance_t<float>(b, x, w, idx, mask, counts, mean_prob, loss, saved, ws, s);
+}
+
+hipError_t launch_balance_bwd(const moe_balance& b, const void* x, const float* w, const uint8_t* mask,
+                              const void* saved, const float* gloss, bool add, void* dx, float* dw, void* ws,
+                              hipStream_t s) {
+  if (b.tokens == 0) {
+    const int64_t n = static_cast<int64_t>(b.d_model) * b.experts;
+    if (!add)
+      MOE_LAUNCH("balance_zero", balance_zero_kernel, dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256), 0, s, dw, n);
+    return hipGetLastError();
+  }
+  const bool wide = expert_blocks(b.experts) == 2;
+  if (b.dtype == MOE_BF16)
+    return wide ? balance_bwd_t<bf16_t, 2>(b, x, w, mask, saved, gloss, add, dx, dw, ws, s)
+                : balance_bwd_t<bf16_t, 1>(b, x, w, mask, saved, gloss, add, dx, dw, ws, s);
+  return wide ? balance_bwd_t<float, 2>(b, x, w, mask, saved, gloss, add, dx, dw, ws, s)
+              : balance_bwd_t<float, 1>(b, x, w, mask, saved, gloss, add, dx, dw, ws, s);
+}
+
+}  // namespace moe

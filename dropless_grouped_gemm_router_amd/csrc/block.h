@@ -156,4 +156,30 @@ hipError_t launch_linear_i8(const moe_i8_linear& l, const void* x, const float* 
                             const int8_t* wq, const float* ws, const float* bias,
                             const moe_routing* r, void* y, void* work, hipStream_t s);
 
+size_t linear_ws_bytes(const moe_linear& l, bool training);
+size_t linear_saved_bytes(const moe_linear& l);
+hipError_t launch_linear(const moe_linear& l, const void* x, const void* w, const float* bias,
+                         const void* res, void* saved, void* y, void* ws, hipStream_t s);
+hipError_t launch_linear_bwd(const moe_linear& l, const void* x, const void* w, const void* saved,
+                             const void* dy, void* dx, void* dw, float* dbias, void* ws,
+                             hipStream_t s);
+
+hipError_t launch_residual_norm(const moe_residual_norm& n, const void* z, const void* res,
+                                const moe_norm_params& w, void* out, void* y, float* stats,
+                                hipStream_t s);
+size_t residual_norm_ws_bytes(const moe_residual_norm& n);
+hipError_t launch_residual_norm_bwd(const moe_residual_norm& n, const void* z, const void* res,
+                                    const moe_norm_params& w, const float* stats, const void* dout,
+                                    const void* dy, void* dz, void* dres, const moe_norm_grads& g,
+                                    void* ws, hipStream_t s);
+
+size_t balance_ws_bytes(const moe_balance& b);
+size_t balance_saved_bytes(const moe_balance& b);
+hipError_t launch_balance(const moe_balance& b, const void* x, const float* w, const int32_t* idx,
+                          const uint8_t* mask, int32_t* counts, float* mean_prob, float* loss,
+                          void* saved, void* ws, hipStream_t s);
+hipError_t launch_balance_bwd(const moe_balance& b, const void* x, const float* w,
+                              const uint8_t* mask, const void* saved, const float* gloss, bool add,
+                              void* dx, float* dw, void* ws, hipStream_t s);
+
 }  // namespace moe

@@ -1,0 +1,629 @@
+// Matrix product with bias, activation and residual in its epilogue, forward
+// and backward.
+//
+//   a = x W + bias, y = act(a) + residual
+//   da = dy act'(a), dx = da W^T, dW = x^T da, dbias = sum_rows da
+//
+// The forward is one product; what follows it is done on the sums while they
+// are in registers, where the tile's rows are handed out (mm_drain): the
+// residual's rows are read one strip ahead, y is rounded once, and the slope
+// act'(a) is kept for the backward, in bf16 in 20 bits of fixed point (slopes lie
+// in [-0.13, 1.13]; 2.5 bytes a value and off by 2^-20: 9e-7 in the 2-norm of
+// dbias, which is fp32 and has no other rounding. A slope of fp16, 2 bytes, made
+// 2.2e-4 of that, one of a bf16 pre-activation would make 2e-3).
+//
+// The weights come [inputs][outputs]: the forward runs over their leading
+// dimension, so it turns them K-contiguous first or, in bf16 up to some
+// thousand tokens, reads them where they are (in_place); up to 16 tokens (fp32:
+// 128) it reads them once, straight into MFMA operands (skinny.h). The
+// backward's dx reads them as they are. da is made in one pass over dy that
+// also adds up dbias and pads the rows; without an activation dy itself is da.
+#include "dense.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int64_t kFewRows = 16, kFewRowsF32 = 128;
+
+size_t elem_bytes(const moe_linear& l) { return l.dtype == MOE_BF16 ? 2 : 4; }
+bool few_rows(const moe_linear& l) { return l.tokens <= (l.dtype == MOE_BF16 ? kFewRows : kFewRowsF32); }
+// Elements between rows of the kept slopes.
+int64_t slope_pitch(const moe_linear& l) { return (l.outputs + 7) / 8 * 8; }
+
+// A kept slope of the bf16 form: slope 2^19 + 2^17, rounded, in 20 bits, as the
+// low bits of a number from 2^23 on; 0, which no slope gives, for a NaN.
+__device__ __forceinline__ uint32_t slope_code(float v) {
+  return __float_as_uint(fmaxf(__builtin_fmaf(v, 524288.0f, 8388608.0f + 131072.0f), 8388608.0f)) & 0xfffff;
+}
+__device__ __forceinline__ float slope_of(uint32_t code) {
+  return code ? __builtin_fmaf(static_cast<float>(code), 1.0f / 524288.0f, -0.25f) : __builtin_nanf("");
+}
+
+// Where slopes are kept: [rows][ld] of T's type, fp32 numbers or the codes' high
+// 16 bits, and behind these their low four, two to a byte.
+template <typename T>
+struct Slopes;
+template <>
+struct Slopes<float> {
+  float* p;
+  int64_t ld;
+  __device__ void put8(int64_t row, int n, const float (&v)[8]) const {
+    float* d = p + row * ld + n;
+    store4(d, v[0], v[1], v[2], v[3]);
+    store4(d + 4, v[4], v[5], v[6], v[7]);
+  }
+  __device__ void get8(int64_t row, int n, float (&v)[8]) const {
+    load4(p + row * ld + n, v);
+    load4(p + row * ld + n + 4, v + 4);
+  }
+  // One column a lane, the next lane having the next one; `in`: the lane has one.
+  __device__ void put1(int64_t row, int n, bool in, float v) const {
+    if (in) p[row * ld + n] = v;
+  }
+};
+template <>
+struct Slopes<bf16_t> {
+  uint16_t* p;
+  int64_t ld;
+  uint8_t* low;
+  __device__ void put8(int64_t row, int n, const float (&v)[8]) const {
+    u32x4 h;
+    uint32_t l = 0;
+#pragma unroll
+    for (int q = 0; q < 8; q += 2) {
+      const uint32_t a = slope_code(v[q]), b = slope_code(v[q + 1]);
+      h[q / 2] = (a >> 4) | (b >> 4 << 16);
+      l |= ((a & 15) | (b & 15) << 4) << 4 * q;
+    }
+    *reinterpret_cast<u32x4*>(p + row * ld + n) = h;
+    *reinterpret_cast<uint32_t*>(low + (row * ld + n) / 2) = l;
+  }
+  __device__ void get8(int64_t row, int n, float (&v)[8]) const {
+    const u32x4 h = *reinterpret_cast<const u32x4*>(p + row * ld + n);
+    const uint32_t l = *reinterpret_cast<const uint32_t*>(low + (row * ld + n) / 2);
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      v[q] = slope_of(((q & 1 ? h[q / 2] >> 16 : h[q / 2] & 0xffff) << 4) | (l >> 4 * q & 15));
+  }
+  __device__ void put1(int64_t row, int n, bool in, float v) const {
+    const uint32_t code = slope_code(v);
+    const uint32_t next = __float_as_uint(dpp<0xb1>(__uint_as_float(code)));  // lane ^ 1
+    if (!in) return;
+    p[row * ld + n] = static_cast<uint16_t>(code >> 4);
+    if (n % 2 == 0) low[(row * ld + n) / 2] = static_cast<uint8_t>((code & 15) | (next & 15) << 4);
+  }
+};
+
+// act(a) and its slope. In bf16 GELU's Phi(-|a|) is exp(-a^2 / 2) R(|a|), R
+// (0.5 exp(x^2 / 2) erfc(x / sqrt 2)) as t p(t), t = 1 / (1 + 0.28 x), with p of
+// degree 6 fitted to the smallest largest relative error, 4.0e-6 over all x in
+// fp32: 2^-18, far under bf16's rounding and the slopes'. One exponential serves
+// the value and the slope. (erff's two branches, 32 times eight of them, were
+// more than the compiler would unroll in a 256 x 256 tile.) fp32 takes erff.
+template <typename T, int kAct>
+__device__ __forceinline__ float lin_act(float a, float* slope) {
+  if constexpr (kAct == MOE_ACT_GELU && sizeof(T) == 2) {
+    const float x = fabsf(a), t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.28f, x, 1.0f));
+    float p = -0.05023228f;
+    p = __builtin_fmaf(p, t, 0.105446689f);
+    p = __builtin_fmaf(p, t, 0.024945872f);
+    p = __builtin_fmaf(p, t, 0.0944580585f);
+    p = __builtin_fmaf(p, t, 0.101935275f);
+    p = __builtin_fmaf(p, t, 0.111740693f);
+    p = __builtin_fmaf(p, t, 0.111703843f);
+    const float e = __expf(-0.5f * a * a), tail = e * (p * t);
+    const float cdf = a < 0.0f ? tail : 1.0f - tail;
+    *slope = __builtin_fmaf(a * 0.39894228f, e, cdf);
+    return a * cdf;
+  }
+  return act_value<kAct>(a, slope);
+}
+
+template <typename T>
+struct LinOut {
+  void* y;           // [M][ld], or fp32 sums [parts][M][ld] of the slices of K
+  int64_t ld;
+  const float* bias;  // or null
+  const void* res;    // [M][N], or null
+  Slopes<T> slope;    // p null: not kept
+  int64_t M;
+  int N;
+  u32x4* zero;        // null, or kTrZeroBytes that the product clears on the way
+};
+
+// Eight elements c.. of a row of n, widened; zeros behind the row.
+template <typename T, bool kFull>
+__device__ __forceinline__ void load8(const T* row, int c, int n, float (&v)[8]) {
+  constexpr int V = Piece<T>::V;
+#pragma unroll
+  for (int h = 0; h < 8 / V; ++h) {
+    const int at = c + h * V;
+    u32x4 p = (u32x4){0u, 0u, 0u, 0u};
+    if (kFull) p = load_any(row + at);
+    else if (at < n) p = load_piece(row, at, n);
+    float e[V];
+    Piece<T>::widen(p, e);
+#pragma unroll
+    for (int q = 0; q < V; ++q) v[h * V + q] = e[q];
+  }
+}
+
+// The callbacks of mm_drain. kPart: the slice's sums as they are; kFull: every
+// column of the tile is below N.
+template <typename T, typename Cfg, int kAct, bool kPart, bool kFull>
+struct LinRows {
+  static constexpr int kJ = Cfg::WN / MmStrip<Cfg>::CB, kPasses = mm_passes<Cfg, false>();
+  static constexpr int kPieces = 8 / Piece<T>::V;
+  const MmTile& t;
+  const LinOut<T>& o;
+  int base, n[kJ];
+  float bias[kPart ? 1 : kJ][8];
+  u32x4 res[kPart ? 1 : 2][kPasses][kPieces];
+
+  __device__ void cols(int j, int c) {
+    n[j] = base + c;
+    if constexpr (!kPart) {
+#pragma unroll
+      for (int q = 0; q < 8; ++q) bias[j][q] = 0.0f;
+      if (o.bias) load8<float, kFull>(o.bias, n[j], o.N, bias[j]);
+    }
+  }
+  __device__ void start(int, int, int) {}
+  __device__ void pre(int set, int j, int k, int m) {
+    if constexpr (!kPart) {
+      if (!o.res) return;
+      const T* row = static_cast<const T*>(o.res) + (t.row0 + m) * o.N;
+#pragma unroll
+      for (int h = 0; h < kPieces; ++h) {
+        const int c = n[j] + h * Piece<T>::V;
+        if (kFull) res[set][k][h] = load_any(row + c);
+        else if (c < o.N) res[set][k][h] = load_piece(row, c, o.N);
+      }
+    }
+  }
+  __device__ void row(int set, int, int j, int k, int m, const uint32_t (&v)[8]) {
+    const int64_t row = t.row0 + m;
+    float y[8];
+    if constexpr (kPart) {
+#pragma unroll
+      for (int q = 0; q < 8; ++q) y[q] = __uint_as_float(v[q]);
+      store8<float, kFull>(static_cast<float*>(o.y) + (t.part * o.M + row) * o.ld, n[j], o.N, y);
+    } else {
+      float slope[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) y[q] = lin_act<T, kAct>(__uint_as_float(v[q]) + bias[j][q], &slope[q]);
+      if (o.res) {
+#pragma unroll
+        for (int h = 0; h < kPieces; ++h) {
+          constexpr int V = Piece<T>::V;
+          float r[V];
+          Piece<T>::widen(res[set][k][h], r);
+#pragma unroll
+          for (int q = 0; q < V; ++q) y[h * V + q] += r[q];
+        }
+      }
+      store8<T, kFull>(static_cast<T*>(o.y) + row * o.ld, n[j], o.N, y);
+      if (kAct != MOE_ACT_NONE && o.slope.p && (kFull || n[j] < o.N)) o.slope.put8(row, n[j], slope);
+    }
+  }
+};
+
+template <typename T, typename Cfg, int kAct, bool kPart, bool kTurned>
+__global__ __launch_bounds__(Cfg::NT) __attribute__((amdgpu_waves_per_eu(Cfg::WPE)))
+void lin_tile_kernel(const MmArgs p, const LinOut<T> o) {
+  __shared__ __attribute__((aligned(1024))) char smem[MmStrip<Cfg>::LDS];
+  f32x16_t acc[Cfg::WM][Cfg::WN];
+  MmTile t;
+  if (o.zero && blockIdx.x == 0 && threadIdx.x < kTrZeroBytes / 16)
+    o.zero[threadIdx.x] = (u32x4){0u, 0u, 0u, 0u};
+  if (!mm_find<Cfg>(p, &t)) return;
+  auto go = [&](auto full) {
+    LinRows<T, Cfg, kAct, kPart, decltype(full)::value> rows{t, o, t.nt * Cfg::BN};
+    mm_begin<Cfg, false>(t.rows, rows);
+    mm_drain<Cfg, false>(smem, acc, t.rows, rows);
+  };
+  mm_tile<typename OpOf<T>::type, Cfg, false, kTurned>(p, smem, t, acc);
+  if ((t.nt + 1) * Cfg::BN <= p.N) go(std::true_type{});
+  else go(std::false_type{});
+}
+
+// One output from its sum, a column a lane; `in`: the lane has one.
+template <typename T, int kAct>
+__device__ __forceinline__ void finish(const LinOut<T>& o, int64_t row, int n, bool in, float sum) {
+  float slope = 0.0f;
+  if (in) {
+    float y = lin_act<T, kAct>(sum + (o.bias ? o.bias[n] : 0.0f), &slope);
+    if (o.res) y += elem(static_cast<const T*>(o.res) + row * o.N + n);
+    put(static_cast<T*>(o.y) + row * o.ld + n, y);
+  }
+  if (kAct != MOE_ACT_NONE && o.slope.p) o.slope.put1(row, n, in, slope);
+}
+
+// Outputs from the sums of the slices of K, added in order; blockIdx.y: the row.
+template <typename T, int kAct>
+__global__ __launch_bounds__(256) void lin_join_kernel(const float* __restrict__ part, int parts,
+                                                       const LinOut<T> o) {
+  const int n = blockIdx.x * 256 + threadIdx.x;
+  const int64_t row = blockIdx.y;
+  const bool in = n < o.N;
+  float v = 0.0f;
+  if (in) {
+#pragma unroll 8
+    for (int p = 0; p < parts; ++p) v += part[(p * o.M + row) * o.N + n];
+  }
+  finish<T, kAct>(o, row, n, in, v);
+}
+
+// Few tokens. part: null (one slice of K), or the slices' sums [k_parts][rows][N].
+template <typename T, int kAct>
+__global__ __launch_bounds__(512) void lin_rows_kernel(const SkinnyArgs<T, 1> a, const LinOut<T> o, float* part) {
+  __shared__ float lds[kSkinnyWaves][kSkinnyLds];
+  float sum[2][1];
+  skinny_sums<T, 1, false>(a, lds, sum);
+#pragma unroll
+  for (int v = 0; v < 2; ++v) {
+    const int64_t row = static_cast<int64_t>(blockIdx.y) * 16 + (threadIdx.x >> 6) + 8 * v;
+    const int n = blockIdx.x * kSkinnyCols + (threadIdx.x & 63);
+    const bool in = row < a.rows && n < a.N;
+    if (!part) finish<T, kAct>(o, row, n, in, sum[v][0]);
+    else if (in) part[(blockIdx.z * a.rows + row) * a.N + n] = sum[v][0];
+  }
+}
+
+// da [rows][np] from dy [rows][n] and the slopes (p null: ones), zeros from
+// column n on, and the sums of its columns, before they are rounded, over the
+// rows of this workgroup's slice: part [gridDim.y][n4]. da and part may each be
+// null. A workgroup takes 256 columns, 32 threads of eight side by side.
+constexpr int kDaCols = 256, kDaRows = 8;
+template <typename T>
+__global__ __launch_bounds__(256) void lin_da_kernel(const T* __restrict__ dy, const Slopes<T> slope,
+                                                     T* __restrict__ da,
+                                                     float* __restrict__ part, int64_t rows, int n, int np,
+                                                     int n4) {
+  __shared__ float sums[kDaRows][kDaCols];
+  const int tx = threadIdx.x % 32, ty = threadIdx.x / 32;
+  const int c = blockIdx.x * kDaCols + tx * 8;
+  const int64_t r0 = rows * blockIdx.y / gridDim.y, r1 = rows * (blockIdx.y + 1) / gridDim.y;
+  float s[8];
+#pragma unroll
+  for (int q = 0; q < 8; ++q) s[q] = 0.0f;
+  auto walk = [&](auto full) {
+    constexpr bool kFull = decltype(full)::value;
+#pragma unroll 4
+    for (int64_t r = r0 + ty; r < r1; r += kDaRows) {
+      float v[8], e[8];
+      load8<T, kFull>(dy + r * n, c, n, v);
+      if (slope.p && (kFull || c < n)) {
+        slope.get8(r, c, e);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[q] = (kFull || c + q < n) ? v[q] * e[q] : 0.0f;
+      }
+      if (da) store8<T, true>(da + r * np, c, np, v);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) s[q] += v[q];
+    }
+  };
+  if (c + 8 <= n) walk(std::true_type{});
+  else if (c < np) walk(std::false_type{});
+  if (!part) return;
+#pragma unroll
+  for (int q = 0; q < 8; ++q) sums[ty][tx * 8 + q] = s[q];
+  __syncthreads();
+  const int col = blockIdx.x * kDaCols + threadIdx.x;
+  float v = 0.0f;
+#pragma unroll
+  for (int r = 0; r < kDaRows; ++r) v += sums[r][threadIdx.x];
+  if (col < n4) part[static_cast<int64_t>(blockIdx.y) * n4 + col] = v;
+}
+
+// ------------------------------------------------------------------ layouts
+
+// Whether the forward's tiles read the weights where they are (mm_tile,
+// kTurned): as in the gated block, bf16, widths that fill stages and pieces,
+// and not so many tokens that turning the weights once is less.
+constexpr int64_t kInPlace = int64_t{1} << 23;  // elements of x
+bool in_place(const moe_linear& l) {
+  return l.dtype == MOE_BF16 && l.inputs % 64 == 0 && l.outputs % 8 == 0 && l.tokens * l.inputs <= kInPlace;
+}
+
+// Slices of the rows in which dbias is added up.
+int bias_slices(const moe_linear& l) {
+  const int64_t across = (l.outputs + kDaCols - 1) / kDaCols;
+  int64_t k = (4 * kCUs + across - 1) / across;
+  const int64_t most = (l.tokens + 4 * kDaRows - 1) / (4 * kDaRows);
+  if (k > most) k = most;
+  return static_cast<int>(k < 1 ? 1 : (k > 64 ? 64 : k));
+}
+
+struct LinLayout {
+  size_t wt, xp, sums;                 // forward: turned weights, padded x, sums of slices
+  size_t dx_sums, da, wp, part, bias, xt, dat, zero;  // backward
+  size_t total;
+  int k_parts, dx_parts, grad_parts, bias_parts;
+};
+int64_t pad4(int64_t v) { return (v + 3) / 4 * 4; }
+
+// Slices of K of a product in tiles.
+int tile_parts(size_t es, int64_t M, int64_t N, int64_t kp) { return parts_of(es, M, N, kp * es / 128); }
+
+LinLayout lin_layout(const moe_linear& l, bool training) {
+  LinLayout L{};
+  const size_t es = elem_bytes(l), T = l.tokens, K = l.inputs, N = l.outputs;
+  const size_t kp = pad128(K), np = pad128(N);
+  size_t o = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = o;
+    o = align_up(o + bytes, 256);
+    return at;
+  };
+  auto sums = [&](int parts, size_t cells) { return take(parts > 1 ? parts * cells * sizeof(float) : 0); };
+  if (few_rows(l)) {
+    // slices of K so that every CU has a workgroup, of two steps a wave at least
+    const int64_t blocks = T == 0 ? 1 : (N + kSkinnyCols - 1) / kSkinnyCols * ((T + 15) / 16);
+    const int64_t most = (K + 2 * kSkinnyStep * kSkinnyWaves - 1) / (2 * kSkinnyStep * kSkinnyWaves);
+    const int64_t want = (kCUs + blocks - 1) / blocks;
+    L.k_parts = static_cast<int>(want < most ? want : most);
+  } else {
+    if (!in_place(l)) {
+      L.wt = take(N * kp * es);
+      L.xp = take(K == kp ? 0 : T * kp * es);
+    }
+    L.k_parts = tile_parts(es, T, N, in_place(l) ? K : kp);
+  }
+  L.sums = sums(L.k_parts, T * N);
+  L.total = o;
+  if (!training) return L;
+  // the backward has the place for itself
+  o = 0;
+  L.zero = take(kTrZeroBytes);
+  L.da = take(l.act == MOE_ACT_NONE && N == np ? 0 : T * np * es);
+  L.wp = take(N == np ? 0 : K * np * es);
+  L.bias_parts = bias_slices(l);
+  L.bias = take(L.bias_parts * pad4(N) * sizeof(float));
+  L.dx_parts = tile_parts(es, T, K, np);
+  if (es == 2) {
+    L.xp = take(K == kp ? 0 : T * kp * es);
+    L.grad_parts = slices(l.tokens, static_cast<int64_t>(kp / 128) * (np / 128));
+  } else {
+    const size_t tp = pad128(T);
+    L.xt = take(K * tp * es);
+    L.dat = take(N * tp * es);
+    L.grad_parts = tile_parts(es, K, N, tp);
+  }
+  // one place for the sums of either product
+  L.dx_sums = L.part = o;
+  sums(L.dx_parts, T * K);
+  L.total = std::max(L.total, o);
+  o = L.part;
+  sums(L.grad_parts, es == 2 ? kp * np : K * pad4(N));
+  L.total = std::max(L.total, o);
+  return L;
+}
+
+// ----------------------------------------------------------------- launches
+
+template <typename T, typename Cfg, int kAct, bool kPart, bool kTurned>
+void lin_tiles_at(const char* name, const MmArgs& a, const LinOut<T>& o, hipStream_t s) {
+  MmArgs p = a;
+  p.tiles_n = (p.N + Cfg::BN - 1) / Cfg::BN;
+  p.nk *= 128 / Cfg::ROW;
+  const int64_t grid = (p.M + Cfg::BM - 1) / Cfg::BM * p.tiles_n * (p.parts > 1 ? p.parts : 1);
+  MOE_LAUNCH(name, (lin_tile_kernel<T, Cfg, kAct, kPart, kTurned>), dim3(static_cast<unsigned>(grid)),
+             dim3(Cfg::NT), 0, s, p, o);
+}
+
+template <typename T, int kAct>
+void lin_tiles(const char* name, const MmArgs& p, const LinOut<T>& o, hipStream_t s, bool turned) {
+  const TileSize size = tile_of(sizeof(T), p.M, p.N, p.nk);
+  if constexpr (sizeof(T) == 2) {
+    if (turned) {
+      if (size == kSmall) return lin_tiles_at<T, MmSmall, kAct, false, true>(name, p, o, s);
+      return lin_tiles_at<T, MmMid, kAct, false, true>(name, p, o, s);
+    }
+    if (size == kBig) return lin_tiles_at<T, MmBig, kAct, false, false>(name, p, o, s);
+    if (size == kTall) return lin_tiles_at<T, MmTall, kAct, false, false>(name, p, o, s);
+  }
+  if (size == kSmall) return lin_tiles_at<T, MmSmall, kAct, false, false>(name, p, o, s);
+  lin_tiles_at<T, MmMid, kAct, false, false>(name, p, o, s);
+}
+
+// f(the activation as a constant).
+template <typename F>
+void with_act(int act, F&& f) {
+  switch (act) {
+    case MOE_ACT_SILU: return f(std::integral_constant<int, MOE_ACT_SILU>{});
+    case MOE_ACT_GELU: return f(std::integral_constant<int, MOE_ACT_GELU>{});
+    case MOE_ACT_GELU_TANH: return f(std::integral_constant<int, MOE_ACT_GELU_TANH>{});
+    case MOE_ACT_RELU: return f(std::integral_constant<int, MOE_ACT_RELU>{});
+    default: return f(std::integral_constant<int, MOE_ACT_NONE>{});
+  }
+}
+
+template <typename T>
+void lin_join(const char* name, int act, const float* part, int parts, const LinOut<T>& o, hipStream_t s) {
+  with_act(act, [&](auto a) {
+    MOE_LAUNCH(name, (lin_join_kernel<T, decltype(a)::value>),
+               dim3((o.N + 255) / 256, static_cast<unsigned>(o.M)), dim3(256), 0, s, part, parts, o);
+  });
+}
+
+// The slopes in `saved`; none without an activation.
+template <typename T>
+Slopes<T> slopes_at(const moe_linear& l, void* saved) {
+  Slopes<T> s{};
+  if (l.act == MOE_ACT_NONE || !saved) return s;
+  s.p = static_cast<decltype(s.p)>(saved);
+  s.ld = slope_pitch(l);
+  if constexpr (sizeof(T) == 2) s.low = reinterpret_cast<uint8_t*>(s.p + l.tokens * s.ld);
+  return s;
+}
+
+// A product in tiles with its epilogue, over slices of K (sums in `part`)
+// where it has few tiles.
+template <typename T>
+void lin_product(const char* name, int act, const MmArgs& a, const LinOut<T>& o, int parts, float* part,
+                 hipStream_t s, bool turned = false) {
+  MmArgs p = a;
+  p.parts = parts;
+  if (parts == 1)
+    return with_act(act, [&](auto k) { lin_tiles<T, decltype(k)::value>(name, p, o, s, turned); });
+  LinOut<T> sums{};
+  sums.y = part;
+  sums.ld = p.N;
+  sums.M = p.M;
+  sums.N = p.N;
+  sums.zero = o.zero;
+  if constexpr (sizeof(T) == 2) {
+    if (turned) lin_tiles_at<T, MmSmall, MOE_ACT_NONE, true, true>(name, p, sums, s);
+  }
+  if (!turned) lin_tiles_at<T, MmSmall, MOE_ACT_NONE, true, false>(name, p, sums, s);
+  lin_join<T>("linear_join", act, part, parts, o, s);
+}
+
+template <typename T>
+hipError_t lin_fwd_t(const moe_linear& l, const void* x, const void* w, const float* bias, const void* res,
+                     void* saved, void* y, void* ws, hipStream_t s) {
+  const LinLayout L = lin_layout(l, false);
+  char* W = static_cast<char*>(ws);
+  const int K = l.inputs, N = l.outputs;
+  const int64_t kp = pad128(K);
+  float* part = reinterpret_cast<float*>(W + L.sums);
+  const LinOut<T> o{y, N, bias, res, slopes_at<T>(l, saved), l.tokens, N, nullptr};
+  if (few_rows(l)) {
+    SkinnyArgs<T, 1> a{static_cast<const T*>(x), nullptr, K, {static_cast<const T*>(w)}, l.tokens, K, N, L.k_parts};
+    const dim3 grid((N + kSkinnyCols - 1) / kSkinnyCols, static_cast<unsigned>((l.tokens + 15) / 16), L.k_parts);
+    if (L.k_parts > 1) {
+      MOE_LAUNCH("linear_rows", (lin_rows_kernel<T, MOE_ACT_NONE>), grid, dim3(512), 0, s, a, o, part);
+      lin_join<T>("linear_join", l.act, part, L.k_parts, o, s);
+    } else {
+      with_act(l.act, [&](auto k) {
+        MOE_LAUNCH("linear_rows", (lin_rows_kernel<T, decltype(k)::value>), grid, dim3(512), 0, s, a, o, nullptr);
+      });
+    }
+    return hipGetLastError();
+  }
+  if (in_place(l)) {
+    lin_product<T>("linear", l.act, rows_of<T>(x, K, w, N, l.tokens, N, K), o, L.k_parts, part, s, true);
+    return hipGetLastError();
+  }
+  TurnJobs jobs{};
+  jobs.add(w, W + L.wt, K, N, N);
+  turn<T>("linear_turn", jobs, s);
+  PadJobs pads{};
+  const void* xp = padded<T>(pads, x, W + L.xp, l.tokens, K);
+  pad<T>("linear_pad", pads, s);
+  lin_product<T>("linear", l.act, rows_of<T>(xp, kp, W + L.wt, kp, l.tokens, N, kp), o, L.k_parts, part, s);
+  return hipGetLastError();
+}
+
+template <typename T, typename G>
+hipError_t lin_bwd_t(const moe_linear& l, const void* x, const void* w, const void* saved, const void* dy,
+                     void* dx, void* dw, float* dbias, void* ws, hipStream_t s) {
+  const LinLayout L = lin_layout(l, true);
+  char* W = static_cast<char*>(ws);
+  const int K = l.inputs, N = l.outputs;
+  const int64_t kp = pad128(K), np = pad128(N), tok = l.tokens;
+  SliceJobs jobs{};
+  int64_t end = 0;
+  auto job = [&](const float* part, int splits, int64_t stride, int64_t ld, int M, int cols, void* out, bool wide) {
+    end += static_cast<int64_t>(M) * ((cols + 3) / 4);
+    jobs.job[jobs.n++] = SliceJob{part, splits, stride, ld, M, cols, out, end, wide};
+  };
+
+  const bool made = l.act != MOE_ACT_NONE || N != np;
+  const void* da = made ? W + L.da : dy;
+  if (made || dbias) {
+    float* part = dbias ? reinterpret_cast<float*>(W + L.bias) : nullptr;
+    MOE_LAUNCH("linear_bwd_da", lin_da_kernel<T>, dim3(static_cast<unsigned>((np + kDaCols - 1) / kDaCols), L.bias_parts),
+               dim3(256), 0, s, static_cast<const T*>(dy),
+               slopes_at<T>(l, const_cast<void*>(saved)), made ? static_cast<T*>(static_cast<void*>(W + L.da)) : nullptr, part, tok, N,
+               static_cast<int>(np), static_cast<int>(pad4(N)));
+    if (dbias) job(part, L.bias_parts, pad4(N), pad4(N), 1, N, dbias, true);
+  }
+  PadJobs pads{};
+  const void* wp = padded<T>(pads, w, W + L.wp, K, N);
+  [[maybe_unused]] const void* xp = x;
+  if constexpr (std::is_same<T, bf16_t>::value) xp = padded<T>(pads, x, W + L.xp, tok, K);
+  pad<T>("linear_pad", pads, s);
+  // the weight gradient reads a row of zeros past the last token
+  u32x4* zero = reinterpret_cast<u32x4*>(W + L.zero);
+  const LinOut<T> o{dx, K, nullptr, nullptr, Slopes<T>{}, tok, K, zero};
+  lin_product<T>("linear_bwd_dx", MOE_ACT_NONE, rows_of<T>(da, np, wp, np, tok, K, np), o, L.dx_parts,
+                 reinterpret_cast<float*>(W + L.dx_sums), s);
+
+  float* part = reinterpret_cast<float*>(W + L.part);
+  if constexpr (std::is_same<T, bf16_t>::value) {
+    if (L.grad_parts == 1) {
+      grad_direct<G>("linear_bwd_dw", xp, kp, da, np, kp, np, tok, K, N, np, dw, dw, zero, s);
+    } else {
+      grad_slices<T>("linear_bwd_dw", xp, kp, da, np, kp, np, tok, L.grad_parts, part, zero, s);
+      job(part, L.grad_parts, kp * np, np, K, N, dw, false);
+    }
+  } else {
+    // rows of consecutive tokens, as the gated block's weight gradients take them
+    TurnJobs turns{};
+    turns.add(x, W + L.xt, tok, K, K);
+    turns.add(da, W + L.dat, tok, static_cast<int>(N), made ? np : N);
+    turn<T>("linear_bwd_turn", turns, s);
+    const int64_t tp = pad128(tok);
+    MmArgs p = rows_of<T>(W + L.xt, tp, W + L.dat, tp, K, N, tp);
+    LinOut<T> g{};
+    g.M = K;
+    g.N = N;
+    if (L.grad_parts == 1) {
+      g.y = dw;
+      g.ld = N;
+      lin_tiles<T, MOE_ACT_NONE>("linear_bwd_dw", p, g, s, false);
+    } else {
+      g.y = part;
+      g.ld = pad4(N);
+      p.parts = L.grad_parts;
+      lin_tiles_at<T, MmSmall, MOE_ACT_NONE, true, false>("linear_bwd_dw", p, g, s);
+      job(part, L.grad_parts, static_cast<int64_t>(K) * pad4(N), pad4(N), K, N, dw, false);
+    }
+  }
+  if (jobs.n)
+    MOE_LAUNCH("linear_slice_sum", slice_sum_kernel<G>, dim3(blocks_for(end)), dim3(256), 0, s, jobs);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+size_t linear_ws_bytes(const moe_linear& l, bool training) {
+  // a training workspace serves inference too
+  size_t n = lin_layout(l, false).total;
+  if (training) n = std::max(n, lin_layout(l, true).total);
+  return align_up(n < 256 ? 256 : n, 256);
+}
+size_t linear_saved_bytes(const moe_linear& l) {
+  if (l.act == MOE_ACT_NONE) return 0;
+  return align_up(l.tokens * slope_pitch(l) * (l.dtype == MOE_BF16 ? 5 : 8) / 2, 256);
+}
+
+hipError_t launch_linear(const moe_linear& l, const void* x, const void* w, const float* bias, const void* res,
+                         void* saved, void* y, void* ws, hipStream_t s) {
+  return l.dtype == MOE_BF16 ? lin_fwd_t<bf16_t>(l, x, w, bias, res, saved, y, ws, s)
+                             : lin_fwd_t<float>(l, x, w, bias, res, saved, y, ws, s);
+}
+
+hipError_t launch_linear_bwd(const moe_linear& l, const void* x, const void* w, const void* saved,
+                             const void* dy, void* dx, void* dw, float* dbias, void* ws, hipStream_t s) {
+  if (l.tokens == 0) {
+    const int64_t n = static_cast<int64_t>(l.inputs) * l.outputs;
+    if (l.grad_dtype == MOE_BF16)
+      MOE_LAUNCH("linear_zero", zero_kernel<bf16_t>, dim3(blocks_for(n)), dim3(256), 0, s,
+                 static_cast<bf16_t*>(dw), n);
+    else
+      MOE_LAUNCH("linear_zero", zero_kernel<float>, dim3(blocks_for(n)), dim3(256), 0, s, static_cast<float*>(dw), n);
+    if (dbias)
+      MOE_LAUNCH("linear_zero", zero_kernel<float>, dim3(blocks_for(l.outputs)), dim3(256), 0, s, dbias,
+                 int64_t{l.outputs});
+    return hipGetLastError();
+  }
+  if (l.dtype != MOE_BF16) return lin_bwd_t<float, float>(l, x, w, saved, dy, dx, dw, dbias, ws, s);
+  return l.grad_dtype == MOE_BF16 ? lin_bwd_t<bf16_t, bf16_t>(l, x, w, saved, dy, dx, dw, dbias, ws, s)
+                                  : lin_bwd_t<bf16_t, float>(l, x, w, saved, dy, dx, dw, dbias, ws, s);
+}
+
+}  // namespace moe

@@ -1,8 +1,10 @@
 /*
  * moe_block.h - C ABI of libmoe's operators around the MoE layer (moe.h):
  * the layer norm in front of it, the dense gated feed-forward block that
- * stands in for it in a model's dense layers, and matrix products with
- * weights held in 8-bit integers, dense or grouped by the layer's routing.
+ * stands in for it in a model's dense layers, matrix products with weights
+ * held in 8-bit integers, dense or grouped by the layer's routing, dense
+ * products with bias, activation and residual, the norms, gate and residual
+ * between two blocks, and the balance loss of the layer's router.
  *
  * Conventions as in moe.h: device pointers unless stated otherwise, memory
  * and workspaces owned by the caller, nothing allocated or retained, work
@@ -77,7 +79,8 @@ typedef enum {
   MOE_ACT_SILU = 0,      /* a / (1 + exp(-a)) */
   MOE_ACT_GELU = 1,      /* a Phi(a), Phi the normal distribution function */
   MOE_ACT_GELU_TANH = 2, /* a (1 + tanh(sqrt(2/pi) (a + 0.044715 a^3))) / 2 */
-  MOE_ACT_RELU = 3       /* max(a, 0); slope 0 at 0 */
+  MOE_ACT_RELU = 3,      /* max(a, 0); slope 0 at 0 */
+  MOE_ACT_NONE = 4       /* a; moe_linear only */
 } moe_act;
 
 /*
@@ -213,6 +216,203 @@ size_t moe_linear_i8_workspace_bytes(const moe_i8_linear* l);
 int moe_linear_i8(const moe_i8_linear* l, const void* x, const float* x_scale, const int8_t* wq,
                   const float* w_scale, const float* bias, const moe_routing* r, void* y,
                   void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------- product with bias, activation and residual */
+
+/*
+ *   y = act(x W + bias) + residual
+ * x [tokens, inputs], W [inputs, outputs], residual and y [tokens, outputs] in
+ * dtype, bias fp32 [outputs]; sums are fp32 and y is rounded once. In the
+ * backward pass da is rounded to dtype for its two products, and in bf16 the
+ * slopes act'(a) are kept in 20 bits (2^-20).
+ *
+ * Supported (else MOE_ERR_UNSUPPORTED): inputs and outputs up to 65536 (any
+ * value), tokens < 2^31, tokens * max(inputs, outputs) < 2^36.
+ */
+typedef struct {
+  int64_t tokens;
+  int32_t inputs;
+  int32_t outputs;
+  int32_t dtype;      /* moe_dtype */
+  int32_t act;        /* moe_act */
+  int32_t grad_dtype; /* moe_dtype of the weights' gradient: MOE_FP32, or dtype
+                         (rounded once from fp32 sums) */
+} moe_linear;
+
+/* Workspace bytes (host) of moe_linear_fwd (training = 0), or of it and
+ * moe_linear_bwd (training = 1); 0 for an invalid problem. */
+size_t moe_linear_workspace_bytes(const moe_linear* l, int training);
+
+/* Bytes (host) of the buffer that moe_linear_fwd fills for moe_linear_bwd: the
+ * slopes act'(a). 0 with MOE_ACT_NONE, which keeps nothing, and for an
+ * invalid problem. */
+size_t moe_linear_saved_bytes(const moe_linear* l);
+
+/* Forward. bias and residual may be NULL. saved: NULL for inference (or with
+ * MOE_ACT_NONE, where it is not touched), else moe_linear_saved_bytes(l) bytes
+ * (256-byte aligned). tokens == 0 is a successful no-op. */
+int moe_linear_fwd(const moe_linear* l, const void* x, const void* w, const float* bias,
+                   const void* residual, void* saved, void* y, void* workspace,
+                   size_t workspace_bytes, void* stream);
+
+/*
+ * Backward of L = sum(y * grad_out), with a = x W + bias and
+ * da = grad_out act'(a):
+ *   grad_x = da W^T, grad_w = x^T da, grad_bias = sum_t da (fp32; NULL: not
+ *   wanted); the residual's gradient is grad_out itself.
+ * Everything is fully overwritten; with tokens == 0 the gradients of the
+ * parameters are zeroed. saved is read only, and not at all with MOE_ACT_NONE.
+ */
+int moe_linear_bwd(const moe_linear* l, const void* x, const void* w, const void* saved,
+                   const void* grad_out, void* grad_x, void* grad_w, float* grad_bias,
+                   void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------- between two blocks */
+
+typedef enum {
+  MOE_NORM_LAYER = 0, /* (x - mean) / sqrt(var + eps), as moe_layer_norm */
+  MOE_NORM_RMS = 1    /* x / sqrt(mean_j(x^2) + eps) */
+} moe_norm_kind;
+
+/*
+ * What lies between two blocks of a residual stream: the norm after the block
+ * whose output is z, a gate, the residual, and the norm before the next block:
+ *   u = norm(z) post_weight + post_bias   (post = 0: u = z)
+ *   out = scale res + gate u
+ *   y = norm(out) pre_weight + pre_bias   (pre = 0: not computed)
+ * Everything between z, res and out, y is fp32 and rounded once; y is made of
+ * the out that is not rounded. dtype is the storage type of the matrices,
+ * parameters and their gradients are fp32 in both modes.
+ *
+ * Rows may lie apart: ld_* is the number of elements between rows (0: width),
+ * and the matrices need only the alignment of their elements. out and y may be
+ * z or res, and grad_z and grad_res may be z, res, grad_out or grad_y, each
+ * another one and with equal strides.
+ *
+ * Supported (else MOE_ERR_UNSUPPORTED): width <= 16384, rows < 2^31.
+ */
+typedef struct {
+  int64_t rows;
+  int32_t width;
+  int32_t dtype; /* moe_dtype */
+  int32_t kind;  /* moe_norm_kind, of both norms */
+  int32_t post;  /* 1: the norm after the block is there */
+  int32_t pre;   /* 1: the norm before the next block is there */
+  float eps;     /* finite, >= 0 */
+  float scale;   /* of the residual; finite */
+  int64_t ld_z, ld_res, ld_out, ld_y, ld_grad_out, ld_grad_y, ld_grad_z, ld_grad_res;
+} moe_residual_norm;
+
+/* Parameters [width] (device, fp32, read only); each may be NULL (weights and
+ * gate: ones, biases: zeros). */
+typedef struct {
+  const float* post_weight;
+  const float* post_bias;
+  const float* gate;
+  const float* pre_weight;
+  const float* pre_bias;
+} moe_norm_params;
+
+/* Their gradients [width] (device, fp32, fully overwritten); each may be NULL
+ * (not wanted). */
+typedef struct {
+  float* post_weight;
+  float* post_bias;
+  float* gate;
+  float* pre_weight;
+  float* pre_bias;
+} moe_norm_grads;
+
+/*
+ * Forward. y is NULL exactly where pre is 0. stats: NULL, or [4, rows] fp32
+ * (mean and 1 / deviation of z, then of out) for moe_residual_norm_bwd.
+ * rows == 0 is a successful no-op.
+ */
+int moe_residual_norm_fwd(const moe_residual_norm* n, const void* z, const void* res,
+                          const moe_norm_params* params, void* out, void* y, float* stats,
+                          void* stream);
+
+/* Workspace bytes (host) of moe_residual_norm_bwd; 0 for an invalid problem. */
+size_t moe_residual_norm_workspace_bytes(const moe_residual_norm* n);
+
+/*
+ * Backward of L = sum(out * grad_out) + sum(y * grad_y); grad_out may be NULL
+ * (no such term), grad_y is NULL exactly where pre is 0. z and res are the
+ * forward's, unchanged. The sums over rows run in one fixed order. Gradients of
+ * a norm that is not there are zeros. With rows == 0 the parameters' gradients
+ * are zeroed. eps is not read.
+ */
+int moe_residual_norm_bwd(const moe_residual_norm* n, const void* z, const void* res,
+                          const moe_norm_params* params, const float* stats, const void* grad_out,
+                          const void* grad_y, void* grad_z, void* grad_res,
+                          const moe_norm_grads* grads, void* workspace, size_t workspace_bytes,
+                          void* stream);
+
+/* ------------------------------------------------- balance of the router */
+
+/*
+ * Load-balance loss and z loss of the layer's router over a batch, with the
+ * loads of the experts. With l = x w_router (fp32 as the layer's router, but
+ * not in its order of additions), p = softmax(l) over all experts, n the
+ * number of tokens that the mask keeps and sums over those tokens:
+ *   counts[e]    = number of their token-slots that topk_idx gives to expert e
+ *   mean_prob[e] = sum_t p[t,e] / n
+ *   loss[1] = experts sum_e counts[e] / (n top_k) mean_prob[e]
+ *   loss[2] = sum_t logsumexp_e(l[t])^2 / n
+ *   loss[0] = balance loss[1] + z loss[2]
+ * With n == 0 all of them are zeros. Tokens that the mask leaves out may hold
+ * anything, NaN included. x, grad_x and saved are aligned as usual, the other
+ * arrays need only the alignment of their elements.
+ *
+ * Supported (else MOE_ERR_UNSUPPORTED): what moe_problem supports of tokens,
+ * experts (<= 64), top_k and d_model (a multiple of 128, at most 8192).
+ */
+typedef struct {
+  int64_t tokens;
+  int32_t experts;
+  int32_t top_k;
+  int32_t d_model;
+  int32_t dtype;  /* moe_dtype of x and grad_x */
+  float balance;  /* coefficients of the two losses; finite */
+  float z;
+} moe_balance;
+
+/* Workspace bytes (host) of moe_balance_loss and moe_balance_loss_bwd; 0 for an
+ * invalid problem. */
+size_t moe_balance_workspace_bytes(const moe_balance* b);
+
+/* Bytes (host) of the buffer that moe_balance_loss fills for
+ * moe_balance_loss_bwd: the gradient of loss[0] by the logits, in fp32 or, in
+ * bf16, as sums of two bf16 numbers (2^-17). 0 for an invalid problem. */
+size_t moe_balance_saved_bytes(const moe_balance* b);
+
+/*
+ * Forward. topk_idx [tokens, top_k] as moe_route leaves it (entries that are
+ * no expert are not counted); mask: NULL (all tokens) or a byte a token, 0:
+ * left out. counts [experts] int32, mean_prob [experts] and loss [3] fp32 are
+ * fully overwritten. saved: NULL, or moe_balance_saved_bytes(b) bytes
+ * (256-byte aligned).
+ */
+int moe_balance_loss(const moe_balance* b, const void* x, const float* w_router,
+                     const int32_t* topk_idx, const uint8_t* mask, int32_t* counts,
+                     float* mean_prob, float* loss, void* saved, void* workspace,
+                     size_t workspace_bytes, void* stream);
+
+/*
+ * Backward of grad_loss[0] loss[0] with the counts held fixed (grad_loss: one
+ * fp32 number on the device, or NULL: 1), for the x, w_router and mask of the
+ * forward call that filled saved:
+ *   dl[t,e] = p[t,e] (balance experts (f_e - sum_j f_j p[t,j]) + 2 z logsumexp_t) / n,
+ *   f = counts / (n top_k), 0 for tokens that the mask leaves out
+ *   grad_x = dl w_router^T, grad_router = x^T dl
+ * add = 0: both are fully overwritten (with tokens == 0 grad_router is
+ * zeroed); add = 1: both are added to what is there, the layer's own
+ * gradients for instance (moe_bwd), rounded once.
+ */
+int moe_balance_loss_bwd(const moe_balance* b, const void* x, const float* w_router,
+                         const uint8_t* mask, const void* saved, const float* grad_loss, int add,
+                         void* grad_x, float* grad_router, void* workspace,
+                         size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,666 @@
+"""The product with bias, activation and residual, the step between two blocks
+and the balance loss on the GPU against plain 64-bit computations, and a run of
+them together with the layer.
+
+Tolerances, as the 2-norm of the difference over the 2-norm of the result
+unless a test says otherwise; u as in test_gpu_block.py is half a rounding step
+of the storage type (bf16 2^-8, fp32 2^-24).
+
+* linear: y is rounded once (1 u). da is rounded for its products (1 u), dx and a
+  gradient in dtype once more (1 u). fp32 sums of n products add about sqrt(n)
+  2^-24 in the 2-norm: 1e-5 covers n = 2^14. dbias has the slopes' 2^-20 and its
+  own sums and is held to the size of its terms.
+* residual step: out, y, dz and dres are rounded once from fp32 (u + the sums of
+  a row, 64 additions a thread at most, in each of two norms), parameters'
+  gradients are sums over rows, held to their terms.
+* balance loss: fp32 throughout; logits of d products are off by about sqrt(d)
+  2^-24 of |x| |w|, an exponential by 2^-21, so p by 2^-20 of itself; dx in bf16
+  is rounded once and made of halves that leave 2^-16.
+"""
+
+import math
+
+import pytest
+
+from dropless_grouped_gemm_router_amd import binding as B
+from dropless_grouped_gemm_router_amd import block as K
+from dropless_grouped_gemm_router_amd.inputs import Problem
+
+from gpu_util import Case, note
+from test_gpu_block import U, act64, gen, near, off, types
+
+pytestmark = pytest.mark.gpu
+
+
+def within(name, got, want, bound):
+    """The difference's 2-norm against a bound in absolute numbers."""
+    import torch
+    assert got.shape == want.shape, name
+    assert bool(torch.isfinite(got.float()).all()), name
+    e = float((got.double() - want.double()).norm())
+    assert e <= bound, f"{name}: {e:.3g} > {bound:.3g}"
+
+
+# -------------------------------------------------------------------- linear
+
+def linear_case(t, k, n, dtype, act="none", grad="fp32", bias=True, res=True, training=True, seed=0):
+    r = gen(t + 3 * k + 7 * n + seed)
+    l = K.Linear(t, k, n, dtype, act, grad)
+    x, w = r(t, k, dtype=dtype), r(k, n, std=k ** -0.5, dtype=dtype)
+    b = r(n, std=0.5) if bias else None
+    add = r(t, n, dtype=dtype) if res else None
+    return l, x, w, b, add, r(t, n, dtype=dtype), K.allocate_linear(l, "cuda", training=training)
+
+
+def linear64(x, w, b, add, dy, act):
+    import torch
+    x, w = x.double().requires_grad_(), w.double().requires_grad_()
+    b = torch.zeros(w.shape[1], device="cuda", dtype=torch.float64) if b is None else b.double()
+    b.requires_grad_()
+    a = x @ w + b
+    f = a if act == "none" else act64(a, act)
+    slope = torch.autograd.grad(f, a, torch.ones_like(f), retain_graph=True)[0]
+    y = f if add is None else f + add.double()
+    return (y.detach(), *torch.autograd.grad(y, (x, w, b), dy.double()), (dy.double() * slope).abs())
+
+
+def check_linear(t, k, n, dtype, act, grad, bias, res):
+    import torch
+    note(f"linear {t} {k} {n} {dtype} {act} {grad} bias {bias} res {res}")
+    l, x, w, b, add, dy, buf = linear_case(t, k, n, dtype, act, grad, bias, res)
+    for m in (buf.y, buf.grad_x, buf.grad_w, buf.grad_bias):
+        m.fill_(float("nan"))
+    buf.workspace.fill_(255)
+    K.linear(l, x, w, buf, bias=b, residual=add, training=True)
+    again = buf.y.clone()
+    buf.workspace.fill_(255)
+    gx, gw, gb = K.linear_backward(l, x, w, dy, buf, bias=bias)
+    y, dx, dw, db, da = linear64(x, w, b, add, dy, act)
+    u = U[dtype]
+    near("y", buf.y, y, u + 1e-5)
+    # dx sums n products, whose terms may cancel when there are few of them
+    within("dx", gx, dx, (u + 1e-5) * float(dx.norm()) + (u + 1e-5) * float(
+        (da.square() @ w.double().square().t()).sum().sqrt()))
+    within("dw", gw, dw, (U[grad] + 1e-5) * float(dw.norm()) + (u + 1e-5) * float(
+        (x.double().square().t() @ da.square()).sum().sqrt()))
+    if bias:
+        # every slope off by 2^-20 (bf16), 64 sequential additions a thread and slice
+        within("dbias", gb, db, float(((2.0 ** -20 if dtype == "bf16" else 2.0 ** -22) * dy.double().abs()
+                                       + 128 * 2.0 ** -24 * da).sum(0).norm()))
+    else:
+        assert gb is None
+    inference = K.allocate_linear(l, "cuda")
+    K.linear(l, x, w, inference, bias=b, residual=add)
+    assert torch.equal(inference.y, again)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("t,k,n", [
+    (1, 1, 1), (1, 512, 512), (2, 100, 33), (3, 4096, 64), (16, 65, 129), (17, 64, 8), (17, 65, 7), (33, 128, 200),
+    (100, 192, 136), (128, 1001, 500), (129, 64, 64), (300, 1024, 1000), (513, 500, 1001), (700, 130, 2050)])
+def test_linear(t, k, n, dtype):
+    check_linear(t, k, n, dtype, "silu", "fp32", True, True)
+    check_linear(t, k, n, dtype, "none", dtype, (t + n) % 2 == 0, (t + k) % 2 == 0)
+
+
+@pytest.mark.parametrize("act", ["gelu", "gelu_tanh", "relu", "silu", "none"])
+@pytest.mark.parametrize("t,k,n,dtype", [
+    (5, 128, 255, "bf16"), (200, 256, 385, "bf16"), (300, 320, 512, "bf16"), (40, 96, 128, "fp32"),
+    (200, 256, 385, "fp32")])
+def test_linear_activations(t, k, n, dtype, act):
+    check_linear(t, k, n, dtype, act, dtype, True, False)
+
+
+@pytest.mark.parametrize("act", ["gelu", "none"])
+@pytest.mark.parametrize("t,k,n,dtype", [
+    (16400, 512, 512, "bf16"),   # 256 x 128 tiles, the weights turned
+    (4100, 2048, 4096, "bf16"),  # 256 x 256
+    (4000, 2051, 4099, "bf16"),  # the same, ragged
+    (9000, 768, 1000, "bf16"),   # in place, 128 x 128
+    (4200, 300, 1100, "fp32")])
+def test_linear_large(t, k, n, dtype, act):
+    check_linear(t, k, n, dtype, act, dtype, True, True)
+
+
+def test_linear_gradient_against_differences():
+    import torch
+    l, x, w, b, add, dy, buf = linear_case(20, 30, 40, "fp32", "gelu_tanh")
+    K.linear(l, x, w, buf, bias=b, residual=add, training=True)
+    gx, gw, gb = (g.clone() for g in K.linear_backward(l, x, w, dy, buf))
+
+    def loss(x, w, b):
+        return float((act64(x.double() @ w.double() + b.double(), "gelu_tanh") * dy.double()).sum())
+
+    r, h = gen(1), 1e-4
+    for name, t, g in (("x", x, gx), ("w", w, gw), ("b", b, gb)):
+        d = r(*t.shape).double()
+        args = dict(x=x.double(), w=w.double(), b=b.double())
+        up, down = dict(args), dict(args)
+        up[name], down[name] = args[name] + h * d, args[name] - h * d
+        slope = (loss(**up) - loss(**down)) / (2 * h)
+        # central differences in 64 bits are off by h^2; the gradients by 1e-5 of their norm
+        assert abs(slope - float((g.double() * d).sum())) <= 1e-5 * float(g.double().norm() * d.norm()), name
+
+
+@pytest.mark.parametrize("t", [2, 40, 300])
+def test_linear_odd_values(t):
+    import torch
+    l, x, w, b, add, dy, buf = linear_case(t, 256, 192, "bf16", "silu")
+    x[1, 3], add[0, 5] = float("nan"), float("inf")
+    K.linear(l, x, w, buf, bias=b, residual=add, training=True)
+    bad = ~torch.isfinite(buf.y)
+    assert bool(bad[1].all()) and float(buf.y[0, 5]) == float("inf") and int(bad.sum()) == 193
+    gx, gw, gb = K.linear_backward(l, x, w, dy, buf)
+    assert bool(torch.isnan(gx[1]).all()) and bool(torch.isnan(gw).all()) and bool(torch.isnan(gb).all())
+    rest = torch.arange(t, device="cuda") != 1
+    assert bool(torch.isfinite(gx[rest]).all())
+
+
+def test_linear_zero_tokens():
+    l = K.Linear(0, 64, 96, "bf16", "gelu", "bf16")
+    buf = K.allocate_linear(l, "cuda", training=True)
+    import torch
+    x, w = torch.empty(0, 64, dtype=torch.bfloat16, device="cuda"), gen(1)(64, 96, dtype="bf16")
+    y = torch.empty(0, 96, dtype=torch.bfloat16, device="cuda")
+    buf.grad_w.fill_(1), buf.grad_bias.fill_(1)
+    assert K.linear(l, x, w, buf, training=True).shape == (0, 96)
+    K.linear_backward(l, x, w, y, buf)
+    assert not buf.grad_w.any() and not buf.grad_bias.any()
+
+
+# ------------------------------------------------------------- residual step
+
+def step64(n, z, res, p, go, gy):
+    """Results, gradients by differentiation, and the terms of the parameters'."""
+    import torch
+    leaf = {k: v.double().requires_grad_() for k, v in p.items()}
+    z, res = z.double().requires_grad_(), res.double().requires_grad_()
+
+    def norm(x):
+        c = x - x.mean(1, keepdim=True) if n.kind == "layer" else x
+        return c / (c.square().mean(1, keepdim=True) + n.eps).sqrt()
+
+    def apply(h, w, b):
+        h = h * leaf[w] if w in leaf else h
+        return h + leaf[b] if b in leaf else h
+
+    u = apply(norm(z), "post_weight", "post_bias") if n.post else z
+    o = n.scale * res + (leaf["gate"] * u if "gate" in leaf else u)
+    oh = norm(o)
+    y = apply(oh, "pre_weight", "pre_bias") if n.pre else None
+    loss = 0.0
+    if go is not None:
+        loss = loss + (o * go.double()).sum()
+    if n.pre:
+        loss = loss + (y * gy.double()).sum()
+    names = [k for k in leaf if not (k.startswith("post") and not n.post) and not (k.startswith("pre") and not n.pre)]
+    got = torch.autograd.grad(loss, [z, res, o] + [leaf[k] for k in names])
+    do = got[2].abs()
+    gate = leaf["gate"].abs() if "gate" in leaf else 1.0
+    zh = norm(z).abs() if n.post else z.abs()
+    terms = {"post_weight": (do * gate * zh).sum(0), "post_bias": (do * gate).sum(0),
+             "gate": (do * (zh * leaf.get("post_weight", torch.ones(1, device="cuda")).abs()
+                            + (leaf["post_bias"].abs() if "post_bias" in leaf else 0.0))).sum(0)}
+    if n.pre:
+        terms.update(pre_weight=(gy.double() * oh).abs().sum(0), pre_bias=gy.double().abs().sum(0))
+    return (o.detach(), None if y is None else y.detach(), got[0], got[1], dict(zip(names, got[3:])),
+            {k: v.detach() for k, v in terms.items()})
+
+
+def step_params(r, width, names):
+    return {k: (r(width, std=0.3) if k.endswith("bias") else 1 + r(width, std=0.3)) for k in names}
+
+
+STEPS = [(1, 1), (3, 2), (2, 7), (9, 64), (5, 65), (11, 128), (4, 129), (1000, 512), (33, 513), (21, 1024), (300, 1155),
+         (7, 2050), (5, 4096), (4, 4100), (3, 8192), (6, 8200), (2, 16384), (3, 16383), (3001, 96)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("kind", ["layer", "rms"])
+@pytest.mark.parametrize("rows,width", STEPS)
+def test_step(rows, width, kind, dtype):
+    import torch
+    # 64 additions a thread in a row's sums, made of two norms
+    acc = 256 * 2.0 ** -24
+    for post, pre, names, out in ((True, True, K.NORM_PARAMS, True), (False, True, ("gate", "pre_weight"), False),
+                                  (True, False, ("post_weight",), True), (False, True, (), True)):
+        note(f"step {rows} {width} {kind} {dtype} post {post} pre {pre}")
+        n = K.ResidualNorm(rows, width, dtype, kind, 1e-5, 0.75, post, pre)
+        r = gen(rows + width)
+        z, res = r(rows, width, dtype=dtype, std=2.0) + 0.5, r(rows, width, dtype=dtype) - 0.25
+        go, gy = r(rows, width, dtype=dtype) if out else None, r(rows, width, dtype=dtype) if pre else None
+        p = step_params(r, width, names)
+        buf = K.allocate_residual_norm(n, "cuda", training=True)
+        for t in (buf.out, buf.y, buf.grad_z, buf.grad_res, *buf.grads.values()):
+            if t is not None:
+                t.fill_(float("nan"))
+        K.residual_norm(n, z, res, p, buf)
+        gz, gr, g = K.residual_norm_backward(n, z, res, p, go, gy, buf)
+        o, y, dz, dres, dp, terms = step64(n, z, res, p, go, gy)
+        u = U[dtype]
+        near("out", buf.out, o, u + acc)
+        if pre:
+            # a row of one or two values: its deviation is a difference of nearly equal numbers
+            within("y", buf.y, y, (u + acc) * float(y.norm()) + (acc * 64 * math.sqrt(rows) if width < 8 else 0.0))
+        if width < 8 and kind == "layer":
+            continue  # gradients that cancel entirely
+        # dz and dres cancel in part: each is held to its size and its terms'
+        size = float(dres.norm()) + float(dz.norm()) + (float(gy.double().norm()) if pre else 0.0)
+        within("dz", gz, dz, u * float(dz.norm()) + acc * 16 * size)
+        within("dres", gr, dres, u * float(dres.norm()) + acc * 16 * size)
+        for k, want in dp.items():
+            within(k, g[k], want, 1024 * 2.0 ** -24 * float(terms[k].norm()) + acc * size)
+        if post and pre:
+            once = [t.clone() for t in (buf.out, buf.y, gz, gr, *g.values())]
+            K.residual_norm(n, z, res, p, buf)
+            K.residual_norm_backward(n, z, res, p, go, gy, buf)
+            assert all(torch.equal(a, b) for a, b in zip(once, (buf.out, buf.y, gz, gr, *g.values())))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("width", [96, 333, 2050])
+def test_step_strided_and_in_place(width, dtype):
+    import torch
+    rows = 21
+    n = K.ResidualNorm(rows, width, dtype, scale=0.5)
+    r = gen(width)
+    wide = r(rows, 2 * width + 9, dtype=dtype)
+    z, res = wide[:, 3:3 + width], wide[:, width + 5:2 * width + 5]
+    go, gy = r(rows, width + 1, dtype=dtype)[:, 1:], r(rows, width, dtype=dtype)
+    p = step_params(r, width, K.NORM_PARAMS)
+    buf = K.allocate_residual_norm(n, "cuda", training=True)
+    zc, rc = z.contiguous(), res.contiguous()
+    K.residual_norm(n, zc, rc, p, buf)
+    K.residual_norm_backward(n, zc, rc, p, go.contiguous(), gy, buf)
+    want = [t.clone() for t in (buf.out, buf.y, buf.grad_z, buf.grad_res, *buf.grads.values())]
+    before = wide.clone()
+    # strided everything, the outputs with guards behind them
+    guard = [torch.full((rows, width + 6), 7.0, device="cuda").to(wide.dtype) for _ in range(4)]
+    buf.out, buf.y, buf.grad_z, buf.grad_res = (t[:, 1:1 + width] for t in guard)
+    K.residual_norm(n, z, res, p, buf)
+    K.residual_norm_backward(n, z, res, p, go, gy, buf)
+    for t, w in zip((buf.out, buf.y, buf.grad_z, buf.grad_res, *buf.grads.values()), want):
+        assert torch.equal(t, w)
+    for t in guard:
+        assert bool((t[:, :1] == 7).all()) and bool((t[:, 1 + width:] == 7).all())
+    assert torch.equal(wide, before)
+    # gradients over the inputs' gradients, then out over res and y over z
+    go2, gy2 = go.contiguous(), gy.clone()
+    buf.grad_z, buf.grad_res = gy2, go2
+    K.residual_norm_backward(n, z, res, p, go2, gy2, buf)
+    assert torch.equal(gy2, want[2]) and torch.equal(go2, want[3])
+    buf.out, buf.y = res, z
+    K.residual_norm(n, z, res, p, buf)
+    assert torch.equal(res, want[0]) and torch.equal(z, want[1])
+    assert torch.equal(wide[:, :3], before[:, :3]) and torch.equal(wide[:, 2 * width + 5:], before[:, 2 * width + 5:])
+
+
+def test_step_gradient_against_differences():
+    import torch
+    n = K.ResidualNorm(12, 70, "fp32", "rms", 1e-5, 1.25)
+    r = gen(4)
+    z, res, go, gy = (r(12, 70) for _ in range(4))
+    p = step_params(r, 70, K.NORM_PARAMS)
+    buf = K.allocate_residual_norm(n, "cuda", training=True)
+    K.residual_norm(n, z, res, p, buf)
+    gz, gr, g = K.residual_norm_backward(n, z, res, p, go, gy, buf)
+
+    def loss(v):
+        o, y = step64(n, v["z"], v["res"], {k: v[k] for k in K.NORM_PARAMS}, go, gy)[:2]
+        return float((o * go.double()).sum() + (y * gy.double()).sum())
+
+    at = dict(p, z=z, res=res)
+    at = {k: v.double() for k, v in at.items()}
+    h = 1e-5
+    for name, grad in dict(g, z=gz, res=gr).items():
+        d = r(*at[name].shape).double()
+        slope = (loss(dict(at, **{name: at[name] + h * d})) - loss(dict(at, **{name: at[name] - h * d}))) / (2 * h)
+        assert abs(slope - float((grad.double() * d).sum())) <= 1e-5 * float(grad.double().norm() * d.norm()), name
+
+
+def test_step_odd_values_and_no_rows():
+    import torch
+    n = K.ResidualNorm(6, 300, "bf16")
+    r = gen(8)
+    z, res = r(6, 300, dtype="bf16"), r(6, 300, dtype="bf16")
+    z[1, 7], res[2, 0], z[3], res[3] = float("nan"), float("inf"), 0.25, 0.0
+    buf = K.allocate_residual_norm(n, "cuda", training=True)
+    K.residual_norm(n, z, res, {}, buf)
+    assert bool(torch.isnan(buf.out[1].float()).all()) and bool(torch.isnan(buf.y[1].float()).all())
+    assert float(buf.out[2, 0]) == float("inf") and bool(torch.isnan(buf.y[2].float()).any())
+    assert not buf.out[3].any() and not buf.y[3].any()  # a constant row is its mean
+    assert bool(torch.isfinite(buf.y[[0, 3, 4, 5]]).all())
+    n = K.ResidualNorm(0, 300, "bf16")
+    buf = K.allocate_residual_norm(n, "cuda", training=True)
+    for g in buf.grads.values():
+        g.fill_(1)
+    e = torch.empty(0, 300, dtype=torch.bfloat16, device="cuda")
+    K.residual_norm(n, e, e, {}, buf)
+    K.residual_norm_backward(n, e, e, {}, e, e, buf)
+    assert not any(g.any() for g in buf.grads.values())
+
+
+# -------------------------------------------------------------- balance loss
+
+def balance_case(t, e, k, d, dtype, seed=0, mask=None, **kw):
+    import torch
+    r = gen(t + e + d + seed)
+    b = K.BalanceLoss(t, e, k, d, dtype, **kw)
+    x = r(t, d, dtype=dtype)
+    w = r(d, e, std=d ** -0.5) * torch.exp(0.5 * r(e))
+    idx = torch.topk(x.float() @ w, k, dim=1).indices.to(torch.int32)
+    m = None
+    if mask is not None:
+        g = torch.Generator(device="cuda")
+        g.manual_seed(seed + 1)
+        m = torch.rand(t, generator=g, device="cuda") < mask
+    return b, x, w, idx, m, K.allocate_balance_loss(b, "cuda", training=True)
+
+
+def balance64(b, x, w, idx, mask, gloss=1.0):
+    import torch
+    keep = torch.ones(b.tokens, dtype=torch.bool, device="cuda") if mask is None else mask.bool()
+    n = int(keep.sum())
+    x, w = x.double(), w.double().requires_grad_()
+    xk = x[keep].requires_grad_()
+    counts = torch.bincount(idx[keep].reshape(-1).long(), minlength=b.experts)
+    logits = xk @ w
+    p = torch.softmax(logits, 1).sum(0) / max(n, 1)
+    even = b.experts * (counts.double() / max(n * b.top_k, 1) * p).sum()
+    zed = torch.logsumexp(logits, 1).square().sum() / max(n, 1)
+    loss = b.balance * even + b.z * zed
+    gx = torch.zeros_like(x)
+    got = torch.autograd.grad(loss, (xk, w), torch.tensor(float(gloss), dtype=torch.float64, device="cuda"))
+    gx[keep] = got[0]
+    return torch.stack((loss, even, zed)).detach(), p.detach(), counts, gx, got[1]
+
+
+def check_balance(b, x, w, idx, mask, buf, gloss=None, clean=None):
+    import torch
+    for t in (buf.loss, buf.mean_prob, buf.grad_x, buf.grad_router):
+        t.fill_(float("nan"))
+    buf.workspace.fill_(255), buf.saved.fill_(255), buf.counts.fill_(-1)
+    K.balance_loss(b, x, w, idx, buf, mask=mask, training=True)
+    buf.workspace.fill_(255)
+    g = None if gloss is None else torch.tensor([gloss], device="cuda")
+    gx, gw = K.balance_loss_backward(b, x, w, buf, grad_loss=g, mask=mask)
+    loss, p, counts, dx, dw = balance64(b, x if clean is None else clean, w, idx, mask, 1.0 if gloss is None else gloss)
+    assert buf.counts.tolist() == counts.tolist()
+    near("loss", buf.loss, loss, 2.0 ** -18)
+    near("mean_prob", buf.mean_prob, p, 2.0 ** -18)
+    # dl = p (c1 (f - sum f p) + 2 c2 lse): the first bracket cancels where the
+    # experts are balanced, so gradients are held to c1 f p's size as well
+    n = max(1, int(mask.sum()) if mask is not None else b.tokens)
+    rows = math.sqrt(n) * abs(1.0 if gloss is None else gloss) / n * (abs(b.balance) * b.experts + 2 * abs(b.z) * 8)
+    # f <= 1 and |p| <= 1: rows' gradients by the logits are off by 2^-16 of these at most
+    within("dx", gx, dx, (U[b.dtype] + 2.0 ** -15) * float(dx.norm())
+           + 2.0 ** -19 * rows * float(torch.linalg.matrix_norm(w.double(), 2)))
+    within("dw", gw, dw, 2.0 ** -15 * float(dw.norm())
+           + 2.0 ** -19 * rows * math.sqrt(b.d_model) * float((x if clean is None else clean).double().abs().max()))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("t,e,k,d", [
+    (1, 1, 1, 128), (1, 64, 8, 512), (2, 2, 1, 128), (31, 5, 2, 256), (32, 8, 2, 512), (33, 32, 4, 384), (63, 33, 33, 128),
+    (200, 8, 2, 512), (257, 64, 64, 128), (1000, 47, 6, 1152), (4999, 33, 3, 1152), (5000, 64, 8, 512), (300, 16, 4, 8192),
+    (20000, 24, 4, 256)])
+def test_balance(t, e, k, d, dtype):
+    note(f"balance {t} {e} {k} {d} {dtype}")
+    for mask in (None, 0.7):
+        b, x, w, idx, m, buf = balance_case(t, e, k, d, dtype, mask=mask)
+        check_balance(b, x, w, idx, m, buf)
+
+
+@pytest.mark.parametrize("dtype,t,e,k,d", [("bf16", 65537, 64, 8, 512), ("fp32", 66000, 20, 2, 256),
+                                           ("bf16", 131072, 8, 2, 128)])
+def test_balance_large(dtype, t, e, k, d):
+    note(f"balance {t} {e} {k} {d} {dtype}")
+    b, x, w, idx, m, buf = balance_case(t, e, k, d, dtype, mask=0.9, balance=1.0, z=0.1)
+    check_balance(b, x, w, idx, m, buf, gloss=-2.5)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_balance_masks(dtype):
+    """Tokens that are left out may hold anything; none kept gives zeros."""
+    import torch
+    note(f"balance masks {dtype}")
+    b, x, w, idx, m, buf = balance_case(700, 40, 5, 256, dtype, mask=0.6)
+    clean = x.clone()
+    out = torch.nonzero(~m)[:, 0]
+    x[out[0::3]], x[out[1::3]], x[out[2::3]] = float("nan"), float("inf"), -float("inf")
+    check_balance(b, x, w, idx, m, buf, clean=clean)
+    assert not buf.grad_x[out].any()
+    want = [t.clone() for t in (buf.loss, buf.mean_prob, buf.counts, buf.grad_x, buf.grad_router)]
+    bytes_ = m.to(torch.uint8) * 3
+    K.balance_loss(b, x, w, idx, buf, mask=bytes_, training=True)
+    K.balance_loss_backward(b, x, w, buf, mask=bytes_)
+    assert all(torch.equal(a, c) for a, c in zip(want, (buf.loss, buf.mean_prob, buf.counts, buf.grad_x, buf.grad_router)))
+    none = torch.zeros_like(m)
+    K.balance_loss(b, x, w, idx, buf, mask=none, training=True)
+    K.balance_loss_backward(b, x, w, buf, mask=none)
+    assert not any(bool(t.any()) for t in (buf.loss, buf.mean_prob, buf.counts, buf.grad_x, buf.grad_router))
+    # a mask at an odd address
+    shifted = torch.zeros(704, dtype=torch.bool, device="cuda")[3:703]
+    shifted.copy_(m)
+    K.balance_loss(b, x, w, idx, buf, mask=shifted, training=True)
+    K.balance_loss_backward(b, x, w, buf, mask=shifted)
+    assert all(torch.equal(a, c) for a, c in zip(want, (buf.loss, buf.mean_prob, buf.counts, buf.grad_x, buf.grad_router)))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_balance_added_to_gradients(dtype):
+    import torch
+    b, x, w, idx, m, buf = balance_case(333, 20, 3, 256, dtype, mask=0.8, balance=1.0)
+    g = torch.tensor([3.0], device="cuda")
+    K.balance_loss(b, x, w, idx, buf, mask=m, training=True)
+    K.balance_loss_backward(b, x, w, buf, grad_loss=g, mask=m)
+    _, _, _, dx, dw = balance64(b, x, w, idx, m, 3.0)
+    r = gen(5)
+    gx, gw = r(333, 256, dtype=dtype, std=1e-2), r(256, 20)
+    x0, w0 = gx.clone(), gw.clone()
+    back = K.balance_loss_backward(b, x, w, buf, grad_loss=g, mask=m, add_to=(gx, gw))
+    assert back[0] is gx and back[1] is gw
+    near("dx", gx, x0.double() + dx, U[dtype] + 2.0 ** -15)
+    near("dw", gw, w0.double() + dw, 2.0 ** -15)
+    assert torch.equal(gx[~m], x0[~m])
+
+
+def test_balance_gradient_against_differences():
+    b, x, w, idx, m, buf = balance_case(60, 12, 3, 128, "fp32", mask=0.8, balance=1.0, z=0.5)
+    K.balance_loss(b, x, w, idx, buf, mask=m, training=True)
+    gx, gw = K.balance_loss_backward(b, x, w, buf, mask=m)
+    r, h = gen(6), 1e-4
+    d, f = r(60, 128).double(), r(128, 12).double()
+    for dx, dw, g in ((d, 0.0, gx), (0.0, f, gw)):
+        up = float(balance64(b, x.double() + h * dx, w.double() + h * dw, idx, m)[0][0])
+        down = float(balance64(b, x.double() - h * dx, w.double() - h * dw, idx, m)[0][0])
+        step = d if g is gx else f
+        assert abs((up - down) / (2 * h) - float((g.double() * step).sum())) <= 1e-4 * float(g.double().norm() * step.norm())
+
+
+def test_balance_even_router_and_no_tokens():
+    """Equal logits: p is 1 / E, the balance loss is 1 whatever the counts, and
+    its gradient vanishes; no tokens: zeros."""
+    import torch
+    b, x, w, idx, m, buf = balance_case(100, 8, 2, 128, "bf16", balance=1.0, z=0.0)
+    w.zero_()
+    K.balance_loss(b, x, w, idx, buf, training=True)
+    assert bool((buf.mean_prob - 0.125).abs().max() < 1e-6)
+    assert abs(float(buf.loss[1]) - 1.0) < 1e-6 and abs(float(buf.loss[2]) - math.log(8) ** 2) < 1e-5
+    for add in (False, True):
+        b = K.BalanceLoss(0, 8, 2, 128, "bf16")
+        buf = K.allocate_balance_loss(b, "cuda", training=True)
+        e = torch.empty(0, 128, dtype=torch.bfloat16, device="cuda")
+        i = torch.empty(0, 2, dtype=torch.int32, device="cuda")
+        buf.grad_router.fill_(1)
+        K.balance_loss(b, e, w, i, buf, training=True)
+        K.balance_loss_backward(b, e, w, buf, add_to=(buf.grad_x, buf.grad_router) if add else None)
+        assert not buf.loss.any() and not buf.counts.any() and not buf.mean_prob.any()
+        assert bool((buf.grad_router == (1 if add else 0)).all())
+
+
+# ------------------------------------------------------------- used together
+
+def test_large_offsets():
+    """Elements past 2^31: the last rows against a call on them alone."""
+    import torch
+    note("step past 32 bits")
+    rows, width = 300_000, 8192
+    last = 3
+    x = torch.zeros(rows, width, dtype=torch.bfloat16, device="cuda")
+    x[-last:] = gen(1)(last, width, dtype="bf16")
+    n, ns = K.ResidualNorm(rows, width, "bf16", pre=True), K.ResidualNorm(last, width, "bf16", pre=True)
+    buf, small = K.allocate_residual_norm(n, "cuda", training=True), K.allocate_residual_norm(ns, "cuda", training=True)
+    K.residual_norm(n, x, x, {}, buf)
+    K.residual_norm_backward(n, x, x, {}, x, x, buf)
+    xs = x[-last:].contiguous()
+    K.residual_norm(ns, xs, xs, {}, small)
+    K.residual_norm_backward(ns, xs, xs, {}, xs, xs, small)
+    for a in ("out", "y", "grad_z", "grad_res"):
+        assert torch.equal(getattr(buf, a)[-last:], getattr(small, a)), a
+    del x, buf, small
+    note("linear past 32 bits")
+    l, x, w, b, _, dy, buf = linear_case(280_000, 64, 8000, "bf16", "none", res=False)
+    K.linear(l, x, w, buf, bias=b, training=True)
+    gx = K.linear_backward(l, x, w, dy, buf)[0]
+    ls = K.Linear(300, 64, 8000, "bf16")
+    bs = K.allocate_linear(ls, "cuda", training=True)
+    K.linear(ls, x[-300:].contiguous(), w, bs, bias=b, training=True)
+    near("last rows", buf.y[-300:], bs.y.double(), 2 * U["bf16"])
+    near("last rows of dx", gx[-300:], K.linear_backward(ls, x[-300:].contiguous(), w, dy[-300:].contiguous(), bs)[0].double(),
+         2 * U["bf16"])
+    del x, dy, buf, gx
+    note("balance past 32 bits")
+    t, d = 270_000, 8192
+    b, x, w, idx, m, buf = balance_case(t, 8, 2, 128, "bf16")
+    x = torch.zeros(t, d, dtype=torch.bfloat16, device="cuda")
+    x[-last:] = gen(2)(last, d, dtype="bf16")
+    w = gen(3)(d, 8, std=d ** -0.5)
+    mask = torch.zeros(t, dtype=torch.bool, device="cuda")
+    mask[-last:] = True
+    b, bs = K.BalanceLoss(t, 8, 2, d, "bf16"), K.BalanceLoss(last, 8, 2, d, "bf16")
+    buf, small = K.allocate_balance_loss(b, "cuda", training=True), K.allocate_balance_loss(bs, "cuda", training=True)
+    K.balance_loss(b, x, w, idx, buf, mask=mask, training=True)
+    K.balance_loss_backward(b, x, w, buf, mask=mask)
+    xs = x[-last:].contiguous()
+    K.balance_loss(bs, xs, w, idx[-last:].contiguous(), small, training=True)
+    K.balance_loss_backward(bs, xs, w, small)
+    near("loss", buf.loss, small.loss, 2.0 ** -18)
+    near("dx", buf.grad_x[-last:], small.grad_x, 2 * U["bf16"])
+    near("dw", buf.grad_router, small.grad_router, 2.0 ** -15)
+    assert not buf.grad_x[:-last].any()
+
+
+def together(p, c, r):
+    """A projection into the residual stream, the step behind it, the layer as a
+    block with its balance loss and the step behind that, forward and backward."""
+    import torch
+    dtype, t, d = p.dtype, p.tokens, p.d_model
+    l = K.Linear(t, 200, d, dtype)
+    first = K.ResidualNorm(t, d, dtype, post=False)
+    n = K.ResidualNorm(t, d, dtype, "rms", scale=0.9)
+    b = K.BalanceLoss(t, p.experts, p.top_k, d, dtype, balance=1.0, z=0.1)
+    wl = r(200, d, std=200 ** -0.5, dtype=dtype)
+    pf, pn = step_params(r, d, ("pre_weight",)), step_params(r, d, K.NORM_PARAMS)
+    weights = dict(c.weights(), **pn)
+    stream0 = r(t, d, dtype=dtype)
+    mask = torch.arange(t, device="cuda") < t - 5
+
+    def buffers():
+        return dict(l=K.allocate_linear(l, "cuda", training=True), f=K.allocate_residual_norm(first, "cuda", training=True),
+                    n=K.allocate_residual_norm(n, "cuda", training=True), b=K.allocate_balance_loss(b, "cuda", training=True),
+                    layer=B.allocate(p, "cuda", training=True))
+
+    def run(x, go, gy, u):
+        a = K.linear(l, x, wl, u["l"], training=True)
+        s, h = K.residual_norm(first, a, stream0, pf, u["f"])
+        out, y = K.residual_layer_forward(p, h, s, weights, u["layer"], n, u["n"], (b, u["b"]), mask, training=True)
+        gh, gs, grads = K.residual_layer_backward(p, h, s, weights, go, gy, u["layer"], n, u["n"], (b, u["b"]),
+                                                  mask=mask)
+        ga, gstream, gf = K.residual_norm_backward(first, a, stream0, pf, gs, gh, u["f"])
+        gx, gw, _ = K.linear_backward(l, x, wl, ga, u["l"], bias=False)
+        return [out, y, u["b"].loss, gx, gw, gstream, gf["pre_weight"], *(grads[k] for k in sorted(grads))]
+
+    return buffers, run
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_residual_layer(dtype):
+    """The layer as a residual block against its parts run one by one, and
+    through 64-bit differentiation for the gradients of the router."""
+    import torch
+    p = Problem(300, 8, 2, 256, 128, 128, dtype, 64)
+    c = Case(p, seed=1, training=True)
+    r = gen(9)
+    buffers, run = together(p, c, r)
+    x, go, gy = r(300, 200, dtype=dtype), r(300, 256, dtype=dtype), r(300, 256, dtype=dtype)
+    got = [t.clone() for t in run(x, go, gy, buffers())]
+    assert all(bool(torch.isfinite(t.float()).all()) for t in got)
+    # the loss's part of the gradients: the same run without it, and the parts alone
+    h = c.dev["x"]
+    w = dict(c.weights(), **step_params(r, 256, K.NORM_PARAMS))
+    n, b = K.ResidualNorm(300, 256, dtype, "rms"), K.BalanceLoss(300, 8, 2, 256, dtype, 1.0, 0.1)
+    st, bb = K.allocate_residual_norm(n, "cuda", training=True), K.allocate_balance_loss(b, "cuda", training=True)
+    res = r(300, 256, dtype=dtype)
+    out, y = K.residual_layer_forward(p, h, res, w, c.buf, n, st, (b, bb), training=True)
+    gh, gs, grads = K.residual_layer_backward(p, h, res, w, go, gy, c.buf, n, st, (b, bb))
+    gh, grads = gh.clone(), {k: v.clone() for k, v in grads.items()}
+    d = Case(p, seed=1, training=True)
+    z = B.forward(p, h, d.weights(), d.buf, training=True)
+    st2 = K.allocate_residual_norm(n, "cuda", training=True)
+    out2, y2 = K.residual_norm(n, z, res, w, st2)
+    gz, gs2, gn = K.residual_norm_backward(n, z, res, w, go, gy, st2)
+    gx, gl = B.backward(p, h, d.weights(), gz, d.buf)
+    assert torch.equal(out, out2) and torch.equal(y, y2) and torch.equal(gs, gs2)
+    for k in gn:
+        assert torch.equal(grads[k], gn[k]), k
+    for k in gl:
+        if k != "w_router":
+            assert torch.equal(grads[k], gl[k]), k
+    loss, _, _, dx, dw = balance64(b, h, d.weights()["w_router"], d.buf.routing["topk_idx"], None)
+    near("loss", bb.loss, loss, 2.0 ** -18)
+    near("dx", gh, gx.double() + dx, U[dtype] + 2.0 ** -15)
+    near("dw", grads["w_router"], gl["w_router"].double() + dw, 2.0 ** -15)
+
+
+def test_streams_and_graphs():
+    """The run on two side streams at once with buffers of their own, and
+    captured and replayed between eager work."""
+    import torch
+    p = Problem(200, 16, 4, 256, 128, 0, "bf16", 64)
+    c = Case(p, seed=2, training=True)
+    r = gen(3)
+    buffers, run = together(p, c, r)
+    x, go, gy = r(200, 200, dtype="bf16"), r(200, 256, dtype="bf16"), r(200, 256, dtype="bf16")
+    one, two, three = buffers(), buffers(), buffers()
+    want = [t.clone() for t in run(x, go, gy, one)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = []
+    for s, u in zip(streams, (two, three)):
+        with torch.cuda.stream(s):
+            got.append(run(x, go, gy, u))
+    torch.cuda.synchronize()
+    for g in got:
+        assert all(torch.equal(a, b) for a, b in zip(g, want))
+    # a stream given by hand, which is not the current one
+    n, st = K.ResidualNorm(200, 256, "bf16"), K.allocate_residual_norm(K.ResidualNorm(200, 256, "bf16"))
+    a, b = (t.clone() for t in K.residual_norm(n, go, gy, {}, st))
+    st.out.zero_(), st.y.zero_()
+    torch.cuda.synchronize()
+    K.residual_norm(n, go, gy, {}, st, stream=streams[0])
+    streams[0].synchronize()
+    assert torch.equal(a, st.out) and torch.equal(b, st.y)
+    xs = x.clone()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = run(xs, go, gy, one)
+    for i in range(4):
+        xs.copy_(x * (1 + 0.5 * i))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in outs]
+        eager = run(xs, go, gy, two)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, eager)), i
