@@ -122,7 +122,7 @@ def load():
         "moe_balance_workspace_bytes": (size, [S]),
         "moe_balance_saved_bytes": (size, [S]),
         "moe_balance_loss": (ctypes.c_int, [S] + [P] * 9 + [size, P]),
-        "moe_balance_loss_bwd": (ctypes.c_int, [S] + [P] * 5 + [ctypes.c_int] + [P] * 3 + [size, P]),
+        "moe_balance_loss_bwd": (ctypes.c_int, [S] + [P] * 4 + [ctypes.c_int] + [P] * 3 + [size, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -285,12 +285,12 @@ def moe_balance_loss(b: moe_balance, x, w_router, topk_idx, mask, counts, mean_p
                                    _stream(stream)), "moe_balance_loss")
 
 
-def moe_balance_loss_bwd(b: moe_balance, x, w_router, mask, saved, grad_loss, add: bool, grad_x,
-                         grad_router, workspace, workspace_bytes: Optional[int] = None, stream=None):
-    _check(load().moe_balance_loss_bwd(ctypes.byref(b), _ptr(x), _ptr(w_router), _ptr(mask),
-                                       _ptr(saved), _ptr(grad_loss), int(add), _ptr(grad_x),
-                                       _ptr(grad_router), _ptr(workspace),
-                                       _nbytes(workspace, workspace_bytes), _stream(stream)),
+def moe_balance_loss_bwd(b: moe_balance, x, mask, saved, grad_loss, add: bool, grad_x, grad_router,
+                         workspace, workspace_bytes: Optional[int] = None, stream=None):
+    _check(load().moe_balance_loss_bwd(ctypes.byref(b), _ptr(x), _ptr(mask), _ptr(saved),
+                                       _ptr(grad_loss), int(add), _ptr(grad_x), _ptr(grad_router),
+                                       _ptr(workspace), _nbytes(workspace, workspace_bytes),
+                                       _stream(stream)),
            "moe_balance_loss_bwd")
 
 
@@ -1020,7 +1020,8 @@ def balance_loss_backward(b: BalanceLoss, x, w_router, buf: BalanceBuffers, grad
                           add_to=None, stream=None):
     """Gradients of grad_loss * loss[0] (grad_loss: an fp32 tensor of one
     number, or None: 1) after ``balance_loss(..., training=True)`` with the same
-    buffers and mask: (grad_x, grad_router). add_to: a pair of gradients, the
+    buffers and mask: (grad_x, grad_router). w_router is the forward's, whose
+    values the buffers hold (only its shape is looked at). add_to: a pair of gradients, the
     layer's own for instance, that they are added to in place of the buffers'."""
     c, nsv, xs, ws, dt = _balance(b)
     dev = x.device
@@ -1034,8 +1035,8 @@ def balance_loss_backward(b: BalanceLoss, x, w_router, buf: BalanceBuffers, grad
     _want("grad_x", gx, xs, dt, dev)
     _want("gradient of w_router", gw, ws, torch.float32, dev)
     _want_bytes("workspace", buf.workspace, 0, dev)
-    _run("moe_balance_loss_bwd", dev, stream, load().moe_balance_loss_bwd, c, x.data_ptr(),
-         w_router.data_ptr(), m, buf.saved.data_ptr(), _ptr(grad_loss), int(add_to is not None),
+    _run("moe_balance_loss_bwd", dev, stream, load().moe_balance_loss_bwd, c, x.data_ptr(), m,
+         buf.saved.data_ptr(), _ptr(grad_loss), int(add_to is not None),
          gx.data_ptr(), gw.data_ptr(), buf.workspace.data_ptr(), buf.workspace.numel())
     return gx, gw
 

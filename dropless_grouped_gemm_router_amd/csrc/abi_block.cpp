@@ -332,19 +332,19 @@ MOE_EXPORT int moe_balance_loss(const moe_balance* b, const void* x, const float
                                         as_stream(stream)));
 }
 
-MOE_EXPORT int moe_balance_loss_bwd(const moe_balance* b, const void* x, const float* w_router,
-                                    const uint8_t* mask, const void* saved, const float* grad_loss, int add,
-                                    void* grad_x, float* grad_router, void* workspace, size_t workspace_bytes,
+MOE_EXPORT int moe_balance_loss_bwd(const moe_balance* b, const void* x, const uint8_t* mask,
+                                    const void* saved, const float* grad_loss, int add, void* grad_x,
+                                    float* grad_router, void* workspace, size_t workspace_bytes,
                                     void* stream) {
   const int st = check_balance(b);
   if (st != MOE_OK) return st;
   if (add != 0 && add != 1) return MOE_ERR_INVALID;
   if (!ok_ptr(grad_router, 4) || !aligned(grad_loss, 4)) return MOE_ERR_INVALID;
   if (b->tokens > 0) {
-    if (!ok_ptr(x) || !ok_ptr(w_router, 4) || !ok_ptr(saved, 256) || !ok_ptr(grad_x) || !ok_ptr(workspace, 256))
+    if (!ok_ptr(x) || !ok_ptr(saved, 256) || !ok_ptr(grad_x) || !ok_ptr(workspace, 256))
       return MOE_ERR_INVALID;
     if (workspace_bytes < moe::balance_ws_bytes(*b)) return MOE_ERR_WORKSPACE;
   }
-  return hip_status(moe::launch_balance_bwd(*b, x, w_router, mask, saved, grad_loss, add != 0, grad_x, grad_router,
+  return hip_status(moe::launch_balance_bwd(*b, x, mask, saved, grad_loss, add != 0, grad_x, grad_router,
                                             workspace, as_stream(stream)));
 }

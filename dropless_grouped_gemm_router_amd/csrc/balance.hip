@@ -64,18 +64,55 @@ __device__ void split_router(const float* __restrict__ w, int d, int E, int EB, 
   }
 }
 
+// W as the first operand of dx = dl W^T, for the backward: 64 columns of x at a
+// time, four fragments of 16, 16 bytes a lane.
+// bf16: fragment j's row i is column 32 (j / 2) + 8 (i / 4) + 4 (j % 2) + i % 4, so
+// that a lane ends up with eight consecutive columns of two fragments; lane l
+// holds row l % 16 for experts 32 b + 8 (l / 16) .. + 7, the number and what is left
+// of it. fp32: row i is column 16 j + i, experts 16 b + 4 (l / 16) .. + 3. Pieces
+// [columns / 64][j][b][2 or 1][lane].
+template <typename T>
+__device__ void turn_router(const float* __restrict__ w, int d, int E, int EB, u32x4* __restrict__ out, int i) {
+  constexpr bool kHalves = sizeof(T) == 2;
+  constexpr int V = Piece<T>::V;
+  const int lane = i % 64, BN = kHalves ? EB : 2 * EB, b = i / 64 % BN, j = i / 64 / BN % 4;
+  const int c0 = i / 256 / BN * 64, r = lane & 15, g = lane >> 4;
+  if (c0 >= d) return;
+  const int col = c0 + (kHalves ? 32 * (j / 2) + 8 * (r / 4) + 4 * (j % 2) + r % 4 : 16 * j + r);
+  float v[V];
+#pragma unroll
+  for (int q = 0; q < V; ++q) {
+    const int e = (kHalves ? 32 * b + 8 * g : 16 * b + 4 * g) + q;
+    v[q] = e < E ? w[static_cast<int64_t>(col) * E + e] : 0.0f;
+  }
+  const u32x4 p = Piece<T>::narrow(v);
+  if (!kHalves) {
+    out[i] = p;
+    return;
+  }
+  float back[V];
+  Piece<T>::widen(p, back);
+#pragma unroll
+  for (int q = 0; q < V; ++q) v[q] -= back[q];
+  out[static_cast<int64_t>(i / 64) * 128 + lane] = p;
+  out[static_cast<int64_t>(i / 64) * 128 + 64 + lane] = Piece<T>::narrow(v);
+}
+
 // Workgroups below count_blocks count their share of the tokens; the others
-// lay W out.
+// lay W out, for the backward too where there is a place for it.
 template <typename T>
 __global__ __launch_bounds__(kCountThreads) void balance_count_kernel(const BalArgs a,
                                                                      const int32_t* __restrict__ idx,
                                                                      const float* __restrict__ w, int EB,
                                                                      u32x4* __restrict__ wf,
+                                                                     u32x4* __restrict__ wb,
                                                                      int32_t* __restrict__ parts) {
   constexpr int kWaves = kCountThreads / 64;
   __shared__ int hist[kWaves][65];
   if (static_cast<int>(blockIdx.x) >= a.count_blocks) {
-    split_router<T>(w, a.d, a.E, EB, wf, (blockIdx.x - a.count_blocks) * kCountThreads + threadIdx.x);
+    const int i = (blockIdx.x - a.count_blocks) * kCountThreads + threadIdx.x;
+    split_router<T>(w, a.d, a.E, EB, wf, i);
+    if (wb) turn_router<T>(w, a.d, a.E, EB, wb, i);
     return;
   }
   for (int i = threadIdx.x; i < kWaves * 65; i += kCountThreads) (&hist[0][0])[i] = 0;
@@ -176,49 +213,49 @@ __device__ __forceinline__ void store_dl(float* row, int eb, int, int g, const f
     store4(row + 32 * eb + 8 * r + 4 * g, dl[4 * r], dl[4 * r + 1], dl[4 * r + 2], dl[4 * r + 3]);
 }
 
-// A wave makes the logits of 32 RT tokens: MFMA 32x32 with W first, so a lane
-// ends up with 16 EB experts of token lane % 32 and the lane 32 on with the
-// others. x goes from memory straight into operands (a row's 128 bytes over
-// four loads), W's operands come from the caches, where every wave finds the
-// same. KS waves share a token's columns and are added in order.
-template <typename T, int EB, int RT, int KS, int NW>
-__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(RT == 2 ? 2 : 3)))
-void balance_logits_kernel(const BalArgs a, const T* __restrict__ x, const u32x4* __restrict__ wf,
-                           T* __restrict__ saved) {
-  constexpr int S = BalOp<T>::S, kLine = 128 / sizeof(T), EP = 32 * EB;
-  __shared__ float acc_lds[KS > 1 ? NW : 1][KS > 1 ? 16 * EB * 64 : 1];
-  __shared__ float sums[NW][EP + 1];
-  __shared__ int tallies[NW][65];
-  __shared__ __attribute__((aligned(16))) float share[64];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int g = lane >> 5, r32 = lane & 31;
-  const int slice = wave % KS;
-  const int64_t row0 = (static_cast<int64_t>(blockIdx.x) * (NW / KS) + wave / KS) * 32 * RT;
-  if (saved) {
-    // the loads, for the gradient
-    for (int e = lane; e < 65; e += 64) {
-      int v = 0;
-#pragma unroll 8
-      for (int p = wave; p < a.count_blocks; p += NW) v += a.parts[p * 65 + e];
-      tallies[wave][e] = v;
-    }
-  }
-  f32x16_t acc[RT][EB];
+// The same of eight consecutive experts of token t in one lane.
+__device__ __forceinline__ void store_dl8(bf16_t* saved, int64_t t, int EP, int e0, const float (&dl)[8]) {
+  bf16_t* row = saved + t * 2 * EP + e0;
+  const u32x4 hi = Piece<bf16_t>::narrow(dl);
+  float back[8];
+  Piece<bf16_t>::widen(hi, back);
+#pragma unroll
+  for (int q = 0; q < 8; ++q) back[q] = dl[q] - back[q];
+  *reinterpret_cast<u32x4*>(row) = hi;
+  *reinterpret_cast<u32x4*>(row + EP) = Piece<bf16_t>::narrow(back);
+}
+__device__ __forceinline__ void store_dl8(float* saved, int64_t t, int EP, int e0, const float (&dl)[8]) {
+  float* row = saved + t * EP + e0;
+  store4(row, dl[0], dl[1], dl[2], dl[3]);
+  store4(row + 4, dl[4], dl[5], dl[6], dl[7]);
+}
+
+// Logits of 32 RT tokens from row0 on over lines first, first + step, ...: MFMA
+// 32x32 with W first, so a lane ends up with 16 EB experts of token lane % 32 and
+// the lane 32 further with the others. x goes from memory straight into operands (a
+// row's 128 bytes over four loads), W's operands come from the caches, where every
+// wave finds the same; both are loaded a line ahead, W's each into the place of the
+// one that has just been multiplied.
+template <typename T, int EB, int RT>
+__device__ __forceinline__ void logits(const BalArgs& a, const T* __restrict__ x, const u32x4* __restrict__ wf,
+                                       int64_t row0, int first, int step, f32x16_t (&acc)[RT][EB]) {
+  constexpr int S = BalOp<T>::S, kLine = 128 / sizeof(T);
+  const int lane = threadIdx.x & 63, g = lane >> 5, r32 = lane & 31;
 #pragma unroll
   for (int i = 0; i < RT; ++i)
 #pragma unroll
     for (int b = 0; b < EB; ++b)
 #pragma unroll
       for (int q = 0; q < 16; ++q) acc[i][b][q] = 0.0f;
-
   const int lines = a.d / kLine;
+  if (first >= lines) return;
   const T* rows[RT];
 #pragma unroll
   for (int i = 0; i < RT; ++i) {
     const int64_t r = row0 + 32 * i + r32;
     rows[i] = x + (r < a.T ? r : a.T - 1) * a.d + g * (16 / static_cast<int>(sizeof(T)));
   }
-  u32x4 xv[2][RT][4], wv[2][EB][S];
+  u32x4 xv[2][RT][4], wv[4][EB][S];
   auto load_x = [&](int set, int line) {
 #pragma unroll
     for (int i = 0; i < RT; ++i)
@@ -226,130 +263,164 @@ void balance_logits_kernel(const BalArgs a, const T* __restrict__ x, const u32x4
       for (int q = 0; q < 4; ++q)
         xv[set][i][q] = *reinterpret_cast<const u32x4*>(rows[i] + line * kLine + q * (kLine / 4));
   };
-  auto load_w = [&](int set, int step) {
+  auto load_w = [&](int q, int line) {
 #pragma unroll
     for (int b = 0; b < EB; ++b)
 #pragma unroll
-      for (int s = 0; s < S; ++s) wv[set][b][s] = wf[((static_cast<int64_t>(step) * EB + b) * S + s) * 64 + lane];
+      for (int s = 0; s < S; ++s)
+        wv[q][b][s] = wf[((static_cast<int64_t>(line * 4 + q)) * EB * S + b * S + s) * 64 + lane];
   };
-  auto multiply = [&](int set, int line, int next) {
+  auto multiply = [&](int set, int next) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      load_w((q & 1) ^ 1, q < 3 ? line * 4 + q + 1 : next * 4);
 #pragma unroll
       for (int b = 0; b < EB; ++b)
 #pragma unroll
-        for (int i = 0; i < RT; ++i) BalOp<T>::step(wv[q & 1][b], xv[set][i][q], acc[i][b]);
+        for (int i = 0; i < RT; ++i) BalOp<T>::step(wv[q][b], xv[set][i][q], acc[i][b]);
+      load_w(q, next);
     }
   };
-  if (slice < lines) {
-    load_x(0, slice);
-    load_w(0, slice * 4);
-    for (int line = slice; line < lines; line += 2 * KS) {
-      const int n1 = line + KS < lines ? line + KS : line, n2 = line + 2 * KS < lines ? line + 2 * KS : n1;
-      load_x(1, n1);
-      multiply(0, line, n1);
-      load_x(0, n2);
-      if (line + KS < lines) multiply(1, n1, n2);
+  load_x(0, first);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) load_w(q, first);
+  for (int line = first; line < lines; line += 2 * step) {
+    const int n1 = line + step < lines ? line + step : line, n2 = line + 2 * step < lines ? line + 2 * step : n1;
+    load_x(1, n1);
+    multiply(0, n1);
+    load_x(0, n2);
+    if (line + step < lines) multiply(1, n2);
+  }
+}
+
+// Shares f of the experts and 1 / n from the counts (NT threads, all of them;
+// `share` is whole after the caller's next barrier).
+template <int NT>
+struct Tallies {
+  static constexpr int kWaves = NT / 64, kEach = (kCountBlocks + kWaves - 1) / kWaves;
+  int v[kEach], n[kEach];
+  // The loads, early; the sums when they are needed.
+  __device__ void load(const BalArgs& a) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+    for (int u = 0; u < kEach; ++u) {
+      const int p = wave + u * kWaves, at = (p < a.count_blocks ? p : 0) * 65;
+      v[u] = a.parts[at + lane];
+      n[u] = a.parts[at + 64];
     }
   }
-  if constexpr (KS > 1) {
+  __device__ void put(const BalArgs& a, int (*sums)[65]) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    int c = 0, k = 0;
 #pragma unroll
-    for (int b = 0; b < EB; ++b)
-#pragma unroll
-      for (int q = 0; q < 16; ++q) acc_lds[wave][(b * 16 + q) * 64 + lane] = acc[0][b][q];
-  }
-  __syncthreads();
-  if constexpr (KS > 1) {
-    if (slice == 0) {
-#pragma unroll
-      for (int b = 0; b < EB; ++b)
-#pragma unroll
-        for (int q = 0; q < 16; ++q) {
-          float v = acc_lds[wave][(b * 16 + q) * 64 + lane];
-#pragma unroll
-          for (int s = 1; s < KS; ++s) v += acc_lds[wave + s][(b * 16 + q) * 64 + lane];
-          acc[0][b][q] = v;
-        }
+    for (int u = 0; u < kEach; ++u) {
+      const bool there = wave + u * kWaves < a.count_blocks;
+      c += there ? v[u] : 0;
+      k += there ? n[u] : 0;
     }
+    sums[wave][lane] = c;
+    if (lane == 0) sums[wave][64] = k;
   }
+  // After a barrier: the share of expert `e`, and 1 / n.
+  __device__ static float share(const BalArgs& a, const int (*sums)[65], int e, float* inv_n) {
+    int c = 0, k = 0;
+#pragma unroll
+    for (int u = 0; u < kWaves; ++u) {
+      c += sums[u][e];
+      k += sums[u][64];
+    }
+    *inv_n = k > 0 ? 1.0f / static_cast<float>(k) : 0.0f;
+    return k > 0 ? static_cast<float>(c) / (static_cast<float>(k) * static_cast<float>(a.k)) : 0.0f;
+  }
+};
+
+// Many tokens: 64 a wave, whose softmax stays in the registers that the
+// products leave it in.
+template <typename T, int EB>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2)))
+void balance_logits_kernel(const BalArgs a, const T* __restrict__ x, const u32x4* __restrict__ wf,
+                           T* __restrict__ saved) {
+  constexpr int EP = 32 * EB, RT = 2, NW = 4;
+  __shared__ float sums[NW][EP + 1];
+  __shared__ int tallies[NW][65];
+  __shared__ __attribute__((aligned(16))) float share[65];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int g = lane >> 5, r32 = lane & 31;
+  const int64_t row0 = (static_cast<int64_t>(blockIdx.x) * NW + wave) * 32 * RT;
   float inv_n = 0.0f;
   if (saved) {
-    int n = 0;
-#pragma unroll
-    for (int u = 0; u < NW; ++u) n += tallies[u][64];
-    inv_n = n > 0 ? 1.0f / static_cast<float>(n) : 0.0f;
+    Tallies<64 * NW> t;
+    t.load(a);
+    t.put(a, tallies);
+    __syncthreads();
     if (threadIdx.x < 64) {
-      int v = 0;
-#pragma unroll
-      for (int u = 0; u < NW; ++u) v += tallies[u][threadIdx.x];
-      share[threadIdx.x] = n > 0 ? static_cast<float>(v) / (static_cast<float>(n) * static_cast<float>(a.k)) : 0.0f;
+      share[threadIdx.x] = t.share(a, tallies, threadIdx.x, &inv_n);
+      share[64] = inv_n;
     }
     __syncthreads();
+    inv_n = share[64];
   }
+  f32x16_t acc[RT][EB];
+  logits<T, EB, RT>(a, x, wf, row0, 0, 1, acc);
 
   float psum[EB][16], zsum = 0.0f;
 #pragma unroll
   for (int b = 0; b < EB; ++b)
 #pragma unroll
     for (int q = 0; q < 16; ++q) psum[b][q] = 0.0f;
-  if (slice == 0) {
 #pragma unroll
-    for (int i = 0; i < RT; ++i) {
-      const int64_t t = row0 + 32 * i + r32;
-      const bool keep = kept_token(a, t);
-      float other, most = -__builtin_inff();
+  for (int i = 0; i < RT; ++i) {
+    const int64_t t = row0 + 32 * i + r32;
+    const bool keep = kept_token(a, t);
+    float other, most = -__builtin_inff();
 #pragma unroll
-      for (int b = 0; b < EB; ++b)
+    for (int b = 0; b < EB; ++b)
 #pragma unroll
-        for (int q = 0; q < 16; ++q)
-          if (32 * b + 8 * (q / 4) + 4 * g + q % 4 < a.E) most = fmaxf(most, acc[i][b][q]);
-      most = lane32(most, &other);
-      most = fmaxf(most, other);
-      float p[EB][16], total = 0.0f;
+      for (int q = 0; q < 16; ++q)
+        if (32 * b + 8 * (q / 4) + 4 * g + q % 4 < a.E) most = fmaxf(most, acc[i][b][q]);
+    most = lane32(most, &other);
+    most = fmaxf(most, other);
+    float p[EB][16], total = 0.0f;
 #pragma unroll
-      for (int b = 0; b < EB; ++b)
+    for (int b = 0; b < EB; ++b)
 #pragma unroll
-        for (int q = 0; q < 16; ++q) {
-          p[b][q] = 32 * b + 8 * (q / 4) + 4 * g + q % 4 < a.E ? __expf(acc[i][b][q] - most) : 0.0f;
-          total += p[b][q];
-        }
-      total = lane32(total, &other);
-      total += other;
-      const float inv = 1.0f / total, lse = most + logf(total);
-      float inner = 0.0f;
-#pragma unroll
-      for (int b = 0; b < EB; ++b)
-#pragma unroll
-        for (int q = 0; q < 16; ++q) {
-          p[b][q] *= inv;
-          if (keep) psum[b][q] += p[b][q];
-        }
-      if (keep && g == 0) zsum += lse * lse;
-      if (!saved) continue;
-      float f[EB][16];
-#pragma unroll
-      for (int b = 0; b < EB; ++b)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const float4 v = *reinterpret_cast<const float4*>(share + 32 * b + 8 * r + 4 * g);
-          f[b][4 * r] = v.x; f[b][4 * r + 1] = v.y; f[b][4 * r + 2] = v.z; f[b][4 * r + 3] = v.w;
-        }
-#pragma unroll
-      for (int b = 0; b < EB; ++b)
-#pragma unroll
-        for (int q = 0; q < 16; ++q) inner = __builtin_fmaf(f[b][q], p[b][q], inner);
-      inner = lane32(inner, &other);
-      inner += other;
-      const float zed = a.c2 * lse;
-#pragma unroll
-      for (int b = 0; b < EB; ++b) {
-        float dl[16];
-#pragma unroll
-        for (int q = 0; q < 16; ++q)
-          dl[q] = keep ? p[b][q] * __builtin_fmaf(a.c1, f[b][q] - inner, zed) * inv_n : 0.0f;
-        if (t < a.T) store_dl(saved + t * (sizeof(T) == 2 ? 2 * EP : EP), b, EP, g, dl);
+      for (int q = 0; q < 16; ++q) {
+        p[b][q] = 32 * b + 8 * (q / 4) + 4 * g + q % 4 < a.E ? __expf(acc[i][b][q] - most) : 0.0f;
+        total += p[b][q];
       }
+    total = lane32(total, &other);
+    total += other;
+    const float inv = 1.0f / total, lse = most + logf(total);
+#pragma unroll
+    for (int b = 0; b < EB; ++b)
+#pragma unroll
+      for (int q = 0; q < 16; ++q) {
+        p[b][q] *= inv;
+        if (keep) psum[b][q] += p[b][q];
+      }
+    if (keep && g == 0) zsum += lse * lse;
+    if (!saved) continue;
+    float f[EB][16], inner = 0.0f;
+#pragma unroll
+    for (int b = 0; b < EB; ++b)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float4 v = *reinterpret_cast<const float4*>(share + 32 * b + 8 * r + 4 * g);
+        f[b][4 * r] = v.x; f[b][4 * r + 1] = v.y; f[b][4 * r + 2] = v.z; f[b][4 * r + 3] = v.w;
+      }
+#pragma unroll
+    for (int b = 0; b < EB; ++b)
+#pragma unroll
+      for (int q = 0; q < 16; ++q) inner = __builtin_fmaf(f[b][q], p[b][q], inner);
+    inner = lane32(inner, &other);
+    inner += other;
+    const float zed = a.c2 * lse;
+#pragma unroll
+    for (int b = 0; b < EB; ++b) {
+      float dl[16];
+#pragma unroll
+      for (int q = 0; q < 16; ++q)
+        dl[q] = keep ? p[b][q] * __builtin_fmaf(a.c1, f[b][q] - inner, zed) * inv_n : 0.0f;
+      if (t < a.T) store_dl(saved + t * (sizeof(T) == 2 ? 2 * EP : EP), b, EP, g, dl);
     }
   }
   // sums over the wave's 32 lanes, then over the waves
@@ -358,7 +429,8 @@ void balance_logits_kernel(const BalArgs a, const T* __restrict__ x, const u32x4
 #pragma unroll
     for (int q = 0; q < 16; ++q) {
       float other, v = row16_sum(psum[b][q]);
-      v = lane16(v, &other) + other;
+      v = lane16(v, &other);
+      v += other;
       if (r32 == 0) sums[wave][32 * b + 8 * (q / 4) + 4 * g + q % 4] = v;
     }
   zsum = wave_sum(zsum);
@@ -367,8 +439,115 @@ void balance_logits_kernel(const BalArgs a, const T* __restrict__ x, const u32x4
   if (threadIdx.x <= EP) {
     float v = 0.0f;
 #pragma unroll
-    for (int u = 0; u < NW; u += KS) v += sums[u][threadIdx.x];
+    for (int u = 0; u < NW; ++u) v += sums[u][threadIdx.x];
     // the last one is the sum of lse^2
+    a.stats[static_cast<int64_t>(blockIdx.x) * 65 + (static_cast<int>(threadIdx.x) == EP ? 64 : threadIdx.x)] = v;
+  }
+}
+
+// Fewer tokens: 32 a workgroup, whose KS waves share the columns. Their sums go
+// through LDS, from where the softmax takes eight experts of a token a lane,
+// 4 EB lanes to a token, so that all waves work on it.
+template <typename T, int EB, int KS>
+__global__ __launch_bounds__(64 * KS) void balance_logits_few_kernel(const BalArgs a, const T* __restrict__ x,
+                                                                     const u32x4* __restrict__ wf,
+                                                                     T* __restrict__ saved) {
+  constexpr int EP = 32 * EB, L = 4 * EB, kTokens = 64 / L, kPitch = 66;
+  constexpr int kUsed = 32 / kTokens < KS ? 32 / kTokens : KS, kPasses = 32 / kTokens / kUsed;
+  __shared__ float part[KS][16 * EB * kPitch];
+  __shared__ float sums[KS][EP + 1];
+  __shared__ int tallies[KS][65];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * 32;
+  Tallies<64 * KS> counts;
+  if (saved) counts.load(a);
+  f32x16_t acc[1][EB];
+  logits<T, EB, 1>(a, x, wf, row0, wave, KS, acc);
+  if (saved) counts.put(a, tallies);
+#pragma unroll
+  for (int b = 0; b < EB; ++b)
+#pragma unroll
+    for (int q = 0; q < 16; ++q) part[wave][(b * 16 + q) * kPitch + lane] = acc[0][b][q];
+  __syncthreads();
+  // lane: eight experts e0.. of a token
+  const int m = lane % L, e0 = 8 * m;
+  float psum[8], zsum = 0.0f, f[8], inv_n = 0.0f;
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    psum[q] = 0.0f;
+    f[q] = saved ? counts.share(a, tallies, e0 + q, &inv_n) : 0.0f;
+  }
+  // a sum over the lanes of a token, and over those of an octet of experts
+  auto over_token = [&](float v) {
+    v += dpp<0xb1>(v);  // lane ^ 1
+    v += dpp<0x4e>(v);  // lane ^ 2
+    if (L == 8) v += dpp<0x141>(v);  // half row mirrored
+    return v;
+  };
+#pragma unroll
+  for (int pass = 0; pass < kPasses; ++pass) {
+    if (wave >= kUsed) break;
+    const int tok = (pass * kUsed + wave) * kTokens + lane / L;
+    const int64_t t = row0 + tok;
+    const bool keep = kept_token(a, t);
+    float v[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      // expert e0 + q of the products' layout: register 16 (m / 4) + 4 (m % 4) + q % 4, lane 32 (q / 4) + tok
+      const int at = (4 * m + q % 4) * kPitch + 32 * (q / 4) + tok;
+      v[q] = part[0][at];
+#pragma unroll
+      for (int s = 1; s < KS; ++s) v[q] += part[s][at];
+    }
+    float most = -__builtin_inff();
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      if (e0 + q < a.E) most = fmaxf(most, v[q]);
+    most = fmaxf(most, dpp<0xb1>(most));
+    most = fmaxf(most, dpp<0x4e>(most));
+    if (L == 8) most = fmaxf(most, dpp<0x141>(most));
+    float p[8], total = 0.0f;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      p[q] = e0 + q < a.E ? __expf(v[q] - most) : 0.0f;
+      total += p[q];
+    }
+    total = over_token(total);
+    const float inv = 1.0f / total, lse = most + logf(total);
+    float inner = 0.0f;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      p[q] *= inv;
+      if (keep) psum[q] += p[q];
+      inner = __builtin_fmaf(f[q], p[q], inner);
+    }
+    if (keep && m == 0) zsum += lse * lse;
+    if (!saved) continue;
+    inner = over_token(inner);
+    const float zed = a.c2 * lse;
+    float dl[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) dl[q] = keep ? p[q] * __builtin_fmaf(a.c1, f[q] - inner, zed) * inv_n : 0.0f;
+    if (t < a.T) store_dl8(saved, t, EP, e0, dl);
+  }
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    float other, s = psum[q];
+    if (L == 4) s += dpp<0x141>(dpp<0x1b>(s));  // lane ^ 4: quad reversed, half row mirrored
+    s += dpp<0x128>(s);  // lane ^ 8: row rotated by eight
+    s = lane16(s, &other);
+    s += other;
+    s = lane32(s, &other);
+    s += other;
+    if (lane < L) sums[wave][e0 + q] = s;
+  }
+  zsum = wave_sum(zsum);
+  if (lane == 0) sums[wave][EP] = zsum;
+  __syncthreads();
+  if (threadIdx.x <= EP) {
+    float v = 0.0f;
+#pragma unroll
+    for (int u = 0; u < kUsed; ++u) v += sums[u][threadIdx.x];
     a.stats[static_cast<int64_t>(blockIdx.x) * 65 + (static_cast<int>(threadIdx.x) == EP ? 64 : threadIdx.x)] = v;
   }
 }
@@ -439,43 +618,30 @@ constexpr int kGradCols = 128, kGradSets = 4, kGradThreads = 512;
 
 struct BalGradArgs {
   int64_t T;
-  int E, d;
+  int d;
   int ranges;          // of the tokens: a partial dW each
   const uint8_t* mask;
   const float* gloss;  // or null
   bool add;
 };
 
-// W of a wave's 64 columns as the first operand of dx = dl W^T, and dl's LDS rows.
+// W of a wave's 64 columns (turn_router) and dl's LDS rows.
 template <typename T, int EB>
 struct BalGrad;
 
 template <int EB>
 struct BalGrad<bf16_t, EB> {
   static constexpr int EP = 32 * EB, ROW = 4 * EP;  // bytes of a token: high halves, then low
-  // Fragment j's row i is column 32 (j / 2) + 8 (i / 4) + 4 (j % 2) + i % 4: a
-  // lane ends up with eight consecutive columns of two fragments.
   u32x4 hi[4][EB], lo[4][EB];
-  __device__ void load(const float* w, int c0, int E, int lane) {
-    const int i = lane & 15, g = lane >> 4;
+  __device__ void load(const u32x4* wb, int c0, int lane) {
+    const u32x4* p = wb + static_cast<int64_t>(c0 / 64) * 4 * EB * 128 + lane;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float* row = w + static_cast<int64_t>(c0 + 32 * (j / 2) + 8 * (i / 4) + 4 * (j % 2) + i % 4) * E;
+    for (int j = 0; j < 4; ++j)
 #pragma unroll
       for (int b = 0; b < EB; ++b) {
-        float v[8], back[8];
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const int e = 32 * b + 8 * g + q;
-          v[q] = e < E ? row[e] : 0.0f;
-        }
-        hi[j][b] = Piece<bf16_t>::narrow(v);
-        Piece<bf16_t>::widen(hi[j][b], back);
-#pragma unroll
-        for (int q = 0; q < 8; ++q) v[q] -= back[q];
-        lo[j][b] = Piece<bf16_t>::narrow(v);
+        hi[j][b] = p[(j * EB + b) * 128];
+        lo[j][b] = p[(j * EB + b) * 128 + 64];
       }
-    }
   }
   // 16-byte chunk c of token row r: spread over the banks
   __device__ static int at(int r, int c) { return r * ROW + ((c ^ (r & (ROW / 16 - 1))) << 4); }
@@ -530,20 +696,15 @@ struct BalGrad<bf16_t, EB> {
 template <int EB>
 struct BalGrad<float, EB> {
   static constexpr int EP = 32 * EB, ROW = 4 * EP;
-  // Fragment j's row i is column 16 j + i; step s takes element s % 4 of the lane
-  // groups' 16 bytes s / 4 on both sides: experts 16 (s / 4) + 4 (lane / 16) + s % 4.
-  float w[4][2 * EB][4];
-  __device__ void load(const float* src, int c0, int E, int lane) {
-    const int i = lane & 15, g = lane >> 4;
+  // Step s takes element s % 4 of the lane groups' 16 bytes s / 4 on both sides:
+  // experts 16 (s / 4) + 4 (lane / 16) + s % 4.
+  f32x4_t w[4][2 * EB];
+  __device__ void load(const u32x4* wb, int c0, int lane) {
+    const u32x4* p = wb + static_cast<int64_t>(c0 / 64) * 8 * EB * 64 + lane;
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int b = 0; b < 2 * EB; ++b)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int e = 16 * b + 4 * g + q;
-          w[j][b][q] = e < E ? src[static_cast<int64_t>(c0 + 16 * j + i) * E + e] : 0.0f;
-        }
+      for (int b = 0; b < 2 * EB; ++b) w[j][b] = __builtin_bit_cast(f32x4_t, p[(j * 2 * EB + b) * 64]);
   }
   __device__ static int at(int r, int c) { return r * ROW + ((c ^ (r & (ROW / 16 - 1))) << 4); }
   // v[h]: columns c0 + 16 (2 h) + 4 (lane / 16) .. + 3, then 16 further on
@@ -586,25 +747,40 @@ struct BalGrad<float, EB> {
   __device__ static int expert(int m, int q, int lane) { return 2 * EB * (4 * (lane >> 4) + q) + m; }
 };
 
-// Tokens of x that the mask leaves out, zeroed: they may hold NaN.
-__device__ __forceinline__ void drop_tokens(SkinnyW<bf16_t>& x, const uint8_t* mask, int64_t t0, int64_t T, int lane) {
+// x of 32 tokens from `rows` on (`left` of them there) and the four columns of
+// a lane, without a branch: tokens past the last are read as the last.
+__device__ __forceinline__ void load_tokens(SkinnyW<bf16_t>& x, const bf16_t* rows, int d, int left, int col, int lane) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const int64_t t = t0 + 8 * (lane >> 4) + i;
-    if (t < T && !mask[t]) x.r[i] = (u32x2){0u, 0u};
+    const uint32_t r = min(8 * (lane >> 4) + i, left - 1);
+    x.r[i] = *reinterpret_cast<const u32x2*>(rows + (r * d + col));
   }
 }
-__device__ __forceinline__ void drop_tokens(SkinnyW<float>& x, const uint8_t* mask, int64_t t0, int64_t T, int lane) {
+__device__ __forceinline__ void load_tokens(SkinnyW<float>& x, const float* rows, int d, int left, int col, int lane) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const int64_t t = t0 + 4 * i + (lane >> 4);
-    if (t < T && !mask[t]) x.r[i] = (u32x4){0u, 0u, 0u, 0u};
+    const uint32_t r = min(4 * i + (lane >> 4), left - 1);
+    x.r[i] = *reinterpret_cast<const u32x4*>(rows + (r * d + col));
   }
+}
+// Zeros for the tokens that are not there or that the mask leaves out (they
+// may hold NaN): a byte a token in LDS, all ones or zeros.
+__device__ __forceinline__ void drop_tokens(SkinnyW<bf16_t>& x, const char* keep, int lane) {
+  const uint2 k = *reinterpret_cast<const uint2*>(keep + 8 * (lane >> 4));
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int word = static_cast<int>(i < 4 ? k.x : k.y);
+    x.r[i] &= static_cast<uint32_t>((word << (24 - 8 * (i % 4))) >> 24);
+  }
+}
+__device__ __forceinline__ void drop_tokens(SkinnyW<float>& x, const char* keep, int lane) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x.r[i] &= static_cast<uint32_t>(static_cast<int>(keep[4 * i + (lane >> 4)]));
 }
 
 template <typename T, int EB>
 __global__ __launch_bounds__(kGradThreads) __attribute__((amdgpu_waves_per_eu(2)))
-void balance_grad_kernel(const BalGradArgs a, const T* __restrict__ x, const float* __restrict__ w,
+void balance_grad_kernel(const BalGradArgs a, const T* __restrict__ x, const u32x4* __restrict__ wb,
                          const T* __restrict__ saved, T* dx, float* __restrict__ partial) {
   typedef BalGrad<T, EB> G;
   constexpr int EP = 32 * EB, kPieces = 32 * G::ROW / 16;       // 16-byte pieces of 32 tokens
@@ -614,6 +790,7 @@ void balance_grad_kernel(const BalGradArgs a, const T* __restrict__ x, const flo
   // the sums of three sets, a quarter at a time, share the place
   constexpr int kSums = (kGradSets - 1) * 2 * 2 * EB * 4 * 64 * 4;
   __shared__ __attribute__((aligned(1024))) char smem[2 * kBuf > kSums ? 2 * kBuf : kSums];
+  __shared__ __attribute__((aligned(16))) char kept[2][kGradSets * 32];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int set = wave / 2;
   const int slices = a.d / kGradCols;
@@ -623,41 +800,52 @@ void balance_grad_kernel(const BalGradArgs a, const T* __restrict__ x, const flo
   const int64_t k0 = chunks * range / a.ranges, k1 = chunks * (range + 1) / a.ranges;
   const float scale = a.gloss ? a.gloss[0] : 1.0f;
   G weights;
-  weights.load(w, c0, a.E, lane);
+  weights.load(wb, c0, lane);
   f32x4_t acc[4][2 * EB];
 #pragma unroll
   for (int j = 0; j < 4; ++j)
 #pragma unroll
     for (int m = 0; m < 2 * EB; ++m) acc[j][m] = (f32x4_t){0.0f, 0.0f, 0.0f, 0.0f};
 
+  // dl of the next chunks, a token's 16-byte pieces side by side, and whether a
+  // token counts; tokens past the end and chunks past the range as zeros
   u32x4 dl[kLoads];
-  // tokens past the end, and chunks past the range, as zeros
+  uint32_t keep = 0;  // 0: no
   auto load_dl = [&](int64_t k) {
 #pragma unroll
     for (int u = 0; u < kLoads; ++u) {
       const int i = u * kGradThreads + threadIdx.x, r = i % kPieces / (G::ROW / 16);
-      const int64_t chunk = k + i / kPieces, t = chunk * 32 + r;
-      dl[u] = (u32x4){0u, 0u, 0u, 0u};
-      if (chunk < k1 && t < a.T)
-        dl[u] = *reinterpret_cast<const u32x4*>(reinterpret_cast<const char*>(saved) + t * G::ROW + i % (G::ROW / 16) * 16);
+      const int64_t t = (k + i / kPieces) * 32 + r;
+      const bool there = k + i / kPieces < k1 && t < a.T;
+      const u32x4 v = *reinterpret_cast<const u32x4*>(reinterpret_cast<const char*>(saved) +
+                                                      (there ? t : 0) * G::ROW + i % (G::ROW / 16) * 16);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) dl[u][q] = there ? v[q] : 0u;
+    }
+    if (threadIdx.x < kGradSets * 32) {
+      const int64_t t = k * 32 + threadIdx.x;
+      keep = t < a.T;
+      if (a.mask && t < a.T) keep = a.mask[t];
     }
   };
-  auto store_lds = [&](char* buf) {
+  auto store_lds = [&](int to) {
+    char* buf = smem + to * kBuf;
 #pragma unroll
     for (int u = 0; u < kLoads; ++u) {
       const int i = u * kGradThreads + threadIdx.x, r = i % kPieces / (G::ROW / 16);
       *reinterpret_cast<u32x4*>(buf + i / kPieces * 32 * G::ROW + G::at(r, i % (G::ROW / 16))) = dl[u];
     }
+    if (threadIdx.x < kGradSets * 32) kept[to][threadIdx.x] = keep ? '\xff' : '\0';
   };
-  SkinnyW<T> xv[2];
-  auto load_x = [&](int to, int64_t k) {
-    const int64_t chunk = k + set, t0 = chunk * 32;
-    // rows from t0 on, none past the range or the end
-    const int64_t left = chunk < k1 ? a.T - t0 : 0;
-    xv[to].load(x + t0 * a.d, a.d, 0, static_cast<int>(left < 32 ? left : 32), c0 + 4 * (lane & 15), a.d, lane);
-    if (a.mask && left > 0) drop_tokens(xv[to], a.mask, t0, a.T, lane);
+  SkinnyW<T> xv;
+  auto load_x = [&](int64_t k) {
+    // a chunk past the range: the last one again, not used
+    const int64_t t0 = min(k + set, chunks - 1) * 32;
+    const int left = static_cast<int>(a.T - t0 < 32 ? a.T - t0 : 32);
+    load_tokens(xv, x + t0 * a.d, a.d, left, c0 + 4 * (lane & 15), lane);
   };
-  auto work = [&](int from, const char* lds, int64_t k) {
+  auto work = [&](int from, int64_t k) {
+    const char* lds = smem + from * kBuf + set * 32 * G::ROW;
     const int64_t t0 = (k + set) * 32;
     if (k + set < k1) {
 #pragma unroll
@@ -682,24 +870,22 @@ void balance_grad_kernel(const BalGradArgs a, const T* __restrict__ x, const flo
             *reinterpret_cast<u32x4*>(row + c) = Piece<T>::narrow(e);
           }
       }
-      G::dw(lds, xv[from], lane, acc);
+      drop_tokens(xv, kept[from] + 32 * set, lane);
+      G::dw(lds, xv, lane, acc);
     }
   };
   load_dl(k0);
-  load_x(0, k0);
-  store_lds(smem);
+  load_x(k0);
+  store_lds(0);
   __syncthreads();
-  for (int64_t k = k0; k < k1; k += 2 * kGradSets) {
-    // buffers in turn; the other one was last read before the last barrier
+  // buffers in turn: the one that is written was last read before the last
+  // barrier; x of the next tokens is on its way through the barrier and dx
+  int buf = 0;
+  for (int64_t k = k0; k < k1; k += kGradSets, buf ^= 1) {
     load_dl(k + kGradSets);
-    load_x(1, k + kGradSets);
-    work(0, smem + set * 32 * G::ROW, k);
-    store_lds(smem + kBuf);
-    __syncthreads();
-    load_dl(k + 2 * kGradSets);
-    load_x(0, k + 2 * kGradSets);
-    work(1, smem + kBuf + set * 32 * G::ROW, k + kGradSets);
-    store_lds(smem);
+    work(buf, k);
+    load_x(k + kGradSets);
+    store_lds(buf ^ 1);
     __syncthreads();
   }
   // the sets' sums in order, a fragment of columns at a time, then out
@@ -808,14 +994,19 @@ BalLayout bal_layout(const moe_balance& b) {
   return L;
 }
 
+// Bytes of dl in `saved`; W for the backward is behind it.
+size_t saved_rows_bytes(const moe_balance& b) {
+  return align_up(static_cast<size_t>(b.tokens) * 32 * expert_blocks(b.experts) * 4, 256);
+}
+
 template <typename T, int EB>
 void launch_logits(const BalArgs& a, const T* x, const u32x4* wf, T* saved, hipStream_t s) {
   const int rows = logits_rows(a.T);
   const dim3 grid(static_cast<unsigned>((a.T + rows - 1) / rows));
   if (rows == 256)
-    MOE_LAUNCH("balance_logits", (balance_logits_kernel<T, EB, 2, 1, 4>), grid, dim3(256), 0, s, a, x, wf, saved);
+    MOE_LAUNCH("balance_logits", (balance_logits_kernel<T, EB>), grid, dim3(256), 0, s, a, x, wf, saved);
   else
-    MOE_LAUNCH("balance_logits", (balance_logits_kernel<T, EB, 1, 4, 4>), grid, dim3(256), 0, s, a, x, wf, saved);
+    MOE_LAUNCH("balance_logits", (balance_logits_few_kernel<T, EB, 4>), grid, dim3(256), 0, s, a, x, wf, saved);
 }
 
 template <typename T>
@@ -826,6 +1017,7 @@ hipError_t balance_t(const moe_balance& b, const void* x, const float* w, const 
   const int EB = expert_blocks(b.experts);
   int32_t* parts = reinterpret_cast<int32_t*>(W + L.parts);
   u32x4* wf = reinterpret_cast<u32x4*>(W + L.wf);
+  u32x4* wb = saved ? reinterpret_cast<u32x4*>(static_cast<char*>(saved) + saved_rows_bytes(b)) : nullptr;
   BalArgs a{b.tokens, b.experts, b.top_k, b.d_model, b.balance * static_cast<float>(b.experts), 2.0f * b.z, mask,
             parts, 0, reinterpret_cast<float*>(W + L.stats)};
   int groups = 0;
@@ -835,7 +1027,7 @@ hipError_t balance_t(const moe_balance& b, const void* x, const float* w, const 
     const int pieces = b.d_model / (2 * Piece<T>::V) * EB * 64;
     MOE_LAUNCH("balance_count", balance_count_kernel<T>,
                dim3(a.count_blocks + (pieces + kCountThreads - 1) / kCountThreads), dim3(kCountThreads), 0, s, a, idx,
-               w, EB, wf, parts);
+               w, EB, wf, wb, parts);
     if (EB == 1) launch_logits<T, 1>(a, static_cast<const T*>(x), wf, static_cast<T*>(saved), s);
     else launch_logits<T, 2>(a, static_cast<const T*>(x), wf, static_cast<T*>(saved), s);
     groups = static_cast<int>((b.tokens + logits_rows(b.tokens) - 1) / logits_rows(b.tokens));
@@ -846,13 +1038,14 @@ hipError_t balance_t(const moe_balance& b, const void* x, const float* w, const 
 }
 
 template <typename T, int EB>
-hipError_t balance_bwd_t(const moe_balance& b, const void* x, const float* w, const uint8_t* mask, const void* saved,
+hipError_t balance_bwd_t(const moe_balance& b, const void* x, const uint8_t* mask, const void* saved,
                          const float* gloss, bool add, void* dx, float* dw, void* ws, hipStream_t s) {
   const int ranges = grad_ranges(b), EP = 32 * EB;
   float* partial = reinterpret_cast<float*>(static_cast<char*>(ws) + bal_layout(b).partial);
-  const BalGradArgs a{b.tokens, b.experts, b.d_model, ranges, mask, gloss, add};
+  const BalGradArgs a{b.tokens, b.d_model, ranges, mask, gloss, add};
+  const u32x4* wb = reinterpret_cast<const u32x4*>(static_cast<const char*>(saved) + saved_rows_bytes(b));
   MOE_LAUNCH("balance_grad", (balance_grad_kernel<T, EB>), dim3(b.d_model / kGradCols * ranges), dim3(kGradThreads), 0, s, a,
-             static_cast<const T*>(x), w, static_cast<const T*>(saved), static_cast<T*>(dx), partial);
+             static_cast<const T*>(x), wb, static_cast<const T*>(saved), static_cast<T*>(dx), partial);
   MOE_LAUNCH("balance_sum", balance_sum_kernel, dim3(b.d_model * EP / 4 / 16), dim3(256), 0, s, partial, ranges,
              b.d_model, b.experts, EP, gloss, add, dw);
   return hipGetLastError();
@@ -862,8 +1055,7 @@ hipError_t balance_bwd_t(const moe_balance& b, const void* x, const float* w, co
 
 size_t balance_ws_bytes(const moe_balance& b) { return bal_layout(b).total; }
 size_t balance_saved_bytes(const moe_balance& b) {
-  const size_t n = align_up(static_cast<size_t>(b.tokens) * 32 * expert_blocks(b.experts) * 4, 256);
-  return n ? n : 256;
+  return saved_rows_bytes(b) + static_cast<size_t>(b.d_model) * 32 * expert_blocks(b.experts) * 4;
 }
 
 hipError_t launch_balance(const moe_balance& b, const void* x, const float* w, const int32_t* idx,
@@ -873,8 +1065,8 @@ hipError_t launch_balance(const moe_balance& b, const void* x, const float* w, c
                              : balance_t<float>(b, x, w, idx, mask, counts, mean_prob, loss, saved, ws, s);
 }
 
-hipError_t launch_balance_bwd(const moe_balance& b, const void* x, const float* w, const uint8_t* mask,
-                              const void* saved, const float* gloss, bool add, void* dx, float* dw, void* ws,
+hipError_t launch_balance_bwd(const moe_balance& b, const void* x, const uint8_t* mask, const void* saved,
+                              const float* gloss, bool add, void* dx, float* dw, void* ws,
                               hipStream_t s) {
   if (b.tokens == 0) {
     const int64_t n = static_cast<int64_t>(b.d_model) * b.experts;
@@ -884,10 +1076,10 @@ hipError_t launch_balance_bwd(const moe_balance& b, const void* x, const float* 
   }
   const bool wide = expert_blocks(b.experts) == 2;
   if (b.dtype == MOE_BF16)
-    return wide ? balance_bwd_t<bf16_t, 2>(b, x, w, mask, saved, gloss, add, dx, dw, ws, s)
-                : balance_bwd_t<bf16_t, 1>(b, x, w, mask, saved, gloss, add, dx, dw, ws, s);
-  return wide ? balance_bwd_t<float, 2>(b, x, w, mask, saved, gloss, add, dx, dw, ws, s)
-              : balance_bwd_t<float, 1>(b, x, w, mask, saved, gloss, add, dx, dw, ws, s);
+    return wide ? balance_bwd_t<bf16_t, 2>(b, x, mask, saved, gloss, add, dx, dw, ws, s)
+                : balance_bwd_t<bf16_t, 1>(b, x, mask, saved, gloss, add, dx, dw, ws, s);
+  return wide ? balance_bwd_t<float, 2>(b, x, mask, saved, gloss, add, dx, dw, ws, s)
+              : balance_bwd_t<float, 1>(b, x, mask, saved, gloss, add, dx, dw, ws, s);
 }
 
 }  // namespace moe

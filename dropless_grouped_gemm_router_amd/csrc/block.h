@@ -178,8 +178,8 @@ size_t balance_saved_bytes(const moe_balance& b);
 hipError_t launch_balance(const moe_balance& b, const void* x, const float* w, const int32_t* idx,
                           const uint8_t* mask, int32_t* counts, float* mean_prob, float* loss,
                           void* saved, void* ws, hipStream_t s);
-hipError_t launch_balance_bwd(const moe_balance& b, const void* x, const float* w,
-                              const uint8_t* mask, const void* saved, const float* gloss, bool add,
+hipError_t launch_balance_bwd(const moe_balance& b, const void* x, const uint8_t* mask,
+                              const void* saved, const float* gloss, bool add,
                               void* dx, float* dw, void* ws, hipStream_t s);
 
 }  // namespace moe

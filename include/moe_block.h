@@ -382,8 +382,9 @@ typedef struct {
 size_t moe_balance_workspace_bytes(const moe_balance* b);
 
 /* Bytes (host) of the buffer that moe_balance_loss fills for
- * moe_balance_loss_bwd: the gradient of loss[0] by the logits, in fp32 or, in
- * bf16, as sums of two bf16 numbers (2^-17). 0 for an invalid problem. */
+ * moe_balance_loss_bwd: the gradient of loss[0] by the logits and the router's
+ * matrix, in fp32 or, in bf16, as sums of two bf16 numbers (2^-17). 0 for an
+ * invalid problem. */
 size_t moe_balance_saved_bytes(const moe_balance* b);
 
 /*
@@ -400,8 +401,8 @@ int moe_balance_loss(const moe_balance* b, const void* x, const float* w_router,
 
 /*
  * Backward of grad_loss[0] loss[0] with the counts held fixed (grad_loss: one
- * fp32 number on the device, or NULL: 1), for the x, w_router and mask of the
- * forward call that filled saved:
+ * fp32 number on the device, or NULL: 1), for the x and mask of the forward call
+ * that filled saved, which holds the w_router of that call:
  *   dl[t,e] = p[t,e] (balance experts (f_e - sum_j f_j p[t,j]) + 2 z logsumexp_t) / n,
  *   f = counts / (n top_k), 0 for tokens that the mask leaves out
  *   grad_x = dl w_router^T, grad_router = x^T dl
@@ -409,10 +410,10 @@ int moe_balance_loss(const moe_balance* b, const void* x, const float* w_router,
  * zeroed); add = 1: both are added to what is there, the layer's own
  * gradients for instance (moe_bwd), rounded once.
  */
-int moe_balance_loss_bwd(const moe_balance* b, const void* x, const float* w_router,
-                         const uint8_t* mask, const void* saved, const float* grad_loss, int add,
-                         void* grad_x, float* grad_router, void* workspace,
-                         size_t workspace_bytes, void* stream);
+int moe_balance_loss_bwd(const moe_balance* b, const void* x, const uint8_t* mask,
+                         const void* saved, const float* grad_loss, int add, void* grad_x,
+                         float* grad_router, void* workspace, size_t workspace_bytes,
+                         void* stream);
 
 #ifdef __cplusplus
 }

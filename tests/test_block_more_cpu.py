@@ -191,7 +191,7 @@ def bal(tokens=100, experts=8, top_k=2, d=512, dtype=1, balance=0.01, z=0.001):
 def test_balance_problem_refusals(kw, code):
     b = bal(**kw)
     refused(code, K.moe_balance_loss, b, A, C, D, E, F, G, H, A, C, stream=0)
-    refused(code, K.moe_balance_loss_bwd, b, A, C, D, E, F, False, G, H, A, stream=0)
+    refused(code, K.moe_balance_loss_bwd, b, A, C, D, E, False, G, H, A, stream=0)
     assert K.moe_balance_workspace_bytes(b) == K.moe_balance_saved_bytes(b) == 0
 
 
@@ -205,12 +205,12 @@ def test_balance_argument_refusals():
     refused(INV, fwd, bal(), A, C, D, E, F, G, H, ODD16, C, workspace_bytes=big, stream=0)
     need = K.moe_balance_workspace_bytes(bal())
     refused(WS, fwd, bal(), *args, workspace_bytes=need - 1, stream=0)
-    args = [A, C, D, E, F, False, G, H, A]
-    for a in each(args, None, skip=(2, 4, 5)):
+    args = [A, C, D, E, False, F, G, H]
+    for a in each(args, None, skip=(1, 3, 4)):
         refused(INV, bwd, bal(), *a, workspace_bytes=big, stream=0)
-    for a in each(args, ODD2, skip=(2, 5)):
+    for a in each(args, ODD2, skip=(1, 4)):
         refused(INV, bwd, bal(), *a, workspace_bytes=big, stream=0)
-    refused(INV, bwd, bal(), A, C, D, E, F, 2, G, H, A, workspace_bytes=big, stream=0)
+    refused(INV, bwd, bal(), A, C, D, E, 2, F, G, H, workspace_bytes=big, stream=0)
     refused(WS, bwd, bal(), *args, workspace_bytes=need - 1, stream=0)
     assert K.moe_balance_saved_bytes(bal()) >= 100 * 32 * 4
     assert K.moe_balance_saved_bytes(bal(experts=33)) >= 100 * 64 * 4
