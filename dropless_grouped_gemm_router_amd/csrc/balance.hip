@@ -24,7 +24,7 @@ namespace moe {
 
 namespace {
 
-constexpr int kCountBlocks = 32, kCountThreads = 1024;
+constexpr int kCountBlocks = 64, kCountThreads = 1024;
 
 // Experts are padded to 32 or 64: EB blocks of 32.
 inline int expert_blocks(int E) { return E <= 32 ? 1 : 2; }
@@ -34,7 +34,7 @@ struct BalArgs {
   int E, k, d;
   float c1, c2;           // balance * E, 2 * z
   const uint8_t* mask;    // or null
-  const int32_t* parts;   // [count_blocks][65]: counts by expert, kept tokens
+  const int32_t* parts;   // [kCountBlocks][64] counts by expert, [kCountBlocks] kept tokens
   int count_blocks;
   float* stats;           // [workgroups][65]: sums of p by expert, of lse^2
 };
@@ -152,7 +152,7 @@ __global__ __launch_bounds__(kCountThreads) void balance_count_kernel(const BalA
     int v = 0;
 #pragma unroll
     for (int u = 0; u < kWaves; ++u) v += hist[u][threadIdx.x];
-    parts[blockIdx.x * 65 + threadIdx.x] = v;
+    parts[threadIdx.x < 64 ? blockIdx.x * 64 + threadIdx.x : kCountBlocks * 64 + blockIdx.x] = v;
   }
 }
 
@@ -230,38 +230,29 @@ __device__ __forceinline__ void store_dl8(float* saved, int64_t t, int EP, int e
   store4(row + 4, dl[4], dl[5], dl[6], dl[7]);
 }
 
-// Logits of 32 RT tokens from row0 on over lines first, first + step, ...: MFMA
-// 32x32 with W first, so a lane ends up with 16 EB experts of token lane % 32 and
-// the lane 32 further with the others. x goes from memory straight into operands (a
-// row's 128 bytes over four loads), W's operands come from the caches, where every
-// wave finds the same; both are loaded a line ahead, W's each into the place of the
-// one that has just been multiplied.
-template <typename T, int EB, int RT>
+// Logits of 32 tokens from row0 on over lines first, first + step, ...: MFMA 32x32
+// with W first, so a lane ends up with 16 EB experts of token lane % 32 and the lane
+// 32 further with the others. x goes from memory straight into operands (a row's
+// 128 bytes over four loads), W's operands come from the caches; both are loaded
+// a line ahead, W's each into the place of the one that has just been multiplied.
+template <typename T, int EB>
 __device__ __forceinline__ void logits(const BalArgs& a, const T* __restrict__ x, const u32x4* __restrict__ wf,
-                                       int64_t row0, int first, int step, f32x16_t (&acc)[RT][EB]) {
+                                       int64_t row0, int first, int step, f32x16_t (&acc)[EB]) {
   constexpr int S = BalOp<T>::S, kLine = 128 / sizeof(T);
   const int lane = threadIdx.x & 63, g = lane >> 5, r32 = lane & 31;
 #pragma unroll
-  for (int i = 0; i < RT; ++i)
+  for (int b = 0; b < EB; ++b)
 #pragma unroll
-    for (int b = 0; b < EB; ++b)
-#pragma unroll
-      for (int q = 0; q < 16; ++q) acc[i][b][q] = 0.0f;
+    for (int q = 0; q < 16; ++q) acc[b][q] = 0.0f;
   const int lines = a.d / kLine;
   if (first >= lines) return;
-  const T* rows[RT];
-#pragma unroll
-  for (int i = 0; i < RT; ++i) {
-    const int64_t r = row0 + 32 * i + r32;
-    rows[i] = x + (r < a.T ? r : a.T - 1) * a.d + g * (16 / static_cast<int>(sizeof(T)));
-  }
-  u32x4 xv[2][RT][4], wv[4][EB][S];
+  const int64_t r = row0 + r32;
+  const T* row = x + (r < a.T ? r : a.T - 1) * a.d + g * (16 / static_cast<int>(sizeof(T)));
+  u32x4 xv[2][4], wv[4][EB][S];
   auto load_x = [&](int set, int line) {
 #pragma unroll
-    for (int i = 0; i < RT; ++i)
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        xv[set][i][q] = *reinterpret_cast<const u32x4*>(rows[i] + line * kLine + q * (kLine / 4));
+    for (int q = 0; q < 4; ++q)
+      xv[set][q] = *reinterpret_cast<const u32x4*>(row + line * kLine + q * (kLine / 4));
   };
   auto load_w = [&](int q, int line) {
 #pragma unroll
@@ -270,68 +261,148 @@ __device__ __forceinline__ void logits(const BalArgs& a, const T* __restrict__ x
       for (int s = 0; s < S; ++s)
         wv[q][b][s] = wf[((static_cast<int64_t>(line * 4 + q)) * EB * S + b * S + s) * 64 + lane];
   };
-  auto multiply = [&](int set, int next) {
+  auto multiply = [&](int set, bool more, int next) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
 #pragma unroll
-      for (int b = 0; b < EB; ++b)
-#pragma unroll
-        for (int i = 0; i < RT; ++i) BalOp<T>::step(wv[q][b], xv[set][i][q], acc[i][b]);
-      load_w(q, next);
+      for (int b = 0; b < EB; ++b) BalOp<T>::step(wv[q][b], xv[set][q], acc[b]);
+      if (more) load_w(q, next);
     }
   };
   load_x(0, first);
 #pragma unroll
   for (int q = 0; q < 4; ++q) load_w(q, first);
   for (int line = first; line < lines; line += 2 * step) {
-    const int n1 = line + step < lines ? line + step : line, n2 = line + 2 * step < lines ? line + 2 * step : n1;
-    load_x(1, n1);
-    multiply(0, n1);
-    load_x(0, n2);
-    if (line + step < lines) multiply(1, n2);
+    const int n1 = line + step, n2 = line + 2 * step;
+    if (n1 < lines) load_x(1, n1);
+    multiply(0, n1 < lines, n1);
+    if (n1 >= lines) break;
+    if (n2 < lines) load_x(0, n2);
+    multiply(1, n2 < lines, n2);
   }
 }
 
-// Shares f of the experts and 1 / n from the counts (NT threads, all of them;
-// `share` is whole after the caller's next barrier).
+// The same of 32 RT tokens a wave, all lines (an even number of them: d_model is a
+// multiple of 128), with W's operands of a line going through LDS once for the NW
+// waves of a workgroup: [2][4 EB S] pieces of 1 KB in turns, the next line's on
+// their way in registers while a line is multiplied. Where every wave read W
+// through the vector cache, 24 KB a line beside its own 8 KB of x, 131072 tokens
+// took 47 us; so 33. No conditions on the loads: they cost the loop their order
+// (104 us).
+template <typename T, int EB, int RT, int NW>
+__device__ __forceinline__ void logits_shared(const BalArgs& a, const T* __restrict__ x,
+                                              const u32x4* __restrict__ wf, int64_t row0, u32x4* lds,
+                                              f32x16_t (&acc)[RT][EB]) {
+  constexpr int S = BalOp<T>::S, kLine = 128 / sizeof(T), kPieces = 4 * EB * S, kEach = kPieces / NW;
+  static_assert(kPieces % NW == 0, "pieces");
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int g = lane >> 5, r32 = lane & 31;
+#pragma unroll
+  for (int i = 0; i < RT; ++i)
+#pragma unroll
+    for (int b = 0; b < EB; ++b)
+#pragma unroll
+      for (int q = 0; q < 16; ++q) acc[i][b][q] = 0.0f;
+  const int lines = a.d / kLine;
+  const T* rows[RT];
+#pragma unroll
+  for (int i = 0; i < RT; ++i) {
+    const int64_t r = row0 + 32 * i + r32;
+    rows[i] = x + (r < a.T ? r : a.T - 1) * a.d + g * (16 / static_cast<int>(sizeof(T)));
+  }
+  u32x4 xv[2][RT][4], w[kEach];
+  auto load_x = [&](int set, int line) {
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        xv[set][i][q] = *reinterpret_cast<const u32x4*>(rows[i] + line * kLine + q * (kLine / 4));
+  };
+  auto load_w = [&](int line) {
+#pragma unroll
+    for (int u = 0; u < kEach; ++u) w[u] = wf[(static_cast<int64_t>(line) * kPieces + wave * kEach + u) * 64 + lane];
+  };
+  auto store_w = [&](int set) {
+#pragma unroll
+    for (int u = 0; u < kEach; ++u) lds[(set * kPieces + wave * kEach + u) * 64 + lane] = w[u];
+  };
+  auto multiply = [&](int set) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+      for (int b = 0; b < EB; ++b) {
+        u32x4 f[S];
+#pragma unroll
+        for (int s = 0; s < S; ++s) f[s] = lds[(set * kPieces + (q * EB + b) * S + s) * 64 + lane];
+#pragma unroll
+        for (int i = 0; i < RT; ++i) BalOp<T>::step(f, xv[set][i][q], acc[i][b]);
+      }
+  };
+  load_w(0);
+  load_x(0, 0);
+  store_w(0);
+  __syncthreads();
+  int line = 0;
+  for (; line + 2 < lines; line += 2) {
+    load_w(line + 1);
+    load_x(1, line + 1);
+    multiply(0);
+    store_w(1);
+    __syncthreads();
+    load_w(line + 2);
+    load_x(0, line + 2);
+    multiply(1);
+    store_w(0);
+    __syncthreads();
+  }
+  load_w(line + 1);
+  load_x(1, line + 1);
+  multiply(0);
+  store_w(1);
+  __syncthreads();
+  multiply(1);
+}
+
+// Counts of the experts and the number of kept tokens from the count blocks',
+// by all NT threads: the loads early, the sums when they are needed.
 template <int NT>
 struct Tallies {
-  static constexpr int kWaves = NT / 64, kEach = (kCountBlocks + kWaves - 1) / kWaves;
-  int v[kEach], n[kEach];
-  // The loads, early; the sums when they are needed.
+  static constexpr int kWaves = NT / 64, kEach = kCountBlocks / kWaves;
+  static_assert(kCountBlocks == 64 && kCountBlocks % kWaves == 0, "a lane has a block's kept tokens");
+  int v[kEach], n;
   __device__ void load(const BalArgs& a) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
 #pragma unroll
     for (int u = 0; u < kEach; ++u) {
-      const int p = wave + u * kWaves, at = (p < a.count_blocks ? p : 0) * 65;
-      v[u] = a.parts[at + lane];
-      n[u] = a.parts[at + 64];
+      const int p = wave + u * kWaves;
+      v[u] = a.parts[(p < a.count_blocks ? p : 0) * 64 + lane];
     }
+    n = a.parts[kCountBlocks * 64 + (lane < a.count_blocks ? lane : 0)];
   }
-  __device__ void put(const BalArgs& a, int (*sums)[65]) {
+  // sums: [kWaves][64], whole after the caller's next barrier; returns n (at most
+  // 2^31, exact in every lane).
+  __device__ int put(const BalArgs& a, int (*sums)[64]) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    int c = 0, k = 0;
+    int c = 0;
 #pragma unroll
-    for (int u = 0; u < kEach; ++u) {
-      const bool there = wave + u * kWaves < a.count_blocks;
-      c += there ? v[u] : 0;
-      k += there ? n[u] : 0;
-    }
+    for (int u = 0; u < kEach; ++u) c += wave + u * kWaves < a.count_blocks ? v[u] : 0;
     sums[wave][lane] = c;
-    if (lane == 0) sums[wave][64] = k;
-  }
-  // After a barrier: the share of expert `e`, and 1 / n.
-  __device__ static float share(const BalArgs& a, const int (*sums)[65], int e, float* inv_n) {
-    int c = 0, k = 0;
+    int k = lane < a.count_blocks ? n : 0;
 #pragma unroll
-    for (int u = 0; u < kWaves; ++u) {
-      c += sums[u][e];
-      k += sums[u][64];
-    }
-    *inv_n = k > 0 ? 1.0f / static_cast<float>(k) : 0.0f;
-    return k > 0 ? static_cast<float>(c) / (static_cast<float>(k) * static_cast<float>(a.k)) : 0.0f;
+    for (int o = 1; o < 64; o *= 2) k += __shfl_xor(k, o);
+    return k;
+  }
+  __device__ static int count(const int (*sums)[64], int e) {
+    int c = 0;
+#pragma unroll
+    for (int u = 0; u < kWaves; ++u) c += sums[u][e];
+    return c;
+  }
+  __device__ static float share(const BalArgs& a, const int (*sums)[64], int e, int n) {
+    return n > 0 ? static_cast<float>(count(sums, e)) / (static_cast<float>(n) * static_cast<float>(a.k)) : 0.0f;
   }
 };
+__device__ __forceinline__ float one_over(int n) { return n > 0 ? 1.0f / static_cast<float>(n) : 0.0f; }
 
 // Many tokens: 64 a wave, whose softmax stays in the registers that the
 // products leave it in.
@@ -341,8 +412,8 @@ void balance_logits_kernel(const BalArgs a, const T* __restrict__ x, const u32x4
                            T* __restrict__ saved) {
   constexpr int EP = 32 * EB, RT = 2, NW = 4;
   __shared__ float sums[NW][EP + 1];
-  __shared__ int tallies[NW][65];
-  __shared__ __attribute__((aligned(16))) float share[65];
+  __shared__ int tallies[NW][64];
+  __shared__ __attribute__((aligned(16))) float share[64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 5, r32 = lane & 31;
   const int64_t row0 = (static_cast<int64_t>(blockIdx.x) * NW + wave) * 32 * RT;
@@ -350,17 +421,15 @@ void balance_logits_kernel(const BalArgs a, const T* __restrict__ x, const u32x4
   if (saved) {
     Tallies<64 * NW> t;
     t.load(a);
-    t.put(a, tallies);
+    const int n = t.put(a, tallies);
+    inv_n = one_over(n);
     __syncthreads();
-    if (threadIdx.x < 64) {
-      share[threadIdx.x] = t.share(a, tallies, threadIdx.x, &inv_n);
-      share[64] = inv_n;
-    }
-    __syncthreads();
-    inv_n = share[64];
+    if (threadIdx.x < 64) share[threadIdx.x] = t.share(a, tallies, threadIdx.x, n);
+    // the products' barriers lie before the shares' use
   }
   f32x16_t acc[RT][EB];
-  logits<T, EB, RT>(a, x, wf, row0, 0, 1, acc);
+  __shared__ u32x4 lds[2 * 4 * EB * BalOp<T>::S * 64];
+  logits_shared<T, EB, RT, NW>(a, x, wf, row0, lds, acc);
 
   float psum[EB][16], zsum = 0.0f;
 #pragma unroll
@@ -456,26 +525,27 @@ __global__ __launch_bounds__(64 * KS) void balance_logits_few_kernel(const BalAr
   constexpr int kUsed = 32 / kTokens < KS ? 32 / kTokens : KS, kPasses = 32 / kTokens / kUsed;
   __shared__ float part[KS][16 * EB * kPitch];
   __shared__ float sums[KS][EP + 1];
-  __shared__ int tallies[KS][65];
+  __shared__ int tallies[KS][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t row0 = static_cast<int64_t>(blockIdx.x) * 32;
   Tallies<64 * KS> counts;
   if (saved) counts.load(a);
-  f32x16_t acc[1][EB];
-  logits<T, EB, 1>(a, x, wf, row0, wave, KS, acc);
-  if (saved) counts.put(a, tallies);
+  f32x16_t acc[EB];
+  logits<T, EB>(a, x, wf, row0, wave, KS, acc);
+  const int n = saved ? counts.put(a, tallies) : 0;
 #pragma unroll
   for (int b = 0; b < EB; ++b)
 #pragma unroll
-    for (int q = 0; q < 16; ++q) part[wave][(b * 16 + q) * kPitch + lane] = acc[0][b][q];
+    for (int q = 0; q < 16; ++q) part[wave][(b * 16 + q) * kPitch + lane] = acc[b][q];
   __syncthreads();
   // lane: eight experts e0.. of a token
   const int m = lane % L, e0 = 8 * m;
-  float psum[8], zsum = 0.0f, f[8], inv_n = 0.0f;
+  float psum[8], zsum = 0.0f, f[8];
+  const float inv_n = one_over(n);
 #pragma unroll
   for (int q = 0; q < 8; ++q) {
     psum[q] = 0.0f;
-    f[q] = saved ? counts.share(a, tallies, e0 + q, &inv_n) : 0.0f;
+    f[q] = saved ? counts.share(a, tallies, e0 + q, n) : 0.0f;
   }
   // a sum over the lanes of a token, and over those of an octet of experts
   auto over_token = [&](float v) {
@@ -552,58 +622,45 @@ __global__ __launch_bounds__(64 * KS) void balance_logits_few_kernel(const BalAr
   }
 }
 
-// The results from the workgroups' sums: column e of them in thread e's group,
-// 16 threads to a column.
+// The results from the workgroups' sums: 16 threads to an expert.
 __global__ __launch_bounds__(1024) void balance_loss_kernel(const BalArgs a, int groups, float balance, float z,
                                                             int32_t* __restrict__ counts,
                                                             float* __restrict__ mean_prob,
                                                             float* __restrict__ loss) {
-  __shared__ float sums[16][64], zeds[1024], even[64];
-  __shared__ int tallies[65];
+  __shared__ float sums[16][64], zeds[16];
+  __shared__ int tallies[16][64];
   const int e = threadIdx.x % 64, j = threadIdx.x / 64;
-  if (threadIdx.x < 65) {
-    int v = 0;
-#pragma unroll 8
-    for (int p = 0; p < a.count_blocks; ++p) v += a.parts[p * 65 + threadIdx.x];
-    tallies[threadIdx.x] = v;
-  }
+  Tallies<1024> t;
+  t.load(a);
   float v = 0.0f, zed = 0.0f;
   if (e < a.E) {
-#pragma unroll 8
+#pragma unroll 16
     for (int p = j; p < groups; p += 16) v += a.stats[static_cast<int64_t>(p) * 65 + e];
   }
   for (int p = threadIdx.x; p < groups; p += 1024) zed += a.stats[static_cast<int64_t>(p) * 65 + 64];
   sums[j][e] = v;
-  zeds[threadIdx.x] = zed;
+  zed = wave_sum(zed);
+  if (e == 0) zeds[j] = zed;
+  const int n = t.put(a, tallies);
   __syncthreads();
+  if (j) return;
+  float p = 0.0f, zz = 0.0f;
 #pragma unroll
-  for (int half = 512; half > 0; half /= 2) {
-    if (static_cast<int>(threadIdx.x) < half) zeds[threadIdx.x] += zeds[threadIdx.x + half];
-    __syncthreads();
+  for (int u = 0; u < 16; ++u) {
+    p += sums[u][e];
+    zz += zeds[u];
   }
-  const int n = tallies[64];
-  const float inv_n = n > 0 ? 1.0f / static_cast<float>(n) : 0.0f;
-  if (j == 0) {
-    float p = 0.0f;
-#pragma unroll
-    for (int u = 0; u < 16; ++u) p += sums[u][e];
-    p *= inv_n;
-    even[e] = 0.0f;
-    if (e < a.E) {
-      mean_prob[e] = p;
-      counts[e] = tallies[e];
-      even[e] = n > 0 ? static_cast<float>(tallies[e]) / (static_cast<float>(n) * static_cast<float>(a.k)) * p : 0.0f;
-    }
+  p *= one_over(n);
+  zz *= one_over(n);
+  if (e < a.E) {
+    mean_prob[e] = p;
+    counts[e] = t.count(tallies, e);
   }
-  __syncthreads();
-  if (threadIdx.x < 64) {
-    const float total = static_cast<float>(a.E) * wave_sum(even[threadIdx.x]);
-    if (threadIdx.x == 0) {
-      const float zz = zeds[0] * inv_n;
-      loss[0] = __builtin_fmaf(balance, total, z * zz);
-      loss[1] = total;
-      loss[2] = zz;
-    }
+  const float total = static_cast<float>(a.E) * wave_sum(e < a.E ? t.share(a, tallies, e, n) * p : 0.0f);
+  if (e == 0) {
+    loss[0] = __builtin_fmaf(balance, total, z * zz);
+    loss[1] = total;
+    loss[2] = zz;
   }
 }
 
@@ -960,9 +1017,12 @@ __global__ __launch_bounds__(256) void balance_zero_kernel(float* p, int64_t n) 
 
 // ------------------------------------------------------------------ layouts
 
-// Tokens of a logits workgroup, and its form: 256 with whole rows of 64 a wave
-// where that gives every CU two workgroups, else waves that share the columns.
-int logits_rows(int64_t T) { return T >= 65536 ? 256 : 32; }
+// Tokens of a logits workgroup: 256 with whole rows of 64 tokens a wave, or 32
+// with waves that share the columns, which fill the chip with fewer tokens. bf16,
+// 64 experts x 512: 32768 tokens 21.3 and 17.9 us, 50000 22.6 and 26.2; fp32 50000
+// 48.4 and 44.8, 65536 49 and 58 (fp32 MFMAs take longer: less is won by sharing W).
+constexpr int64_t kManyTokens = 40960, kManyTokensF32 = 57344;
+int logits_rows(int64_t T, int dtype) { return T >= (dtype == MOE_BF16 ? kManyTokens : kManyTokensF32) ? 256 : 32; }
 
 int grad_ranges(const moe_balance& b) {
   const int64_t slices = b.d_model / kGradCols, chunks = (b.tokens + 31) / 32;
@@ -985,7 +1045,8 @@ BalLayout bal_layout(const moe_balance& b) {
   };
   const size_t EP = 32 * expert_blocks(b.experts), d = b.d_model;
   L.parts = take(kCountBlocks * 65 * sizeof(int32_t));
-  L.stats = take((b.tokens + logits_rows(b.tokens) - 1) / logits_rows(b.tokens) * 65 * sizeof(float));
+  const int64_t rows = logits_rows(b.tokens, b.dtype);
+  L.stats = take((b.tokens + rows - 1) / rows * 65 * sizeof(float));
   L.wf = take(d * EP * (b.dtype == MOE_BF16 ? 6 : 4));
   L.total = o;
   o = 0;  // the backward has the place for itself
@@ -1001,7 +1062,7 @@ size_t saved_rows_bytes(const moe_balance& b) {
 
 template <typename T, int EB>
 void launch_logits(const BalArgs& a, const T* x, const u32x4* wf, T* saved, hipStream_t s) {
-  const int rows = logits_rows(a.T);
+  const int rows = logits_rows(a.T, sizeof(T) == 2 ? MOE_BF16 : MOE_FP32);
   const dim3 grid(static_cast<unsigned>((a.T + rows - 1) / rows));
   if (rows == 256)
     MOE_LAUNCH("balance_logits", (balance_logits_kernel<T, EB>), grid, dim3(256), 0, s, a, x, wf, saved);
@@ -1030,7 +1091,8 @@ hipError_t balance_t(const moe_balance& b, const void* x, const float* w, const 
                w, EB, wf, wb, parts);
     if (EB == 1) launch_logits<T, 1>(a, static_cast<const T*>(x), wf, static_cast<T*>(saved), s);
     else launch_logits<T, 2>(a, static_cast<const T*>(x), wf, static_cast<T*>(saved), s);
-    groups = static_cast<int>((b.tokens + logits_rows(b.tokens) - 1) / logits_rows(b.tokens));
+    const int rows = logits_rows(b.tokens, b.dtype);
+    groups = static_cast<int>((b.tokens + rows - 1) / rows);
   }
   MOE_LAUNCH("balance_loss", balance_loss_kernel, dim3(1), dim3(1024), 0, s, a, groups, b.balance, b.z, counts,
              mean_prob, loss);
