@@ -902,9 +902,9 @@ def residual_norm(n: ResidualNorm, z, res, params: Dict, buf: ResidualNormBuffer
 def residual_norm_backward(n: ResidualNorm, z, res, params: Dict, grad_out, grad_y,
                            buf: ResidualNormBuffers, stream=None):
     """Gradients of sum(out * grad_out) + sum(y * grad_y) after
-    ``residual_norm`` with the same buffers: (grad_z, grad_res, {the
-    parameters' gradients, fp32}). grad_out may be None; grad_y is None without
-    the norm before the next block."""
+    ``residual_norm`` with the same buffers: (grad_z, grad_res, {the gradients,
+    fp32, of the parameters that params holds}). grad_out may be None; grad_y is
+    None without the norm before the next block."""
     shape, stats, dt, dev, ld_z, ld_res, p = _want_step(n, z, res, params)
     gz, gr, g = buf.grad_z, buf.grad_res, buf.grads
     if gz is None:
@@ -915,8 +915,9 @@ def residual_norm_backward(n: ResidualNorm, z, res, params: Dict, grad_out, grad
     ld_gy = 0 if grad_y is None else _want_rows("grad_y", grad_y, shape, dt, dev)
     ld_gz, ld_gr = _want_rows("grad_z", gz, shape, dt, dev), _want_rows("grad_res", gr, shape, dt, dev)
     _want("stats", buf.stats, stats, torch.float32, dev)
-    for name in NORM_PARAMS:
-        _want("gradient of " + name, g[name], (n.width,), torch.float32, dev)
+    g = {name: g[name] for name in NORM_PARAMS if params.get(name) is not None}
+    for name, t in g.items():
+        _want("gradient of " + name, t, (n.width,), torch.float32, dev)
     _want_bytes("workspace", buf.workspace, 0, dev)
     grads = norm_grads_struct(g)
     _run("moe_residual_norm_bwd", dev, stream, load().moe_residual_norm_bwd,

@@ -52,7 +52,9 @@ __device__ void split_router(const float* __restrict__ w, int d, int E, int EB, 
   if (k0 >= d) return;
   float v[V];
 #pragma unroll
-  for (int q = 0; q < V; ++q) v[q] = e < E ? w[static_cast<int64_t>(k0 + q) * E + e] : 0.0f;
+  for (int q = 0; q < V; ++q) v[q] = w[static_cast<int64_t>(k0 + q) * E + (e < E ? e : 0)];  // without a branch
+#pragma unroll
+  for (int q = 0; q < V; ++q) v[q] = e < E ? v[q] : 0.0f;
 #pragma unroll
   for (int s = 0; s < S; ++s) {
     const u32x4 p = Piece<T>::narrow(v);
@@ -83,8 +85,11 @@ __device__ void turn_router(const float* __restrict__ w, int d, int E, int EB, u
 #pragma unroll
   for (int q = 0; q < V; ++q) {
     const int e = (kHalves ? 32 * b + 8 * g : 16 * b + 4 * g) + q;
-    v[q] = e < E ? w[static_cast<int64_t>(col) * E + e] : 0.0f;
+    v[q] = w[static_cast<int64_t>(col) * E + (e < E ? e : 0)];
   }
+#pragma unroll
+  for (int q = 0; q < V; ++q)
+    if ((kHalves ? 32 * b + 8 * g : 16 * b + 4 * g) + q >= E) v[q] = 0.0f;
   const u32x4 p = Piece<T>::narrow(v);
   if (!kHalves) {
     out[i] = p;
@@ -110,9 +115,11 @@ __global__ __launch_bounds__(kCountThreads) void balance_count_kernel(const BalA
   constexpr int kWaves = kCountThreads / 64;
   __shared__ int hist[kWaves][65];
   if (static_cast<int>(blockIdx.x) >= a.count_blocks) {
+    // as many pieces for the backward as for the logits
     const int i = (blockIdx.x - a.count_blocks) * kCountThreads + threadIdx.x;
-    split_router<T>(w, a.d, a.E, EB, wf, i);
-    if (wb) turn_router<T>(w, a.d, a.E, EB, wb, i);
+    const int pieces = a.d / (2 * Piece<T>::V) * EB * 64;
+    if (i < pieces) split_router<T>(w, a.d, a.E, EB, wf, i);
+    else if (wb) turn_router<T>(w, a.d, a.E, EB, wb, i - pieces);
     return;
   }
   for (int i = threadIdx.x; i < kWaves * 65; i += kCountThreads) (&hist[0][0])[i] = 0;
@@ -1085,7 +1092,7 @@ hipError_t balance_t(const moe_balance& b, const void* x, const float* w, const 
   if (b.tokens > 0) {
     const int64_t blocks = (b.tokens * b.top_k + 8 * kCountThreads - 1) / (8 * kCountThreads);
     a.count_blocks = static_cast<int>(blocks > kCountBlocks ? kCountBlocks : blocks);
-    const int pieces = b.d_model / (2 * Piece<T>::V) * EB * 64;
+    const int pieces = b.d_model / (2 * Piece<T>::V) * EB * 64 * (wb ? 2 : 1);
     MOE_LAUNCH("balance_count", balance_count_kernel<T>,
                dim3(a.count_blocks + (pieces + kCountThreads - 1) / kCountThreads), dim3(kCountThreads), 0, s, a, idx,
                w, EB, wf, wb, parts);

@@ -27,6 +27,12 @@ namespace moe {
 
 namespace {
 
+// Floats of a partial row.
+__host__ __device__ constexpr int step_pitch(int width) { return (width + 3) / 4 * 4; }
+
+// Threads of a workgroup that holds several rows.
+constexpr int kFwdThreads = 256, kBwdThreads = 768;
+
 struct StepArgs {
   int64_t rows;
   int width;
@@ -38,6 +44,7 @@ struct StepArgs {
   const float *w1, *b1, *gate, *w2, *b2;
   float* stats;  // [4][rows]: mean and 1 / deviation of z, of o
   float* partial;
+  int wanted;    // bit k: column sum k
 };
 
 // Sums of a row over its threads: 16 lanes, a wave, or the workgroup (kRow 0)
@@ -81,10 +88,10 @@ __device__ __forceinline__ void load_scales(const float* p, float fill, int c, i
 }
 
 // Whether the backward reads the parameters again for every row (from the
-// caches): a workgroup of more than 512 threads has 128 registers a thread,
+// caches): a workgroup of 1024 threads has 128 registers a thread,
 // beside the sums too few for them.
 template <int kMax>
-constexpr bool kAgain = kMax > 512;
+constexpr bool kAgain = kMax == 1024;
 
 // The thread's place: its column piece within a row, its first row, and the
 // rows that all workgroups take in one go.
@@ -212,10 +219,10 @@ __global__ __launch_bounds__(kMax) void step_fwd_kernel(const StepArgs a) {
   }
 }
 
-// partial: [gridDim.x][4][width], A, B, dw2 and db2; null when none is wanted.
+// partial: [gridDim.x][4][pitch], A, B, dw2 and db2, those that are wanted.
 template <typename T, int kRow, int NV, int kMax>
 __global__ __launch_bounds__(kMax) void step_bwd_kernel(const StepArgs a) {
-  constexpr int V = Piece<T>::V, kThreads = 256;
+  constexpr int V = Piece<T>::V, kThreads = kMax;  // of a workgroup that holds several rows
   __shared__ float slots[4][2][16];
   // column sums of the rows of a workgroup that holds several
   __shared__ float cols[kRow ? NV * V * kThreads : 1];
@@ -320,28 +327,30 @@ __global__ __launch_bounds__(kMax) void step_bwd_kernel(const StepArgs a) {
     }
     cur = nxt;
   }
-  if (!a.partial) return;
-  float* out = a.partial + static_cast<int64_t>(blockIdx.x) * 4 * a.width;
+  if (!a.wanted) return;
+  const int pitch = step_pitch(a.width);
+  float* out = a.partial + static_cast<int64_t>(blockIdx.x) * 4 * pitch;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
+    if (!(a.wanted >> k & 1)) continue;
     if (kRow == 0) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         if (at(i) + V <= a.width) {
 #pragma unroll
           for (int h = 0; h < V; h += 4)
-            store_any(out + static_cast<int64_t>(k) * a.width + at(i) + h,
+            store_any(out + static_cast<int64_t>(k) * pitch + at(i) + h,
                       (u32x4){__float_as_uint(sum[k][i][h]), __float_as_uint(sum[k][i][h + 1]),
                               __float_as_uint(sum[k][i][h + 2]), __float_as_uint(sum[k][i][h + 3])});
           continue;
         }
 #pragma unroll
         for (int q = 0; q < V; ++q)
-          if (at(i) + q < a.width) out[static_cast<int64_t>(k) * a.width + at(i) + q] = sum[k][i][q];
+          if (at(i) + q < a.width) out[static_cast<int64_t>(k) * pitch + at(i) + q] = sum[k][i][q];
       }
       continue;
     }
-    if (k) __syncthreads();
+    __syncthreads();
     // element (i, q) of lane t at ((i V + q) tpr + t): lanes side by side
     constexpr int kPer = kRow ? kRow : 1, kRows = kThreads / kPer;
 #pragma unroll
@@ -355,49 +364,54 @@ __global__ __launch_bounds__(kMax) void step_bwd_kernel(const StepArgs a) {
       float v = 0.0f;
 #pragma unroll
       for (int r = 0; r < kRows; ++r) v += cols[r * NV * V * kPer + from];
-      out[static_cast<int64_t>(k) * a.width + c] = v;
+      out[static_cast<int64_t>(k) * pitch + c] = v;
     }
   }
 }
 
 // The parameters' gradients (each may be null) from `parts` partial rows
-// [parts][4][width]: a workgroup owns 16 columns, 64 threads to each, thread j
-// adding the four sums of rows j, j + 64, ... and the 64 then added in order.
+// [parts][4][pitch]: a workgroup owns 32 columns, 32 threads to four of them and
+// one of the four sums; thread j adds rows j, j + 32, ... (unwanted sums too,
+// whatever they hold: conditions would put the loads one after the other) and the
+// 32 are then added in order.
 struct StepGrads {
   const float *w1, *b1, *gate;
   float *dw1, *db1, *dgate, *dw2, *db2;
+  int wanted() const {
+    return (dw1 || dgate) | (db1 || (dgate && b1)) << 1 | (dw2 != nullptr) << 2 | (db2 != nullptr) << 3;
+  }
 };
-constexpr int kSumCols = 16, kSumGroups = 64;
-__global__ __launch_bounds__(kSumCols* kSumGroups) void step_sum_kernel(const float* __restrict__ partial,
-                                                                       int parts, int width, const StepGrads g) {
-  __shared__ float sums[4][kSumGroups][kSumCols];
-  const int c = threadIdx.x % kSumCols, j = threadIdx.x / kSumCols;
-  const int col = blockIdx.x * kSumCols + c;
-  float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  if (col < width) {
-#pragma unroll 4
+constexpr int kSumCols = 32, kSumGroups = 32;
+__global__ __launch_bounds__(1024) void step_sum_kernel(const float* __restrict__ partial, int parts, int width,
+                                                        int pitch, const StepGrads g) {
+  __shared__ float sums[kSumGroups][4][kSumCols], total[4][kSumCols];
+  {
+    const int c = threadIdx.x % 8 * 4, k = threadIdx.x / 8 % 4, j = threadIdx.x / 32;
+    const int at = min(static_cast<int>(blockIdx.x) * kSumCols + c, pitch - 4);
+    f32x4_t v = (f32x4_t){0.0f, 0.0f, 0.0f, 0.0f};
+    const float* src = partial + static_cast<int64_t>(k) * pitch + at;
+#pragma unroll 8
     for (int p = j; p < parts; p += kSumGroups)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) v[k] += partial[(static_cast<int64_t>(p) * 4 + k) * width + col];
+      v += *reinterpret_cast<const f32x4_t*>(src + static_cast<int64_t>(p) * 4 * pitch);
+    *reinterpret_cast<f32x4_t*>(&sums[j][k][c]) = v;
   }
-#pragma unroll
-  for (int k = 0; k < 4; ++k) sums[k][j][c] = v[k];
   __syncthreads();
+  const int c = threadIdx.x % kSumCols, j = threadIdx.x / kSumCols;
+  if (j < 4) {
+    float t = 0.0f;
 #pragma unroll
-  for (int half = kSumGroups / 2; half > 0; half /= 2) {
-    if (j < half) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) sums[k][j][c] += sums[k][j + half][c];
-    }
-    __syncthreads();
+    for (int u = 0; u < kSumGroups; ++u) t += sums[u][j][c];
+    total[j][c] = t;
   }
+  __syncthreads();
+  const int col = blockIdx.x * kSumCols + c;
   if (j || col >= width) return;
-  const float A = sums[0][0][c], B = sums[1][0][c], gate = g.gate ? g.gate[col] : 1.0f;
+  const float A = total[0][c], B = total[1][c], gate = g.gate ? g.gate[col] : 1.0f;
   if (g.dw1) g.dw1[col] = gate * A;
   if (g.db1) g.db1[col] = gate * B;
   if (g.dgate) g.dgate[col] = (g.w1 ? g.w1[col] : 1.0f) * A + (g.b1 ? g.b1[col] * B : 0.0f);
-  if (g.dw2) g.dw2[col] = sums[2][0][c];
-  if (g.db2) g.db2[col] = sums[3][0][c];
+  if (g.dw2) g.dw2[col] = total[2][c];
+  if (g.db2) g.db2[col] = total[3][c];
 }
 
 __global__ __launch_bounds__(256) void step_zero_kernel(const StepGrads g, int width) {
@@ -412,31 +426,32 @@ __global__ __launch_bounds__(256) void step_zero_kernel(const StepGrads g, int w
 struct StepShape {
   int row, threads, pieces;  // row: 16, 64, or 0
 };
-StepShape step_shape(int width, int V) {
-  const int n = (width + V - 1) / V;  // pieces of a row
-  if (n <= 16) return {16, 256, 1};
-  if (n <= 64) return {64, 256, 1};
-  if (V == 4 && n <= 128) return {64, 256, 2};
-  if (n <= 1024) return {0, (n + 63) / 64 * 64, 1};
-  return {0, n <= 2048 ? (n + 127) / 128 * 64 : 1024, n <= 2048 ? 2 : 4};
+StepShape step_shape(const moe_residual_norm& n, bool bwd) {
+  const int V = n.dtype == MOE_BF16 ? 8 : 4, p = (n.width + V - 1) / V;  // pieces of a row
+  const int waves = bwd ? kBwdThreads : kFwdThreads;
+  if (p <= 16) return {16, waves, 1};
+  if (p <= 64) return {64, waves, 1};
+  if (V == 4 && p <= 128) return {64, waves, 2};
+  if (p <= 1024) return {0, (p + 63) / 64 * 64, 1};
+  return {0, p <= 2048 ? (p + 127) / 128 * 64 : 1024, p <= 2048 ? 2 : 4};
 }
 
-template <typename F>
+template <int kWaves, typename F>
 void with_step_shape(int dtype, const StepShape& r, F&& f) {
 #define MOE_STEP_CASE(T, ROW, NV, MAX)                                \
   if (r.row == ROW && r.pieces == NV && (ROW || r.threads <= MAX))    \
   return f(T{}, std::integral_constant<int, ROW>{}, std::integral_constant<int, NV>{}, \
            std::integral_constant<int, MAX>{})
   if (dtype == MOE_BF16) {
-    MOE_STEP_CASE(bf16_t, 16, 1, 256);
-    MOE_STEP_CASE(bf16_t, 64, 1, 256);
+    MOE_STEP_CASE(bf16_t, 16, 1, kWaves);
+    MOE_STEP_CASE(bf16_t, 64, 1, kWaves);
     MOE_STEP_CASE(bf16_t, 0, 1, 512);
     MOE_STEP_CASE(bf16_t, 0, 1, 1024);
     MOE_STEP_CASE(bf16_t, 0, 2, 1024);
   } else {
-    MOE_STEP_CASE(float, 16, 1, 256);
-    MOE_STEP_CASE(float, 64, 1, 256);
-    MOE_STEP_CASE(float, 64, 2, 256);
+    MOE_STEP_CASE(float, 16, 1, kWaves);
+    MOE_STEP_CASE(float, 64, 1, kWaves);
+    MOE_STEP_CASE(float, 64, 2, kWaves);
     MOE_STEP_CASE(float, 0, 1, 512);
     MOE_STEP_CASE(float, 0, 1, 1024);
     MOE_STEP_CASE(float, 0, 2, 1024);
@@ -445,17 +460,14 @@ void with_step_shape(int dtype, const StepShape& r, F&& f) {
 #undef MOE_STEP_CASE
 }
 
-StepShape shape_of(const moe_residual_norm& n) { return step_shape(n.width, n.dtype == MOE_BF16 ? 8 : 4); }
 int rows_per_block(const StepShape& r) { return r.row ? r.threads / r.row : 1; }
 
-// Workgroups of the backward: enough to fill the chip, at least four row steps
-// each (a partial row costs 16 bytes a column).
+// Workgroups of the backward: as many as are at once on the chip.
 int step_bwd_blocks(const moe_residual_norm& n) {
-  const StepShape r = shape_of(n);
-  const int64_t steps = (n.rows + rows_per_block(r) - 1) / rows_per_block(r);
-  const int64_t most = 256 * (r.threads > 768 ? 1 : 768 / r.threads);
-  const int64_t b = (steps + 3) / 4;
-  return static_cast<int>(b < 1 ? 1 : (b > most ? most : b));
+  const StepShape r = step_shape(n, true);
+  const int64_t need = (n.rows + rows_per_block(r) - 1) / rows_per_block(r);
+  const int64_t most = 256 * (r.threads >= 768 ? 1 : 768 / r.threads);
+  return static_cast<int>(need < 1 ? 1 : (need > most ? most : need));
 }
 
 StepArgs step_args(const moe_residual_norm& n) {
@@ -499,8 +511,8 @@ hipError_t launch_residual_norm(const moe_residual_norm& n, const void* z, const
   a.o = out;
   a.y = y;
   a.stats = stats;
-  const StepShape r = shape_of(n);
-  with_step_shape(n.dtype, r, [&](auto t, auto row, auto nv, auto max) {
+  const StepShape r = step_shape(n, false);
+  with_step_shape<kFwdThreads>(n.dtype, r, [&](auto t, auto row, auto nv, auto max) {
     const int64_t need = (n.rows + rows_per_block(r) - 1) / rows_per_block(r);
     const int64_t most = static_cast<int64_t>(cu_count()) * (1536 / r.threads);
     MOE_LAUNCH("residual_norm", (step_fwd_kernel<decltype(t), decltype(row)::value, decltype(nv)::value, decltype(max)::value>),
@@ -510,7 +522,7 @@ hipError_t launch_residual_norm(const moe_residual_norm& n, const void* z, const
 }
 
 size_t residual_norm_ws_bytes(const moe_residual_norm& n) {
-  return align_up(static_cast<size_t>(step_bwd_blocks(n)) * 4 * n.width * sizeof(float), 256);
+  return align_up(static_cast<size_t>(step_bwd_blocks(n)) * 4 * step_pitch(n.width) * sizeof(float), 256);
 }
 
 hipError_t launch_residual_norm_bwd(const moe_residual_norm& n, const void* z, const void* res,
@@ -520,9 +532,9 @@ hipError_t launch_residual_norm_bwd(const moe_residual_norm& n, const void* z, c
   StepArgs a = step_args(n);
   set_params(&a, w, n.post != 0);
   const StepGrads grads{a.w1, a.b1, a.gate, g.post_weight, g.post_bias, g.gate, g.pre_weight, g.pre_bias};
-  const bool any = g.post_weight || g.post_bias || g.gate || g.pre_weight || g.pre_bias;
+  const int wanted = grads.wanted();
   if (n.rows == 0) {
-    if (!any) return hipSuccess;
+    if (!wanted) return hipSuccess;
     MOE_LAUNCH("residual_norm_zero", step_zero_kernel, dim3((n.width + 255) / 256), dim3(256), 0, s, grads,
                n.width);
     return hipGetLastError();
@@ -534,16 +546,17 @@ hipError_t launch_residual_norm_bwd(const moe_residual_norm& n, const void* z, c
   a.dz = dz;
   a.dres = dres;
   a.stats = const_cast<float*>(stats);
-  a.partial = any ? static_cast<float*>(ws) : nullptr;
-  const StepShape r = shape_of(n);
+  a.partial = static_cast<float*>(ws);
+  a.wanted = wanted;
+  const StepShape r = step_shape(n, true);
   const int blocks = step_bwd_blocks(n);
-  with_step_shape(n.dtype, r, [&](auto t, auto row, auto nv, auto max) {
+  with_step_shape<kBwdThreads>(n.dtype, r, [&](auto t, auto row, auto nv, auto max) {
     MOE_LAUNCH("residual_norm_bwd", (step_bwd_kernel<decltype(t), decltype(row)::value, decltype(nv)::value, decltype(max)::value>),
                dim3(blocks), dim3(r.threads), 0, s, a);
   });
-  if (any)
+  if (wanted)
     MOE_LAUNCH("residual_norm_sum", step_sum_kernel, dim3((n.width + kSumCols - 1) / kSumCols),
-               dim3(kSumCols * kSumGroups), 0, s, a.partial, blocks, n.width, grads);
+               dim3(1024), 0, s, a.partial, blocks, n.width, step_pitch(n.width), grads);
   return hipGetLastError();
 }
 

@@ -171,7 +171,7 @@ def test_step_tensor_refusals():
     for name, t in (("grad_z", z[:, :9]), ("grad_res", z.float()), ("grads", dict(buf.grads, gate=z)),
                     ("workspace", z), ("stats", z)):
         with pytest.raises(ValueError):
-            K.residual_norm_backward(n, z, z, {}, z, z, K.ResidualNormBuffers(**dict(vars(buf), **{name: t})))
+            K.residual_norm_backward(n, z, z, dict(gate=buf.grads["gate"]), z, z, K.ResidualNormBuffers(**dict(vars(buf), **{name: t})))
     with pytest.raises(ValueError, match="GPU"):
         K.residual_norm_backward(n, z, z, {}, z, z, buf)
     with pytest.raises(ValueError):

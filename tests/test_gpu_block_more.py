@@ -334,9 +334,9 @@ def test_step_odd_values_and_no_rows():
     buf = K.allocate_residual_norm(n, "cuda", training=True)
     for g in buf.grads.values():
         g.fill_(1)
-    e = torch.empty(0, 300, dtype=torch.bfloat16, device="cuda")
-    K.residual_norm(n, e, e, {}, buf)
-    K.residual_norm_backward(n, e, e, {}, e, e, buf)
+    e, p = torch.empty(0, 300, dtype=torch.bfloat16, device="cuda"), step_params(r, 300, K.NORM_PARAMS)
+    K.residual_norm(n, e, e, p, buf)
+    K.residual_norm_backward(n, e, e, p, e, e, buf)
     assert not any(g.any() for g in buf.grads.values())
 
 
