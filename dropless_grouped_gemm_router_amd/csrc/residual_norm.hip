@@ -13,9 +13,9 @@
 // bf16 or four fp32 columns a thread and piece, so nothing is read twice: the
 // forward takes its four statistics from there, and the backward makes o again
 // from z and res, unrounded, instead of reading the rounded o. Rows of up to 16
-// pieces take 16 lanes, up to 64 (fp32: 128) a wave, wider ones a workgroup
-// whose waves add up through LDS; the next row's loads are issued before the
-// current row is reduced.
+// pieces take 16 lanes, up to 64 (fp32: 128) a wave, wider ones several waves
+// that add up through LDS; the next row's loads are issued before the current row
+// is reduced.
 //
 // The five column sums come of four: with A = sum do zh and B = sum do, dw1 =
 // gate A, db1 = gate B and dgate = w1 A + b1 B. Each thread keeps those of its
@@ -45,29 +45,51 @@ struct StepArgs {
   float* stats;  // [4][rows]: mean and 1 / deviation of z, of o
   float* partial;
   int wanted;    // bit k: column sum k
+  int tpr, rpb;  // threads of a row, rows of a workgroup
 };
 
-// Sums of a row over its threads: 16 lanes, a wave, or the workgroup (kRow 0)
-// through LDS. `slot` is this reduction's own array, another one in every other
-// row, so that one barrier is enough: whoever writes it again has met all
-// waves at a barrier that they reach after reading it.
+// Sums of a row over its threads: 16 lanes, a wave, or, kRow 0, the waves from
+// `first` on, `waves` of them, through LDS. `slot` is this reduction's own array,
+// another one in every other row, so that one barrier is enough: whoever writes it
+// again has met all waves at a barrier that they reach after reading it.
 template <int kRow, int N>
-__device__ __forceinline__ void step_sums(float (&v)[N], float (*slot)[16]) {
+__device__ __forceinline__ void step_sums(float (&v)[N], float (*slot)[16], int first, int waves) {
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] = kRow == 16 ? row16_sum(v[i]) : wave_sum(v[i]);
   if (kRow) return;
-  const int wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
   if ((threadIdx.x & 63) == 0) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) slot[i][wave] = v[i];
+    for (int i = 0; i < N; ++i) slot[i][threadIdx.x >> 6] = v[i];
   }
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     float t = 0.0f;
-    for (int w = 0; w < waves; ++w) t += slot[i][w];
+    for (int w = 0; w < waves; ++w) t += slot[i][first + w];
     v[i] = t;
   }
+}
+
+// load_piece without a branch, for rows of V or more: a piece that is not whole
+// takes the row's last V elements, and where it is used trim_step moves its own
+// to the front, zeros behind them. (A wave with one lane at the row's end had every
+// other lane wait for its loads of single elements: 10000 x 1023 bf16, backward, 58
+// us against 31 at 1024.)
+template <typename T>
+__device__ __forceinline__ u32x4 load_step(const T* row, int c, int n) {
+  if (n < Piece<T>::V) return load_piece(row, c, n);
+  return load_any(row + min(c, n - Piece<T>::V));
+}
+template <typename T>
+__device__ __forceinline__ void trim_step(u32x4& v, int c, int n) {
+  const int past = c + Piece<T>::V - n;  // elements of the piece behind the row
+  if (past <= 0 || n < Piece<T>::V) return;
+  const int w = sizeof(T) == 2 ? past / 2 : past;
+  if (sizeof(T) == 2 && past & 1)
+    v = (u32x4){v[0] >> 16 | v[1] << 16, v[1] >> 16 | v[2] << 16, v[2] >> 16 | v[3] << 16, v[3] >> 16};
+  if (w & 1) v = (u32x4){v[1], v[2], v[3], 0u};
+  if (w & 2) v = (u32x4){v[2], v[3], 0u, 0u};
+  if (w >= 4) v = (u32x4){0u, 0u, 0u, 0u};
 }
 
 // V parameters from column c on: `fill` where there is no array, zeros past the
@@ -88,23 +110,25 @@ __device__ __forceinline__ void load_scales(const float* p, float fill, int c, i
 }
 
 // Whether the backward reads the parameters again for every row (from the
-// caches): a workgroup of 1024 threads has 128 registers a thread,
-// beside the sums too few for them.
+// caches), and no row ahead: a workgroup of 1024 threads has 128 registers a
+// thread, beside the sums too few for them.
 template <int kMax>
 constexpr bool kAgain = kMax == 1024;
 
-// The thread's place: its column piece within a row, its first row, and the
-// rows that all workgroups take in one go.
+// The thread's place: its column piece within a row and its row of the
+// workgroup's; the rows that all workgroups take in one go.
 template <int kRow>
 struct StepPlace {
-  int t, tpr;
-  int64_t row, step;
-  __device__ StepPlace() {
-    tpr = kRow ? kRow : blockDim.x;
-    t = kRow ? threadIdx.x % (kRow ? kRow : 1) : threadIdx.x;
-    const int rows = kRow ? blockDim.x / (kRow ? kRow : 1) : 1;
-    row = static_cast<int64_t>(blockIdx.x) * rows + (kRow ? threadIdx.x / (kRow ? kRow : 1) : 0);
-    step = static_cast<int64_t>(gridDim.x) * rows;
+  int t, tpr, in, first, waves;
+  int64_t row0, step;
+  __device__ StepPlace(const StepArgs& a) {
+    tpr = kRow ? kRow : a.tpr;
+    in = threadIdx.x / tpr;
+    t = threadIdx.x - in * tpr;
+    waves = tpr / 64;
+    first = in * waves;
+    row0 = static_cast<int64_t>(blockIdx.x) * a.rpb;
+    step = static_cast<int64_t>(gridDim.x) * a.rpb;
   }
 };
 
@@ -120,7 +144,7 @@ __device__ __forceinline__ void normalise(const StepArgs& a, const StepPlace<kRo
     for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int q = 0; q < V; ++q) s[0] += f[i][q];
-    step_sums<kRow, 1>(s, slots[0]);
+    step_sums<kRow, 1>(s, slots[0], p.first, p.waves);
     mean = s[0] / a.count;  // a division: the mean of a constant row is its value
   }
   float ss[1] = {0.0f};
@@ -131,7 +155,7 @@ __device__ __forceinline__ void normalise(const StepArgs& a, const StepPlace<kRo
       f[i][q] -= mean;
       if ((i * p.tpr + p.t) * V + q < a.width) ss[0] = __builtin_fmaf(f[i][q], f[i][q], ss[0]);
     }
-  step_sums<kRow, 1>(ss, slots[1]);
+  step_sums<kRow, 1>(ss, slots[1], p.first, p.waves);
   const float rstd = 1.0f / sqrtf(ss[0] / a.count + a.eps);
 #pragma unroll
   for (int i = 0; i < NV; ++i)
@@ -145,18 +169,18 @@ template <typename T, int kRow, int NV, int kMax>
 __global__ __launch_bounds__(kMax) void step_fwd_kernel(const StepArgs a) {
   constexpr int V = Piece<T>::V;
   __shared__ float slots[8][1][16];
-  const StepPlace<kRow> p;
-  int64_t row = p.row;
+  const StepPlace<kRow> p(a);
+  int64_t row = p.row0 + p.in;
   int odd = 0;
-  if (row >= a.rows) return;  // all threads of a row together
+  if (row >= a.rows) return;  // all threads of a row together; kRow 0: of the workgroup
   const T* z = static_cast<const T*>(a.z);
   const T* res = static_cast<const T*>(a.res);
   auto at = [&](int i) { return (i * p.tpr + p.t) * V; };
   u32x4 cz[NV], cr[NV], nz[NV], nr[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    cz[i] = load_piece(z + row * a.ld_z, at(i), a.width);
-    cr[i] = load_piece(res + row * a.ld_res, at(i), a.width);
+    cz[i] = load_step(z + row * a.ld_z, at(i), a.width);
+    cr[i] = load_step(res + row * a.ld_res, at(i), a.width);
   }
   float w1[NV][V], b1[NV][V], g[NV][V], w2[NV][V], b2[NV][V];
 #pragma unroll
@@ -172,13 +196,15 @@ __global__ __launch_bounds__(kMax) void step_fwd_kernel(const StepArgs a) {
     if (next < a.rows) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        nz[i] = load_piece(z + next * a.ld_z, at(i), a.width);
-        nr[i] = load_piece(res + next * a.ld_res, at(i), a.width);
+        nz[i] = load_step(z + next * a.ld_z, at(i), a.width);
+        nr[i] = load_step(res + next * a.ld_res, at(i), a.width);
       }
     }
     float f[NV][V], r[NV][V], st[4] = {0.0f, 1.0f, 0.0f, 1.0f};
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
+      trim_step<T>(cz[i], at(i), a.width);
+      trim_step<T>(cr[i], at(i), a.width);
       Piece<T>::widen(cz[i], f[i]);
       Piece<T>::widen(cr[i], r[i]);
     }
@@ -222,11 +248,11 @@ __global__ __launch_bounds__(kMax) void step_fwd_kernel(const StepArgs a) {
 // partial: [gridDim.x][4][pitch], A, B, dw2 and db2, those that are wanted.
 template <typename T, int kRow, int NV, int kMax>
 __global__ __launch_bounds__(kMax) void step_bwd_kernel(const StepArgs a) {
-  constexpr int V = Piece<T>::V, kThreads = kMax;  // of a workgroup that holds several rows
+  constexpr int V = Piece<T>::V;
   __shared__ float slots[4][2][16];
   // column sums of the rows of a workgroup that holds several
-  __shared__ float cols[kRow ? NV * V * kThreads : 1];
-  const StepPlace<kRow> p;
+  __shared__ float cols[kMax < 1024 ? NV * V * kMax : 1];
+  const StepPlace<kRow> p(a);
   auto at = [&](int i) { return (i * p.tpr + p.t) * V; };
   const T* z = static_cast<const T*>(a.z);
   const T* res = static_cast<const T*>(a.res);
@@ -253,34 +279,49 @@ __global__ __launch_bounds__(kMax) void step_bwd_kernel(const StepArgs a) {
     u32x4 z[NV], r[NV], o[NV], y[NV];
     float st[4];
   };
+  // a row past the last as zeros, which add nothing
   auto load = [&](Row& v, int64_t row) {
+    if (row >= a.rows) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) v.z[i] = v.r[i] = v.o[i] = v.y[i] = (u32x4){0u, 0u, 0u, 0u};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v.st[k] = 0.0f;
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      v.z[i] = load_piece(z + row * a.ld_z, at(i), a.width);
-      v.r[i] = load_piece(res + row * a.ld_res, at(i), a.width);
+      v.z[i] = load_step(z + row * a.ld_z, at(i), a.width);
+      v.r[i] = load_step(res + row * a.ld_res, at(i), a.width);
       v.o[i] = v.y[i] = (u32x4){0u, 0u, 0u, 0u};
-      if (dout) v.o[i] = load_piece(dout + row * a.ld_dout, at(i), a.width);
-      if (dy) v.y[i] = load_piece(dy + row * a.ld_dy, at(i), a.width);
+      if (dout) v.o[i] = load_step(dout + row * a.ld_dout, at(i), a.width);
+      if (dy) v.y[i] = load_step(dy + row * a.ld_dy, at(i), a.width);
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k) v.st[k] = a.stats[k * a.rows + row];
   };
   Row cur, nxt;
-  if (p.row < a.rows) load(cur, p.row);
+  if (!kAgain<kMax>) load(cur, p.row0 + p.in);
   int odd = 0;
-  for (int64_t row = p.row; row < a.rows; row += p.step, odd ^= 2) {
-    const int64_t next = row + p.step;
-    if (next < a.rows) load(nxt, next);
-    if (kAgain<kMax>) params();
+  for (int64_t base = p.row0; base < a.rows; base += p.step, odd ^= 2) {
+    const int64_t row = base + p.in;
+    if (kAgain<kMax>) {
+      load(cur, row);
+      params();
+    } else if (base + p.step < a.rows) {
+      load(nxt, row + p.step);
+    }
     const float zm = cur.st[0], zr = cur.st[1], om = cur.st[2], ostd = cur.st[3];
     float zh[NV][V], oh[NV][V], d[NV][V], s[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      float r[V], dv[V];
+      float r[V];
+      trim_step<T>(cur.z[i], at(i), a.width);
+      trim_step<T>(cur.r[i], at(i), a.width);
+      trim_step<T>(cur.o[i], at(i), a.width);
+      trim_step<T>(cur.y[i], at(i), a.width);
       Piece<T>::widen(cur.z[i], zh[i]);
       Piece<T>::widen(cur.r[i], r);
       Piece<T>::widen(cur.y[i], d[i]);
-      Piece<T>::widen(cur.o[i], dv);
 #pragma unroll
       for (int q = 0; q < V; ++q) {
         zh[i][q] = (zh[i][q] - zm) * zr;  // without the norm after the block 0 and 1: z
@@ -293,7 +334,7 @@ __global__ __launch_bounds__(kMax) void step_bwd_kernel(const StepArgs a) {
         s[1] = __builtin_fmaf(d[i][q], oh[i][q], s[1]);
       }
     }
-    if (dy) step_sums<kRow, 2>(s, slots[odd]);
+    if (dy) step_sums<kRow, 2>(s, slots[odd], p.first, p.waves);
     float mean = a.rms ? 0.0f : s[0] * a.inv, proj = s[1] * a.inv;
     s[0] = s[1] = 0.0f;
 #pragma unroll
@@ -311,10 +352,10 @@ __global__ __launch_bounds__(kMax) void step_bwd_kernel(const StepArgs a) {
         s[0] += d[i][q];
         s[1] = __builtin_fmaf(d[i][q], zh[i][q], s[1]);
       }
-      store_piece(static_cast<T*>(a.dres) + row * a.ld_dres, at(i), a.width, out);
+      if (row < a.rows) store_piece(static_cast<T*>(a.dres) + row * a.ld_dres, at(i), a.width, out);
     }
     if (a.post) {
-      step_sums<kRow, 2>(s, slots[odd + 1]);
+      step_sums<kRow, 2>(s, slots[odd + 1], p.first, p.waves);
       mean = a.rms ? 0.0f : s[0] * a.inv;
       proj = s[1] * a.inv;
     }
@@ -323,9 +364,9 @@ __global__ __launch_bounds__(kMax) void step_bwd_kernel(const StepArgs a) {
       float out[V];
 #pragma unroll
       for (int q = 0; q < V; ++q) out[q] = a.post ? zr * (d[i][q] - mean - zh[i][q] * proj) : d[i][q];
-      store_piece(static_cast<T*>(a.dz) + row * a.ld_dz, at(i), a.width, out);
+      if (row < a.rows) store_piece(static_cast<T*>(a.dz) + row * a.ld_dz, at(i), a.width, out);
     }
-    cur = nxt;
+    if (!kAgain<kMax>) cur = nxt;
   }
   if (!a.wanted) return;
   const int pitch = step_pitch(a.width);
@@ -333,7 +374,7 @@ __global__ __launch_bounds__(kMax) void step_bwd_kernel(const StepArgs a) {
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     if (!(a.wanted >> k & 1)) continue;
-    if (kRow == 0) {
+    if (a.rpb == 1) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         if (at(i) + V <= a.width) {
@@ -350,21 +391,20 @@ __global__ __launch_bounds__(kMax) void step_bwd_kernel(const StepArgs a) {
       }
       continue;
     }
-    __syncthreads();
-    // element (i, q) of lane t at ((i V + q) tpr + t): lanes side by side
-    constexpr int kPer = kRow ? kRow : 1, kRows = kThreads / kPer;
+    if constexpr (kMax < 1024) {
+      __syncthreads();
+      // element (i, q) of thread t of a row at ((i V + q) tpr + t): threads side by side
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
+      for (int i = 0; i < NV; ++i)
 #pragma unroll
-      for (int q = 0; q < V; ++q)
-        cols[(threadIdx.x / kPer * NV * V + i * V + q) * kPer + p.t] = sum[k][i][q];
-    __syncthreads();
-    for (int c = threadIdx.x; c < a.width; c += kThreads) {
-      const int piece = c / V, from = ((piece / kPer) * V + c % V) * kPer + piece % kPer;
-      float v = 0.0f;
-#pragma unroll
-      for (int r = 0; r < kRows; ++r) v += cols[r * NV * V * kPer + from];
-      out[static_cast<int64_t>(k) * pitch + c] = v;
+        for (int q = 0; q < V; ++q) cols[(p.in * NV * V + i * V + q) * p.tpr + p.t] = sum[k][i][q];
+      __syncthreads();
+      for (int c = threadIdx.x; c < a.width; c += blockDim.x) {
+        const int piece = c / V, from = ((piece / p.tpr) * V + c % V) * p.tpr + piece % p.tpr;
+        float v = 0.0f;
+        for (int r = 0; r < a.rpb; ++r) v += cols[r * NV * V * p.tpr + from];
+        out[static_cast<int64_t>(k) * pitch + c] = v;
+      }
     }
   }
 }
@@ -421,38 +461,47 @@ __global__ __launch_bounds__(256) void step_zero_kernel(const StepGrads g, int w
     if (p) p[c] = 0.0f;
 }
 
-// Threads of a row (a workgroup of its own where they are not 16 or 64) and
-// pieces a thread.
+// Threads of a row and pieces a thread, rows of a workgroup. Rows wider than a
+// wave's pieces take whole waves. The backward fills a workgroup of up to 768
+// threads with rows, so that there are few partial rows of column sums.
 struct StepShape {
-  int row, threads, pieces;  // row: 16, 64, or 0
+  int row, tpr, rpb, pieces;  // row: 16, 64, or 0: whole waves
+  int threads() const { return tpr * rpb; }
 };
 StepShape step_shape(const moe_residual_norm& n, bool bwd) {
   const int V = n.dtype == MOE_BF16 ? 8 : 4, p = (n.width + V - 1) / V;  // pieces of a row
-  const int waves = bwd ? kBwdThreads : kFwdThreads;
-  if (p <= 16) return {16, waves, 1};
-  if (p <= 64) return {64, waves, 1};
-  if (V == 4 && p <= 128) return {64, waves, 2};
-  if (p <= 1024) return {0, (p + 63) / 64 * 64, 1};
-  return {0, p <= 2048 ? (p + 127) / 128 * 64 : 1024, p <= 2048 ? 2 : 4};
+  const int most = bwd ? kBwdThreads : kFwdThreads;
+  if (p <= 16) return {16, 16, most / 16, 1};
+  if (p <= 64) return {64, 64, most / 64, 1};
+  if (V == 4 && p <= 128) return {64, 64, most / 64, 2};
+  auto waves = [](int pieces) { return (pieces + 63) / 64 * 64; };
+  const int one = waves(p), two = waves((p + 1) / 2);
+  if (!bwd) return p <= 1024 ? StepShape{0, one, 1, 1} : p <= 2048 ? StepShape{0, two, 1, 2} : StepShape{0, 1024, 1, 4};
+  if (one <= most) return {0, one, most / one, 1};
+  if (V == 4 && two <= most) return {0, two, most / two, 2};
+  return one <= 1024 ? StepShape{0, one, 1, 1} : two <= 1024 ? StepShape{0, two, 1, 2} : StepShape{0, 1024, 1, 4};
 }
 
-template <int kWaves, typename F>
+template <bool kBwd, typename F>
 void with_step_shape(int dtype, const StepShape& r, F&& f) {
+  // the largest workgroup of a kernel: what its registers are for
+  constexpr int kSome = kBwd ? kBwdThreads : kFwdThreads, kWide = kBwd ? kBwdThreads : 512;
 #define MOE_STEP_CASE(T, ROW, NV, MAX)                                \
-  if (r.row == ROW && r.pieces == NV && (ROW || r.threads <= MAX))    \
+  if (r.row == ROW && r.pieces == NV && r.threads() <= MAX)    \
   return f(T{}, std::integral_constant<int, ROW>{}, std::integral_constant<int, NV>{}, \
            std::integral_constant<int, MAX>{})
   if (dtype == MOE_BF16) {
-    MOE_STEP_CASE(bf16_t, 16, 1, kWaves);
-    MOE_STEP_CASE(bf16_t, 64, 1, kWaves);
-    MOE_STEP_CASE(bf16_t, 0, 1, 512);
+    MOE_STEP_CASE(bf16_t, 16, 1, kSome);
+    MOE_STEP_CASE(bf16_t, 64, 1, kSome);
+    MOE_STEP_CASE(bf16_t, 0, 1, kWide);
     MOE_STEP_CASE(bf16_t, 0, 1, 1024);
     MOE_STEP_CASE(bf16_t, 0, 2, 1024);
   } else {
-    MOE_STEP_CASE(float, 16, 1, kWaves);
-    MOE_STEP_CASE(float, 64, 1, kWaves);
-    MOE_STEP_CASE(float, 64, 2, kWaves);
-    MOE_STEP_CASE(float, 0, 1, 512);
+    MOE_STEP_CASE(float, 16, 1, kSome);
+    MOE_STEP_CASE(float, 64, 1, kSome);
+    MOE_STEP_CASE(float, 64, 2, kSome);
+    MOE_STEP_CASE(float, 0, 1, kWide);
+    if constexpr (kBwd) MOE_STEP_CASE(float, 0, 2, kWide);
     MOE_STEP_CASE(float, 0, 1, 1024);
     MOE_STEP_CASE(float, 0, 2, 1024);
     MOE_STEP_CASE(float, 0, 4, 1024);
@@ -460,14 +509,12 @@ void with_step_shape(int dtype, const StepShape& r, F&& f) {
 #undef MOE_STEP_CASE
 }
 
-int rows_per_block(const StepShape& r) { return r.row ? r.threads / r.row : 1; }
-
-// Workgroups of the backward: as many as are at once on the chip.
+// Workgroups of the backward: as many as are at once on the chip, one a CU where
+// they are full.
 int step_bwd_blocks(const moe_residual_norm& n) {
   const StepShape r = step_shape(n, true);
-  const int64_t need = (n.rows + rows_per_block(r) - 1) / rows_per_block(r);
-  const int64_t most = 256 * (r.threads >= 768 ? 1 : 768 / r.threads);
-  return static_cast<int>(need < 1 ? 1 : (need > most ? most : need));
+  const int64_t need = (n.rows + r.rpb - 1) / r.rpb;
+  return static_cast<int>(need < 1 ? 1 : (need > 256 ? 256 : need));
 }
 
 StepArgs step_args(const moe_residual_norm& n) {
@@ -512,11 +559,13 @@ hipError_t launch_residual_norm(const moe_residual_norm& n, const void* z, const
   a.y = y;
   a.stats = stats;
   const StepShape r = step_shape(n, false);
-  with_step_shape<kFwdThreads>(n.dtype, r, [&](auto t, auto row, auto nv, auto max) {
-    const int64_t need = (n.rows + rows_per_block(r) - 1) / rows_per_block(r);
-    const int64_t most = static_cast<int64_t>(cu_count()) * (1536 / r.threads);
+  a.tpr = r.tpr;
+  a.rpb = r.rpb;
+  with_step_shape<false>(n.dtype, r, [&](auto t, auto row, auto nv, auto max) {
+    const int64_t need = (n.rows + r.rpb - 1) / r.rpb;
+    const int64_t most = static_cast<int64_t>(cu_count()) * (1536 / r.threads());
     MOE_LAUNCH("residual_norm", (step_fwd_kernel<decltype(t), decltype(row)::value, decltype(nv)::value, decltype(max)::value>),
-               dim3(static_cast<unsigned>(need < most ? need : most)), dim3(r.threads), 0, s, a);
+               dim3(static_cast<unsigned>(need < most ? need : most)), dim3(r.threads()), 0, s, a);
   });
   return hipGetLastError();
 }
@@ -549,10 +598,12 @@ hipError_t launch_residual_norm_bwd(const moe_residual_norm& n, const void* z, c
   a.partial = static_cast<float*>(ws);
   a.wanted = wanted;
   const StepShape r = step_shape(n, true);
+  a.tpr = r.tpr;
+  a.rpb = r.rpb;
   const int blocks = step_bwd_blocks(n);
-  with_step_shape<kBwdThreads>(n.dtype, r, [&](auto t, auto row, auto nv, auto max) {
+  with_step_shape<true>(n.dtype, r, [&](auto t, auto row, auto nv, auto max) {
     MOE_LAUNCH("residual_norm_bwd", (step_bwd_kernel<decltype(t), decltype(row)::value, decltype(nv)::value, decltype(max)::value>),
-               dim3(blocks), dim3(r.threads), 0, s, a);
+               dim3(blocks), dim3(r.threads()), 0, s, a);
   });
   if (wanted)
     MOE_LAUNCH("residual_norm_sum", step_sum_kernel, dim3((n.width + kSumCols - 1) / kSumCols),
