@@ -17,7 +17,7 @@ from __future__ import annotations
 
 import ctypes
 from dataclasses import dataclass
-from functools import lru_cache
+from functools import cached_property, lru_cache
 from typing import Dict, Optional
 
 import torch
@@ -724,11 +724,12 @@ class Linear:
         return moe_linear(*self._fields)
 
 
-@lru_cache(maxsize=256)
-def _linear(l):
-    c = l.struct()
-    return (ctypes.byref(c), moe_linear_saved_bytes(c), torch.Size((l.tokens, l.inputs)),
-            torch.Size((l.inputs, l.outputs)), torch.Size((l.tokens, l.outputs)), _TORCH[l.dtype])
+    @cached_property
+    def _plan(self):
+        c = self.struct()
+        return (ctypes.byref(c), moe_linear_saved_bytes(c), torch.Size((self.tokens, self.inputs)),
+                torch.Size((self.inputs, self.outputs)), torch.Size((self.tokens, self.outputs)),
+                torch.Size((self.outputs,)), _TORCH[self.dtype])
 
 
 @dataclass
@@ -762,12 +763,12 @@ def linear(l: Linear, x, w, buf: LinearBuffers, bias=None, residual=None, traini
            stream=None):
     """The product of x [tokens, inputs] and w [inputs, outputs] with its
     epilogue; bias is fp32. Returns buf.y."""
-    c, nsv, xs, ws, ys, dt = _linear(l)
+    c, nsv, xs, ws, ys, bs, dt = l._plan
     dev, y = x.device, buf.y
     _want("x", x, xs, dt, dev)
     _want("w", w, ws, dt, dev)
     if bias is not None:
-        _want("bias", bias, (l.outputs,), torch.float32, dev)
+        _want("bias", bias, bs, torch.float32, dev)
     if residual is not None:
         _want("residual", residual, ys, dt, dev)
     _want("y", y, ys, dt, dev)
@@ -785,7 +786,7 @@ def linear_backward(l: Linear, x, w, grad_out, buf: LinearBuffers, bias: bool = 
     """Gradients of sum(y * grad_out) after ``linear(..., training=True)`` with
     the same buffers: (grad_x, grad_w, grad_bias), the last None where bias is
     False; the residual's gradient is grad_out."""
-    c, nsv, xs, ws, ys, dt = _linear(l)
+    c, nsv, xs, ws, ys, bs, dt = l._plan
     dev = x.device
     _want("x", x, xs, dt, dev)
     _want("w", w, ws, dt, dev)
@@ -794,7 +795,7 @@ def linear_backward(l: Linear, x, w, grad_out, buf: LinearBuffers, bias: bool = 
     _want("grad_x", buf.grad_x, xs, dt, dev)
     _want("gradient of w", buf.grad_w, ws, _TORCH[l.grad_dtype], dev)
     if bias:
-        _want("gradient of bias", buf.grad_bias, (l.outputs,), torch.float32, dev)
+        _want("gradient of bias", buf.grad_bias, bs, torch.float32, dev)
     _want_bytes("workspace", buf.workspace, 0, dev)
     _run("moe_linear_bwd", dev, stream, load().moe_linear_bwd, c, x.data_ptr(), w.data_ptr(),
          buf.saved.data_ptr(), grad_out.data_ptr(), buf.grad_x.data_ptr(), buf.grad_w.data_ptr(),
@@ -825,14 +826,16 @@ class ResidualNorm:
                                  int(self.post), int(self.pre), self.eps, self.scale, *lds)
 
 
+    @cached_property
+    def _plan(self):
+        # what every call compares with, and the C problem of contiguous matrices
+        return (torch.Size((self.rows, self.width)), torch.Size((4, self.rows)), torch.Size((self.width,)),
+                _TORCH[self.dtype], ctypes.byref(self.struct()))
+
+
 @lru_cache(maxsize=256)
 def _step(n, *lds):
     return ctypes.byref(n.struct(*lds))
-
-
-@lru_cache(maxsize=256)
-def _step_shapes(n):
-    return torch.Size((n.rows, n.width)), torch.Size((4, n.rows)), _TORCH[n.dtype]
 
 
 @dataclass
@@ -846,6 +849,8 @@ class ResidualNormBuffers:
     grad_res: Optional[object] = None
     grads: Optional[Dict] = None
     workspace: Optional[object] = None
+    # what allocate_residual_norm made, with its problem and device: as NormBuffers.made
+    made: Optional[tuple] = None
 
 
 def allocate_residual_norm(n: ResidualNorm, device="cuda", training: bool = False) -> ResidualNormBuffers:
@@ -863,21 +868,24 @@ def allocate_residual_norm(n: ResidualNorm, device="cuda", training: bool = Fals
         b.grad_z, b.grad_res = matrix(), matrix()
         b.grads = {name: torch.empty(n.width, **f32) for name in NORM_PARAMS}
         b.workspace = torch.empty(nws, dtype=torch.uint8, device=device)
+    b.made = (n, device, b.out, b.y, b.stats, b.grad_z, b.grad_res, b.workspace)
     return b
 
 
-def _want_step(n, z, res, params):
-    shape, stats, dt = _step_shapes(n)
-    dev = z.device
-    ld_z, ld_res = _want_rows("z", z, shape, dt, dev), _want_rows("res", res, shape, dt, dev)
-    ptrs = []
+def _step_params(params, shape, dev, struct=moe_norm_params):
+    f32, ptrs = torch.float32, []
     for name in NORM_PARAMS:
         t = params.get(name)
         if t is not None:
-            _want(name, t, (n.width,), torch.float32, dev)
+            if t.shape != shape or t.dtype is not f32 or t.device != dev or not t.is_contiguous():
+                _refuse(name, t, shape, f32, dev)
             t = t.data_ptr()
         ptrs.append(t)
-    return shape, stats, dt, dev, ld_z, ld_res, moe_norm_params(*ptrs)
+    return struct(*ptrs)
+
+
+def _fits(t, shape, dt, dev):
+    return t.shape == shape and t.dtype is dt and t.device == dev and t.is_contiguous()
 
 
 def residual_norm(n: ResidualNorm, z, res, params: Dict, buf: ResidualNormBuffers, stream=None):
@@ -885,18 +893,23 @@ def residual_norm(n: ResidualNorm, z, res, params: Dict, buf: ResidualNormBuffer
     (rows may be strided); params may hold post_weight, post_bias, gate,
     pre_weight and pre_bias (fp32). Returns (buf.out, buf.y), with buf.stats
     kept for the backward pass."""
-    shape, stats, dt, dev, ld_z, ld_res, p = _want_step(n, z, res, params)
-    ld_out, ld_y, y = _want_rows("out", buf.out, shape, dt, dev), 0, None
-    if n.pre:
-        y = buf.y
-        if y is None:
-            raise ValueError("y: the buffers were allocated for a step without the norm before the next block")
-        ld_y, y = _want_rows("y", y, shape, dt, dev), y.data_ptr()
-    _want("stats", buf.stats, stats, torch.float32, dev)
-    _run("moe_residual_norm_fwd", dev, stream, load().moe_residual_norm_fwd,
-         _step(n, ld_z, ld_res, ld_out, ld_y, 0, 0, 0, 0), z.data_ptr(), res.data_ptr(), ctypes.byref(p),
-         buf.out.data_ptr(), y, buf.stats.data_ptr())
-    return buf.out, buf.y if n.pre else None
+    shape, stats, width, dt, c = n._plan
+    dev, out, y, st, m = z.device, buf.out, buf.y, buf.stats, buf.made
+    known = m and m[0] is n and m[1] == dev and out is m[2] and y is m[3] and st is m[4]
+    if not (known and _fits(z, shape, dt, dev) and _fits(res, shape, dt, dev)):
+        lds = [_want_rows(name, t, shape, dt, dev) for name, t in (("z", z), ("res", res), ("out", out))]
+        if n.pre:
+            if y is None:
+                raise ValueError("y: the buffers were allocated for a step without the norm before the next block")
+            lds.append(_want_rows("y", y, shape, dt, dev))
+        _want("stats", st, stats, torch.float32, dev)
+        c = _step(n, *lds)
+    if not n.pre:
+        y = None
+    p = _step_params(params, width, dev)
+    _run("moe_residual_norm_fwd", dev, stream, load().moe_residual_norm_fwd, c, z.data_ptr(), res.data_ptr(),
+         ctypes.byref(p), out.data_ptr(), None if y is None else y.data_ptr(), st.data_ptr())
+    return out, y
 
 
 def residual_norm_backward(n: ResidualNorm, z, res, params: Dict, grad_out, grad_y,
@@ -905,26 +918,31 @@ def residual_norm_backward(n: ResidualNorm, z, res, params: Dict, grad_out, grad
     ``residual_norm`` with the same buffers: (grad_z, grad_res, {the gradients,
     fp32, of the parameters that params holds}). grad_out may be None; grad_y is
     None without the norm before the next block."""
-    shape, stats, dt, dev, ld_z, ld_res, p = _want_step(n, z, res, params)
-    gz, gr, g = buf.grad_z, buf.grad_res, buf.grads
+    shape, stats, width, dt, c = n._plan
+    dev, st, gz, gr, ws, m, f32 = z.device, buf.stats, buf.grad_z, buf.grad_res, buf.workspace, buf.made, torch.float32
     if gz is None:
         raise ValueError("the buffers were allocated without training=True")
     if (grad_y is not None) != n.pre:
         raise ValueError("grad_y: expected exactly where there is a norm before the next block")
-    ld_go = 0 if grad_out is None else _want_rows("grad_out", grad_out, shape, dt, dev)
-    ld_gy = 0 if grad_y is None else _want_rows("grad_y", grad_y, shape, dt, dev)
-    ld_gz, ld_gr = _want_rows("grad_z", gz, shape, dt, dev), _want_rows("grad_res", gr, shape, dt, dev)
-    _want("stats", buf.stats, stats, torch.float32, dev)
-    g = {name: g[name] for name in NORM_PARAMS if params.get(name) is not None}
-    for name, t in g.items():
-        _want("gradient of " + name, t, (n.width,), torch.float32, dev)
-    _want_bytes("workspace", buf.workspace, 0, dev)
-    grads = norm_grads_struct(g)
-    _run("moe_residual_norm_bwd", dev, stream, load().moe_residual_norm_bwd,
-         _step(n, ld_z, ld_res, 0, 0, ld_go, ld_gy, ld_gz, ld_gr), z.data_ptr(), res.data_ptr(),
-         ctypes.byref(p), buf.stats.data_ptr(), _ptr(grad_out), _ptr(grad_y), gz.data_ptr(), gr.data_ptr(),
-         ctypes.byref(grads), buf.workspace.data_ptr(), buf.workspace.numel())
-    return gz, gr, g
+    known = (m and m[0] is n and m[1] == dev and st is m[4] and gz is m[5] and gr is m[6] and ws is m[7]
+             and _fits(z, shape, dt, dev) and _fits(res, shape, dt, dev))
+    if not (known and (grad_out is None or _fits(grad_out, shape, dt, dev))
+            and (grad_y is None or _fits(grad_y, shape, dt, dev))):
+        ld_z, ld_res = _want_rows("z", z, shape, dt, dev), _want_rows("res", res, shape, dt, dev)
+        ld_go = 0 if grad_out is None else _want_rows("grad_out", grad_out, shape, dt, dev)
+        ld_gy = 0 if grad_y is None else _want_rows("grad_y", grad_y, shape, dt, dev)
+        ld_gz, ld_gr = _want_rows("grad_z", gz, shape, dt, dev), _want_rows("grad_res", gr, shape, dt, dev)
+        _want("stats", st, stats, f32, dev)
+        _want_bytes("workspace", ws, 0, dev)
+        c = _step(n, ld_z, ld_res, 0, 0, ld_go, ld_gy, ld_gz, ld_gr)
+    p = _step_params(params, width, dev)
+    grads = {name: buf.grads[name] for name in NORM_PARAMS if params.get(name) is not None}
+    g = _step_params(grads, width, dev, moe_norm_grads)
+    _run("moe_residual_norm_bwd", dev, stream, load().moe_residual_norm_bwd, c, z.data_ptr(), res.data_ptr(),
+         ctypes.byref(p), st.data_ptr(), None if grad_out is None else grad_out.data_ptr(),
+         None if grad_y is None else grad_y.data_ptr(), gz.data_ptr(), gr.data_ptr(),
+         ctypes.byref(g), ws.data_ptr(), ws.numel())
+    return gz, gr, grads
 
 
 # ------------------------------------------------------ balance of the router
@@ -947,11 +965,12 @@ class BalanceLoss:
                            self.balance, self.z)
 
 
-@lru_cache(maxsize=256)
-def _balance(b):
-    c = b.struct()
-    return (ctypes.byref(c), moe_balance_saved_bytes(c), torch.Size((b.tokens, b.d_model)),
-            torch.Size((b.d_model, b.experts)), _TORCH[b.dtype])
+    @cached_property
+    def _plan(self):
+        c = self.struct()
+        return (ctypes.byref(c), moe_balance_saved_bytes(c), torch.Size((self.tokens, self.d_model)),
+                torch.Size((self.d_model, self.experts)), torch.Size((self.tokens, self.top_k)),
+                torch.Size((self.experts,)), _TORCH[self.dtype])
 
 
 @dataclass
@@ -965,6 +984,8 @@ class BalanceBuffers:
     saved: Optional[object] = None
     grad_x: Optional[object] = None
     grad_router: Optional[object] = None
+    # what allocate_balance_loss made, with its problem and device: as NormBuffers.made
+    made: Optional[tuple] = None
 
 
 def allocate_balance_loss(b: BalanceLoss, device="cuda", training: bool = False) -> BalanceBuffers:
@@ -980,6 +1001,7 @@ def allocate_balance_loss(b: BalanceLoss, device="cuda", training: bool = False)
         buf.saved = torch.empty(moe_balance_saved_bytes(c), dtype=torch.uint8, device=device)
         buf.grad_x = torch.empty((b.tokens, b.d_model), dtype=_TORCH[b.dtype], device=device)
         buf.grad_router = torch.empty((b.d_model, b.experts), **f32)
+    buf.made = (b, device, buf.loss, buf.mean_prob, buf.counts, buf.workspace)
     return buf
 
 
@@ -999,16 +1021,19 @@ def balance_loss(b: BalanceLoss, x, w_router, topk_idx, buf: BalanceBuffers, mas
     [tokens, top_k] was made of (the routing's dictionary holds it); mask [tokens]
     (bool or uint8) leaves out tokens where it is false. Returns buf.loss, with
     buf.mean_prob and buf.counts beside it."""
-    c, nsv, xs, ws, dt = _balance(b)
+    c, nsv, xs, ws, ks, es, dt = b._plan
     dev = x.device
     _want("x", x, xs, dt, dev)
     _want("w_router", w_router, ws, torch.float32, dev)
-    _want("topk_idx", topk_idx, (b.tokens, b.top_k), torch.int32, dev)
+    _want("topk_idx", topk_idx, ks, torch.int32, dev)
     m = _want_mask(mask, b, dev)
-    _want("counts", buf.counts, (b.experts,), torch.int32, dev)
-    _want("mean_prob", buf.mean_prob, (b.experts,), torch.float32, dev)
-    _want("loss", buf.loss, (3,), torch.float32, dev)
-    _want_bytes("workspace", buf.workspace, 0, dev)
+    made = buf.made
+    if not (made and made[0] is b and made[1] == dev and made[2] is buf.loss and made[3] is buf.mean_prob
+            and made[4] is buf.counts and made[5] is buf.workspace):
+        _want("counts", buf.counts, es, torch.int32, dev)
+        _want("mean_prob", buf.mean_prob, es, torch.float32, dev)
+        _want("loss", buf.loss, (3,), torch.float32, dev)
+        _want_bytes("workspace", buf.workspace, 0, dev)
     if training:
         _want_saved(buf, nsv, dev)
     _run("moe_balance_loss", dev, stream, load().moe_balance_loss, c, x.data_ptr(), w_router.data_ptr(),
@@ -1024,7 +1049,7 @@ def balance_loss_backward(b: BalanceLoss, x, w_router, buf: BalanceBuffers, grad
     buffers and mask: (grad_x, grad_router). w_router is the forward's, whose
     values the buffers hold (only its shape is looked at). add_to: a pair of gradients, the
     layer's own for instance, that they are added to in place of the buffers'."""
-    c, nsv, xs, ws, dt = _balance(b)
+    c, nsv, xs, ws, _, _, dt = b._plan
     dev = x.device
     gx, gw = (buf.grad_x, buf.grad_router) if add_to is None else add_to
     _want("x", x, xs, dt, dev)
