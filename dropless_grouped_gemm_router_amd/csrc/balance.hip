@@ -37,6 +37,11 @@ struct BalArgs {
   const int32_t* parts;   // [kCountBlocks][64] counts by expert, [kCountBlocks] kept tokens
   int count_blocks;
   float* stats;           // [workgroups][65]: sums of p by expert, of lse^2
+  // few tokens, inference (nothing waits for the counts): the logits' workgroups
+  // count their own tokens and split W themselves; else null
+  const int32_t* idx;
+  int32_t* own;           // [workgroups][65]: counts by expert, kept tokens
+  const float* w;
 };
 
 // ---------------------------------------------------- counts, and W in operands
@@ -103,6 +108,41 @@ __device__ void turn_router(const float* __restrict__ w, int d, int E, int EB, u
   out[static_cast<int64_t>(i / 64) * 128 + 64 + lane] = Piece<T>::narrow(v);
 }
 
+// Counts by expert of the token-slots of tokens t0 .. t1 - 1 that are kept, into
+// `hist` (LDS) by the calling threads, this one the i-th of `threads`; hist[64]:
+// the kept tokens. Entries that are no expert are left out.
+__device__ __forceinline__ void count_slots(const BalArgs& a, const int32_t* __restrict__ idx, int64_t t0, int64_t t1,
+                                            int i, int threads, int* hist) {
+  constexpr int kBatch = 8;
+  const int64_t s1 = t1 * a.k;
+  for (int64_t s0 = t0 * a.k + i; s0 < s1; s0 += kBatch * threads) {
+    int e[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int64_t s = s0 + u * threads;
+      e[u] = idx[s < s1 ? s : s0];
+    }
+    if (a.mask) {
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int64_t s = s0 + u * threads;
+        // slots are below 2^31
+        if (!a.mask[static_cast<uint32_t>(s < s1 ? s : s0) / static_cast<uint32_t>(a.k)]) e[u] = -1;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u)
+      if (s0 + u * threads < s1 && static_cast<unsigned>(e[u]) < static_cast<unsigned>(a.E)) atomicAdd(hist + e[u], 1);
+  }
+  int kept = 0;
+  if (a.mask) {
+    for (int64_t t = t0 + i; t < t1; t += threads) kept += a.mask[t] != 0;
+  } else if (i == 0) {
+    kept = static_cast<int>(t1 - t0);
+  }
+  if (kept) atomicAdd(hist + 64, kept);
+}
+
 // Workgroups below count_blocks count their share of the tokens; the others
 // lay W out, for the backward too where there is a place for it.
 template <typename T>
@@ -124,36 +164,8 @@ __global__ __launch_bounds__(kCountThreads) void balance_count_kernel(const BalA
   }
   for (int i = threadIdx.x; i < kWaves * 65; i += kCountThreads) (&hist[0][0])[i] = 0;
   __syncthreads();
-  int* mine = hist[threadIdx.x >> 6];
   const int64_t t0 = a.T * blockIdx.x / a.count_blocks, t1 = a.T * (blockIdx.x + 1) / a.count_blocks;
-  const int64_t s1 = t1 * a.k;
-  constexpr int kBatch = 8;
-  for (int64_t s0 = t0 * a.k + threadIdx.x; s0 < s1; s0 += kBatch * kCountThreads) {
-    int e[kBatch];
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const int64_t s = s0 + u * kCountThreads;
-      e[u] = s < s1 ? idx[s] : -1;
-    }
-    if (a.mask) {
-#pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        const int64_t s = s0 + u * kCountThreads;
-        // slots are below 2^31
-        if (s < s1 && !a.mask[static_cast<uint32_t>(s) / static_cast<uint32_t>(a.k)]) e[u] = -1;
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u)
-      if (static_cast<unsigned>(e[u]) < static_cast<unsigned>(a.E)) atomicAdd(mine + e[u], 1);
-  }
-  int kept = 0;
-  if (a.mask) {
-    for (int64_t t = t0 + threadIdx.x; t < t1; t += kCountThreads) kept += a.mask[t] != 0;
-  } else if (threadIdx.x == 0) {
-    kept = static_cast<int>(t1 - t0);
-  }
-  if (kept) atomicAdd(mine + 64, kept);
+  count_slots(a, idx, t0, t1, threadIdx.x, kCountThreads, hist[threadIdx.x >> 6]);
   __syncthreads();
   if (threadIdx.x < 65) {
     int v = 0;
@@ -242,10 +254,11 @@ __device__ __forceinline__ void store_dl8(float* saved, int64_t t, int EP, int e
 // 32 further with the others. x goes from memory straight into operands (a row's
 // 128 bytes over four loads), W's operands come from the caches; both are loaded
 // a line ahead, W's each into the place of the one that has just been multiplied.
-template <typename T, int EB>
+// kRaw: W as it is, split on the way into the products.
+template <typename T, int EB, bool kRaw>
 __device__ __forceinline__ void logits(const BalArgs& a, const T* __restrict__ x, const u32x4* __restrict__ wf,
                                        int64_t row0, int first, int step, f32x16_t (&acc)[EB]) {
-  constexpr int S = BalOp<T>::S, kLine = 128 / sizeof(T);
+  constexpr int S = BalOp<T>::S, kLine = 128 / sizeof(T), V = Piece<T>::V;
   const int lane = threadIdx.x & 63, g = lane >> 5, r32 = lane & 31;
 #pragma unroll
   for (int b = 0; b < EB; ++b)
@@ -255,7 +268,8 @@ __device__ __forceinline__ void logits(const BalArgs& a, const T* __restrict__ x
   if (first >= lines) return;
   const int64_t r = row0 + r32;
   const T* row = x + (r < a.T ? r : a.T - 1) * a.d + g * (16 / static_cast<int>(sizeof(T)));
-  u32x4 xv[2][4], wv[4][EB][S];
+  u32x4 xv[2][4], wv[kRaw ? 1 : 4][EB][S];
+  float raw[kRaw ? 4 : 1][EB][V];
   auto load_x = [&](int set, int line) {
 #pragma unroll
     for (int q = 0; q < 4; ++q)
@@ -263,16 +277,37 @@ __device__ __forceinline__ void logits(const BalArgs& a, const T* __restrict__ x
   };
   auto load_w = [&](int q, int line) {
 #pragma unroll
-    for (int b = 0; b < EB; ++b)
+    for (int b = 0; b < EB; ++b) {
+      if constexpr (kRaw) {
+        const int e = 32 * b + r32;
+        const float* p = a.w + static_cast<int64_t>((line * 4 + q) * 2 * V + V * g) * a.E + (e < a.E ? e : 0);
 #pragma unroll
-      for (int s = 0; s < S; ++s)
-        wv[q][b][s] = wf[((static_cast<int64_t>(line * 4 + q)) * EB * S + b * S + s) * 64 + lane];
+        for (int j = 0; j < V; ++j) raw[q][b][j] = p[static_cast<int64_t>(j) * a.E];
+      } else {
+#pragma unroll
+        for (int s = 0; s < S; ++s)
+          wv[q][b][s] = wf[((static_cast<int64_t>(line * 4 + q)) * EB * S + b * S + s) * 64 + lane];
+      }
+    }
   };
   auto multiply = [&](int set, bool more, int next) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
 #pragma unroll
-      for (int b = 0; b < EB; ++b) BalOp<T>::step(wv[q][b], xv[set][q], acc[b]);
+      for (int b = 0; b < EB; ++b) {
+        if constexpr (kRaw) {
+          // experts past E take the first's weights; nothing reads their logits
+#pragma unroll
+          for (int s = 0; s < S; ++s) {
+            wv[0][b][s] = Piece<T>::narrow(raw[q][b]);
+            float back[V];
+            Piece<T>::widen(wv[0][b][s], back);
+#pragma unroll
+            for (int j = 0; j < V; ++j) raw[q][b][j] -= back[j];
+          }
+        }
+        BalOp<T>::step(wv[kRaw ? 0 : q][b], xv[set][q], acc[b]);
+      }
       if (more) load_w(q, next);
     }
   };
@@ -524,7 +559,7 @@ void balance_logits_kernel(const BalArgs a, const T* __restrict__ x, const u32x4
 // Fewer tokens: 32 a workgroup, whose KS waves share the columns. Their sums go
 // through LDS, from where the softmax takes eight experts of a token a lane,
 // 4 EB lanes to a token, so that all waves work on it.
-template <typename T, int EB, int KS>
+template <typename T, int EB, int KS, bool kRaw>
 __global__ __launch_bounds__(64 * KS) void balance_logits_few_kernel(const BalArgs a, const T* __restrict__ x,
                                                                      const u32x4* __restrict__ wf,
                                                                      T* __restrict__ saved) {
@@ -535,10 +570,16 @@ __global__ __launch_bounds__(64 * KS) void balance_logits_few_kernel(const BalAr
   __shared__ int tallies[KS][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t row0 = static_cast<int64_t>(blockIdx.x) * 32;
+  __shared__ int hist[65];
+  if constexpr (kRaw) {
+    if (threadIdx.x < 65) hist[threadIdx.x] = 0;
+    __syncthreads();
+    count_slots(a, a.idx, row0, row0 + 32 < a.T ? row0 + 32 : a.T, threadIdx.x, 64 * KS, hist);
+  }
   Tallies<64 * KS> counts;
   if (saved) counts.load(a);
   f32x16_t acc[EB];
-  logits<T, EB>(a, x, wf, row0, wave, KS, acc);
+  logits<T, EB, kRaw>(a, x, wf, row0, wave, KS, acc);
   const int n = saved ? counts.put(a, tallies) : 0;
 #pragma unroll
   for (int b = 0; b < EB; ++b)
@@ -627,19 +668,27 @@ __global__ __launch_bounds__(64 * KS) void balance_logits_few_kernel(const BalAr
     for (int u = 0; u < kUsed; ++u) v += sums[u][threadIdx.x];
     a.stats[static_cast<int64_t>(blockIdx.x) * 65 + (static_cast<int>(threadIdx.x) == EP ? 64 : threadIdx.x)] = v;
   }
+  if (kRaw && threadIdx.x < 65) a.own[static_cast<int64_t>(blockIdx.x) * 65 + threadIdx.x] = hist[threadIdx.x];
 }
 
-// The results from the workgroups' sums: 16 threads to an expert.
+// The results from the workgroups' sums, and from their counts or the count
+// blocks': 16 threads to an expert.
 __global__ __launch_bounds__(1024) void balance_loss_kernel(const BalArgs a, int groups, float balance, float z,
                                                             int32_t* __restrict__ counts,
                                                             float* __restrict__ mean_prob,
                                                             float* __restrict__ loss) {
   __shared__ float sums[16][64], zeds[16];
-  __shared__ int tallies[16][64];
+  __shared__ int tallies[16][64], kept[16];
   const int e = threadIdx.x % 64, j = threadIdx.x / 64;
   Tallies<1024> t;
-  t.load(a);
+  if (!a.own) t.load(a);
   float v = 0.0f, zed = 0.0f;
+  int c = 0, k = 0;
+  if (a.own) {
+#pragma unroll 16
+    for (int p = j; p < groups; p += 16) c += a.own[static_cast<int64_t>(p) * 65 + e];
+    for (int p = threadIdx.x; p < groups; p += 1024) k += a.own[static_cast<int64_t>(p) * 65 + 64];
+  }
   if (e < a.E) {
 #pragma unroll 16
     for (int p = j; p < groups; p += 16) v += a.stats[static_cast<int64_t>(p) * 65 + e];
@@ -648,7 +697,15 @@ __global__ __launch_bounds__(1024) void balance_loss_kernel(const BalArgs a, int
   sums[j][e] = v;
   zed = wave_sum(zed);
   if (e == 0) zeds[j] = zed;
-  const int n = t.put(a, tallies);
+  int n = 0;
+  if (a.own) {
+    tallies[j][e] = c;
+#pragma unroll
+    for (int o = 1; o < 64; o *= 2) k += __shfl_xor(k, o);
+    if (e == 0) kept[j] = k;
+  } else {
+    n = t.put(a, tallies);
+  }
   __syncthreads();
   if (j) return;
   float p = 0.0f, zz = 0.0f;
@@ -656,6 +713,7 @@ __global__ __launch_bounds__(1024) void balance_loss_kernel(const BalArgs a, int
   for (int u = 0; u < 16; ++u) {
     p += sums[u][e];
     zz += zeds[u];
+    if (a.own) n += kept[u];
   }
   p *= one_over(n);
   zz *= one_over(n);
@@ -1039,8 +1097,14 @@ int grad_ranges(const moe_balance& b) {
   return static_cast<int>(r < 1 ? 1 : r);
 }
 
+// Up to how many tokens the workgroups of an inference call split W and count
+// themselves, a launch less: bf16, 64 experts x 512, 200 tokens 10.1 and 13.6 us,
+// 8192 13.1 and 15.4; x 2048, 8192 tokens 24.3 and 24.8. (With 256-token workgroups
+// the last kernel would have 512 counts an expert to add: 131072 tokens, 45 and 41.5.)
+constexpr int64_t kRawTokens = 8192;
+
 struct BalLayout {
-  size_t parts, stats, wf, partial, total;
+  size_t parts, stats, own, wf, partial, total;
 };
 BalLayout bal_layout(const moe_balance& b) {
   BalLayout L{};
@@ -1054,6 +1118,7 @@ BalLayout bal_layout(const moe_balance& b) {
   L.parts = take(kCountBlocks * 65 * sizeof(int32_t));
   const int64_t rows = logits_rows(b.tokens, b.dtype);
   L.stats = take((b.tokens + rows - 1) / rows * 65 * sizeof(float));
+  L.own = take(b.tokens <= kRawTokens ? (b.tokens + rows - 1) / rows * 65 * sizeof(int32_t) : 0);
   L.wf = take(d * EP * (b.dtype == MOE_BF16 ? 6 : 4));
   L.total = o;
   o = 0;  // the backward has the place for itself
@@ -1073,8 +1138,10 @@ void launch_logits(const BalArgs& a, const T* x, const u32x4* wf, T* saved, hipS
   const dim3 grid(static_cast<unsigned>((a.T + rows - 1) / rows));
   if (rows == 256)
     MOE_LAUNCH("balance_logits", (balance_logits_kernel<T, EB>), grid, dim3(256), 0, s, a, x, wf, saved);
+  else if (a.w)
+    MOE_LAUNCH("balance_logits", (balance_logits_few_kernel<T, EB, 4, true>), grid, dim3(256), 0, s, a, x, wf, saved);
   else
-    MOE_LAUNCH("balance_logits", (balance_logits_few_kernel<T, EB, 4>), grid, dim3(256), 0, s, a, x, wf, saved);
+    MOE_LAUNCH("balance_logits", (balance_logits_few_kernel<T, EB, 4, false>), grid, dim3(256), 0, s, a, x, wf, saved);
 }
 
 template <typename T>
@@ -1087,15 +1154,21 @@ hipError_t balance_t(const moe_balance& b, const void* x, const float* w, const 
   u32x4* wf = reinterpret_cast<u32x4*>(W + L.wf);
   u32x4* wb = saved ? reinterpret_cast<u32x4*>(static_cast<char*>(saved) + saved_rows_bytes(b)) : nullptr;
   BalArgs a{b.tokens, b.experts, b.top_k, b.d_model, b.balance * static_cast<float>(b.experts), 2.0f * b.z, mask,
-            parts, 0, reinterpret_cast<float*>(W + L.stats)};
+            parts, 0, reinterpret_cast<float*>(W + L.stats), nullptr, nullptr, nullptr};
   int groups = 0;
   if (b.tokens > 0) {
-    const int64_t blocks = (b.tokens * b.top_k + 8 * kCountThreads - 1) / (8 * kCountThreads);
-    a.count_blocks = static_cast<int>(blocks > kCountBlocks ? kCountBlocks : blocks);
-    const int pieces = b.d_model / (2 * Piece<T>::V) * EB * 64 * (wb ? 2 : 1);
-    MOE_LAUNCH("balance_count", balance_count_kernel<T>,
-               dim3(a.count_blocks + (pieces + kCountThreads - 1) / kCountThreads), dim3(kCountThreads), 0, s, a, idx,
-               w, EB, wf, wb, parts);
+    if (!saved && b.tokens <= kRawTokens) {
+      a.idx = idx;
+      a.own = reinterpret_cast<int32_t*>(W + L.own);
+      a.w = w;
+    } else {
+      const int64_t blocks = (b.tokens * b.top_k + 8 * kCountThreads - 1) / (8 * kCountThreads);
+      a.count_blocks = static_cast<int>(blocks > kCountBlocks ? kCountBlocks : blocks);
+      const int pieces = b.d_model / (2 * Piece<T>::V) * EB * 64 * (wb ? 2 : 1);
+      MOE_LAUNCH("balance_count", balance_count_kernel<T>,
+                 dim3(a.count_blocks + (pieces + kCountThreads - 1) / kCountThreads), dim3(kCountThreads), 0, s, a,
+                 idx, w, EB, wf, wb, parts);
+    }
     if (EB == 1) launch_logits<T, 1>(a, static_cast<const T*>(x), wf, static_cast<T*>(saved), s);
     else launch_logits<T, 2>(a, static_cast<const T*>(x), wf, static_cast<T*>(saved), s);
     const int rows = logits_rows(b.tokens, b.dtype);

@@ -386,6 +386,10 @@ def check_balance(b, x, w, idx, mask, buf, gloss=None, clean=None):
     gx, gw = K.balance_loss_backward(b, x, w, buf, grad_loss=g, mask=mask)
     loss, p, counts, dx, dw = balance64(b, x if clean is None else clean, w, idx, mask, 1.0 if gloss is None else gloss)
     assert buf.counts.tolist() == counts.tolist()
+    watched = K.allocate_balance_loss(b, "cuda")
+    watched.workspace.fill_(255)
+    K.balance_loss(b, x, w, idx, watched, mask=mask)
+    assert all(torch.equal(getattr(watched, n), getattr(buf, n)) for n in ("loss", "mean_prob", "counts"))
     near("loss", buf.loss, loss, 2.0 ** -18)
     near("mean_prob", buf.mean_prob, p, 2.0 ** -18)
     # dl = p (c1 (f - sum f p) + 2 c2 lse): the first bracket cancels where the
@@ -402,7 +406,7 @@ def check_balance(b, x, w, idx, mask, buf, gloss=None, clean=None):
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("t,e,k,d", [
     (1, 1, 1, 128), (1, 64, 8, 512), (2, 2, 1, 128), (31, 5, 2, 256), (32, 8, 2, 512), (33, 32, 4, 384), (63, 33, 33, 128),
-    (200, 8, 2, 512), (257, 64, 64, 128), (1000, 47, 6, 1152), (4999, 33, 3, 1152), (5000, 64, 8, 512), (300, 16, 4, 8192),
+    (200, 8, 2, 512), (257, 64, 64, 128), (8192, 17, 2, 256), (8193, 40, 2, 256), (1000, 47, 6, 1152), (4999, 33, 3, 1152), (5000, 64, 8, 512), (300, 16, 4, 8192),
     (20000, 24, 4, 256)])
 def test_balance(t, e, k, d, dtype):
     note(f"balance {t} {e} {k} {d} {dtype}")
