@@ -70,28 +70,6 @@ __device__ __forceinline__ void step_sums(float (&v)[N], float (*slot)[16], int 
   }
 }
 
-// load_piece without a branch, for rows of V or more: a piece that is not whole
-// takes the row's last V elements, and where it is used trim_step moves its own
-// to the front, zeros behind them. (A wave with one lane at the row's end had every
-// other lane wait for its loads of single elements: 10000 x 1023 bf16, backward, 58
-// us against 31 at 1024.)
-template <typename T>
-__device__ __forceinline__ u32x4 load_step(const T* row, int c, int n) {
-  if (n < Piece<T>::V) return load_piece(row, c, n);
-  return load_any(row + min(c, n - Piece<T>::V));
-}
-template <typename T>
-__device__ __forceinline__ void trim_step(u32x4& v, int c, int n) {
-  const int past = c + Piece<T>::V - n;  // elements of the piece behind the row
-  if (past <= 0 || n < Piece<T>::V) return;
-  const int w = sizeof(T) == 2 ? past / 2 : past;
-  if (sizeof(T) == 2 && past & 1)
-    v = (u32x4){v[0] >> 16 | v[1] << 16, v[1] >> 16 | v[2] << 16, v[2] >> 16 | v[3] << 16, v[3] >> 16};
-  if (w & 1) v = (u32x4){v[1], v[2], v[3], 0u};
-  if (w & 2) v = (u32x4){v[2], v[3], 0u, 0u};
-  if (w >= 4) v = (u32x4){0u, 0u, 0u, 0u};
-}
-
 // V parameters from column c on: `fill` where there is no array, zeros past the
 // row, so that what is made of them there is zero.
 template <int V>
@@ -179,8 +157,8 @@ __global__ __launch_bounds__(kMax) void step_fwd_kernel(const StepArgs a) {
   u32x4 cz[NV], cr[NV], nz[NV], nr[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    cz[i] = load_step(z + row * a.ld_z, at(i), a.width);
-    cr[i] = load_step(res + row * a.ld_res, at(i), a.width);
+    cz[i] = load_near(z + row * a.ld_z, at(i), a.width);
+    cr[i] = load_near(res + row * a.ld_res, at(i), a.width);
   }
   float w1[NV][V], b1[NV][V], g[NV][V], w2[NV][V], b2[NV][V];
 #pragma unroll
@@ -196,15 +174,15 @@ __global__ __launch_bounds__(kMax) void step_fwd_kernel(const StepArgs a) {
     if (next < a.rows) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        nz[i] = load_step(z + next * a.ld_z, at(i), a.width);
-        nr[i] = load_step(res + next * a.ld_res, at(i), a.width);
+        nz[i] = load_near(z + next * a.ld_z, at(i), a.width);
+        nr[i] = load_near(res + next * a.ld_res, at(i), a.width);
       }
     }
     float f[NV][V], r[NV][V], st[4] = {0.0f, 1.0f, 0.0f, 1.0f};
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      trim_step<T>(cz[i], at(i), a.width);
-      trim_step<T>(cr[i], at(i), a.width);
+      trim_piece<T>(cz[i], at(i), a.width);
+      trim_piece<T>(cr[i], at(i), a.width);
       Piece<T>::widen(cz[i], f[i]);
       Piece<T>::widen(cr[i], r[i]);
     }
@@ -290,11 +268,11 @@ __global__ __launch_bounds__(kMax) void step_bwd_kernel(const StepArgs a) {
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      v.z[i] = load_step(z + row * a.ld_z, at(i), a.width);
-      v.r[i] = load_step(res + row * a.ld_res, at(i), a.width);
+      v.z[i] = load_near(z + row * a.ld_z, at(i), a.width);
+      v.r[i] = load_near(res + row * a.ld_res, at(i), a.width);
       v.o[i] = v.y[i] = (u32x4){0u, 0u, 0u, 0u};
-      if (dout) v.o[i] = load_step(dout + row * a.ld_dout, at(i), a.width);
-      if (dy) v.y[i] = load_step(dy + row * a.ld_dy, at(i), a.width);
+      if (dout) v.o[i] = load_near(dout + row * a.ld_dout, at(i), a.width);
+      if (dy) v.y[i] = load_near(dy + row * a.ld_dy, at(i), a.width);
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k) v.st[k] = a.stats[k * a.rows + row];
@@ -315,10 +293,10 @@ __global__ __launch_bounds__(kMax) void step_bwd_kernel(const StepArgs a) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       float r[V];
-      trim_step<T>(cur.z[i], at(i), a.width);
-      trim_step<T>(cur.r[i], at(i), a.width);
-      trim_step<T>(cur.o[i], at(i), a.width);
-      trim_step<T>(cur.y[i], at(i), a.width);
+      trim_piece<T>(cur.z[i], at(i), a.width);
+      trim_piece<T>(cur.r[i], at(i), a.width);
+      trim_piece<T>(cur.o[i], at(i), a.width);
+      trim_piece<T>(cur.y[i], at(i), a.width);
       Piece<T>::widen(cur.z[i], zh[i]);
       Piece<T>::widen(cur.r[i], r);
       Piece<T>::widen(cur.y[i], d[i]);
