@@ -25,6 +25,12 @@ namespace moe {
 namespace {
 
 constexpr int64_t kFewRows = 16, kFewRowsF32 = 128;
+// The serving form's workgroups: 16 waves over the whole of K where that is short,
+// else slices of K to 8 waves each and a second launch that adds them. One row,
+// bf16, one slice and slices: 1024 x 4096 7.3 and 10.5 us, 700 x 1001 7.4 and 10.8,
+// 4096 x 4096 11.8 and 10.5, 8192 x 2048 20 and 11; 8 rows, 2048 x 8192 8.4 and 10.9;
+// fp32, 64 rows, 512 x 2048 8.1 and 8.4, 16 rows, 1024 x 1024 12.8 and 10.9.
+constexpr int kRowsWaves = 16, kShortK = 2048, kShortKF32 = 512;
 
 size_t elem_bytes(const moe_linear& l) { return l.dtype == MOE_BF16 ? 2 : 4; }
 bool few_rows(const moe_linear& l) { return l.tokens <= (l.dtype == MOE_BF16 ? kFewRows : kFewRowsF32); }
@@ -269,14 +275,15 @@ __global__ __launch_bounds__(256) void lin_join_kernel(const float* __restrict__
 }
 
 // Few tokens. part: null (one slice of K), or the slices' sums [k_parts][rows][N].
-template <typename T, int kAct>
-__global__ __launch_bounds__(512) void lin_rows_kernel(const SkinnyArgs<T, 1> a, const LinOut<T> o, float* part) {
-  __shared__ float lds[kSkinnyWaves][kSkinnyLds];
-  float sum[2][1];
-  skinny_sums<T, 1, false>(a, lds, sum);
+template <typename T, int kAct, int kWaves>
+__global__ __launch_bounds__(64 * kWaves) void lin_rows_kernel(const SkinnyArgs<T, 1> a, const LinOut<T> o,
+                                                               float* part) {
+  __shared__ float lds[kWaves][kSkinnyLds];
+  float sum[16 / kWaves][1];
+  skinny_sums<T, 1, false, kWaves>(a, lds, sum);
 #pragma unroll
-  for (int v = 0; v < 2; ++v) {
-    const int64_t row = static_cast<int64_t>(blockIdx.y) * 16 + (threadIdx.x >> 6) + 8 * v;
+  for (int v = 0; v < 16 / kWaves; ++v) {
+    const int64_t row = static_cast<int64_t>(blockIdx.y) * 16 + (threadIdx.x >> 6) + kWaves * v;
     const int n = blockIdx.x * kSkinnyCols + (threadIdx.x & 63);
     const bool in = row < a.rows && n < a.N;
     if (!part) finish<T, kAct>(o, row, n, in, sum[v][0]);
@@ -390,11 +397,11 @@ LinLayout lin_layout(const moe_linear& l, bool training) {
   };
   auto sums = [&](int parts, size_t cells) { return take(parts > 1 ? parts * cells * sizeof(float) : 0); };
   if (few_rows(l)) {
-    // slices of K so that every CU has a workgroup, of two steps a wave at least
+    // slices of a long K so that every CU has a workgroup, of two steps a wave at least
     const int64_t blocks = T == 0 ? 1 : (N + kSkinnyCols - 1) / kSkinnyCols * ((T + 15) / 16);
     const int64_t most = (K + 2 * kSkinnyStep * kSkinnyWaves - 1) / (2 * kSkinnyStep * kSkinnyWaves);
     const int64_t want = (kCUs + blocks - 1) / blocks;
-    L.k_parts = static_cast<int>(want < most ? want : most);
+    L.k_parts = K <= static_cast<size_t>(es == 2 ? kShortK : kShortKF32) ? 1 : static_cast<int>(want < most ? want : most);
   } else {
     if (!in_place(l)) {
       L.wt = take(N * kp * es);
@@ -525,11 +532,12 @@ hipError_t lin_fwd_t(const moe_linear& l, const void* x, const void* w, const fl
     SkinnyArgs<T, 1> a{static_cast<const T*>(x), nullptr, K, {static_cast<const T*>(w)}, l.tokens, K, N, L.k_parts};
     const dim3 grid((N + kSkinnyCols - 1) / kSkinnyCols, static_cast<unsigned>((l.tokens + 15) / 16), L.k_parts);
     if (L.k_parts > 1) {
-      MOE_LAUNCH("linear_rows", (lin_rows_kernel<T, MOE_ACT_NONE>), grid, dim3(512), 0, s, a, o, part);
+      MOE_LAUNCH("linear_rows", (lin_rows_kernel<T, MOE_ACT_NONE, 8>), grid, dim3(512), 0, s, a, o, part);
       lin_join<T>("linear_join", l.act, part, L.k_parts, o, s);
     } else {
       with_act(l.act, [&](auto k) {
-        MOE_LAUNCH("linear_rows", (lin_rows_kernel<T, decltype(k)::value>), grid, dim3(512), 0, s, a, o, nullptr);
+        MOE_LAUNCH("linear_rows", (lin_rows_kernel<T, decltype(k)::value, kRowsWaves>), grid, dim3(64 * kRowsWaves), 0, s, a, o,
+                   nullptr);
       });
     }
     return hipGetLastError();

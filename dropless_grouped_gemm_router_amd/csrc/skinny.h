@@ -129,13 +129,13 @@ struct SkinnyArgs {
 };
 
 // Sums of this workgroup's columns over its slice of K, for 16 rows: after the
-// call thread t holds, for v = 0, 1, those of column t % 64 and row t / 64 +
-// 8 v of the tile, all kW of them. In LDS register
+// call thread t holds, for v < 16 / kWaves, those of column t % 64 and row t / 64 +
+// kWaves v of the tile, all kW of them. In LDS register
 // 4 q + j of a lane stands at 65 (4 q + j) + lane: both sides use all banks.
 constexpr int kSkinnyLds = 16 * 65;
-template <typename T, int kW, bool kLow>
+template <typename T, int kW, bool kLow, int kWaves = kSkinnyWaves>
 __device__ __forceinline__ void skinny_sums(const SkinnyArgs<T, kW>& a, float (*lds)[kSkinnyLds],
-                                            float (&sum)[2][kW]) {
+                                            float (&sum)[16 / kWaves][kW]) {
   // the wave's number as a scalar: a step past the end has to be branched over,
   // for MFMAs run whatever lanes are on
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -171,11 +171,11 @@ __device__ __forceinline__ void skinny_sums(const SkinnyArgs<T, kW>& a, float (*
   // two steps in flight
   int s = s0 + wave;
   if (s < s1) load(0, s);
-  for (; s < s1; s += 2 * kSkinnyWaves) {
-    if (s + kSkinnyWaves < s1) load(1, s + kSkinnyWaves);
+  for (; s < s1; s += 2 * kWaves) {
+    if (s + kWaves < s1) load(1, s + kWaves);
     multiply(0);
-    if (s + 2 * kSkinnyWaves < s1) load(0, s + 2 * kSkinnyWaves);
-    if (s + kSkinnyWaves < s1) multiply(1);
+    if (s + 2 * kWaves < s1) load(0, s + 2 * kWaves);
+    if (s + kWaves < s1) multiply(1);
   }
 
   const int c = lane;  // column that this thread adds up
@@ -188,10 +188,10 @@ __device__ __forceinline__ void skinny_sums(const SkinnyArgs<T, kW>& a, float (*
       for (int q = 0; q < 4; ++q) lds[wave][(4 * q + j) * 65 + lane] = acc[m][j][q];
     __syncthreads();
 #pragma unroll
-    for (int v = 0; v < 2; ++v) {
+    for (int v = 0; v < 16 / kWaves; ++v) {
       float t = 0.0f;
 #pragma unroll
-      for (int u = 0; u < kSkinnyWaves; ++u) t += lds[u][(c & 15) * 65 + (c >> 4) * 16 + wave + 8 * v];
+      for (int u = 0; u < kWaves; ++u) t += lds[u][(c & 15) * 65 + (c >> 4) * 16 + wave + kWaves * v];
       sum[v][m] = t;
     }
     __syncthreads();
