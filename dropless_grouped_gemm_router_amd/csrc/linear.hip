@@ -18,7 +18,11 @@
 // 128) it reads them once, straight into MFMA operands (skinny.h). The
 // backward's dx reads them as they are. da is made in one pass over dy that
 // also adds up dbias and pads the rows; without an activation dy itself is da.
+//
+// fp32 products of moderate size take both passes' operands from memory as they
+// are, in one launch each (direct.h).
 #include "dense.h"
+#include "direct.h"
 
 namespace moe {
 
@@ -32,6 +36,7 @@ constexpr int64_t kFewRows = 16, kFewRowsF32 = 128;
 // fp32, 64 rows, 512 x 2048 8.1 and 8.4, 16 rows, 1024 x 1024 12.8 and 10.9.
 constexpr int kRowsWaves = 16, kShortK = 2048, kShortKF32 = 512;
 
+int64_t pad4(int64_t v) { return (v + 3) / 4 * 4; }
 size_t elem_bytes(const moe_linear& l) { return l.dtype == MOE_BF16 ? 2 : 4; }
 bool few_rows(const moe_linear& l) { return l.tokens <= (l.dtype == MOE_BF16 ? kFewRows : kFewRowsF32); }
 // Elements between rows of the kept slopes.
@@ -355,6 +360,89 @@ __global__ __launch_bounds__(32 * kDaRows) void lin_da_kernel(const T* __restric
   if (col < n4) part[static_cast<int64_t>(blockIdx.y) * n4 + col] = v;
 }
 
+// ---------------------------------------------------- fp32 of moderate size
+
+// The products of one launch, their tiles one after the other; parts > 1: sums of
+// slices of k, [parts][M][ld], added by another launch.
+struct DirProduct {
+  DirOperand s, f;
+  int64_t K;
+  int64_t M;
+  int N;
+  int tiles_n, parts;
+  int64_t end;  // exclusive end of its workgroups
+  float* out;   // or the slices' sums
+  int64_t ld;
+};
+// This workgroup's tile and steps of k.
+struct DirPlace {
+  int64_t m0, n0, s0, s1;
+  int part;
+  __device__ DirPlace(const DirProduct& p, int64_t w) {
+    part = static_cast<int>(w % p.parts);
+    const int64_t tile = w / p.parts, steps = (p.K + kDirStep - 1) / kDirStep;
+    m0 = tile / p.tiles_n * kDirTile;
+    n0 = tile % p.tiles_n * kDirTile;
+    s0 = steps * part / p.parts;
+    s1 = steps * (part + 1) / p.parts;
+  }
+};
+__device__ __forceinline__ void dir_store(const DirProduct& p, const DirPlace& t, const float (&v)[8]) {
+  const int64_t m = t.m0 + (threadIdx.x >> 3);
+  const int n = static_cast<int>(t.n0) + (threadIdx.x & 7) * 8;
+  if (m < p.M && n < p.N) store8<float, false>(p.out + (t.part * p.M + m) * p.ld, n, p.N, v);
+}
+
+// y: x W, then what follows it.
+template <int kAct>
+__global__ __launch_bounds__(kDirThreads) void lin_direct_kernel(const DirProduct p, const LinOut<float> o) {
+  __shared__ float lds[kDirLds];
+  const DirPlace t(p, xcd_remap(blockIdx.x, gridDim.x));
+  float v[8];
+  dir_tile<kAlong, kAcross, false, false, false>(p.s, p.f, p.K, t.m0, t.n0, t.s0, t.s1, false, lds, nullptr, v);
+  if (p.parts > 1) return dir_store(p, t, v);
+  const int64_t m = t.m0 + (threadIdx.x >> 3);
+  const int n = static_cast<int>(t.n0) + (threadIdx.x & 7) * 8;
+  if (m >= p.M || n >= p.N) return;
+  float y[8], slope[8], b[8], r[8];
+#pragma unroll
+  for (int q = 0; q < 8; ++q) b[q] = r[q] = 0.0f;
+  if (o.bias) load8<float, false>(o.bias, n, p.N, b);
+  if (o.res) load8<float, false>(static_cast<const float*>(o.res) + m * p.N, n, p.N, r);
+#pragma unroll
+  for (int q = 0; q < 8; ++q) y[q] = lin_act<float, kAct>(v[q] + b[q], &slope[q]) + r[q];
+  store8<float, false>(static_cast<float*>(o.y) + m * o.ld, n, p.N, y);
+  if (kAct != MOE_ACT_NONE && o.slope.p) o.slope.put8(m, n, slope);
+}
+
+// dx = (dy slope) W^T and dW = x^T (dy slope), with the columns' sums for dbias
+// (null: not wanted; [parts of dW][pitch of its sums]) from the tiles of dW's first rows.
+template <bool kSlope>
+__global__ __launch_bounds__(kDirThreads) void lin_direct_bwd_kernel(const DirProduct dx, const DirProduct dw,
+                                                                    float* dbias, int64_t ld_bias) {
+  __shared__ float lds[kDirLds];
+  __shared__ float cols[kDirWaves][64];
+  float v[8];
+  // the longer tiles first; each product's neighbours on one XCD
+  const int first = static_cast<int>(dw.end - dx.end), b = blockIdx.x;
+  if (b >= first) {
+    const DirPlace t(dx, xcd_remap(b - first, static_cast<int>(dx.end)));
+    dir_tile<kAlong, kAlong, kSlope, false, false>(dx.s, dx.f, dx.K, t.m0, t.n0, t.s0, t.s1, false, lds, cols, v);
+    return dir_store(dx, t, v);
+  }
+  const DirPlace t(dw, xcd_remap(b, first));
+  const bool columns = dbias && t.m0 == 0;
+  dir_tile<kAcross, kAcross, false, kSlope, true>(dw.s, dw.f, dw.K, t.m0, t.n0, t.s0, t.s1, columns, lds, cols, v);
+  dir_store(dw, t, v);
+  const int64_t n = t.n0 + threadIdx.x;
+  if (columns && threadIdx.x < 64 && n < dw.N) {
+    float sum = 0.0f;
+#pragma unroll
+    for (int u = 0; u < kDirWaves; ++u) sum += cols[u][threadIdx.x];
+    dbias[t.part * ld_bias + n] = sum;
+  }
+}
+
 // ------------------------------------------------------------------ layouts
 
 // Whether the forward's tiles read the weights where they are (mm_tile,
@@ -374,13 +462,36 @@ int bias_slices(const moe_linear& l) {
   return static_cast<int>(k < 1 ? 1 : (k > 64 ? 64 : k));
 }
 
+// Products taken from memory as they are (direct.h): fp32, up to so many
+// multiplications; a training pass, from memory and in tiles through LDS, us: 100 x
+// 100 x 100 (rows, inputs, outputs) 17 and 32, 1000 x 512 x 512 53 and 65, 300 x 1024
+// x 1024 62 and 67, 777 x 500 x 1001 53 and 85, 640 x 640 x 960 50 and 76; above it
+// 2000 x 512 x 512 79 and 68, 120 x 2048 x 2048 102 and 72, 8192 x 512 x 512 190 and
+// 156 (where the tiles' rows are padded: 701 x 901 x 803 75 and 95).
+constexpr int64_t kDirect = int64_t{3} << 27;
+bool direct(const moe_linear& l) {
+  const int64_t n = static_cast<int64_t>(l.inputs) * l.outputs, wide = l.inputs > l.outputs ? l.inputs : l.outputs;
+  // operands below 2^32 bytes, rows of four or more
+  if (l.dtype != MOE_FP32 || l.inputs < 4 || l.outputs < 4 || n >= int64_t{1} << 29) return false;
+  return l.tokens * (wide + 8) < int64_t{1} << 29 && l.tokens * n <= kDirect;
+}
+// Slices of k: a workgroup a CU, of two steps a wave at least.
+int64_t dir_tiles(int64_t M, int64_t N) {
+  return (M + kDirTile - 1) / kDirTile * ((N + kDirTile - 1) / kDirTile);
+}
+int64_t dir_steps(int64_t K) { return (K + kDirStep - 1) / kDirStep; }
+int dir_parts(int64_t K, int64_t all_steps) {
+  const int64_t least = 2 * kDirWaves, each = (all_steps + kCUs - 1) / kCUs;
+  const int64_t p = dir_steps(K) / (each > least ? each : least);
+  return static_cast<int>(p < 1 ? 1 : (p > 64 ? 64 : p));
+}
+
 struct LinLayout {
   size_t wt, xp, sums;                 // forward: turned weights, padded x, sums of slices
   size_t dx_sums, da, wp, part, bias, xt, dat, zero;  // backward
   size_t total;
   int k_parts, dx_parts, grad_parts, bias_parts;
 };
-int64_t pad4(int64_t v) { return (v + 3) / 4 * 4; }
 
 // Slices of K of a product in tiles.
 int tile_parts(size_t es, int64_t M, int64_t N, int64_t kp) { return parts_of(es, M, N, kp * es / 128); }
@@ -402,6 +513,8 @@ LinLayout lin_layout(const moe_linear& l, bool training) {
     const int64_t most = (K + 2 * kSkinnyStep * kSkinnyWaves - 1) / (2 * kSkinnyStep * kSkinnyWaves);
     const int64_t want = (kCUs + blocks - 1) / blocks;
     L.k_parts = K <= static_cast<size_t>(es == 2 ? kShortK : kShortKF32) ? 1 : static_cast<int>(want < most ? want : most);
+  } else if (direct(l)) {
+    L.k_parts = dir_parts(K, dir_tiles(T, N) * dir_steps(K));
   } else {
     if (!in_place(l)) {
       L.wt = take(N * kp * es);
@@ -414,6 +527,16 @@ LinLayout lin_layout(const moe_linear& l, bool training) {
   if (!training) return L;
   // the backward has the place for itself
   o = 0;
+  if (direct(l)) {
+    const int64_t all = dir_tiles(T, K) * dir_steps(N) + dir_tiles(K, N) * dir_steps(T);
+    L.dx_parts = dir_parts(N, all);
+    L.grad_parts = dir_parts(T, all);
+    L.dx_sums = sums(L.dx_parts, T * pad4(K));
+    L.part = sums(L.grad_parts, K * pad4(N));
+    L.bias = sums(L.grad_parts, pad4(N));
+    L.total = std::max(L.total, o);
+    return L;
+  }
   L.zero = take(kTrZeroBytes);
   L.da = take(l.act == MOE_ACT_NONE && N == np ? 0 : T * np * es);
   L.wp = take(N == np ? 0 : K * np * es);
@@ -519,6 +642,20 @@ void lin_product(const char* name, int act, const MmArgs& a, const LinOut<T>& o,
   lin_join<T>("linear_join", act, part, parts, o, s);
 }
 
+// A product's tiles behind `start` workgroups; out, or from two slices of k on
+// their sums with rows of `ld` (out: of N).
+inline void dir_place(DirProduct* p, int64_t start, int64_t K, int64_t M, int N, int parts, float* out, float* sums,
+                      int64_t ld) {
+  p->K = K;
+  p->M = M;
+  p->N = N;
+  p->tiles_n = (N + kDirTile - 1) / kDirTile;
+  p->parts = parts;
+  p->end = start + dir_tiles(M, N) * parts;
+  p->out = parts > 1 ? sums : out;
+  p->ld = parts > 1 ? ld : N;
+}
+
 template <typename T>
 hipError_t lin_fwd_t(const moe_linear& l, const void* x, const void* w, const float* bias, const void* res,
                      void* saved, void* y, void* ws, hipStream_t s) {
@@ -541,6 +678,20 @@ hipError_t lin_fwd_t(const moe_linear& l, const void* x, const void* w, const fl
       });
     }
     return hipGetLastError();
+  }
+  if constexpr (sizeof(T) == 4) {
+    if (direct(l)) {
+      DirProduct p{};
+      p.s = DirOperand{static_cast<const float*>(x), K, nullptr, 0, l.tokens};
+      p.f = DirOperand{static_cast<const float*>(w), N, nullptr, 0, N};
+      dir_place(&p, 0, K, l.tokens, N, L.k_parts, nullptr, part, N);
+      with_act(l.act, [&](auto k) {
+        MOE_LAUNCH("linear_direct", (lin_direct_kernel<decltype(k)::value>), dim3(static_cast<unsigned>(p.end)),
+                   dim3(kDirThreads), 0, s, p, o);
+      });
+      if (L.k_parts > 1) lin_join<T>("linear_join", l.act, part, L.k_parts, o, s);
+      return hipGetLastError();
+    }
   }
   if (in_place(l)) {
     lin_product<T>("linear", l.act, rows_of<T>(x, K, w, N, l.tokens, N, K), o, L.k_parts, part, s, true);
@@ -570,6 +721,37 @@ hipError_t lin_bwd_t(const moe_linear& l, const void* x, const void* w, const vo
     jobs.job[jobs.n++] = SliceJob{part, splits, stride, ld, M, cols, out, end, wide};
   };
 
+  if constexpr (sizeof(T) == 4) {
+    if (direct(l)) {
+      const Slopes<float> sl = slopes_at<float>(l, const_cast<void*>(saved));
+      const float* g = static_cast<const float*>(dy);
+      DirProduct p{}, q{};
+      p.s = DirOperand{g, N, sl.p, sl.ld, tok};
+      p.f = DirOperand{static_cast<const float*>(w), N, nullptr, 0, K};
+      float* dx_sums = reinterpret_cast<float*>(W + L.dx_sums);
+      float* dw_sums = reinterpret_cast<float*>(W + L.part);
+      float* bias_sums = reinterpret_cast<float*>(W + L.bias);
+      dir_place(&p, 0, N, tok, K, L.dx_parts, static_cast<float*>(dx), dx_sums, pad4(K));
+      q.s = DirOperand{static_cast<const float*>(x), K, nullptr, 0, K};
+      q.f = DirOperand{g, N, sl.p, sl.ld, N};
+      dir_place(&q, p.end, tok, K, N, L.grad_parts, static_cast<float*>(dw), dw_sums, pad4(N));
+      float* db = dbias && L.grad_parts > 1 ? bias_sums : dbias;
+      auto go = [&](auto slope) {
+        MOE_LAUNCH("linear_direct_bwd", (lin_direct_bwd_kernel<decltype(slope)::value>),
+                   dim3(static_cast<unsigned>(q.end)), dim3(kDirThreads), 0, s, p, q, db, pad4(N));
+      };
+      if (sl.p) go(std::true_type{});
+      else go(std::false_type{});
+      if (L.dx_parts > 1) job(dx_sums, L.dx_parts, tok * pad4(K), pad4(K), static_cast<int>(tok), K, dx, true);
+      if (L.grad_parts > 1) {
+        job(dw_sums, L.grad_parts, K * pad4(N), pad4(N), K, N, dw, true);
+        if (dbias) job(bias_sums, L.grad_parts, pad4(N), pad4(N), 1, N, dbias, true);
+      }
+      if (jobs.n)
+        MOE_LAUNCH("linear_slice_sum", slice_sum_kernel<G>, dim3(blocks_for(end)), dim3(256), 0, s, jobs);
+      return hipGetLastError();
+    }
+  }
   const bool made = l.act != MOE_ACT_NONE || N != np;
   const void* da = made ? W + L.da : dy;
   if (made || dbias) {

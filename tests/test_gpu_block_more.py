@@ -122,6 +122,34 @@ def test_linear_large(t, k, n, dtype, act):
     check_linear(t, k, n, dtype, act, dtype, True, True)
 
 
+@pytest.mark.parametrize("act", ["silu", "none"])
+@pytest.mark.parametrize("t,k,n", [
+    (1, 4, 4), (2, 3, 5), (2, 5, 3), (4, 4, 5), (65, 7, 66), (130, 65, 4), (129, 128, 64), (2000, 260, 301),
+    (3001, 5, 2049), (5000, 36, 37), (16000, 128, 128), (260, 1500, 901),  # operands from memory as they are
+    (130, 2048, 1701), (901, 701, 803)])                                   # and in tiles
+def test_linear_fp32_products(t, k, n, act):
+    check_linear(t, k, n, "fp32", act, "fp32", True, act == "silu")
+
+
+def test_linear_fp32_odd_values():
+    # the last row's values are loaded for the rows behind it too
+    import torch
+    l, x, w, b, add, dy, buf = linear_case(197, 30, 69, "fp32", "silu")
+    x[196, 29], add[0, 68] = float("nan"), float("inf")
+    K.linear(l, x, w, buf, bias=b, residual=add, training=True)
+    bad = ~torch.isfinite(buf.y)
+    assert bool(bad[196].all()) and float(buf.y[0, 68]) == float("inf") and int(bad.sum()) == 70
+    gx, gw, gb = K.linear_backward(l, x, w, dy, buf)
+    assert bool(torch.isnan(gx[196]).all()) and bool(torch.isfinite(gx[:196]).all())
+    assert bool(torch.isnan(gw).all()) and bool(torch.isnan(gb).all())
+    dy[5, 68] = float("nan")
+    x[196, 29] = 0.5
+    K.linear(l, x, w, buf, bias=b, residual=add, training=True)
+    gx, gw, gb = K.linear_backward(l, x, w, dy, buf)
+    assert int(torch.isnan(gx).any(1).sum()) == 1 and bool(torch.isnan(gw[:, 68]).all())
+    assert bool(torch.isfinite(gw[:, :68]).all()) and bool(torch.isfinite(gb[:68]).all())
+
+
 def test_linear_gradient_against_differences():
     import torch
     l, x, w, b, add, dy, buf = linear_case(20, 30, 40, "fp32", "gelu_tanh")
