@@ -8,7 +8,7 @@
 // are in registers, where the tile's rows are handed out (mm_drain): the
 // residual's rows are read one strip ahead, y is rounded once, and the slope
 // act'(a) is kept for the backward, in bf16 in 20 bits of fixed point (slopes lie
-// in [-0.13, 1.13]; 2.5 bytes a value and off by 2^-20: 9e-7 in the 2-norm of
+// in [-0.13, 1.13]; 2.5 bytes a value and off by at most 6.4e-7: 6e-7 in the 2-norm of
 // dbias, which is fp32 and has no other rounding. A slope of fp16, 2 bytes, made
 // 2.2e-4 of that, one of a bf16 pre-activation would make 2e-3).
 //
@@ -42,13 +42,14 @@ bool few_rows(const moe_linear& l) { return l.tokens <= (l.dtype == MOE_BF16 ? k
 // Elements between rows of the kept slopes.
 int64_t slope_pitch(const moe_linear& l) { return (l.outputs + 7) / 8 * 8; }
 
-// A kept slope of the bf16 form: slope 2^19 + 2^17, rounded, in 20 bits, as the
-// low bits of a number from 2^23 on; 0, which no slope gives, for a NaN.
+// A kept slope of the bf16 form: 3 2^18 slope + 2^17, rounded, in 20 bits, as the
+// low bits of a number from 2^23 on; 0, which no slope gives, for a NaN. Slopes of 0
+// and 1 come back as they were.
 __device__ __forceinline__ uint32_t slope_code(float v) {
-  return __float_as_uint(fmaxf(__builtin_fmaf(v, 524288.0f, 8388608.0f + 131072.0f), 8388608.0f)) & 0xfffff;
+  return __float_as_uint(fmaxf(__builtin_fmaf(v, 786432.0f, 8388608.0f + 131072.0f), 8388608.0f)) & 0xfffff;
 }
 __device__ __forceinline__ float slope_of(uint32_t code) {
-  return code ? __builtin_fmaf(static_cast<float>(code), 1.0f / 524288.0f, -0.25f) : __builtin_nanf("");
+  return code ? __builtin_fmaf(static_cast<float>(code), 1.0f / 786432.0f, -1.0f / 6.0f) : __builtin_nanf("");
 }
 
 // Where slopes are kept: [rows][ld] of T's type, fp32 numbers or the codes' high
@@ -120,22 +121,25 @@ struct Slopes<bf16_t> {
 };
 
 // act(a) and its slope. In bf16 GELU's Phi(-|a|) is exp(-a^2 / 2) R(|a|), R
-// (0.5 exp(x^2 / 2) erfc(x / sqrt 2)) as t p(t), t = 1 / (1 + 0.28 x), with p of
-// degree 6 fitted to the smallest largest relative error, 4.0e-6 over all x in
-// fp32: 2^-18, far under bf16's rounding and the slopes'. One exponential serves
+// (0.5 exp(x^2 / 2) erfc(x / sqrt 2)) as t p(t), t = 1 / (1 + 0.285 x), with p of
+// degree 8 fitted to the smallest largest relative error, 4.8e-7 over all x in
+// fp32, so that Phi is off by at most 2.2e-7, less than the slopes' rounding (degree
+// 6: 4e-6, which showed in dbias). One exponential serves
 // the value and the slope. (erff's two branches, 32 times eight of them, were
 // more than the compiler would unroll in a 256 x 256 tile.) fp32 takes erff.
 template <typename T, int kAct>
 __device__ __forceinline__ float lin_act(float a, float* slope) {
   if constexpr (kAct == MOE_ACT_GELU && sizeof(T) == 2) {
-    const float x = fabsf(a), t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.28f, x, 1.0f));
-    float p = -0.05023228f;
-    p = __builtin_fmaf(p, t, 0.105446689f);
-    p = __builtin_fmaf(p, t, 0.024945872f);
-    p = __builtin_fmaf(p, t, 0.0944580585f);
-    p = __builtin_fmaf(p, t, 0.101935275f);
-    p = __builtin_fmaf(p, t, 0.111740693f);
-    p = __builtin_fmaf(p, t, 0.111703843f);
+    const float x = fabsf(a), t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.285f, x, 1.0f));
+    float p = 0.0245698374f;
+    p = __builtin_fmaf(p, t, -0.0865935981f);
+    p = __builtin_fmaf(p, t, 0.0739199519f);
+    p = __builtin_fmaf(p, t, 0.00349686155f);
+    p = __builtin_fmaf(p, t, 0.0675795525f);
+    p = __builtin_fmaf(p, t, 0.0851249918f);
+    p = __builtin_fmaf(p, t, 0.104505382f);
+    p = __builtin_fmaf(p, t, 0.113698572f);
+    p = __builtin_fmaf(p, t, 0.113698535f);
     const float e = __expf(-0.5f * a * a), tail = e * (p * t);
     const float cdf = a < 0.0f ? tail : 1.0f - tail;
     *slope = __builtin_fmaf(a * 0.39894228f, e, cdf);
