@@ -19,6 +19,7 @@
 // backward's dx reads them as they are. da is made in one pass over dy that
 // also adds up dbias and pads the rows; without an activation dy itself is da.
 //
+// Up to 16 bf16 rows have a backward pass of one launch (lin_few_bwd_kernel), and
 // fp32 products of moderate size take both passes' operands from memory as they
 // are, in one launch each (direct.h).
 #include "dense.h"
@@ -35,6 +36,13 @@ constexpr int64_t kFewRows = 16, kFewRowsF32 = 128;
 // 4096 x 4096 11.8 and 10.5, 8192 x 2048 20 and 11; 8 rows, 2048 x 8192 8.4 and 10.9;
 // fp32, 64 rows, 512 x 2048 8.1 and 8.4, 16 rows, 1024 x 1024 12.8 and 10.9.
 constexpr int kRowsWaves = 16, kShortK = 2048, kShortKF32 = 512;
+
+// The backward of few rows in one launch; a training pass so and in tiles, us: 1 x
+// 512 x 512 17 and 29, 16 x 512 x 4096 23 and 28, 16 x 2048 x 2048 25 and 29, 2 x 8192
+// x 2048 36 and 39; past its limits 16 x 128 x 16384 64 and 29, 16 x 65536 x 64 67 and 44,
+// 16 x 4096 x 4096 56 and 41.
+constexpr int kFewInputs = 8192, kFewOutputs = 4096;
+constexpr int64_t kFewProducts = int64_t{1} << 26;
 
 int64_t pad4(int64_t v) { return (v + 3) / 4 * 4; }
 size_t elem_bytes(const moe_linear& l) { return l.dtype == MOE_BF16 ? 2 : 4; }
@@ -364,6 +372,138 @@ __global__ __launch_bounds__(32 * kDaRows) void lin_da_kernel(const T* __restric
   if (col < n4) part[static_cast<int64_t>(blockIdx.y) * n4 + col] = v;
 }
 
+// --------------------------------------------------------- backward of few rows
+
+// The backward pass of up to 16 bf16 rows in one launch, dy's rows times their
+// slopes formed where they are used, in fp32. The first workgroups make dx, 16
+// columns each: mfma 16x16x32 takes 16 rows of w and the rows of da as they lie in
+// memory, eight waves share the outputs, and da goes in as two bf16 numbers, of which
+// the second holds what the first one rounds away (one row's da would err in every
+// term alike). In the others a wave makes 64 x 64 of dW, eight by eight a lane in
+// plain fp32. 16 rows, 1024 x 1024: a training pass 19 us, where forming da, two
+// products in tiles and adding slices made it 29; the backward alone at 2048 x 2048, 1
+// row to 16: 13 to 18 us (24 MB: 5), bound by the lanes' additions.
+constexpr int kFewWaves = 8, kFewTile = 64, kFewCols = 16;
+__device__ __forceinline__ f32x4_t few_mfma(const u32x4& a, const u32x4& b, const f32x4_t& c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c, 0,
+                                                 0, 0);
+}
+template <typename G, bool kSlope>
+__global__ __launch_bounds__(64 * kFewWaves) void lin_few_bwd_kernel(
+    const bf16_t* __restrict__ x, const bf16_t* __restrict__ w, const bf16_t* __restrict__ dy,
+    const Slopes<bf16_t> slope, bf16_t* __restrict__ dx, G* __restrict__ dw, float* __restrict__ dbias, int rows, int K,
+    int N, int first) {
+  typedef Slopes<bf16_t>::Raw Raw;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int last = static_cast<int>(slope.ld) - 8;  // slopes of columns there are
+  // da of eight columns from c on
+  auto form = [&](u32x4 raw, const Raw& sl, int c, float (&v)[8]) {
+    trim_piece<bf16_t>(raw, c, N);
+    Piece<bf16_t>::widen(raw, v);
+    if constexpr (kSlope) {
+      float e[8];
+      Slopes<bf16_t>::get8(sl, e);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) v[q] = c + q < N ? v[q] * e[q] : 0.0f;
+    }
+  };
+  if (static_cast<int>(blockIdx.x) < first) {
+    constexpr int kBatch = 4;
+    __shared__ float sums[kFewWaves][16 * kFewCols];
+    const int k0 = blockIdx.x * kFewCols, i = lane & 15, g = lane >> 4;
+    const bf16_t* wr = w + static_cast<int64_t>(min(k0 + i, K - 1)) * N;
+    const int row = min(i, rows - 1);
+    const bf16_t* dr = dy + static_cast<int64_t>(row) * N;
+    f32x4_t acc = (f32x4_t){0.0f, 0.0f, 0.0f, 0.0f};
+    for (int s = wave * 32 + 8 * g; s - 8 * g < N; s += kBatch * kFewWaves * 32) {
+      u32x4 a[kBatch], b[kBatch];
+      Raw e[kBatch];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int c = s + u * kFewWaves * 32;
+        a[u] = load_near(wr, c, N);
+        b[u] = load_near(dr, c, N);
+        if constexpr (kSlope) e[u] = slope.load8(row, min(c, last));
+      }
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int c = s + u * kFewWaves * 32;
+        trim_piece<bf16_t>(a[u], c, N);
+        if constexpr (kSlope) {
+          float v[8], rest[8];
+          form(b[u], e[u], c, v);
+          const u32x4 high = Piece<bf16_t>::narrow(v);
+          Piece<bf16_t>::widen(high, rest);
+#pragma unroll
+          for (int q = 0; q < 8; ++q) rest[q] = __builtin_isinf(rest[q]) ? 0.0f : v[q] - rest[q];
+          acc = few_mfma(a[u], Piece<bf16_t>::narrow(rest), acc);
+          acc = few_mfma(a[u], high, acc);
+        } else {
+          trim_piece<bf16_t>(b[u], c, N);
+          acc = few_mfma(a[u], b[u], acc);
+        }
+      }
+    }
+    // column k0 + 4 (lane / 16) + q of row lane % 16
+    *reinterpret_cast<f32x4_t*>(&sums[wave][lane * 4]) = acc;
+    __syncthreads();
+    const int t = threadIdx.x / kFewCols, k = threadIdx.x % kFewCols;
+    if (t >= rows || k0 + k >= K) return;
+    float v = 0.0f;
+#pragma unroll
+    for (int u = 0; u < kFewWaves; ++u) v += sums[u][(k / 4 * 16 + t) * 4 + k % 4];
+    put(dx + static_cast<int64_t>(t) * K + k0 + k, v);
+    return;
+  }
+  constexpr int kBatch = 2;
+  const int tiles_n = (N + kFewTile - 1) / kFewTile;
+  const int tile = (blockIdx.x - first) * kFewWaves + wave;
+  const int k = tile / tiles_n * kFewTile + (lane >> 3) * 8, c = tile % tiles_n * kFewTile + (lane & 7) * 8;
+  if (tile / tiles_n * kFewTile >= K) return;
+  const bool columns = dbias && tile < tiles_n && lane < 8;
+  float acc[8][8], total[8];
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    total[q] = 0.0f;
+#pragma unroll
+    for (int r = 0; r < 8; ++r) acc[r][q] = 0.0f;
+  }
+  for (int t = 0; t < rows; t += kBatch) {
+    u32x4 a[kBatch], b[kBatch];
+    Raw e[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int64_t row = min(t + u, rows - 1);
+      a[u] = load_near(x + row * K, k, K);
+      b[u] = load_near(dy + row * N, c, N);
+      if constexpr (kSlope) e[u] = slope.load8(row, min(c, last));
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      if (t + u >= rows) break;
+      float xs[8], v[8];
+      trim_piece<bf16_t>(a[u], k, K);
+      Piece<bf16_t>::widen(a[u], xs);
+      form(b[u], e[u], c, v);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) total[q] += v[q];
+#pragma unroll
+      for (int r = 0; r < 8; ++r)
+#pragma unroll
+        for (int q = 0; q < 8; ++q) acc[r][q] = __builtin_fmaf(xs[r], v[q], acc[r][q]);
+    }
+  }
+  if (c >= N) return;
+#pragma unroll
+  for (int r = 0; r < 8; ++r)
+    if (k + r < K) store8<G, false>(dw + static_cast<int64_t>(k + r) * N, c, N, acc[r]);
+  if (columns) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      if (c + q < N) dbias[c + q] = total[q];
+  }
+}
+
 // ---------------------------------------------------- fp32 of moderate size
 
 // The products of one launch, their tiles one after the other; parts > 1: sums of
@@ -479,6 +619,11 @@ bool direct(const moe_linear& l) {
   if (l.dtype != MOE_FP32 || l.inputs < 4 || l.outputs < 4 || n >= int64_t{1} << 29) return false;
   return l.tokens * (wide + 8) < int64_t{1} << 29 && l.tokens * n <= kDirect;
 }
+// Whether the backward pass is that of few rows.
+bool few_bwd(const moe_linear& l) {
+  return l.dtype == MOE_BF16 && few_rows(l) && l.inputs <= kFewInputs && l.outputs <= kFewOutputs &&
+         l.tokens * l.inputs * l.outputs <= kFewProducts;
+}
 // Slices of k: a workgroup a CU, of two steps a wave at least.
 int64_t dir_tiles(int64_t M, int64_t N) {
   return (M + kDirTile - 1) / kDirTile * ((N + kDirTile - 1) / kDirTile);
@@ -531,6 +676,7 @@ LinLayout lin_layout(const moe_linear& l, bool training) {
   if (!training) return L;
   // the backward has the place for itself
   o = 0;
+  if (few_bwd(l)) return L;
   if (direct(l)) {
     const int64_t all = dir_tiles(T, K) * dir_steps(N) + dir_tiles(K, N) * dir_steps(T);
     L.dx_parts = dir_parts(N, all);
@@ -753,6 +899,22 @@ hipError_t lin_bwd_t(const moe_linear& l, const void* x, const void* w, const vo
       }
       if (jobs.n)
         MOE_LAUNCH("linear_slice_sum", slice_sum_kernel<G>, dim3(blocks_for(end)), dim3(256), 0, s, jobs);
+      return hipGetLastError();
+    }
+  }
+  if constexpr (sizeof(T) == 2) {
+    if (few_bwd(l)) {
+      const int first = (K + kFewCols - 1) / kFewCols;
+      const int64_t tiles = static_cast<int64_t>((K + kFewTile - 1) / kFewTile) * ((N + kFewTile - 1) / kFewTile);
+      const dim3 grid(static_cast<unsigned>(first + (tiles + kFewWaves - 1) / kFewWaves));
+      auto go = [&](auto slope) {
+        MOE_LAUNCH("linear_few_bwd", (lin_few_bwd_kernel<G, decltype(slope)::value>), grid, dim3(64 * kFewWaves), 0, s,
+                   static_cast<const bf16_t*>(x), static_cast<const bf16_t*>(w), static_cast<const bf16_t*>(dy),
+                   slopes_at<bf16_t>(l, const_cast<void*>(saved)), static_cast<bf16_t*>(dx), static_cast<G*>(dw), dbias,
+                   static_cast<int>(tok), K, N, first);
+      };
+      if (l.act == MOE_ACT_NONE) go(std::false_type{});
+      else go(std::true_type{});
       return hipGetLastError();
     }
   }

@@ -131,6 +131,34 @@ def test_linear_fp32_products(t, k, n, act):
     check_linear(t, k, n, "fp32", act, "fp32", True, act == "silu")
 
 
+@pytest.mark.parametrize("act,grad", [("gelu", "bf16"), ("none", "fp32"), ("gelu_tanh", "fp32")])
+@pytest.mark.parametrize("t,k,n", [
+    (1, 1, 1), (1, 9, 7), (2, 7, 9), (3, 64, 4096), (5, 63, 1025), (15, 130, 2047), (16, 1000, 31), (16, 8192, 65),
+    (16, 2048, 2048),                                  # one launch
+    (2, 64, 4104), (3, 8200, 40), (16, 2056, 2048)])   # in tiles
+def test_linear_few_rows(t, k, n, act, grad):
+    check_linear(t, k, n, "bf16", act, grad, True, False)
+
+
+@pytest.mark.parametrize("t", [1, 7])
+def test_linear_few_rows_round_once(t):
+    # one row's rounded da would be wrong in every term alike: the gradients are
+    # rounded once (2^-8 of each value at most, 1e-5 for sums and slopes)
+    import torch
+    l, x, w, b, add, dy, buf = linear_case(t, 130, 70, "bf16", "gelu", "bf16")
+    K.linear(l, x, w, buf, bias=b, residual=add, training=True)
+    gx, gw, gb = K.linear_backward(l, x, w, dy, buf)
+    y, dx, dw, db, da = linear64(x, w, b, add, dy, "gelu")
+    for name, got, want, size in (("dx", gx, dx, da @ w.double().abs().t()),
+                                  ("dw", gw, dw, x.double().abs().t() @ da)):
+        off = (got.double() - want).abs()
+        assert bool((off <= 2.0 ** -8 * want.abs() + 1e-5 * size).all()), name
+    # an infinite gradient stays one
+    dy[0, 3] = float("inf")
+    gx, gw, gb = K.linear_backward(l, x, w, dy, buf)
+    assert bool((torch.isinf(gx[0]) | (w[:, 3] == 0)).all()) and bool(torch.isinf(gb[3]))
+
+
 def test_linear_fp32_odd_values():
     # the last row's values are loaded for the rows behind it too
     import torch
