@@ -9,14 +9,14 @@
 // writing dx. The gradient by the logits needs the counts, which the routing
 // already fixes, and nothing else of the batch: a first launch counts, the pass
 // over x then makes p and dl while the logits are in registers, and the backward
-// starts from dl (a seventh of x's bytes at 64 experts of 512 columns in bf16: two
-// halves of 2 bytes) instead of multiplying by W again.
+// starts from dl (fp32: a quarter of x's bytes at 64 experts of 512 columns in bf16)
+// instead of multiplying by W again.
 //
 // Precision. bf16: x is exact in bf16 and W is the sum of three bf16 numbers, all
 // of fp32's 24 bits, so three bf16 MFMAs make the logits as fp32 products would,
-// at a fifth of fp32 MFMAs' time. dl is the sum of two bf16 numbers (2^-17) and W
-// of two in the backward: dx is off by 2^-16 before it is rounded to bf16, dW is
-// x (exact) times dl. fp32: fp32 MFMAs throughout.
+// at a fifth of fp32 MFMAs' time. In the backward dl is the sum of three for dW, x
+// being exact, and of two for dx, as W is there: dx is off by 2^-16 before it is
+// rounded to bf16. fp32: fp32 MFMAs throughout.
 #include "block.h"
 #include "skinny.h"
 
@@ -206,43 +206,13 @@ struct BalOp<float> {
 
 // The kept gradient by the logits of eight experts of a token (one lane) or,
 // in fp32, of four; the two lanes of a token hold experts in turns of four.
-__device__ __forceinline__ void store_dl(bf16_t* row, int eb, int EP, int g, const float (&dl)[16]) {
-  uint32_t hi[8], lo[8];
-#pragma unroll
-  for (int q = 0; q < 8; ++q) {
-    hi[q] = pack_bf16x2(dl[2 * q], dl[2 * q + 1]);
-    lo[q] = pack_bf16x2(dl[2 * q] - bf16lo(hi[q]), dl[2 * q + 1] - bf16hi(hi[q]));
-  }
-  // registers 2 r, 2 r + 1 are experts 8 r + 4 g .. + 3: after the swap of two
-  // runs the lower lane has all eight of the first, the upper of the second
-#pragma unroll
-  for (int r = 0; r < 4; r += 2) {
-    auto put = [&](bf16_t* dst, const uint32_t (&v)[8]) {
-      const auto a = __builtin_amdgcn_permlane32_swap(v[2 * r], v[2 * r + 2], false, false);
-      const auto b = __builtin_amdgcn_permlane32_swap(v[2 * r + 1], v[2 * r + 3], false, false);
-      *reinterpret_cast<u32x4*>(dst + 32 * eb + 8 * (r + g)) = (u32x4){a[0], b[0], a[1], b[1]};
-    };
-    put(row, hi);
-    put(row + EP, lo);
-  }
-}
-__device__ __forceinline__ void store_dl(float* row, int eb, int, int g, const float (&dl)[16]) {
+__device__ __forceinline__ void store_dl(float* row, int eb, int g, const float (&dl)[16]) {
 #pragma unroll
   for (int r = 0; r < 4; ++r)
     store4(row + 32 * eb + 8 * r + 4 * g, dl[4 * r], dl[4 * r + 1], dl[4 * r + 2], dl[4 * r + 3]);
 }
 
 // The same of eight consecutive experts of token t in one lane.
-__device__ __forceinline__ void store_dl8(bf16_t* saved, int64_t t, int EP, int e0, const float (&dl)[8]) {
-  bf16_t* row = saved + t * 2 * EP + e0;
-  const u32x4 hi = Piece<bf16_t>::narrow(dl);
-  float back[8];
-  Piece<bf16_t>::widen(hi, back);
-#pragma unroll
-  for (int q = 0; q < 8; ++q) back[q] = dl[q] - back[q];
-  *reinterpret_cast<u32x4*>(row) = hi;
-  *reinterpret_cast<u32x4*>(row + EP) = Piece<bf16_t>::narrow(back);
-}
 __device__ __forceinline__ void store_dl8(float* saved, int64_t t, int EP, int e0, const float (&dl)[8]) {
   float* row = saved + t * EP + e0;
   store4(row, dl[0], dl[1], dl[2], dl[3]);
@@ -451,7 +421,7 @@ __device__ __forceinline__ float one_over(int n) { return n > 0 ? 1.0f / static_
 template <typename T, int EB>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2)))
 void balance_logits_kernel(const BalArgs a, const T* __restrict__ x, const u32x4* __restrict__ wf,
-                           T* __restrict__ saved) {
+                           float* __restrict__ saved) {
   constexpr int EP = 32 * EB, RT = 2, NW = 4;
   __shared__ float sums[NW][EP + 1];
   __shared__ int tallies[NW][64];
@@ -531,7 +501,7 @@ void balance_logits_kernel(const BalArgs a, const T* __restrict__ x, const u32x4
 #pragma unroll
       for (int q = 0; q < 16; ++q)
         dl[q] = keep ? p[b][q] * __builtin_fmaf(a.c1, f[b][q] - inner, zed) * inv_n : 0.0f;
-      if (t < a.T) store_dl(saved + t * (sizeof(T) == 2 ? 2 * EP : EP), b, EP, g, dl);
+      if (t < a.T) store_dl(saved + t * EP, b, g, dl);
     }
   }
   // sums over the wave's 32 lanes, then over the waves
@@ -562,7 +532,7 @@ void balance_logits_kernel(const BalArgs a, const T* __restrict__ x, const u32x4
 template <typename T, int EB, int KS, bool kRaw>
 __global__ __launch_bounds__(64 * KS) void balance_logits_few_kernel(const BalArgs a, const T* __restrict__ x,
                                                                      const u32x4* __restrict__ wf,
-                                                                     T* __restrict__ saved) {
+                                                                     float* __restrict__ saved) {
   constexpr int EP = 32 * EB, L = 4 * EB, kTokens = 64 / L, kPitch = 66;
   constexpr int kUsed = 32 / kTokens < KS ? 32 / kTokens : KS, kPasses = 32 / kTokens / kUsed;
   __shared__ float part[KS][16 * EB * kPitch];
@@ -753,7 +723,10 @@ struct BalGrad;
 
 template <int EB>
 struct BalGrad<bf16_t, EB> {
-  static constexpr int EP = 32 * EB, ROW = 4 * EP;  // bytes of a token: high halves, then low
+  // dl goes in as three bf16 numbers, each what the ones before it round away. dx,
+  // rounded to bf16, takes two; dW takes all (two, off by 2^-18 at most, made it
+  // 1.5e-6 to 2.9e-6 off in the 2-norm). ROW: bytes of a token's dl in memory, BYTES: here.
+  static constexpr int EP = 32 * EB, ROW = 4 * EP, BYTES = 6 * EP;
   u32x4 hi[4][EB], lo[4][EB];
   __device__ void load(const u32x4* wb, int c0, int lane) {
     const u32x4* p = wb + static_cast<int64_t>(c0 / 64) * 4 * EB * 128 + lane;
@@ -765,8 +738,27 @@ struct BalGrad<bf16_t, EB> {
         lo[j][b] = p[(j * EB + b) * 128 + 64];
       }
   }
-  // 16-byte chunk c of token row r: spread over the banks
-  __device__ static int at(int r, int c) { return r * ROW + ((c ^ (r & (ROW / 16 - 1))) << 4); }
+  // 16-byte chunk c of number `part` of token row r: spread over the banks, the same
+  // way in the three
+  __device__ static int at(int part, int r, int c) {
+    return part * 64 * EP + r * 2 * EP + ((c ^ (r & (EP / 8 - 1))) << 4);
+  }
+  // dl of experts 4 c .. + 3 of token row r.
+  __device__ static void put_dl(char* lds, int r, int c, const u32x4& dl) {
+    float v[4];
+    Piece<float>::widen(dl, v);
+    u32x2 part[3];
+#pragma unroll
+    for (int u = 0; u < 3; ++u) {
+      part[u] = (u32x2){pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+      v[0] -= bf16lo(part[u][0]);
+      v[1] -= bf16hi(part[u][0]);
+      v[2] -= bf16lo(part[u][1]);
+      v[3] -= bf16hi(part[u][1]);
+    }
+#pragma unroll
+    for (int u = 0; u < 3; ++u) *reinterpret_cast<u32x2*>(lds + at(u, r, c >> 1) + (c & 1) * 8) = part[u];
+  }
   // dx of 16 tokens (rows r0..): v[h] are columns c0 + 32 h + 8 (lane / 16) .. + 7
   // of token lane % 16.
   __device__ void dx(const char* lds, int r0, int lane, float (&v)[2][8]) const {
@@ -776,8 +768,8 @@ struct BalGrad<bf16_t, EB> {
     for (int j = 0; j < 4; ++j) acc[j] = (f32x4_t){0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int b = 0; b < EB; ++b) {
-      const bf16x8_t dh = *reinterpret_cast<const bf16x8_t*>(lds + at(r, 4 * b + g));
-      const bf16x8_t dlo = *reinterpret_cast<const bf16x8_t*>(lds + at(r, 4 * EB + 4 * b + g));
+      const bf16x8_t dh = *reinterpret_cast<const bf16x8_t*>(lds + at(0, r, 4 * b + g));
+      const bf16x8_t dlo = *reinterpret_cast<const bf16x8_t*>(lds + at(1, r, 4 * b + g));
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, lo[j][b]), dh, acc[j], 0, 0, 0);
@@ -790,7 +782,7 @@ struct BalGrad<bf16_t, EB> {
 #pragma unroll
       for (int q = 0; q < 4; ++q) v[j / 2][4 * (j % 2) + q] = acc[j][q];
   }
-  // dW: expert rows 16 m + i of the 32 tokens, high and low half, times x.
+  // dW: expert rows 16 m + i of the 32 tokens, each of the three, times x.
   __device__ static void dw(const char* lds, const SkinnyW<bf16_t>& x, int lane, f32x4_t (&acc)[4][2 * EB]) {
     typedef short v4i16 __attribute__((ext_vector_type(4)));
     typedef __attribute__((address_space(3))) v4i16 lds_v4i16;
@@ -799,10 +791,10 @@ struct BalGrad<bf16_t, EB> {
 #pragma unroll
     for (int j = 0; j < 4; ++j) xf[j] = x.frag(j);
 #pragma unroll
-    for (int m = 0; m < 4 * EB; ++m) {  // low halves behind the high ones
-      const int c = 16 * m + 4 * (s & 3), r = 8 * g + (s >> 2);
-      const char* p0 = lds + at(r, c >> 3) + (c & 7) * 2;
-      const char* p1 = lds + at(r + 4, c >> 3) + (c & 7) * 2;
+    for (int m = 0; m < 6 * EB; ++m) {
+      const int c = 16 * (m % (2 * EB)) + 4 * (s & 3), r = 8 * g + (s >> 2), part = m / (2 * EB);
+      const char* p0 = lds + at(part, r, c >> 3) + (c & 7) * 2;
+      const char* p1 = lds + at(part, r + 4, c >> 3) + (c & 7) * 2;
       const v4i16 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(p0));
       const v4i16 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(p1));
       const bf16x8_t dl = __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
@@ -817,7 +809,7 @@ struct BalGrad<bf16_t, EB> {
 
 template <int EB>
 struct BalGrad<float, EB> {
-  static constexpr int EP = 32 * EB, ROW = 4 * EP;
+  static constexpr int EP = 32 * EB, ROW = 4 * EP, BYTES = ROW;
   // Step s takes element s % 4 of the lane groups' 16 bytes s / 4 on both sides:
   // experts 16 (s / 4) + 4 (lane / 16) + s % 4.
   f32x4_t w[4][2 * EB];
@@ -829,6 +821,9 @@ struct BalGrad<float, EB> {
       for (int b = 0; b < 2 * EB; ++b) w[j][b] = __builtin_bit_cast(f32x4_t, p[(j * 2 * EB + b) * 64]);
   }
   __device__ static int at(int r, int c) { return r * ROW + ((c ^ (r & (ROW / 16 - 1))) << 4); }
+  __device__ static void put_dl(char* lds, int r, int c, const u32x4& dl) {
+    *reinterpret_cast<u32x4*>(lds + at(r, c)) = dl;
+  }
   // v[h]: columns c0 + 16 (2 h) + 4 (lane / 16) .. + 3, then 16 further on
   __device__ void dx(const char* lds, int r0, int lane, float (&v)[2][8]) const {
     const int r = r0 + (lane & 15), g = lane >> 4;
@@ -903,11 +898,11 @@ __device__ __forceinline__ void drop_tokens(SkinnyW<float>& x, const char* keep,
 template <typename T, int EB>
 __global__ __launch_bounds__(kGradThreads) __attribute__((amdgpu_waves_per_eu(2)))
 void balance_grad_kernel(const BalGradArgs a, const T* __restrict__ x, const u32x4* __restrict__ wb,
-                         const T* __restrict__ saved, T* dx, float* __restrict__ partial) {
+                         const float* __restrict__ saved, T* dx, float* __restrict__ partial) {
   typedef BalGrad<T, EB> G;
   constexpr int EP = 32 * EB, kPieces = 32 * G::ROW / 16;       // 16-byte pieces of 32 tokens
   constexpr int kLoads = kGradSets * kPieces / kGradThreads;    // of a thread
-  constexpr int kBuf = kGradSets * 32 * G::ROW;
+  constexpr int kBuf = kGradSets * 32 * G::BYTES;
   static_assert(kGradSets * kPieces % kGradThreads == 0 && kPieces % 64 == 0, "loads");
   // the sums of three sets, a quarter at a time, share the place
   constexpr int kSums = (kGradSets - 1) * 2 * 2 * EB * 4 * 64 * 4;
@@ -955,7 +950,7 @@ void balance_grad_kernel(const BalGradArgs a, const T* __restrict__ x, const u32
 #pragma unroll
     for (int u = 0; u < kLoads; ++u) {
       const int i = u * kGradThreads + threadIdx.x, r = i % kPieces / (G::ROW / 16);
-      *reinterpret_cast<u32x4*>(buf + i / kPieces * 32 * G::ROW + G::at(r, i % (G::ROW / 16))) = dl[u];
+      G::put_dl(buf + i / kPieces * 32 * G::BYTES, r, i % (G::ROW / 16), dl[u]);
     }
     if (threadIdx.x < kGradSets * 32) kept[to][threadIdx.x] = keep ? '\xff' : '\0';
   };
@@ -967,7 +962,7 @@ void balance_grad_kernel(const BalGradArgs a, const T* __restrict__ x, const u32
     load_tokens(xv, x + t0 * a.d, a.d, left, c0 + 4 * (lane & 15), lane);
   };
   auto work = [&](int from, int64_t k) {
-    const char* lds = smem + from * kBuf + set * 32 * G::ROW;
+    const char* lds = smem + from * kBuf + set * 32 * G::BYTES;
     const int64_t t0 = (k + set) * 32;
     if (k + set < k1) {
 #pragma unroll
@@ -1135,7 +1130,7 @@ size_t saved_rows_bytes(const moe_balance& b) {
 }
 
 template <typename T, int EB>
-void launch_logits(const BalArgs& a, const T* x, const u32x4* wf, T* saved, hipStream_t s) {
+void launch_logits(const BalArgs& a, const T* x, const u32x4* wf, float* saved, hipStream_t s) {
   const int rows = logits_rows(a.T, sizeof(T) == 2 ? MOE_BF16 : MOE_FP32);
   const dim3 grid(static_cast<unsigned>((a.T + rows - 1) / rows));
   if (rows == 256)
@@ -1171,8 +1166,8 @@ hipError_t balance_t(const moe_balance& b, const void* x, const float* w, const 
                  dim3(a.count_blocks + (pieces + kCountThreads - 1) / kCountThreads), dim3(kCountThreads), 0, s, a,
                  idx, w, EB, wf, wb, parts);
     }
-    if (EB == 1) launch_logits<T, 1>(a, static_cast<const T*>(x), wf, static_cast<T*>(saved), s);
-    else launch_logits<T, 2>(a, static_cast<const T*>(x), wf, static_cast<T*>(saved), s);
+    if (EB == 1) launch_logits<T, 1>(a, static_cast<const T*>(x), wf, static_cast<float*>(saved), s);
+    else launch_logits<T, 2>(a, static_cast<const T*>(x), wf, static_cast<float*>(saved), s);
     const int rows = logits_rows(b.tokens, b.dtype);
     groups = static_cast<int>((b.tokens + rows - 1) / rows);
   }
@@ -1189,7 +1184,7 @@ hipError_t balance_bwd_t(const moe_balance& b, const void* x, const uint8_t* mas
   const BalGradArgs a{b.tokens, b.d_model, ranges, mask, gloss, add};
   const u32x4* wb = reinterpret_cast<const u32x4*>(static_cast<const char*>(saved) + saved_rows_bytes(b));
   MOE_LAUNCH("balance_grad", (balance_grad_kernel<T, EB>), dim3(b.d_model / kGradCols * ranges), dim3(kGradThreads), 0, s, a,
-             static_cast<const T*>(x), wb, static_cast<const T*>(saved), static_cast<T*>(dx), partial);
+             static_cast<const T*>(x), wb, static_cast<const float*>(saved), static_cast<T*>(dx), partial);
   MOE_LAUNCH("balance_sum", balance_sum_kernel, dim3(b.d_model * EP / 4 / 16), dim3(256), 0, s, partial, ranges,
              b.d_model, b.experts, EP, gloss, add, dw);
   return hipGetLastError();
