@@ -222,9 +222,9 @@ int moe_linear_i8(const moe_i8_linear* l, const void* x, const float* x_scale, c
 /*
  *   y = act(x W + bias) + residual
  * x [tokens, inputs], W [inputs, outputs], residual and y [tokens, outputs] in
- * dtype, bias fp32 [outputs]; sums are fp32 and y is rounded once. In the
- * backward pass da is rounded to dtype for its two products, and in bf16 the
- * slopes act'(a) are kept in 20 bits (2^-20).
+ * dtype, bias fp32 [outputs]; sums are fp32 and y is rounded once. In bf16 the
+ * slopes act'(a) are kept in 20 bits for the backward pass (off by at most
+ * 6.4e-7), where da is rounded to bf16 for its two products unless tokens are few.
  *
  * Supported (else MOE_ERR_UNSUPPORTED): inputs and outputs up to 65536 (any
  * value), tokens < 2^31, tokens * max(inputs, outputs) < 2^36.
@@ -382,9 +382,9 @@ typedef struct {
 size_t moe_balance_workspace_bytes(const moe_balance* b);
 
 /* Bytes (host) of the buffer that moe_balance_loss fills for
- * moe_balance_loss_bwd: the gradient of loss[0] by the logits and the router's
- * matrix, in fp32 or, in bf16, as sums of two bf16 numbers (2^-17). 0 for an
- * invalid problem. */
+ * moe_balance_loss_bwd: the gradient of loss[0] by the logits in fp32, and the
+ * router's matrix, in bf16 as sums of two bf16 numbers (2^-17). 0 for an invalid
+ * problem. */
 size_t moe_balance_saved_bytes(const moe_balance* b);
 
 /*
