@@ -525,6 +525,24 @@ def test_balance_added_to_gradients(dtype):
     assert torch.equal(gx[~m], x0[~m])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("t", [1, 3])
+def test_balance_router_gradient_has_fp32_products(t, dtype):
+    # w 0: every p is 1 / 8 and lse log 8, so dl = z log 8 / (4 t) without a
+    # cancellation. Its five operations, log's two units and the t (t + 1) / 2 additions of
+    # three products each stay under 16 roundings of 2^-24
+    import torch
+    for i, z in enumerate((0.37, 0.731, 1.9, 0.0113, 5.77, 0.299)):
+        b, x, w, idx, m, buf = balance_case(t, 8, 2, 128, dtype, seed=i, balance=0.0, z=z)
+        w.zero_()
+        K.balance_loss(b, x, w, idx, buf, training=True)
+        gx, gw = K.balance_loss_backward(b, x, w, buf)
+        dl = float(torch.tensor(z, dtype=torch.float32)) * math.log(8) / (4 * t)
+        want, size = x.double().sum(0) * dl, x.double().abs().sum(0) * dl
+        assert bool(((gw.double() - want[:, None]).abs() <= 16 * 2.0 ** -24 * size[:, None]).all()), z
+        assert not gx.any()
+
+
 def test_balance_gradient_against_differences():
     b, x, w, idx, m, buf = balance_case(60, 12, 3, 128, "fp32", mask=0.8, balance=1.0, z=0.5)
     K.balance_loss(b, x, w, idx, buf, mask=m, training=True)
@@ -724,3 +742,33 @@ def test_streams_and_graphs():
         eager = run(xs, go, gy, two)
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, eager)), i
+
+
+@pytest.mark.parametrize("t,k,n,dtype", [
+    (7, 512, 1024, "bf16"), (16, 4096, 2100, "bf16"), (600, 300, 500, "bf16"),
+    (150, 500, 333, "fp32"), (3001, 36, 65, "fp32"), (90, 2048, 2048, "fp32")])
+def test_linear_forms_in_graphs(t, k, n, dtype):
+    # each form of the product, replayed beside eager calls of the same problem
+    import torch
+    l, x, w, b, add, dy, buf = linear_case(t, k, n, dtype, "gelu", dtype)
+    other = K.allocate_linear(l, "cuda", training=True)
+
+    def run(x, u):
+        y = K.linear(l, x, w, u, bias=b, residual=add, training=True)
+        return (y, *K.linear_backward(l, x, w, dy, u))
+
+    xs = x.clone()
+    run(xs, buf), run(xs, other)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = run(xs, buf)
+    stream = torch.cuda.Stream()
+    for i in range(3):
+        xs.copy_(x * (1 + 0.5 * i))
+        torch.cuda.synchronize()
+        graph.replay()
+        with torch.cuda.stream(stream):  # at the same time, over its own buffers
+            eager = run(xs, other)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, c) for a, c in zip(outs, eager)), i
