@@ -723,7 +723,6 @@ class Linear:
         """The C problem, the caller's own to change."""
         return moe_linear(*self._fields)
 
-
     @cached_property
     def _plan(self):
         c = self.struct()
@@ -786,6 +785,8 @@ def linear_backward(l: Linear, x, w, grad_out, buf: LinearBuffers, bias: bool = 
     """Gradients of sum(y * grad_out) after ``linear(..., training=True)`` with
     the same buffers: (grad_x, grad_w, grad_bias), the last None where bias is
     False; the residual's gradient is grad_out."""
+    if not isinstance(bias, bool):
+        raise ValueError("bias: True or False, whether its gradient is wanted")
     c, nsv, xs, ws, ys, bs, dt = l._plan
     dev = x.device
     _want("x", x, xs, dt, dev)

@@ -419,7 +419,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void lin_few_bwd_kernel(
     const bf16_t* wr = w + static_cast<int64_t>(min(k0 + i, K - 1)) * N;
     const int row = min(i, rows - 1);
     const bf16_t* dr = dy + static_cast<int64_t>(row) * N;
-    f32x4_t acc = (f32x4_t){0.0f, 0.0f, 0.0f, 0.0f};
+    f32x4_t acc = (f32x4_t){0.0f, 0.0f, 0.0f, 0.0f}, second = acc;
     for (int s = wave * 32 + 8 * g; s - 8 * g < N; s += kBatch * kFewWaves * 32) {
       u32x4 a[kBatch], b[kBatch];
       Raw e[kBatch];
@@ -440,8 +440,8 @@ __global__ __launch_bounds__(64 * kFewWaves) void lin_few_bwd_kernel(
           const u32x4 high = Piece<bf16_t>::narrow(v);
           Piece<bf16_t>::widen(high, rest);
 #pragma unroll
-          for (int q = 0; q < 8; ++q) rest[q] = __builtin_isinf(rest[q]) ? 0.0f : v[q] - rest[q];
-          acc = few_mfma(a[u], Piece<bf16_t>::narrow(rest), acc);
+          for (int q = 0; q < 8; ++q) rest[q] = v[q] - rest[q];
+          second = few_mfma(a[u], Piece<bf16_t>::narrow(rest), second);
           acc = few_mfma(a[u], high, acc);
         } else {
           trim_piece<bf16_t>(b[u], c, N);
@@ -449,6 +449,9 @@ __global__ __launch_bounds__(64 * kFewWaves) void lin_few_bwd_kernel(
         }
       }
     }
+    // an infinity in w or da is in the first sum; the second one's is inf - inf or inf 0
+#pragma unroll
+    for (int q = 0; q < 4; ++q) acc[q] = __builtin_isfinite(acc[q]) ? acc[q] + second[q] : acc[q];
     // column k0 + 4 (lane / 16) + q of row lane % 16
     *reinterpret_cast<f32x4_t*>(&sums[wave][lane * 4]) = acc;
     __syncthreads();

@@ -84,6 +84,8 @@ def test_linear_tensor_refusals():
         K.linear_backward(l, x, w, y[:2], buf)
     with pytest.raises(ValueError, match="GPU"):
         K.linear_backward(l, x, w, y, buf)
+    with pytest.raises(ValueError, match="True or False"):
+        K.linear_backward(l, x, w, y, buf, bias=bias)
     with pytest.raises(ValueError):
         K.allocate_linear(K.Linear(1, 70000, 5), "cpu")
     l.struct().tokens = 99  # the caller's own

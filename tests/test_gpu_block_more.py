@@ -157,6 +157,24 @@ def test_linear_few_rows_round_once(t):
     dy[0, 3] = float("inf")
     gx, gw, gb = K.linear_backward(l, x, w, dy, buf)
     assert bool((torch.isinf(gx[0]) | (w[:, 3] == 0)).all()) and bool(torch.isinf(gb[3]))
+    # as does an infinite weight, whatever da's second half is
+    dy[0, 3], dy[0, 5], w[9, 5] = 0.5, 1.0, float("inf")
+    gx, gw, gb = K.linear_backward(l, x, w, dy, buf)
+    assert bool(torch.isinf(gx[:, 9]).all())
+    gx[:, 9] = 0
+    assert bool(torch.isfinite(gx).all() and torch.isfinite(gw).all())
+
+
+def test_linear_few_rows_infinite_weight_exact_slopes():
+    # relu: da is 0 or exact, its second half 0
+    import torch
+    l, x, w, b, add, dy, buf = linear_case(5, 64, 72, "bf16", "relu", "bf16")
+    K.linear(l, x, w, buf, bias=b, residual=add, training=True)
+    da = linear64(x, w, b, add, dy, "relu")[4]
+    w[3, 4] = float("inf")
+    gx = K.linear_backward(l, x, w, dy, buf)[0]
+    want = da[:, 4] > 0
+    assert torch.equal(torch.isinf(gx[:, 3]), want) and torch.equal(torch.isnan(gx[:, 3]), ~want)
 
 
 def test_linear_fp32_odd_values():
