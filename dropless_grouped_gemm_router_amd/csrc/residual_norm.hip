@@ -398,8 +398,9 @@ __global__ __launch_bounds__(kMax) void step_bwd_kernel(const StepArgs a) {
 struct StepGrads {
   const float *w1, *b1, *gate;
   float *dw1, *db1, *dgate, *dw2, *db2;
+  bool post, pre;  // a norm that is not there has gradients of zero, whatever the sums hold
   int wanted() const {
-    return (dw1 || dgate) | (db1 || (dgate && b1)) << 1 | (dw2 != nullptr) << 2 | (db2 != nullptr) << 3;
+    return ((dw1 && post) || dgate) | ((db1 && post) || (dgate && b1)) << 1 | (dw2 && pre) << 2 | (db2 && pre) << 3;
   }
 };
 constexpr int kSumCols = 32, kSumGroups = 32;
@@ -428,11 +429,11 @@ __global__ __launch_bounds__(1024) void step_sum_kernel(const float* __restrict_
   const int col = blockIdx.x * kSumCols + c;
   if (j || col >= width) return;
   const float A = total[0][c], B = total[1][c], gate = g.gate ? g.gate[col] : 1.0f;
-  if (g.dw1) g.dw1[col] = gate * A;
-  if (g.db1) g.db1[col] = gate * B;
+  if (g.dw1) g.dw1[col] = g.post ? gate * A : 0.0f;
+  if (g.db1) g.db1[col] = g.post ? gate * B : 0.0f;
   if (g.dgate) g.dgate[col] = (g.w1 ? g.w1[col] : 1.0f) * A + (g.b1 ? g.b1[col] * B : 0.0f);
-  if (g.dw2) g.dw2[col] = total[2][c];
-  if (g.db2) g.db2[col] = total[3][c];
+  if (g.dw2) g.dw2[col] = g.pre ? total[2][c] : 0.0f;
+  if (g.db2) g.db2[col] = g.pre ? total[3][c] : 0.0f;
 }
 
 __global__ __launch_bounds__(256) void step_zero_kernel(const StepGrads g, int width) {
@@ -561,10 +562,12 @@ hipError_t launch_residual_norm_bwd(const moe_residual_norm& n, const void* z, c
                                     hipStream_t s) {
   StepArgs a = step_args(n);
   set_params(&a, w, n.post != 0);
-  const StepGrads grads{a.w1, a.b1, a.gate, g.post_weight, g.post_bias, g.gate, g.pre_weight, g.pre_bias};
+  const StepGrads grads{a.w1,         a.b1,         a.gate,      g.post_weight, g.post_bias, g.gate,
+                        g.pre_weight, g.pre_bias, n.post != 0, n.pre != 0};
   const int wanted = grads.wanted();
+  const bool any = g.post_weight || g.post_bias || g.gate || g.pre_weight || g.pre_bias;
   if (n.rows == 0) {
-    if (!wanted) return hipSuccess;
+    if (!any) return hipSuccess;
     MOE_LAUNCH("residual_norm_zero", step_zero_kernel, dim3((n.width + 255) / 256), dim3(256), 0, s, grads,
                n.width);
     return hipGetLastError();
@@ -586,7 +589,7 @@ hipError_t launch_residual_norm_bwd(const moe_residual_norm& n, const void* z, c
     MOE_LAUNCH("residual_norm_bwd", (step_bwd_kernel<decltype(t), decltype(row)::value, decltype(nv)::value, decltype(max)::value>),
                dim3(blocks), dim3(r.threads()), 0, s, a);
   });
-  if (wanted)
+  if (any)  // zeros where no sum is wanted
     MOE_LAUNCH("residual_norm_sum", step_sum_kernel, dim3((n.width + kSumCols - 1) / kSumCols),
                dim3(1024), 0, s, a.partial, blocks, n.width, step_pitch(n.width), grads);
   return hipGetLastError();
