@@ -701,10 +701,18 @@ def linear_i8(l: LinearI8, x, wq, w_scale, buf: I8Buffers, bias=None, routing: O
     return y
 
 
+class _Planned:
+    """A problem that keeps its C struct and what its calls compare with once it
+    has been used (``_plan``): a copy or a pickle is of the problem alone."""
+
+    def __getstate__(self):
+        return {k: v for k, v in vars(self).items() if k != "_plan"}
+
+
 # ----------------------------------- products with bias, activation and residual
 
 @dataclass(frozen=True)
-class Linear:
+class Linear(_Planned):
     """A dense product with its epilogue: y = act(x W + bias) + residual."""
 
     tokens: int
@@ -807,7 +815,7 @@ def linear_backward(l: Linear, x, w, grad_out, buf: LinearBuffers, bias: bool = 
 # ---------------------------------------------------------- between two blocks
 
 @dataclass(frozen=True)
-class ResidualNorm:
+class ResidualNorm(_Planned):
     """What lies between two blocks: out = scale res + gate (norm(z) post_weight
     + post_bias), y = norm(out) pre_weight + pre_bias; without post the block's
     output z is added as it is, without pre there is no y."""
@@ -825,7 +833,6 @@ class ResidualNorm:
         """The C problem, the caller's own to change."""
         return moe_residual_norm(self.rows, self.width, DTYPES[self.dtype], NORM_KINDS[self.kind],
                                  int(self.post), int(self.pre), self.eps, self.scale, *lds)
-
 
     @cached_property
     def _plan(self):
@@ -949,7 +956,7 @@ def residual_norm_backward(n: ResidualNorm, z, res, params: Dict, grad_out, grad
 # ------------------------------------------------------ balance of the router
 
 @dataclass(frozen=True)
-class BalanceLoss:
+class BalanceLoss(_Planned):
     """The router's balance loss and z loss over a batch; see moe_balance_loss."""
 
     tokens: int
@@ -964,7 +971,6 @@ class BalanceLoss:
         """The C problem, the caller's own to change."""
         return moe_balance(self.tokens, self.experts, self.top_k, self.d_model, DTYPES[self.dtype],
                            self.balance, self.z)
-
 
     @cached_property
     def _plan(self):
