@@ -769,7 +769,7 @@ def allocate_linear(l: Linear, device="cuda", training: bool = False) -> LinearB
 def linear(l: Linear, x, w, buf: LinearBuffers, bias=None, residual=None, training: bool = False,
            stream=None):
     """The product of x [tokens, inputs] and w [inputs, outputs] with its
-    epilogue; bias is fp32. Returns buf.y."""
+    epilogue; bias is fp32. Returns buf.y, which may not be the residual's memory."""
     c, nsv, xs, ws, ys, bs, dt = l._plan
     dev, y = x.device, buf.y
     _want("x", x, xs, dt, dev)
@@ -779,6 +779,9 @@ def linear(l: Linear, x, w, buf: LinearBuffers, bias=None, residual=None, traini
     if residual is not None:
         _want("residual", residual, ys, dt, dev)
     _want("y", y, ys, dt, dev)
+    # the library refuses whatever else is shared
+    if residual is not None and l.tokens and residual.data_ptr() == y.data_ptr():
+        raise ValueError("residual: is the buffer of y; rows are stored while others are still read")
     _want_bytes("workspace", buf.workspace, 0, dev)
     if training:
         _want_saved(buf, nsv, dev)

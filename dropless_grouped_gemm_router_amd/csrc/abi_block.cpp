@@ -15,6 +15,11 @@ bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % 
 bool ok_ptr(const void* p, size_t a = 16) { return p != nullptr && aligned(p, a); }
 bool is_float(int t) { return t == MOE_FP32 || t == MOE_BF16; }
 size_t bytes_of(int t) { return t == MOE_BF16 ? 2 : 4; }
+// Whether two arrays of na and nb bytes share any (a null one shares none).
+bool share(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
+  return a && b && p < q + nb && q < p + na;
+}
 int hip_status(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
 hipStream_t as_stream(void* s) { return static_cast<hipStream_t>(s); }
 
@@ -244,6 +249,10 @@ MOE_EXPORT int moe_linear_fwd(const moe_linear* l, const void* x, const void* w,
       !ok_ptr(y) || !ok_ptr(workspace, 256))
     return MOE_ERR_INVALID;
   if (workspace_bytes < moe::linear_ws_bytes(*l, false)) return MOE_ERR_WORKSPACE;
+  // y is stored tile by tile while others still read
+  const size_t e = bytes_of(l->dtype), nx = l->tokens * l->inputs * e, ny = l->tokens * l->outputs * e;
+  const size_t nw = static_cast<size_t>(l->inputs) * l->outputs * e;
+  if (share(y, ny, residual, ny) || share(y, ny, x, nx) || share(y, ny, w, nw)) return MOE_ERR_INVALID;
   return hip_status(moe::launch_linear(*l, x, w, bias, residual, saved, y, workspace, as_stream(stream)));
 }
 
@@ -258,6 +267,12 @@ MOE_EXPORT int moe_linear_bwd(const moe_linear* l, const void* x, const void* w,
       return MOE_ERR_INVALID;
     if (l->act != MOE_ACT_NONE && !ok_ptr(saved, 256)) return MOE_ERR_INVALID;
     if (workspace_bytes < moe::linear_ws_bytes(*l, true)) return MOE_ERR_WORKSPACE;
+    const size_t e = bytes_of(l->dtype), nx = l->tokens * l->inputs * e, ny = l->tokens * l->outputs * e;
+    const size_t cells = static_cast<size_t>(l->inputs) * l->outputs, nw = cells * e, ng = cells * bytes_of(l->grad_dtype);
+    if (share(grad_x, nx, x, nx) || share(grad_x, nx, w, nw) || share(grad_x, nx, grad_out, ny) ||
+        share(grad_w, ng, x, nx) || share(grad_w, ng, w, nw) || share(grad_w, ng, grad_out, ny) ||
+        share(grad_x, nx, grad_w, ng))
+      return MOE_ERR_INVALID;
   }
   return hip_status(moe::launch_linear_bwd(*l, x, w, saved, grad_out, grad_x, grad_w, grad_bias, workspace,
                                            as_stream(stream)));

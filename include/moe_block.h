@@ -250,7 +250,9 @@ size_t moe_linear_saved_bytes(const moe_linear* l);
 
 /* Forward. bias and residual may be NULL. saved: NULL for inference (or with
  * MOE_ACT_NONE, where it is not touched), else moe_linear_saved_bytes(l) bytes
- * (256-byte aligned). tokens == 0 is a successful no-op. */
+ * (256-byte aligned). tokens == 0 is a successful no-op. A y that shares memory
+ * with x, W or the residual is refused (MOE_ERR_INVALID), as are gradients that
+ * share it with each other or with an input of moe_linear_bwd. */
 int moe_linear_fwd(const moe_linear* l, const void* x, const void* w, const float* bias,
                    const void* residual, void* saved, void* y, void* workspace,
                    size_t workspace_bytes, void* stream);

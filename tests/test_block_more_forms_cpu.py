@@ -6,8 +6,11 @@ import copy
 import pickle
 
 import pytest
+import torch
 
 from dropless_grouped_gemm_router_amd import block as K
+
+from test_block_cpu import INV, A, At, C, D, E, F, G, H, refused
 
 
 @pytest.mark.parametrize("problem", [K.Linear(4, 64, 96, "bf16", "gelu"), K.ResidualNorm(3, 65, "fp32", "rms", pre=False),
@@ -21,3 +24,39 @@ def test_problems_are_copied_and_pickled(problem):
             assert again._plan[1:-1] == problem._plan[1:-1]
             assert again._plan is not problem._plan
         assert "_plan" in vars(problem)
+
+
+@pytest.mark.parametrize("dtype", [0, 1])
+def test_linear_refuses_shared_memory(dtype):
+    """An output over an input would be stored while other tiles still read it."""
+    l = K.moe_linear(300, 256, 512, dtype, 0, dtype)
+    e = 2 if dtype else 4
+    nx, ny, nw = 300 * 256 * e, 300 * 512 * e, 256 * 512 * e
+    room = dict(workspace_bytes=1 << 40, stream=0)
+    fwd = [A, C, D, E, F, G, H]  # x, w, bias, residual, saved, y, workspace
+    for i, n in ((0, nx), (1, nw), (3, ny)):
+        # the same address, the output's last bytes over the input's first, and the reverse
+        for at in (0, 16 - ny, n - 16):
+            args = list(fwd)
+            args[5] = At(args[i].addr + at)
+            refused(INV, K.moe_linear_fwd, l, *args, **room)
+    bwd = [A, C, D, E, F, G, H, At(9 << 28)]  # x, w, saved, grad_out, grad_x, grad_w, grad_bias, workspace
+    for o, no in ((4, nx), (5, nw)):
+        for i, n in ((0, nx), (1, nw), (3, ny)):
+            for at in (0, 16 - no, n - 16):
+                args = list(bwd)
+                args[o] = At(args[i].addr + at)
+                refused(INV, K.moe_linear_bwd, l, *args, **room)
+    args = list(bwd)
+    args[5] = At(args[4].addr + nx - 16)
+    refused(INV, K.moe_linear_bwd, l, *args, **room)
+
+
+def test_linear_refuses_its_output_as_residual():
+    l = K.Linear(6, 64, 96, "bf16")
+    x, w, y = (torch.zeros(s, dtype=torch.bfloat16) for s in ((6, 64), (64, 96), (6, 96)))
+    buf = K.LinearBuffers(y, torch.zeros(1 << 20, dtype=torch.uint8))
+    with pytest.raises(ValueError, match="residual"):
+        K.linear(l, x, w, buf, residual=y)
+    with pytest.raises(ValueError, match="GPU"):
+        K.linear(l, x, w, buf, residual=y.clone())
