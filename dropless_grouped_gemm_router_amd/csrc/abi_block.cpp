@@ -4,6 +4,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <initializer_list>
 
 #include "block.h"
 
@@ -87,6 +88,20 @@ int check_residual_norm(const moe_residual_norm* n) {
     if (ld >= kRowLimit) return MOE_ERR_UNSUPPORTED;
   }
   return MOE_OK;
+}
+
+// Whether an output lies over an input with other rows than the input's: a row
+// would be stored over one that is still to be read.
+struct Rows {
+  const void* p;
+  int64_t ld;
+};
+bool askew(const moe_residual_norm& n, std::initializer_list<Rows> outs, std::initializer_list<Rows> ins) {
+  auto ld = [&](int64_t v) { return v ? v : static_cast<int64_t>(n.width); };
+  for (const Rows& o : outs)
+    for (const Rows& i : ins)
+      if (o.p && o.p == i.p && n.rows > 1 && ld(o.ld) != ld(i.ld)) return true;
+  return false;
 }
 
 bool ok_params(const moe_norm_params* p) {
@@ -289,6 +304,7 @@ MOE_EXPORT int moe_residual_norm_fwd(const moe_residual_norm* n, const void* z, 
   if (!ok_ptr(z, e) || !ok_ptr(res, e) || !ok_ptr(out, e) || !aligned(y, e) || !aligned(stats, 4) ||
       (y != nullptr) != (n->pre == 1) || out == y)
     return MOE_ERR_INVALID;
+  if (askew(*n, {{out, n->ld_out}, {y, n->ld_y}}, {{z, n->ld_z}, {res, n->ld_res}})) return MOE_ERR_INVALID;
   return hip_status(moe::launch_residual_norm(*n, z, res, *params, out, y, stats, as_stream(stream)));
 }
 
@@ -315,6 +331,9 @@ MOE_EXPORT int moe_residual_norm_bwd(const moe_residual_norm* n, const void* z, 
         !ok_ptr(grad_z, e) || !ok_ptr(grad_res, e) || grad_z == grad_res)
       return MOE_ERR_INVALID;
     if ((grad_y != nullptr) != (n->pre == 1)) return MOE_ERR_INVALID;
+    if (askew(*n, {{grad_z, n->ld_grad_z}, {grad_res, n->ld_grad_res}},
+              {{z, n->ld_z}, {res, n->ld_res}, {grad_out, n->ld_grad_out}, {grad_y, n->ld_grad_y}}))
+      return MOE_ERR_INVALID;
     if (any) {
       if (!ok_ptr(workspace, 256)) return MOE_ERR_INVALID;
       if (workspace_bytes < moe::residual_norm_ws_bytes(*n)) return MOE_ERR_WORKSPACE;

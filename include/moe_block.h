@@ -289,7 +289,7 @@ typedef enum {
  * Rows may lie apart: ld_* is the number of elements between rows (0: width),
  * and the matrices need only the alignment of their elements. out and y may be
  * z or res, and grad_z and grad_res may be z, res, grad_out or grad_y, each
- * another one and with equal strides.
+ * another one and with equal strides (MOE_ERR_INVALID where these differ).
  *
  * Supported (else MOE_ERR_UNSUPPORTED): width <= 16384, rows < 2^31.
  */

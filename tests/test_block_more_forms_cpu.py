@@ -60,3 +60,25 @@ def test_linear_refuses_its_output_as_residual():
         K.linear(l, x, w, buf, residual=y)
     with pytest.raises(ValueError, match="GPU"):
         K.linear(l, x, w, buf, residual=y.clone())
+
+
+def test_step_refuses_other_strides_in_place():
+    """An output over an input has to have its rows."""
+    def step(**ld):
+        names = ("z", "res", "out", "y", "grad_out", "grad_y", "grad_z", "grad_res")
+        return K.moe_residual_norm(10, 512, 1, 0, 1, 1, 1e-5, 1.0, *[ld.get(n, 0) for n in names])
+
+    p = dict(post_weight=A)
+    for out in ("out", "y"):
+        for given in ("z", "res"):
+            at = dict(z=A, res=C, out=D, y=E)
+            at[out] = at[given]
+            for ld in ({out: 520}, {given: 520}, {out: 520, given: 528}):
+                refused(INV, K.moe_residual_norm_fwd, step(**ld), at["z"], at["res"], p, at["out"], at["y"], F, stream=0)
+    for out in ("grad_z", "grad_res"):
+        for given in ("z", "res", "grad_out", "grad_y"):
+            at = dict(z=A, res=C, grad_out=D, grad_y=E, grad_z=F, grad_res=G)
+            at[out] = at[given]
+            for ld in ({out: 520}, {given: 520}, {out: 520, given: 528}):
+                refused(INV, K.moe_residual_norm_bwd, step(**ld), at["z"], at["res"], p, H, at["grad_out"], at["grad_y"],
+                        at["grad_z"], at["grad_res"], p, At(9 << 28), stream=0)
