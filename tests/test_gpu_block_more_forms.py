@@ -8,7 +8,7 @@ from dropless_grouped_gemm_router_amd import block as K
 
 from gpu_util import note
 from test_gpu_block import gen
-from test_gpu_block_more import step_params
+from test_gpu_block_more import step_params, test_step_strided_and_in_place as strided_and_in_place
 
 pytestmark = pytest.mark.gpu
 
@@ -48,3 +48,12 @@ def test_step_gradients_of_an_absent_norm(rows, width, dtype):
             assert set(w) == set(only)
             for k in only:
                 assert torch.equal(g[k].view(torch.int32), w[k].view(torch.int32)), k
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("width", [257, 4100, 6200, 8191, 8200, 16383])
+def test_wide_step_strided_and_in_place(width, dtype):
+    # rows of several waves, and workgroups of 1024 threads that read the parameters
+    # for every row
+    note(f"step strided {width} {dtype}")
+    strided_and_in_place(width, dtype)
