@@ -1169,7 +1169,8 @@ def prenorm_backward(p, x, weights: Dict, grad_out, buf, norm: NormBuffers, stre
 
 def _want_loss(p, loss):
     b = loss[0]
-    if (b.tokens, b.experts, b.top_k, b.d_model, b.dtype) != (p.tokens, p.experts, p.top_k, p.d_model, p.dtype):
+    if ((b.tokens, b.experts, b.top_k, b.d_model, DTYPES[b.dtype])
+            != (p.tokens, p.experts, p.top_k, p.d_model, _dtype(p.dtype))):
         raise ValueError(f"loss: of {b}, not of {p}")
 
 

@@ -8,7 +8,9 @@ import pickle
 import pytest
 import torch
 
+from dropless_grouped_gemm_router_amd import binding as B
 from dropless_grouped_gemm_router_amd import block as K
+from dropless_grouped_gemm_router_amd.inputs import Problem
 
 from test_block_cpu import INV, A, At, C, D, E, F, G, H, refused
 
@@ -82,3 +84,12 @@ def test_step_refuses_other_strides_in_place():
             for ld in ({out: 520}, {given: 520}, {out: 520, given: 528}):
                 refused(INV, K.moe_residual_norm_bwd, step(**ld), at["z"], at["res"], p, H, at["grad_out"], at["grad_y"],
                         at["grad_z"], at["grad_res"], p, At(9 << 28), stream=0)
+
+
+def test_loss_of_a_problem_struct():
+    """The layer takes any object with its fields, the type a name or a number."""
+    for p in (Problem(12, 4, 2, 128, 64, 0, "bf16", 64), B.problem_struct(Problem(12, 4, 2, 128, 64, 0, "bf16", 64))):
+        K._want_loss(p, (K.BalanceLoss(12, 4, 2, 128, "bf16"), None))
+        for b in (K.BalanceLoss(12, 4, 2, 128, "fp32"), K.BalanceLoss(13, 4, 2, 128, "bf16"), K.BalanceLoss(12, 4, 1, 128)):
+            with pytest.raises(ValueError, match="loss"):
+                K._want_loss(p, (b, None))

@@ -4,9 +4,11 @@ a rounding step of the storage type (bf16 2^-8, fp32 2^-24)."""
 
 import pytest
 
+from dropless_grouped_gemm_router_amd import binding as B
 from dropless_grouped_gemm_router_amd import block as K
+from dropless_grouped_gemm_router_amd.inputs import Problem
 
-from gpu_util import note
+from gpu_util import Case, note
 from test_gpu_block import gen
 from test_gpu_block_more import step_params, test_step_strided_and_in_place as strided_and_in_place
 
@@ -57,3 +59,22 @@ def test_wide_step_strided_and_in_place(width, dtype):
     # for every row
     note(f"step strided {width} {dtype}")
     strided_and_in_place(width, dtype)
+
+
+# -------------------------------------------------------------- balance loss
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_residual_layer_of_a_problem_struct(dtype):
+    # the layer's C problem, whose type is a number, gives what the named one gives
+    import torch
+    p = Problem(70, 8, 2, 128, 128, 0, dtype, 64)
+    c, r = Case(p, seed=3, training=True), gen(11)
+    n, b = K.ResidualNorm(70, 128, dtype), K.BalanceLoss(70, 8, 2, 128, dtype, 1.0, 0.1)
+    step, loss = K.allocate_residual_norm(n, "cuda", training=True), K.allocate_balance_loss(b, "cuda", training=True)
+    h, w, res, go, gy = c.dev["x"], c.weights(), *(r(70, 128, dtype=dtype) for _ in range(3))
+    got = []
+    for problem in (p, B.problem_struct(p)):
+        out, y = K.residual_layer_forward(problem, h, res, w, c.buf, n, step, (b, loss), training=True)
+        gh, gs, grads = K.residual_layer_backward(problem, h, res, w, go, gy, c.buf, n, step, (b, loss))
+        got.append([t.clone() for t in (out, y, loss.loss, gh, gs, *(grads[k] for k in sorted(grads)))])
+    assert all(torch.equal(a, c) for a, c in zip(*got))
