@@ -19,7 +19,8 @@
 // backward's dx reads them as they are. da is made in one pass over dy that
 // also adds up dbias and pads the rows; without an activation dy itself is da.
 //
-// Up to 16 bf16 rows have a backward pass of one launch (lin_few_bwd_kernel), and
+// Up to 16 bf16 rows keep da unrounded, in a backward pass of one launch
+// (lin_few_bwd_kernel) or, where weights are large, in tiles (lin_halves_kernel), and
 // fp32 products of moderate size take both passes' operands from memory as they
 // are, in one launch each (direct.h).
 #include "dense.h"
@@ -37,10 +38,10 @@ constexpr int64_t kFewRows = 16, kFewRowsF32 = 128;
 // fp32, 64 rows, 512 x 2048 8.1 and 8.4, 16 rows, 1024 x 1024 12.8 and 10.9.
 constexpr int kRowsWaves = 16, kShortK = 2048, kShortKF32 = 512;
 
-// The backward of few rows in one launch; a training pass so and in tiles, us: 1 x
-// 512 x 512 17 and 29, 16 x 512 x 4096 23 and 28, 16 x 2048 x 2048 25 and 29, 2 x 8192
-// x 2048 36 and 39; past its limits 16 x 128 x 16384 64 and 29, 16 x 65536 x 64 67 and 44,
-// 16 x 4096 x 4096 56 and 41.
+// The backward of few rows in one launch; a training pass so and in tiles
+// (lin_halves_kernel), us: 1 x 512 x 512 15 and 22, 16 x 512 x 4096 22 and 22, 16 x 2048 x
+// 2048 24 and 25, 2 x 8192 x 2048 35 and 35; past its limits 16 x 128 x 16384 64 and 22, 16 x
+// 65536 x 64 67 and 42, 16 x 4096 x 4096 56 and 37.
 constexpr int kFewInputs = 8192, kFewOutputs = 4096;
 constexpr int64_t kFewProducts = int64_t{1} << 26;
 
@@ -385,10 +386,22 @@ __global__ __launch_bounds__(32 * kDaRows) void lin_da_kernel(const T* __restric
 // memory, eight waves share the outputs, and da goes in as two bf16 numbers, of which
 // the second holds what the first one rounds away (one row's da would err in every
 // term alike). In the others a wave makes 64 x 64 of dW, eight by eight a lane in
-// plain fp32. 16 rows, 1024 x 1024: a training pass 19 us, where forming da, two
-// products in tiles and adding slices made it 29; the backward alone at 2048 x 2048, 1
+// plain fp32. 16 rows, 1024 x 1024: a training pass 18 us, with its products in tiles 22;
+// the backward alone at 2048 x 2048, 1
 // row to 16: 13 to 18 us (24 MB: 5), bound by the lanes' additions.
 constexpr int kFewWaves = 8, kFewTile = 64, kFewCols = 16;
+// da of eight columns from c on, zeros from column n on.
+template <bool kSlope>
+__device__ __forceinline__ void few_da(u32x4 raw, const Slopes<bf16_t>::Raw& sl, int c, int n, float (&v)[8]) {
+  trim_piece<bf16_t>(raw, c, n);
+  Piece<bf16_t>::widen(raw, v);
+  if constexpr (kSlope) {
+    float e[8];
+    Slopes<bf16_t>::get8(sl, e);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) v[q] = c + q < n ? v[q] * e[q] : 0.0f;
+  }
+}
 __device__ __forceinline__ f32x4_t few_mfma(const u32x4& a, const u32x4& b, const f32x4_t& c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c, 0,
                                                  0, 0);
@@ -401,17 +414,6 @@ __global__ __launch_bounds__(64 * kFewWaves) void lin_few_bwd_kernel(
   typedef Slopes<bf16_t>::Raw Raw;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int last = static_cast<int>(slope.ld) - 8;  // slopes of columns there are
-  // da of eight columns from c on
-  auto form = [&](u32x4 raw, const Raw& sl, int c, float (&v)[8]) {
-    trim_piece<bf16_t>(raw, c, N);
-    Piece<bf16_t>::widen(raw, v);
-    if constexpr (kSlope) {
-      float e[8];
-      Slopes<bf16_t>::get8(sl, e);
-#pragma unroll
-      for (int q = 0; q < 8; ++q) v[q] = c + q < N ? v[q] * e[q] : 0.0f;
-    }
-  };
   if (static_cast<int>(blockIdx.x) < first) {
     constexpr int kBatch = 4;
     __shared__ float sums[kFewWaves][16 * kFewCols];
@@ -436,7 +438,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void lin_few_bwd_kernel(
         trim_piece<bf16_t>(a[u], c, N);
         if constexpr (kSlope) {
           float v[8], rest[8];
-          form(b[u], e[u], c, v);
+          few_da<kSlope>(b[u], e[u], c, N, v);
           const u32x4 high = Piece<bf16_t>::narrow(v);
           Piece<bf16_t>::widen(high, rest);
 #pragma unroll
@@ -492,7 +494,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void lin_few_bwd_kernel(
       float xs[8], v[8];
       trim_piece<bf16_t>(a[u], k, K);
       Piece<bf16_t>::widen(a[u], xs);
-      form(b[u], e[u], c, v);
+      few_da<kSlope>(b[u], e[u], c, N, v);
 #pragma unroll
       for (int q = 0; q < 8; ++q) total[q] += v[q];
 #pragma unroll
@@ -510,6 +512,78 @@ __global__ __launch_bounds__(64 * kFewWaves) void lin_few_bwd_kernel(
     for (int q = 0; q < 8; ++q)
       if (c + q < N) dbias[c + q] = total[q];
   }
+}
+
+// Up to 16 bf16 rows past the limits of that launch take the products in tiles, with
+// da as the same two bf16 numbers: `rows` rows of the first ones and behind them as
+// many of the second, zeros from column N on. A tile has 64 rows and a stage of the
+// weights' gradient 64 tokens, so the second ones cost no step of either product: dx
+// comes as 2 rows' sums, which lin_join_halves_kernel adds, and for dW x goes in
+// twice, behind its padding's zeros; the second time without infinities and NaN, whose
+// products the first numbers make. dbias is added up on the way, in fp32.
+// Training passes, us, and what they were with one rounded da: 16 x 4096 x 4096 37
+// (40), 1 x 4096 x 8192 54 (57), 16 x 128 x 16384 22 (26): no launch for dbias's slices.
+constexpr int kHalvesCols = 128;
+__global__ __launch_bounds__(256) void lin_halves_kernel(const bf16_t* __restrict__ dy, const Slopes<bf16_t> slope,
+                                                         bf16_t* __restrict__ da, float* __restrict__ dbias,
+                                                         const bf16_t* __restrict__ x, bf16_t* __restrict__ xs,
+                                                         int rows, int K, int kp, int N, int np) {
+  typedef Piece<bf16_t> P;
+  __shared__ float sums[16][kHalvesCols];
+  // 16 rows of 16 pieces: of da first, of x behind it
+  const int t = threadIdx.x / 16, tx = threadIdx.x % 16, across = np / kHalvesCols;
+  if (static_cast<int>(blockIdx.x) >= across) {
+    const int c = (blockIdx.x - across) * kHalvesCols + tx * 8;
+    if (t >= rows) return;
+    const u32x4 v = load_piece(x + static_cast<int64_t>(t) * K, c, K);
+    bf16_t* to = xs + static_cast<int64_t>(t) * kp + c;
+    *reinterpret_cast<u32x4*>(to) = v;
+    float e[8];
+    P::widen(v, e);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) e[q] = __builtin_isfinite(e[q]) ? e[q] : 0.0f;
+    *reinterpret_cast<u32x4*>(to + static_cast<int64_t>(rows) * kp) = P::narrow(e);
+    return;
+  }
+  const int c = blockIdx.x * kHalvesCols + tx * 8, row = min(t, rows - 1);
+  float v[8], rest[8];
+  few_da<true>(load_near(dy + static_cast<int64_t>(row) * N, c, N),
+               slope.load8(row, min(c, static_cast<int>(slope.ld) - 8)), c, N, v);
+  const u32x4 high = P::narrow(v);
+  P::widen(high, rest);
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    sums[t][tx * 8 + q] = v[q];
+    rest[q] = __builtin_isfinite(rest[q]) ? v[q] - rest[q] : 0.0f;
+  }
+  if (t < rows) {
+    bf16_t* to = da + static_cast<int64_t>(t) * np + c;
+    *reinterpret_cast<u32x4*>(to) = high;
+    *reinterpret_cast<u32x4*>(to + static_cast<int64_t>(rows) * np) = P::narrow(rest);
+  }
+  if (!dbias) return;
+  __syncthreads();
+  const int n = blockIdx.x * kHalvesCols + threadIdx.x;
+  if (threadIdx.x >= kHalvesCols || n >= N) return;
+  float total = 0.0f;
+  for (int r = 0; r < rows; ++r) total += sums[r][threadIdx.x];
+  dbias[n] = total;
+}
+
+// dx [rows][K] from the sums [parts][2 rows][K] of the slices and of da's two numbers;
+// an infinity of w or da is in the first one's.
+__global__ __launch_bounds__(256) void lin_join_halves_kernel(const float* __restrict__ part, int parts, int rows,
+                                                              int K, bf16_t* __restrict__ dx) {
+  const int n = blockIdx.x * 256 + threadIdx.x;
+  if (n >= K) return;
+  const int64_t row = blockIdx.y;
+  float first = 0.0f, second = 0.0f;
+#pragma unroll 4
+  for (int p = 0; p < parts; ++p) {
+    first += part[(int64_t{2} * p * rows + row) * K + n];
+    second += part[((int64_t{2} * p + 1) * rows + row) * K + n];
+  }
+  put(dx + row * K + n, __builtin_isfinite(first) ? first + second : first);
 }
 
 // ---------------------------------------------------- fp32 of moderate size
@@ -632,6 +706,11 @@ bool few_bwd(const moe_linear& l) {
   return l.dtype == MOE_BF16 && few_rows(l) && l.inputs <= kFewInputs && l.outputs <= kFewOutputs &&
          l.tokens * l.inputs * l.outputs <= kFewProducts;
 }
+// Whether da goes into the tiles as two numbers (lin_halves_kernel); without an
+// activation it is dy itself.
+bool halves(const moe_linear& l) {
+  return l.dtype == MOE_BF16 && few_rows(l) && l.act != MOE_ACT_NONE && !few_bwd(l);
+}
 // Slices of k: a workgroup a CU, of two steps a wave at least.
 int64_t dir_tiles(int64_t M, int64_t N) {
   return (M + kDirTile - 1) / kDirTile * ((N + kDirTile - 1) / kDirTile);
@@ -696,6 +775,16 @@ LinLayout lin_layout(const moe_linear& l, bool training) {
     return L;
   }
   L.zero = take(kTrZeroBytes);
+  if (halves(l)) {
+    L.da = take(2 * T * np * es);
+    L.wp = take(N == np ? 0 : K * np * es);
+    L.xp = take(2 * T * kp * es);
+    L.dx_parts = tile_parts(es, 2 * T, K, np);
+    L.dx_sums = take(L.dx_parts * 2 * T * K * sizeof(float));
+    L.grad_parts = 1;
+    L.total = std::max(L.total, o);
+    return L;
+  }
   L.da = take(l.act == MOE_ACT_NONE && N == np ? 0 : T * np * es);
   L.wp = take(N == np ? 0 : K * np * es);
   L.bias_parts = bias_slices(l);
@@ -923,6 +1012,33 @@ hipError_t lin_bwd_t(const moe_linear& l, const void* x, const void* w, const vo
       };
       if (l.act == MOE_ACT_NONE) go(std::false_type{});
       else go(std::true_type{});
+      return hipGetLastError();
+    }
+    if (halves(l)) {
+      const int rows = static_cast<int>(tok);
+      bf16_t* da = reinterpret_cast<bf16_t*>(W + L.da);
+      bf16_t* xs = reinterpret_cast<bf16_t*>(W + L.xp);
+      u32x4* zero = reinterpret_cast<u32x4*>(W + L.zero);
+      float* part = reinterpret_cast<float*>(W + L.dx_sums);
+      // padded widths are multiples of kHalvesCols
+      MOE_LAUNCH("linear_bwd_da", lin_halves_kernel, dim3(static_cast<unsigned>((np + kp) / kHalvesCols)), dim3(256), 0, s,
+                 static_cast<const bf16_t*>(dy), slopes_at<bf16_t>(l, const_cast<void*>(saved)), da, dbias,
+                 static_cast<const bf16_t*>(x), xs, rows, K, static_cast<int>(kp), N, static_cast<int>(np));
+      PadJobs pads{};
+      const void* wp = padded<T>(pads, w, W + L.wp, K, N);
+      pad<T>("linear_pad", pads, s);
+      LinOut<T> sums{};
+      sums.y = part;
+      sums.ld = K;
+      sums.M = 2 * tok;
+      sums.N = K;
+      sums.zero = zero;
+      MmArgs p = rows_of<T>(da, np, wp, np, 2 * tok, K, np);
+      p.parts = L.dx_parts;
+      lin_tiles_at<T, MmSmall, MOE_ACT_NONE, true, false>("linear_bwd_dx", p, sums, s);
+      MOE_LAUNCH("linear_join", lin_join_halves_kernel, dim3((K + 255) / 256, rows), dim3(256), 0, s, part, L.dx_parts,
+                 rows, K, static_cast<bf16_t*>(dx));
+      grad_direct<G>("linear_bwd_dw", xs, kp, da, np, kp, np, 2 * tok, K, N, np, dw, dw, zero, s);
       return hipGetLastError();
     }
   }

@@ -224,7 +224,7 @@ int moe_linear_i8(const moe_i8_linear* l, const void* x, const float* x_scale, c
  * x [tokens, inputs], W [inputs, outputs], residual and y [tokens, outputs] in
  * dtype, bias fp32 [outputs]; sums are fp32 and y is rounded once. In bf16 the
  * slopes act'(a) are kept in 20 bits for the backward pass (off by at most
- * 6.4e-7), where da is rounded to bf16 for its two products unless tokens are few.
+ * 6.4e-7), where from 17 tokens on da is rounded to bf16 for its two products.
  *
  * Supported (else MOE_ERR_UNSUPPORTED): inputs and outputs up to 65536 (any
  * value), tokens < 2^31, tokens * max(inputs, outputs) < 2^36.

@@ -9,10 +9,89 @@ from dropless_grouped_gemm_router_amd import block as K
 from dropless_grouped_gemm_router_amd.inputs import Problem
 
 from gpu_util import Case, note
-from test_gpu_block import gen
-from test_gpu_block_more import step_params, test_step_strided_and_in_place as strided_and_in_place
+from test_gpu_block import U, gen
+from test_gpu_block_forms import slope64
+from test_gpu_block_more import linear_case, step_params
+from test_gpu_block_more import test_step_strided_and_in_place as strided_and_in_place
 
 pytestmark = pytest.mark.gpu
+
+
+# -------------------------------------------------------------------- product
+
+def products64(x, w, b, dy, act):
+    """da and the gradients (dx, dw, dbias) in 64 bits, and the sizes of their
+    terms; with the sizes of the terms that the slopes' errors make, dy for da."""
+    x, w, dy = x.double(), w.double(), dy.double()
+    a = x @ w + b.double()
+    da = dy * slope64(a, act)
+
+    def back(da, x, w):
+        return da @ w.t(), x.t() @ da, da.sum(0)
+
+    return da, back(da, x, w), back(da.abs(), x.abs(), w.abs()), back(dy.abs(), x.abs(), w.abs())
+
+
+@pytest.mark.parametrize("grad", ["bf16", "fp32"])
+@pytest.mark.parametrize("t,k,n", [(1, 130, 70), (7, 2048, 4096), (16, 2048, 2048),   # on one side of the limits
+                                   (1, 64, 4104), (2, 9001, 33), (7, 8200, 40), (16, 2056, 2048), (9, 70, 6001),
+                                   (1, 4096, 8192), (16, 65536, 8)])                   # and on the other
+def test_linear_few_rows_round_the_result_only(t, k, n, grad):
+    """Every gradient of up to 16 bf16 rows, element by element: half a step of
+    its type; da as two bf16 numbers, which leave 2^-17 of it; fp32 sums, sqrt(terms)
+    2^-24 four times over; and slopes off by 2^-20, as they are kept and GELU's
+    distribution is fitted, and by the error of a, four sqrt(k) 2^-24 of its deviation of
+    about one, times the slope's own slope, below 0.8. (da rounded to bf16 would be 2^-9 off
+    in every term of a column of dw.)"""
+    note(f"linear few rows {t} {k} {n} {grad}")
+    l, x, w, b, _, dy, buf = linear_case(t, k, n, "bf16", "gelu", grad, res=False)
+    for m in (buf.grad_x, buf.grad_w, buf.grad_bias):
+        m.fill_(float("nan"))
+    K.linear(l, x, w, buf, bias=b, training=True)
+    buf.workspace.fill_(255)
+    got = K.linear_backward(l, x, w, dy, buf)
+    _, want, terms, slopes = products64(x, w, b, dy, "gelu")
+    u = 2.0 ** -24
+    slope = 2.0 ** -20 + 0.8 * 4 * k ** 0.5 * u
+    for name, g, v, size, dsize, half, long in zip(("dx", "dw", "dbias"), got, want, terms, slopes,
+                                                   (U["bf16"], U[grad], 0.0), (n, t, t)):
+        bound = half * v.abs() + ((0.0 if name == "dbias" else 2.0 ** -17) + 4 * long ** 0.5 * u) * size + slope * dsize
+        assert bool(((g.double() - v).abs() <= bound).all()), name
+
+
+@pytest.mark.parametrize("t,k,n", [(3, 64, 96), (3, 64, 4104), (16, 8200, 65)])
+def test_linear_few_rows_infinities(t, k, n):
+    """Infinite gradients, inputs and weights give what they give in da and its
+    products, whatever the second half of a number is."""
+    import torch
+    note(f"linear few rows infinities {t} {k} {n}")
+    l, x, w, b, _, dy, buf = linear_case(t, k, n, "bf16", "gelu", "fp32", res=False)
+
+    def run(x, w, dy):
+        # the forward's slopes are those of finite numbers
+        return [g.clone() for g in K.linear_backward(l, x, w, dy, buf)]
+
+    K.linear(l, x, w, buf, bias=b, training=True)
+    plain = run(x, w, dy)
+    da, want, _, _ = products64(x, w, b, dy, "gelu")
+    inf = float("inf")
+    dys, xs, ws = dy.clone(), x.clone(), w.clone()
+    dys[1, 3], xs[2, 5], ws[7, 2] = inf, -inf, inf
+    gx, gw, gb = run(x, w, dys)
+    sign = (dys[1, 3].double() * (da[1, 3] / dy[1, 3].double())).sign()
+    assert bool((gx[1].double() == inf * sign * w[:, 3].double().sign()).all())
+    assert bool((gw[:, 3].double() == inf * sign * x[1].double().sign()).all()) and float(gb[3]) == float(inf * sign)
+    others = torch.arange(n, device="cuda") != 3
+    assert torch.equal(gw[:, others], plain[1][:, others]) and torch.equal(gx[[0, 2]], plain[0][[0, 2]])
+    gx, gw, gb = run(xs, w, dy)
+    assert torch.equal(gx, plain[0]) and torch.equal(gb, plain[2])
+    assert bool((gw[5].double() == -inf * da[2].sign()).all())
+    others = torch.arange(k, device="cuda") != 5
+    assert torch.equal(gw[others], plain[1][others])
+    gx, gw, gb = run(x, ws, dy)
+    assert bool((gx[:, 7].double() == inf * da[:, 2].sign()).all())
+    others = torch.arange(k, device="cuda") != 7
+    assert torch.equal(gx[:, others], plain[0][:, others]) and torch.equal(gw, plain[1])
 
 
 # ------------------------------------------------------------- residual step
