@@ -11,7 +11,7 @@ from dropless_grouped_gemm_router_amd.inputs import Problem
 from gpu_util import Case, note
 from test_gpu_block import U, gen
 from test_gpu_block_forms import slope64
-from test_gpu_block_more import linear_case, step_params
+from test_gpu_block_more import balance64, balance_case, linear_case, step_params
 from test_gpu_block_more import test_step_strided_and_in_place as strided_and_in_place
 
 pytestmark = pytest.mark.gpu
@@ -141,6 +141,27 @@ def test_wide_step_strided_and_in_place(width, dtype):
 
 
 # -------------------------------------------------------------- balance loss
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("t,e,k,d", [(31, 5, 2, 256), (200, 8, 2, 512), (1000, 47, 6, 1152), (5000, 64, 8, 512),
+                                     (8193, 40, 2, 256), (66000, 20, 2, 128)])
+def test_balance_each_loss(t, e, k, d, dtype):
+    """Each of the three against its own size. A logit is off by sqrt(d) 2^-24 of
+    |x| |w|, under 2^-20, p by that and an exponential's 2^-21 of itself and lse by as
+    much: 2^-18 of each loss, whose terms are of one sign, holds both. The weighted sum
+    is held to its two terms."""
+    import torch
+    note(f"balance losses {t} {e} {k} {d} {dtype}")
+    for kw in ({}, dict(balance=1.0, z=0.1), dict(balance=0.5, z=-0.02)):
+        b, x, w, idx, m, buf = balance_case(t, e, k, d, dtype, mask=0.8, **kw)
+        want = balance64(b, x, w, idx, m)[0].tolist()
+        c1, c2 = (float(torch.tensor(c, dtype=torch.float32)) for c in (b.balance, b.z))
+        for training in (False, True):
+            got = K.balance_loss(b, x, w, idx, buf, mask=m, training=training).tolist()
+            for i in (1, 2):
+                assert abs(got[i] - want[i]) <= 2.0 ** -18 * want[i], i
+            assert abs(got[0] - (c1 * want[1] + c2 * want[2])) <= 2.0 ** -18 * (abs(c1) * want[1] + abs(c2) * want[2])
+
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_residual_layer_of_a_problem_struct(dtype):
