@@ -9,7 +9,7 @@ from dropless_grouped_gemm_router_amd import block as K
 from dropless_grouped_gemm_router_amd.inputs import Problem
 
 from gpu_util import Case, note
-from test_gpu_block import U, gen
+from test_gpu_block import U, act64, gen, off
 from test_gpu_block_forms import slope64
 from test_gpu_block_more import balance64, balance_case, linear_case, step_params
 from test_gpu_block_more import test_step_strided_and_in_place as strided_and_in_place
@@ -94,6 +94,36 @@ def test_linear_few_rows_infinities(t, k, n):
     assert torch.equal(gx[:, others], plain[0][:, others]) and torch.equal(gw, plain[1])
 
 
+@pytest.mark.parametrize("grad", ["bf16", "fp32"])
+@pytest.mark.parametrize("t,k,n,act", [(17, 300, 200, "gelu"), (33, 512, 1000, "silu"), (300, 1024, 512, "gelu_tanh"),
+                                       (2000, 256, 512, "silu"), (2000, 2048, 640, "gelu"), (5000, 640, 1155, "silu")])
+def test_linear_roundings(t, k, n, act, grad):
+    """From 17 bf16 rows on the results are rounded, and da before its products, and
+    nothing else that counts. These roundings are made here in 64 bits, and a kernel may
+    be off the unrounded result by at most 1.08 times what they are, in the 2-norm: slopes
+    are off by 2^-20, sums in fp32 by less than 2^-18, beside errors of 2^-10 and more, and
+    the roundings of thousands of elements average to a few per cent at most. Every call
+    repeats bit for bit, whatever its buffers held."""
+    import torch
+    note(f"linear roundings {t} {k} {n} {act} {grad}")
+    l, x, w, b, add, dy, buf = linear_case(t, k, n, "bf16", act, grad)
+    da, (dx, dw, _), _, _ = products64(x, w, b, dy, act)
+    y = act64(x.double() @ w.double() + b.double(), act) + add.double()
+    da = da.bfloat16().double()
+    rx, rw = (da @ w.double().t()).bfloat16(), (x.double().t() @ da).to(buf.grad_w.dtype)
+    once = None
+    for fill in (255, 0):
+        for m in (buf.workspace, buf.saved):
+            m.fill_(fill)
+        K.linear(l, x, w, buf, bias=b, residual=add, training=True)
+        buf.workspace.fill_(fill)
+        got = [buf.y.clone(), *(g.clone() for g in K.linear_backward(l, x, w, dy, buf))]
+        for name, g, r, want in zip(("y", "dx", "dw"), got, (y.bfloat16(), rx, rw), (y, dx, dw)):
+            assert off(g, want) <= 1.08 * off(r, want), name
+        assert once is None or all(torch.equal(a, c) for a, c in zip(got, once))
+        once = got
+
+
 # ------------------------------------------------------------- residual step
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
@@ -161,6 +191,35 @@ def test_balance_each_loss(t, e, k, d, dtype):
             for i in (1, 2):
                 assert abs(got[i] - want[i]) <= 2.0 ** -18 * want[i], i
             assert abs(got[0] - (c1 * want[1] + c2 * want[2])) <= 2.0 ** -18 * (abs(c1) * want[1] + abs(c2) * want[2])
+
+
+@pytest.mark.parametrize("t,e,k,d", [(300, 8, 2, 512), (4999, 33, 3, 1152), (16384, 64, 8, 512)])
+def test_balance_gradient_is_rounded_once(t, e, k, d):
+    """dx in bf16, element by element: half a step; dl and the router as two bf16
+    numbers each, which leave 2^-17 of either and, of the product of their second ones,
+    2^-16; and dl itself, whose p, lse and shares are 2^-18 off, from the size of its
+    terms. In the 2-norm that is nothing beside the rounding. Calls repeat bit for bit."""
+    import torch
+    note(f"balance dx {t} {e} {k} {d}")
+    b, x, w, idx, m, buf = balance_case(t, e, k, d, "bf16", mask=0.9)
+    _, p, counts, dx, _ = balance64(b, x, w, idx, m)
+    n, l, w64 = int(m.sum()), x.double() @ w.double(), w.double().abs()
+    p, lse, f = torch.softmax(l, 1), torch.logsumexp(l, 1, keepdim=True), counts.double() / (int(m.sum()) * k)
+    inner = (p * f).sum(1, keepdim=True)
+    dl = p * (b.balance * e * (f - inner) + 2 * b.z * lse) / n
+    terms = p * (b.balance * e * (f + inner) + 2 * b.z * lse.abs()) / n
+    bound = U["bf16"] * dx.abs() + 2.0 ** -15 * dl.abs() @ w64.t() + 2.0 ** -18 * terms @ w64.t()
+    once = None
+    for fill in (255, 0):
+        for t in (buf.workspace, buf.saved):
+            t.fill_(fill)
+        K.balance_loss(b, x, w, idx, buf, mask=m, training=True)
+        buf.workspace.fill_(fill)
+        gx, gw = (g.clone() for g in K.balance_loss_backward(b, x, w, buf, mask=m))
+        assert bool(((gx.double() - dx).abs() <= bound).all())
+        assert off(gx, dx) <= 1.01 * off(dx.bfloat16(), dx)
+        assert once is None or torch.equal(gx, once[0]) and torch.equal(gw, once[1])
+        once = gx, gw
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
