@@ -897,7 +897,8 @@ __device__ __forceinline__ void drop_tokens(SkinnyW<float>& x, const char* keep,
 }
 
 // 16384 tokens of 64 experts x 512 bf16: 17 us for 38 MB (7.4), MFMA 22% busy: five
-// or six turns of a workgroup, each waiting for its x; 4999 x 1152 fp32 27 us, MFMA 44%.
+// or six turns of a workgroup, each waiting for its x; 4999 x 1152 fp32 27 us, MFMA 44%
+// (two blocks of experts in fp32 put 16 bytes a thread into scratch memory).
 template <typename T, int EB>
 __global__ __launch_bounds__(kGradThreads) __attribute__((amdgpu_waves_per_eu(2)))
 void balance_grad_kernel(const BalGradArgs a, const T* __restrict__ x, const u32x4* __restrict__ wb,

@@ -14,8 +14,9 @@
 //
 // The weights come [inputs][outputs]: the forward runs over their leading
 // dimension, so it turns them K-contiguous first or, in bf16 up to some
-// thousand tokens, reads them where they are (in_place); up to 16 tokens (fp32:
-// 128) it reads them once, straight into MFMA operands (skinny.h). The
+// thousand tokens, reads them where they are (in_place); up to 16 tokens it reads
+// them once, straight into MFMA operands (skinny.h), and in fp32 up to 128, once for
+// every 16. The
 // backward's dx reads them as they are. da is made in one pass over dy that
 // also adds up dbias and pads the rows; without an activation dy itself is da.
 //
@@ -693,7 +694,8 @@ int bias_slices(const moe_linear& l) {
 // 100 x 100 (rows, inputs, outputs) 17 and 32, 1000 x 512 x 512 53 and 65, 300 x 1024
 // x 1024 62 and 67, 777 x 500 x 1001 53 and 85, 640 x 640 x 960 50 and 76; above it
 // 2000 x 512 x 512 79 and 68, 120 x 2048 x 2048 102 and 72, 8192 x 512 x 512 190 and
-// 156 (where the tiles' rows are padded: 701 x 901 x 803 75 and 95).
+// 156. Where the tiles' rows are padded the limit is low: 701 x 901 x 803 takes tiles,
+// 95, and would take 75 from memory; the rule does not look at padding.
 constexpr int64_t kDirect = int64_t{3} << 27;
 bool direct(const moe_linear& l) {
   const int64_t n = static_cast<int64_t>(l.inputs) * l.outputs, wide = l.inputs > l.outputs ? l.inputs : l.outputs;

@@ -89,7 +89,9 @@ __device__ __forceinline__ void load_scales(const float* p, float fill, int c, i
 
 // Whether the backward reads the parameters again for every row (from the
 // caches), and no row ahead: a workgroup of 1024 threads has 128 registers a
-// thread, beside the sums too few for them.
+// thread, beside the sums too few for them. (One piece a thread still puts 44 bytes
+// into scratch memory, two of fp32 92; above 8192 columns 524 and 692, at 0.7 to 1.1 TB/s
+// where 4096 x 4096 reaches 4.)
 template <int kMax>
 constexpr bool kAgain = kMax == 1024;
 
@@ -144,7 +146,8 @@ __device__ __forceinline__ void normalise(const StepArgs& a, const StepPlace<kRo
 }
 
 // 131072 x 512 bf16, two norms: 117 us for 537 MB, 4.6 TB/s (a copy 5.1); 5001 x 1155
-// fp32, rows of no alignment: 23 us for 92 MB (18).
+// fp32, rows of no alignment: 23 us for 92 MB (18). Above 8192 columns registers do not
+// suffice (scratch memory: 172 bytes a thread in bf16, 348 in fp32): 1.2 to 2 TB/s.
 template <typename T, int kRow, int NV, int kMax>
 __global__ __launch_bounds__(kMax) void step_fwd_kernel(const StepArgs a) {
   constexpr int V = Piece<T>::V;
@@ -484,7 +487,7 @@ void with_step_shape(int dtype, const StepShape& r, F&& f) {
     MOE_STEP_CASE(float, 64, 2, kSome);
     MOE_STEP_CASE(float, 0, 1, kWide);
     if constexpr (kBwd) MOE_STEP_CASE(float, 0, 2, kWide);
-    MOE_STEP_CASE(float, 0, 1, 1024);
+    else MOE_STEP_CASE(float, 0, 1, 1024);
     MOE_STEP_CASE(float, 0, 2, 1024);
     MOE_STEP_CASE(float, 0, 4, 1024);
   }

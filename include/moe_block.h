@@ -385,7 +385,8 @@ size_t moe_balance_workspace_bytes(const moe_balance* b);
 
 /* Bytes (host) of the buffer that moe_balance_loss fills for
  * moe_balance_loss_bwd: the gradient of loss[0] by the logits in fp32, and the
- * router's matrix, in bf16 as sums of two bf16 numbers (2^-17). 0 for an invalid
+ * router's matrix, in bf16 as sums of two bf16 numbers (2^-17; grad_x, with the
+ * logits' gradient in two as well, is 2^-16 off before it is rounded). 0 for an invalid
  * problem. */
 size_t moe_balance_saved_bytes(const moe_balance* b);
 
