@@ -486,8 +486,11 @@ void with_step_shape(int dtype, const StepShape& r, F&& f) {
     MOE_STEP_CASE(float, 64, 1, kSome);
     MOE_STEP_CASE(float, 64, 2, kSome);
     MOE_STEP_CASE(float, 0, 1, kWide);
-    if constexpr (kBwd) MOE_STEP_CASE(float, 0, 2, kWide);
-    else MOE_STEP_CASE(float, 0, 1, 1024);
+    if constexpr (kBwd) {
+      MOE_STEP_CASE(float, 0, 2, kWide);
+    } else {
+      MOE_STEP_CASE(float, 0, 1, 1024);
+    }
     MOE_STEP_CASE(float, 0, 2, 1024);
     MOE_STEP_CASE(float, 0, 4, 1024);
   }
