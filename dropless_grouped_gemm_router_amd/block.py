@@ -779,16 +779,15 @@ def linear(l: Linear, x, w, buf: LinearBuffers, bias=None, residual=None, traini
     if residual is not None:
         _want("residual", residual, ys, dt, dev)
     _want("y", y, ys, dt, dev)
-    # the library refuses whatever else is shared
-    if residual is not None and l.tokens and residual.data_ptr() == y.data_ptr():
+    out, add = y.data_ptr(), None if residual is None else residual.data_ptr()
+    if add == out and l.tokens:  # the library refuses whatever else is shared
         raise ValueError("residual: is the buffer of y; rows are stored while others are still read")
     _want_bytes("workspace", buf.workspace, 0, dev)
     if training:
         _want_saved(buf, nsv, dev)
     _run("moe_linear_fwd", dev, stream, load().moe_linear_fwd, c, x.data_ptr(), w.data_ptr(),
-         None if bias is None else bias.data_ptr(), None if residual is None else residual.data_ptr(),
-         buf.saved.data_ptr() if training else None, y.data_ptr(), buf.workspace.data_ptr(),
-         buf.workspace.numel())
+         None if bias is None else bias.data_ptr(), add, buf.saved.data_ptr() if training else None, out,
+         buf.workspace.data_ptr(), buf.workspace.numel())
     return y
 
 
@@ -904,6 +903,13 @@ def residual_norm(n: ResidualNorm, z, res, params: Dict, buf: ResidualNormBuffer
     (rows may be strided); params may hold post_weight, post_bias, gate,
     pre_weight and pre_bias (fp32). Returns (buf.out, buf.y), with buf.stats
     kept for the backward pass."""
+    _run("moe_residual_norm_fwd", z.device, stream, load().moe_residual_norm_fwd,
+         *_step_forward(n, z, res, params, buf))
+    return buf.out, buf.y if n.pre else None
+
+
+def _step_forward(n, z, res, params, buf):
+    """The checked arguments of residual_norm's call."""
     shape, stats, width, dt, c = n._plan
     dev, out, y, st, m = z.device, buf.out, buf.y, buf.stats, buf.made
     known = m and m[0] is n and m[1] == dev and out is m[2] and y is m[3] and st is m[4]
@@ -918,9 +924,8 @@ def residual_norm(n: ResidualNorm, z, res, params: Dict, buf: ResidualNormBuffer
     if not n.pre:
         y = None
     p = _step_params(params, width, dev)
-    _run("moe_residual_norm_fwd", dev, stream, load().moe_residual_norm_fwd, c, z.data_ptr(), res.data_ptr(),
-         ctypes.byref(p), out.data_ptr(), None if y is None else y.data_ptr(), st.data_ptr())
-    return out, y
+    return (c, z.data_ptr(), res.data_ptr(), ctypes.byref(p), out.data_ptr(), None if y is None else y.data_ptr(),
+            st.data_ptr())
 
 
 def residual_norm_backward(n: ResidualNorm, z, res, params: Dict, grad_out, grad_y,
@@ -929,6 +934,14 @@ def residual_norm_backward(n: ResidualNorm, z, res, params: Dict, grad_out, grad
     ``residual_norm`` with the same buffers: (grad_z, grad_res, {the gradients,
     fp32, of the parameters that params holds}). grad_out may be None; grad_y is
     None without the norm before the next block."""
+    args, grads = _step_backward(n, z, res, params, grad_out, grad_y, buf)
+    _run("moe_residual_norm_bwd", z.device, stream, load().moe_residual_norm_bwd, *args)
+    return buf.grad_z, buf.grad_res, grads
+
+
+def _step_backward(n, z, res, params, grad_out, grad_y, buf):
+    """The checked arguments of residual_norm_backward's call, and the gradients
+    that it returns."""
     shape, stats, width, dt, c = n._plan
     dev, st, gz, gr, ws, m, f32 = z.device, buf.stats, buf.grad_z, buf.grad_res, buf.workspace, buf.made, torch.float32
     if gz is None:
@@ -949,11 +962,9 @@ def residual_norm_backward(n: ResidualNorm, z, res, params: Dict, grad_out, grad
     p = _step_params(params, width, dev)
     grads = {name: buf.grads[name] for name in NORM_PARAMS if params.get(name) is not None}
     g = _step_params(grads, width, dev, moe_norm_grads)
-    _run("moe_residual_norm_bwd", dev, stream, load().moe_residual_norm_bwd, c, z.data_ptr(), res.data_ptr(),
-         ctypes.byref(p), st.data_ptr(), None if grad_out is None else grad_out.data_ptr(),
-         None if grad_y is None else grad_y.data_ptr(), gz.data_ptr(), gr.data_ptr(),
-         ctypes.byref(g), ws.data_ptr(), ws.numel())
-    return gz, gr, grads
+    return (c, z.data_ptr(), res.data_ptr(), ctypes.byref(p), st.data_ptr(),
+            None if grad_out is None else grad_out.data_ptr(), None if grad_y is None else grad_y.data_ptr(),
+            gz.data_ptr(), gr.data_ptr(), ctypes.byref(g), ws.data_ptr(), ws.numel()), grads
 
 
 # ------------------------------------------------------ balance of the router
@@ -1031,6 +1042,13 @@ def balance_loss(b: BalanceLoss, x, w_router, topk_idx, buf: BalanceBuffers, mas
     [tokens, top_k] was made of (the routing's dictionary holds it); mask [tokens]
     (bool or uint8) leaves out tokens where it is false. Returns buf.loss, with
     buf.mean_prob and buf.counts beside it."""
+    _run("moe_balance_loss", x.device, stream, load().moe_balance_loss,
+         *_balance_forward(b, x, w_router, topk_idx, buf, mask, training))
+    return buf.loss
+
+
+def _balance_forward(b, x, w_router, topk_idx, buf, mask, training):
+    """The checked arguments of balance_loss's call."""
     c, nsv, xs, ws, ks, es, dt = b._plan
     dev = x.device
     _want("x", x, xs, dt, dev)
@@ -1046,10 +1064,9 @@ def balance_loss(b: BalanceLoss, x, w_router, topk_idx, buf: BalanceBuffers, mas
         _want_bytes("workspace", buf.workspace, 0, dev)
     if training:
         _want_saved(buf, nsv, dev)
-    _run("moe_balance_loss", dev, stream, load().moe_balance_loss, c, x.data_ptr(), w_router.data_ptr(),
-         topk_idx.data_ptr(), m, buf.counts.data_ptr(), buf.mean_prob.data_ptr(), buf.loss.data_ptr(),
-         buf.saved.data_ptr() if training else None, buf.workspace.data_ptr(), buf.workspace.numel())
-    return buf.loss
+    return (c, x.data_ptr(), w_router.data_ptr(), topk_idx.data_ptr(), m, buf.counts.data_ptr(),
+            buf.mean_prob.data_ptr(), buf.loss.data_ptr(), buf.saved.data_ptr() if training else None,
+            buf.workspace.data_ptr(), buf.workspace.numel())
 
 
 def balance_loss_backward(b: BalanceLoss, x, w_router, buf: BalanceBuffers, grad_loss=None, mask=None,
@@ -1059,6 +1076,13 @@ def balance_loss_backward(b: BalanceLoss, x, w_router, buf: BalanceBuffers, grad
     buffers and mask: (grad_x, grad_router). w_router is the forward's, whose
     values the buffers hold (only its shape is looked at). add_to: a pair of gradients, the
     layer's own for instance, that they are added to in place of the buffers'."""
+    _run("moe_balance_loss_bwd", x.device, stream, load().moe_balance_loss_bwd,
+         *_balance_backward(b, x, w_router, buf, grad_loss, mask, add_to))
+    return (buf.grad_x, buf.grad_router) if add_to is None else tuple(add_to)
+
+
+def _balance_backward(b, x, w_router, buf, grad_loss, mask, add_to):
+    """The checked arguments of balance_loss_backward's call."""
     c, nsv, xs, ws, _, _, dt = b._plan
     dev = x.device
     gx, gw = (buf.grad_x, buf.grad_router) if add_to is None else add_to
@@ -1071,10 +1095,8 @@ def balance_loss_backward(b: BalanceLoss, x, w_router, buf: BalanceBuffers, grad
     _want("grad_x", gx, xs, dt, dev)
     _want("gradient of w_router", gw, ws, torch.float32, dev)
     _want_bytes("workspace", buf.workspace, 0, dev)
-    _run("moe_balance_loss_bwd", dev, stream, load().moe_balance_loss_bwd, c, x.data_ptr(), m,
-         buf.saved.data_ptr(), _ptr(grad_loss), int(add_to is not None),
-         gx.data_ptr(), gw.data_ptr(), buf.workspace.data_ptr(), buf.workspace.numel())
-    return gx, gw
+    return (c, x.data_ptr(), m, buf.saved.data_ptr(), _ptr(grad_loss), int(add_to is not None), gx.data_ptr(),
+            gw.data_ptr(), buf.workspace.data_ptr(), buf.workspace.numel())
 
 
 # ------------------------------------------------------- with the layer itself
@@ -1181,14 +1203,18 @@ def residual_layer_forward(p, h, res, weights: Dict, buf, n: ResidualNorm, step:
     step's parameters (``NORM_PARAMS``, each may be missing) beside the layer's.
     loss: a pair (BalanceLoss, BalanceBuffers) to have the router's balance loss
     of the tokens that mask keeps in its buffers. Returns (step.out, step.y)."""
+    # every part is checked before the first is launched
     _want_layer(p, "h", h, buf, weights, training)
     if loss is not None:
         _want_loss(p, loss)
+        balance = _balance_forward(loss[0], h, weights["w_router"], buf.routing["topk_idx"], loss[1], mask, training)
+    after = _step_forward(n, buf.out, res, weights, step)
     with torch.cuda.device(h.device):
-        out = binding.forward(p, h, weights, buf, training=training, stream=stream)
+        binding.forward(p, h, weights, buf, training=training, stream=stream)
     if loss is not None:
-        balance_loss(loss[0], h, weights["w_router"], buf.routing["topk_idx"], loss[1], mask, training, stream)
-    return residual_norm(n, out, res, weights, step, stream)
+        _run("moe_balance_loss", h.device, stream, load().moe_balance_loss, *balance)
+    _run("moe_residual_norm_fwd", h.device, stream, load().moe_residual_norm_fwd, *after)
+    return step.out, step.y if n.pre else None
 
 
 def residual_layer_backward(p, h, res, weights: Dict, grad_out, grad_y, buf, n: ResidualNorm,
@@ -1200,16 +1226,19 @@ def residual_layer_backward(p, h, res, weights: Dict, grad_out, grad_y, buf, n: 
     parameters' beside them), the loss's part added to the layer's."""
     if buf.grads is None:
         raise ValueError("the buffers were allocated without training=True")
+    # every part is checked before the first is launched
     if loss is not None:
         _want_loss(p, loss)
-    gz, gres, steps = residual_norm_backward(n, buf.out, res, weights, grad_out, grad_y, step, stream)
-    _want_layer(p, "h", h, buf, weights, True, gz)
+        balance = _balance_backward(loss[0], h, weights["w_router"], loss[1], grad_loss, mask,
+                                    (buf.grad_x, buf.grads["w_router"]))
+    after, steps = _step_backward(n, buf.out, res, weights, grad_out, grad_y, step)
+    _want_layer(p, "h", h, buf, weights, True, step.grad_z)
+    _run("moe_residual_norm_bwd", h.device, stream, load().moe_residual_norm_bwd, *after)
     with torch.cuda.device(h.device):
-        gh, grads = binding.backward(p, h, weights, gz, buf, stream=stream, side_stream=side_stream)
+        gh, grads = binding.backward(p, h, weights, step.grad_z, buf, stream=stream, side_stream=side_stream)
     if loss is not None:
-        balance_loss_backward(loss[0], h, weights["w_router"], loss[1], grad_loss, mask,
-                              add_to=(gh, grads["w_router"]), stream=stream)
-    return gh, gres, dict(grads, **steps)
+        _run("moe_balance_loss_bwd", h.device, stream, load().moe_balance_loss_bwd, *balance)
+    return gh, step.grad_res, dict(grads, **steps)
 
 
 @dataclass

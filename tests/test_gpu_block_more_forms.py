@@ -237,3 +237,31 @@ def test_residual_layer_of_a_problem_struct(dtype):
         gh, gs, grads = K.residual_layer_backward(problem, h, res, w, go, gy, c.buf, n, step, (b, loss))
         got.append([t.clone() for t in (out, y, loss.loss, gh, gs, *(grads[k] for k in sorted(grads)))])
     assert all(torch.equal(a, c) for a, c in zip(*got))
+
+
+def test_residual_layer_refuses_before_it_launches():
+    """A part that does not fit leaves every buffer as it was."""
+    import torch
+    p = Problem(70, 8, 2, 128, 128, 0, "bf16", 64)
+    c, r = Case(p, seed=4, training=True), gen(12)
+    n, b = K.ResidualNorm(70, 128, "bf16"), K.BalanceLoss(70, 8, 2, 128, "bf16")
+    step, loss = K.allocate_residual_norm(n, "cuda", training=True), K.allocate_balance_loss(b, "cuda", training=True)
+    h, w, res, go, gy = c.dev["x"], c.weights(), *(r(70, 128, dtype="bf16") for _ in range(3))
+    mask = torch.ones(70, dtype=torch.bool, device="cuda")
+    kept = [c.buf.out, c.buf.saved, c.buf.grad_x, *c.buf.grads.values(), *c.buf.routing.values(), step.out, step.y,
+            step.stats, step.grad_z, step.grad_res, loss.loss, loss.counts, loss.saved]
+    for t in kept:
+        t.fill_(7)
+    bad = [dict(res=res[:69]), dict(res=res.float()), dict(mask=mask[:69]), dict(mask=mask.float()),
+           dict(w=dict(w, gate=r(127))), dict(loss=(K.BalanceLoss(70, 8, 2, 128, "fp32"), loss))]
+    for kw in bad:
+        a = dict(dict(res=res, mask=mask, w=w, loss=(b, loss)), **kw)
+        with pytest.raises(ValueError):
+            K.residual_layer_forward(p, h, a["res"], a["w"], c.buf, n, step, a["loss"], a["mask"], training=True)
+        with pytest.raises(ValueError):
+            K.residual_layer_backward(p, h, a["res"], a["w"], go, gy, c.buf, n, step, a["loss"], mask=a["mask"])
+    for go2, gy2, gl in ((go[:9], gy, None), (go, None, None), (go, gy, r(2))):
+        with pytest.raises(ValueError):
+            K.residual_layer_backward(p, h, res, w, go2, gy2, c.buf, n, step, (b, loss), gl, mask)
+    torch.cuda.synchronize()
+    assert all(bool((t == 7).all()) for t in kept)
